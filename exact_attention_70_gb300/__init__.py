@@ -1,12 +1,14 @@
 """Exact tiled scaled-dot-product attention for GB300 (sm_103a).
 
 The compute lives in ``libattn.so`` (hand-written CUDA behind a C ABI declared in
-``include/attn.h``); this package only marshals arguments.  ``attn_fwd`` and
-``attn_decode_kvcache`` are loaded on first use and raise if the library is missing.
+``include/attn.h``); this package only marshals arguments.  The calls are
+loaded on first use and raise if the library is missing.
 """
 
 __all__ = ["attn_fwd", "attn_decode_kvcache", "attn_fwd_workspace_bytes",
-           "attn_decode_workspace_bytes", "attn_get_device_status", "AttnError"]
+           "attn_decode_workspace_bytes", "attn_get_device_status", "AttnError",
+           "attn_kvcache_append_fp8", "attn_kvcache_read_fp8", "attn_decode_kvcache_fp8",
+           "attn_fwd_kvcache_fp8"]
 
 
 def __getattr__(name):

@@ -78,6 +78,20 @@ def load():
             lib.attn_bwd_workspace_bytes.argtypes = [i32, i32]
             lib.attn_fwd_kvcache_workspace_bytes.restype = sz
             lib.attn_fwd_kvcache_workspace_bytes.argtypes = [i32] * 7
+            lib.attn_kvcache_append_fp8.restype = i32
+            lib.attn_kvcache_append_fp8.argtypes = [P] * 11 + [i32] * 10 + [P]
+            lib.attn_kvcache_read_fp8.restype = i32
+            lib.attn_kvcache_read_fp8.argtypes = [P] * 8 + [i32] * 7 + [P]
+            lib.attn_decode_kvcache_fp8.restype = i32
+            lib.attn_decode_kvcache_fp8.argtypes = [P] * 7 + [i32, i32, P, P] + [i32] * 6 + [
+                f32, P, sz, P]
+            lib.attn_decode_kvcache_fp8_workspace_bytes.restype = sz
+            lib.attn_decode_kvcache_fp8_workspace_bytes.argtypes = [i32] * 7
+            lib.attn_fwd_kvcache_fp8.restype = i32
+            lib.attn_fwd_kvcache_fp8.argtypes = [P] * 12 + [i32] * 3 + [P, P] + [i32] * 10 + [
+                f32, i32, i32, i32, P, sz, P]
+            lib.attn_fwd_kvcache_fp8_workspace_bytes.restype = sz
+            lib.attn_fwd_kvcache_fp8_workspace_bytes.argtypes = [i32] * 10
             lib.attn_status_string.restype = ctypes.c_char_p
             lib.attn_status_string.argtypes = [i32]
             lib.attn_kv_block_range.restype = i32
@@ -464,3 +478,232 @@ def attn_decode_kvcache_noalloc(q, k_cache, v_cache, cache_seqlens, block_table,
     if rc != 0:
         raise AttnError(rc, "attn_decode_kvcache_noalloc")
     return out, lse
+
+
+# ---- 8-bit paged KV cache ------------------------------------------------------------------
+
+
+def _on(device, stream, body):
+    """body(stream pointer) with `device` current and what it allocates belonging to `stream`
+    (default: the device's current stream)."""
+    if stream is None:
+        if torch.cuda.current_device() == device.index:
+            return body(ctypes.c_void_p(torch.cuda.current_stream().cuda_stream))
+        with torch.cuda.device(device):
+            return body(ctypes.c_void_p(torch.cuda.current_stream().cuda_stream))
+    if stream.device != device:
+        raise ValueError("the stream must belong to the tensors' device")
+    with torch.cuda.device(device), torch.cuda.stream(stream):
+        return body(ctypes.c_void_p(stream.cuda_stream))
+
+
+def _same_device(first, *others):
+    for t in others:
+        if t is not None and t.device != first.device:
+            raise ValueError("all tensors must be on one device")
+
+
+def _kv8_shapes(k_cache, v_cache, k_scale, v_scale, block_table, batch):
+    """Checks shared by the calls on the 8-bit cache; returns its sizes."""
+    _check(k_cache, "k_cache", torch.uint8, 4)
+    _check(v_cache, "v_cache", torch.uint8, 4)
+    _check(k_scale, "k_scale", torch.uint8, 3)
+    _check(v_scale, "v_scale", torch.uint8, 3)
+    _check(block_table, "block_table", torch.int32, 2)
+    num_pages, page_size, Hkv, d = k_cache.shape
+    if v_cache.shape != k_cache.shape:
+        raise ValueError("k_cache and v_cache must both be [num_pages, page_size, Hkv, d]")
+    if k_scale.shape != (num_pages, Hkv, page_size) or v_scale.shape != k_scale.shape:
+        raise ValueError("k_scale and v_scale must both be [num_pages, Hkv, page_size]")
+    if block_table.shape[0] != batch:
+        raise ValueError("block_table must have one row per sequence")
+    return num_pages, page_size, Hkv, d
+
+
+def _rotary_shapes(rotary_cos, rotary_sin):
+    if rotary_cos is None and rotary_sin is None:
+        return 0, 0
+    _check(rotary_cos, "rotary_cos", torch.float32, 2)
+    _check(rotary_sin, "rotary_sin", torch.float32, 2)
+    if rotary_sin.shape != rotary_cos.shape:
+        raise ValueError("rotary_cos and rotary_sin must both be [rows, rotary_dim / 2]")
+    return rotary_cos.shape[0], 2 * rotary_cos.shape[1]
+
+
+def _new_tokens(k_new, v_new, cache_seqlens, cu_seqlens_q, Hkv, d):
+    _check(k_new, "k_new", torch.bfloat16, 3)
+    _check(v_new, "v_new", torch.bfloat16, 3)
+    _check(cache_seqlens, "cache_seqlens", torch.int32, 1)
+    if k_new.shape[1:] != (Hkv, d) or v_new.shape != k_new.shape:
+        raise ValueError("k_new and v_new must both be [total_q, Hkv, d] with the cache's Hkv and d")
+    if cache_seqlens.numel() != cu_seqlens_q.numel() - 1:
+        raise ValueError("cache_seqlens must have one entry per sequence")
+
+
+def attn_kvcache_append_fp8(k_new, v_new, k_cache, v_cache, k_scale, v_scale, cache_seqlens,
+                            block_table, cu_seqlens_q, rotary_cos=None, rotary_sin=None,
+                            rotary_interleaved=False, stream=None):
+    """Write new tokens' keys (rotated) and values into the 8-bit paged cache, in place.
+
+    k_new / v_new [total_q, Hkv, d] bf16; caches uint8 e4m3 codes [num_pages, page_size, Hkv, d]
+    with scale bytes uint8 [num_pages, Hkv, page_size]; token i of sequence b goes to position
+    cache_seqlens[b] + i.  rotary_cos / rotary_sin fp32 [rows, rotary_dim / 2] or None.
+    """
+    lib = load()
+    _check(cu_seqlens_q, "cu_seqlens_q", torch.int32, 1)
+    batch = cu_seqlens_q.numel() - 1
+    num_pages, page_size, Hkv, d = _kv8_shapes(k_cache, v_cache, k_scale, v_scale, block_table,
+                                               batch)
+    _new_tokens(k_new, v_new, cache_seqlens, cu_seqlens_q, Hkv, d)
+    rot_rows, rot_dim = _rotary_shapes(rotary_cos, rotary_sin)
+    _same_device(k_new, v_new, k_cache, v_cache, k_scale, v_scale, cache_seqlens, block_table,
+                 cu_seqlens_q, rotary_cos, rotary_sin)
+
+    def body(s):
+        return lib.attn_kvcache_append_fp8(
+            _ptr(k_new), _ptr(v_new), _ptr(k_cache), _ptr(v_cache), _ptr(k_scale), _ptr(v_scale),
+            _ptr(cache_seqlens), _ptr(block_table), _ptr(cu_seqlens_q), _ptr(rotary_cos),
+            _ptr(rotary_sin), rot_dim, rot_rows, int(bool(rotary_interleaved)), batch,
+            k_new.shape[0], Hkv, d, page_size, block_table.shape[1], num_pages, s)
+
+    rc = _on(k_new.device, stream, body)
+    if rc != 0:
+        raise AttnError(rc, "attn_kvcache_append_fp8")
+
+
+def attn_kvcache_read_fp8(k_cache, v_cache, k_scale, v_scale, block_table, cu_seqlens_k, total_k,
+                          k=None, v=None, stream=None):
+    """Read the first cu_seqlens_k[b + 1] - cu_seqlens_k[b] tokens of every sequence of the 8-bit
+    cache back.  Returns (k, v), bf16 [total_k, Hkv, d], packed as attn_fwd takes them."""
+    lib = load()
+    _check(cu_seqlens_k, "cu_seqlens_k", torch.int32, 1)
+    batch = cu_seqlens_k.numel() - 1
+    num_pages, page_size, Hkv, d = _kv8_shapes(k_cache, v_cache, k_scale, v_scale, block_table,
+                                               batch)
+    shape = (int(total_k), Hkv, d)
+    for t, n in ((k, "k"), (v, "v")):
+        if t is not None:
+            _check(t, n, torch.bfloat16, 3)
+            if t.shape != shape:
+                raise ValueError(f"{n} must be [total_k, Hkv, d]")
+    _same_device(k_cache, v_cache, k_scale, v_scale, block_table, cu_seqlens_k, k, v)
+
+    def body(s):
+        ko = torch.empty(shape, dtype=torch.bfloat16, device=k_cache.device) if k is None else k
+        vo = torch.empty(shape, dtype=torch.bfloat16, device=k_cache.device) if v is None else v
+        rc = lib.attn_kvcache_read_fp8(
+            _ptr(k_cache), _ptr(v_cache), _ptr(k_scale), _ptr(v_scale), _ptr(block_table),
+            _ptr(cu_seqlens_k), _ptr(ko), _ptr(vo), batch, shape[0], Hkv, d, page_size,
+            block_table.shape[1], num_pages, s)
+        if rc != 0:
+            raise AttnError(rc, "attn_kvcache_read_fp8")
+        return ko, vo
+
+    return _on(k_cache.device, stream, body)
+
+
+def attn_decode_kvcache_fp8_workspace_bytes(batch, nheads_q, nheads_kv, head_dim, page_size,
+                                            max_pages_per_seq, num_splits=0) -> int:
+    return int(load().attn_decode_kvcache_fp8_workspace_bytes(
+        batch, nheads_q, nheads_kv, head_dim, page_size, max_pages_per_seq, num_splits))
+
+
+def attn_decode_kvcache_fp8(q, k_cache, v_cache, k_scale, v_scale, cache_seqlens, block_table,
+                            softmax_scale=None, num_splits=0, out=None, lse=None,
+                            workspace=None, stream=None):
+    """Decode over the 8-bit paged cache.  q [batch, Hq, d] bf16, one token per sequence.
+
+    Returns (out [batch, Hq, d] bf16, lse [batch, Hq] fp32).
+    """
+    lib = load()
+    _check(q, "q", torch.bfloat16, 3)
+    _check(cache_seqlens, "cache_seqlens", torch.int32, 1)
+    batch, Hq, d = q.shape
+    num_pages, page_size, Hkv, dk = _kv8_shapes(k_cache, v_cache, k_scale, v_scale, block_table,
+                                                batch)
+    if dk != d:
+        raise ValueError("q must have the cache's head dimension")
+    if cache_seqlens.numel() != batch:
+        raise ValueError("cache_seqlens must have one entry per sequence")
+    _same_device(q, k_cache, v_cache, k_scale, v_scale, cache_seqlens, block_table, out, lse,
+                 workspace)
+    scale = d ** -0.5 if softmax_scale is None else float(softmax_scale)
+    nbytes = int(lib.attn_decode_kvcache_fp8_workspace_bytes(batch, Hq, Hkv, d, page_size,
+                                                             block_table.shape[1],
+                                                             int(num_splits)))
+
+    def body(s):
+        o, l = _decode_outputs(q, out, lse)
+        ws = _workspace(nbytes, q.device, workspace)
+        rc = lib.attn_decode_kvcache_fp8(
+            _ptr(q), _ptr(k_cache), _ptr(v_cache), _ptr(k_scale), _ptr(v_scale),
+            _ptr(cache_seqlens), _ptr(block_table), page_size, int(num_splits), _ptr(o), _ptr(l),
+            batch, Hq, Hkv, d, block_table.shape[1], num_pages, scale, _ptr(ws), nbytes, s)
+        if rc != 0:
+            raise AttnError(rc, "attn_decode_kvcache_fp8")
+        return o, l
+
+    return _on(q.device, stream, body)
+
+
+def attn_fwd_kvcache_fp8_workspace_bytes(batch, total_q, max_seqlen_q, max_total_k, nheads_q,
+                                         nheads_kv, head_dim, page_size, max_pages_per_seq,
+                                         rotary_dim=0) -> int:
+    return int(load().attn_fwd_kvcache_fp8_workspace_bytes(
+        batch, total_q, max_seqlen_q, max_total_k, nheads_q, nheads_kv, head_dim, page_size,
+        max_pages_per_seq, rotary_dim))
+
+
+def attn_fwd_kvcache_fp8(q, k_new, v_new, k_cache, v_cache, k_scale, v_scale, cache_seqlens,
+                         block_table, cu_seqlens_q, max_seqlen_q, max_total_k=None,
+                         softmax_scale=None, causal=True, window_left=-1, window_right=-1,
+                         rotary_cos=None, rotary_sin=None, rotary_interleaved=False, out=None,
+                         lse=None, workspace=None, stream=None):
+    """A chunk of new tokens against the 8-bit paged cache; the new k, v are written into it.
+
+    q [total_q, Hq, d], k_new / v_new [total_q, Hkv, d] bf16; the cache as for
+    attn_kvcache_append_fp8; max_total_k bounds sum_b (cache_seqlens[b] + new tokens of b) (default:
+    what block_table can hold).  Returns (out [total_q, Hq, d], lse [Hq, total_q]).
+    """
+    lib = load()
+    _check(q, "q", torch.bfloat16, 3)
+    _check(cu_seqlens_q, "cu_seqlens_q", torch.int32, 1)
+    batch = cu_seqlens_q.numel() - 1
+    num_pages, page_size, Hkv, d = _kv8_shapes(k_cache, v_cache, k_scale, v_scale, block_table,
+                                               batch)
+    _new_tokens(k_new, v_new, cache_seqlens, cu_seqlens_q, Hkv, d)
+    total_q, Hq = q.shape[:2]
+    if q.shape[2] != d or k_new.shape[0] != total_q:
+        raise ValueError("q, k_new and v_new must have the same tokens and head dimension")
+    rot_rows, rot_dim = _rotary_shapes(rotary_cos, rotary_sin)
+    for t, n, dt, shape in ((out, "out", torch.bfloat16, (total_q, Hq, d)),
+                            (lse, "lse", torch.float32, (Hq, total_q))):
+        if t is not None:
+            _check(t, n, dt, len(shape))
+            if t.shape != shape:
+                raise ValueError(f"{n} must be {list(shape)}")
+    _same_device(q, k_new, v_new, k_cache, v_cache, k_scale, v_scale, cache_seqlens, block_table,
+                 cu_seqlens_q, rotary_cos, rotary_sin, out, lse, workspace)
+    max_pages = block_table.shape[1]
+    total_k = (min(batch * max_pages * page_size, 2 ** 31 - 1) if max_total_k is None
+               else int(max_total_k))
+    scale = d ** -0.5 if softmax_scale is None else float(softmax_scale)
+    nbytes = int(lib.attn_fwd_kvcache_fp8_workspace_bytes(
+        batch, total_q, int(max_seqlen_q), total_k, Hq, Hkv, d, page_size, max_pages, rot_dim))
+
+    def body(s):
+        o = torch.empty_like(q) if out is None else out
+        l = torch.empty((Hq, total_q), dtype=torch.float32, device=q.device) if lse is None else lse
+        ws = _workspace(nbytes, q.device, workspace)
+        rc = lib.attn_fwd_kvcache_fp8(
+            _ptr(q), _ptr(k_new), _ptr(v_new), _ptr(k_cache), _ptr(v_cache), _ptr(k_scale),
+            _ptr(v_scale), _ptr(cache_seqlens), _ptr(block_table), _ptr(cu_seqlens_q),
+            _ptr(rotary_cos), _ptr(rotary_sin), rot_dim, rot_rows, int(bool(rotary_interleaved)),
+            _ptr(o), _ptr(l), batch, total_q, int(max_seqlen_q), total_k, Hq, Hkv, d, page_size,
+            max_pages, num_pages, scale, int(bool(causal)), int(window_left), int(window_right),
+            _ptr(ws), nbytes, s)
+        if rc != 0:
+            raise AttnError(rc, "attn_fwd_kvcache_fp8")
+        return o, l
+
+    return _on(q.device, stream, body)

@@ -17,7 +17,8 @@ LIB = os.path.join(BUILD, "libattn.so")
 # The debugging build with device bounds checks (-DATTN_CHECK_BOUNDS): a separate library.
 BUILD_CHECKED = os.path.join(HERE, "_build_checked")
 LIB_CHECKED = os.path.join(BUILD_CHECKED, "libattn.so")
-SOURCES = ["attn_api.cu", "fwd_kernel.cu", "decode_kernel.cu", "decode_noalloc.cu", "selftest.cu", "kvcache.cu", "bwd_kernel.cu", "fwd_fp8_kernel.cu", "quantize_fp8.cu"]
+SOURCES = ["attn_api.cu", "fwd_kernel.cu", "decode_kernel.cu", "decode_noalloc.cu", "selftest.cu", "kvcache.cu", "bwd_kernel.cu", "fwd_fp8_kernel.cu", "quantize_fp8.cu",
+           "kvcache_fp8.cu", "attn_kv8_kernel.cu"]
 HEADERS = ["ptx.cuh", "kernels.h", "tile_math.h"]
 ARCH = ["-gencode", "arch=compute_103a,code=sm_103a"]
 NVCC = os.environ.get("NVCC", "/usr/local/cuda/bin/nvcc")

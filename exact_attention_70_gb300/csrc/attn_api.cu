@@ -20,6 +20,7 @@ namespace {
 __device__ unsigned g_status_word;
 
 constexpr int kMaxDevices = 64;
+constexpr int kGb300Sms = 152;
 
 struct DeviceState {
     bool ready = false;
@@ -52,6 +53,7 @@ attn_status_t device_state(DeviceState** out) {
             return ATTN_ERR_CUDA;
         if (configure_fwd_kernels() != cudaSuccess) return ATTN_ERR_CUDA;
         if (configure_decode_kernels() != cudaSuccess) return ATTN_ERR_CUDA;
+        if (configure_kv8_kernels() != cudaSuccess) return ATTN_ERR_CUDA;
         s.status = static_cast<unsigned*>(addr);
         s.ready = true;
     }
@@ -93,6 +95,23 @@ attn_status_t encode_3d_u8(CUtensorMap* map, const void* base, uint64_t n0, uint
                                 dims, strides, box, estr, CU_TENSOR_MAP_INTERLEAVE_NONE,
                                 CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
                                 CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE);
+    return r == CUDA_SUCCESS ? ATTN_OK : ATTN_ERR_CUDA;
+}
+
+// Codes of the 8-bit cache [rows][Hkv][d]: boxes {d, 1, box_rows}, swizzled over the d bytes of
+// a row (128 or 64).
+attn_status_t encode_kv8(CUtensorMap* map, const void* base, int head_dim, int nheads_kv,
+                         uint64_t rows, uint32_t box_rows) {
+    const uint64_t d = static_cast<uint64_t>(head_dim), n1 = static_cast<uint64_t>(nheads_kv);
+    const cuuint64_t dims[3] = {d, n1, rows};
+    const cuuint64_t strides[2] = {d, d * n1};
+    const cuuint32_t box[3] = {static_cast<cuuint32_t>(head_dim), 1, box_rows};
+    const cuuint32_t estr[3] = {1, 1, 1};
+    const CUresult r = g_encode(
+        map, CU_TENSOR_MAP_DATA_TYPE_UINT8, 3, const_cast<void*>(base), dims, strides, box, estr,
+        CU_TENSOR_MAP_INTERLEAVE_NONE,
+        head_dim == 128 ? CU_TENSOR_MAP_SWIZZLE_128B : CU_TENSOR_MAP_SWIZZLE_64B,
+        CU_TENSOR_MAP_L2_PROMOTION_L2_256B, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE);
     return r == CUDA_SUCCESS ? ATTN_OK : ATTN_ERR_CUDA;
 }
 
@@ -787,6 +806,390 @@ attn_status_t attn_decode_kvcache(const void* q, const void* k_cache, const void
         if (launch_combine(cp, head_dim, s) != cudaSuccess) return ATTN_ERR_CUDA;
     }
     return ATTN_OK;
+}
+
+}  // extern "C"
+
+// ---- 8-bit (e4m3) paged KV cache ------------------------------------------------------------
+
+namespace {
+
+// What every call on the 8-bit cache asks of its sizes.
+attn_status_t kv8_sizes(int batch, int nheads_kv, int head_dim, int page_size,
+                        int max_pages_per_seq, int num_pages) {
+    if (batch < 0 || nheads_kv <= 0 || page_size <= 0 || max_pages_per_seq <= 0 || num_pages <= 0)
+        return ATTN_ERR_INVALID_ARG;
+    if (head_dim != 64 && head_dim != 128) return ATTN_ERR_UNSUPPORTED;
+    if (page_size % 16 != 0 || !(page_size % kKv8Chunk == 0 || kKv8Chunk % page_size == 0))
+        return ATTN_ERR_UNSUPPORTED;
+    if (batch > 65535 || nheads_kv > 65535 ||
+        static_cast<long long>(num_pages + 1LL) * page_size > (1LL << 31) - 1 ||
+        static_cast<long long>(max_pages_per_seq) * page_size > (1LL << 30))
+        return ATTN_ERR_UNSUPPORTED;
+    return ATTN_OK;
+}
+
+// 0: every pointer given and aligned.
+bool kv8_cache_ok(const void* k_cache, const void* v_cache, const void* k_scale,
+                  const void* v_scale, const int32_t* block_table) {
+    return k_cache && v_cache && k_scale && v_scale && block_table && aligned(k_cache, 16) &&
+           aligned(v_cache, 16) && aligned(k_scale, 16) && aligned(v_scale, 16) &&
+           aligned(block_table, 4);
+}
+
+attn_status_t rotary_ok(const float* cos, const float* sin, int rotary_dim, int rotary_rows,
+                        int head_dim) {
+    if (rotary_dim < 0 || rotary_dim > head_dim || rotary_dim % 16 != 0) return ATTN_ERR_UNSUPPORTED;
+    if (rotary_dim > 0 &&
+        (!cos || !sin || rotary_rows <= 0 || !aligned(cos, 16) || !aligned(sin, 16)))
+        return ATTN_ERR_INVALID_ARG;
+    return ATTN_OK;
+}
+
+// Splits of the key axis for the attention kernel: enough CTAs for about four waves of two per
+// SM of a GB300, about one split per 2048 keys where sequences may be that long (so that
+// short and long ones make CTAs of similar length), never an empty split by construction.
+int kv8_splits(int batch, int max_seqlen_q, int nheads_q, int nheads_kv, int page_size,
+               int max_pages_per_seq) {
+    const long long groups =
+        (static_cast<long long>(max_seqlen_q) * (nheads_q / nheads_kv) + kKv8Rows - 1) / kKv8Rows;
+    const long long ctas = static_cast<long long>(batch) * nheads_kv * groups;
+    const long long keys = static_cast<long long>(max_pages_per_seq) * page_size;
+    if (ctas <= 0) return 1;
+    const long long by_len = (keys + 2047) / 2048 < 16 ? (keys + 2047) / 2048 : 16;
+    const long long by_sms = (4LL * 2 * kGb300Sms + ctas - 1) / ctas;
+    const long long chunks = (keys + kKv8Chunk - 1) / kKv8Chunk;
+    long long s = by_len > by_sms ? by_len : by_sms;
+    if (s > chunks) s = chunks;
+    if (s > kKv8MaxSplits) s = kKv8MaxSplits;
+    return static_cast<int>(s < 1 ? 1 : s);
+}
+
+size_t kv8_partial_bytes(long long rows, int head_dim, int splits) {
+    if (splits <= 1) return 0;
+    return align_up(static_cast<size_t>(rows) * splits * head_dim * sizeof(float), 256) +
+           align_up(static_cast<size_t>(rows) * splits * sizeof(float), 256);
+}
+
+// The rotated queries (f16) and their units.
+size_t kv8_query_bytes(long long rows, int head_dim, int rotary_dim) {
+    if (rotary_dim <= 0) return 0;
+    return align_up(static_cast<size_t>(rows) * head_dim * 2, 256) +
+           align_up(static_cast<size_t>(rows) * sizeof(float), 256);
+}
+
+// The attention kernel and, for more than one split, the combine.
+attn_status_t kv8_attend(Kv8Params& kp, const void* k_cache, const void* v_cache, int head_dim,
+                         void* partials, cudaStream_t s) {
+    const uint64_t cache_rows = static_cast<uint64_t>(kp.num_pages) * kp.page_size;
+    kp.box_rows = kp.page_size < kKv8Chunk ? kp.page_size : kKv8Chunk;
+    if (encode_kv8(&kp.tm_k, k_cache, head_dim, kp.Hkv, cache_rows, kp.box_rows) != ATTN_OK ||
+        encode_kv8(&kp.tm_v, v_cache, head_dim, kp.Hkv, cache_rows, kp.box_rows) != ATTN_OK)
+        return ATTN_ERR_CUDA;
+    if (kp.num_splits > 1) {
+        const size_t rows = static_cast<size_t>(kp.total_q) * kp.Hq;
+        kp.part_o = static_cast<float*>(partials);
+        kp.part_lse = reinterpret_cast<float*>(
+            static_cast<uint8_t*>(partials) +
+            align_up(rows * kp.num_splits * head_dim * sizeof(float), 256));
+    }
+    if (launch_kv8_attn(kp, head_dim, s) != cudaSuccess) return ATTN_ERR_CUDA;
+    if (kp.num_splits > 1) {
+        Kv8CombineParams cp;
+        cp.part_o = kp.part_o;
+        cp.part_lse = kp.part_lse;
+        cp.out = kp.out;
+        cp.lse = kp.lse;
+        cp.cu_q = kp.cu_q;
+        cp.batch = kp.batch;
+        cp.total_q = kp.total_q;
+        cp.Hq = kp.Hq;
+        cp.num_splits = kp.num_splits;
+        cp.lse_head = kp.lse_head;
+        cp.lse_tok = kp.lse_tok;
+        if (launch_kv8_combine(cp, head_dim, s) != cudaSuccess) return ATTN_ERR_CUDA;
+    }
+    return ATTN_OK;
+}
+
+}  // namespace
+
+extern "C" {
+
+attn_status_t attn_kvcache_append_fp8(const void* k_new, const void* v_new, void* k_cache,
+                                      void* v_cache, void* k_scale, void* v_scale,
+                                      const int32_t* cache_seqlens, const int32_t* block_table,
+                                      const int32_t* cu_seqlens_q, const float* rotary_cos,
+                                      const float* rotary_sin, int rotary_dim, int rotary_rows,
+                                      int rotary_interleaved, int batch, int total_q,
+                                      int nheads_kv, int head_dim, int page_size,
+                                      int max_pages_per_seq, int num_pages, void* stream) {
+    NvtxRange nvtx_range("attn_kvcache_append_fp8");
+    attn_status_t st = kv8_sizes(batch, nheads_kv, head_dim, page_size, max_pages_per_seq, num_pages);
+    if (st != ATTN_OK) return st;
+    if (total_q < 0) return ATTN_ERR_INVALID_ARG;
+    st = rotary_ok(rotary_cos, rotary_sin, rotary_dim, rotary_rows, head_dim);
+    if (st != ATTN_OK) return st;
+    if (batch == 0 || total_q == 0) return ATTN_OK;
+    if (!kv8_cache_ok(k_cache, v_cache, k_scale, v_scale, block_table) || !k_new || !v_new ||
+        !cache_seqlens || !cu_seqlens_q || !aligned(k_new, 16) || !aligned(v_new, 16) ||
+        !aligned(cache_seqlens, 4) || !aligned(cu_seqlens_q, 4))
+        return ATTN_ERR_INVALID_ARG;
+    DeviceState* dev = nullptr;
+    st = device_state(&dev);
+    if (st != ATTN_OK) return st;
+    AppendFp8Params ap;
+    memset(&ap, 0, sizeof(ap));
+    ap.k_new = static_cast<const __nv_bfloat16*>(k_new);
+    ap.v_new = static_cast<const __nv_bfloat16*>(v_new);
+    ap.k_cache = static_cast<uint8_t*>(k_cache);
+    ap.v_cache = static_cast<uint8_t*>(v_cache);
+    ap.k_scale = static_cast<uint8_t*>(k_scale);
+    ap.v_scale = static_cast<uint8_t*>(v_scale);
+    ap.cu_q = cu_seqlens_q;
+    ap.cache_seqlens = cache_seqlens;
+    ap.block_table = block_table;
+    ap.rot_cos = rotary_cos;
+    ap.rot_sin = rotary_sin;
+    ap.status = dev->status;
+    ap.batch = batch;
+    ap.total_q = total_q;
+    ap.Hkv = nheads_kv;
+    ap.page_size = page_size;
+    ap.max_pages = max_pages_per_seq;
+    ap.num_pages = num_pages;
+    ap.rot_dim = rotary_dim;
+    ap.rot_rows = rotary_rows;
+    ap.interleaved = rotary_interleaved ? 1 : 0;
+    if (launch_kvcache_append_fp8(ap, head_dim, dev->num_sms, static_cast<cudaStream_t>(stream)) !=
+        cudaSuccess)
+        return ATTN_ERR_CUDA;
+    return ATTN_OK;
+}
+
+attn_status_t attn_kvcache_read_fp8(const void* k_cache, const void* v_cache, const void* k_scale,
+                                    const void* v_scale, const int32_t* block_table,
+                                    const int32_t* cu_seqlens_k, void* k, void* v, int batch,
+                                    int total_k, int nheads_kv, int head_dim, int page_size,
+                                    int max_pages_per_seq, int num_pages, void* stream) {
+    NvtxRange nvtx_range("attn_kvcache_read_fp8");
+    attn_status_t st = kv8_sizes(batch, nheads_kv, head_dim, page_size, max_pages_per_seq, num_pages);
+    if (st != ATTN_OK) return st;
+    if (total_k < 0) return ATTN_ERR_INVALID_ARG;
+    if (batch == 0 || total_k == 0) return ATTN_OK;
+    if (!kv8_cache_ok(k_cache, v_cache, k_scale, v_scale, block_table) || !cu_seqlens_k || !k || !v ||
+        !aligned(cu_seqlens_k, 4) || !aligned(k, 16) || !aligned(v, 16))
+        return ATTN_ERR_INVALID_ARG;
+    DeviceState* dev = nullptr;
+    st = device_state(&dev);
+    if (st != ATTN_OK) return st;
+    ReadFp8Params rp;
+    memset(&rp, 0, sizeof(rp));
+    rp.k_cache = static_cast<const uint8_t*>(k_cache);
+    rp.v_cache = static_cast<const uint8_t*>(v_cache);
+    rp.k_scale = static_cast<const uint8_t*>(k_scale);
+    rp.v_scale = static_cast<const uint8_t*>(v_scale);
+    rp.block_table = block_table;
+    rp.cu_k = cu_seqlens_k;
+    rp.k = static_cast<__nv_bfloat16*>(k);
+    rp.v = static_cast<__nv_bfloat16*>(v);
+    rp.status = dev->status;
+    rp.batch = batch;
+    rp.total_k = total_k;
+    rp.Hkv = nheads_kv;
+    rp.page_size = page_size;
+    rp.max_pages = max_pages_per_seq;
+    rp.num_pages = num_pages;
+    if (launch_kvcache_read_fp8(rp, head_dim, dev->num_sms, static_cast<cudaStream_t>(stream)) !=
+        cudaSuccess)
+        return ATTN_ERR_CUDA;
+    return ATTN_OK;
+}
+
+size_t attn_decode_kvcache_fp8_workspace_bytes(int batch, int nheads_q, int nheads_kv,
+                                               int head_dim, int page_size,
+                                               int max_pages_per_seq, int num_splits) {
+    if (batch <= 0 || nheads_q <= 0 || nheads_kv <= 0 || nheads_q % nheads_kv != 0 ||
+        num_splits < 0 || num_splits > kKv8MaxSplits ||
+        kv8_sizes(batch, nheads_kv, head_dim, page_size, max_pages_per_seq, 1) != ATTN_OK)
+        return 0;
+    const int S = num_splits != 0 ? num_splits
+                                  : kv8_splits(batch, 1, nheads_q, nheads_kv, page_size,
+                                               max_pages_per_seq);
+    return kv8_partial_bytes(static_cast<long long>(batch) * nheads_q, head_dim, S);
+}
+
+attn_status_t attn_decode_kvcache_fp8(const void* q, const void* k_cache, const void* v_cache,
+                                      const void* k_scale, const void* v_scale,
+                                      const int32_t* cache_seqlens, const int32_t* block_table,
+                                      int page_size, int num_splits, void* out, float* lse,
+                                      int batch, int nheads_q, int nheads_kv, int head_dim,
+                                      int max_pages_per_seq, int num_pages, float softmax_scale,
+                                      void* workspace, size_t workspace_bytes, void* stream) {
+    NvtxRange nvtx_range("attn_decode_kvcache_fp8");
+    attn_status_t st = kv8_sizes(batch, nheads_kv, head_dim, page_size, max_pages_per_seq, num_pages);
+    if (st != ATTN_OK) return st;
+    if (nheads_q <= 0 || nheads_q % nheads_kv != 0 || num_splits < 0 ||
+        num_splits > kKv8MaxSplits || !scale_ok(softmax_scale))
+        return ATTN_ERR_INVALID_ARG;
+    if (static_cast<long long>(batch) * nheads_q > (1LL << 31) - 1) return ATTN_ERR_UNSUPPORTED;
+    if (batch == 0) return ATTN_OK;
+    if (!kv8_cache_ok(k_cache, v_cache, k_scale, v_scale, block_table) || !q || !cache_seqlens ||
+        !out || !lse || !aligned(q, 16) || !aligned(out, 16) || !aligned(lse, 4) ||
+        !aligned(cache_seqlens, 4))
+        return ATTN_ERR_INVALID_ARG;
+    const int S = num_splits != 0 ? num_splits
+                                  : kv8_splits(batch, 1, nheads_q, nheads_kv, page_size,
+                                               max_pages_per_seq);
+    const size_t need = kv8_partial_bytes(static_cast<long long>(batch) * nheads_q, head_dim, S);
+    if (need > 0 && (!workspace || workspace_bytes < need || !aligned(workspace, 256)))
+        return ATTN_ERR_WORKSPACE;
+    DeviceState* dev = nullptr;
+    st = device_state(&dev);
+    if (st != ATTN_OK) return st;
+    Kv8Params kp;
+    memset(&kp, 0, sizeof(kp));
+    kp.k_scale = static_cast<const uint8_t*>(k_scale);
+    kp.v_scale = static_cast<const uint8_t*>(v_scale);
+    kp.q = static_cast<const __nv_bfloat16*>(q);
+    kp.out = static_cast<__nv_bfloat16*>(out);
+    kp.lse = lse;
+    kp.seqlens = cache_seqlens;
+    kp.block_table = block_table;
+    kp.status = dev->status;
+    kp.batch = batch;
+    kp.total_q = batch;
+    kp.max_seqlen_q = 1;
+    kp.Hq = nheads_q;
+    kp.Hkv = nheads_kv;
+    kp.g = nheads_q / nheads_kv;
+    kp.page_size = page_size;
+    kp.max_pages = max_pages_per_seq;
+    kp.num_pages = num_pages;
+    kp.num_splits = S;
+    kp.causal = 1;
+    kp.wl = kp.wr = -1;
+    kp.lse_head = 1;
+    kp.lse_tok = nheads_q;
+    kp.scale_log2 = softmax_scale * kLog2eF;
+    return kv8_attend(kp, k_cache, v_cache, head_dim, workspace, static_cast<cudaStream_t>(stream));
+}
+
+size_t attn_fwd_kvcache_fp8_workspace_bytes(int batch, int total_q, int max_seqlen_q,
+                                            int max_total_k, int nheads_q, int nheads_kv,
+                                            int head_dim, int page_size, int max_pages_per_seq,
+                                            int rotary_dim) {
+    if (batch <= 0 || total_q < 0 || max_seqlen_q < 0 || max_total_k < 0 || nheads_q <= 0 ||
+        nheads_kv <= 0 || nheads_q % nheads_kv != 0 || rotary_dim < 0 ||
+        kv8_sizes(batch, nheads_kv, head_dim, page_size, max_pages_per_seq, 1) != ATTN_OK)
+        return 0;
+    return kv8_query_bytes(static_cast<long long>(total_q) * nheads_q, head_dim, rotary_dim) + kv8_partial_bytes(static_cast<long long>(total_q) * nheads_q, head_dim,
+                                    kv8_splits(batch, max_seqlen_q, nheads_q, nheads_kv, page_size,
+                                               max_pages_per_seq));
+}
+
+attn_status_t attn_fwd_kvcache_fp8(const void* q, const void* k_new, const void* v_new,
+                                   void* k_cache, void* v_cache, void* k_scale, void* v_scale,
+                                   const int32_t* cache_seqlens, const int32_t* block_table,
+                                   const int32_t* cu_seqlens_q, const float* rotary_cos,
+                                   const float* rotary_sin, int rotary_dim, int rotary_rows,
+                                   int rotary_interleaved, void* out, float* lse, int batch,
+                                   int total_q, int max_seqlen_q, int max_total_k, int nheads_q,
+                                   int nheads_kv, int head_dim, int page_size,
+                                   int max_pages_per_seq, int num_pages, float softmax_scale,
+                                   int causal, int window_left, int window_right, void* workspace,
+                                   size_t workspace_bytes, void* stream) {
+    NvtxRange nvtx_range("attn_fwd_kvcache_fp8");
+    attn_status_t st = kv8_sizes(batch, nheads_kv, head_dim, page_size, max_pages_per_seq, num_pages);
+    if (st != ATTN_OK) return st;
+    if (total_q < 0 || max_seqlen_q < 0 || max_total_k < 0 || nheads_q <= 0 ||
+        nheads_q % nheads_kv != 0 || window_left < -1 || window_right < -1 || !scale_ok(softmax_scale))
+        return ATTN_ERR_INVALID_ARG;
+    st = rotary_ok(rotary_cos, rotary_sin, rotary_dim, rotary_rows, head_dim);
+    if (st != ATTN_OK) return st;
+    if (static_cast<long long>(total_q) * nheads_q > (1LL << 31) - 1) return ATTN_ERR_UNSUPPORTED;
+    if (batch == 0 || total_q == 0) return ATTN_OK;
+    if (!kv8_cache_ok(k_cache, v_cache, k_scale, v_scale, block_table) || !q || !k_new || !v_new ||
+        !cache_seqlens || !cu_seqlens_q || !out || !lse || !aligned(q, 16) || !aligned(k_new, 16) ||
+        !aligned(v_new, 16) || !aligned(out, 16) || !aligned(lse, 4) || !aligned(cache_seqlens, 4) ||
+        !aligned(cu_seqlens_q, 4))
+        return ATTN_ERR_INVALID_ARG;
+    const size_t need = attn_fwd_kvcache_fp8_workspace_bytes(
+        batch, total_q, max_seqlen_q, max_total_k, nheads_q, nheads_kv, head_dim, page_size,
+        max_pages_per_seq, rotary_dim);
+    if (need > 0 && (!workspace || workspace_bytes < need || !aligned(workspace, 256)))
+        return ATTN_ERR_WORKSPACE;
+    DeviceState* dev = nullptr;
+    st = device_state(&dev);
+    if (st != ATTN_OK) return st;
+    const cudaStream_t s = static_cast<cudaStream_t>(stream);
+    uint8_t* ws = static_cast<uint8_t*>(workspace);
+    const size_t q_rows = static_cast<size_t>(total_q) * nheads_q;
+
+    // 1. append the new keys (rotated) and values; rotate the queries
+    AppendFp8Params ap;
+    memset(&ap, 0, sizeof(ap));
+    ap.q = static_cast<const __nv_bfloat16*>(q);
+    ap.k_new = static_cast<const __nv_bfloat16*>(k_new);
+    ap.v_new = static_cast<const __nv_bfloat16*>(v_new);
+    ap.k_cache = static_cast<uint8_t*>(k_cache);
+    ap.v_cache = static_cast<uint8_t*>(v_cache);
+    ap.k_scale = static_cast<uint8_t*>(k_scale);
+    ap.v_scale = static_cast<uint8_t*>(v_scale);
+    if (rotary_dim > 0) {
+        ap.q_rot = reinterpret_cast<__half*>(ws);
+        ap.q_unit = reinterpret_cast<float*>(ws + align_up(q_rows * head_dim * 2, 256));
+    }
+    ap.cu_q = cu_seqlens_q;
+    ap.cache_seqlens = cache_seqlens;
+    ap.block_table = block_table;
+    ap.rot_cos = rotary_cos;
+    ap.rot_sin = rotary_sin;
+    ap.status = dev->status;
+    ap.batch = batch;
+    ap.total_q = total_q;
+    ap.Hq = nheads_q;
+    ap.Hkv = nheads_kv;
+    ap.page_size = page_size;
+    ap.max_pages = max_pages_per_seq;
+    ap.num_pages = num_pages;
+    ap.rot_dim = rotary_dim;
+    ap.rot_rows = rotary_rows;
+    ap.interleaved = rotary_interleaved ? 1 : 0;
+    if (launch_kvcache_append_fp8(ap, head_dim, dev->num_sms, s) != cudaSuccess) return ATTN_ERR_CUDA;
+
+    // 2. attention over the cache
+    Kv8Params kp;
+    memset(&kp, 0, sizeof(kp));
+    kp.k_scale = static_cast<const uint8_t*>(k_scale);
+    kp.v_scale = static_cast<const uint8_t*>(v_scale);
+    kp.q = ap.q;
+    kp.q_rot = ap.q_rot;
+    kp.q_unit = ap.q_unit;
+    kp.out = static_cast<__nv_bfloat16*>(out);
+    kp.lse = lse;
+    kp.cu_q = cu_seqlens_q;
+    kp.seqlens = cache_seqlens;
+    kp.block_table = block_table;
+    kp.status = dev->status;
+    kp.batch = batch;
+    kp.total_q = total_q;
+    kp.max_seqlen_q = max_seqlen_q;
+    kp.Hq = nheads_q;
+    kp.Hkv = nheads_kv;
+    kp.g = nheads_q / nheads_kv;
+    kp.page_size = page_size;
+    kp.max_pages = max_pages_per_seq;
+    kp.num_pages = num_pages;
+    kp.num_splits = kv8_splits(batch, max_seqlen_q, nheads_q, nheads_kv, page_size, max_pages_per_seq);
+    kp.causal = causal ? 1 : 0;
+    kp.wl = window_left;
+    kp.wr = window_right;
+    kp.lse_head = total_q;
+    kp.lse_tok = 1;
+    kp.scale_log2 = softmax_scale * kLog2eF;
+    return kv8_attend(kp, k_cache, v_cache, head_dim,
+                      ws + kv8_query_bytes(q_rows, head_dim, rotary_dim), s);
 }
 
 attn_status_t attn_selftest_wait_timeout(void* stream) {

@@ -4,6 +4,7 @@
 
 #include <cuda.h>
 #include <cuda_bf16.h>
+#include <cuda_fp16.h>
 #include <cuda_runtime.h>
 #include <stdint.h>
 
@@ -178,6 +179,87 @@ struct QuantParams {
 
 cudaError_t launch_quantize_fp8(const QuantParams& p, cudaStream_t stream);
 
+// ---- 8-bit (e4m3) paged KV cache --------------------------------------------------------------
+
+// Codes [num_pages, page_size, Hkv, d], scale bytes (E8M0) [num_pages, Hkv, page_size].
+struct AppendFp8Params {
+    const __nv_bfloat16* q;      // [total_q, Hq, d], rotated into q_rot (null q_rot: no queries)
+    const __nv_bfloat16* k_new;  // [total_q, Hkv, d]
+    const __nv_bfloat16* v_new;
+    uint8_t* k_cache;
+    uint8_t* v_cache;
+    uint8_t* k_scale;
+    uint8_t* v_scale;
+    __half* q_rot;   // [total_q, Hq, d]: the rotated query times a power of two a row
+    float* q_unit;   // [total_q, Hq]: what one unit of q_rot stands for
+    const int* cu_q;
+    const int* cache_seqlens;
+    const int* block_table;
+    const float* rot_cos;  // [rot_rows, rot_dim / 2]
+    const float* rot_sin;
+    unsigned* status;
+    int batch, total_q, Hq, Hkv, page_size, max_pages, num_pages;
+    int rot_dim, rot_rows, interleaved;
+};
+
+struct ReadFp8Params {
+    const uint8_t* k_cache;
+    const uint8_t* v_cache;
+    const uint8_t* k_scale;
+    const uint8_t* v_scale;
+    const int* block_table;
+    const int* cu_k;
+    __nv_bfloat16* k;  // [total_k, Hkv, d]
+    __nv_bfloat16* v;
+    unsigned* status;
+    int batch, total_k, Hkv, page_size, max_pages, num_pages;
+};
+
+constexpr int kKv8Chunk = 64;     // keys per pipeline stage
+constexpr int kKv8Threads = 160;  // 4 MMA warps + 1 TMA warp
+constexpr int kKv8Rows = 16;      // packed query rows of one CTA
+constexpr int kKv8MaxSplits = 64;
+
+struct Kv8Params {
+    CUtensorMap tm_k;  // 3-D over the codes [num_pages * page_size, Hkv, d] u8, box {d, 1, box_rows}
+    CUtensorMap tm_v;
+    const uint8_t* k_scale;
+    const uint8_t* v_scale;
+    const __nv_bfloat16* q;  // [total_q, Hq, d], or, where the queries were rotated,
+    const __half* q_rot;     //   their scaled f16 form
+    const float* q_unit;     //   and its units [total_q, Hq]
+    __nv_bfloat16* out;
+    float* lse;
+    float* part_o;    // [total_q, Hq, num_splits, d]  (num_splits > 1)
+    float* part_lse;  // [total_q, Hq, num_splits]
+    const int* cu_q;  // [batch + 1], or null: one query per sequence, at its last key
+    const int* seqlens;  // keys in the cache; with cu_q, before the call's new tokens
+    const int* block_table;
+    unsigned* status;
+    int batch, total_q, max_seqlen_q, Hq, Hkv, g;
+    int page_size, box_rows, max_pages, num_pages, num_splits;
+    int causal, wl, wr;
+    int lse_head, lse_tok;  // strides of lse
+    float scale_log2;
+};
+
+struct Kv8CombineParams {
+    const float* part_o;
+    const float* part_lse;
+    __nv_bfloat16* out;
+    float* lse;
+    const int* cu_q;  // or null: every token has a sequence
+    int batch, total_q, Hq, num_splits;
+    int lse_head, lse_tok;
+};
+
+cudaError_t launch_kvcache_append_fp8(const AppendFp8Params& p, int head_dim, int num_sms,
+                                      cudaStream_t stream);
+cudaError_t launch_kvcache_read_fp8(const ReadFp8Params& p, int head_dim, int num_sms,
+                                    cudaStream_t stream);
+cudaError_t launch_kv8_attn(const Kv8Params& p, int head_dim, cudaStream_t stream);
+cudaError_t launch_kv8_combine(const Kv8CombineParams& p, int head_dim, cudaStream_t stream);
+
 // ---- failure-path self-test ------------------------------------------------------------
 
 cudaError_t launch_watchdog_selftest(unsigned* status, cudaStream_t stream);
@@ -222,5 +304,6 @@ int decode_smem_bytes(int head_dim);
 // Configure the kernels' shared-memory limits on the current device (idempotent).
 cudaError_t configure_fwd_kernels();
 cudaError_t configure_decode_kernels();
+cudaError_t configure_kv8_kernels();
 
 }  // namespace attn

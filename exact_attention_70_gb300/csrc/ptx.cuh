@@ -181,6 +181,17 @@ __device__ __forceinline__ void tma_store_3d(const CUtensorMap* map, const void*
         : "memory");
 }
 
+// Untiled copy of `bytes` (a multiple of 16, both addresses 16-byte aligned) into shared memory;
+// completion is counted on `bar` in bytes.
+__device__ __forceinline__ void bulk_load(void* smem_dst, const void* src, uint32_t bytes,
+                                          uint64_t* bar) {
+    asm volatile(
+        "cp.async.bulk.shared::cluster.global.mbarrier::complete_tx::bytes [%0], [%1], %2, [%3];" ::"r"(
+            smem_u32(smem_dst)),
+        "l"(src), "r"(bytes), "r"(smem_u32(bar))
+        : "memory");
+}
+
 __device__ __forceinline__ void bulk_commit_group() {
     asm volatile("cp.async.bulk.commit_group;" ::: "memory");
 }
@@ -509,6 +520,50 @@ __device__ __forceinline__ uint32_t pack_e4m3x4(float a, float b, float c, float
     return r;
 }
 
+// Two e4m3 bytes (the low half of `codes`, low byte first) to f16x2, exactly.
+__device__ __forceinline__ uint32_t e4m3x2_to_f16x2(uint32_t codes) {
+    uint32_t r;
+    asm("{\n\t.reg .b16 lo, hi;\n\t"
+        "mov.b32 {lo, hi}, %1;\n\t"
+        "cvt.rn.f16x2.e4m3x2 %0, lo;\n\t}\n"
+        : "=r"(r)
+        : "r"(codes));
+    return r;
+}
+
+__device__ __forceinline__ float2 f16x2_to_float2(uint32_t v) {
+    float2 f;
+    asm("{\n\t.reg .b16 lo, hi;\n\t"
+        "mov.b32 {lo, hi}, %2;\n\t"
+        "cvt.f32.f16 %0, lo;\n\t"
+        "cvt.f32.f16 %1, hi;\n\t}\n"
+        : "=f"(f.x), "=f"(f.y)
+        : "r"(v));
+    return f;
+}
+
+// Pack two fp32 into f16x2 with round-to-nearest-even; `lo` lands in the low half.
+__device__ __forceinline__ uint32_t pack_f16x2(float lo, float hi) {
+    uint32_t r;
+    asm("cvt.rn.f16x2.f32 %0, %1, %2;" : "=r"(r) : "f"(hi), "f"(lo));
+    return r;
+}
+
+// 2^n for n <= 127; 0 below the normal range.
+__device__ __forceinline__ float exp2_int(int n) {
+    return n < -126 ? 0.f : __int_as_float((n + 127) << 23);
+}
+
+// The power of two a that brings a query row with largest exponent field `top` to [2^13, 2^14):
+// f16 then holds the row's elements to 11 bits down to 2^-28 of the largest.  (At most 2^120,
+// so that 2^a and 2^-a are normal; rows below 2^-107 stay smaller.)
+__device__ __forceinline__ int kv8_query_shift(int top) { return min(13 - (top - 127), 120); }
+
+// The value of an E8M0 scale byte: 2^(b - 127), NaN for 255.
+__device__ __forceinline__ float e8m0_to_f32(int b) {
+    return b == 255 ? __int_as_float(0x7fffffff) : __int_as_float(b == 0 ? 0x00400000 : b << 23);
+}
+
 __device__ __forceinline__ uint64_t f2_make(float lo, float hi) {
     uint64_t r;
     asm("mov.b64 %0, {%1, %2};" : "=l"(r) : "f"(lo), "f"(hi));
@@ -564,6 +619,16 @@ __device__ __forceinline__ void mma_bf16_16816(float (&c)[4], const uint32_t (&a
                                                uint32_t b0, uint32_t b1) {
     asm volatile(
         "mma.sync.aligned.m16n8k16.row.col.f32.bf16.bf16.f32 "
+        "{%0, %1, %2, %3}, {%4, %5, %6, %7}, {%8, %9}, {%0, %1, %2, %3};"
+        : "+f"(c[0]), "+f"(c[1]), "+f"(c[2]), "+f"(c[3])
+        : "r"(a[0]), "r"(a[1]), "r"(a[2]), "r"(a[3]), "r"(b0), "r"(b1));
+}
+
+// C(16x8 f32) += A(16x16 f16, row) * B(16x8 f16, col)
+__device__ __forceinline__ void mma_f16_16816(float (&c)[4], const uint32_t (&a)[4], uint32_t b0,
+                                              uint32_t b1) {
+    asm volatile(
+        "mma.sync.aligned.m16n8k16.row.col.f32.f16.f16.f32 "
         "{%0, %1, %2, %3}, {%4, %5, %6, %7}, {%8, %9}, {%0, %1, %2, %3};"
         : "+f"(c[0]), "+f"(c[1]), "+f"(c[2]), "+f"(c[3])
         : "r"(a[0]), "r"(a[1]), "r"(a[2]), "r"(a[3]), "r"(b0), "r"(b1));

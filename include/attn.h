@@ -294,6 +294,121 @@ attn_status_t attn_quantize_fp8(const void* q, const void* k, const void* v,
                                 void* k8, float* k_scale, void* v8t, float* v_scale,
                                 void* stream);
 
+/*
+ * The 8-bit paged KV cache ("Attention kernels: FlashAttention and PagedAttention", sections
+ * 四.2 and 五.1; "04 · FA4 (CuTeDSL) and engineering interfaces", sections 6.1-6.2: the paged
+ * cache of attn_decode_kvcache and attn_fwd_kvcache at half its bytes).  Four calls share it:
+ *
+ *   k_cache, v_cache  device u8 e4m3 [num_pages, page_size, nheads_kv, head_dim]
+ *   k_scale, v_scale  device u8 E8M0 [num_pages, nheads_kv, page_size]: byte b stands for
+ *                     2^(b - 127) (255: NaN), one per (token, kv head)
+ *   A row's value is code * 2^(b - 127).  A row x is stored with e = the smallest integer
+ *   >= -126 with max|x| <= 448 * 2^e, b = e + 127 and the codes e4m3(x * 2^-e), to nearest,
+ *   ties to even; an element that is not finite gets the NaN code 0x7F and does not count for
+ *   the maximum; an all-zero row gets b = 1.
+ *   block_table       device int32 [batch, max_pages_per_seq], as for attn_decode_kvcache
+ *   page_size         a multiple of 16 that divides 64 or is a multiple of 64
+ *   head_dim          64 or 128
+ * All four arrays are 16-byte aligned.  The caller owns every buffer; nothing is allocated.  A
+ * page id outside [0, num_pages), a position past the table or the rotary tables, a negative
+ * length, or cu_seqlens that leave the packed tensors raise ATTN_ERR_DEVICE_BOUNDS (read with
+ * attn_get_device_status): what is written or read there is skipped, and the results of that
+ * sequence are unspecified.
+ */
+
+/*
+ * attn_kvcache_append_fp8 -- write the keys and values of new tokens into the 8-bit cache.
+ *   k_new, v_new  device bf16 [total_q, nheads_kv, head_dim]; sequence b owns rows
+ *                 [cu_seqlens_q[b], cu_seqlens_q[b+1]); rows outside every sequence are skipped
+ *   cache_seqlens device int32 [batch], tokens cached before the call: token i of sequence b goes
+ *                 to position cache_seqlens[b] + i; not advanced
+ *   rotary_*      as attn_fwd_kvcache (tables 16-byte aligned): keys are rotated first, and the
+ *                 rotated value is rounded once, to its code
+ * Every byte written equals what rounding the exactly rotated row gives, up to ties closer than
+ * 2^-45 of the row's largest element.
+ */
+attn_status_t attn_kvcache_append_fp8(const void* k_new, const void* v_new, void* k_cache,
+                                      void* v_cache, void* k_scale, void* v_scale,
+                                      const int32_t* cache_seqlens, const int32_t* block_table,
+                                      const int32_t* cu_seqlens_q, const float* rotary_cos,
+                                      const float* rotary_sin, int rotary_dim, int rotary_rows,
+                                      int rotary_interleaved, int batch, int total_q,
+                                      int nheads_kv, int head_dim, int page_size,
+                                      int max_pages_per_seq, int num_pages, void* stream);
+
+/*
+ * attn_kvcache_read_fp8 -- read the first cu_seqlens_k[b+1] - cu_seqlens_k[b] tokens of every
+ * sequence back into the packed tensors attn_fwd takes.
+ *   cu_seqlens_k  device int32 [batch + 1], non-decreasing
+ *   k, v          device bf16 [total_k, nheads_kv, head_dim]; row cu_seqlens_k[b] + j is token j of
+ *                 sequence b; rows outside every sequence are left as they were
+ * The values are exact except where bf16 cannot hold them (below its normal range).
+ */
+attn_status_t attn_kvcache_read_fp8(const void* k_cache, const void* v_cache, const void* k_scale,
+                                    const void* v_scale, const int32_t* block_table,
+                                    const int32_t* cu_seqlens_k, void* k, void* v, int batch,
+                                    int total_k, int nheads_kv, int head_dim, int page_size,
+                                    int max_pages_per_seq, int num_pages, void* stream);
+
+/*
+ * attn_decode_kvcache_fp8 -- attn_decode_kvcache over the 8-bit cache.
+ *   q   device bf16 [batch, nheads_q, head_dim]; out the same shape; lse device fp32
+ *       [batch, nheads_q], natural log
+ *   cache_seqlens  device int32 [batch]; sequence b attends to its keys 0 .. cache_seqlens[b]-1
+ *       (none: O = 0, LSE = -inf)
+ *   num_splits     0 = choose automatically, else 1..64
+ *   workspace      attn_decode_kvcache_fp8_workspace_bytes(...) bytes, 256-byte aligned (may be
+ *       NULL when that is 0)
+ * The result is the attention of the stored values: the codes and the queries enter the tensor
+ * cores exactly, the weights P with 11 significant bits.
+ */
+attn_status_t attn_decode_kvcache_fp8(const void* q, const void* k_cache, const void* v_cache,
+                                      const void* k_scale, const void* v_scale,
+                                      const int32_t* cache_seqlens, const int32_t* block_table,
+                                      int page_size, int num_splits, void* out, float* lse,
+                                      int batch, int nheads_q, int nheads_kv, int head_dim,
+                                      int max_pages_per_seq, int num_pages, float softmax_scale,
+                                      void* workspace, size_t workspace_bytes, void* stream);
+
+/* Workspace bytes of attn_decode_kvcache_fp8 (split partials; 0 with one split, or on sizes the
+ * call would refuse). */
+size_t attn_decode_kvcache_fp8_workspace_bytes(int batch, int nheads_q, int nheads_kv,
+                                               int head_dim, int page_size,
+                                               int max_pages_per_seq, int num_splits);
+
+/*
+ * attn_fwd_kvcache_fp8 -- attn_fwd_kvcache over the 8-bit cache: appends the new tokens' keys and
+ * values as attn_kvcache_append_fp8 does, rotates the queries (in the workspace, to 11 significant
+ * bits), then attends from every new token to the cached and the new ones, as they are stored.
+ *   q    device bf16 [total_q, nheads_q, head_dim]; out the same shape; lse device fp32
+ *        [nheads_q, total_q]; rows outside every sequence are left as they were
+ *   max_seqlen_q  an upper bound on the new tokens of a sequence (checked on the device)
+ *   max_total_k   an upper bound on sum_b (cache_seqlens[b] + new tokens of b) (checked on the
+ *                 device); sizes the workspace
+ *   causal, window_left, window_right   see "Visibility"
+ *   workspace     attn_fwd_kvcache_fp8_workspace_bytes(...) bytes, 256-byte aligned (may be NULL
+ *                 when that is 0)
+ * A NaN or an infinity among the new values reaches the rows that see it, and may reach the other
+ * new tokens of its sequence, as in attn_fwd.
+ */
+attn_status_t attn_fwd_kvcache_fp8(const void* q, const void* k_new, const void* v_new,
+                                   void* k_cache, void* v_cache, void* k_scale, void* v_scale,
+                                   const int32_t* cache_seqlens, const int32_t* block_table,
+                                   const int32_t* cu_seqlens_q, const float* rotary_cos,
+                                   const float* rotary_sin, int rotary_dim, int rotary_rows,
+                                   int rotary_interleaved, void* out, float* lse, int batch,
+                                   int total_q, int max_seqlen_q, int max_total_k, int nheads_q,
+                                   int nheads_kv, int head_dim, int page_size,
+                                   int max_pages_per_seq, int num_pages, float softmax_scale,
+                                   int causal, int window_left, int window_right, void* workspace,
+                                   size_t workspace_bytes, void* stream);
+
+/* Workspace bytes of attn_fwd_kvcache_fp8 (0 on sizes the call would refuse). */
+size_t attn_fwd_kvcache_fp8_workspace_bytes(int batch, int total_q, int max_seqlen_q,
+                                            int max_total_k, int nheads_q, int nheads_kv,
+                                            int head_dim, int page_size, int max_pages_per_seq,
+                                            int rotary_dim);
+
 /* Bytes of split-partial workspace for attn_decode_kvcache; num_splits 0 sizes for the
  * automatic choice (at most 16 splits).  0 when one split needs no workspace. */
 size_t attn_decode_workspace_bytes(int batch, int nheads_q, int head_dim, int num_splits);
