@@ -83,10 +83,10 @@ def load():
             lib.attn_kvcache_read_fp8.restype = i32
             lib.attn_kvcache_read_fp8.argtypes = [P] * 8 + [i32] * 7 + [P]
             lib.attn_decode_kvcache_fp8.restype = i32
-            lib.attn_decode_kvcache_fp8.argtypes = [P] * 7 + [i32, i32, P, P] + [i32] * 6 + [
+            lib.attn_decode_kvcache_fp8.argtypes = [P] * 7 + [i32, P, P] + [i32] * 6 + [
                 f32, P, sz, P]
             lib.attn_decode_kvcache_fp8_workspace_bytes.restype = sz
-            lib.attn_decode_kvcache_fp8_workspace_bytes.argtypes = [i32] * 7
+            lib.attn_decode_kvcache_fp8_workspace_bytes.argtypes = [i32] * 6
             lib.attn_fwd_kvcache_fp8.restype = i32
             lib.attn_fwd_kvcache_fp8.argtypes = [P] * 12 + [i32] * 3 + [P, P] + [i32] * 10 + [
                 f32, i32, i32, i32, P, sz, P]
@@ -603,14 +603,13 @@ def attn_kvcache_read_fp8(k_cache, v_cache, k_scale, v_scale, block_table, cu_se
 
 
 def attn_decode_kvcache_fp8_workspace_bytes(batch, nheads_q, nheads_kv, head_dim, page_size,
-                                            max_pages_per_seq, num_splits=0) -> int:
+                                            max_pages_per_seq) -> int:
     return int(load().attn_decode_kvcache_fp8_workspace_bytes(
-        batch, nheads_q, nheads_kv, head_dim, page_size, max_pages_per_seq, num_splits))
+        batch, nheads_q, nheads_kv, head_dim, page_size, max_pages_per_seq))
 
 
 def attn_decode_kvcache_fp8(q, k_cache, v_cache, k_scale, v_scale, cache_seqlens, block_table,
-                            softmax_scale=None, num_splits=0, out=None, lse=None,
-                            workspace=None, stream=None):
+                            softmax_scale=None, out=None, lse=None, workspace=None, stream=None):
     """Decode over the 8-bit paged cache.  q [batch, Hq, d] bf16, one token per sequence.
 
     Returns (out [batch, Hq, d] bf16, lse [batch, Hq] fp32).
@@ -629,16 +628,15 @@ def attn_decode_kvcache_fp8(q, k_cache, v_cache, k_scale, v_scale, cache_seqlens
                  workspace)
     scale = d ** -0.5 if softmax_scale is None else float(softmax_scale)
     nbytes = int(lib.attn_decode_kvcache_fp8_workspace_bytes(batch, Hq, Hkv, d, page_size,
-                                                             block_table.shape[1],
-                                                             int(num_splits)))
+                                                             block_table.shape[1]))
 
     def body(s):
         o, l = _decode_outputs(q, out, lse)
         ws = _workspace(nbytes, q.device, workspace)
         rc = lib.attn_decode_kvcache_fp8(
             _ptr(q), _ptr(k_cache), _ptr(v_cache), _ptr(k_scale), _ptr(v_scale),
-            _ptr(cache_seqlens), _ptr(block_table), page_size, int(num_splits), _ptr(o), _ptr(l),
-            batch, Hq, Hkv, d, block_table.shape[1], num_pages, scale, _ptr(ws), nbytes, s)
+            _ptr(cache_seqlens), _ptr(block_table), page_size, _ptr(o), _ptr(l), batch, Hq, Hkv,
+            d, block_table.shape[1], num_pages, scale, _ptr(ws), nbytes, s)
         if rc != 0:
             raise AttnError(rc, "attn_decode_kvcache_fp8")
         return o, l

@@ -820,7 +820,7 @@ attn_status_t kv8_sizes(int batch, int nheads_kv, int head_dim, int page_size,
     if (batch < 0 || nheads_kv <= 0 || page_size <= 0 || max_pages_per_seq <= 0 || num_pages <= 0)
         return ATTN_ERR_INVALID_ARG;
     if (head_dim != 64 && head_dim != 128) return ATTN_ERR_UNSUPPORTED;
-    if (page_size % 16 != 0 || !(page_size % kKv8Chunk == 0 || kKv8Chunk % page_size == 0))
+    if (page_size % 16 != 0 || !(page_size % 64 == 0 || 64 % page_size == 0))
         return ATTN_ERR_UNSUPPORTED;
     if (batch > 65535 || nheads_kv > 65535 ||
         static_cast<long long>(num_pages + 1LL) * page_size > (1LL << 31) - 1 ||
@@ -846,29 +846,28 @@ attn_status_t rotary_ok(const float* cos, const float* sin, int rotary_dim, int 
     return ATTN_OK;
 }
 
-// Splits of the key axis for the attention kernel: enough CTAs for about four waves of two per
-// SM of a GB300, about one split per 2048 keys where sequences may be that long (so that
-// short and long ones make CTAs of similar length), never an empty split by construction.
-int kv8_splits(int batch, int max_seqlen_q, int nheads_q, int nheads_kv, int page_size,
-               int max_pages_per_seq) {
+// CTAs of the attention kernel: as many for each kv head as make two an SM of a GB300, fewer where
+// the largest possible work (every sequence as long as its table) would leave some without
+// any; 0 where a head's work does not count in 31 bits.
+int kv8_grid(int batch, int max_seqlen_q, int nheads_q, int nheads_kv, int page_size,
+             int max_pages_per_seq) {
     const long long groups =
         (static_cast<long long>(max_seqlen_q) * (nheads_q / nheads_kv) + kKv8Rows - 1) / kKv8Rows;
-    const long long ctas = static_cast<long long>(batch) * nheads_kv * groups;
     const long long keys = static_cast<long long>(max_pages_per_seq) * page_size;
-    if (ctas <= 0) return 1;
-    const long long by_len = (keys + 2047) / 2048 < 16 ? (keys + 2047) / 2048 : 16;
-    const long long by_sms = (4LL * 2 * kGb300Sms + ctas - 1) / ctas;
     const long long chunks = (keys + kKv8Chunk - 1) / kKv8Chunk;
-    long long s = by_len > by_sms ? by_len : by_sms;
-    if (s > chunks) s = chunks;
-    if (s > kKv8MaxSplits) s = kKv8MaxSplits;
-    return static_cast<int>(s < 1 ? 1 : s);
+    const long long units = static_cast<long long>(batch) * groups;
+    if (units > ((1LL << 31) - 1) / chunks) return 0;
+    const long long cap = 2 * kGb300Sms / nheads_kv;
+    const long long n = (units * chunks + kKv8MinShare - 1) / kKv8MinShare;
+    return static_cast<int>(n < 1 || cap < 1 ? 1 : n < cap ? n : cap) * nheads_kv;
 }
 
-size_t kv8_partial_bytes(long long rows, int head_dim, int splits) {
-    if (splits <= 1) return 0;
-    return align_up(static_cast<size_t>(rows) * splits * head_dim * sizeof(float), 256) +
-           align_up(static_cast<size_t>(rows) * splits * sizeof(float), 256);
+// The parts of cut units, their LSE, and the CTAs' entries for the merge.
+size_t kv8_partial_bytes(int grid, int head_dim) {
+    if (grid <= 0) return 0;
+    const size_t rows = 2 * static_cast<size_t>(grid) * kKv8Rows;
+    return align_up(rows * head_dim * sizeof(float), 256) + align_up(rows * sizeof(float), 256) +
+           align_up(grid * sizeof(int4), 256);
 }
 
 // The rotated queries (f16) and their units.
@@ -878,38 +877,23 @@ size_t kv8_query_bytes(long long rows, int head_dim, int rotary_dim) {
            align_up(static_cast<size_t>(rows) * sizeof(float), 256);
 }
 
-// The attention kernel and, for more than one split, the combine.
+// The attention kernel and the merge of the units it cut.
 attn_status_t kv8_attend(Kv8Params& kp, const void* k_cache, const void* v_cache, int head_dim,
-                         void* partials, cudaStream_t s) {
+                         int grid, bool after_append, void* partials, cudaStream_t s) {
     const uint64_t cache_rows = static_cast<uint64_t>(kp.num_pages) * kp.page_size;
-    kp.box_rows = kp.page_size < kKv8Chunk ? kp.page_size : kKv8Chunk;
+    kp.box_rows = kp.page_size % kKv8Chunk == 0 ? kKv8Chunk : kp.page_size < 64 ? kp.page_size : 64;
     if (encode_kv8(&kp.tm_k, k_cache, head_dim, kp.Hkv, cache_rows, kp.box_rows) != ATTN_OK ||
         encode_kv8(&kp.tm_v, v_cache, head_dim, kp.Hkv, cache_rows, kp.box_rows) != ATTN_OK)
         return ATTN_ERR_CUDA;
-    if (kp.num_splits > 1) {
-        const size_t rows = static_cast<size_t>(kp.total_q) * kp.Hq;
-        kp.part_o = static_cast<float*>(partials);
-        kp.part_lse = reinterpret_cast<float*>(
-            static_cast<uint8_t*>(partials) +
-            align_up(rows * kp.num_splits * head_dim * sizeof(float), 256));
-    }
-    if (launch_kv8_attn(kp, head_dim, s) != cudaSuccess) return ATTN_ERR_CUDA;
-    if (kp.num_splits > 1) {
-        Kv8CombineParams cp;
-        cp.part_o = kp.part_o;
-        cp.part_lse = kp.part_lse;
-        cp.out = kp.out;
-        cp.lse = kp.lse;
-        cp.cu_q = kp.cu_q;
-        cp.batch = kp.batch;
-        cp.total_q = kp.total_q;
-        cp.Hq = kp.Hq;
-        cp.num_splits = kp.num_splits;
-        cp.lse_head = kp.lse_head;
-        cp.lse_tok = kp.lse_tok;
-        if (launch_kv8_combine(cp, head_dim, s) != cudaSuccess) return ATTN_ERR_CUDA;
-    }
-    return ATTN_OK;
+    const size_t rows = 2 * static_cast<size_t>(grid) * kKv8Rows;
+    uint8_t* ws = static_cast<uint8_t*>(partials);
+    kp.part_o = reinterpret_cast<float*>(ws);
+    ws += align_up(rows * head_dim * sizeof(float), 256);
+    kp.part_lse = reinterpret_cast<float*>(ws);
+    ws += align_up(rows * sizeof(float), 256);
+    kp.meta = reinterpret_cast<int4*>(ws);
+    return launch_kv8_attn(kp, head_dim, grid, after_append, s) == cudaSuccess ? ATTN_OK
+                                                                               : ATTN_ERR_CUDA;
 }
 
 }  // namespace
@@ -1008,29 +992,25 @@ attn_status_t attn_kvcache_read_fp8(const void* k_cache, const void* v_cache, co
 
 size_t attn_decode_kvcache_fp8_workspace_bytes(int batch, int nheads_q, int nheads_kv,
                                                int head_dim, int page_size,
-                                               int max_pages_per_seq, int num_splits) {
+                                               int max_pages_per_seq) {
     if (batch <= 0 || nheads_q <= 0 || nheads_kv <= 0 || nheads_q % nheads_kv != 0 ||
-        num_splits < 0 || num_splits > kKv8MaxSplits ||
         kv8_sizes(batch, nheads_kv, head_dim, page_size, max_pages_per_seq, 1) != ATTN_OK)
         return 0;
-    const int S = num_splits != 0 ? num_splits
-                                  : kv8_splits(batch, 1, nheads_q, nheads_kv, page_size,
-                                               max_pages_per_seq);
-    return kv8_partial_bytes(static_cast<long long>(batch) * nheads_q, head_dim, S);
+    return kv8_partial_bytes(
+        kv8_grid(batch, 1, nheads_q, nheads_kv, page_size, max_pages_per_seq), head_dim);
 }
 
 attn_status_t attn_decode_kvcache_fp8(const void* q, const void* k_cache, const void* v_cache,
                                       const void* k_scale, const void* v_scale,
                                       const int32_t* cache_seqlens, const int32_t* block_table,
-                                      int page_size, int num_splits, void* out, float* lse,
-                                      int batch, int nheads_q, int nheads_kv, int head_dim,
+                                      int page_size, void* out, float* lse, int batch,
+                                      int nheads_q, int nheads_kv, int head_dim,
                                       int max_pages_per_seq, int num_pages, float softmax_scale,
                                       void* workspace, size_t workspace_bytes, void* stream) {
     NvtxRange nvtx_range("attn_decode_kvcache_fp8");
     attn_status_t st = kv8_sizes(batch, nheads_kv, head_dim, page_size, max_pages_per_seq, num_pages);
     if (st != ATTN_OK) return st;
-    if (nheads_q <= 0 || nheads_q % nheads_kv != 0 || num_splits < 0 ||
-        num_splits > kKv8MaxSplits || !scale_ok(softmax_scale))
+    if (nheads_q <= 0 || nheads_q % nheads_kv != 0 || !scale_ok(softmax_scale))
         return ATTN_ERR_INVALID_ARG;
     if (static_cast<long long>(batch) * nheads_q > (1LL << 31) - 1) return ATTN_ERR_UNSUPPORTED;
     if (batch == 0) return ATTN_OK;
@@ -1038,11 +1018,9 @@ attn_status_t attn_decode_kvcache_fp8(const void* q, const void* k_cache, const 
         !out || !lse || !aligned(q, 16) || !aligned(out, 16) || !aligned(lse, 4) ||
         !aligned(cache_seqlens, 4))
         return ATTN_ERR_INVALID_ARG;
-    const int S = num_splits != 0 ? num_splits
-                                  : kv8_splits(batch, 1, nheads_q, nheads_kv, page_size,
-                                               max_pages_per_seq);
-    const size_t need = kv8_partial_bytes(static_cast<long long>(batch) * nheads_q, head_dim, S);
-    if (need > 0 && (!workspace || workspace_bytes < need || !aligned(workspace, 256)))
+    const int grid = kv8_grid(batch, 1, nheads_q, nheads_kv, page_size, max_pages_per_seq);
+    if (grid == 0) return ATTN_ERR_UNSUPPORTED;
+    if (!workspace || workspace_bytes < kv8_partial_bytes(grid, head_dim) || !aligned(workspace, 256))
         return ATTN_ERR_WORKSPACE;
     DeviceState* dev = nullptr;
     st = device_state(&dev);
@@ -1066,13 +1044,13 @@ attn_status_t attn_decode_kvcache_fp8(const void* q, const void* k_cache, const 
     kp.page_size = page_size;
     kp.max_pages = max_pages_per_seq;
     kp.num_pages = num_pages;
-    kp.num_splits = S;
     kp.causal = 1;
     kp.wl = kp.wr = -1;
     kp.lse_head = 1;
     kp.lse_tok = nheads_q;
     kp.scale_log2 = softmax_scale * kLog2eF;
-    return kv8_attend(kp, k_cache, v_cache, head_dim, workspace, static_cast<cudaStream_t>(stream));
+    return kv8_attend(kp, k_cache, v_cache, head_dim, grid, false, workspace,
+                      static_cast<cudaStream_t>(stream));
 }
 
 size_t attn_fwd_kvcache_fp8_workspace_bytes(int batch, int total_q, int max_seqlen_q,
@@ -1083,9 +1061,10 @@ size_t attn_fwd_kvcache_fp8_workspace_bytes(int batch, int total_q, int max_seql
         nheads_kv <= 0 || nheads_q % nheads_kv != 0 || rotary_dim < 0 ||
         kv8_sizes(batch, nheads_kv, head_dim, page_size, max_pages_per_seq, 1) != ATTN_OK)
         return 0;
-    return kv8_query_bytes(static_cast<long long>(total_q) * nheads_q, head_dim, rotary_dim) + kv8_partial_bytes(static_cast<long long>(total_q) * nheads_q, head_dim,
-                                    kv8_splits(batch, max_seqlen_q, nheads_q, nheads_kv, page_size,
-                                               max_pages_per_seq));
+    return kv8_query_bytes(static_cast<long long>(total_q) * nheads_q, head_dim, rotary_dim) +
+           kv8_partial_bytes(kv8_grid(batch, max_seqlen_q, nheads_q, nheads_kv, page_size,
+                                      max_pages_per_seq),
+                             head_dim);
 }
 
 attn_status_t attn_fwd_kvcache_fp8(const void* q, const void* k_new, const void* v_new,
@@ -1114,6 +1093,8 @@ attn_status_t attn_fwd_kvcache_fp8(const void* q, const void* k_new, const void*
         !aligned(v_new, 16) || !aligned(out, 16) || !aligned(lse, 4) || !aligned(cache_seqlens, 4) ||
         !aligned(cu_seqlens_q, 4))
         return ATTN_ERR_INVALID_ARG;
+    const int grid = kv8_grid(batch, max_seqlen_q, nheads_q, nheads_kv, page_size, max_pages_per_seq);
+    if (grid == 0) return ATTN_ERR_UNSUPPORTED;
     const size_t need = attn_fwd_kvcache_fp8_workspace_bytes(
         batch, total_q, max_seqlen_q, max_total_k, nheads_q, nheads_kv, head_dim, page_size,
         max_pages_per_seq, rotary_dim);
@@ -1181,15 +1162,15 @@ attn_status_t attn_fwd_kvcache_fp8(const void* q, const void* k_new, const void*
     kp.page_size = page_size;
     kp.max_pages = max_pages_per_seq;
     kp.num_pages = num_pages;
-    kp.num_splits = kv8_splits(batch, max_seqlen_q, nheads_q, nheads_kv, page_size, max_pages_per_seq);
     kp.causal = causal ? 1 : 0;
     kp.wl = window_left;
     kp.wr = window_right;
     kp.lse_head = total_q;
     kp.lse_tok = 1;
     kp.scale_log2 = softmax_scale * kLog2eF;
-    return kv8_attend(kp, k_cache, v_cache, head_dim,
-                      ws + kv8_query_bytes(q_rows, head_dim, rotary_dim), s);
+    return kv8_attend(
+        kp, k_cache, v_cache, head_dim, grid, true,
+        ws + kv8_query_bytes(q_rows, head_dim, rotary_dim), s);
 }
 
 attn_status_t attn_selftest_wait_timeout(void* stream) {

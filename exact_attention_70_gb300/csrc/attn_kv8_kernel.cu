@@ -14,9 +14,11 @@
 //     row i's largest |q| just below 2^14: the 8 significant bits of bf16 fit f16's 11, and
 //     elements down to 2^-28 of the row's largest stay exact (below that the error is less than
 //     2^-39 of the largest);
-//   * O_i = 2^(E - 15) sum_j (P_ij 2^(15 + ev_j - E)) v_j with E the largest ev_j seen so far:
-//     P <= 1, so the f16 factor is at most 2^15, and it loses precision only below 2^-29 of a
-//     row's largest term.  When E grows, O is rescaled together with the running maximum.
+//   * O_i = 2^(E - 5) sum_j (P_ij 2^(5 + ev_j - E)) v_j with P = exp2(x - m), where the references
+//     m (of a row) and E (of a warp) only move when a logit passes m by more than 8 (log2) or
+//     an ev_j passes E by more than 2.  The f16 factor is then at most 2^15 and keeps its 11 bits
+//     down to 2^-14, i.e. for weights down to 2^-19 of a row's largest where the V scales are alike;
+//     below that it is off by less than 2^-30.  When a reference moves, O is rescaled.
 #include <cuda_bf16.h>
 
 #include "kernels.h"
@@ -28,26 +30,93 @@ namespace attn {
 namespace {
 
 constexpr float kLn2f = 0.69314718055994530942f;
-constexpr float kLog2e = 1.44269504088896340736f;
+constexpr float kMaxScale = 0x1p127f;  // the largest scale; byte 255 reads as infinity before it is NaN
+constexpr int kMinE = 8;  // E as a scale byte; its floor keeps 2^(5 - E) a normal number
 
 template <int D>
 struct Kv8Cfg {
     static constexpr int kTileBytes = kKv8Chunk * D;       // K (or V) codes of one chunk
     static constexpr int kStageBytes = 2 * kTileBytes;
-    static constexpr int kStages = D == 128 ? 6 : 12;
-    static constexpr int kOffScale = kStages * kStageBytes;  // [stage][K, V][64] scale bytes
-    static constexpr int kOffBar = kOffScale + kStages * 2 * kKv8Chunk;
-    static constexpr int kMergeStride = D + 4;               // floats a row of the merge buffer
-    static constexpr int kMergeBytes = 4 * kKv8Rows * kMergeStride * 4 + 2 * 4 * kKv8Rows * 4;
-    static_assert(kMergeBytes <= kOffScale, "merge buffer must fit in the stage ring");
+    static constexpr int kStages = D == 128 ? 3 : 6;
+    static constexpr int kOffScale = kStages * kStageBytes;  // [stage][K, V][kKv8Chunk] scale bytes
+    static constexpr int kOffMerge = kOffScale + kStages * 2 * kKv8Chunk;
+    static constexpr int kMergeStride = D + 4;               // floats a row: [16][kMergeStride] of O,
+    static constexpr int kMergeBytes = kKv8Rows * kMergeStride * 4 + 2 * 2 * 4 * kKv8Rows * 4;  // m, l
+    static constexpr int kOffBar = kOffMerge + kMergeBytes;
     static constexpr int kSmem = kOffBar + 256 + 1024;
+    static_assert(2 * (kSmem + 1024) <= 228 * 1024, "two CTAs per SM");
 };
 
 struct Kv8Bars {
-    uint64_t full[12], empty[12];
+    uint64_t full[6], empty[6];
     int abort_flag;
+    int fail[2];       // a consumer warp gave up in a segment of this parity
+    // the CTA's share of the work: chunks [start, start + count) of the list, the first of them
+    // chunk first_off of sequence first_seq's; share: what every CTA but the last ones takes
+    int first_seq, first_off, start, count, share;
 };
 static_assert(sizeof(Kv8Bars) <= 256, "barrier block");
+
+// One sequence as the kernel cuts it for a kv head: ng units of 16 packed query rows, each walking
+// the same nc chunks from chunk lo on (what any of the sequence's rows sees; at least one, so
+// that rows without keys are written too).
+struct Kv8Seq {
+    int q0, Lq, L, lo, nc, ng;
+    bool bad;
+};
+
+__device__ __forceinline__ Kv8Seq kv8_seq(const Kv8Params& p, int b) {
+    Kv8Seq s;
+    s.q0 = b;  // a decode call: one query a sequence, at the last of its keys
+    s.Lq = 1;
+    if (p.cu_q != nullptr) {
+        s.q0 = p.cu_q[b];
+        s.Lq = p.cu_q[b + 1] - s.q0;
+    }
+    long long keys = p.seqlens[b];
+    s.bad = keys < 0 || s.q0 < 0 || s.Lq < 0 || s.Lq > p.max_seqlen_q ||
+            static_cast<long long>(s.q0) + s.Lq > p.total_q;
+    if (p.cu_q != nullptr) keys += s.Lq;
+    s.bad = s.bad || keys > static_cast<long long>(p.max_pages) * p.page_size;
+    s.L = s.bad ? 0 : static_cast<int>(keys);
+    if (s.bad) s.Lq = 0;  // nothing of this sequence is computed
+    const KvRange r = kv_block_range(0, s.Lq - 1, s.Lq, s.L, kKv8Chunk, p.causal, p.wl, p.wr);
+    s.lo = r.lo;
+    s.nc = max(1, r.hi - r.lo);
+    s.ng = (s.Lq * p.g + kKv8Rows - 1) / kKv8Rows;
+    return s;
+}
+
+// Its chunks (the host has made sure that the whole list counts in 31 bits).
+__device__ __forceinline__ int kv8_work(const Kv8Seq& s) { return s.ng * s.nc; }
+
+// The walk over a CTA's share: segments, each a run of chunks of one unit.
+struct Kv8Walk {
+    int left, off;  // chunks still to do; the next chunk's position inside sequence b
+    int b;
+    Kv8Seq s;
+    int row0, rows, c0, c1;  // the current segment: chunks [c0, c1) of the sequence's list
+    bool first, last;             // it holds its unit's first / last chunk
+
+    __device__ __forceinline__ bool next(const Kv8Params& p) {
+        if (left <= 0) return false;
+        while (off >= kv8_work(s)) {
+            off = 0;
+            s = kv8_seq(p, ++b);
+        }
+        const int unit = off / s.nc, c = off - unit * s.nc;
+        const int len = min(s.nc - c, left);
+        row0 = unit * kKv8Rows;
+        rows = min(kKv8Rows, s.Lq * p.g - row0);
+        c0 = s.lo + c;
+        c1 = c0 + len;
+        first = c == 0;
+        last = c + len == s.nc;
+        off += len;
+        left -= len;
+        return true;
+    }
+};
 
 // Byte offset of the 16-byte unit u of row r in a tile of D-byte rows as TMA swizzles it: the
 // unit's index xor the row inside the 8 x 128-byte (D = 128) or 4 x 128-byte (D = 64) pattern.
@@ -57,6 +126,20 @@ __device__ __forceinline__ uint32_t kv8_unit(int r, int u) {
                                           : r * 64 + ((u ^ ((r >> 1) & 3)) << 4));
 }
 
+// Two scale bytes as floats (byte 0 is 2^-127).
+__device__ __forceinline__ void scale_pair(uint32_t w, float (&f)[2]) {
+    f[0] = __int_as_float(max(static_cast<int>((w & 0xffu) << 23), 0x00400000));
+    f[1] = __int_as_float(max(static_cast<int>((w & 0xff00u) << 15), 0x00400000));
+}
+
+// Persistent CTAs, two an SM.  For a kv head, the chunks of all units of all sequences form one
+// list, and the CTAs of that head take equal shares of it: every CTA reads the same number of
+// bytes whatever the sequences' lengths, and its ring of loads runs on from one segment to the
+// next.  CTA i has kv head i % Hkv and share i / Hkv, so that CTAs side by side walk the
+// same tokens for all heads and the cache's rows are read whole (with the heads one after the
+// other in one list, each access 128 bytes out of 1 KB, the 64-sequence case below took 562 us).
+// A unit cut by a share's border leaves partial results in the CTAs' slots (slot 1 of the CTA
+// that starts it, slot 0 of those that go on with it), which kv8_combine_kernel merges.
 template <int D>
 __global__ void __launch_bounds__(kKv8Threads, 2)
     kv8_split_kernel(const __grid_constant__ Kv8Params p) {
@@ -66,53 +149,69 @@ __global__ void __launch_bounds__(kKv8Threads, 2)
         (reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~static_cast<uintptr_t>(1023));
     Kv8Bars* bars = reinterpret_cast<Kv8Bars*>(smem + C::kOffBar);
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
-    const int S = p.num_splits;
-    const int split = blockIdx.x % S, hg = blockIdx.x / S;
-    const int kvh = blockIdx.y, b = blockIdx.z;
-
-    // The sequence: its query rows and keys.  A decode call has one query per sequence, at the
-    // last of cache_seqlens keys; a chunk's queries follow cache_seqlens cached keys.
-    int q0 = b, Lq = 1;
-    if (p.cu_q != nullptr) {
-        q0 = p.cu_q[b];
-        Lq = p.cu_q[b + 1] - q0;
-    }
-    const int kmax_keys = p.max_pages * p.page_size;
-    long long keys = p.seqlens[b];
-    bool bad = keys < 0 || q0 < 0 || Lq < 0 || Lq > p.max_seqlen_q ||
-               static_cast<long long>(q0) + Lq > p.total_q;
-    if (p.cu_q != nullptr) keys += Lq;
-    bad = bad || keys > kmax_keys;
-    if (bad) {  // the same decision in every thread: nothing of this sequence is computed
-        if (threadIdx.x == 0) atomicOr(p.status, kStatusBounds);
-        return;
-    }
-    const int L = static_cast<int>(keys);
-    const int row0 = hg * kKv8Rows;                    // first packed row: token r / g, head r % g
-    const int rows = min(kKv8Rows, Lq * p.g - row0);   // valid packed rows
-    if (rows <= 0) return;
+    const int cta = blockIdx.x, kvh = cta % p.Hkv, at_list = cta / p.Hkv;
+    griddep_launch_dependents();
 
     if (threadIdx.x == 0) {
         for (int i = 0; i < C::kStages; ++i) {
             mbar_init(&bars->full[i], 1);
             mbar_init(&bars->empty[i], 4);
         }
-        bars->abort_flag = 0;
+        bars->abort_flag = bars->fail[0] = bars->fail[1] = 0;
         mbar_fence_init();
     }
-    __syncthreads();
-    const Watchdog wd{&bars->abort_flag, p.status};
-
-    const int imin = row0 / p.g, imax = (row0 + rows - 1) / p.g;
-    const KvRange range = kv_block_range(imin, imax, Lq, L, kKv8Chunk, p.causal, p.wl, p.wr);
-    const int per = (range.hi - range.lo + S - 1) / S;
-    const int c0 = min(range.lo + split * per, range.hi), c1 = min(c0 + per, range.hi);
-
-    float m_run[2] = {-INFINITY, -INFINITY}, l_run[2] = {0.f, 0.f};
-    int e_run = 1;  // E as a scale byte
-    float o[D / 8][4];
+    if (warp == 4) {  // the list's length, the share, and where this CTA's starts
+        int total = 0;
+        for (int b0 = 0; b0 < p.batch; b0 += 32) {
+            int n = 0;
+            if (b0 + lane < p.batch) {
+                const Kv8Seq s = kv8_seq(p, b0 + lane);
+                if (s.bad && cta == 0) atomicOr(p.status, kStatusBounds);
+                n = kv8_work(s);
+            }
 #pragma unroll
-    for (int n = 0; n < D / 8; ++n) o[n][0] = o[n][1] = o[n][2] = o[n][3] = 0.f;
+            for (int o = 16; o > 0; o >>= 1) n += __shfl_xor_sync(0xffffffffu, n, o);
+            total += n;
+        }
+        const int share = max((total - 1) / static_cast<int>(gridDim.x / p.Hkv) + 1, kKv8MinShare);
+        const int start = static_cast<int>(min(static_cast<long long>(at_list) * share,
+                                               static_cast<long long>(total)));
+        const int count = min(share, total - start);
+        int before = 0;
+        for (int b0 = 0; count > 0 && b0 < p.batch; b0 += 32) {
+            const int n = b0 + lane < p.batch ? kv8_work(kv8_seq(p, b0 + lane)) : 0;
+            int upto = n;
+#pragma unroll
+            for (int o = 1; o < 32; o <<= 1) {
+                const int x = __shfl_up_sync(0xffffffffu, upto, o);
+                if (lane >= o) upto += x;
+            }
+            const int lo = before + upto - n;
+            if (lo <= start && start < lo + n) {
+                bars->first_seq = b0 + lane;
+                bars->first_off = start - lo;
+            }
+            before += __shfl_sync(0xffffffffu, upto, 31);
+            if (start < before) break;
+        }
+        if (lane == 0) {
+            bars->count = count;
+            bars->start = start;
+            bars->share = share;
+            // what kv8_combine_kernel finds of this CTA: nothing, until a segment ends a unit
+            // that an earlier CTA started
+            p.meta[cta] = make_int4(-1, 0, 0, 0);
+        }
+    }
+    __syncthreads();
+    Kv8Walk w;
+    w.left = bars->count;
+    if (w.left == 0) return;
+    w.off = bars->first_off;
+    w.b = bars->first_seq;
+    w.s = kv8_seq(p, w.b);
+    const Watchdog wd{&bars->abort_flag, p.status};
+    griddep_wait();  // what the append kernel before this one wrote
 
     if (warp == 4) {
         // ---- producer: lane i gathers piece i of each chunk through block_table ----
@@ -120,62 +219,70 @@ __global__ void __launch_bounds__(kKv8Threads, 2)
             tma_prefetch_desc(&p.tm_k);
             tma_prefetch_desc(&p.tm_v);
         }
-        const int* bt = p.block_table + static_cast<size_t>(b) * p.max_pages;
         const int pieces = kKv8Chunk / p.box_rows;
         uint32_t issued = 0;
         bool ok = true;
-        for (int c = c0; c < c1; ++c, ++issued) {
-            const uint32_t st = issued % C::kStages;
-            // Pieces wholly past the sequence end (whose table entries are never read) and pieces
-            // of a bad page are aimed past the end of the cache: TMA fills them with zeros.
-            int page = p.num_pages, slot = 0;
-            bool real = false;
-            if (lane < pieces) {
-                const int key = c * kKv8Chunk + lane * p.box_rows;
-                if (key < L) {
-                    page = bt[key / p.page_size];
-                    slot = key % p.page_size;
-                    real = page >= 0 && page < p.num_pages;
-                    if (!real) {
-                        atomicOr(p.status, kStatusBounds);
-                        page = p.num_pages;
-                        slot = 0;
+        while (ok && w.next(p)) {
+            const int* bt = p.block_table + static_cast<size_t>(w.b) * p.max_pages;
+            for (int c = w.c0; c < w.c1; ++c, ++issued) {
+                const uint32_t st = issued % C::kStages;
+                // Pieces wholly past the sequence end (whose table entries are never read) and
+                // pieces of a bad page are aimed past the end of the cache: TMA fills them with
+                // zeros.
+                int page = p.num_pages, slot = 0;
+                bool real = false;
+                if (lane < pieces) {
+                    const int key = c * kKv8Chunk + lane * p.box_rows;
+                    if (key < w.s.L) {
+                        page = bt[key / p.page_size];
+                        slot = key % p.page_size;
+                        real = page >= 0 && page < p.num_pages;
+                        if (!real) {
+                            atomicOr(p.status, kStatusBounds);
+                            page = p.num_pages;
+                            slot = 0;
+                        }
                     }
                 }
-            }
-            if (issued >= C::kStages)
-                ok = wd.wait(&bars->empty[st], ((issued / C::kStages) - 1) & 1);
-            if (!__all_sync(0xffffffffu, ok)) break;
-            uint8_t* kdst = smem + st * C::kStageBytes;
-            uint8_t* sdst = smem + C::kOffScale + st * 2 * kKv8Chunk;
-            if (lane < pieces && !real) {  // no scales to copy: zero bytes (2^-127)
-                for (int i = 0; i < p.box_rows; i += 16) {
-                    *reinterpret_cast<uint4*>(sdst + lane * p.box_rows + i) = make_uint4(0, 0, 0, 0);
-                    *reinterpret_cast<uint4*>(sdst + kKv8Chunk + lane * p.box_rows + i) =
-                        make_uint4(0, 0, 0, 0);
+                if (issued >= C::kStages)
+                    ok = wd.wait(&bars->empty[st], ((issued / C::kStages) - 1) & 1);
+                ok = __all_sync(0xffffffffu, ok);
+                if (!ok) break;
+                uint8_t* kdst = smem + st * C::kStageBytes;
+                uint8_t* sdst = smem + C::kOffScale + st * 2 * kKv8Chunk;
+                if (lane < pieces && !real) {  // no scales to copy: zero bytes
+                    for (int i = 0; i < p.box_rows; i += 16) {
+                        *reinterpret_cast<uint4*>(sdst + lane * p.box_rows + i) =
+                            make_uint4(0, 0, 0, 0);
+                        *reinterpret_cast<uint4*>(sdst + kKv8Chunk + lane * p.box_rows + i) =
+                            make_uint4(0, 0, 0, 0);
+                    }
+                    fence_proxy_async_smem();
                 }
-                fence_proxy_async_smem();
-            }
-            const int n_real = __popc(__ballot_sync(0xffffffffu, real));
-            if (lane == 0)
-                mbar_arrive_expect_tx(&bars->full[st], C::kStageBytes + 2 * p.box_rows * n_real);
-            __syncwarp();
-            if (lane < pieces) {
-                const int row = page * p.page_size + slot;
-                tma_load_3d(kdst + lane * p.box_rows * D, &p.tm_k, &bars->full[st], 0, kvh, row);
-                tma_load_3d(kdst + C::kTileBytes + lane * p.box_rows * D, &p.tm_v, &bars->full[st],
-                            0, kvh, row);
-                if (real) {
-                    const size_t at = (static_cast<size_t>(page) * p.Hkv + kvh) * p.page_size + slot;
-                    bulk_load(sdst + lane * p.box_rows, p.k_scale + at, p.box_rows, &bars->full[st]);
-                    bulk_load(sdst + kKv8Chunk + lane * p.box_rows, p.v_scale + at, p.box_rows,
-                              &bars->full[st]);
+                const int n_real = __popc(__ballot_sync(0xffffffffu, real));
+                if (lane == 0)
+                    mbar_arrive_expect_tx(&bars->full[st], C::kStageBytes + 2 * p.box_rows * n_real);
+                __syncwarp();
+                if (lane < pieces) {
+                    const int row = page * p.page_size + slot;
+                    tma_load_3d(kdst + lane * p.box_rows * D, &p.tm_k, &bars->full[st], 0, kvh,
+                                row);
+                    tma_load_3d(kdst + C::kTileBytes + lane * p.box_rows * D, &p.tm_v,
+                                &bars->full[st], 0, kvh, row);
+                    if (real) {
+                        const size_t at =
+                            (static_cast<size_t>(page) * p.Hkv + kvh) * p.page_size + slot;
+                        bulk_load(sdst + lane * p.box_rows, p.k_scale + at, p.box_rows,
+                                  &bars->full[st]);
+                        bulk_load(sdst + kKv8Chunk + lane * p.box_rows, p.v_scale + at, p.box_rows,
+                                  &bars->full[st]);
+                    }
                 }
             }
         }
         __syncwarp();
-        // every load still in flight lands before the ring is reused for the merge; one that
-        // never does raises the timeout status and the abort flag
+        // every load still in flight lands before the CTA's shared memory goes; one that never
+        // does raises the timeout status and the abort flag
         if (lane == 0) {
             const uint32_t n_st = issued < C::kStages ? issued : C::kStages;
             for (uint32_t st = 0; st < n_st; ++st) {
@@ -194,10 +301,23 @@ __global__ void __launch_bounds__(kKv8Threads, 2)
                 }
             }
         }
-        __syncwarp();
-    } else {
-        // ---- consumers: warp w owns keys [16 w, 16 w + 16) of every chunk ----
-        const int gq = lane >> 2, tq = lane & 3;
+        return;
+    }
+
+    // ---- consumers: warp w owns keys [32 w, 32 w + 32) of every chunk ----
+    const int gq = lane >> 2, tq = lane & 3;
+    const int mi = lane >> 3, ri = lane & 7;  // ldmatrix: matrix id, row within matrix
+    float* const mo = reinterpret_cast<float*>(smem + C::kOffMerge);   // [16 rows][kMergeStride]
+    float* const ml_all = mo + kKv8Rows * C::kMergeStride;             // [parity][m, l][4][16]
+    uint32_t n = 0;  // chunks consumed
+    for (int seg = 0; w.next(p); ++seg) {
+        const int Lq = w.s.Lq, L = w.s.L, q0 = w.s.q0, rows = w.rows, row0 = w.row0;
+        float m_run[2] = {-INFINITY, -INFINITY};
+        uint64_t l2[2] = {0, 0};  // the rows' denominators, even and odd keys apart
+        int e_run = kMinE;        // E as a scale byte
+        float o[D / 8][4];
+#pragma unroll
+        for (int x = 0; x < D / 8; ++x) o[x][0] = o[x][1] = o[x][2] = o[x][3] = 0.f;
         // Q as the A operand.  An f16 k-step covers 16 elements of d; the thread's four k slots
         // {2 tq, 2 tq + 1, 2 tq + 8, 2 tq + 9} stand for elements 4 tq .. 4 tq + 3 of them, the
         // four bytes ldmatrix hands it of a key's 16.
@@ -215,22 +335,22 @@ __global__ void __launch_bounds__(kKv8Threads, 2)
                 c_row[h] = p.scale_log2 * p.q_unit[row];
 #pragma unroll
                 for (int s = 0; s < D / 16; ++s) {
-                    const uint2 w = r < rows ? src[4 * s] : make_uint2(0u, 0u);
-                    qa[s][h] = w.x;
-                    qa[s][h + 2] = w.y;
+                    const uint2 x = r < rows ? src[4 * s] : make_uint2(0u, 0u);
+                    qa[s][h] = x.x;
+                    qa[s][h + 2] = x.y;
                 }
                 continue;
             }
             const uint2* src = reinterpret_cast<const uint2*>(p.q + row * D + 4 * tq);
-            uint2 w[D / 16];
+            uint2 qw[D / 16];
             int top = 0;
 #pragma unroll
             for (int s = 0; s < D / 16; ++s) {
-                w[s] = r < rows ? src[4 * s] : make_uint2(0u, 0u);
-                top = max(max(top, static_cast<int>(w[s].x & 0x7fff)),
-                          static_cast<int>((w[s].x >> 16) & 0x7fff));
-                top = max(max(top, static_cast<int>(w[s].y & 0x7fff)),
-                          static_cast<int>((w[s].y >> 16) & 0x7fff));
+                qw[s] = r < rows ? src[4 * s] : make_uint2(0u, 0u);
+                top = max(max(top, static_cast<int>(qw[s].x & 0x7fff)),
+                          static_cast<int>((qw[s].x >> 16) & 0x7fff));
+                top = max(max(top, static_cast<int>(qw[s].y & 0x7fff)),
+                          static_cast<int>((qw[s].y >> 16) & 0x7fff));
             }
             top = max(top, __shfl_xor_sync(0xffffffffu, top, 1));
             top = max(top, __shfl_xor_sync(0xffffffffu, top, 2));
@@ -239,233 +359,323 @@ __global__ void __launch_bounds__(kKv8Threads, 2)
             c_row[h] = p.scale_log2 * __int_as_float((127 - a) << 23);
 #pragma unroll
             for (int s = 0; s < D / 16; ++s) {
-                qa[s][h] = pack_f16x2(__uint_as_float(w[s].x << 16) * up,
-                                      __uint_as_float(w[s].x & 0xffff0000u) * up);
-                qa[s][h + 2] = pack_f16x2(__uint_as_float(w[s].y << 16) * up,
-                                          __uint_as_float(w[s].y & 0xffff0000u) * up);
+                qa[s][h] = pack_f16x2(__uint_as_float(qw[s].x << 16) * up,
+                                      __uint_as_float(qw[s].x & 0xffff0000u) * up);
+                qa[s][h + 2] = pack_f16x2(__uint_as_float(qw[s].y << 16) * up,
+                                          __uint_as_float(qw[s].y & 0xffff0000u) * up);
             }
         }
-        // keys every row of the CTA sees: [full_lo, full_hi]
+        // keys every row of the unit sees: [full_lo, full_hi]
         int full_lo, full_hi;
         {
             int lo, hi;
-            row_key_interval(imin, Lq, L, p.causal, p.wl, p.wr, lo, full_hi);
-            row_key_interval(imax, Lq, L, p.causal, p.wl, p.wr, full_lo, hi);
+            row_key_interval(row0 / p.g, Lq, L, p.causal, p.wl, p.wr, lo, full_hi);
+            row_key_interval((row0 + rows - 1) / p.g, Lq, L, p.causal, p.wl, p.wr, full_lo, hi);
         }
-        const int mi = lane >> 3, ri = lane & 7;  // ldmatrix: matrix id, row within matrix
-        for (int c = c0; c < c1; ++c) {
-            const uint32_t n = c - c0, st = n % C::kStages;
-            if (!__all_sync(0xffffffffu, wd.wait(&bars->full[st], (n / C::kStages) & 1))) break;
-            const uint8_t* kst = smem + st * C::kStageBytes;
-            const uint8_t* sst = smem + C::kOffScale + st * 2 * kKv8Chunk + warp * 16;
-            const int key0 = c * kKv8Chunk + warp * 16;
-            const int nvalid = min(16, L - key0);
-            if (nvalid > 0) {
-                // S (16 rows x 16 keys) = Q K^T on the codes
-                float s[2][4] = {{0.f, 0.f, 0.f, 0.f}, {0.f, 0.f, 0.f, 0.f}};
-                const uint32_t kbase = smem_u32(kst);
-                const int key = warp * 16 + (mi & 1) * 8 + ri;
+        const uint64_t c2[2] = {f2_make(c_row[0], c_row[0]), f2_make(c_row[1], c_row[1])};
+        bool ok = true;
+        for (int c = w.c0; c < w.c1; ++c, ++n) {
+            const uint32_t st = n % C::kStages;
+            ok = __all_sync(0xffffffffu, wd.wait(&bars->full[st], (n / C::kStages) & 1));
+            if (!ok) break;
+            const uint32_t kbase = smem_u32(smem + st * C::kStageBytes);
+            const uint32_t sbase =
+                smem_u32(smem + C::kOffScale + st * 2 * kKv8Chunk) + warp * 32 + 2 * tq;
+            const int key0 = c * kKv8Chunk + warp * 32;
+            if (key0 < L) {
+                // S (16 rows x 32 keys) = Q K^T on the codes; the thread's keys are
+                // 8 nt + 2 tq + {0, 1} of the four n-tiles
+                float s[4][4];
+#pragma unroll
+                for (int nt = 0; nt < 4; ++nt) s[nt][0] = s[nt][1] = s[nt][2] = s[nt][3] = 0.f;
+                const int key = warp * 32 + (mi & 1) * 8 + ri;
 #pragma unroll
                 for (int u = 0; u < D / 16; u += 2) {
-                    uint32_t r0, r1, r2, r3;
-                    ldmatrix_x4(kbase + kv8_unit<D>(key, u + (mi >> 1)), r0, r1, r2, r3);
-                    mma_f16_16816(s[0], qa[u], e4m3x2_to_f16x2(r0), e4m3x2_to_f16x2(r0 >> 16));
-                    mma_f16_16816(s[1], qa[u], e4m3x2_to_f16x2(r1), e4m3x2_to_f16x2(r1 >> 16));
-                    mma_f16_16816(s[0], qa[u + 1], e4m3x2_to_f16x2(r2), e4m3x2_to_f16x2(r2 >> 16));
-                    mma_f16_16816(s[1], qa[u + 1], e4m3x2_to_f16x2(r3), e4m3x2_to_f16x2(r3 >> 16));
-                }
-                // the thread's keys are 8 nt + 2 tq + {0, 1}: their scale bytes, and for V
-                // the largest of the tile's valid keys
-                int kb[4], vb[4], e_tile = 1;
 #pragma unroll
-                for (int i = 0; i < 4; ++i) {
-                    const int col = (i >> 1) * 8 + 2 * tq + (i & 1);
-                    kb[i] = sst[col];
-                    vb[i] = col < nvalid ? sst[kKv8Chunk + col] : 0;
-                    e_tile = max(e_tile, vb[i]);
-                }
-                e_tile = max(e_tile, __shfl_xor_sync(0xffffffffu, e_tile, 1));
-                e_tile = max(e_tile, __shfl_xor_sync(0xffffffffu, e_tile, 2));
-                const int e_new = max(e_run, e_tile);
-                const float e_drop = exp2_int(e_run - e_new);
-                e_run = e_new;
-                const bool masked = key0 < full_lo || key0 + 15 > full_hi;
+                    for (int h = 0; h < 2; ++h) {
+                        uint32_t r[4], b[8];
+                        ldmatrix_x4(kbase + kv8_unit<D>(key + 16 * h, u + (mi >> 1)), r[0], r[1],
+                                    r[2], r[3]);
 #pragma unroll
-                for (int nt = 0; nt < 2; ++nt)
-#pragma unroll
-                    for (int e = 0; e < 4; ++e) {
-                        const int j = key0 + nt * 8 + 2 * tq + (e & 1);
-                        float x = s[nt][e] * c_row[e >> 1] * e8m0_to_f32(kb[2 * nt + (e & 1)]);
-                        if (masked && (j < kmin[e >> 1] || j > kmax[e >> 1])) x = -INFINITY;
-                        s[nt][e] = x;
+                        for (int i = 0; i < 4; ++i) e4m3x4_to_f16x2(r[i], b[2 * i], b[2 * i + 1]);
+                        mma_f16_16816(s[2 * h], qa[u], b[0], b[1]);
+                        mma_f16_16816(s[2 * h + 1], qa[u], b[2], b[3]);
+                        mma_f16_16816(s[2 * h], qa[u + 1], b[4], b[5]);
+                        mma_f16_16816(s[2 * h + 1], qa[u + 1], b[6], b[7]);
                     }
-                float alpha[2], m_use[2];
+                }
+                // the keys' scales, in pairs: 2^(b - 127) is the float with exponent field b
+                float ks[4][2], vs[4][2];
+                float k_top = 0.f, v_top = 0.f;
+#pragma unroll
+                for (int nt = 0; nt < 4; ++nt) {
+                    scale_pair(ld_shared_u16(sbase + 8 * nt), ks[nt]);
+                    scale_pair(ld_shared_u16(sbase + kKv8Chunk + 8 * nt), vs[nt]);
+                }
+                uint32_t sel[4] = {0x3120u, 0x3120u, 0x3120u, 0x3120u};
+                const bool masked = key0 < full_lo || key0 + 31 > full_hi;
+                if (masked && key0 + 32 > L) {
+                    // keys past the end: their slots may hold anything
+#pragma unroll
+                    for (int nt = 0; nt < 4; ++nt) {
+                        const int j = key0 + 8 * nt + 2 * tq;
+                        if (j >= L) ks[nt][0] = vs[nt][0] = 0.f;
+                        if (j + 1 >= L) ks[nt][1] = vs[nt][1] = 0.f;
+                        sel[nt] = (j < L ? 0x0100u : 0x0404u) | (j + 1 < L ? 0x3020u : 0x4040u);
+                    }
+                }
+#pragma unroll
+                for (int nt = 0; nt < 4; ++nt) {
+                    k_top = fmax3(k_top, ks[nt][0], ks[nt][1]);
+                    v_top = fmax3(v_top, vs[nt][0], vs[nt][1]);
+                }
+                if (__any_sync(0xffffffffu, k_top > kMaxScale)) {  // byte 255 stands for NaN
+#pragma unroll
+                    for (int nt = 0; nt < 4; ++nt)
+#pragma unroll
+                        for (int i = 0; i < 2; ++i)
+                            if (ks[nt][i] > kMaxScale) ks[nt][i] = __int_as_float(0x7fffffff);
+                }
+#pragma unroll
+                for (int nt = 0; nt < 4; ++nt) {
+                    const uint64_t kp = f2_make(ks[nt][0], ks[nt][1]);
+                    f2_split(f2_mul(f2_make(s[nt][0], s[nt][1]), kp), s[nt][0], s[nt][1]);
+                    f2_split(f2_mul(f2_make(s[nt][2], s[nt][3]), kp), s[nt][2], s[nt][3]);
+                }
+                if (masked) {
+#pragma unroll
+                    for (int nt = 0; nt < 4; ++nt)
+#pragma unroll
+                        for (int e = 0; e < 4; ++e) {
+                            const int j = key0 + nt * 8 + 2 * tq + (e & 1);
+                            if (j < kmin[e >> 1] || j > kmax[e >> 1]) s[nt][e] = -INFINITY;
+                        }
+                }
+                // The references move only when a row's maximum passes m by more than 8 or a V
+                // scale passes E by more than 2: the weights stay below 2^8, their f16 form
+                // P 2^(5 + ev - E) below 2^15, and most chunks leave O alone.
+                float mx[2];
 #pragma unroll
                 for (int r = 0; r < 2; ++r) {
-                    float mx = fmaxf(fmaxf(s[0][2 * r], s[0][2 * r + 1]),
-                                     fmaxf(s[1][2 * r], s[1][2 * r + 1]));
-                    mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, 1));
-                    mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, 2));
-                    const float m_new = fmaxf(m_run[r], mx);
-                    m_use[r] = m_new == -INFINITY ? 0.f : m_new;  // no key seen yet
-                    alpha[r] = ex2_approx(m_run[r] - m_use[r]);
-                    m_run[r] = m_new;
+                    float x = fmax3(s[0][2 * r], s[0][2 * r + 1], s[1][2 * r]);
+                    x = fmax3(x, s[1][2 * r + 1], s[2][2 * r]);
+                    x = fmax3(x, s[2][2 * r + 1], s[3][2 * r]);
+                    x = fmaxf(x, s[3][2 * r + 1]);
+                    x = fmaxf(x, __shfl_xor_sync(0xffffffffu, x, 1));
+                    x = fmaxf(x, __shfl_xor_sync(0xffffffffu, x, 2));
+                    mx[r] = x * c_row[r];
                 }
-                uint32_t pa[4];
-                float rs[2] = {0.f, 0.f};
+                const bool m_moves = mx[0] > m_run[0] + 8.f || mx[1] > m_run[1] + 8.f;
+                const bool e_moves = v_top > __int_as_float((e_run + 2) << 23);
+                if (__any_sync(0xffffffffu, m_moves || e_moves)) {
+                    int e_new = __float_as_int(v_top) >> 23;
 #pragma unroll
-                for (int nt = 0; nt < 2; ++nt) {
-                    const float f0 = exp2_int(15 + vb[2 * nt] - e_run);
-                    const float f1 = exp2_int(15 + vb[2 * nt + 1] - e_run);
-                    const float p0 = ex2_approx(s[nt][0] - m_use[0]);
-                    const float p1 = ex2_approx(s[nt][1] - m_use[0]);
-                    const float p2 = ex2_approx(s[nt][2] - m_use[1]);
-                    const float p3 = ex2_approx(s[nt][3] - m_use[1]);
-                    rs[0] += p0 + p1;
-                    rs[1] += p2 + p3;
-                    pa[2 * nt + 0] = pack_f16x2(p0 * f0, p1 * f1);
-                    pa[2 * nt + 1] = pack_f16x2(p2 * f0, p3 * f1);
+                    for (int i = 16; i > 0; i >>= 1)
+                        e_new = max(e_new, __shfl_xor_sync(0xffffffffu, e_new, i));
+                    e_new = max(e_run, e_new);
+                    const float e_drop = exp2_int(e_run - e_new);
+                    e_run = min(e_new, 252);
+                    float alpha[2];
+#pragma unroll
+                    for (int r = 0; r < 2; ++r) {
+                        const float m_new = fmaxf(m_run[r], mx[r]);
+                        alpha[r] = m_new == -INFINITY ? 1.f : ex2_approx(m_run[r] - m_new);
+                        m_run[r] = m_new;
+                        l2[r] = f2_mul(l2[r], f2_make(alpha[r], alpha[r]));
+                        alpha[r] *= e_drop;
+                    }
+                    // a V scale byte of 255: every output of the rows becomes NaN
+                    if (e_new == 255) alpha[0] = alpha[1] = __int_as_float(0x7fffffff);
+#pragma unroll
+                    for (int x = 0; x < D / 8; ++x)
+#pragma unroll
+                        for (int e = 0; e < 4; ++e) o[x][e] *= alpha[e >> 1];
                 }
-                l_run[0] = l_run[0] * alpha[0] + rs[0];
-                l_run[1] = l_run[1] * alpha[1] + rs[1];
-                alpha[0] *= e_drop;
-                alpha[1] *= e_drop;
+                const uint64_t inv = f2_make(exp2_int(132 - e_run), exp2_int(132 - e_run));
+                uint64_t nm[2];
 #pragma unroll
-                for (int x = 0; x < D / 8; ++x)
+                for (int r = 0; r < 2; ++r) {
+                    const float m = m_run[r] == -INFINITY ? 0.f : -m_run[r];  // no key seen yet
+                    nm[r] = f2_make(m, m);
+                }
+                uint32_t pa[2][4];  // P as the A operand of two k-steps of 16 keys
 #pragma unroll
-                    for (int e = 0; e < 4; ++e) o[x][e] *= alpha[e >> 1];
+                for (int nt = 0; nt < 4; ++nt) {
+                    const uint64_t f = f2_mul(f2_make(vs[nt][0], vs[nt][1]), inv);
+#pragma unroll
+                    for (int r = 0; r < 2; ++r) {
+                        float x0, x1;
+                        f2_split(f2_fma(f2_make(s[nt][2 * r], s[nt][2 * r + 1]), c2[r], nm[r]), x0, x1);
+                        const uint64_t pp = f2_make(ex2_approx(x0), ex2_approx(x1));
+                        l2[r] = f2_add(l2[r], pp);
+                        f2_split(f2_mul(pp, f), x0, x1);
+                        pa[nt >> 1][2 * (nt & 1) + r] = pack_f16x2(x0, x1);
+                    }
+                }
                 // O += P V.  A transposed 8 x 8 matrix of byte pairs gives the thread elements
                 // 2 gq, 2 gq + 1 of keys 2 tq, 2 tq + 1: the pair of even elements is one n-tile's
                 // operand, the odd pair the next one's.  The selector puts them in that order and
-                // takes zeros for keys past the end, whose slots may hold anything.
-                const uint32_t sel0 = (2 * tq < nvalid ? 0x0100u : 0x0404u) |
-                                      (2 * tq + 1 < nvalid ? 0x3020u : 0x4040u);
-                const uint32_t sel1 = (2 * tq + 8 < nvalid ? 0x0100u : 0x0404u) |
-                                      (2 * tq + 9 < nvalid ? 0x3020u : 0x4040u);
+                // takes zeros for keys past the end.
                 const uint32_t vbase = kbase + C::kTileBytes;
 #pragma unroll
                 for (int u = 0; u < D / 16; u += 2) {
-                    uint32_t r0, r1, r2, r3;
-                    ldmatrix_x4_trans(vbase + kv8_unit<D>(key, u + (mi >> 1)), r0, r1, r2, r3);
-                    r0 = __byte_perm(r0, 0u, sel0);
-                    r1 = __byte_perm(r1, 0u, sel1);
-                    r2 = __byte_perm(r2, 0u, sel0);
-                    r3 = __byte_perm(r3, 0u, sel1);
-                    mma_f16_16816(o[2 * u], pa, e4m3x2_to_f16x2(r0), e4m3x2_to_f16x2(r1));
-                    mma_f16_16816(o[2 * u + 1], pa, e4m3x2_to_f16x2(r0 >> 16), e4m3x2_to_f16x2(r1 >> 16));
-                    mma_f16_16816(o[2 * u + 2], pa, e4m3x2_to_f16x2(r2), e4m3x2_to_f16x2(r3));
-                    mma_f16_16816(o[2 * u + 3], pa, e4m3x2_to_f16x2(r2 >> 16), e4m3x2_to_f16x2(r3 >> 16));
+#pragma unroll
+                    for (int h = 0; h < 2; ++h) {
+                        uint32_t r[4], b[8];
+                        ldmatrix_x4_trans(vbase + kv8_unit<D>(key + 16 * h, u + (mi >> 1)), r[0],
+                                          r[1], r[2], r[3]);
+#pragma unroll
+                        for (int i = 0; i < 4; ++i)
+                            e4m3x4_to_f16x2(__byte_perm(r[i], 0u, sel[2 * h + (i & 1)]), b[2 * i],
+                                            b[2 * i + 1]);
+                        mma_f16_16816(o[2 * u], pa[h], b[0], b[2]);
+                        mma_f16_16816(o[2 * u + 1], pa[h], b[1], b[3]);
+                        mma_f16_16816(o[2 * u + 2], pa[h], b[4], b[6]);
+                        mma_f16_16816(o[2 * u + 3], pa[h], b[5], b[7]);
+                    }
                 }
             }
             __syncwarp();
             if (lane == 0) mbar_arrive(&bars->empty[st]);
         }
+
+        // ---- the warps' results merge, in a fixed order ----
+        float* const mm = ml_all + (seg & 1) * 2 * 4 * kKv8Rows;  // [4][16] references m
+        float* const ml = mm + 4 * kKv8Rows;                      // [4][16] denominators
 #pragma unroll
         for (int r = 0; r < 2; ++r) {
-            l_run[r] += __shfl_xor_sync(0xffffffffu, l_run[r], 1);
-            l_run[r] += __shfl_xor_sync(0xffffffffu, l_run[r], 2);
+            float even, odd;
+            f2_split(l2[r], even, odd);
+            even += odd;
+            even += __shfl_xor_sync(0xffffffffu, even, 1);
+            even += __shfl_xor_sync(0xffffffffu, even, 2);
+            if (tq == 0) {
+                mm[warp * kKv8Rows + gq + 8 * r] = m_run[r];
+                ml[warp * kKv8Rows + gq + 8 * r] = even;
+            }
         }
-    }
-    __syncthreads();  // the ring is idle from here on: reuse it for the cross-warp merge
-    if (wd.aborted()) return;  // a wait ran out: the status word says so, nothing is stored
-
-    float* mo = reinterpret_cast<float*>(smem);             // [4 warps][16 rows][kMergeStride]
-    float* mm = mo + 4 * kKv8Rows * C::kMergeStride;        // [4][16] running max
-    float* ml = mm + 4 * kKv8Rows;                          // [4][16] denominators
-    if (warp < 4) {
-        const int gq = lane >> 2, tq = lane & 3;
-        float* w = mo + warp * kKv8Rows * C::kMergeStride;
-        const float unit = e8m0_to_f32(e_run) * 0x1p-15f;
+        if (!ok && lane == 0) bars->fail[seg & 1] = 1;
+        named_bar_sync(1, 128);
+        // the same answer in all four warps: the flag of this parity was last written before the
+        // barrier, and is written again only behind the next segment's barriers
+        if (*reinterpret_cast<volatile int*>(&bars->fail[seg & 1])) return;
+        float sc[2];
 #pragma unroll
-        for (int u = 0; u < D / 16; ++u)
-#pragma unroll
-            for (int h = 0; h < 2; ++h)
-                *reinterpret_cast<float4*>(w + (gq + 8 * h) * C::kMergeStride + 16 * u + 4 * tq) =
-                    make_float4(o[2 * u][2 * h] * unit, o[2 * u + 1][2 * h] * unit,
-                                o[2 * u][2 * h + 1] * unit, o[2 * u + 1][2 * h + 1] * unit);
-        if (tq == 0) {
-            mm[warp * kKv8Rows + gq] = m_run[0];
-            mm[warp * kKv8Rows + gq + 8] = m_run[1];
-            ml[warp * kKv8Rows + gq] = l_run[0];
-            ml[warp * kKv8Rows + gq + 8] = l_run[1];
-        }
-    }
-    __syncthreads();
-    if (threadIdx.x < 128) {
-        for (int e = threadIdx.x; e < rows * D; e += 128) {
-            const int r = e / D, d = e % D;
+        for (int r = 0; r < 2; ++r) {
             float M = -INFINITY;
 #pragma unroll
-            for (int w = 0; w < 4; ++w) M = fmaxf(M, mm[w * kKv8Rows + r]);
-            if (M == -INFINITY) M = 0.f;  // no key seen, or only NaN scores: l tells which
-            float lsum = 0.f, acc = 0.f;
+            for (int i = 0; i < 4; ++i) M = fmaxf(M, mm[i * kKv8Rows + gq + 8 * r]);
+            if (M == -INFINITY) M = 0.f;
+            sc[r] = ex2_approx(m_run[r] - M) * (__int_as_float(e_run << 23) * 0x1p-5f);  // 2^(E - 5)
+        }
+        for (int turn = 0; turn < 4; ++turn) {
+            if (turn == warp) {
 #pragma unroll
-            for (int w = 0; w < 4; ++w) {
-                const float sc = ex2_approx(mm[w * kKv8Rows + r] - M);
-                lsum += ml[w * kKv8Rows + r] * sc;
-                acc += mo[(w * kKv8Rows + r) * C::kMergeStride + d] * sc;
+                for (int u = 0; u < D / 16; ++u)
+#pragma unroll
+                    for (int h = 0; h < 2; ++h) {
+                        float4* dst = reinterpret_cast<float4*>(mo + (gq + 8 * h) * C::kMergeStride +
+                                                                16 * u + 4 * tq);
+                        float4 v = make_float4(o[2 * u][2 * h] * sc[h], o[2 * u + 1][2 * h] * sc[h],
+                                               o[2 * u][2 * h + 1] * sc[h],
+                                               o[2 * u + 1][2 * h + 1] * sc[h]);
+                        if (turn > 0) {
+                            const float4 a = *dst;
+                            v = make_float4(a.x + v.x, a.y + v.y, a.z + v.z, a.w + v.w);
+                        }
+                        *dst = v;
+                    }
             }
-            const float out = lsum == 0.f ? 0.f : acc / lsum;
-            const float lse = lsum == 0.f ? -INFINITY : (M + __log2f(lsum)) * kLn2f;
+            named_bar_sync(1, 128);
+        }
+        const bool whole = w.first && w.last;
+        for (int e = threadIdx.x; e < rows * (D / 4); e += 128) {
+            const int r = e / (D / 4), d = 4 * (e % (D / 4));
+            float M = -INFINITY, lsum = 0.f;
+#pragma unroll
+            for (int i = 0; i < 4; ++i) M = fmaxf(M, mm[i * kKv8Rows + r]);
+            if (M == -INFINITY) M = 0.f;  // no key seen, or only NaN scores: l tells which
+#pragma unroll
+            for (int i = 0; i < 4; ++i)
+                lsum += ml[i * kKv8Rows + r] * ex2_approx(mm[i * kKv8Rows + r] - M);
+            const float inv = lsum == 0.f ? 0.f : 1.f / lsum;
+            const float lse = lsum == 0.f ? -INFINITY : M + __log2f(lsum);  // log2
+            float4 v = *reinterpret_cast<const float4*>(mo + r * C::kMergeStride + d);
+            v = make_float4(v.x * inv, v.y * inv, v.z * inv, v.w * inv);
             const int tok = q0 + (row0 + r) / p.g, head = kvh * p.g + (row0 + r) % p.g;
-            const size_t at = static_cast<size_t>(tok) * p.Hq + head;
             if (!ATTN_IN_BOUNDS(head < p.Hq && tok < p.total_q, p.status)) continue;
-            if (S == 1) {
-                p.out[at * D + d] = __float2bfloat16_rn(out);
-                if (d == 0) p.lse[static_cast<size_t>(head) * p.lse_head + static_cast<size_t>(tok) * p.lse_tok] = lse;
+            if (whole) {
+                *reinterpret_cast<uint2*>(p.out + (static_cast<size_t>(tok) * p.Hq + head) * D + d) =
+                    make_uint2(pack_bf16x2(v.x, v.y), pack_bf16x2(v.z, v.w));
+                if (d == 0)
+                    p.lse[static_cast<size_t>(head) * p.lse_head + static_cast<size_t>(tok) * p.lse_tok] =
+                        lse * kLn2f;
             } else {
-                p.part_o[(at * S + split) * D + d] = out;
-                if (d == 0) p.part_lse[at * S + split] = lse;
+                const size_t at = (2 * static_cast<size_t>(cta) + (w.first ? 1 : 0)) * kKv8Rows + r;
+                *reinterpret_cast<float4*>(p.part_o + at * D + d) = v;
+                if (d == 0) p.part_lse[at] = lse;
             }
+        }
+        if (w.last && !w.first && threadIdx.x == 0) {
+            // the unit started (c1 - lo) chunks before this segment's end
+            const int begin = bars->start + bars->count - w.left - (w.c1 - w.s.lo);
+            p.meta[cta] = make_int4(begin / bars->share, q0, row0, rows);
         }
     }
 }
 
-// One warp per (token, head): LSE = log sum_s exp(LSE_s), O = sum_s exp(LSE_s - LSE) O_s (an
-// empty split has LSE_s = -inf and weight 0).
+// Merges the units that were cut: a CTA's entry names the share in which the unit it ended started.
+// LSE = log2 sum_s 2^LSE_s, O = sum_s 2^(LSE_s - LSE) O_s (a part without keys has LSE_s = -inf
+// and weight 0).
 template <int D>
-__global__ void __launch_bounds__(128) kv8_combine_kernel(const Kv8CombineParams p) {
-    const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
-    const int row = blockIdx.x * 4 + warp;
-    if (row >= p.total_q * p.Hq) return;
-    const int tok = row / p.Hq, head = row % p.Hq;
-    // tokens outside every sequence have no partials and no output
-    if (p.cu_q != nullptr && (tok < p.cu_q[0] || tok >= p.cu_q[p.batch])) return;
-    const int S = p.num_splits;
-    const float* pl = p.part_lse + static_cast<size_t>(row) * S;
+__global__ void __launch_bounds__(kKv8Rows * 16) kv8_combine_kernel(const Kv8Params p) {
+    griddep_wait();
+    const int cta = blockIdx.x;
+    const int4 m = p.meta[cta];
+    const int kvh = cta % p.Hkv, last = cta / p.Hkv;
+    const int r = threadIdx.x / 16, d0 = (threadIdx.x % 16) * 4;
+    if (m.x < 0 || r >= m.w) return;
+    // parts: slot 1 of the CTA with the head's share m.x, then slot 0 of those up to this one
+    const auto part = [&](int s) {
+        return (2 * (static_cast<size_t>(s) * p.Hkv + kvh) + (s == m.x ? 1 : 0)) * kKv8Rows + r;
+    };
     float M = -INFINITY;
     bool nan = false;
-    for (int s = lane; s < S; s += 32) {
-        M = fmaxf(M, pl[s]);
-        nan = nan || pl[s] != pl[s];
+    for (int s = m.x; s <= last; ++s) {
+        const float x = p.part_lse[part(s)];
+        M = fmaxf(M, x);
+        nan = nan || x != x;
     }
+    if (M == -INFINITY) M = 0.f;
+    if (nan) M = __int_as_float(0x7fffffff);
+    float sum = 0.f;
+    float4 acc[D / 64];
 #pragma unroll
-    for (int o = 16; o > 0; o >>= 1) M = fmaxf(M, __shfl_xor_sync(0xffffffffu, M, o));
-    if (__any_sync(0xffffffffu, nan)) M = __int_as_float(0x7fffffff);
-    constexpr int E = D / 32;  // elements per lane
-    float acc[E];
+    for (int i = 0; i < D / 64; ++i) acc[i] = make_float4(0.f, 0.f, 0.f, 0.f);
+#pragma unroll 4
+    for (int s = m.x; s <= last; ++s) {
+        const size_t at = part(s);
+        const float wgt = ex2_approx(p.part_lse[at] - M);
+        sum += wgt;
 #pragma unroll
-    for (int e = 0; e < E; ++e) acc[e] = 0.f;
-    float lse = -INFINITY;
-    if (M != -INFINITY) {
-        float sum = 0.f;
-        for (int s = lane; s < S; s += 32) sum += ex2_approx((pl[s] - M) * kLog2e);
-#pragma unroll
-        for (int o = 16; o > 0; o >>= 1) sum += __shfl_xor_sync(0xffffffffu, sum, o);
-        lse = M + __logf(sum);
-        const float* po = p.part_o + static_cast<size_t>(row) * S * D + lane * E;
-        for (int s = 0; s < S; ++s) {
-            const float w = ex2_approx((pl[s] - lse) * kLog2e);
-            const float* src = po + static_cast<size_t>(s) * D;
-#pragma unroll
-            for (int e = 0; e < E; ++e) acc[e] += w * src[e];
+        for (int i = 0; i < D / 64; ++i) {
+            const float4 v = *reinterpret_cast<const float4*>(p.part_o + at * D + d0 + 64 * i);
+            acc[i].x += wgt * v.x;
+            acc[i].y += wgt * v.y;
+            acc[i].z += wgt * v.z;
+            acc[i].w += wgt * v.w;
         }
     }
-    __nv_bfloat16* dst = p.out + static_cast<size_t>(row) * D + lane * E;
+    const float inv = sum == 0.f ? 0.f : 1.f / sum;
+    const int tok = m.y + (m.z + r) / p.g, head = kvh * p.g + (m.z + r) % p.g;
 #pragma unroll
-    for (int e = 0; e < E; e += 2)
-        *reinterpret_cast<uint32_t*>(dst + e) = pack_bf16x2(acc[e], acc[e + 1]);
-    if (lane == 0) p.lse[static_cast<size_t>(head) * p.lse_head + static_cast<size_t>(tok) * p.lse_tok] = lse;
+    for (int i = 0; i < D / 64; ++i)
+        *reinterpret_cast<uint2*>(p.out + (static_cast<size_t>(tok) * p.Hq + head) * D + d0 + 64 * i) =
+            make_uint2(pack_bf16x2(acc[i].x * inv, acc[i].y * inv),
+                       pack_bf16x2(acc[i].z * inv, acc[i].w * inv));
+    if (threadIdx.x % 16 == 0)
+        p.lse[static_cast<size_t>(head) * p.lse_head + static_cast<size_t>(tok) * p.lse_tok] =
+            sum == 0.f ? -INFINITY : (M + __log2f(sum)) * kLn2f;
 }
 
 }  // namespace
@@ -477,24 +687,39 @@ cudaError_t configure_kv8_kernels() {
     return e;
 }
 
-cudaError_t launch_kv8_attn(const Kv8Params& p, int head_dim, cudaStream_t stream) {
-    const long long groups =
-        (static_cast<long long>(p.max_seqlen_q) * p.g + kKv8Rows - 1) / kKv8Rows;
-    const dim3 grid(static_cast<unsigned>(groups * p.num_splits), p.Hkv, p.batch);
-    if (head_dim == 128)
-        kv8_split_kernel<128><<<grid, kKv8Threads, Kv8Cfg<128>::kSmem, stream>>>(p);
-    else
-        kv8_split_kernel<64><<<grid, kKv8Threads, Kv8Cfg<64>::kSmem, stream>>>(p);
-    return cudaGetLastError();
+namespace {
+
+template <typename Kernel>
+cudaError_t launch(Kernel kernel, int grid, int threads, size_t smem, bool dependent,
+                   const Kv8Params& p, cudaStream_t stream) {
+    cudaLaunchConfig_t cfg = {};
+    cfg.gridDim = dim3(grid);
+    cfg.blockDim = dim3(threads);
+    cfg.dynamicSmemBytes = smem;
+    cfg.stream = stream;
+    cudaLaunchAttribute attr[1];
+    attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+    attr[0].val.programmaticStreamSerializationAllowed = 1;
+    cfg.attrs = attr;
+    cfg.numAttrs = dependent ? 1 : 0;
+    return cudaLaunchKernelEx(&cfg, kernel, p);
 }
 
-cudaError_t launch_kv8_combine(const Kv8CombineParams& p, int head_dim, cudaStream_t stream) {
-    const unsigned grid = (static_cast<unsigned>(p.total_q) * p.Hq + 3) / 4;
-    if (head_dim == 128)
-        kv8_combine_kernel<128><<<grid, 128, 0, stream>>>(p);
-    else
-        kv8_combine_kernel<64><<<grid, 128, 0, stream>>>(p);
-    return cudaGetLastError();
+}  // namespace
+
+// Both kernels set up while the one before them finishes (the first only behind the append kernel
+// of the same call).
+cudaError_t launch_kv8_attn(const Kv8Params& p, int head_dim, int grid, bool after_append,
+                            cudaStream_t stream) {
+    cudaError_t e =
+        head_dim == 128 ? launch(kv8_split_kernel<128>, grid, kKv8Threads, Kv8Cfg<128>::kSmem,
+                                 after_append, p, stream)
+                        : launch(kv8_split_kernel<64>, grid, kKv8Threads, Kv8Cfg<64>::kSmem,
+                                 after_append, p, stream);
+    if (e != cudaSuccess || grid == p.Hkv) return e;  // (one CTA a head cuts nothing)
+    return head_dim == 128
+               ? launch(kv8_combine_kernel<128>, grid, kKv8Rows * 16, 0, true, p, stream)
+               : launch(kv8_combine_kernel<64>, grid, kKv8Rows * 16, 0, true, p, stream);
 }
 
 }  // namespace attn

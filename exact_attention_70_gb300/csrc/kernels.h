@@ -215,10 +215,10 @@ struct ReadFp8Params {
     int batch, total_k, Hkv, page_size, max_pages, num_pages;
 };
 
-constexpr int kKv8Chunk = 64;     // keys per pipeline stage
+constexpr int kKv8Chunk = 128;    // keys per pipeline stage
 constexpr int kKv8Threads = 160;  // 4 MMA warps + 1 TMA warp
 constexpr int kKv8Rows = 16;      // packed query rows of one CTA
-constexpr int kKv8MaxSplits = 64;
+constexpr int kKv8MinShare = 2;   // chunks a CTA takes at least
 
 struct Kv8Params {
     CUtensorMap tm_k;  // 3-D over the codes [num_pages * page_size, Hkv, d] u8, box {d, 1, box_rows}
@@ -230,35 +230,27 @@ struct Kv8Params {
     const float* q_unit;     //   and its units [total_q, Hq]
     __nv_bfloat16* out;
     float* lse;
-    float* part_o;    // [total_q, Hq, num_splits, d]  (num_splits > 1)
-    float* part_lse;  // [total_q, Hq, num_splits]
+    float* part_o;    // [CTA][2][16 rows][d]: the parts of units cut by a share's border
+    float* part_lse;  // [CTA][2][16 rows], log2
+    int4* meta;       // [CTA]: the unit it ended for an earlier one {share that started it or -1, first
+                      //   token row q0, first packed row, rows}
     const int* cu_q;  // [batch + 1], or null: one query per sequence, at its last key
     const int* seqlens;  // keys in the cache; with cu_q, before the call's new tokens
     const int* block_table;
     unsigned* status;
     int batch, total_q, max_seqlen_q, Hq, Hkv, g;
-    int page_size, box_rows, max_pages, num_pages, num_splits;
+    int page_size, box_rows, max_pages, num_pages;
     int causal, wl, wr;
     int lse_head, lse_tok;  // strides of lse
     float scale_log2;
-};
-
-struct Kv8CombineParams {
-    const float* part_o;
-    const float* part_lse;
-    __nv_bfloat16* out;
-    float* lse;
-    const int* cu_q;  // or null: every token has a sequence
-    int batch, total_q, Hq, num_splits;
-    int lse_head, lse_tok;
 };
 
 cudaError_t launch_kvcache_append_fp8(const AppendFp8Params& p, int head_dim, int num_sms,
                                       cudaStream_t stream);
 cudaError_t launch_kvcache_read_fp8(const ReadFp8Params& p, int head_dim, int num_sms,
                                     cudaStream_t stream);
-cudaError_t launch_kv8_attn(const Kv8Params& p, int head_dim, cudaStream_t stream);
-cudaError_t launch_kv8_combine(const Kv8CombineParams& p, int head_dim, cudaStream_t stream);
+cudaError_t launch_kv8_attn(const Kv8Params& p, int head_dim, int grid, bool after_append,
+                            cudaStream_t stream);
 
 // ---- failure-path self-test ------------------------------------------------------------
 

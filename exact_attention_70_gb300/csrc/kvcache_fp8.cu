@@ -66,6 +66,7 @@ __device__ __forceinline__ float det2_odd(float a, float b, float c, float d) {
 template <int D>
 __global__ void __launch_bounds__(256) kvcache_append_fp8_kernel(const AppendFp8Params p) {
     constexpr int kLanes = D / 8;
+    griddep_launch_dependents();  // an attention kernel behind this one may set up
     const int lane = threadIdx.x & 31;
     const int e0 = (lane % kLanes) * 8;
     const int rows_per_tok = 2 * p.Hkv + (p.q_rot != nullptr ? p.Hq : 0);

@@ -531,6 +531,25 @@ __device__ __forceinline__ uint32_t e4m3x2_to_f16x2(uint32_t codes) {
     return r;
 }
 
+// Four e4m3 bytes to two f16x2, exactly.
+__device__ __forceinline__ void e4m3x4_to_f16x2(uint32_t codes, uint32_t& lo, uint32_t& hi) {
+    asm("{\n\t.reg .b16 l, h;\n\t"
+        "mov.b32 {l, h}, %2;\n\t"
+        "cvt.rn.f16x2.e4m3x2 %0, l;\n\t"
+        "cvt.rn.f16x2.e4m3x2 %1, h;\n\t}\n"
+        : "=r"(lo), "=r"(hi)
+        : "r"(codes));
+}
+
+__device__ __forceinline__ uint32_t ld_shared_u16(uint32_t addr) {
+    uint32_t v;
+    asm volatile("{\n\t.reg .u16 h;\n\tld.shared.u16 h, [%1];\n\tcvt.u32.u16 %0, h;\n\t}\n"
+                 : "=r"(v)
+                 : "r"(addr)
+                 : "memory");
+    return v;
+}
+
 __device__ __forceinline__ float2 f16x2_to_float2(uint32_t v) {
     float2 f;
     asm("{\n\t.reg .b16 lo, hi;\n\t"

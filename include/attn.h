@@ -356,25 +356,23 @@ attn_status_t attn_kvcache_read_fp8(const void* k_cache, const void* v_cache, co
  *       [batch, nheads_q], natural log
  *   cache_seqlens  device int32 [batch]; sequence b attends to its keys 0 .. cache_seqlens[b]-1
  *       (none: O = 0, LSE = -inf)
- *   num_splits     0 = choose automatically, else 1..64
- *   workspace      attn_decode_kvcache_fp8_workspace_bytes(...) bytes, 256-byte aligned (may be
- *       NULL when that is 0)
- * The result is the attention of the stored values: the codes and the queries enter the tensor
+ *   workspace      attn_decode_kvcache_fp8_workspace_bytes(...) bytes, 256-byte aligned
+ * The keys of all sequences are shared out evenly over the GPU; what is cut is merged.  The result is the attention of the stored values: the codes and the queries enter the tensor
  * cores exactly, the weights P with 11 significant bits.
  */
 attn_status_t attn_decode_kvcache_fp8(const void* q, const void* k_cache, const void* v_cache,
                                       const void* k_scale, const void* v_scale,
                                       const int32_t* cache_seqlens, const int32_t* block_table,
-                                      int page_size, int num_splits, void* out, float* lse,
-                                      int batch, int nheads_q, int nheads_kv, int head_dim,
+                                      int page_size, void* out, float* lse, int batch,
+                                      int nheads_q, int nheads_kv, int head_dim,
                                       int max_pages_per_seq, int num_pages, float softmax_scale,
                                       void* workspace, size_t workspace_bytes, void* stream);
 
-/* Workspace bytes of attn_decode_kvcache_fp8 (split partials; 0 with one split, or on sizes the
- * call would refuse). */
+/* Workspace bytes of attn_decode_kvcache_fp8: the partial results of sequences that are cut, at
+ * most 5 MiB (0 on sizes the call would refuse). */
 size_t attn_decode_kvcache_fp8_workspace_bytes(int batch, int nheads_q, int nheads_kv,
                                                int head_dim, int page_size,
-                                               int max_pages_per_seq, int num_splits);
+                                               int max_pages_per_seq);
 
 /*
  * attn_fwd_kvcache_fp8 -- attn_fwd_kvcache over the 8-bit cache: appends the new tokens' keys and
@@ -386,8 +384,7 @@ size_t attn_decode_kvcache_fp8_workspace_bytes(int batch, int nheads_q, int nhea
  *   max_total_k   an upper bound on sum_b (cache_seqlens[b] + new tokens of b) (checked on the
  *                 device); sizes the workspace
  *   causal, window_left, window_right   see "Visibility"
- *   workspace     attn_fwd_kvcache_fp8_workspace_bytes(...) bytes, 256-byte aligned (may be NULL
- *                 when that is 0)
+ *   workspace     attn_fwd_kvcache_fp8_workspace_bytes(...) bytes, 256-byte aligned
  * A NaN or an infinity among the new values reaches the rows that see it, and may reach the other
  * new tokens of its sequence, as in attn_fwd.
  */

@@ -152,15 +152,18 @@ DECODE = [
     ([300, 20], 16, 1, 64, 32),
     ([77, 513], 40, 1, 128, 128),   # more heads than one CTA's rows
     ([2500], 12, 4, 64, 128),
+    ([40 * i % 997 for i in range(100)], 4, 2, 64, 16),     # more sequences than a warp has lanes
+    ([9000, 1, 0, 20000], 8, 4, 128, 192),                  # units cut into many parts
+    ([100000], 2, 1, 64, 64),
+    ([128 * (i % 3) for i in range(700)], 2, 1, 64, 64),    # many units a CTA, whole and cut
 ]
 
 
-@pytest.mark.parametrize("splits", [0, 1, 2, 7, 64])
 @pytest.mark.parametrize("i", range(len(DECODE)))
-def test_decode_matches_the_definition(attn, i, splits):
+def test_decode_matches_the_definition(attn, i):
     lens, Hq, Hkv, d, ps = DECODE[i]
     c = kv8_case(lens, None, Hq, Hkv, d, ps, seed=50 + i)
-    out, lse = decode(attn, c, num_splits=splits)
+    out, lse = decode(attn, c)
     ref = kv8_exact.attention(c, [t.numpy() for t in c.cache])
     kv8_exact.check(out, lse, ref, 2.0 ** -11, False, f"decode{i}")
 
@@ -265,7 +268,7 @@ def test_a_generation_from_prompt_to_tokens(attn):
 def test_nan_in_a_visible_token_reaches_its_rows_only(attn):
     c = kv8_case([40, 50], None, 4, 2, 64, 16, seed=120)
     c.k_cache[int(c.block_table[1, 1]), 3, 0, 5] = 0x7F   # kv head 0 of sequence 1
-    out, lse = decode(attn, c, num_splits=2)
+    out, lse = decode(attn, c)
     assert torch.isnan(out[1, :2]).all() and torch.isnan(lse[1, :2]).all()
     ref = kv8_exact.attention(c, [t.numpy() for t in c.cache])
     keep = ((0, slice(None)), (1, slice(2, 4)))
@@ -372,7 +375,7 @@ def test_binding_refuses_mismatched_arguments(attn):
     with pytest.raises(ValueError):
         f(q, *cache, sl, bt, out=torch.empty(2, 4, 32, dtype=torch.bfloat16, device="cuda"))
     with pytest.raises(attn.AttnError):
-        f(q, *cache, sl, bt, num_splits=4, workspace=torch.empty(16, dtype=torch.uint8, device="cuda"))
+        f(q, *cache, sl, bt, workspace=torch.empty(16, dtype=torch.uint8, device="cuda"))
     with pytest.raises(ValueError):
         attn.attn_kvcache_read_fp8(*cache, bt, torch.tensor([0, 3, 5], dtype=torch.int32).cuda(), 5,
                                    k=torch.empty(4, 2, 64, dtype=torch.bfloat16, device="cuda"))

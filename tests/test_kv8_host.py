@@ -126,14 +126,12 @@ def test_read_refusals(lib):
 
 
 def test_decode_refusals(lib):
-    names = ["q", "kc", "vc", "ks", "vs", "sl", "bt", "ps", "splits", "out", "lse", "batch", "hq", "hkv",
+    names = ["q", "kc", "vc", "ks", "vs", "sl", "bt", "ps", "out", "lse", "batch", "hq", "hkv",
              "d", "mp", "np", "scale", "ws", "wsb", "stream"]
     call = refusals(lib.attn_decode_kvcache_fp8, names,
-                    [FAKE] * 7 + [64, 0, FAKE, FAKE, 2, 8, 2, 128, 4, 16, 0.1, FAKE, 1 << 24, None])
+                    [FAKE] * 7 + [64, FAKE, FAKE, 2, 8, 2, 128, 4, 16, 0.1, FAKE, 1 << 24, None])
     common_refusals(call)
     assert call(hq=3) == -1
-    assert call(splits=65) == -1
-    assert call(splits=-1) == -1
     for bad in (0.0, -1.0, float("nan"), float("inf"), 1e-39):
         assert call(scale=bad) == -1
     assert call(q=None) == -1
@@ -142,10 +140,11 @@ def test_decode_refusals(lib):
     assert call(wsb=16) == -3
     assert call(ws=P(4096 + 16)) == -3
     need = binding.attn_decode_kvcache_fp8_workspace_bytes
-    assert need(2, 8, 2, 128, 64, 4, 1) == 0
-    assert need(2, 8, 2, 128, 64, 4, 4) == 2 * 8 * 4 * 128 * 4 + 256
-    assert need(2, 8, 2, 128, 64, 4, 65) == 0
-    assert need(2, 8, 2, 96, 64, 4, 4) == 0
+    # two parts of 16 rows of O and LSE and one entry a CTA; at most two CTAs an SM
+    assert need(64, 32, 8, 128, 256, 128) == 304 * (2 * 16 * (128 + 1) * 4 + 16)
+    assert need(1, 8, 2, 64, 64, 4) == 2 * 2 * 16 * (64 + 1) * 4 + 256  # 2 chunks, 2 heads
+    assert need(2, 8, 2, 96, 64, 4) == 0
+    assert need(2, 7, 2, 64, 64, 4) == 0
 
 
 def test_chunk_refusals(lib):
