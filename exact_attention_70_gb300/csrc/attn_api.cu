@@ -871,10 +871,37 @@ size_t kv8_partial_bytes(int grid, int head_dim) {
 }
 
 // The rotated queries (f16) and their units.
-size_t kv8_query_bytes(long long rows, int head_dim, int rotary_dim) {
-    if (rotary_dim <= 0) return 0;
+size_t kv8_query_bytes(long long rows, int head_dim) {
     return align_up(static_cast<size_t>(rows) * head_dim * 2, 256) +
            align_up(static_cast<size_t>(rows) * sizeof(float), 256);
+}
+
+// Whether a chunk call runs the tensor-core prefill on staged f16 keys and values, or the 16-row
+// kernel on the codes.
+bool kv8_staged(int batch, int max_seqlen_q, int nheads_q, int nheads_kv) {
+    return static_cast<long long>(max_seqlen_q) * (nheads_q / nheads_kv) > kKv8DirectRows;
+}
+
+// The staged path's workspace behind the queries.
+struct Kv8StageLayout {
+    long long rows;  // of k and v
+    size_t k, v, spans, k_unit, v_unit, list, total;
+};
+
+Kv8StageLayout kv8_stage_layout(int batch, int max_seqlen_q, int max_total_k, int nheads_q,
+                                int nheads_kv, int head_dim) {
+    Kv8StageLayout l;
+    l.rows = static_cast<long long>(max_total_k) + static_cast<long long>(kFwdBlockN) * batch;
+    const size_t bytes = align_up(static_cast<size_t>(l.rows) * nheads_kv * head_dim * 2, 256);
+    const size_t units = align_up(static_cast<size_t>(batch) * nheads_kv * sizeof(float), 256);
+    l.k = 0;
+    l.v = bytes;
+    l.spans = 2 * bytes;
+    l.k_unit = l.spans + align_up(static_cast<size_t>(batch) * sizeof(int2), 256);
+    l.v_unit = l.k_unit + units;
+    l.list = l.v_unit + units;
+    l.total = l.list + attn_fwd_workspace_bytes(batch, max_seqlen_q, nheads_q, nheads_kv);
+    return l;
 }
 
 // The attention kernel and the merge of the units it cut.
@@ -1061,10 +1088,15 @@ size_t attn_fwd_kvcache_fp8_workspace_bytes(int batch, int total_q, int max_seql
         nheads_kv <= 0 || nheads_q % nheads_kv != 0 || rotary_dim < 0 ||
         kv8_sizes(batch, nheads_kv, head_dim, page_size, max_pages_per_seq, 1) != ATTN_OK)
         return 0;
-    return kv8_query_bytes(static_cast<long long>(total_q) * nheads_q, head_dim, rotary_dim) +
-           kv8_partial_bytes(kv8_grid(batch, max_seqlen_q, nheads_q, nheads_kv, page_size,
-                                      max_pages_per_seq),
-                             head_dim);
+    const bool staged = kv8_staged(batch, max_seqlen_q, nheads_q, nheads_kv);
+    if (staged && nheads_q / nheads_kv > 128) return 0;
+    return (rotary_dim > 0 || staged
+                ? kv8_query_bytes(static_cast<long long>(total_q) * nheads_q, head_dim)
+                : 0) +
+           (staged ? kv8_stage_layout(batch, max_seqlen_q, max_total_k, nheads_q, nheads_kv, head_dim).total
+                   : kv8_partial_bytes(kv8_grid(batch, max_seqlen_q, nheads_q, nheads_kv, page_size,
+                                                max_pages_per_seq),
+                                       head_dim));
 }
 
 attn_status_t attn_fwd_kvcache_fp8(const void* q, const void* k_new, const void* v_new,
@@ -1093,8 +1125,15 @@ attn_status_t attn_fwd_kvcache_fp8(const void* q, const void* k_new, const void*
         !aligned(v_new, 16) || !aligned(out, 16) || !aligned(lse, 4) || !aligned(cache_seqlens, 4) ||
         !aligned(cu_seqlens_q, 4))
         return ATTN_ERR_INVALID_ARG;
-    const int grid = kv8_grid(batch, max_seqlen_q, nheads_q, nheads_kv, page_size, max_pages_per_seq);
-    if (grid == 0) return ATTN_ERR_UNSUPPORTED;
+    const int g = nheads_q / nheads_kv;
+    const bool staged = kv8_staged(batch, max_seqlen_q, nheads_q, nheads_kv);
+    const int grid = staged ? 0
+                            : kv8_grid(batch, max_seqlen_q, nheads_q, nheads_kv, page_size,
+                                       max_pages_per_seq);
+    if (staged ? g > 128 || (static_cast<long long>(max_total_k) + 128LL * batch) * nheads_kv >
+                                (1LL << 31) - 1
+               : grid == 0)
+        return ATTN_ERR_UNSUPPORTED;
     const size_t need = attn_fwd_kvcache_fp8_workspace_bytes(
         batch, total_q, max_seqlen_q, max_total_k, nheads_q, nheads_kv, head_dim, page_size,
         max_pages_per_seq, rotary_dim);
@@ -1117,9 +1156,10 @@ attn_status_t attn_fwd_kvcache_fp8(const void* q, const void* k_new, const void*
     ap.v_cache = static_cast<uint8_t*>(v_cache);
     ap.k_scale = static_cast<uint8_t*>(k_scale);
     ap.v_scale = static_cast<uint8_t*>(v_scale);
-    if (rotary_dim > 0) {
+    if (rotary_dim > 0 || staged) {
         ap.q_rot = reinterpret_cast<__half*>(ws);
         ap.q_unit = reinterpret_cast<float*>(ws + align_up(q_rows * head_dim * 2, 256));
+        ws += kv8_query_bytes(q_rows, head_dim);
     }
     ap.cu_q = cu_seqlens_q;
     ap.cache_seqlens = cache_seqlens;
@@ -1139,7 +1179,92 @@ attn_status_t attn_fwd_kvcache_fp8(const void* q, const void* k_new, const void*
     ap.interleaved = rotary_interleaved ? 1 : 0;
     if (launch_kvcache_append_fp8(ap, head_dim, dev->num_sms, s) != cudaSuccess) return ATTN_ERR_CUDA;
 
-    // 2. attention over the cache
+    if (staged) {
+        // 2. the keys and values the new tokens see, in f16
+        const Kv8StageLayout l =
+            kv8_stage_layout(batch, max_seqlen_q, max_total_k, nheads_q, nheads_kv, head_dim);
+        StageFp8Params sp;
+        memset(&sp, 0, sizeof(sp));
+        sp.k_cache = ap.k_cache;
+        sp.v_cache = ap.v_cache;
+        sp.k_scale = ap.k_scale;
+        sp.v_scale = ap.v_scale;
+        sp.block_table = block_table;
+        sp.cu_q = cu_seqlens_q;
+        sp.cache_seqlens = cache_seqlens;
+        sp.k = reinterpret_cast<__half*>(ws + l.k);
+        sp.v = reinterpret_cast<__half*>(ws + l.v);
+        sp.spans = reinterpret_cast<int2*>(ws + l.spans);
+        sp.k_unit = reinterpret_cast<float*>(ws + l.k_unit);
+        sp.v_unit = reinterpret_cast<float*>(ws + l.v_unit);
+        sp.status = dev->status;
+        sp.batch = batch;
+        sp.total_q = total_q;
+        sp.Hkv = nheads_kv;
+        sp.page_size = page_size;
+        sp.max_pages = max_pages_per_seq;
+        sp.num_pages = num_pages;
+        sp.wl = window_left;
+        sp.rows = static_cast<int>(l.rows);
+        if (launch_kvcache_stage_fp8(sp, head_dim, dev->num_sms, s) != cudaSuccess)
+            return ATTN_ERR_CUDA;
+
+        // 3. the prefill kernel on them
+        const int tpt = tokens_per_tile(g);
+        FwdWorkspaceHeader* header = reinterpret_cast<FwdWorkspaceHeader*>(ws + l.list);
+        FwdPrepParams pp;
+        memset(&pp, 0, sizeof(pp));
+        pp.cu_q = cu_seqlens_q;
+        pp.cache_seqlens = cache_seqlens;
+        pp.max_keys = max_pages_per_seq * page_size;
+        pp.prefix = reinterpret_cast<int*>(header + 1);
+        pp.items = reinterpret_cast<int4*>(reinterpret_cast<uint8_t*>(header + 1) +
+                                           align_up(sizeof(int) * (batch + 1), 16));
+        pp.header = header;
+        pp.status = dev->status;
+        pp.batch = batch;
+        pp.total_q = total_q;
+        pp.max_seqlen_q = max_seqlen_q;
+        pp.Hkv = nheads_kv;
+        pp.tpt = tpt;
+        pp.capacity_pairs = static_cast<int>(fwd_capacity_pairs(batch, max_seqlen_q, g));
+        pp.causal = causal ? 1 : 0;
+        pp.wl = window_left;
+        pp.wr = window_right;
+        pp.heads_per_group = fwd_heads_per_group(max_total_k, nheads_kv, head_dim);
+        FwdParams fp;
+        memset(&fp, 0, sizeof(fp));
+        if (encode_3d(&fp.tm_q, ap.q_rot, head_dim, nheads_q, total_q, g, tpt) != ATTN_OK ||
+            encode_3d(&fp.tm_o, out, head_dim, nheads_q, total_q, g, tpt) != ATTN_OK ||
+            encode_3d(&fp.tm_k, sp.k, head_dim, nheads_kv, l.rows, 1, kFwdBlockN) != ATTN_OK ||
+            encode_3d(&fp.tm_v, sp.v, head_dim, nheads_kv, l.rows, 1, kFwdBlockN) != ATTN_OK)
+            return ATTN_ERR_CUDA;
+        fp.out = static_cast<__nv_bfloat16*>(out);
+        fp.lse = lse;
+        fp.cu_q = cu_seqlens_q;
+        fp.items = pp.items;
+        fp.header = header;
+        fp.status = dev->status;
+        fp.Hq = nheads_q;
+        fp.Hkv = nheads_kv;
+        fp.g = g;
+        fp.tpt = tpt;
+        fp.total_q = total_q;
+        fp.causal = pp.causal;
+        fp.wl = window_left;
+        fp.wr = window_right;
+        fp.scale_log2 = softmax_scale * kLog2eF;
+        fp.scale = softmax_scale;
+        fp.spans = sp.spans;
+        fp.q_unit = ap.q_unit;
+        fp.k_unit = sp.k_unit;
+        fp.v_unit = sp.v_unit;
+        if (launch_fwd_prepare(pp, s) != cudaSuccess) return ATTN_ERR_CUDA;
+        if (launch_fwd(fp, head_dim, dev->num_sms, s) != cudaSuccess) return ATTN_ERR_CUDA;
+        return ATTN_OK;
+    }
+
+    // 2. attention on the codes
     Kv8Params kp;
     memset(&kp, 0, sizeof(kp));
     kp.k_scale = static_cast<const uint8_t*>(k_scale);
@@ -1168,9 +1293,7 @@ attn_status_t attn_fwd_kvcache_fp8(const void* q, const void* k_new, const void*
     kp.lse_head = total_q;
     kp.lse_tok = 1;
     kp.scale_log2 = softmax_scale * kLog2eF;
-    return kv8_attend(
-        kp, k_cache, v_cache, head_dim, grid, true,
-        ws + kv8_query_bytes(q_rows, head_dim, rotary_dim), s);
+    return kv8_attend(kp, k_cache, v_cache, head_dim, grid, true, ws, s);
 }
 
 attn_status_t attn_selftest_wait_timeout(void* stream) {

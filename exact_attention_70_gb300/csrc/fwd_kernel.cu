@@ -29,6 +29,10 @@
 //   * the running max only moves the accumulator's reference when it grows by more than
 //     2^8 (the result is exact for any reference; this only bounds P <= 256), so the O
 //     rescale through TMEM is rare after the first blocks.
+//
+// An instance with f16 operands (kHalf) serves the 8-bit cache: Q, K and V are f16 multiples of
+// powers of two (of a query row, of a sequence and kv head), which join the softmax scale and
+// the epilogue's 1 / l, and P is f16, whose 11 bits hold P <= 256 down to 2^-14.
 #include <cuda_bf16.h>
 
 #include "kernels.h"
@@ -97,7 +101,7 @@ struct Item {
     bool any;
 };
 
-template <bool kPaged>
+template <bool kPaged, bool kHalf>
 __device__ __forceinline__ Item load_item(const FwdParams& p, int idx) {
     Item it;
     const int4 w = p.items[idx];
@@ -109,6 +113,10 @@ __device__ __forceinline__ Item load_item(const FwdParams& p, int idx) {
     if constexpr (kPaged) {  // the cached prefix, then this call's new tokens
         it.k0 = 0;
         it.Lk = p.cache_seqlens[it.b] + it.Lq;
+    } else if constexpr (kHalf) {  // the staged keys: each sequence starts a block of its own
+        const int2 span = p.spans[it.b];
+        it.k0 = span.x;
+        it.Lk = span.y;
     } else {
         it.k0 = p.cu_k[it.b];
         it.Lk = p.cu_k[it.b + 1] - it.k0;
@@ -219,7 +227,7 @@ struct RingState {
     uint32_t n = 0, kpar = 0, vpar = 0, lastv = 0;
 };
 
-template <int D, bool kPaged>
+template <int D, bool kPaged, bool kHalf>
 __device__ void fwd_producer_loop(const FwdParams& p, uint8_t* smem, FwdBars* bars,
                                   const Watchdog& wd, int n_items, uint32_t& q_cnt,
                                   RingState& ring) {
@@ -232,7 +240,7 @@ __device__ void fwd_producer_loop(const FwdParams& p, uint8_t* smem, FwdBars* ba
     int idx;
     if (!fwd_claim_item(p, bars, wd, n_items, claims++, idx)) return;
     while (idx >= 0) {
-        const Item it = load_item<kPaged>(p, idx);
+        const Item it = load_item<kPaged, kHalf>(p, idx);
         int next = -1;
         bool claimed = false;
         if (!it.any) {
@@ -316,13 +324,13 @@ __device__ void fwd_producer_loop(const FwdParams& p, uint8_t* smem, FwdBars* ba
     }
 }
 
-template <int D, bool kPaged>
+template <int D, bool kPaged, bool kHalf>
 __device__ void fwd_producer(const FwdParams& p, uint8_t* smem, FwdBars* bars,
                              const Watchdog& wd, int n_items) {
     using C = FwdCfg<D>;
     uint32_t q_cnt = 0;
     RingState ring;
-    fwd_producer_loop<D, kPaged>(p, smem, bars, wd, n_items, q_cnt, ring);
+    fwd_producer_loop<D, kPaged, kHalf>(p, smem, bars, wd, n_items, q_cnt, ring);
     // Every slot holds at most one load in flight: wait for the latest load of each one (its
     // phase has the parity before that load's flip).
     if (q_cnt > 0) drain_wait(&bars->q_full, (q_cnt - 1) & 1);
@@ -337,11 +345,12 @@ __device__ void fwd_producer(const FwdParams& p, uint8_t* smem, FwdBars* bars,
 
 // S_t(j) for every (j, t) of every item.  S_t(j) overwrites the TMEM columns of S_t(j-1), so
 // it waits for tile t's softmax to have read them (s_free).
-template <int D, bool kPaged>
+template <int D, bool kPaged, bool kHalf>
 __device__ void fwd_mma_s(const FwdParams& p, uint8_t* smem, FwdBars* bars, uint32_t tmem,
                           const Watchdog& wd, int n_items) {
     using C = FwdCfg<D>;
-    constexpr uint32_t kIdesc = idesc_bf16_f32(128, kFwdBlockN, false, false);
+    constexpr uint32_t kIdesc = kHalf ? idesc_f16_f32(128, kFwdBlockN, false, false)
+                                       : idesc_bf16_f32(128, kFwdBlockN, false, false);
     // K-major operand descriptors (128-byte swizzle, 8-row groups 1024 B apart), as halves
     const uint64_t dq = sdesc_sw128(smem_u32(smem + C::kOffQ), 16, 1024);
     const uint64_t dkv = sdesc_sw128(smem_u32(smem + C::kOffKV), 16, 1024);
@@ -353,7 +362,7 @@ __device__ void fwd_mma_s(const FwdParams& p, uint8_t* smem, FwdBars* bars, uint
     for (uint32_t rd = 0;;) {
         const int idx = fwd_take_item(bars, wd, rd);
         if (idx < 0) return;
-        const Item it = load_item<kPaged>(p, idx);
+        const Item it = load_item<kPaged, kHalf>(p, idx);
         if (!it.any) continue;
         if (!wd.wait(&bars->q_full, q_cnt & 1)) return;
         ++q_cnt;
@@ -391,11 +400,12 @@ __device__ void fwd_mma_s(const FwdParams& p, uint8_t* smem, FwdBars* bars, uint
 // O_t (+)= P_t(j) V_j for every (j, t) of every item, P_t from shared memory.  The item's
 // first PV_t overwrites O_t, so it first waits for the previous item's epilogue to have read
 // O_t (o_free).
-template <int D, bool kPaged>
+template <int D, bool kPaged, bool kHalf>
 __device__ void fwd_mma_pv(const FwdParams& p, uint8_t* smem, FwdBars* bars, uint32_t tmem,
                            const Watchdog& wd, int n_items) {
     using C = FwdCfg<D>;
-    constexpr uint32_t kIdesc = idesc_bf16_f32(128, D, false, true);
+    constexpr uint32_t kIdesc =
+        kHalf ? idesc_f16_f32(128, D, false, true) : idesc_bf16_f32(128, D, false, true);
     // A = P_t (K-major), B = V (MN-major: 64-wide d atoms kAtomBytes apart), as halves
     const uint64_t dp = sdesc_sw128(smem_u32(smem + C::kOffP), 16, 1024);
     const uint64_t dv = sdesc_sw128(smem_u32(smem + C::kOffKV), C::kAtomBytes, 1024);
@@ -408,7 +418,7 @@ __device__ void fwd_mma_pv(const FwdParams& p, uint8_t* smem, FwdBars* bars, uin
     for (uint32_t rd = 0;;) {
         const int idx = fwd_take_item(bars, wd, rd);
         if (idx < 0) return;
-        const Item it = load_item<kPaged>(p, idx);
+        const Item it = load_item<kPaged, kHalf>(p, idx);
         if (!it.any) continue;
         bool first0 = true, first1 = true;
         const int m = it.jhi - it.jlo;
@@ -482,7 +492,7 @@ __device__ __forceinline__ uint32_t sw128_unit(uint32_t base, int r, int u) {
     return base + (u >> 3) * (128 * 128) + r * 128 + (((u & 7) ^ (r & 7)) << 4);
 }
 
-template <int D, bool kPaged, bool kMods>
+template <int D, bool kPaged, bool kMods, bool kHalf>
 __device__ void fwd_softmax(const FwdParams& p, uint8_t* smem, FwdBars* bars, uint32_t tmem,
                             const Watchdog& wd, int n_items, int t, int k, int lane) {
     using C = FwdCfg<D>;
@@ -533,7 +543,7 @@ __device__ void fwd_softmax(const FwdParams& p, uint8_t* smem, FwdBars* bars, ui
     for (uint32_t rd = 0;;) {
         const int idx = fwd_take_item_warp(bars, wd, rd, lane);
         if (idx < 0) break;
-        const Item it = load_item<kPaged>(p, idx);
+        const Item it = load_item<kPaged, kHalf>(p, idx);
         const uint32_t kv_base = kv_cnt;
         const uint32_t vpar_item = vpar;
         if (it.any) {
@@ -544,6 +554,15 @@ __device__ void fwd_softmax(const FwdParams& p, uint8_t* smem, FwdBars* bars, ui
         }
         const TileView tv = tile_view(it, t);
         if (!tv.rows) continue;
+        // f16 operands come as multiples of a unit per query row and per (sequence, kv head)
+        float sl2_a = sl2, sl2_b = sl2;
+        if constexpr (kHalf) {
+            const float unit = p.k_unit[it.b * p.Hkv + it.kvh] * sl2;
+            const int ta = tv.tok0 + ra / g, tb = tv.tok0 + (ra + 8) / g;
+            const float* qu = p.q_unit + it.kvh * g;
+            sl2_a = unit * (ta < it.Lq ? qu[static_cast<size_t>(it.q0 + ta) * p.Hq + ra % g] : 1.f);
+            sl2_b = unit * (tb < it.Lq ? qu[static_cast<size_t>(it.q0 + tb) * p.Hq + (ra + 8) % g] : 1.f);
+        }
         // this thread's rows ra and ra + 8; packed row r is token tok0 + r / g, head kvh g + r % g
         float m_a = -INFINITY, m_b = -INFINITY, l_a = 0.f, l_b = 0.f;  // l: this thread's part
         // ALiBi: the rows' slopes and bottom-right key positions
@@ -682,8 +701,8 @@ __device__ void fwd_softmax(const FwdParams& p, uint8_t* smem, FwdBars* bars, ui
                     mba = fmaf(mxa, sl2, ra0);
                     mbb = fmaf(mxb, sl2, rb0);
                 } else {
-                    mba = mxa * sl2;
-                    mbb = mxb * sl2;
+                    mba = mxa * (kHalf ? sl2_a : sl2);
+                    mbb = mxb * (kHalf ? sl2_b : sl2);
                 }
                 const bool need_a = mba > m_a + kRescaleThreshold;
                 const bool need_b = mbb > m_b + kRescaleThreshold;
@@ -705,14 +724,16 @@ __device__ void fwd_softmax(const FwdParams& p, uint8_t* smem, FwdBars* bars, ui
                     nmb = f2_make(-rb_ref, -rb_ref);
                 }
                 // P = exp2(s * scale*log2e - m): paired FFMA, MUFU ex2, paired sums
+                const uint64_t sa2 = kHalf ? f2_make(sl2_a, sl2_a) : sl2x2;
+                const uint64_t sb2 = kHalf ? f2_make(sl2_b, sl2_b) : sl2x2;
                 uint64_t suma = 0, sumb = 0;
                 uint32_t pka[16], pkb[16];
 #pragma unroll
                 for (int c = 0; c < 16; ++c) {
                     const uint64_t xa = f2_fma(f2_make(__uint_as_float(s[4 * c]), __uint_as_float(s[4 * c + 1])),
-                                               sl2x2, nma);
+                                               sa2, nma);
                     const uint64_t xb = f2_fma(f2_make(__uint_as_float(s[4 * c + 2]), __uint_as_float(s[4 * c + 3])),
-                                               sl2x2, nmb);
+                                               sb2, nmb);
                     float a0, a1, b0, b1;
                     f2_split(xa, a0, a1);
                     f2_split(xb, b0, b1);
@@ -720,8 +741,8 @@ __device__ void fwd_softmax(const FwdParams& p, uint8_t* smem, FwdBars* bars, ui
                     const float pb0 = ex2_approx(b0), pb1 = ex2_approx(b1);
                     suma = f2_add(suma, f2_make(pa0, pa1));
                     sumb = f2_add(sumb, f2_make(pb0, pb1));
-                    pka[c] = pack_bf16x2(pa0, pa1);
-                    pkb[c] = pack_bf16x2(pb0, pb1);
+                    pka[c] = kHalf ? pack_f16x2(pa0, pa1) : pack_bf16x2(pa0, pa1);
+                    pkb[c] = kHalf ? pack_f16x2(pb0, pb1) : pack_bf16x2(pb0, pb1);
                 }
                 {
                     float lo, hi;
@@ -802,8 +823,13 @@ __device__ void fwd_softmax(const FwdParams& p, uint8_t* smem, FwdBars* bars, ui
             l_b += __shfl_xor_sync(0xffffffffu, l_b, 2);
             if (!__all_sync(0xffffffffu, wd.wait(pv_done, (blk - 1) & 1))) return;
             tc_fence_after();
-            const float inv_a = l_a > 0.f ? 1.f / l_a : 0.f;
-            const float inv_b = l_b > 0.f ? 1.f / l_b : 0.f;
+            float inv_a = l_a > 0.f ? 1.f / l_a : 0.f;
+            float inv_b = l_b > 0.f ? 1.f / l_b : 0.f;
+            if constexpr (kHalf) {
+                const float unit = p.v_unit[it.b * p.Hkv + it.kvh];
+                inv_a *= unit;
+                inv_b *= unit;
+            }
 #pragma unroll
             for (int cc = 0; cc < D / 64; ++cc) {
                 uint32_t o[32];
@@ -922,7 +948,7 @@ __device__ void fwd_softmax(const FwdParams& p, uint8_t* smem, FwdBars* bars, ui
     }
 }
 
-template <int D, bool kPaged, bool kMods>
+template <int D, bool kPaged, bool kMods, bool kHalf>
 __global__ void __launch_bounds__(kFwdThreads, 1) fwd_kernel(const __grid_constant__ FwdParams p) {
     using C = FwdCfg<D>;
     extern __shared__ uint8_t smem_raw[];
@@ -974,14 +1000,14 @@ __global__ void __launch_bounds__(kFwdThreads, 1) fwd_kernel(const __grid_consta
     if (warp >= kSoftmaxWarps) {
         regs_decrease<64>();
         if (warp == kSoftmaxWarps) {
-            if (lane == 0) fwd_producer<D, kPaged>(p, smem, bars, wd, n_items);
+            if (lane == 0) fwd_producer<D, kPaged, kHalf>(p, smem, bars, wd, n_items);
         } else if (warp == kSoftmaxWarps + 1 || warp == kSoftmaxWarps + 2) {
             if (lane == 0) {
                 const int w = warp - kSoftmaxWarps - 1;
                 if (w == 0)
-                    fwd_mma_s<D, kPaged>(p, smem, bars, tmem, wd, n_items);
+                    fwd_mma_s<D, kPaged, kHalf>(p, smem, bars, tmem, wd, n_items);
                 else
-                    fwd_mma_pv<D, kPaged>(p, smem, bars, tmem, wd, n_items);
+                    fwd_mma_pv<D, kPaged, kHalf>(p, smem, bars, tmem, wd, n_items);
                 // every tcgen05 op this thread issued has finished before TMEM is released
                 umma_commit(&bars->drain[w]);
                 drain_wait(&bars->drain[w], 0);
@@ -989,7 +1015,7 @@ __global__ void __launch_bounds__(kFwdThreads, 1) fwd_kernel(const __grid_consta
         }
     } else {
         regs_increase<104>();
-        fwd_softmax<D, kPaged, kMods>(p, smem, bars, tmem, wd, n_items, warp >> 3, warp & 7, lane);
+        fwd_softmax<D, kPaged, kMods, kHalf>(p, smem, bars, tmem, wd, n_items, warp >> 3, warp & 7, lane);
         // the output stores this thread issued have completed before the CTA's memory goes
         if ((warp & 7) == 0 && lane == 0) bulk_wait_group_all();
     }
@@ -1155,12 +1181,14 @@ int fwd_smem_bytes(int head_dim) {
 
 cudaError_t configure_fwd_kernels() {
     const cudaFuncAttribute smem = cudaFuncAttributeMaxDynamicSharedMemorySize;
-    cudaError_t e = cudaFuncSetAttribute(fwd_kernel<128, false, false>, smem, FwdCfg<128>::kSmem);
-    if (e == cudaSuccess) e = cudaFuncSetAttribute(fwd_kernel<64, false, false>, smem, FwdCfg<64>::kSmem);
-    if (e == cudaSuccess) e = cudaFuncSetAttribute(fwd_kernel<128, true, false>, smem, FwdCfg<128>::kSmem);
-    if (e == cudaSuccess) e = cudaFuncSetAttribute(fwd_kernel<64, true, false>, smem, FwdCfg<64>::kSmem);
-    if (e == cudaSuccess) e = cudaFuncSetAttribute(fwd_kernel<128, false, true>, smem, FwdCfg<128>::kSmem);
-    if (e == cudaSuccess) e = cudaFuncSetAttribute(fwd_kernel<64, false, true>, smem, FwdCfg<64>::kSmem);
+    cudaError_t e = cudaFuncSetAttribute(fwd_kernel<128, false, false, false>, smem, FwdCfg<128>::kSmem);
+    if (e == cudaSuccess) e = cudaFuncSetAttribute(fwd_kernel<64, false, false, false>, smem, FwdCfg<64>::kSmem);
+    if (e == cudaSuccess) e = cudaFuncSetAttribute(fwd_kernel<128, true, false, false>, smem, FwdCfg<128>::kSmem);
+    if (e == cudaSuccess) e = cudaFuncSetAttribute(fwd_kernel<64, true, false, false>, smem, FwdCfg<64>::kSmem);
+    if (e == cudaSuccess) e = cudaFuncSetAttribute(fwd_kernel<128, false, true, false>, smem, FwdCfg<128>::kSmem);
+    if (e == cudaSuccess) e = cudaFuncSetAttribute(fwd_kernel<64, false, true, false>, smem, FwdCfg<64>::kSmem);
+    if (e == cudaSuccess) e = cudaFuncSetAttribute(fwd_kernel<128, false, false, true>, smem, FwdCfg<128>::kSmem);
+    if (e == cudaSuccess) e = cudaFuncSetAttribute(fwd_kernel<64, false, false, true>, smem, FwdCfg<64>::kSmem);
     return e;
 }
 
@@ -1171,7 +1199,7 @@ cudaError_t launch_fwd_prepare(const FwdPrepParams& p, cudaStream_t stream) {
 
 // The forward kernel goes out as a programmatic dependent of the work-list kernel just before
 // it: its CTAs initialise barriers and TMEM while the list is built (griddep_wait in the kernel).
-template <int D, bool kPaged, bool kMods>
+template <int D, bool kPaged, bool kMods, bool kHalf>
 cudaError_t launch_fwd_instance(const FwdParams& p, int grid, cudaStream_t stream) {
     cudaLaunchConfig_t cfg = {};
     cfg.gridDim = dim3(grid);
@@ -1183,23 +1211,28 @@ cudaError_t launch_fwd_instance(const FwdParams& p, int grid, cudaStream_t strea
     attr[0].val.programmaticStreamSerializationAllowed = 1;
     cfg.attrs = attr;
     cfg.numAttrs = 1;
-    return cudaLaunchKernelEx(&cfg, fwd_kernel<D, kPaged, kMods>, p);
+    return cudaLaunchKernelEx(&cfg, fwd_kernel<D, kPaged, kMods, kHalf>, p);
 }
 
 // K/V through block_table when p.block_table is set, else contiguous; the score-modifier
-// instance when softcap or ALiBi is requested (contiguous K/V only).
+// instance when softcap or ALiBi is requested (contiguous K/V only), the f16 instance for staged
+// keys and values of the 8-bit cache.
 cudaError_t launch_fwd(const FwdParams& p, int head_dim, int grid, cudaStream_t stream) {
     const bool paged = p.block_table != nullptr;
     const bool mods = p.softcap > 0.f || p.alibi != nullptr;
-    if (paged && mods) return cudaErrorInvalidValue;
+    const bool half = p.spans != nullptr;
+    if ((paged && mods) || (half && (paged || mods))) return cudaErrorInvalidValue;
+    if (half)
+        return head_dim == 128 ? launch_fwd_instance<128, false, false, true>(p, grid, stream)
+                               : launch_fwd_instance<64, false, false, true>(p, grid, stream);
     if (head_dim == 128) {
-        if (paged) return launch_fwd_instance<128, true, false>(p, grid, stream);
-        if (mods) return launch_fwd_instance<128, false, true>(p, grid, stream);
-        return launch_fwd_instance<128, false, false>(p, grid, stream);
+        if (paged) return launch_fwd_instance<128, true, false, false>(p, grid, stream);
+        if (mods) return launch_fwd_instance<128, false, true, false>(p, grid, stream);
+        return launch_fwd_instance<128, false, false, false>(p, grid, stream);
     }
-    if (paged) return launch_fwd_instance<64, true, false>(p, grid, stream);
-    if (mods) return launch_fwd_instance<64, false, true>(p, grid, stream);
-    return launch_fwd_instance<64, false, false>(p, grid, stream);
+    if (paged) return launch_fwd_instance<64, true, false, false>(p, grid, stream);
+    if (mods) return launch_fwd_instance<64, false, true, false>(p, grid, stream);
+    return launch_fwd_instance<64, false, false, false>(p, grid, stream);
 }
 
 }  // namespace attn

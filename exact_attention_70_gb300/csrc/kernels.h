@@ -83,6 +83,12 @@ struct FwdParams {
     const int* block_table;     // [batch, max_pages]
     const int* cache_seqlens;
     int page_size, max_pages, num_pages, box_rows;
+    // Staged f16 K/V (spans != null): q, k, v are f16 multiples of the units, sequence b's keys
+    // are rows [spans[b].x, spans[b].x + spans[b].y) of k and v.
+    const int2* spans;
+    const float* q_unit;  // [total_q, Hq]
+    const float* k_unit;  // [batch, Hkv]
+    const float* v_unit;
 };
 
 // ---- paged-cache append (chunked prefill) ---------------------------------------------------
@@ -215,10 +221,32 @@ struct ReadFp8Params {
     int batch, total_k, Hkv, page_size, max_pages, num_pages;
 };
 
+// The 8-bit cache's keys and values in f16 for the tensor-core prefill: sequence b's keys from
+// the first one its new tokens see, each sequence padded with zero rows to whole key blocks.
+struct StageFp8Params {
+    const uint8_t* k_cache;
+    const uint8_t* v_cache;
+    const uint8_t* k_scale;
+    const uint8_t* v_scale;
+    const int* block_table;
+    const int* cu_q;
+    const int* cache_seqlens;
+    __half* k;      // [rows, Hkv, d]
+    __half* v;
+    int2* spans;    // [batch]: first row, keys
+    float* k_unit;  // [batch, Hkv]: what one unit of k stands for
+    float* v_unit;
+    unsigned* status;
+    int batch, total_q, Hkv, page_size, max_pages, num_pages, wl, rows;
+};
+
 constexpr int kKv8Chunk = 128;    // keys per pipeline stage
 constexpr int kKv8Threads = 160;  // 4 MMA warps + 1 TMA warp
 constexpr int kKv8Rows = 16;      // packed query rows of one CTA
 constexpr int kKv8MinShare = 2;   // chunks a CTA takes at least
+// A chunk call whose longest sequence packs more query rows than this (tokens x heads of a kv
+// head) stages K and V in f16 for the tensor-core prefill.
+constexpr int kKv8DirectRows = 128;
 
 struct Kv8Params {
     CUtensorMap tm_k;  // 3-D over the codes [num_pages * page_size, Hkv, d] u8, box {d, 1, box_rows}
@@ -249,6 +277,8 @@ cudaError_t launch_kvcache_append_fp8(const AppendFp8Params& p, int head_dim, in
                                       cudaStream_t stream);
 cudaError_t launch_kvcache_read_fp8(const ReadFp8Params& p, int head_dim, int num_sms,
                                     cudaStream_t stream);
+cudaError_t launch_kvcache_stage_fp8(const StageFp8Params& p, int head_dim, int num_sms,
+                                     cudaStream_t stream);
 cudaError_t launch_kv8_attn(const Kv8Params& p, int head_dim, int grid, bool after_append,
                             cudaStream_t stream);
 

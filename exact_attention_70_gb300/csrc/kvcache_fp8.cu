@@ -220,6 +220,136 @@ __global__ void __launch_bounds__(256) kvcache_read_fp8_kernel(const ReadFp8Para
     }
 }
 
+// ---- staging for the tensor-core prefill ----------------------------------------------------
+//
+// A chunk of many query rows reads each key once per 256 rows, so it pays to turn the codes into
+// an MMA operand once, in f16: code 2^(e - E) with E = (the largest e of the sequence and kv head) - 7.
+// The largest magnitude is then 448 2^7 = 57344, below f16's 65504, and rows whose e is up to 22
+// below the largest stay exact (the smallest code 2^-9 meets f16's smallest 2^-24).
+
+// The first key that a new token of a sequence sees, and the keys from there on.
+__device__ __forceinline__ int2 staged_keys(const StageFp8Params& p, int b) {
+    const int q0 = p.cu_q[b], Lq = p.cu_q[b + 1] - q0, ctx = p.cache_seqlens[b];
+    if (Lq <= 0 || q0 < 0 || static_cast<long long>(q0) + Lq > p.total_q || ctx < 0 ||
+        static_cast<long long>(ctx) + Lq > static_cast<long long>(p.max_pages) * p.page_size)
+        return make_int2(0, 0);
+    const int skip = p.wl >= 0 ? max(0, ctx - p.wl) : 0;
+    return make_int2(skip, ctx + Lq - skip);
+}
+
+// One block per (sequence, kv head): the span of the sequence's rows and the units of k and v.
+constexpr int kUnitsThreads = 512;
+
+__global__ void __launch_bounds__(kUnitsThreads)
+    kvcache_units_fp8_kernel(const StageFp8Params p) {
+    constexpr int kWarps = kUnitsThreads / 32;
+    __shared__ int red[2][kWarps];
+    __shared__ long long sum[kWarps];
+    const int b = blockIdx.x / p.Hkv, kvh = blockIdx.x % p.Hkv;
+    const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+    long long before = 0;
+    for (int i = threadIdx.x; i < b; i += blockDim.x)
+        before += (staged_keys(p, i).y + kFwdBlockN - 1) / kFwdBlockN * kFwdBlockN;
+#pragma unroll
+    for (int o = 16; o > 0; o >>= 1) before += __shfl_xor_sync(0xffffffffu, before, o);
+    if (lane == 0) sum[warp] = before;
+    const int2 keys = staged_keys(p, b);
+    int top[2] = {1, 1};  // scale bytes of K and V; 255 (NaN) does not count
+    const int* bt = p.block_table + static_cast<size_t>(b) * p.max_pages;
+    const int end = keys.x + keys.y;
+    for (int g = keys.x / 16 + threadIdx.x; g * 16 < end; g += blockDim.x) {
+        const int page = bt[g * 16 / p.page_size];
+        if (page < 0 || page >= p.num_pages) continue;  // (reported where the rows are read)
+        const size_t at = (static_cast<size_t>(page) * p.Hkv + kvh) * p.page_size + g * 16 % p.page_size;
+        const uint4 kw = *reinterpret_cast<const uint4*>(p.k_scale + at);
+        const uint4 vw = *reinterpret_cast<const uint4*>(p.v_scale + at);
+        const uint32_t w[2][4] = {{kw.x, kw.y, kw.z, kw.w}, {vw.x, vw.y, vw.z, vw.w}};
+#pragma unroll
+        for (int i = 0; i < 16; ++i) {
+            if (g * 16 + i < keys.x || g * 16 + i >= end) continue;
+#pragma unroll
+            for (int j = 0; j < 2; ++j) {
+                const int e = (w[j][i / 4] >> (8 * (i % 4))) & 0xff;
+                if (e != 255) top[j] = max(top[j], e);
+            }
+        }
+    }
+#pragma unroll
+    for (int j = 0; j < 2; ++j) {
+#pragma unroll
+        for (int o = 16; o > 0; o >>= 1) top[j] = max(top[j], __shfl_xor_sync(0xffffffffu, top[j], o));
+        if (lane == 0) red[j][warp] = top[j];
+    }
+    __syncthreads();
+    if (threadIdx.x == 0) {
+        long long first = 0;
+        int e[2] = {1, 1};
+        for (int i = 0; i < kWarps; ++i) {
+            first += sum[i];
+            e[0] = max(e[0], red[0][i]);
+            e[1] = max(e[1], red[1][i]);
+        }
+        const long long padded = (keys.y + kFwdBlockN - 1) / kFwdBlockN * kFwdBlockN;
+        const bool fits = first + padded <= p.rows;
+        if (!fits) atomicOr(p.status, kStatusBounds);  // more keys than the caller's bound
+        if (kvh == 0) p.spans[b] = fits ? make_int2(static_cast<int>(first), keys.y) : make_int2(p.rows, 0);
+        p.k_unit[blockIdx.x] = e8m0_to_f32(max(1, e[0] - 7));
+        p.v_unit[blockIdx.x] = e8m0_to_f32(max(1, e[1] - 7));
+    }
+}
+
+// 16 codes a thread, k and v row by row.
+template <int D>
+__global__ void __launch_bounds__(256) kvcache_stage_fp8_kernel(const StageFp8Params p) {
+    constexpr int kLanes = D / 16;
+    const long long total = static_cast<long long>(p.rows) * 2 * p.Hkv * kLanes;
+    for (long long i = static_cast<long long>(blockIdx.x) * blockDim.x + threadIdx.x; i < total;
+         i += static_cast<long long>(gridDim.x) * blockDim.x) {
+        const int e0 = static_cast<int>(i % kLanes) * 16;
+        const long long row = i / kLanes;
+        const int r = static_cast<int>(row % (2 * p.Hkv));
+        const int t = static_cast<int>(row / (2 * p.Hkv));
+        int lo = 0, hi = p.batch - 1;
+        while (lo < hi) {
+            const int mid = (lo + hi + 1) >> 1;
+            if (p.spans[mid].x <= t) lo = mid; else hi = mid - 1;
+        }
+        const int b = lo;
+        const int2 span = p.spans[b];
+        const int j = t - span.x;
+        if (j < 0 || j >= (span.y + kFwdBlockN - 1) / kFwdBlockN * kFwdBlockN) continue;
+        const bool is_v = r >= p.Hkv;
+        const int kvh = is_v ? r - p.Hkv : r;
+        uint32_t out[8] = {0, 0, 0, 0, 0, 0, 0, 0};
+        if (j < span.y) {
+            const int pos = staged_keys(p, b).x + j;
+            const int page = p.block_table[static_cast<size_t>(b) * p.max_pages + pos / p.page_size];
+            if (page < 0 || page >= p.num_pages) {
+                atomicOr(p.status, kStatusBounds);  // zeros
+            } else {
+                const size_t slot = static_cast<size_t>(pos % p.page_size);
+                const uint4 w = *reinterpret_cast<const uint4*>(
+                    (is_v ? p.v_cache : p.k_cache) +
+                    ((static_cast<size_t>(page) * p.page_size + slot) * p.Hkv + kvh) * D + e0);
+                const int sb = (is_v ? p.v_scale : p.k_scale)[
+                    (static_cast<size_t>(page) * p.Hkv + kvh) * p.page_size + slot];
+                const int eb = __float_as_int((is_v ? p.v_unit : p.k_unit)[b * p.Hkv + kvh]) >> 23;
+                const float scale = sb == 255 ? __int_as_float(0x7fffffff) : exp2_int(sb - eb);
+                const uint32_t in[4] = {w.x, w.y, w.z, w.w};
+#pragma unroll
+                for (int k = 0; k < 8; ++k) {
+                    const float2 f = f16x2_to_float2(e4m3x2_to_f16x2(in[k / 2] >> (16 * (k & 1))));
+                    out[k] = pack_f16x2(f.x * scale, f.y * scale);
+                }
+            }
+        }
+        uint4* dst = reinterpret_cast<uint4*>((is_v ? p.v : p.k) +
+                                              (static_cast<size_t>(t) * p.Hkv + kvh) * D + e0);
+        dst[0] = make_uint4(out[0], out[1], out[2], out[3]);
+        dst[1] = make_uint4(out[4], out[5], out[6], out[7]);
+    }
+}
+
 unsigned grid_for(long long threads, int num_sms) {
     const long long blocks = (threads + 255) / 256, cap = static_cast<long long>(num_sms) * 8;
     return static_cast<unsigned>(blocks < cap ? blocks : cap);
@@ -237,6 +367,20 @@ cudaError_t launch_kvcache_append_fp8(const AppendFp8Params& p, int head_dim, in
         kvcache_append_fp8_kernel<128><<<grid, 256, 0, stream>>>(p);
     else
         kvcache_append_fp8_kernel<64><<<grid, 256, 0, stream>>>(p);
+    return cudaGetLastError();
+}
+
+cudaError_t launch_kvcache_stage_fp8(const StageFp8Params& p, int head_dim, int num_sms,
+                                     cudaStream_t stream) {
+    kvcache_units_fp8_kernel<<<static_cast<unsigned>(p.batch) * p.Hkv, kUnitsThreads, 0, stream>>>(p);
+    cudaError_t e = cudaGetLastError();
+    if (e != cudaSuccess) return e;
+    const unsigned grid =
+        grid_for(static_cast<long long>(p.rows) * 2 * p.Hkv * (head_dim / 16), num_sms);
+    if (head_dim == 128)
+        kvcache_stage_fp8_kernel<128><<<grid, 256, 0, stream>>>(p);
+    else
+        kvcache_stage_fp8_kernel<64><<<grid, 256, 0, stream>>>(p);
     return cudaGetLastError();
 }
 

@@ -199,6 +199,8 @@ CHUNK = [
     ([50, 300], [40, 5], 6, 2, 64, 64, 0, False, False, (30, 7)),   # both sides bounded
     ([2000], [4], 8, 2, 128, 64, 128, False, True, (0, 0)),         # a row sees itself alone
     ([1500, 10], [3, 9], 20, 1, 128, 128, 64, False, True, (-1, -1)),
+    ([0, 0, 700, 5], [0, 129, 1, 300], 4, 4, 128, 16, 128, True, True, (64, -1)),
+    ([300, 77], [50, 140], 12, 4, 64, 192, 0, False, False, (-1, 20)),
 ]
 
 
@@ -312,6 +314,9 @@ def test_bad_pages_and_lengths_are_reported(attn):
     c = kv8_case([100, 30], [20, 3], 4, 2, 64, 16, seed=133)
     c.new = [19, 3]                                                       # max_seqlen_q too small
     chunk(attn, c, gpu_cache(c), max_total_k=153)
+    assert status() == -6
+    c = kv8_case([900, 30], [100, 3], 4, 1, 64, 16, seed=133)
+    chunk(attn, c, gpu_cache(c), max_total_k=700)                         # max_total_k too small
     assert status() == -6
     for cu in ([0, 20, 90], [-4, 20, 23], [0, 23, 20]):                   # bad offsets
         c = kv8_case([100, 30], [20, 3], 4, 2, 64, 16, seed=134)
