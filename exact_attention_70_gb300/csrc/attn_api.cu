@@ -877,9 +877,18 @@ size_t kv8_query_bytes(long long rows, int head_dim) {
 }
 
 // Whether a chunk call runs the tensor-core prefill on staged f16 keys and values, or the 16-row
-// kernel on the codes.
+// kernel on the codes.  The latter's time grows with the query rows (tokens x heads of a kv
+// head) and is spread over the whole GPU; the former pays for the staging and for a pass of 256
+// rows over all keys by one SM, whatever the rows, so it needs more of them where few (sequence,
+// kv head) pairs keep few SMs busy.  Measured, us (16-row kernel / staged):
+//   16 sequences x 8 kv heads, 8000 keys:   64 rows 187 / 299,  128 rows 352 / 304,  256 rows 666 / 329
+//   64 x 8, 1000 keys:                      64 rows 143 / 206,  128 rows 286 / 232
+//   4 x 8, 8000 keys:                      128 rows  96 / 141,  256 rows 179 / 172
+//   1 x 8, 16000 keys:                     512 rows 162 / 229, 1024 rows 308 / 235
 bool kv8_staged(int batch, int max_seqlen_q, int nheads_q, int nheads_kv) {
-    return static_cast<long long>(max_seqlen_q) * (nheads_q / nheads_kv) > kKv8DirectRows;
+    const long long rows = static_cast<long long>(max_seqlen_q) * (nheads_q / nheads_kv);
+    const long long pairs = static_cast<long long>(batch) * nheads_kv;
+    return rows > 112 && rows * pairs > 6144;
 }
 
 // The staged path's workspace behind the queries.
@@ -939,6 +948,7 @@ attn_status_t attn_kvcache_append_fp8(const void* k_new, const void* v_new, void
     attn_status_t st = kv8_sizes(batch, nheads_kv, head_dim, page_size, max_pages_per_seq, num_pages);
     if (st != ATTN_OK) return st;
     if (total_q < 0) return ATTN_ERR_INVALID_ARG;
+    if (static_cast<long long>(total_q) * nheads_kv > (1LL << 31) - 1) return ATTN_ERR_UNSUPPORTED;
     st = rotary_ok(rotary_cos, rotary_sin, rotary_dim, rotary_rows, head_dim);
     if (st != ATTN_OK) return st;
     if (batch == 0 || total_q == 0) return ATTN_OK;
@@ -972,8 +982,7 @@ attn_status_t attn_kvcache_append_fp8(const void* k_new, const void* v_new, void
     ap.rot_dim = rotary_dim;
     ap.rot_rows = rotary_rows;
     ap.interleaved = rotary_interleaved ? 1 : 0;
-    if (launch_kvcache_append_fp8(ap, head_dim, dev->num_sms, static_cast<cudaStream_t>(stream)) !=
-        cudaSuccess)
+    if (launch_kvcache_append_fp8(ap, head_dim, static_cast<cudaStream_t>(stream)) != cudaSuccess)
         return ATTN_ERR_CUDA;
     return ATTN_OK;
 }
@@ -987,6 +996,7 @@ attn_status_t attn_kvcache_read_fp8(const void* k_cache, const void* v_cache, co
     attn_status_t st = kv8_sizes(batch, nheads_kv, head_dim, page_size, max_pages_per_seq, num_pages);
     if (st != ATTN_OK) return st;
     if (total_k < 0) return ATTN_ERR_INVALID_ARG;
+    if (static_cast<long long>(total_k) * nheads_kv > (1LL << 31) - 1) return ATTN_ERR_UNSUPPORTED;
     if (batch == 0 || total_k == 0) return ATTN_OK;
     if (!kv8_cache_ok(k_cache, v_cache, k_scale, v_scale, block_table) || !cu_seqlens_k || !k || !v ||
         !aligned(cu_seqlens_k, 4) || !aligned(k, 16) || !aligned(v, 16))
@@ -1011,8 +1021,7 @@ attn_status_t attn_kvcache_read_fp8(const void* k_cache, const void* v_cache, co
     rp.page_size = page_size;
     rp.max_pages = max_pages_per_seq;
     rp.num_pages = num_pages;
-    if (launch_kvcache_read_fp8(rp, head_dim, dev->num_sms, static_cast<cudaStream_t>(stream)) !=
-        cudaSuccess)
+    if (launch_kvcache_read_fp8(rp, head_dim, static_cast<cudaStream_t>(stream)) != cudaSuccess)
         return ATTN_ERR_CUDA;
     return ATTN_OK;
 }
@@ -1177,7 +1186,7 @@ attn_status_t attn_fwd_kvcache_fp8(const void* q, const void* k_new, const void*
     ap.rot_dim = rotary_dim;
     ap.rot_rows = rotary_rows;
     ap.interleaved = rotary_interleaved ? 1 : 0;
-    if (launch_kvcache_append_fp8(ap, head_dim, dev->num_sms, s) != cudaSuccess) return ATTN_ERR_CUDA;
+    if (launch_kvcache_append_fp8(ap, head_dim, s) != cudaSuccess) return ATTN_ERR_CUDA;
 
     if (staged) {
         // 2. the keys and values the new tokens see, in f16
@@ -1206,8 +1215,7 @@ attn_status_t attn_fwd_kvcache_fp8(const void* q, const void* k_new, const void*
         sp.num_pages = num_pages;
         sp.wl = window_left;
         sp.rows = static_cast<int>(l.rows);
-        if (launch_kvcache_stage_fp8(sp, head_dim, dev->num_sms, s) != cudaSuccess)
-            return ATTN_ERR_CUDA;
+        if (launch_kvcache_stage_fp8(sp, head_dim, s) != cudaSuccess) return ATTN_ERR_CUDA;
 
         // 3. the prefill kernel on them
         const int tpt = tokens_per_tile(g);

@@ -244,9 +244,6 @@ constexpr int kKv8Chunk = 128;    // keys per pipeline stage
 constexpr int kKv8Threads = 160;  // 4 MMA warps + 1 TMA warp
 constexpr int kKv8Rows = 16;      // packed query rows of one CTA
 constexpr int kKv8MinShare = 2;   // chunks a CTA takes at least
-// A chunk call whose longest sequence packs more query rows than this (tokens x heads of a kv
-// head) stages K and V in f16 for the tensor-core prefill.
-constexpr int kKv8DirectRows = 128;
 
 struct Kv8Params {
     CUtensorMap tm_k;  // 3-D over the codes [num_pages * page_size, Hkv, d] u8, box {d, 1, box_rows}
@@ -273,12 +270,9 @@ struct Kv8Params {
     float scale_log2;
 };
 
-cudaError_t launch_kvcache_append_fp8(const AppendFp8Params& p, int head_dim, int num_sms,
-                                      cudaStream_t stream);
-cudaError_t launch_kvcache_read_fp8(const ReadFp8Params& p, int head_dim, int num_sms,
-                                    cudaStream_t stream);
-cudaError_t launch_kvcache_stage_fp8(const StageFp8Params& p, int head_dim, int num_sms,
-                                     cudaStream_t stream);
+cudaError_t launch_kvcache_append_fp8(const AppendFp8Params& p, int head_dim, cudaStream_t stream);
+cudaError_t launch_kvcache_read_fp8(const ReadFp8Params& p, int head_dim, cudaStream_t stream);
+cudaError_t launch_kvcache_stage_fp8(const StageFp8Params& p, int head_dim, cudaStream_t stream);
 cudaError_t launch_kv8_attn(const Kv8Params& p, int head_dim, int grid, bool after_append,
                             cudaStream_t stream);
 

@@ -574,6 +574,12 @@ __device__ __forceinline__ uint32_t pack_f16x2(float lo, float hi) {
     return r;
 }
 
+__device__ __forceinline__ uint32_t f16x2_mul(uint32_t a, uint32_t b) {
+    uint32_t r;
+    asm("mul.rn.f16x2 %0, %1, %2;" : "=r"(r) : "r"(a), "r"(b));
+    return r;
+}
+
 // 2^n for n <= 127; 0 below the normal range.
 __device__ __forceinline__ float exp2_int(int n) {
     return n < -126 ? 0.f : __int_as_float((n + 127) << 23);

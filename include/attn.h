@@ -381,8 +381,9 @@ size_t attn_decode_kvcache_fp8_workspace_bytes(int batch, int nheads_q, int nhea
  *   q    device bf16 [total_q, nheads_q, head_dim]; out the same shape; lse device fp32
  *        [nheads_q, total_q]; rows outside every sequence are left as they were
  *   max_seqlen_q  an upper bound on the new tokens of a sequence (checked on the device)
- *   max_total_k   an upper bound on sum_b (cache_seqlens[b] + new tokens of b) (checked on the
- *                 device); sizes the workspace
+ *   max_total_k   an upper bound on sum_b (cache_seqlens[b] + new tokens of b); sizes the workspace
+ *                 (long chunks stage keys and values there; sequences past the bound raise
+ *                 ATTN_ERR_DEVICE_BOUNDS)
  *   causal, window_left, window_right   see "Visibility"
  *   workspace     attn_fwd_kvcache_fp8_workspace_bytes(...) bytes, 256-byte aligned
  * A NaN or an infinity among the new values reaches the rows that see it, and may reach the other

@@ -201,6 +201,13 @@ CHUNK = [
     ([1500, 10], [3, 9], 20, 1, 128, 128, 64, False, True, (-1, -1)),
     ([0, 0, 700, 5], [0, 129, 1, 300], 4, 4, 128, 16, 128, True, True, (64, -1)),
     ([300, 77], [50, 140], 12, 4, 64, 192, 0, False, False, (-1, 20)),
+    # enough rows for the staged path
+    ([3000, 40], [200, 90], 32, 8, 64, 128, 64, True, True, (300, 0)),
+    ([0], [250], 32, 8, 128, 16, 0, False, False, (-1, -1)),
+    ([640, 7, 0, 3], [64, 200, 1, 0], 64, 8, 64, 16, 16, True, True, (100, 0)),
+    ([50, 300, 900], [40, 90, 2], 30, 10, 64, 64, 0, False, False, (30, 7)),
+    ([700, 5], [1, 100], 128, 2, 128, 192, 128, False, True, (64, -1)),
+    ([0, 130], [400, 300], 16, 8, 128, 32, 96, False, True, (-1, -1)),
 ]
 
 
@@ -267,6 +274,20 @@ def test_a_generation_from_prompt_to_tokens(attn):
     kv8_exact.check(out, lse.t(), kv8_exact.attention(c, arrays), 2.0 ** -8, False, "attn_fwd")
 
 
+@pytest.mark.parametrize("q", [3, 200])
+def test_chunk_with_rows_of_very_different_scales(attn, q):
+    """Cached and new rows 2^24 apart, in both ways a chunk is computed."""
+    c = kv8_case([100, 257], [q, q // 2], 32, 8, 64, 32, seed=115, rotary_dim=64, spread=6.0, scale=2e-3)
+    f = 2.0 ** torch.arange(-6, 7).float().repeat(q)[:c.k_new.shape[0], None, None]
+    c.k_new, c.v_new = (c.k_new.float() * f).to(torch.bfloat16), (c.v_new.float() / f).to(torch.bfloat16)
+    cache = gpu_cache(c)
+    out, lse = chunk(attn, c, cache)
+    assert attn.attn_get_device_status() == 0
+    arrays = kv8_exact.appended(c)
+    same_cache(cache, arrays)
+    kv8_exact.check(out, lse.t(), kv8_exact.attention(c, arrays), 2.0 ** -11, True)
+
+
 def test_nan_in_a_visible_token_reaches_its_rows_only(attn):
     c = kv8_case([40, 50], None, 4, 2, 64, 16, seed=120)
     c.k_cache[int(c.block_table[1, 1]), 3, 0, 5] = 0x7F   # kv head 0 of sequence 1
@@ -315,7 +336,7 @@ def test_bad_pages_and_lengths_are_reported(attn):
     c.new = [19, 3]                                                       # max_seqlen_q too small
     chunk(attn, c, gpu_cache(c), max_total_k=153)
     assert status() == -6
-    c = kv8_case([900, 30], [100, 3], 4, 1, 64, 16, seed=133)
+    c = kv8_case([900, 30], [100, 3], 32, 8, 64, 16, seed=133)
     chunk(attn, c, gpu_cache(c), max_total_k=700)                         # max_total_k too small
     assert status() == -6
     for cu in ([0, 20, 90], [-4, 20, 23], [0, 23, 20]):                   # bad offsets
