@@ -104,7 +104,7 @@ def load():
 
 
 def _ptr(t):
-    return ctypes.c_void_p(t.data_ptr()) if t is not None else None
+    return t.data_ptr() if t is not None else None
 
 
 def _stream(stream):
@@ -114,6 +114,9 @@ def _stream(stream):
 
 
 def _check(t, name, dtype, ndim):
+    if (type(t) is torch.Tensor and t.dtype is dtype and t.dim() == ndim and t.is_cuda
+            and t.is_contiguous()):
+        return
     if not isinstance(t, torch.Tensor):
         raise TypeError(f"{name} must be a torch.Tensor")
     if t.device.type != "cuda":
@@ -483,61 +486,97 @@ def attn_decode_kvcache_noalloc(q, k_cache, v_cache, cache_seqlens, block_table,
 # ---- 8-bit paged KV cache ------------------------------------------------------------------
 
 
-def _on(device, stream, body):
-    """body(stream pointer) with `device` current and what it allocates belonging to `stream`
-    (default: the device's current stream)."""
+# The current stream's handle without building a Stream object (a few microseconds a call).
+_raw_stream = getattr(torch._C, "_cuda_getCurrentRawStream",
+                      lambda index: torch.cuda.current_stream(index).cuda_stream)
+
+
+def _on(index, stream, body, *args):
+    """body(stream handle, *args) with device `index` current and what it allocates belonging to
+    `stream` (default: the device's current stream)."""
     if stream is None:
-        if torch.cuda.current_device() == device.index:
-            return body(ctypes.c_void_p(torch.cuda.current_stream().cuda_stream))
-        with torch.cuda.device(device):
-            return body(ctypes.c_void_p(torch.cuda.current_stream().cuda_stream))
-    if stream.device != device:
+        if torch.cuda.current_device() == index:
+            return body(_raw_stream(index), *args)
+        with torch.cuda.device(index):
+            return body(_raw_stream(index), *args)
+    if stream.device.index != index:
         raise ValueError("the stream must belong to the tensors' device")
-    with torch.cuda.device(device), torch.cuda.stream(stream):
-        return body(ctypes.c_void_p(stream.cuda_stream))
+    with torch.cuda.device(index), torch.cuda.stream(stream):
+        return body(stream.cuda_stream, *args)
 
 
-def _same_device(first, *others):
+def _at(t, name, dtype, ndim):
+    """The address of a tensor argument (_check's conditions)."""
+    if type(t) is torch.Tensor and t.dtype is dtype and t.dim() == ndim and t.is_contiguous():
+        return t.data_ptr()  # (CPU tensors fail _device)
+    _check(t, name, dtype, ndim)
+    return t.data_ptr()
+
+
+def _maybe_at(t, name, dtype, shape):
+    """The same for an optional argument of a known shape."""
+    if t is None:
+        return None
+    if t.shape != shape:
+        raise ValueError(f"{name} must be {list(shape)}")
+    return _at(t, name, dtype, len(shape))
+
+
+def _device(first, *others):
+    """The index of the CUDA device that all the tensors are on."""
+    index = first.get_device()
     for t in others:
-        if t is not None and t.device != first.device:
-            raise ValueError("all tensors must be on one device")
+        if t is not None and t.get_device() != index:
+            raise ValueError("all tensors must be on one CUDA device")
+    if index < 0:
+        raise ValueError("all tensors must be CUDA tensors")
+    return index
 
 
-def _kv8_shapes(k_cache, v_cache, k_scale, v_scale, block_table, batch):
-    """Checks shared by the calls on the 8-bit cache; returns its sizes."""
-    _check(k_cache, "k_cache", torch.uint8, 4)
-    _check(v_cache, "v_cache", torch.uint8, 4)
-    _check(k_scale, "k_scale", torch.uint8, 3)
-    _check(v_scale, "v_scale", torch.uint8, 3)
-    _check(block_table, "block_table", torch.int32, 2)
-    num_pages, page_size, Hkv, d = k_cache.shape
-    if v_cache.shape != k_cache.shape:
+def _kv8_at(k_cache, v_cache, k_scale, v_scale, block_table):
+    """The addresses of what describes the 8-bit cache."""
+    u8 = torch.uint8
+    return (_at(k_cache, "k_cache", u8, 4), _at(v_cache, "v_cache", u8, 4),
+            _at(k_scale, "k_scale", u8, 3), _at(v_scale, "v_scale", u8, 3),
+            _at(block_table, "block_table", torch.int32, 2))
+
+
+def _kv8_sizes(k_cache, v_cache, k_scale, v_scale, block_table, batch):
+    """The sizes the calls on the 8-bit cache share: (num_pages, page_size, Hkv, d, max_pages)."""
+    shape = k_cache.shape
+    num_pages, page_size, Hkv, d = shape
+    if v_cache.shape != shape:
         raise ValueError("k_cache and v_cache must both be [num_pages, page_size, Hkv, d]")
     if k_scale.shape != (num_pages, Hkv, page_size) or v_scale.shape != k_scale.shape:
         raise ValueError("k_scale and v_scale must both be [num_pages, Hkv, page_size]")
-    if block_table.shape[0] != batch:
+    rows, max_pages = block_table.shape
+    if rows != batch:
         raise ValueError("block_table must have one row per sequence")
-    return num_pages, page_size, Hkv, d
+    return num_pages, page_size, Hkv, d, max_pages
 
 
-def _rotary_shapes(rotary_cos, rotary_sin):
+def _rotary(rotary_cos, rotary_sin):
+    """(cos address, sin address, rotary_dim, rows)."""
     if rotary_cos is None and rotary_sin is None:
-        return 0, 0
-    _check(rotary_cos, "rotary_cos", torch.float32, 2)
-    _check(rotary_sin, "rotary_sin", torch.float32, 2)
+        return None, None, 0, 0
+    cos = _at(rotary_cos, "rotary_cos", torch.float32, 2)
+    sin = _at(rotary_sin, "rotary_sin", torch.float32, 2)
+    rows, half = rotary_cos.shape
     if rotary_sin.shape != rotary_cos.shape:
         raise ValueError("rotary_cos and rotary_sin must both be [rows, rotary_dim / 2]")
-    return rotary_cos.shape[0], 2 * rotary_cos.shape[1]
+    return cos, sin, 2 * half, rows
 
 
-def _new_tokens(k_new, v_new, cache_seqlens, cu_seqlens_q, Hkv, d):
-    _check(k_new, "k_new", torch.bfloat16, 3)
-    _check(v_new, "v_new", torch.bfloat16, 3)
-    _check(cache_seqlens, "cache_seqlens", torch.int32, 1)
-    if k_new.shape[1:] != (Hkv, d) or v_new.shape != k_new.shape:
+def _new_tokens(k_new, v_new, cache_seqlens, batch, Hkv, d):
+    """The addresses of the new keys and values and of cache_seqlens, and the tokens."""
+    at = (_at(k_new, "k_new", torch.bfloat16, 3), _at(v_new, "v_new", torch.bfloat16, 3),
+          _at(cache_seqlens, "cache_seqlens", torch.int32, 1))
+    total_q = k_new.shape[0]
+    if k_new.shape != (total_q, Hkv, d) or v_new.shape != k_new.shape:
         raise ValueError("k_new and v_new must both be [total_q, Hkv, d] with the cache's Hkv and d")
-    if cache_seqlens.numel() != cu_seqlens_q.numel() - 1:
+    if cache_seqlens.numel() != batch:
         raise ValueError("cache_seqlens must have one entry per sequence")
+    return *at, total_q
 
 
 def attn_kvcache_append_fp8(k_new, v_new, k_cache, v_cache, k_scale, v_scale, cache_seqlens,
@@ -550,23 +589,23 @@ def attn_kvcache_append_fp8(k_new, v_new, k_cache, v_cache, k_scale, v_scale, ca
     cache_seqlens[b] + i.  rotary_cos / rotary_sin fp32 [rows, rotary_dim / 2] or None.
     """
     lib = load()
-    _check(cu_seqlens_q, "cu_seqlens_q", torch.int32, 1)
+    kc, vc, ks, vs, bt = _kv8_at(k_cache, v_cache, k_scale, v_scale, block_table)
+    cu = _at(cu_seqlens_q, "cu_seqlens_q", torch.int32, 1)
     batch = cu_seqlens_q.numel() - 1
-    num_pages, page_size, Hkv, d = _kv8_shapes(k_cache, v_cache, k_scale, v_scale, block_table,
-                                               batch)
-    _new_tokens(k_new, v_new, cache_seqlens, cu_seqlens_q, Hkv, d)
-    rot_rows, rot_dim = _rotary_shapes(rotary_cos, rotary_sin)
-    _same_device(k_new, v_new, k_cache, v_cache, k_scale, v_scale, cache_seqlens, block_table,
-                 cu_seqlens_q, rotary_cos, rotary_sin)
+    num_pages, page_size, Hkv, d, max_pages = _kv8_sizes(k_cache, v_cache, k_scale, v_scale,
+                                                         block_table, batch)
+    kn, vn, sl, total_q = _new_tokens(k_new, v_new, cache_seqlens, batch, Hkv, d)
+    cos, sin, rot_dim, rot_rows = _rotary(rotary_cos, rotary_sin)
+    index = _device(k_cache, v_cache, k_scale, v_scale, block_table, cu_seqlens_q, k_new, v_new,
+                    cache_seqlens, rotary_cos, rotary_sin)
 
     def body(s):
         return lib.attn_kvcache_append_fp8(
-            _ptr(k_new), _ptr(v_new), _ptr(k_cache), _ptr(v_cache), _ptr(k_scale), _ptr(v_scale),
-            _ptr(cache_seqlens), _ptr(block_table), _ptr(cu_seqlens_q), _ptr(rotary_cos),
-            _ptr(rotary_sin), rot_dim, rot_rows, int(bool(rotary_interleaved)), batch,
-            k_new.shape[0], Hkv, d, page_size, block_table.shape[1], num_pages, s)
+            kn, vn, kc, vc, ks, vs, sl, bt, cu, cos, sin, rot_dim, rot_rows,
+            1 if rotary_interleaved else 0, batch, total_q, Hkv, d, page_size, max_pages,
+            num_pages, s)
 
-    rc = _on(k_new.device, stream, body)
+    rc = _on(index, stream, body)
     if rc != 0:
         raise AttnError(rc, "attn_kvcache_append_fp8")
 
@@ -576,30 +615,27 @@ def attn_kvcache_read_fp8(k_cache, v_cache, k_scale, v_scale, block_table, cu_se
     """Read the first cu_seqlens_k[b + 1] - cu_seqlens_k[b] tokens of every sequence of the 8-bit
     cache back.  Returns (k, v), bf16 [total_k, Hkv, d], packed as attn_fwd takes them."""
     lib = load()
-    _check(cu_seqlens_k, "cu_seqlens_k", torch.int32, 1)
+    kc, vc, ks, vs, bt = _kv8_at(k_cache, v_cache, k_scale, v_scale, block_table)
+    cu = _at(cu_seqlens_k, "cu_seqlens_k", torch.int32, 1)
     batch = cu_seqlens_k.numel() - 1
-    num_pages, page_size, Hkv, d = _kv8_shapes(k_cache, v_cache, k_scale, v_scale, block_table,
-                                               batch)
+    num_pages, page_size, Hkv, d, max_pages = _kv8_sizes(k_cache, v_cache, k_scale, v_scale,
+                                                         block_table, batch)
     shape = (int(total_k), Hkv, d)
-    for t, n in ((k, "k"), (v, "v")):
-        if t is not None:
-            _check(t, n, torch.bfloat16, 3)
-            if t.shape != shape:
-                raise ValueError(f"{n} must be [total_k, Hkv, d]")
-    _same_device(k_cache, v_cache, k_scale, v_scale, block_table, cu_seqlens_k, k, v)
+    _maybe_at(k, "k", torch.bfloat16, shape)
+    _maybe_at(v, "v", torch.bfloat16, shape)
+    index = _device(k_cache, v_cache, k_scale, v_scale, block_table, cu_seqlens_k, k, v)
 
     def body(s):
-        ko = torch.empty(shape, dtype=torch.bfloat16, device=k_cache.device) if k is None else k
-        vo = torch.empty(shape, dtype=torch.bfloat16, device=k_cache.device) if v is None else v
-        rc = lib.attn_kvcache_read_fp8(
-            _ptr(k_cache), _ptr(v_cache), _ptr(k_scale), _ptr(v_scale), _ptr(block_table),
-            _ptr(cu_seqlens_k), _ptr(ko), _ptr(vo), batch, shape[0], Hkv, d, page_size,
-            block_table.shape[1], num_pages, s)
+        device = k_cache.device
+        ko = torch.empty(shape, dtype=torch.bfloat16, device=device) if k is None else k
+        vo = torch.empty(shape, dtype=torch.bfloat16, device=device) if v is None else v
+        rc = lib.attn_kvcache_read_fp8(kc, vc, ks, vs, bt, cu, ko.data_ptr(), vo.data_ptr(), batch,
+                                       shape[0], Hkv, d, page_size, max_pages, num_pages, s)
         if rc != 0:
             raise AttnError(rc, "attn_kvcache_read_fp8")
         return ko, vo
 
-    return _on(k_cache.device, stream, body)
+    return _on(index, stream, body)
 
 
 def attn_decode_kvcache_fp8_workspace_bytes(batch, nheads_q, nheads_kv, head_dim, page_size,
@@ -615,33 +651,35 @@ def attn_decode_kvcache_fp8(q, k_cache, v_cache, k_scale, v_scale, cache_seqlens
     Returns (out [batch, Hq, d] bf16, lse [batch, Hq] fp32).
     """
     lib = load()
-    _check(q, "q", torch.bfloat16, 3)
-    _check(cache_seqlens, "cache_seqlens", torch.int32, 1)
-    batch, Hq, d = q.shape
-    num_pages, page_size, Hkv, dk = _kv8_shapes(k_cache, v_cache, k_scale, v_scale, block_table,
-                                                batch)
-    if dk != d:
+    kc, vc, ks, vs, bt = _kv8_at(k_cache, v_cache, k_scale, v_scale, block_table)
+    qp = _at(q, "q", torch.bfloat16, 3)
+    sl = _at(cache_seqlens, "cache_seqlens", torch.int32, 1)
+    batch, Hq, dq = q.shape
+    num_pages, page_size, Hkv, d, max_pages = _kv8_sizes(k_cache, v_cache, k_scale, v_scale,
+                                                         block_table, batch)
+    if dq != d:
         raise ValueError("q must have the cache's head dimension")
     if cache_seqlens.numel() != batch:
         raise ValueError("cache_seqlens must have one entry per sequence")
-    _same_device(q, k_cache, v_cache, k_scale, v_scale, cache_seqlens, block_table, out, lse,
-                 workspace)
+    _maybe_at(out, "out", torch.bfloat16, (batch, Hq, d))
+    _maybe_at(lse, "lse", torch.float32, (batch, Hq))
+    index = _device(k_cache, v_cache, k_scale, v_scale, block_table, q, cache_seqlens, out, lse,
+                    workspace)
     scale = d ** -0.5 if softmax_scale is None else float(softmax_scale)
-    nbytes = int(lib.attn_decode_kvcache_fp8_workspace_bytes(batch, Hq, Hkv, d, page_size,
-                                                             block_table.shape[1]))
+    nbytes = lib.attn_decode_kvcache_fp8_workspace_bytes(batch, Hq, Hkv, d, page_size, max_pages)
 
     def body(s):
-        o, l = _decode_outputs(q, out, lse)
+        o = torch.empty_like(q) if out is None else out
+        l = torch.empty((batch, Hq), dtype=torch.float32, device=q.device) if lse is None else lse
         ws = _workspace(nbytes, q.device, workspace)
-        rc = lib.attn_decode_kvcache_fp8(
-            _ptr(q), _ptr(k_cache), _ptr(v_cache), _ptr(k_scale), _ptr(v_scale),
-            _ptr(cache_seqlens), _ptr(block_table), page_size, _ptr(o), _ptr(l), batch, Hq, Hkv,
-            d, block_table.shape[1], num_pages, scale, _ptr(ws), nbytes, s)
+        rc = lib.attn_decode_kvcache_fp8(qp, kc, vc, ks, vs, sl, bt, page_size, o.data_ptr(),
+                                         l.data_ptr(), batch, Hq, Hkv, d, max_pages, num_pages,
+                                         scale, _ptr(ws), nbytes, s)
         if rc != 0:
             raise AttnError(rc, "attn_decode_kvcache_fp8")
         return o, l
 
-    return _on(q.device, stream, body)
+    return _on(index, stream, body)
 
 
 def attn_fwd_kvcache_fp8_workspace_bytes(batch, total_q, max_seqlen_q, max_total_k, nheads_q,
@@ -664,44 +702,39 @@ def attn_fwd_kvcache_fp8(q, k_new, v_new, k_cache, v_cache, k_scale, v_scale, ca
     what block_table can hold).  Returns (out [total_q, Hq, d], lse [Hq, total_q]).
     """
     lib = load()
-    _check(q, "q", torch.bfloat16, 3)
-    _check(cu_seqlens_q, "cu_seqlens_q", torch.int32, 1)
+    kc, vc, ks, vs, bt = _kv8_at(k_cache, v_cache, k_scale, v_scale, block_table)
+    qp = _at(q, "q", torch.bfloat16, 3)
+    cu = _at(cu_seqlens_q, "cu_seqlens_q", torch.int32, 1)
     batch = cu_seqlens_q.numel() - 1
-    num_pages, page_size, Hkv, d = _kv8_shapes(k_cache, v_cache, k_scale, v_scale, block_table,
-                                               batch)
-    _new_tokens(k_new, v_new, cache_seqlens, cu_seqlens_q, Hkv, d)
-    total_q, Hq = q.shape[:2]
-    if q.shape[2] != d or k_new.shape[0] != total_q:
+    num_pages, page_size, Hkv, d, max_pages = _kv8_sizes(k_cache, v_cache, k_scale, v_scale,
+                                                         block_table, batch)
+    kn, vn, sl, total_q = _new_tokens(k_new, v_new, cache_seqlens, batch, Hkv, d)
+    Hq = q.shape[1]
+    if q.shape != (total_q, Hq, d):
         raise ValueError("q, k_new and v_new must have the same tokens and head dimension")
-    rot_rows, rot_dim = _rotary_shapes(rotary_cos, rotary_sin)
-    for t, n, dt, shape in ((out, "out", torch.bfloat16, (total_q, Hq, d)),
-                            (lse, "lse", torch.float32, (Hq, total_q))):
-        if t is not None:
-            _check(t, n, dt, len(shape))
-            if t.shape != shape:
-                raise ValueError(f"{n} must be {list(shape)}")
-    _same_device(q, k_new, v_new, k_cache, v_cache, k_scale, v_scale, cache_seqlens, block_table,
-                 cu_seqlens_q, rotary_cos, rotary_sin, out, lse, workspace)
-    max_pages = block_table.shape[1]
+    cos, sin, rot_dim, rot_rows = _rotary(rotary_cos, rotary_sin)
+    _maybe_at(out, "out", torch.bfloat16, (total_q, Hq, d))
+    _maybe_at(lse, "lse", torch.float32, (Hq, total_q))
+    index = _device(k_cache, v_cache, k_scale, v_scale, block_table, q, cu_seqlens_q, k_new, v_new,
+                    cache_seqlens, rotary_cos, rotary_sin, out, lse, workspace)
+    max_q = int(max_seqlen_q)
     total_k = (min(batch * max_pages * page_size, 2 ** 31 - 1) if max_total_k is None
                else int(max_total_k))
     scale = d ** -0.5 if softmax_scale is None else float(softmax_scale)
-    nbytes = int(lib.attn_fwd_kvcache_fp8_workspace_bytes(
-        batch, total_q, int(max_seqlen_q), total_k, Hq, Hkv, d, page_size, max_pages, rot_dim))
+    nbytes = lib.attn_fwd_kvcache_fp8_workspace_bytes(batch, total_q, max_q, total_k, Hq, Hkv, d,
+                                                      page_size, max_pages, rot_dim)
 
     def body(s):
         o = torch.empty_like(q) if out is None else out
         l = torch.empty((Hq, total_q), dtype=torch.float32, device=q.device) if lse is None else lse
         ws = _workspace(nbytes, q.device, workspace)
         rc = lib.attn_fwd_kvcache_fp8(
-            _ptr(q), _ptr(k_new), _ptr(v_new), _ptr(k_cache), _ptr(v_cache), _ptr(k_scale),
-            _ptr(v_scale), _ptr(cache_seqlens), _ptr(block_table), _ptr(cu_seqlens_q),
-            _ptr(rotary_cos), _ptr(rotary_sin), rot_dim, rot_rows, int(bool(rotary_interleaved)),
-            _ptr(o), _ptr(l), batch, total_q, int(max_seqlen_q), total_k, Hq, Hkv, d, page_size,
-            max_pages, num_pages, scale, int(bool(causal)), int(window_left), int(window_right),
-            _ptr(ws), nbytes, s)
+            qp, kn, vn, kc, vc, ks, vs, sl, bt, cu, cos, sin, rot_dim, rot_rows,
+            1 if rotary_interleaved else 0, o.data_ptr(), l.data_ptr(), batch, total_q, max_q,
+            total_k, Hq, Hkv, d, page_size, max_pages, num_pages, scale, 1 if causal else 0,
+            int(window_left), int(window_right), _ptr(ws), nbytes, s)
         if rc != 0:
             raise AttnError(rc, "attn_fwd_kvcache_fp8")
         return o, l
 
-    return _on(q.device, stream, body)
+    return _on(index, stream, body)

@@ -20,7 +20,6 @@ namespace {
 __device__ unsigned g_status_word;
 
 constexpr int kMaxDevices = 64;
-constexpr int kGb300Sms = 152;
 
 struct DeviceState {
     bool ready = false;
@@ -948,7 +947,7 @@ attn_status_t attn_kvcache_append_fp8(const void* k_new, const void* v_new, void
     attn_status_t st = kv8_sizes(batch, nheads_kv, head_dim, page_size, max_pages_per_seq, num_pages);
     if (st != ATTN_OK) return st;
     if (total_q < 0) return ATTN_ERR_INVALID_ARG;
-    if (static_cast<long long>(total_q) * nheads_kv > (1LL << 31) - 1) return ATTN_ERR_UNSUPPORTED;
+    if (static_cast<long long>(total_q) * nheads_kv > (1LL << 29)) return ATTN_ERR_UNSUPPORTED;
     st = rotary_ok(rotary_cos, rotary_sin, rotary_dim, rotary_rows, head_dim);
     if (st != ATTN_OK) return st;
     if (batch == 0 || total_q == 0) return ATTN_OK;
@@ -1127,7 +1126,7 @@ attn_status_t attn_fwd_kvcache_fp8(const void* q, const void* k_new, const void*
         return ATTN_ERR_INVALID_ARG;
     st = rotary_ok(rotary_cos, rotary_sin, rotary_dim, rotary_rows, head_dim);
     if (st != ATTN_OK) return st;
-    if (static_cast<long long>(total_q) * nheads_q > (1LL << 31) - 1) return ATTN_ERR_UNSUPPORTED;
+    if (static_cast<long long>(total_q) * nheads_q > (1LL << 29)) return ATTN_ERR_UNSUPPORTED;
     if (batch == 0 || total_q == 0) return ATTN_OK;
     if (!kv8_cache_ok(k_cache, v_cache, k_scale, v_scale, block_table) || !q || !k_new || !v_new ||
         !cache_seqlens || !cu_seqlens_q || !out || !lse || !aligned(q, 16) || !aligned(k_new, 16) ||

@@ -10,6 +10,8 @@
 
 namespace attn {
 
+constexpr int kGb300Sms = 152;
+
 // Bits of the per-device status word the kernels raise instead of trapping.
 constexpr unsigned kStatusTimeout = 1u;
 constexpr unsigned kStatusBounds = 2u;

@@ -11,8 +11,8 @@
 //
 // Keys are rotated first (kvcache.cu states the rotation), and the rotated value a cos - b sin
 // goes to e4m3 as if it were rounded once.  Kahan's fp32 form of it is within 1.5 units in the
-// last place (kvcache.cu); only where that lies within 2 units of a border between two codes (or
-// between two scales) is it not certain, about one element in 2^18.  The warp then forms the
+// last place (kvcache.cu).  Where the codes of that value less and plus 2^-21 of itself differ (or
+// the scales of the row's largest), about one element in 2^16, the warp forms the
 // value again as an unevaluated sum of two fp32 numbers (Dekker's and Knuth's error-free product
 // and sum), brought to one by rounding to odd, after which rounding to a shorter format gives
 // what rounding the exact value would (S. Boldo, G. Melquiond, "Emulation of FMA and correctly
@@ -35,21 +35,6 @@ __device__ __forceinline__ int find_seq(const int* cu, int batch, int t) {
     return lo;
 }
 
-__device__ __forceinline__ void unpack8(const uint4& w, float (&x)[8]) {
-    const uint32_t u[4] = {w.x, w.y, w.z, w.w};
-#pragma unroll
-    for (int i = 0; i < 4; ++i) {
-        x[2 * i] = __uint_as_float(u[i] << 16);
-        x[2 * i + 1] = __uint_as_float(u[i] & 0xFFFF0000u);
-    }
-}
-
-// a b - c d within 1.5 units in the last place (Kahan).
-__device__ __forceinline__ float det2(float a, float b, float c, float d) {
-    const float w = __fmul_rn(c, d);
-    return __fadd_rn(__fmaf_rn(a, b, -w), __fmaf_rn(-c, d, w));
-}
-
 // a b - c d as one fp32 number, rounded to odd.
 __device__ __forceinline__ float det2_odd(float a, float b, float c, float d) {
     const float ph = __fmul_rn(a, b), pl = __fmaf_rn(a, b, -ph);
@@ -66,201 +51,363 @@ __device__ __forceinline__ float det2_odd(float a, float b, float c, float d) {
     return __int_as_float((lo != 0.f && (u & 1) == 0) ? u + towards : u);
 }
 
-// The 8 rotated values of a lane; other: the partner plane's elements (rotate-half), c, s: the
-// lane's table entries (4 of each when interleaved).
-template <bool kOdd>
-__device__ __forceinline__ void rotate8(const uint4& own, const uint4& other, const float (&c)[8],
-                                        const float (&s)[8], bool interleaved, bool lower,
-                                        float (&y)[8]) {
-    float x[8], z[8];
-    unpack8(own, x);
-    unpack8(other, z);
-    const auto det = [](float a, float b, float e, float f) {
-        return kOdd ? det2_odd(a, b, e, f) : det2(a, b, e, f);
-    };
-    if (interleaved) {
+// 8 elements as four fp32 pairs.
+__device__ __forceinline__ void unpack_pairs(const uint4& w, uint64_t* x) {
+    const uint32_t u[4] = {w.x, w.y, w.z, w.w};
 #pragma unroll
-        for (int i = 0; i < 4; ++i) {
-            y[2 * i] = det(x[2 * i], c[i], x[2 * i + 1], s[i]);
-            y[2 * i + 1] = det(x[2 * i], s[i], -x[2 * i + 1], c[i]);
-        }
-    } else {
-#pragma unroll
-        for (int i = 0; i < 8; ++i)  // lower: x cos - z sin; upper (z the lower half): z sin + x cos
-            y[i] = det(x[i], c[i], lower ? z[i] : -z[i], s[i]);
-    }
+    for (int i = 0; i < 4; ++i)
+        x[i] = f2_make(__uint_as_float(u[i] << 16), __uint_as_float(u[i] & 0xFFFF0000u));
 }
 
-// The largest |y| of a row (of kLanes lanes), as bits: what is not finite compares above all else.
-template <int kLanes>
-__device__ __forceinline__ int row_top(const float (&y)[8]) {
-    int top = 0;
+// The rotation of 8 elements, in pairs: y = x c + z s, z the partner plane's elements, s signed
+// (c and s hold each table entry twice when interleaved).
+struct Turn {
+    uint64_t c[4], s[4];
+};
+
+// Kahan's form: w = z s rounded, e = z s - w exactly, y = (x c + w) + e.
+__device__ __forceinline__ uint64_t turn_pair(uint64_t c, uint64_t s, uint64_t x, uint64_t z) {
+    const uint64_t w = f2_mul(z, s);
+    const uint64_t e = f2_fma(z, s, f2_mul(w, f2_make(-1.f, -1.f)));
+    return f2_add(f2_fma(x, c, w), e);
+}
+
+// The same to one fp32 number each, rounded to odd.
+__device__ __forceinline__ uint64_t turn_pair_odd(uint64_t c, uint64_t s, uint64_t x, uint64_t z) {
+    float x0, x1, z0, z1, c0, c1, s0, s1;
+    f2_split(x, x0, x1);
+    f2_split(z, z0, z1);
+    f2_split(c, c0, c1);
+    f2_split(s, s0, s1);
+    return f2_make(det2_odd(x0, c0, z0, -s0), det2_odd(x1, c1, z1, -s1));
+}
+
+// The largest |y| of a lane's 16; NaNs do not count.
+__device__ __forceinline__ float lane_top(const uint64_t (&y)[8]) {
+    float top = 0.f;
 #pragma unroll
-    for (int i = 0; i < 8; ++i) top = max(top, __float_as_int(y[i]) & 0x7fffffff);
-#pragma unroll
-    for (int o = kLanes / 2; o > 0; o >>= 1) top = max(top, __shfl_xor_sync(0xffffffffu, top, o));
+    for (int i = 0; i < 8; ++i) {
+        float a, b;
+        f2_split(y[i], a, b);
+        top = fmax3(top, fabsf(a), fabsf(b));
+    }
     return top;
 }
 
-// 448 = 1.75 2^8: the exponent of the largest magnitude less 8, one more when its significand
-// is above 1.75.
-__device__ __forceinline__ int scale_byte(int top) {
-    return max(1, (top >> 23) - 8 + ((top & 0x7fffff) > 0x600000 ? 1 : 0));
+// The largest over the kLanes lanes of a row.
+template <int kLanes>
+__device__ __forceinline__ uint32_t row_max(uint32_t v) {
+#pragma unroll
+    for (int o = kLanes / 2; o > 0; o >>= 1) v = max(v, __shfl_xor_sync(0xffffffffu, v, o));
+    return v;
 }
 
-// Is the code of z (a value times 2^-e) uncertain when z may be off by two units in the last
-// place?  Normal codes change at values whose 20 low bits are 0x80000, subnormal ones (below
-// 2^-6) at odd multiples of 2^-10.
-__device__ __forceinline__ bool near_border(float z) {
-    const int u = __float_as_int(z) & 0x7fffffff;
-    const bool normal = ((u - (0x80000 - 2)) & 0xfffff) <= 4;
-    if (u >= 0x3c800000) return normal;  // 2^-6
-    const float f = fabsf(z) * 1024.f;
-    return fabsf(f - rintf(f)) < 0x1p-12f && f > 0.25f;
+// 448 = 1.75 2^8: the exponent of the largest magnitude (u: its bits) less 8, one more when its
+// significand is above 1.75.
+__device__ __forceinline__ int scale_byte(int u) {
+    return max(1, (u >> 23) - 8 + ((u & 0x7fffff) > 0x600000 ? 1 : 0));
 }
 
-__device__ __forceinline__ uint2 codes8(const float (&y)[8], float inv) {
-    return make_uint2(pack_e4m3x4(y[0] * inv, y[1] * inv, y[2] * inv, y[3] * inv),
-                      pack_e4m3x4(y[4] * inv, y[5] * inv, y[6] * inv, y[7] * inv));
+// The codes of y times f.
+__device__ __forceinline__ uint2 codes8(const uint64_t* y, float f) {
+    float z[8];
+#pragma unroll
+    for (int i = 0; i < 4; ++i) f2_split(f2_mul(y[i], f2_make(f, f)), z[2 * i], z[2 * i + 1]);
+    return make_uint2(pack_e4m3x4(z[0], z[1], z[2], z[3]), pack_e4m3x4(z[4], z[5], z[6], z[7]));
 }
 
-constexpr int kAppendRows = 4;  // rows (heads) of one token a group of lanes takes
+// The table entries of chunk c (8 elements) of a row at position pos; plane: the chunk that holds
+// its planes' first elements.
+__device__ __forceinline__ Turn turn_of(const AppendFp8Params& p, int pos, int c, int plane,
+                                        bool lower) {
+    Turn t;
+    const size_t row = static_cast<size_t>(pos) * (p.rot_dim / 2);
+    if (p.interleaved) {
+        const float4 cv = *reinterpret_cast<const float4*>(p.rot_cos + row + 4 * c);
+        const float4 sv = *reinterpret_cast<const float4*>(p.rot_sin + row + 4 * c);
+        const float cc[4] = {cv.x, cv.y, cv.z, cv.w}, ss[4] = {sv.x, sv.y, sv.z, sv.w};
+#pragma unroll
+        for (int i = 0; i < 4; ++i) {
+            t.c[i] = f2_make(cc[i], cc[i]);
+            t.s[i] = f2_make(-ss[i], ss[i]);
+        }
+        return t;
+    }
+    const float sign = lower ? -1.f : 1.f;
+#pragma unroll
+    for (int i = 0; i < 2; ++i) {
+        const float4 cv = *reinterpret_cast<const float4*>(p.rot_cos + row + 8 * plane + 4 * i);
+        const float4 sv = *reinterpret_cast<const float4*>(p.rot_sin + row + 8 * plane + 4 * i);
+        t.c[2 * i] = f2_make(cv.x, cv.y);
+        t.c[2 * i + 1] = f2_make(cv.z, cv.w);
+        t.s[2 * i] = f2_make(sign * sv.x, sign * sv.y);
+        t.s[2 * i + 1] = f2_make(sign * sv.z, sign * sv.w);
+    }
+    return t;
+}
+
+// A lane's elements of a staged row.
+__device__ __forceinline__ void read_row(uint64_t (&x)[8], const uint8_t* row, int l, int lanes) {
+#pragma unroll
+    for (int m = 0; m < 2; ++m)
+        unpack_pairs(*reinterpret_cast<const uint4*>(row + 16 * (l + m * lanes)), &x[4 * m]);
+}
+
+// How the keys turn: not at all, whole heads in halves, or otherwise.
+constexpr int kNoTurn = 0, kWholeTurn = 1, kAnyTurn = 2;
+
+// x rotated; the partners are the lane's other run, or chunks `from` of the staged row.
+template <int kTurn, bool kOdd>
+__device__ __forceinline__ void turn_row(uint64_t (&x)[8], const uint8_t* row,
+                                         const Turn (&turn)[2], const bool (&turns)[2],
+                                         const int (&from)[2], bool interleaved) {
+    uint64_t z[8];
+#pragma unroll
+    for (int m = 0; m < 2; ++m) {
+        if (kTurn == kWholeTurn) {
+#pragma unroll
+            for (int j = 0; j < 4; ++j) z[4 * m + j] = x[4 * (1 - m) + j];
+        } else {
+            uint4 w = *reinterpret_cast<const uint4*>(row + 16 * from[m]);
+            if (interleaved)  // the other one of each pair
+                w = make_uint4(__byte_perm(w.x, 0, 0x1032), __byte_perm(w.y, 0, 0x1032),
+                               __byte_perm(w.z, 0, 0x1032), __byte_perm(w.w, 0, 0x1032));
+            unpack_pairs(w, &z[4 * m]);
+        }
+    }
+#pragma unroll
+    for (int j = 0; j < 8; ++j) {
+        const uint64_t c = turn[j / 4].c[j % 4], s = turn[j / 4].s[j % 4];
+        if (kTurn == kWholeTurn || turns[j / 4])
+            x[j] = kOdd ? turn_pair_odd(c, s, x[j], z[j]) : turn_pair(c, s, x[j], z[j]);
+    }
+}
+
+constexpr int kAppendRows = 2;  // rows (heads) of one token a group of lanes takes at a time
+constexpr int kAppendThreads = 128;
+constexpr int kAppendTokens = 16;  // tokens a block takes at most
+constexpr int kAppendStages = 3;
+constexpr float kFltMax = 3.402823466e38f;
+
+struct AppendToken {
+    long long row;    // of the cache [num_pages * page_size], -1: none
+    long long scale;  // of k_scale / v_scale for kv head 0
+    int pos;
+};
+
+__device__ __forceinline__ AppendToken append_token(const AppendFp8Params& p, int t) {
+    AppendToken a{-1, 0, 0};
+    if (t >= p.total_q) return a;
+    const int b = find_seq(p.cu_q, p.batch, t);
+    const int q0 = p.cu_q[b], q1 = p.cu_q[b + 1], ctx = p.cache_seqlens[b];
+    if (t < q0 || t >= q1) return a;  // tokens outside every sequence are left alone
+    const long long pos = static_cast<long long>(ctx) + (t - q0);
+    if (ctx >= 0 && pos < static_cast<long long>(p.max_pages) * p.page_size &&
+        (p.rot_dim == 0 || pos < p.rot_rows)) {
+        const int i = static_cast<int>(pos) / p.page_size;
+        const int slot = static_cast<int>(pos) - i * p.page_size;
+        const int page = p.block_table[static_cast<size_t>(b) * p.max_pages + i];
+        if (page >= 0 && page < p.num_pages)
+            return AppendToken{static_cast<long long>(page) * p.page_size + slot,
+                               static_cast<long long>(page) * p.Hkv * p.page_size + slot,
+                               static_cast<int>(pos)};
+    }
+    atomicOr(p.status, kStatusBounds);
+    return a;
+}
 
 // Rotated queries go to the attention kernel as f16 times a power of two a row: 11 significant
 // bits of the rotated value, where bf16's 8 would put up to 2^-9 of a logit's terms on it.
 //
-// A group of D / 8 lanes, 8 elements a lane, takes up to four rows (heads) of one token: their
-// loads go out together and before the token's place is known, the rotary tables are read
-// once for the four, and single tokens still spread over many groups.  Keys come first, then
-// values, then queries, so that a warp's rows are of one kind.
-template <int D>
-__global__ void __launch_bounds__(256) kvcache_append_fp8_kernel(const AppendFp8Params p) {
-    constexpr int kLanes = D / 8;
-    griddep_launch_dependents();  // an attention kernel behind this one may set up
-    const int lane = threadIdx.x & 31;
-    const int e0 = (lane % kLanes) * 8;
-    const int kv_blocks = (p.Hkv + kAppendRows - 1) / kAppendRows;
-    const int q_blocks = p.q_rot != nullptr ? (p.Hq + kAppendRows - 1) / kAppendRows : 0;
-    const long long kv_items = static_cast<long long>(p.total_q) * kv_blocks;
-    const long long items = 2 * kv_items + static_cast<long long>(p.total_q) * q_blocks;
-    const long long item = (static_cast<long long>(blockIdx.x) * blockDim.x + threadIdx.x) / kLanes;
-    bool live = item < items;
-    const int kind = !live ? 1 : item < kv_items ? 0 : item < 2 * kv_items ? 1 : 2;  // K, V, Q
-    const long long at = live ? item - (kind == 0 ? 0 : kind == 1 ? kv_items : 2 * kv_items) : 0;
-    const int blocks = kind == 2 ? q_blocks : kv_blocks, H = kind == 2 ? p.Hq : p.Hkv;
-    const int t = static_cast<int>(at / blocks);
-    const int h0 = static_cast<int>(at - static_cast<long long>(t) * blocks) * kAppendRows;
-    const int n = min(kAppendRows, H - h0);
-    const __nv_bfloat16* src = (kind == 0 ? p.k_new : kind == 1 ? p.v_new : p.q) +
-                               (static_cast<size_t>(t) * H + h0) * D + e0;
-    uint4 own[kAppendRows];
-#pragma unroll
-    for (int i = 0; i < kAppendRows; ++i)
-        own[i] = live && i < n ? *reinterpret_cast<const uint4*>(src + i * D) : make_uint4(0, 0, 0, 0);
+// Bound by memory, and by its latency: a block takes a run of tokens, whose places (sequence,
+// position, page) its first threads find once, and each group of D / 16 lanes walks its share of
+// the tokens' rows, two (heads) at a time, with the loads of the next two steps under way into
+// shared memory.  A lane holds elements [8 l, 8 l + 8) and [D / 2 + 8 l, ...) of a row, which are
+// each other's partners when the whole head is rotated in halves.  The scale byte is monotone in
+// the magnitude, so each lane forms its own and a row's is their maximum.
+//
+// kKind: keys, values or queries (blockIdx.y): one instruction stream each, since the selects
+// that rows of several kinds in one warp cost were a third of all instructions.  kTurn: no
+// rotation, the whole head in halves (a lane then has both partners and one set of table
+// entries), or any other.
+constexpr int kKeys = 0, kValues = 1, kQueries = 2;
 
-    // the token's place
-    const int b = find_seq(p.cu_q, p.batch, t);
-    const int q0 = p.cu_q[b], q1 = p.cu_q[b + 1], ctx = p.cache_seqlens[b];
-    live = live && t >= q0 && t < q1;  // tokens outside every sequence are left alone
-    const long long pos = static_cast<long long>(ctx) + (t - q0);
-    if (live && (ctx < 0 || pos >= static_cast<long long>(p.max_pages) * p.page_size ||
-                 (p.rot_dim > 0 && pos >= p.rot_rows))) {
-        atomicOr(p.status, kStatusBounds);
-        live = false;
-    }
-    int page = 0, slot = 0;
-    if (live && kind != 2) {
-        const int i = static_cast<int>(pos) / p.page_size;
-        slot = static_cast<int>(pos) - i * p.page_size;
-        page = p.block_table[static_cast<size_t>(b) * p.max_pages + i];
-        if (page < 0 || page >= p.num_pages) {
-            atomicOr(p.status, kStatusBounds);
-            live = false;
-        }
-    }
+template <int D, int kTurn, int kKind>
+__device__ __forceinline__ void append_rows(const AppendFp8Params& p, int tokens,
+                                            uint8_t (&stage)[kAppendStages][kAppendThreads * 16 / D]
+                                                            [kAppendRows][D * 2],
+                                            AppendToken (&place_of)[kAppendTokens]) {
+    constexpr int kLanes = D / 16, kGroups = kAppendThreads / kLanes;
+    constexpr bool kRotated = kTurn != kNoTurn && kKind != kValues;
+    const int lane = threadIdx.x & 31, l = lane % kLanes, group = threadIdx.x / kLanes;
+    const int t0 = blockIdx.x * tokens;
+    const int H = kKind == kQueries ? p.Hq : p.Hkv;
+    const __nv_bfloat16* const in = kKind == kKeys ? p.k_new : kKind == kValues ? p.v_new : p.q;
+    const int blocks = (H + kAppendRows - 1) / kAppendRows, items = tokens * blocks;
+    const float inv_blocks = 1.f / blocks;
 
-    const int half = p.rot_dim / 2;
-    const bool lower = e0 < half;
-    const bool turns = live && kind != 1 && e0 < p.rot_dim;
-    float c[8], s[8];
-    if (turns) {
-        const size_t row = static_cast<size_t>(pos) * half;
-        const int plane = p.interleaved ? e0 / 2 : lower ? e0 : e0 - half;
-        const float4* cr = reinterpret_cast<const float4*>(p.rot_cos + row + plane);
-        const float4* sr = reinterpret_cast<const float4*>(p.rot_sin + row + plane);
+    // Item: (token, first head).  The quotient is taken in fp32: (x + 1/2) / n is at least
+    // 1 / (2 n) away from an integer, far beyond the error.
+    struct Item {
+        int tok, h0, n;  // n: rows, 0 for items past the end
+    };
+    const auto item_of = [&](int item) {
+        Item it;
+        it.tok = static_cast<int>((item + 0.5f) * inv_blocks);
+        it.h0 = (item - it.tok * blocks) * kAppendRows;
+        it.n = item < items && t0 + it.tok < p.total_q ? min(kAppendRows, H - it.h0) : 0;
+        return it;
+    };
+    const auto fetch = [&](int step) {
+        const Item it = item_of(group + step * kGroups);
+        const __nv_bfloat16* src = in + (static_cast<size_t>(t0 + it.tok) * H + it.h0) * D + 8 * l;
 #pragma unroll
-        for (int i = 0; i < 2; ++i) {
-            if (i == 1 && p.interleaved) break;
-            const float4 cv = cr[i], sv = sr[i];
-            c[4 * i] = cv.x, c[4 * i + 1] = cv.y, c[4 * i + 2] = cv.z, c[4 * i + 3] = cv.w;
-            s[4 * i] = sv.x, s[4 * i + 1] = sv.y, s[4 * i + 2] = sv.z, s[4 * i + 3] = sv.w;
-        }
-    }
-    const bool any_turns = __any_sync(0xffffffffu, turns);
+        for (int i = 0; i < kAppendRows; ++i)
+            if (i < it.n) {
+                uint8_t* dst = stage[step % kAppendStages][group][i] + 16 * l;
+                cp_async16(dst, src + i * D);
+                cp_async16(dst + D, src + i * D + D / 2);
+            }
+        cp_async_commit();
+    };
+    const int h = p.rot_dim / 16;  // a chunk's partner is h chunks further on, or before
+    // (a warp's groups take the same number of steps)
+    const int steps = (items - threadIdx.x / 32 * (32 / kLanes) + kGroups - 1) / kGroups;
 #pragma unroll
-    for (int i = 0; i < kAppendRows; ++i) {
-        if (__all_sync(0xffffffffu, i >= n)) break;
-        float y[8];
-        unpack8(own[i], y);
-        uint4 other = make_uint4(0, 0, 0, 0);
-        if (any_turns) {
-            // the partner planes of rotate-half live half / 8 lanes further on, or before
-            const int from = (lower ? lane + half / 8 : lane - half / 8) & 31;
-            other.x = __shfl_sync(0xffffffffu, own[i].x, from);
-            other.y = __shfl_sync(0xffffffffu, own[i].y, from);
-            other.z = __shfl_sync(0xffffffffu, own[i].z, from);
-            other.w = __shfl_sync(0xffffffffu, own[i].w, from);
-            if (turns) rotate8<false>(own[i], other, c, s, p.interleaved, lower, y);
-        }
-        int top = row_top<kLanes>(y);
-        const bool mine = live && i < n;
-        if (kind == 2) {
-            // the row's largest element to [2^13, 2^14) as f16 (kv8_query_shift)
-            const int a = kv8_query_shift(top >> 23);
-            const float up = __int_as_float((a + 127) << 23);
-            if (mine) {
-                const size_t row = static_cast<size_t>(t) * p.Hq + h0 + i;
-                *reinterpret_cast<uint4*>(p.q_rot + row * D + e0) =
-                    make_uint4(pack_f16x2(y[0] * up, y[1] * up), pack_f16x2(y[2] * up, y[3] * up),
-                               pack_f16x2(y[4] * up, y[5] * up), pack_f16x2(y[6] * up, y[7] * up));
-                if (e0 == 0) p.q_unit[row] = __int_as_float((127 - a) << 23);
+    for (int s = 0; s < kAppendStages - 1; ++s) fetch(s);
+    if (threadIdx.x < tokens) place_of[threadIdx.x] = append_token(p, t0 + threadIdx.x);
+    __syncthreads();
+
+    for (int step = 0; step < steps; ++step) {
+        const Item it = item_of(group + step * kGroups);
+        AppendToken place{-1, 0, 0};
+        if (it.n > 0) place = place_of[it.tok];
+        const int n = place.row >= 0 ? it.n : 0;
+        // The lane's two runs of 8 elements (chunks of the row): do they turn, where is their
+        // partner, and the rotary tables' entries for them.
+        bool turns[2] = {kRotated, kRotated};
+        int from[2] = {l, l + kLanes};
+        Turn turn[2];
+        if (kRotated && kTurn == kWholeTurn && n > 0) {
+            turn[0] = turn_of(p, place.pos, l, l, true);
+#pragma unroll
+            for (int j = 0; j < 4; ++j) {
+                turn[1].c[j] = turn[0].c[j];
+                turn[1].s[j] = f2_mul(turn[0].s[j], f2_make(-1.f, -1.f));
             }
         }
-        int sb = scale_byte(top);
-        float inv = __int_as_float((254 - min(sb, 253)) << 23);  // 2^-e
-        // What is certain of the above?  Not a row with an element that is not finite, nor, of
-        // a rotated row, codes and scales near a border.
-        bool redo = top >= 0x7f800000;
-        if (turns && kind == 0) {
-            redo = redo || static_cast<unsigned>((top & 0x7fffff) - (0x600000 - 2)) <= 4u;
+        if (kRotated && kTurn == kAnyTurn) {
 #pragma unroll
-            for (int j = 0; j < 8; ++j) redo = redo || near_border(y[j] * inv);
+            for (int m = 0; m < 2; ++m) {
+                const int c = l + m * kLanes;
+                const bool lower = c < h;
+                turns[m] = 8 * c < p.rot_dim;
+                if (turns[m] && !p.interleaved) from[m] = lower ? c + h : c - h;
+                if (turns[m] && n > 0) turn[m] = turn_of(p, place.pos, c, lower ? c : c - h, lower);
+            }
         }
-        if (__any_sync(0xffffffffu, redo && kind != 2)) {
-            if (turns) rotate8<true>(own[i], other, c, s, p.interleaved, lower, y);
+        const int most = __reduce_max_sync(0xffffffffu, n);
+        cp_async_wait<kAppendStages - 2>();
+        __syncwarp();
+#pragma unroll 1
+        for (int i = 0; i < most; ++i) {
+            const bool mine = i < n;  // (other rows' stages hold anything)
+            const uint8_t* const row = stage[step % kAppendStages][group][i];
+            uint64_t y[8];
+            read_row(y, row, l, kLanes);
+            if (kRotated) turn_row<kTurn, false>(y, row, turn, turns, from, p.interleaved);
+            const int u = __float_as_int(lane_top(y));
+            if (kKind == kQueries) {
+                // the row's largest element to [2^13, 2^14) as f16 (kv8_query_shift)
+                const int up = kv8_query_shift(row_max<kLanes>(u >> 23));
+                const float f = __int_as_float((up + 127) << 23);
+                if (!mine) continue;
+                const size_t at = static_cast<size_t>(t0 + it.tok) * p.Hq + it.h0 + i;
 #pragma unroll
-            for (int j = 0; j < 8; ++j)
-                if ((__float_as_int(y[j]) & 0x7fffffff) >= 0x7f800000) y[j] = 0.f;
-            top = row_top<kLanes>(y);  // (of the finite elements)
-            if (turns)
-                rotate8<true>(own[i], other, c, s, p.interleaved, lower, y);
-            else
-                unpack8(own[i], y);
-            sb = scale_byte(top);
-            inv = __int_as_float((254 - sb) << 23);
+                for (int m = 0; m < 2; ++m) {
+                    uint32_t out[4];
 #pragma unroll
-            for (int j = 0; j < 8; ++j)  // the NaN code, where infinity would saturate
-                if ((__float_as_int(y[j]) & 0x7fffffff) >= 0x7f800000) y[j] = __int_as_float(0x7fffffff);
+                    for (int j = 0; j < 4; ++j) {
+                        float f0, f1;
+                        f2_split(f2_mul(y[4 * m + j], f2_make(f, f)), f0, f1);
+                        out[j] = pack_f16x2(f0, f1);
+                    }
+                    *reinterpret_cast<uint4*>(p.q_rot + at * D + m * (D / 2) + 8 * l) =
+                        make_uint4(out[0], out[1], out[2], out[3]);
+                }
+                if (l == 0) p.q_unit[at] = __int_as_float((127 - up) << 23);
+                continue;
+            }
+            // Not certain: a row with an element that is not finite (0 times it is NaN); a rotated
+            // one whose scale (it changes where the largest's significand passes 1.75) or,
+            // below, whose codes change within the rotation's error.
+            uint64_t zero = 0;
+#pragma unroll
+            for (int j = 0; j < 8; ++j) zero = f2_fma(y[j], 0, zero);
+            float z0, z1;
+            f2_split(zero, z0, z1);
+            bool redo = z0 + z1 != 0.f || (kRotated && ((u - (0x600000 - 8)) & 0x7fffff) <= 16);
+            uint32_t sb = row_max<kLanes>(scale_byte(u));
+            const float inv = __int_as_float((254 - min(sb, 253u)) << 23);  // 2^-e
+            uint2 codes[2];
+#pragma unroll
+            for (int m = 0; m < 2; ++m) {
+                codes[m] = codes8(&y[4 * m], turns[m] ? inv * (1.f - 0x1p-21f) : inv);
+                if (kRotated) {
+                    const uint2 above = codes8(&y[4 * m], turns[m] ? inv * (1.f + 0x1p-21f) : inv);
+                    redo = redo || codes[m].x != above.x || codes[m].y != above.y;
+                }
+            }
+            if (__any_sync(0xffffffffu, redo)) {
+                read_row(y, row, l, kLanes);
+                if (kRotated) turn_row<kTurn, true>(y, row, turn, turns, from, p.interleaved);
+                float top = 0.f;
+#pragma unroll
+                for (int j = 0; j < 8; ++j) {
+                    float f[2];
+                    f2_split(y[j], f[0], f[1]);
+#pragma unroll
+                    for (int k = 0; k < 2; ++k) {
+                        if (fabsf(f[k]) <= kFltMax)
+                            top = fmaxf(top, fabsf(f[k]));
+                        else
+                            f[k] = __int_as_float(0x7fffffff);  // the NaN code; infinity would saturate
+                    }
+                    y[j] = f2_make(f[0], f[1]);
+                }
+                sb = row_max<kLanes>(scale_byte(__float_as_int(top)));
+#pragma unroll
+                for (int m = 0; m < 2; ++m) codes[m] = codes8(&y[4 * m], __int_as_float((254 - sb) << 23));
+            }
+            if (mine) {
+                uint8_t* const dst = (kKind == kValues ? p.v_cache : p.k_cache) +
+                                     (place.row * p.Hkv + it.h0 + i) * D + 8 * l;
+                *reinterpret_cast<uint2*>(dst) = codes[0];
+                *reinterpret_cast<uint2*>(dst + D / 2) = codes[1];
+                if (l == 0)
+                    (kKind == kValues ? p.v_scale : p.k_scale)
+                        [place.scale + static_cast<long long>(it.h0 + i) * p.page_size] =
+                            static_cast<uint8_t>(sb);
+            }
         }
-        if (mine && kind != 2) {
-            const size_t row = (static_cast<size_t>(page) * p.page_size + slot) * p.Hkv + h0 + i;
-            *reinterpret_cast<uint2*>((kind == 1 ? p.v_cache : p.k_cache) + row * D + e0) = codes8(y, inv);
-            if (e0 == 0)
-                (kind == 1 ? p.v_scale : p.k_scale)[
-                    (static_cast<size_t>(page) * p.Hkv + h0 + i) * p.page_size + slot] =
-                    static_cast<uint8_t>(sb);
-        }
+        __syncwarp();  // the stage's rows have been read (by partners too)
+        fetch(step + kAppendStages - 1);
     }
+    cp_async_wait<0>();
+}
+
+template <int D, int kTurn>
+__global__ void __launch_bounds__(kAppendThreads, 5)
+    kvcache_append_fp8_kernel(const AppendFp8Params p, int tokens) {
+    __shared__ __align__(16) uint8_t stage[kAppendStages][kAppendThreads * 16 / D][kAppendRows][D * 2];
+    __shared__ AppendToken place_of[kAppendTokens];
+    griddep_launch_dependents();  // an attention kernel behind this one may set up
+    if (blockIdx.y == kKeys)
+        append_rows<D, kTurn, kKeys>(p, tokens, stage, place_of);
+    else if (blockIdx.y == kValues)
+        append_rows<D, kTurn, kValues>(p, tokens, stage, place_of);
+    else
+        append_rows<D, kTurn, kQueries>(p, tokens, stage, place_of);
 }
 
 // ---- staging for the tensor-core prefill ----------------------------------------------------
@@ -513,15 +660,29 @@ cudaError_t launch_read(const Params& p, void* k, void* v, int rows, int head_di
 }  // namespace
 
 cudaError_t launch_kvcache_append_fp8(const AppendFp8Params& p, int head_dim, cudaStream_t stream) {
-    const long long blocks = (p.Hkv + kAppendRows - 1) / kAppendRows * 2 +
-                             (p.q_rot != nullptr ? (p.Hq + kAppendRows - 1) / kAppendRows : 0);
-    const long long threads = p.total_q * blocks * (head_dim / 8);
-    if (threads == 0) return cudaSuccess;
-    const unsigned grid = static_cast<unsigned>((threads + 255) / 256);
-    if (head_dim == 128)
-        kvcache_append_fp8_kernel<128><<<grid, 256, 0, stream>>>(p);
-    else
-        kvcache_append_fp8_kernel<64><<<grid, 256, 0, stream>>>(p);
+    if (p.total_q == 0) return cudaSuccess;
+    // Single tokens spread over the GPU, about one step a group of lanes; prompts take up to 16
+    // tokens a block.
+    const int blocks = (p.Hkv + kAppendRows - 1) / kAppendRows;
+    const int groups = kAppendThreads / (head_dim / 16);
+    int tokens = 1;
+    while (tokens < kAppendTokens &&
+           (2 * tokens * blocks <= groups || p.total_q / (2 * tokens) >= 4 * kGb300Sms))
+        tokens *= 2;
+    const dim3 grid(static_cast<unsigned>((p.total_q + tokens - 1) / tokens), p.q_rot != nullptr ? 3 : 2);
+    const int turn = p.rot_dim == 0 ? kNoTurn
+                     : p.rot_dim == head_dim && !p.interleaved ? kWholeTurn
+                                                               : kAnyTurn;
+    const auto launch = [&](auto kernel) { kernel<<<grid, kAppendThreads, 0, stream>>>(p, tokens); };
+    if (head_dim == 128) {
+        if (turn == kNoTurn) launch(kvcache_append_fp8_kernel<128, kNoTurn>);
+        if (turn == kWholeTurn) launch(kvcache_append_fp8_kernel<128, kWholeTurn>);
+        if (turn == kAnyTurn) launch(kvcache_append_fp8_kernel<128, kAnyTurn>);
+    } else {
+        if (turn == kNoTurn) launch(kvcache_append_fp8_kernel<64, kNoTurn>);
+        if (turn == kWholeTurn) launch(kvcache_append_fp8_kernel<64, kWholeTurn>);
+        if (turn == kAnyTurn) launch(kvcache_append_fp8_kernel<64, kAnyTurn>);
+    }
     return cudaGetLastError();
 }
 
