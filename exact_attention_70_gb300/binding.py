@@ -36,6 +36,8 @@ def lib_path() -> str:
 def load():
     """Load libattn.so (built by ``__graft_entry__.build()`` / ``exact_attention_70_gb300.build``)."""
     global _lib
+    if _lib is not None:
+        return _lib
     with _lock:
         if _lib is None:
             path = _build.LIB
@@ -547,7 +549,8 @@ def _kv8_sizes(k_cache, v_cache, k_scale, v_scale, block_table, batch):
     num_pages, page_size, Hkv, d = shape
     if v_cache.shape != shape:
         raise ValueError("k_cache and v_cache must both be [num_pages, page_size, Hkv, d]")
-    if k_scale.shape != (num_pages, Hkv, page_size) or v_scale.shape != k_scale.shape:
+    shape = k_scale.shape
+    if shape != (num_pages, Hkv, page_size) or v_scale.shape != shape:
         raise ValueError("k_scale and v_scale must both be [num_pages, Hkv, page_size]")
     rows, max_pages = block_table.shape
     if rows != batch:
@@ -561,8 +564,9 @@ def _rotary(rotary_cos, rotary_sin):
         return None, None, 0, 0
     cos = _at(rotary_cos, "rotary_cos", torch.float32, 2)
     sin = _at(rotary_sin, "rotary_sin", torch.float32, 2)
-    rows, half = rotary_cos.shape
-    if rotary_sin.shape != rotary_cos.shape:
+    shape = rotary_cos.shape
+    rows, half = shape
+    if rotary_sin.shape != shape:
         raise ValueError("rotary_cos and rotary_sin must both be [rows, rotary_dim / 2]")
     return cos, sin, 2 * half, rows
 
@@ -571,8 +575,9 @@ def _new_tokens(k_new, v_new, cache_seqlens, batch, Hkv, d):
     """The addresses of the new keys and values and of cache_seqlens, and the tokens."""
     at = (_at(k_new, "k_new", torch.bfloat16, 3), _at(v_new, "v_new", torch.bfloat16, 3),
           _at(cache_seqlens, "cache_seqlens", torch.int32, 1))
-    total_q = k_new.shape[0]
-    if k_new.shape != (total_q, Hkv, d) or v_new.shape != k_new.shape:
+    shape = k_new.shape
+    total_q = shape[0]
+    if shape[1:] != (Hkv, d) or v_new.shape != shape:
         raise ValueError("k_new and v_new must both be [total_q, Hkv, d] with the cache's Hkv and d")
     if cache_seqlens.numel() != batch:
         raise ValueError("cache_seqlens must have one entry per sequence")

@@ -490,9 +490,9 @@ __global__ void __launch_bounds__(kUnitsThreads)
 
 // ---- reading the cache: packed bf16 rows, or the staged f16 ones ---------------------------
 //
-// Bound by memory: a byte in and two out per element.  A block takes a run of tokens; its first
-// threads find the tokens' places (sequence, page), then every thread moves 16 codes at a time,
-// four loads in flight.
+// Bound by memory: a byte in and two out per element.  A block takes a run of tokens' keys or
+// values (blockIdx.y); its first threads find the tokens' places (sequence, page), then every
+// thread moves 16 codes at a time, four loads in flight.
 
 constexpr int kReadTokens = 128;  // tokens a block takes at most
 
@@ -601,37 +601,41 @@ __global__ void __launch_bounds__(256)
         seq_of[threadIdx.x] = b;
     }
     __syncthreads();
-    const int per_kind = tokens * p.Hkv * kLanes, items = 2 * per_kind;
+    const bool is_v = blockIdx.y != 0;
+    const uint8_t* const cache = is_v ? p.v_cache : p.k_cache;
+    const uint8_t* const scales = is_v ? p.v_scale : p.k_scale;
+    uint16_t* const to = (is_v ? v_out : k_out) + static_cast<size_t>(t0) * p.Hkv * D;
+    const int items = tokens * p.Hkv * kLanes;
+    // (the quotient in fp32: (x + 1/2) / n is at least 1 / (2 n) away from an integer; x is
+    // below 2^22)
+    const float inv = 1.f / p.Hkv;
     for (int i0 = threadIdx.x; i0 < items; i0 += 256 * kUnroll) {
         uint4 w[kUnroll];
-        int sb[kUnroll], tok[kUnroll], kvh[kUnroll];
+        int sb[kUnroll], at[kUnroll];  // at: token * Hkv + kv head
         long long row[kUnroll];
 #pragma unroll
         for (int u = 0; u < kUnroll; ++u) {
             const int i = i0 + 256 * u;
             row[u] = -1;
             if (i >= items) continue;
-            const bool is_v = i >= per_kind;
-            const int j = (is_v ? i - per_kind : i) / kLanes;
-            tok[u] = j / p.Hkv;
-            kvh[u] = j - tok[u] * p.Hkv;
-            const ReadToken r = place_of[tok[u]];
+            at[u] = i / kLanes;
+            const int tok = static_cast<int>((at[u] + 0.5f) * inv), kvh = at[u] - tok * p.Hkv;
+            const ReadToken r = place_of[tok];
             row[u] = r.row;
             if (r.row < 0) continue;
-            w[u] = *reinterpret_cast<const uint4*>((is_v ? p.v_cache : p.k_cache) +
-                                                   (r.row * p.Hkv + kvh[u]) * D + i % kLanes * 16);
-            sb[u] = (is_v ? p.v_scale : p.k_scale)[r.scale + static_cast<long long>(kvh[u]) * p.page_size];
+            w[u] = *reinterpret_cast<const uint4*>(cache + (r.row * p.Hkv + kvh) * D + i % kLanes * 16);
+            sb[u] = scales[r.scale + static_cast<long long>(kvh) * p.page_size];
         }
 #pragma unroll
         for (int u = 0; u < kUnroll; ++u) {
-            const int i = i0 + 256 * u;
             if (row[u] == -1) continue;
-            const bool is_v = i >= per_kind;
             uint32_t out[8] = {0, 0, 0, 0, 0, 0, 0, 0};
-            if (row[u] >= 0) convert16(p, w[u], sb[u], seq_of[tok[u]] * p.Hkv + kvh[u], is_v, out);
-            uint4* dst = reinterpret_cast<uint4*>(
-                (is_v ? v_out : k_out) +
-                (static_cast<size_t>(t0 + tok[u]) * p.Hkv + kvh[u]) * D + i % kLanes * 16);
+            if (row[u] >= 0) {
+                const int tok = static_cast<int>((at[u] + 0.5f) * inv);
+                convert16(p, w[u], sb[u], seq_of[tok] * p.Hkv + at[u] - tok * p.Hkv, is_v, out);
+            }
+            uint4* dst = reinterpret_cast<uint4*>(to + static_cast<size_t>(at[u]) * D +
+                                                  (i0 + 256 * u) % kLanes * 16);
             dst[0] = make_uint4(out[0], out[1], out[2], out[3]);
             dst[1] = make_uint4(out[4], out[5], out[6], out[7]);
         }
@@ -641,14 +645,14 @@ __global__ void __launch_bounds__(256)
 // About 2048 moves of 16 codes a block.
 int read_tokens(int Hkv, int head_dim) {
     int n = kReadTokens;
-    while (n > 8 && n * 2 * Hkv * (head_dim / 16) > 2048) n /= 2;
+    while (n > 8 && n * Hkv * (head_dim / 16) > 2048) n /= 2;
     return n;
 }
 
 template <typename Params>
 cudaError_t launch_read(const Params& p, void* k, void* v, int rows, int head_dim, cudaStream_t stream) {
     const int tokens = read_tokens(p.Hkv, head_dim);
-    const int grid = (rows + tokens - 1) / tokens;
+    const dim3 grid((rows + tokens - 1) / tokens, 2);
     uint16_t *ko = static_cast<uint16_t*>(k), *vo = static_cast<uint16_t*>(v);
     if (head_dim == 128)
         kvcache_read_fp8_kernel<128><<<grid, 256, 0, stream>>>(p, ko, vo, rows, tokens);
