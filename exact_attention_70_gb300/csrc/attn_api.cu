@@ -249,6 +249,7 @@ attn_status_t fwd_impl(const void* q, const void* k, const void* v, void* out, f
     pp.max_seqlen_k = max_seqlen_k;
     pp.Hkv = nheads_kv;
     pp.tpt = tpt;
+    pp.tiles = kFwdTilesPerItem;
     pp.capacity_pairs = static_cast<int>(fwd_capacity_pairs(batch, max_seqlen_q, g));
     pp.causal = causal ? 1 : 0;
     pp.wl = window_left;
@@ -552,6 +553,7 @@ attn_status_t attn_fwd_kvcache(const void* q, const void* k_new, const void* v_n
     pp.max_seqlen_q = max_seqlen_q;
     pp.Hkv = nheads_kv;
     pp.tpt = tpt;
+    pp.tiles = kFwdTilesPerItem;
     pp.capacity_pairs = static_cast<int>(fwd_capacity_pairs(batch, max_seqlen_q, g));
     pp.causal = causal ? 1 : 0;
     pp.wl = window_left;
@@ -869,9 +871,9 @@ size_t kv8_partial_bytes(int grid, int head_dim) {
            align_up(grid * sizeof(int4), 256);
 }
 
-// The rotated queries (f16) and their units.
-size_t kv8_query_bytes(long long rows, int head_dim) {
-    return align_up(static_cast<size_t>(rows) * head_dim * 2, 256) +
+// The queries in f16 (rotated: in two parts) and their units.
+size_t kv8_query_bytes(long long rows, int head_dim, int rotary_dim) {
+    return align_up(static_cast<size_t>(rows) * head_dim * 2, 256) * (rotary_dim > 0 ? 2 : 1) +
            align_up(static_cast<size_t>(rows) * sizeof(float), 256);
 }
 
@@ -890,14 +892,18 @@ bool kv8_staged(int batch, int max_seqlen_q, int nheads_q, int nheads_kv) {
     return rows > 112 && rows * pairs > 6144;
 }
 
+// Q tiles of a work item of the staged path: one where the queries are in two parts.
+int kv8_tiles(int rotary_dim) { return rotary_dim > 0 ? 1 : kFwdTilesPerItem; }
+
 // The staged path's workspace behind the queries.
 struct Kv8StageLayout {
-    long long rows;  // of k and v
+    long long rows;   // of k and v
+    long long items;  // of the work list, per kv head
     size_t k, v, spans, k_unit, v_unit, list, total;
 };
 
 Kv8StageLayout kv8_stage_layout(int batch, int max_seqlen_q, int max_total_k, int nheads_q,
-                                int nheads_kv, int head_dim) {
+                                int nheads_kv, int head_dim, int tiles) {
     Kv8StageLayout l;
     l.rows = static_cast<long long>(max_total_k) + static_cast<long long>(kFwdBlockN) * batch;
     const size_t bytes = align_up(static_cast<size_t>(l.rows) * nheads_kv * head_dim * 2, 256);
@@ -908,7 +914,10 @@ Kv8StageLayout kv8_stage_layout(int batch, int max_seqlen_q, int max_total_k, in
     l.k_unit = l.spans + align_up(static_cast<size_t>(batch) * sizeof(int2), 256);
     l.v_unit = l.k_unit + units;
     l.list = l.v_unit + units;
-    l.total = l.list + attn_fwd_workspace_bytes(batch, max_seqlen_q, nheads_q, nheads_kv);
+    const long long per = static_cast<long long>(tiles) * tokens_per_tile(nheads_q / nheads_kv);
+    l.items = batch * ((max_seqlen_q + per - 1) / per);
+    l.total = l.list + sizeof(FwdWorkspaceHeader) + align_up(sizeof(int) * (batch + 1), 16) +
+              static_cast<size_t>(l.items) * nheads_kv * sizeof(int4);
     return l;
 }
 
@@ -1099,9 +1108,11 @@ size_t attn_fwd_kvcache_fp8_workspace_bytes(int batch, int total_q, int max_seql
     const bool staged = kv8_staged(batch, max_seqlen_q, nheads_q, nheads_kv);
     if (staged && nheads_q / nheads_kv > 128) return 0;
     return (rotary_dim > 0 || staged
-                ? kv8_query_bytes(static_cast<long long>(total_q) * nheads_q, head_dim)
+                ? kv8_query_bytes(static_cast<long long>(total_q) * nheads_q, head_dim, rotary_dim)
                 : 0) +
-           (staged ? kv8_stage_layout(batch, max_seqlen_q, max_total_k, nheads_q, nheads_kv, head_dim).total
+           (staged ? kv8_stage_layout(batch, max_seqlen_q, max_total_k, nheads_q, nheads_kv, head_dim,
+                                      kv8_tiles(rotary_dim))
+                         .total
                    : kv8_partial_bytes(kv8_grid(batch, max_seqlen_q, nheads_q, nheads_kv, page_size,
                                                 max_pages_per_seq),
                                        head_dim));
@@ -1165,9 +1176,11 @@ attn_status_t attn_fwd_kvcache_fp8(const void* q, const void* k_new, const void*
     ap.k_scale = static_cast<uint8_t*>(k_scale);
     ap.v_scale = static_cast<uint8_t*>(v_scale);
     if (rotary_dim > 0 || staged) {
+        const size_t part = align_up(q_rows * head_dim * 2, 256);
         ap.q_rot = reinterpret_cast<__half*>(ws);
-        ap.q_unit = reinterpret_cast<float*>(ws + align_up(q_rows * head_dim * 2, 256));
-        ws += kv8_query_bytes(q_rows, head_dim);
+        ap.q_lo = rotary_dim > 0 ? reinterpret_cast<__half*>(ws + part) : nullptr;
+        ap.q_unit = reinterpret_cast<float*>(ws + part * (rotary_dim > 0 ? 2 : 1));
+        ws += kv8_query_bytes(q_rows, head_dim, rotary_dim);
     }
     ap.cu_q = cu_seqlens_q;
     ap.cache_seqlens = cache_seqlens;
@@ -1190,7 +1203,8 @@ attn_status_t attn_fwd_kvcache_fp8(const void* q, const void* k_new, const void*
     if (staged) {
         // 2. the keys and values the new tokens see, in f16
         const Kv8StageLayout l =
-            kv8_stage_layout(batch, max_seqlen_q, max_total_k, nheads_q, nheads_kv, head_dim);
+            kv8_stage_layout(batch, max_seqlen_q, max_total_k, nheads_q, nheads_kv, head_dim,
+                             kv8_tiles(rotary_dim));
         StageFp8Params sp;
         memset(&sp, 0, sizeof(sp));
         sp.k_cache = ap.k_cache;
@@ -1234,7 +1248,8 @@ attn_status_t attn_fwd_kvcache_fp8(const void* q, const void* k_new, const void*
         pp.max_seqlen_q = max_seqlen_q;
         pp.Hkv = nheads_kv;
         pp.tpt = tpt;
-        pp.capacity_pairs = static_cast<int>(fwd_capacity_pairs(batch, max_seqlen_q, g));
+        pp.tiles = kv8_tiles(rotary_dim);
+        pp.capacity_pairs = static_cast<int>(l.items);
         pp.causal = causal ? 1 : 0;
         pp.wl = window_left;
         pp.wr = window_right;
@@ -1262,6 +1277,10 @@ attn_status_t attn_fwd_kvcache_fp8(const void* q, const void* k_new, const void*
         fp.wr = window_right;
         fp.scale_log2 = softmax_scale * kLog2eF;
         fp.scale = softmax_scale;
+        if (ap.q_lo != nullptr &&
+            encode_3d(&fp.tm_qlo, ap.q_lo, head_dim, nheads_q, total_q, g, tpt) != ATTN_OK)
+            return ATTN_ERR_CUDA;
+        fp.hi_lo = ap.q_lo != nullptr ? 1 : 0;
         fp.spans = sp.spans;
         fp.q_unit = ap.q_unit;
         fp.k_unit = sp.k_unit;
@@ -1278,6 +1297,7 @@ attn_status_t attn_fwd_kvcache_fp8(const void* q, const void* k_new, const void*
     kp.v_scale = static_cast<const uint8_t*>(v_scale);
     kp.q = ap.q;
     kp.q_rot = ap.q_rot;
+    kp.q_lo = ap.q_lo;
     kp.q_unit = ap.q_unit;
     kp.out = static_cast<__nv_bfloat16*>(out);
     kp.lse = lse;

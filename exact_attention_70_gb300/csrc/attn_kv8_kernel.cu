@@ -13,7 +13,9 @@
 //   * S_ij = 2^ek_j c_i sum_d (2^a_i q_id) k_jd with c_i = scale log2(e) 2^-a_i, where a_i brings
 //     row i's largest |q| just below 2^14: the 8 significant bits of bf16 fit f16's 11, and
 //     elements down to 2^-28 of the row's largest stay exact (below that the error is less than
-//     2^-39 of the largest);
+//     2^-39 of the largest).  A rotated query has no 8 significant bits: it comes as the sum of
+//     two f16 numbers, hi + lo, and both parts are multiplied (rounding it to one moved LSE by up to
+//     1e-4 of itself where a row sees few keys);
 //   * O_i = 2^(E - 5) sum_j (P_ij 2^(5 + ev_j - E)) v_j with P = exp2(x - m), where the references
 //     m (of a row) and E (of a warp) only move when a logit passes m by more than 8 (log2) or
 //     an ev_j passes E by more than 2.  The f16 factor is then at most 2^15 and keeps its 11 bits
@@ -42,7 +44,8 @@ struct Kv8Cfg {
     static constexpr int kOffMerge = kOffScale + kStages * 2 * kKv8Chunk;
     static constexpr int kMergeStride = D + 4;               // floats a row: [16][kMergeStride] of O,
     static constexpr int kMergeBytes = kKv8Rows * kMergeStride * 4 + 2 * 2 * 4 * kKv8Rows * 4;  // m, l
-    static constexpr int kOffBar = kOffMerge + kMergeBytes;
+    static constexpr int kOffQlo = kOffMerge + kMergeBytes;  // the unit's low query parts, as fragments
+    static constexpr int kOffBar = kOffQlo + D / 16 * 32 * 16;
     static constexpr int kSmem = kOffBar + 256 + 1024;
     static_assert(2 * (kSmem + 1024) <= 228 * 1024, "two CTAs per SM");
 };
@@ -140,7 +143,7 @@ __device__ __forceinline__ void scale_pair(uint32_t w, float (&f)[2]) {
 // other in one list, each access 128 bytes out of 1 KB, the 64-sequence case below took 562 us).
 // A unit cut by a share's border leaves partial results in the CTAs' slots (slot 1 of the CTA
 // that starts it, slot 0 of those that go on with it), which kv8_combine_kernel merges.
-template <int D>
+template <int D, bool kLo>
 __global__ void __launch_bounds__(kKv8Threads, 2)
     kv8_split_kernel(const __grid_constant__ Kv8Params p) {
     using C = Kv8Cfg<D>;
@@ -309,6 +312,7 @@ __global__ void __launch_bounds__(kKv8Threads, 2)
     const int mi = lane >> 3, ri = lane & 7;  // ldmatrix: matrix id, row within matrix
     float* const mo = reinterpret_cast<float*>(smem + C::kOffMerge);   // [16 rows][kMergeStride]
     float* const ml_all = mo + kKv8Rows * C::kMergeStride;             // [parity][m, l][4][16]
+    const uint32_t qlo = smem_u32(smem + C::kOffQlo);
     uint32_t n = 0;  // chunks consumed
     for (int seg = 0; w.next(p); ++seg) {
         const int Lq = w.s.Lq, L = w.s.L, q0 = w.s.q0, rows = w.rows, row0 = w.row0;
@@ -330,7 +334,7 @@ __global__ void __launch_bounds__(kKv8Threads, 2)
             const int tok = (row0 + min(r, rows - 1)) / p.g, hd = (row0 + min(r, rows - 1)) % p.g;
             const size_t row = static_cast<size_t>(q0 + tok) * p.Hq + kvh * p.g + hd;
             row_key_interval(tok, Lq, L, p.causal, p.wl, p.wr, kmin[h], kmax[h]);
-            if (p.q_rot != nullptr) {  // rotated and scaled by the append kernel
+            if (kLo) {  // rotated and scaled by the append kernel
                 const uint2* src = reinterpret_cast<const uint2*>(p.q_rot + row * D + 4 * tq);
                 c_row[h] = p.scale_log2 * p.q_unit[row];
 #pragma unroll
@@ -365,6 +369,27 @@ __global__ void __launch_bounds__(kKv8Threads, 2)
                                           __uint_as_float(qw[s].y & 0xffff0000u) * up);
             }
         }
+        if (kLo) {
+            // the low parts, the same for all warps: each brings its k-steps' fragments to shared
+            // memory (every warp is past the previous segment's last read of them: the merge's
+            // barriers lie between)
+#pragma unroll
+            for (int s = warp; s < D / 16; s += 4) {
+                uint2 x[2];
+#pragma unroll
+                for (int h = 0; h < 2; ++h) {
+                    const int r = min(gq + 8 * h, rows - 1);
+                    const int tok = (row0 + r) / p.g, hd = (row0 + r) % p.g;
+                    x[h] = gq + 8 * h < rows
+                               ? *reinterpret_cast<const uint2*>(
+                                     p.q_lo + (static_cast<size_t>(q0 + tok) * p.Hq + kvh * p.g + hd) * D +
+                                     16 * s + 4 * tq)
+                               : make_uint2(0u, 0u);
+                }
+                st_shared_v4(qlo + (s * 32 + lane) * 16, x[0].x, x[1].x, x[0].y, x[1].y);
+            }
+            named_bar_sync(1, 128);
+        }
         // keys every row of the unit sees: [full_lo, full_hi]
         int full_lo, full_hi;
         {
@@ -391,6 +416,14 @@ __global__ void __launch_bounds__(kKv8Threads, 2)
                 const int key = warp * 32 + (mi & 1) * 8 + ri;
 #pragma unroll
                 for (int u = 0; u < D / 16; u += 2) {
+                    uint32_t lo[2][4];
+                    if (kLo) {
+#pragma unroll
+                        for (int i = 0; i < 2; ++i) {
+                            const uint4 f = ld_shared_v4(qlo + ((u + i) * 32 + lane) * 16);
+                            lo[i][0] = f.x, lo[i][1] = f.y, lo[i][2] = f.z, lo[i][3] = f.w;
+                        }
+                    }
 #pragma unroll
                     for (int h = 0; h < 2; ++h) {
                         uint32_t r[4], b[8];
@@ -402,6 +435,12 @@ __global__ void __launch_bounds__(kKv8Threads, 2)
                         mma_f16_16816(s[2 * h + 1], qa[u], b[2], b[3]);
                         mma_f16_16816(s[2 * h], qa[u + 1], b[4], b[5]);
                         mma_f16_16816(s[2 * h + 1], qa[u + 1], b[6], b[7]);
+                        if (kLo) {
+                            mma_f16_16816(s[2 * h], lo[0], b[0], b[1]);
+                            mma_f16_16816(s[2 * h + 1], lo[0], b[2], b[3]);
+                            mma_f16_16816(s[2 * h], lo[1], b[4], b[5]);
+                            mma_f16_16816(s[2 * h + 1], lo[1], b[6], b[7]);
+                        }
                     }
                 }
                 // the keys' scales, in pairs: 2^(b - 127) is the float with exponent field b
@@ -682,8 +721,10 @@ __global__ void __launch_bounds__(kKv8Rows * 16) kv8_combine_kernel(const Kv8Par
 
 cudaError_t configure_kv8_kernels() {
     const cudaFuncAttribute smem = cudaFuncAttributeMaxDynamicSharedMemorySize;
-    cudaError_t e = cudaFuncSetAttribute(kv8_split_kernel<128>, smem, Kv8Cfg<128>::kSmem);
-    if (e == cudaSuccess) e = cudaFuncSetAttribute(kv8_split_kernel<64>, smem, Kv8Cfg<64>::kSmem);
+    cudaError_t e = cudaFuncSetAttribute(kv8_split_kernel<128, false>, smem, Kv8Cfg<128>::kSmem);
+    if (e == cudaSuccess) e = cudaFuncSetAttribute(kv8_split_kernel<128, true>, smem, Kv8Cfg<128>::kSmem);
+    if (e == cudaSuccess) e = cudaFuncSetAttribute(kv8_split_kernel<64, false>, smem, Kv8Cfg<64>::kSmem);
+    if (e == cudaSuccess) e = cudaFuncSetAttribute(kv8_split_kernel<64, true>, smem, Kv8Cfg<64>::kSmem);
     return e;
 }
 
@@ -711,11 +752,13 @@ cudaError_t launch(Kernel kernel, int grid, int threads, size_t smem, bool depen
 // of the same call).
 cudaError_t launch_kv8_attn(const Kv8Params& p, int head_dim, int grid, bool after_append,
                             cudaStream_t stream) {
-    cudaError_t e =
-        head_dim == 128 ? launch(kv8_split_kernel<128>, grid, kKv8Threads, Kv8Cfg<128>::kSmem,
-                                 after_append, p, stream)
-                        : launch(kv8_split_kernel<64>, grid, kKv8Threads, Kv8Cfg<64>::kSmem,
-                                 after_append, p, stream);
+    const bool lo = p.q_lo != nullptr;
+    const cudaError_t e =
+        head_dim == 128
+            ? launch(lo ? kv8_split_kernel<128, true> : kv8_split_kernel<128, false>, grid,
+                     kKv8Threads, Kv8Cfg<128>::kSmem, after_append, p, stream)
+            : launch(lo ? kv8_split_kernel<64, true> : kv8_split_kernel<64, false>, grid,
+                     kKv8Threads, Kv8Cfg<64>::kSmem, after_append, p, stream);
     if (e != cudaSuccess || grid == p.Hkv) return e;  // (one CTA a head cuts nothing)
     return head_dim == 128
                ? launch(kv8_combine_kernel<128>, grid, kKv8Rows * 16, 0, true, p, stream)

@@ -30,9 +30,14 @@
 //     2^8 (the result is exact for any reference; this only bounds P <= 256), so the O
 //     rescale through TMEM is rare after the first blocks.
 //
-// An instance with f16 operands (kHalf) serves the 8-bit cache: Q, K and V are f16 multiples of
-// powers of two (of a query row, of a sequence and kv head), which join the softmax scale and
-// the epilogue's 1 / l, and P is f16, whose 11 bits hold P <= 256 down to 2^-14.
+// Instances with f16 operands (kOps) serve the 8-bit cache: Q, K and V are f16 multiples of powers
+// of two (of a query row, of a sequence and kv head), which join the softmax scale and the
+// epilogue's 1 / l, and P is f16, whose 11 bits hold P <= 256 down to 2^-14.
+// Rotated queries need more than 11 bits: rounding them moves LSE by 1e-5 to 1e-4 of itself where a
+// row sees few keys.  They come as hi + lo, two f16 numbers (kF16HiLo): S = Q_hi K^T + Q_lo K^T,
+// half as many MMAs again.  Both parts of two tiles would not fit in shared memory, so an item is
+// then one tile, whose two halves of the softmax warps take the even and the odd key blocks as
+// two streams with their own maximum, denominator and O; the first stream merges them.
 #include <cuda_bf16.h>
 
 #include "kernels.h"
@@ -43,6 +48,10 @@
 namespace attn {
 
 namespace {
+
+// Operands of the products: bf16; f16; f16 with Q in two parts.
+constexpr int kBf16 = 0, kF16 = 1, kF16HiLo = 2;
+__host__ __device__ constexpr bool is_f16(int ops) { return ops != kBf16; }
 
 constexpr float kRescaleThreshold = 8.0f;  // log2 units
 constexpr float kLn2 = 0.69314718055994530942f;
@@ -60,7 +69,8 @@ struct FwdCfg {
     static constexpr int kOffP = kOffQ + kFwdTilesPerItem * kQTile;
     static constexpr int kOffKV = kOffP + kFwdTilesPerItem * kPTile;
     static constexpr int kOffBar = kOffKV + kSlots * kKvTile;
-    static constexpr int kSmem = kOffBar + 512 + 1024;     // barriers + alignment slack
+    static constexpr int kOffMerge = kOffBar + 512;        // the second stream's (m, l) [128] (kF16HiLo)
+    static constexpr int kSmem = kOffMerge + 1024 + 1024;  // + alignment slack
     static_assert(kSmem <= 227 * 1024, "shared memory per CTA");
     static constexpr uint32_t kTmemCols = 512;
     // TMEM columns of S_t (fp32) and O_t (fp32)
@@ -78,6 +88,7 @@ struct FwdBars {
     uint64_t k_full[8], v_full[8], kv_empty[8];
     uint64_t s_full[2], s_free[2], p_full[2], pv_done[2], o_free[2];
     uint64_t epi_full[2], epi_free[2];  // O staged in P_t for a TMA store / the store read it
+    uint64_t merge_full, merge_free;    // kF16HiLo: the second stream's O, m, l are final / were read
     uint64_t drain[2];
     uint64_t idx_full[4], idx_empty[4];  // the claimed item indices (fwd_claim_item)
     int idx_ring[4];
@@ -101,7 +112,7 @@ struct Item {
     bool any;
 };
 
-template <bool kPaged, bool kHalf>
+template <bool kPaged, int kOps>
 __device__ __forceinline__ Item load_item(const FwdParams& p, int idx) {
     Item it;
     const int4 w = p.items[idx];
@@ -113,7 +124,7 @@ __device__ __forceinline__ Item load_item(const FwdParams& p, int idx) {
     if constexpr (kPaged) {  // the cached prefix, then this call's new tokens
         it.k0 = 0;
         it.Lk = p.cache_seqlens[it.b] + it.Lq;
-    } else if constexpr (kHalf) {  // the staged keys: each sequence starts a block of its own
+    } else if constexpr (is_f16(kOps)) {  // the staged keys: each sequence starts a block of its own
         const int2 span = p.spans[it.b];
         it.k0 = span.x;
         it.Lk = span.y;
@@ -126,7 +137,7 @@ __device__ __forceinline__ Item load_item(const FwdParams& p, int idx) {
     it.any = false;
 #pragma unroll
     for (int t = 0; t < 2; ++t) {
-        it.tok0[t] = (2 * m + t) * p.tpt;
+        it.tok0[t] = (kOps == kF16HiLo ? m : 2 * m + t) * p.tpt;
         it.rows[t] = it.tok0[t] < it.Lq;
         it.imin[t] = it.tok0[t];
         it.imax[t] = min(it.tok0[t] + p.tpt, it.Lq) - 1;
@@ -137,7 +148,7 @@ __device__ __forceinline__ Item load_item(const FwdParams& p, int idx) {
                                              p.causal, p.wl, p.wr);
             it.lo[t] = r.lo;
             it.hi[t] = r.hi;
-            it.mma[t] = r.hi > r.lo;
+            it.mma[t] = r.hi > r.lo + (kOps == kF16HiLo ? t : 0);
             if (it.mma[t]) {
                 it.jlo = min(it.jlo, r.lo);
                 it.jhi = max(it.jhi, r.hi);
@@ -148,7 +159,9 @@ __device__ __forceinline__ Item load_item(const FwdParams& p, int idx) {
     return it;
 }
 
+template <int kOps>
 __device__ __forceinline__ bool tile_uses(const Item& it, int t, int j) {
+    if (kOps == kF16HiLo) return it.mma[t] && ((j - it.jlo) & 1) == t;
     return it.mma[t] && it.lo[t] <= j && j < it.hi[t];
 }
 
@@ -227,7 +240,7 @@ struct RingState {
     uint32_t n = 0, kpar = 0, vpar = 0, lastv = 0;
 };
 
-template <int D, bool kPaged, bool kHalf>
+template <int D, bool kPaged, int kOps>
 __device__ void fwd_producer_loop(const FwdParams& p, uint8_t* smem, FwdBars* bars,
                                   const Watchdog& wd, int n_items, uint32_t& q_cnt,
                                   RingState& ring) {
@@ -240,7 +253,7 @@ __device__ void fwd_producer_loop(const FwdParams& p, uint8_t* smem, FwdBars* ba
     int idx;
     if (!fwd_claim_item(p, bars, wd, n_items, claims++, idx)) return;
     while (idx >= 0) {
-        const Item it = load_item<kPaged, kHalf>(p, idx);
+        const Item it = load_item<kPaged, kOps>(p, idx);
         int next = -1;
         bool claimed = false;
         if (!it.any) {
@@ -249,18 +262,20 @@ __device__ void fwd_producer_loop(const FwdParams& p, uint8_t* smem, FwdBars* ba
             continue;
         }
         if (q_cnt > 0 && !wd.wait(&bars->q_empty, (q_cnt - 1) & 1)) return;
+        // (kF16HiLo: the tile's high part where tile 0's Q would be, its low part where tile 1's would)
         uint32_t qbytes = 0;
 #pragma unroll
         for (int t = 0; t < 2; ++t)
-            if (it.mma[t]) qbytes += q_box_bytes * C::kHalves;
+            if (kOps == kF16HiLo || it.mma[t]) qbytes += q_box_bytes * C::kHalves;
         mbar_arrive_expect_tx(&bars->q_full, qbytes);
 #pragma unroll
         for (int t = 0; t < 2; ++t) {
-            if (!it.mma[t]) continue;
+            if (kOps != kF16HiLo && !it.mma[t]) continue;
 #pragma unroll
             for (int h = 0; h < C::kHalves; ++h)
-                tma_load_3d(smem + C::kOffQ + t * C::kQTile + h * C::kAtomBytes, &p.tm_q,
-                            &bars->q_full, h * 64, it.kvh * p.g, it.q0 + it.tok0[t]);
+                tma_load_3d(smem + C::kOffQ + t * C::kQTile + h * C::kAtomBytes,
+                            kOps == kF16HiLo && t == 1 ? &p.tm_qlo : &p.tm_q, &bars->q_full, h * 64,
+                            it.kvh * p.g, it.q0 + it.tok0[t]);
         }
         ++q_cnt;
         const int m = it.jhi - it.jlo;
@@ -324,13 +339,13 @@ __device__ void fwd_producer_loop(const FwdParams& p, uint8_t* smem, FwdBars* ba
     }
 }
 
-template <int D, bool kPaged, bool kHalf>
+template <int D, bool kPaged, int kOps>
 __device__ void fwd_producer(const FwdParams& p, uint8_t* smem, FwdBars* bars,
                              const Watchdog& wd, int n_items) {
     using C = FwdCfg<D>;
     uint32_t q_cnt = 0;
     RingState ring;
-    fwd_producer_loop<D, kPaged, kHalf>(p, smem, bars, wd, n_items, q_cnt, ring);
+    fwd_producer_loop<D, kPaged, kOps>(p, smem, bars, wd, n_items, q_cnt, ring);
     // Every slot holds at most one load in flight: wait for the latest load of each one (its
     // phase has the parity before that load's flip).
     if (q_cnt > 0) drain_wait(&bars->q_full, (q_cnt - 1) & 1);
@@ -345,11 +360,11 @@ __device__ void fwd_producer(const FwdParams& p, uint8_t* smem, FwdBars* bars,
 
 // S_t(j) for every (j, t) of every item.  S_t(j) overwrites the TMEM columns of S_t(j-1), so
 // it waits for tile t's softmax to have read them (s_free).
-template <int D, bool kPaged, bool kHalf>
+template <int D, bool kPaged, int kOps>
 __device__ void fwd_mma_s(const FwdParams& p, uint8_t* smem, FwdBars* bars, uint32_t tmem,
                           const Watchdog& wd, int n_items) {
     using C = FwdCfg<D>;
-    constexpr uint32_t kIdesc = kHalf ? idesc_f16_f32(128, kFwdBlockN, false, false)
+    constexpr uint32_t kIdesc = is_f16(kOps) ? idesc_f16_f32(128, kFwdBlockN, false, false)
                                        : idesc_bf16_f32(128, kFwdBlockN, false, false);
     // K-major operand descriptors (128-byte swizzle, 8-row groups 1024 B apart), as halves
     const uint64_t dq = sdesc_sw128(smem_u32(smem + C::kOffQ), 16, 1024);
@@ -362,7 +377,7 @@ __device__ void fwd_mma_s(const FwdParams& p, uint8_t* smem, FwdBars* bars, uint
     for (uint32_t rd = 0;;) {
         const int idx = fwd_take_item(bars, wd, rd);
         if (idx < 0) return;
-        const Item it = load_item<kPaged, kHalf>(p, idx);
+        const Item it = load_item<kPaged, kOps>(p, idx);
         if (!it.any) continue;
         if (!wd.wait(&bars->q_full, q_cnt & 1)) return;
         ++q_cnt;
@@ -376,16 +391,24 @@ __device__ void fwd_mma_s(const FwdParams& p, uint8_t* smem, FwdBars* bars, uint
             const uint32_t k_lo = kv_lo + st * (C::kKvTile >> 4);
 #pragma unroll
             for (int t = 0; t < 2; ++t) {
-                if (!tile_uses(it, t, j)) continue;
+                if (!tile_uses<kOps>(it, t, j)) continue;
                 uint32_t& sc = t ? s_cnt1 : s_cnt0;
                 if (sc > 0 && !wd.wait(&bars->s_free[t], (sc - 1) & 1)) return;
                 tc_fence_after();
-                const uint32_t a_lo = q_lo + t * (C::kQTile >> 4);
+                const uint32_t a_lo = q_lo + (kOps == kF16HiLo ? 0 : t * (C::kQTile >> 4));
 #pragma unroll
                 for (int kk = 0; kk < D / 16; ++kk) {
                     const uint32_t off = ((kk >> 2) * C::kAtomBytes + (kk & 3) * 32) >> 4;
                     umma_ss_lh(tmem + C::col_s(t), a_lo + off, d_hi, k_lo + off, d_hi, kIdesc,
                                kk > 0);
+                }
+                if (kOps == kF16HiLo) {
+#pragma unroll
+                    for (int kk = 0; kk < D / 16; ++kk) {
+                        const uint32_t off = ((kk >> 2) * C::kAtomBytes + (kk & 3) * 32) >> 4;
+                        umma_ss_lh(tmem + C::col_s(t), a_lo + (C::kQTile >> 4) + off, d_hi,
+                                   k_lo + off, d_hi, kIdesc, 1u);
+                    }
                 }
                 umma_commit(&bars->s_full[t]);
                 ++sc;
@@ -400,12 +423,12 @@ __device__ void fwd_mma_s(const FwdParams& p, uint8_t* smem, FwdBars* bars, uint
 // O_t (+)= P_t(j) V_j for every (j, t) of every item, P_t from shared memory.  The item's
 // first PV_t overwrites O_t, so it first waits for the previous item's epilogue to have read
 // O_t (o_free).
-template <int D, bool kPaged, bool kHalf>
+template <int D, bool kPaged, int kOps>
 __device__ void fwd_mma_pv(const FwdParams& p, uint8_t* smem, FwdBars* bars, uint32_t tmem,
                            const Watchdog& wd, int n_items) {
     using C = FwdCfg<D>;
     constexpr uint32_t kIdesc =
-        kHalf ? idesc_f16_f32(128, D, false, true) : idesc_bf16_f32(128, D, false, true);
+        is_f16(kOps) ? idesc_f16_f32(128, D, false, true) : idesc_bf16_f32(128, D, false, true);
     // A = P_t (K-major), B = V (MN-major: 64-wide d atoms kAtomBytes apart), as halves
     const uint64_t dp = sdesc_sw128(smem_u32(smem + C::kOffP), 16, 1024);
     const uint64_t dv = sdesc_sw128(smem_u32(smem + C::kOffKV), C::kAtomBytes, 1024);
@@ -418,7 +441,7 @@ __device__ void fwd_mma_pv(const FwdParams& p, uint8_t* smem, FwdBars* bars, uin
     for (uint32_t rd = 0;;) {
         const int idx = fwd_take_item(bars, wd, rd);
         if (idx < 0) return;
-        const Item it = load_item<kPaged, kHalf>(p, idx);
+        const Item it = load_item<kPaged, kOps>(p, idx);
         if (!it.any) continue;
         bool first0 = true, first1 = true;
         const int m = it.jhi - it.jlo;
@@ -431,7 +454,7 @@ __device__ void fwd_mma_pv(const FwdParams& p, uint8_t* smem, FwdBars* bars, uin
             const uint32_t b_lo = v_lo + st * (C::kKvTile >> 4);
 #pragma unroll
             for (int t = 0; t < 2; ++t) {
-                if (!tile_uses(it, t, j)) continue;
+                if (!tile_uses<kOps>(it, t, j)) continue;
                 bool& first = t ? first1 : first0;
                 const uint32_t oi = t ? o_items1 : o_items0;
                 if (first && oi > 0 && !wd.wait(&bars->o_free[t], (oi - 1) & 1)) return;
@@ -492,7 +515,7 @@ __device__ __forceinline__ uint32_t sw128_unit(uint32_t base, int r, int u) {
     return base + (u >> 3) * (128 * 128) + r * 128 + (((u & 7) ^ (r & 7)) << 4);
 }
 
-template <int D, bool kPaged, bool kMods, bool kHalf>
+template <int D, bool kPaged, bool kMods, int kOps>
 __device__ void fwd_softmax(const FwdParams& p, uint8_t* smem, FwdBars* bars, uint32_t tmem,
                             const Watchdog& wd, int n_items, int t, int k, int lane) {
     using C = FwdCfg<D>;
@@ -540,10 +563,11 @@ __device__ void fwd_softmax(const FwdParams& p, uint8_t* smem, FwdBars* bars, ui
     uint32_t blk = 0;  // blocks of tile t processed so far (== S_t consumed == P_t produced)
     uint32_t kv_cnt = 0;  // K/V ring slots filled for earlier items (locates paged V blocks)
     uint32_t vpar = 0;    // per-slot parity of the V blocks loaded for earlier items (paged)
+    uint32_t merge_cnt = 0;  // items in which the second stream handed over its rows (kF16HiLo)
     for (uint32_t rd = 0;;) {
         const int idx = fwd_take_item_warp(bars, wd, rd, lane);
         if (idx < 0) break;
-        const Item it = load_item<kPaged, kHalf>(p, idx);
+        const Item it = load_item<kPaged, kOps>(p, idx);
         const uint32_t kv_base = kv_cnt;
         const uint32_t vpar_item = vpar;
         if (it.any) {
@@ -554,9 +578,11 @@ __device__ void fwd_softmax(const FwdParams& p, uint8_t* smem, FwdBars* bars, ui
         }
         const TileView tv = tile_view(it, t);
         if (!tv.rows) continue;
+        if (kOps == kF16HiLo && t == 1 && !tv.mma) continue;  // no block for the second stream
+        const int j0 = tv.lo + (kOps == kF16HiLo ? t : 0), jstep = kOps == kF16HiLo ? 2 : 1;
         // f16 operands come as multiples of a unit per query row and per (sequence, kv head)
         float sl2_a = sl2, sl2_b = sl2;
-        if constexpr (kHalf) {
+        if constexpr (is_f16(kOps)) {
             const float unit = p.k_unit[it.b * p.Hkv + it.kvh] * sl2;
             const int ta = tv.tok0 + ra / g, tb = tv.tok0 + (ra + 8) / g;
             const float* qu = p.q_unit + it.kvh * g;
@@ -586,7 +612,7 @@ __device__ void fwd_softmax(const FwdParams& p, uint8_t* smem, FwdBars* bars, ui
                                                     kFwdBlockN, p.causal, p.wl, p.wr))
             --full_hi;
         if (tv.mma) {
-            for (int j = tv.lo; j < tv.hi; ++j) {
+            for (int j = j0; j < tv.hi; j += jstep) {
                 if (!__all_sync(0xffffffffu, wd.wait(s_full, blk & 1))) return;
                 tc_fence_after();
                 uint32_t s[64];
@@ -701,8 +727,8 @@ __device__ void fwd_softmax(const FwdParams& p, uint8_t* smem, FwdBars* bars, ui
                     mba = fmaf(mxa, sl2, ra0);
                     mbb = fmaf(mxb, sl2, rb0);
                 } else {
-                    mba = mxa * (kHalf ? sl2_a : sl2);
-                    mbb = mxb * (kHalf ? sl2_b : sl2);
+                    mba = mxa * (is_f16(kOps) ? sl2_a : sl2);
+                    mbb = mxb * (is_f16(kOps) ? sl2_b : sl2);
                 }
                 const bool need_a = mba > m_a + kRescaleThreshold;
                 const bool need_b = mbb > m_b + kRescaleThreshold;
@@ -724,8 +750,8 @@ __device__ void fwd_softmax(const FwdParams& p, uint8_t* smem, FwdBars* bars, ui
                     nmb = f2_make(-rb_ref, -rb_ref);
                 }
                 // P = exp2(s * scale*log2e - m): paired FFMA, MUFU ex2, paired sums
-                const uint64_t sa2 = kHalf ? f2_make(sl2_a, sl2_a) : sl2x2;
-                const uint64_t sb2 = kHalf ? f2_make(sl2_b, sl2_b) : sl2x2;
+                const uint64_t sa2 = is_f16(kOps) ? f2_make(sl2_a, sl2_a) : sl2x2;
+                const uint64_t sb2 = is_f16(kOps) ? f2_make(sl2_b, sl2_b) : sl2x2;
                 uint64_t suma = 0, sumb = 0;
                 uint32_t pka[16], pkb[16];
 #pragma unroll
@@ -741,8 +767,8 @@ __device__ void fwd_softmax(const FwdParams& p, uint8_t* smem, FwdBars* bars, ui
                     const float pb0 = ex2_approx(b0), pb1 = ex2_approx(b1);
                     suma = f2_add(suma, f2_make(pa0, pa1));
                     sumb = f2_add(sumb, f2_make(pb0, pb1));
-                    pka[c] = kHalf ? pack_f16x2(pa0, pa1) : pack_bf16x2(pa0, pa1);
-                    pkb[c] = kHalf ? pack_f16x2(pb0, pb1) : pack_bf16x2(pb0, pb1);
+                    pka[c] = is_f16(kOps) ? pack_f16x2(pa0, pa1) : pack_bf16x2(pa0, pa1);
+                    pkb[c] = is_f16(kOps) ? pack_f16x2(pb0, pb1) : pack_bf16x2(pb0, pb1);
                 }
                 {
                     float lo, hi;
@@ -778,7 +804,7 @@ __device__ void fwd_softmax(const FwdParams& p, uint8_t* smem, FwdBars* bars, ui
                     if (!__all_sync(0xffffffffu, wd.wait(pv_done, (blk - 1) & 1))) return;
                     tc_fence_after();
                 }
-                if (__any_sync(0xffffffffu, need_a || need_b) && j > tv.lo) {
+                if (__any_sync(0xffffffffu, need_a || need_b) && j > j0) {
 #pragma unroll 1
                     for (int cc = 0; cc < D / 32; ++cc) {
                         uint32_t o[16];
@@ -823,9 +849,47 @@ __device__ void fwd_softmax(const FwdParams& p, uint8_t* smem, FwdBars* bars, ui
             l_b += __shfl_xor_sync(0xffffffffu, l_b, 2);
             if (!__all_sync(0xffffffffu, wd.wait(pv_done, (blk - 1) & 1))) return;
             tc_fence_after();
+            // kF16HiLo: the second stream hands over its rows' m and l once its last PV is done (O_1
+            // stays in TMEM); the first one weighs both
+            float w_a = 1.f, w_b = 1.f, w1_a = 0.f, w1_b = 0.f;
+            if constexpr (kOps == kF16HiLo) {
+                float2* const rows_ml = reinterpret_cast<float2*>(smem + C::kOffMerge);
+                if (t == 1) {
+                    if (merge_cnt > 0 &&
+                        !__all_sync(0xffffffffu, wd.wait(&bars->merge_free, (merge_cnt - 1) & 1)))
+                        return;
+                    ++merge_cnt;
+                    if ((lane & 3) == 0) {
+                        rows_ml[ra] = make_float2(m_a, l_a);
+                        rows_ml[ra + 8] = make_float2(m_b, l_b);
+                    }
+                    tc_fence_before();
+                    __syncwarp();
+                    if (lane == 0) mbar_arrive(&bars->merge_full);
+                    continue;
+                }
+                if (it.mma[1]) {
+                    if (!__all_sync(0xffffffffu, wd.wait(&bars->merge_full, merge_cnt & 1))) return;
+                    ++merge_cnt;
+                    tc_fence_after();
+                    const float2 ml_a = rows_ml[ra], ml_b = rows_ml[ra + 8];
+                    __syncwarp();
+                    if (lane == 0) mbar_arrive(&bars->merge_free);
+                    const float M_a = fmaxf(m_a, ml_a.x), M_b = fmaxf(m_b, ml_b.x);
+                    const float Ra = M_a == -INFINITY ? 0.f : M_a, Rb = M_b == -INFINITY ? 0.f : M_b;
+                    w_a = ex2_approx(m_a - Ra);
+                    w_b = ex2_approx(m_b - Rb);
+                    w1_a = ex2_approx(ml_a.x - Ra);
+                    w1_b = ex2_approx(ml_b.x - Rb);
+                    l_a = l_a * w_a + ml_a.y * w1_a;
+                    l_b = l_b * w_b + ml_b.y * w1_b;
+                    m_a = M_a;
+                    m_b = M_b;
+                }
+            }
             float inv_a = l_a > 0.f ? 1.f / l_a : 0.f;
             float inv_b = l_b > 0.f ? 1.f / l_b : 0.f;
-            if constexpr (kHalf) {
+            if constexpr (is_f16(kOps)) {
                 const float unit = p.v_unit[it.b * p.Hkv + it.kvh];
                 inv_a *= unit;
                 inv_b *= unit;
@@ -835,6 +899,18 @@ __device__ void fwd_softmax(const FwdParams& p, uint8_t* smem, FwdBars* bars, ui
                 uint32_t o[32];
                 tmem_ld16x256_x8(tO + 64 * cc, o);
                 tmem_wait_ld();
+                if constexpr (kOps == kF16HiLo) {
+                    if (it.mma[1]) {
+                        uint32_t o1[32];
+                        tmem_ld16x256_x8(tO + C::col_o(1) - C::col_o(0) + 64 * cc, o1);
+                        tmem_wait_ld();
+#pragma unroll
+                        for (int c = 0; c < 32; ++c)
+                            o[c] = __float_as_uint(
+                                __uint_as_float(o[c]) * (c & 2 ? w_b : w_a) +
+                                __uint_as_float(o1[c]) * (c & 2 ? w1_b : w1_a));
+                    }
+                }
 #pragma unroll
                 for (int cp = 0; cp < 4; ++cp) {
                     const int c = 2 * cp;
@@ -852,6 +928,7 @@ __device__ void fwd_softmax(const FwdParams& p, uint8_t* smem, FwdBars* bars, ui
             tc_fence_before();
             __syncwarp();
             if (lane == 0) mbar_arrive(o_free);
+            if (kOps == kF16HiLo && it.mma[1] && lane == 0) mbar_arrive(&bars->o_free[1]);
             if (tv.tok0 + p.tpt <= it.Lq) {
                 // Every packed row of the tile is a row of this sequence: one TMA store per
                 // 64 columns writes the tile's g * tpt rows, asynchronously.
@@ -948,7 +1025,7 @@ __device__ void fwd_softmax(const FwdParams& p, uint8_t* smem, FwdBars* bars, ui
     }
 }
 
-template <int D, bool kPaged, bool kMods, bool kHalf>
+template <int D, bool kPaged, bool kMods, int kOps>
 __global__ void __launch_bounds__(kFwdThreads, 1) fwd_kernel(const __grid_constant__ FwdParams p) {
     using C = FwdCfg<D>;
     extern __shared__ uint8_t smem_raw[];
@@ -966,6 +1043,8 @@ __global__ void __launch_bounds__(kFwdThreads, 1) fwd_kernel(const __grid_consta
             mbar_init(&bars->v_full[i], 1);
             mbar_init(&bars->kv_empty[i], 1);
         }
+        mbar_init(&bars->merge_full, kSoftmaxWarps / 2);
+        mbar_init(&bars->merge_free, kSoftmaxWarps / 2);
         for (int t = 0; t < 2; ++t) {
             mbar_init(&bars->s_full[t], 1);
             mbar_init(&bars->s_free[t], kSoftmaxWarps / 2);
@@ -1000,14 +1079,14 @@ __global__ void __launch_bounds__(kFwdThreads, 1) fwd_kernel(const __grid_consta
     if (warp >= kSoftmaxWarps) {
         regs_decrease<64>();
         if (warp == kSoftmaxWarps) {
-            if (lane == 0) fwd_producer<D, kPaged, kHalf>(p, smem, bars, wd, n_items);
+            if (lane == 0) fwd_producer<D, kPaged, kOps>(p, smem, bars, wd, n_items);
         } else if (warp == kSoftmaxWarps + 1 || warp == kSoftmaxWarps + 2) {
             if (lane == 0) {
                 const int w = warp - kSoftmaxWarps - 1;
                 if (w == 0)
-                    fwd_mma_s<D, kPaged, kHalf>(p, smem, bars, tmem, wd, n_items);
+                    fwd_mma_s<D, kPaged, kOps>(p, smem, bars, tmem, wd, n_items);
                 else
-                    fwd_mma_pv<D, kPaged, kHalf>(p, smem, bars, tmem, wd, n_items);
+                    fwd_mma_pv<D, kPaged, kOps>(p, smem, bars, tmem, wd, n_items);
                 // every tcgen05 op this thread issued has finished before TMEM is released
                 umma_commit(&bars->drain[w]);
                 drain_wait(&bars->drain[w], 0);
@@ -1015,7 +1094,7 @@ __global__ void __launch_bounds__(kFwdThreads, 1) fwd_kernel(const __grid_consta
         }
     } else {
         regs_increase<104>();
-        fwd_softmax<D, kPaged, kMods, kHalf>(p, smem, bars, tmem, wd, n_items, warp >> 3, warp & 7, lane);
+        fwd_softmax<D, kPaged, kMods, kOps>(p, smem, bars, tmem, wd, n_items, warp >> 3, warp & 7, lane);
         // the output stores this thread issued have completed before the CTA's memory goes
         if ((warp & 7) == 0 && lane == 0) bulk_wait_group_all();
     }
@@ -1065,8 +1144,8 @@ __device__ __forceinline__ int seq_keys(const FwdPrepParams& p, int b) {
 
 __device__ int item_cost(const FwdPrepParams& p, int Lq, int Lk, int m) {
     int cost = 0;
-    for (int t = 0; t < 2; ++t) {
-        const int tok0 = (2 * m + t) * p.tpt;
+    for (int t = 0; t < p.tiles; ++t) {
+        const int tok0 = (p.tiles * m + t) * p.tpt;
         if (tok0 >= Lq) continue;
         const KvRange r = kv_block_range(tok0, min(tok0 + p.tpt, Lq) - 1, Lq, Lk, kFwdBlockN,
                                          p.causal, p.wl, p.wr);
@@ -1106,7 +1185,7 @@ __global__ void __launch_bounds__(kPrepThreads) fwd_prepare_kernel(FwdPrepParams
         return;
     }
     // 2. work items (pairs of Q tiles) per sequence, prefix-summed
-    const int per_item = 2 * p.tpt;
+    const int per_item = p.tiles * p.tpt;
     int carry = 0;
     for (int base = 0; base < p.batch; base += blockDim.x) {
         const int b = base + tid;
@@ -1181,14 +1260,16 @@ int fwd_smem_bytes(int head_dim) {
 
 cudaError_t configure_fwd_kernels() {
     const cudaFuncAttribute smem = cudaFuncAttributeMaxDynamicSharedMemorySize;
-    cudaError_t e = cudaFuncSetAttribute(fwd_kernel<128, false, false, false>, smem, FwdCfg<128>::kSmem);
-    if (e == cudaSuccess) e = cudaFuncSetAttribute(fwd_kernel<64, false, false, false>, smem, FwdCfg<64>::kSmem);
-    if (e == cudaSuccess) e = cudaFuncSetAttribute(fwd_kernel<128, true, false, false>, smem, FwdCfg<128>::kSmem);
-    if (e == cudaSuccess) e = cudaFuncSetAttribute(fwd_kernel<64, true, false, false>, smem, FwdCfg<64>::kSmem);
-    if (e == cudaSuccess) e = cudaFuncSetAttribute(fwd_kernel<128, false, true, false>, smem, FwdCfg<128>::kSmem);
-    if (e == cudaSuccess) e = cudaFuncSetAttribute(fwd_kernel<64, false, true, false>, smem, FwdCfg<64>::kSmem);
-    if (e == cudaSuccess) e = cudaFuncSetAttribute(fwd_kernel<128, false, false, true>, smem, FwdCfg<128>::kSmem);
-    if (e == cudaSuccess) e = cudaFuncSetAttribute(fwd_kernel<64, false, false, true>, smem, FwdCfg<64>::kSmem);
+    cudaError_t e = cudaFuncSetAttribute(fwd_kernel<128, false, false, kBf16>, smem, FwdCfg<128>::kSmem);
+    if (e == cudaSuccess) e = cudaFuncSetAttribute(fwd_kernel<64, false, false, kBf16>, smem, FwdCfg<64>::kSmem);
+    if (e == cudaSuccess) e = cudaFuncSetAttribute(fwd_kernel<128, true, false, kBf16>, smem, FwdCfg<128>::kSmem);
+    if (e == cudaSuccess) e = cudaFuncSetAttribute(fwd_kernel<64, true, false, kBf16>, smem, FwdCfg<64>::kSmem);
+    if (e == cudaSuccess) e = cudaFuncSetAttribute(fwd_kernel<128, false, true, kBf16>, smem, FwdCfg<128>::kSmem);
+    if (e == cudaSuccess) e = cudaFuncSetAttribute(fwd_kernel<64, false, true, kBf16>, smem, FwdCfg<64>::kSmem);
+    if (e == cudaSuccess) e = cudaFuncSetAttribute(fwd_kernel<128, false, false, kF16>, smem, FwdCfg<128>::kSmem);
+    if (e == cudaSuccess) e = cudaFuncSetAttribute(fwd_kernel<64, false, false, kF16>, smem, FwdCfg<64>::kSmem);
+    if (e == cudaSuccess) e = cudaFuncSetAttribute(fwd_kernel<128, false, false, kF16HiLo>, smem, FwdCfg<128>::kSmem);
+    if (e == cudaSuccess) e = cudaFuncSetAttribute(fwd_kernel<64, false, false, kF16HiLo>, smem, FwdCfg<64>::kSmem);
     return e;
 }
 
@@ -1199,7 +1280,7 @@ cudaError_t launch_fwd_prepare(const FwdPrepParams& p, cudaStream_t stream) {
 
 // The forward kernel goes out as a programmatic dependent of the work-list kernel just before
 // it: its CTAs initialise barriers and TMEM while the list is built (griddep_wait in the kernel).
-template <int D, bool kPaged, bool kMods, bool kHalf>
+template <int D, bool kPaged, bool kMods, int kOps>
 cudaError_t launch_fwd_instance(const FwdParams& p, int grid, cudaStream_t stream) {
     cudaLaunchConfig_t cfg = {};
     cfg.gridDim = dim3(grid);
@@ -1211,7 +1292,7 @@ cudaError_t launch_fwd_instance(const FwdParams& p, int grid, cudaStream_t strea
     attr[0].val.programmaticStreamSerializationAllowed = 1;
     cfg.attrs = attr;
     cfg.numAttrs = 1;
-    return cudaLaunchKernelEx(&cfg, fwd_kernel<D, kPaged, kMods, kHalf>, p);
+    return cudaLaunchKernelEx(&cfg, fwd_kernel<D, kPaged, kMods, kOps>, p);
 }
 
 // K/V through block_table when p.block_table is set, else contiguous; the score-modifier
@@ -1222,17 +1303,20 @@ cudaError_t launch_fwd(const FwdParams& p, int head_dim, int grid, cudaStream_t 
     const bool mods = p.softcap > 0.f || p.alibi != nullptr;
     const bool half = p.spans != nullptr;
     if ((paged && mods) || (half && (paged || mods))) return cudaErrorInvalidValue;
+    if (half && p.hi_lo)
+        return head_dim == 128 ? launch_fwd_instance<128, false, false, kF16HiLo>(p, grid, stream)
+                               : launch_fwd_instance<64, false, false, kF16HiLo>(p, grid, stream);
     if (half)
-        return head_dim == 128 ? launch_fwd_instance<128, false, false, true>(p, grid, stream)
-                               : launch_fwd_instance<64, false, false, true>(p, grid, stream);
+        return head_dim == 128 ? launch_fwd_instance<128, false, false, kF16>(p, grid, stream)
+                               : launch_fwd_instance<64, false, false, kF16>(p, grid, stream);
     if (head_dim == 128) {
-        if (paged) return launch_fwd_instance<128, true, false, false>(p, grid, stream);
-        if (mods) return launch_fwd_instance<128, false, true, false>(p, grid, stream);
-        return launch_fwd_instance<128, false, false, false>(p, grid, stream);
+        if (paged) return launch_fwd_instance<128, true, false, kBf16>(p, grid, stream);
+        if (mods) return launch_fwd_instance<128, false, true, kBf16>(p, grid, stream);
+        return launch_fwd_instance<128, false, false, kBf16>(p, grid, stream);
     }
-    if (paged) return launch_fwd_instance<64, true, false, false>(p, grid, stream);
-    if (mods) return launch_fwd_instance<64, false, true, false>(p, grid, stream);
-    return launch_fwd_instance<64, false, false, false>(p, grid, stream);
+    if (paged) return launch_fwd_instance<64, true, false, kBf16>(p, grid, stream);
+    if (mods) return launch_fwd_instance<64, false, true, kBf16>(p, grid, stream);
+    return launch_fwd_instance<64, false, false, kBf16>(p, grid, stream);
 }
 
 }  // namespace attn

@@ -57,6 +57,7 @@ struct FwdPrepParams {
     unsigned* status;
     int batch, total_q, total_k, max_seqlen_q, max_seqlen_k;
     int Hkv, tpt, capacity_pairs;
+    int tiles;            // Q tiles per item
     int causal, wl, wr;
     int heads_per_group;  // KV heads whose items are listed together (1..Hkv)
 };
@@ -87,10 +88,13 @@ struct FwdParams {
     int page_size, max_pages, num_pages, box_rows;
     // Staged f16 K/V (spans != null): q, k, v are f16 multiples of the units, sequence b's keys
     // are rows [spans[b].x, spans[b].x + spans[b].y) of k and v.
+    // With hi_lo, q holds the high parts and tm_qlo the low ones, and an item is one tile.
+    CUtensorMap tm_qlo;
     const int2* spans;
     const float* q_unit;  // [total_q, Hq]
     const float* k_unit;  // [batch, Hkv]
     const float* v_unit;
+    int hi_lo;
 };
 
 // ---- paged-cache append (chunked prefill) ---------------------------------------------------
@@ -198,8 +202,9 @@ struct AppendFp8Params {
     uint8_t* v_cache;
     uint8_t* k_scale;
     uint8_t* v_scale;
-    __half* q_rot;   // [total_q, Hq, d]: the rotated query times a power of two a row
-    float* q_unit;   // [total_q, Hq]: what one unit of q_rot stands for
+    __half* q_rot;   // [total_q, Hq, d]: the query times a power of two a row
+    __half* q_lo;    // rotated: what q_rot's rounding left (null without rotation, where it is 0)
+    float* q_unit;   // [total_q, Hq]: what one unit of q_rot and q_lo stands for
     const int* cu_q;
     const int* cache_seqlens;
     const int* block_table;
@@ -253,8 +258,9 @@ struct Kv8Params {
     const uint8_t* k_scale;
     const uint8_t* v_scale;
     const __nv_bfloat16* q;  // [total_q, Hq, d], or, where the queries were rotated,
-    const __half* q_rot;     //   their scaled f16 form
-    const float* q_unit;     //   and its units [total_q, Hq]
+    const __half* q_rot;     //   their scaled f16 form, high part
+    const __half* q_lo;      //   and low part,
+    const float* q_unit;     //   and their units [total_q, Hq]
     __nv_bfloat16* out;
     float* lse;
     float* part_o;    // [CTA][2][16 rows][d]: the parts of units cut by a share's border

@@ -216,8 +216,9 @@ __device__ __forceinline__ AppendToken append_token(const AppendFp8Params& p, in
     return a;
 }
 
-// Rotated queries go to the attention kernel as f16 times a power of two a row: 11 significant
-// bits of the rotated value, where bf16's 8 would put up to 2^-9 of a logit's terms on it.
+// Queries go to the attention kernels as f16 times a power of two a row, rotated ones as the sum
+// of two f16 numbers, 22 significant bits: rounding them to bf16 (or to one f16) moved LSE by
+// up to 1e-3 (1e-4) of itself where a row sees few keys.
 //
 // Bound by memory, and by its latency: a block takes a run of tokens, whose places (sequence,
 // position, page) its first threads find once, and each group of D / 16 lanes walks its share of
@@ -325,15 +326,19 @@ __device__ __forceinline__ void append_rows(const AppendFp8Params& p, int tokens
                 const size_t at = static_cast<size_t>(t0 + it.tok) * p.Hq + it.h0 + i;
 #pragma unroll
                 for (int m = 0; m < 2; ++m) {
-                    uint32_t out[4];
+                    uint32_t hi[4], lo[4];
 #pragma unroll
                     for (int j = 0; j < 4; ++j) {
                         float f0, f1;
                         f2_split(f2_mul(y[4 * m + j], f2_make(f, f)), f0, f1);
-                        out[j] = pack_f16x2(f0, f1);
+                        hi[j] = pack_f16x2(f0, f1);
+                        const float2 h = f16x2_to_float2(hi[j]);
+                        lo[j] = pack_f16x2(f0 - h.x, f1 - h.y);
                     }
-                    *reinterpret_cast<uint4*>(p.q_rot + at * D + m * (D / 2) + 8 * l) =
-                        make_uint4(out[0], out[1], out[2], out[3]);
+                    const size_t to = at * D + m * (D / 2) + 8 * l;
+                    *reinterpret_cast<uint4*>(p.q_rot + to) = make_uint4(hi[0], hi[1], hi[2], hi[3]);
+                    if (kRotated)
+                        *reinterpret_cast<uint4*>(p.q_lo + to) = make_uint4(lo[0], lo[1], lo[2], lo[3]);
                 }
                 if (l == 0) p.q_unit[at] = __int_as_float((127 - up) << 23);
                 continue;

@@ -175,7 +175,7 @@ def attention(c, arrays, causal=True, window=(-1, -1)):
     return O, LSE, dS, W
 
 
-def check(out, lse, ref, u_p, q_rounded, what=""):
+def check(out, lse, ref, u_p, rotated, what=""):
     """The kernels' O (bf16) and LSE against `attention`'s, within what their roundings allow.
 
     A logit is off by at most dS times (d 2^-23: the fp32 sums of d products, each rounded in the
@@ -190,7 +190,7 @@ def check(out, lse, ref, u_p, q_rounded, what=""):
     empty = ~np.isfinite(LSE)
     assert np.array_equal(np.isneginf(lse), empty), what
     assert np.all(out[empty] == 0.0), what
-    x = dS * (d * 2.0 ** -23 + (2.0 ** -11 if q_rounded else 0.0))
+    x = dS * (d * 2.0 ** -23 + (2.0 ** -20 if rotated else 0.0))
     p_err = np.expm1(2 * x) + u_p + 2.0 ** -20
     bound = 2.0 ** -8 * np.abs(O) + (1 + 2.0 ** -8) * p_err[..., None] * W
     err = np.abs(out - O)
