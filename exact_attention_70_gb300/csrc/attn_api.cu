@@ -882,10 +882,11 @@ size_t kv8_query_bytes(long long rows, int head_dim, int rotary_dim) {
 // head) and is spread over the whole GPU; the former pays for the staging and for a pass of 256
 // rows over all keys by one SM, whatever the rows, so it needs more of them where few (sequence,
 // kv head) pairs keep few SMs busy.  Measured, us (16-row kernel / staged):
-//   16 sequences x 8 kv heads, 8000 keys:   64 rows 187 / 299,  128 rows 352 / 304,  256 rows 666 / 329
-//   64 x 8, 1000 keys:                      64 rows 143 / 206,  128 rows 286 / 232
-//   4 x 8, 8000 keys:                      128 rows  96 / 141,  256 rows 179 / 172
-//   1 x 8, 16000 keys:                     512 rows 162 / 229, 1024 rows 308 / 235
+//   16 sequences x 8 kv heads, 8000 keys:   64 rows 220 / 243,  128 rows 412 / 243
+//   16 x 8, 2000 keys:                      64 rows  76 /  90,  128 rows 136 /  89
+//   64 x 8, 1000 keys:                      64 rows 161 / 169,  128 rows 320 / 179
+//   4 x 8, 8000 keys:                      128 rows 116 / 137,  256 rows 215 / 141
+//   1 x 8, 16000 keys:                     256 rows 111 / 189,  512 rows 200 / 187, 1024 rows 383 / 190
 bool kv8_staged(int batch, int max_seqlen_q, int nheads_q, int nheads_kv) {
     const long long rows = static_cast<long long>(max_seqlen_q) * (nheads_q / nheads_kv);
     const long long pairs = static_cast<long long>(batch) * nheads_kv;

@@ -44,8 +44,11 @@ struct Kv8Cfg {
     static constexpr int kOffMerge = kOffScale + kStages * 2 * kKv8Chunk;
     static constexpr int kMergeStride = D + 4;               // floats a row: [16][kMergeStride] of O,
     static constexpr int kMergeBytes = kKv8Rows * kMergeStride * 4 + 2 * 2 * 4 * kKv8Rows * 4;  // m, l
-    static constexpr int kOffQlo = kOffMerge + kMergeBytes;  // the unit's low query parts, as fragments
-    static constexpr int kOffBar = kOffQlo + D / 16 * 32 * 16;
+    // the unit's queries as MMA fragments [high, low][k-step][lane][4], where the merge is later
+    static constexpr int kOffQ = kOffMerge;
+    static constexpr int kQBytes = D / 16 * 32 * 16;
+    static_assert(2 * kQBytes <= kKv8Rows * kMergeStride * 4, "queries fit in the merge buffer's O");
+    static constexpr int kOffBar = kOffMerge + kMergeBytes;
     static constexpr int kSmem = kOffBar + 256 + 1024;
     static_assert(2 * (kSmem + 1024) <= 228 * 1024, "two CTAs per SM");
 };
@@ -312,7 +315,7 @@ __global__ void __launch_bounds__(kKv8Threads, 2)
     const int mi = lane >> 3, ri = lane & 7;  // ldmatrix: matrix id, row within matrix
     float* const mo = reinterpret_cast<float*>(smem + C::kOffMerge);   // [16 rows][kMergeStride]
     float* const ml_all = mo + kKv8Rows * C::kMergeStride;             // [parity][m, l][4][16]
-    const uint32_t qlo = smem_u32(smem + C::kOffQlo);
+    const uint32_t qs = smem_u32(smem + C::kOffQ) + lane * 16;  // this lane's fragments
     uint32_t n = 0;  // chunks consumed
     for (int seg = 0; w.next(p); ++seg) {
         const int Lq = w.s.Lq, L = w.s.L, q0 = w.s.q0, rows = w.rows, row0 = w.row0;
@@ -325,71 +328,67 @@ __global__ void __launch_bounds__(kKv8Threads, 2)
         // Q as the A operand.  An f16 k-step covers 16 elements of d; the thread's four k slots
         // {2 tq, 2 tq + 1, 2 tq + 8, 2 tq + 9} stand for elements 4 tq .. 4 tq + 3 of them, the
         // four bytes ldmatrix hands it of a key's 16.
-        uint32_t qa[D / 16][4];
+        // They are the same for all warps and stay in shared memory (in registers they cost spills):
+        // each warp brings a quarter of the k-steps.
         float c_row[2];
         int kmin[2], kmax[2];
+        size_t q_row[2];
 #pragma unroll
         for (int h = 0; h < 2; ++h) {
-            const int r = gq + 8 * h;
-            const int tok = (row0 + min(r, rows - 1)) / p.g, hd = (row0 + min(r, rows - 1)) % p.g;
-            const size_t row = static_cast<size_t>(q0 + tok) * p.Hq + kvh * p.g + hd;
+            const int r = row0 + min(gq + 8 * h, rows - 1), tok = r / p.g;
+            q_row[h] = static_cast<size_t>(q0 + tok) * p.Hq + kvh * p.g + r % p.g;
             row_key_interval(tok, Lq, L, p.causal, p.wl, p.wr, kmin[h], kmax[h]);
-            if (kLo) {  // rotated and scaled by the append kernel
-                const uint2* src = reinterpret_cast<const uint2*>(p.q_rot + row * D + 4 * tq);
-                c_row[h] = p.scale_log2 * p.q_unit[row];
+        }
+        const bool there[2] = {gq < rows, gq + 8 < rows};
+        const uint2 none = make_uint2(0u, 0u);
+        if (kLo) {  // rotated and scaled by the append kernel
+#pragma unroll
+            for (int h = 0; h < 2; ++h) c_row[h] = p.scale_log2 * p.q_unit[q_row[h]];
+            for (int s = warp; s < D / 16; s += 4) {
+#pragma unroll
+                for (int part = 0; part < 2; ++part) {
+                    const __half* src = (part ? p.q_lo : p.q_rot) + 16 * s + 4 * tq;
+                    uint2 x[2];
+#pragma unroll
+                    for (int h = 0; h < 2; ++h)
+                        x[h] = there[h] ? *reinterpret_cast<const uint2*>(src + q_row[h] * D) : none;
+                    st_shared_v4(qs + part * C::kQBytes + s * 512, x[0].x, x[1].x, x[0].y, x[1].y);
+                }
+            }
+        } else {
+            uint32_t mine[D / 64][4];  // this warp's k-steps
+#pragma unroll
+            for (int h = 0; h < 2; ++h) {
+                const uint2* src = reinterpret_cast<const uint2*>(p.q + q_row[h] * D + 4 * tq);
+                uint2 x[D / 16];
+                int top = 0;
 #pragma unroll
                 for (int s = 0; s < D / 16; ++s) {
-                    const uint2 x = r < rows ? src[4 * s] : make_uint2(0u, 0u);
-                    qa[s][h] = x.x;
-                    qa[s][h + 2] = x.y;
+                    x[s] = there[h] ? src[4 * s] : none;
+                    top = max(max(top, static_cast<int>(x[s].x & 0x7fff)),
+                              static_cast<int>((x[s].x >> 16) & 0x7fff));
+                    top = max(max(top, static_cast<int>(x[s].y & 0x7fff)),
+                              static_cast<int>((x[s].y >> 16) & 0x7fff));
                 }
-                continue;
-            }
-            const uint2* src = reinterpret_cast<const uint2*>(p.q + row * D + 4 * tq);
-            uint2 qw[D / 16];
-            int top = 0;
+                top = max(top, __shfl_xor_sync(0xffffffffu, top, 1));
+                top = max(top, __shfl_xor_sync(0xffffffffu, top, 2));
+                const int a = kv8_query_shift(top >> 7);
+                const float up = __int_as_float((a + 127) << 23);
+                c_row[h] = p.scale_log2 * __int_as_float((127 - a) << 23);
 #pragma unroll
-            for (int s = 0; s < D / 16; ++s) {
-                qw[s] = r < rows ? src[4 * s] : make_uint2(0u, 0u);
-                top = max(max(top, static_cast<int>(qw[s].x & 0x7fff)),
-                          static_cast<int>((qw[s].x >> 16) & 0x7fff));
-                top = max(max(top, static_cast<int>(qw[s].y & 0x7fff)),
-                          static_cast<int>((qw[s].y >> 16) & 0x7fff));
+                for (int s = 0; s < D / 16; ++s)
+                    if (s % 4 == warp) {
+                        mine[s / 4][h] = pack_f16x2(__uint_as_float(x[s].x << 16) * up,
+                                                    __uint_as_float(x[s].x & 0xffff0000u) * up);
+                        mine[s / 4][h + 2] = pack_f16x2(__uint_as_float(x[s].y << 16) * up,
+                                                        __uint_as_float(x[s].y & 0xffff0000u) * up);
+                    }
             }
-            top = max(top, __shfl_xor_sync(0xffffffffu, top, 1));
-            top = max(top, __shfl_xor_sync(0xffffffffu, top, 2));
-            const int a = kv8_query_shift(top >> 7);
-            const float up = __int_as_float((a + 127) << 23);
-            c_row[h] = p.scale_log2 * __int_as_float((127 - a) << 23);
 #pragma unroll
-            for (int s = 0; s < D / 16; ++s) {
-                qa[s][h] = pack_f16x2(__uint_as_float(qw[s].x << 16) * up,
-                                      __uint_as_float(qw[s].x & 0xffff0000u) * up);
-                qa[s][h + 2] = pack_f16x2(__uint_as_float(qw[s].y << 16) * up,
-                                          __uint_as_float(qw[s].y & 0xffff0000u) * up);
-            }
+            for (int i = 0; i < D / 64; ++i)
+                st_shared_v4(qs + (4 * i + warp) * 512, mine[i][0], mine[i][1], mine[i][2], mine[i][3]);
         }
-        if (kLo) {
-            // the low parts, the same for all warps: each brings its k-steps' fragments to shared
-            // memory (every warp is past the previous segment's last read of them: the merge's
-            // barriers lie between)
-#pragma unroll
-            for (int s = warp; s < D / 16; s += 4) {
-                uint2 x[2];
-#pragma unroll
-                for (int h = 0; h < 2; ++h) {
-                    const int r = min(gq + 8 * h, rows - 1);
-                    const int tok = (row0 + r) / p.g, hd = (row0 + r) % p.g;
-                    x[h] = gq + 8 * h < rows
-                               ? *reinterpret_cast<const uint2*>(
-                                     p.q_lo + (static_cast<size_t>(q0 + tok) * p.Hq + kvh * p.g + hd) * D +
-                                     16 * s + 4 * tq)
-                               : make_uint2(0u, 0u);
-                }
-                st_shared_v4(qlo + (s * 32 + lane) * 16, x[0].x, x[1].x, x[0].y, x[1].y);
-            }
-            named_bar_sync(1, 128);
-        }
+        named_bar_sync(1, 128);
         // keys every row of the unit sees: [full_lo, full_hi]
         int full_lo, full_hi;
         {
@@ -416,13 +415,14 @@ __global__ void __launch_bounds__(kKv8Threads, 2)
                 const int key = warp * 32 + (mi & 1) * 8 + ri;
 #pragma unroll
                 for (int u = 0; u < D / 16; u += 2) {
-                    uint32_t lo[2][4];
-                    if (kLo) {
+                    uint32_t qa[2][4], lo[2][4];
 #pragma unroll
-                        for (int i = 0; i < 2; ++i) {
-                            const uint4 f = ld_shared_v4(qlo + ((u + i) * 32 + lane) * 16);
-                            lo[i][0] = f.x, lo[i][1] = f.y, lo[i][2] = f.z, lo[i][3] = f.w;
-                        }
+                    for (int i = 0; i < 2; ++i) {
+                        uint4 f = ld_shared_v4(qs + (u + i) * 512);
+                        qa[i][0] = f.x, qa[i][1] = f.y, qa[i][2] = f.z, qa[i][3] = f.w;
+                        if (!kLo) continue;
+                        f = ld_shared_v4(qs + C::kQBytes + (u + i) * 512);
+                        lo[i][0] = f.x, lo[i][1] = f.y, lo[i][2] = f.z, lo[i][3] = f.w;
                     }
 #pragma unroll
                     for (int h = 0; h < 2; ++h) {
@@ -431,10 +431,10 @@ __global__ void __launch_bounds__(kKv8Threads, 2)
                                     r[2], r[3]);
 #pragma unroll
                         for (int i = 0; i < 4; ++i) e4m3x4_to_f16x2(r[i], b[2 * i], b[2 * i + 1]);
-                        mma_f16_16816(s[2 * h], qa[u], b[0], b[1]);
-                        mma_f16_16816(s[2 * h + 1], qa[u], b[2], b[3]);
-                        mma_f16_16816(s[2 * h], qa[u + 1], b[4], b[5]);
-                        mma_f16_16816(s[2 * h + 1], qa[u + 1], b[6], b[7]);
+                        mma_f16_16816(s[2 * h], qa[0], b[0], b[1]);
+                        mma_f16_16816(s[2 * h + 1], qa[0], b[2], b[3]);
+                        mma_f16_16816(s[2 * h], qa[1], b[4], b[5]);
+                        mma_f16_16816(s[2 * h + 1], qa[1], b[6], b[7]);
                         if (kLo) {
                             mma_f16_16816(s[2 * h], lo[0], b[0], b[1]);
                             mma_f16_16816(s[2 * h + 1], lo[0], b[2], b[3]);
@@ -660,6 +660,7 @@ __global__ void __launch_bounds__(kKv8Threads, 2)
             const int begin = bars->start + bars->count - w.left - (w.c1 - w.s.lo);
             p.meta[cta] = make_int4(begin / bars->share, q0, row0, rows);
         }
+        named_bar_sync(1, 128);  // the merge buffer has been read: the next segment's queries may come
     }
 }
 
