@@ -882,12 +882,13 @@ size_t kv8_query_bytes(long long rows, int head_dim, int rotary_dim) {
 // head) and is spread over the whole GPU; the former pays for the staging and for a pass of 256
 // rows over all keys by one SM, whatever the rows, so it needs more of them where few (sequence,
 // kv head) pairs keep few SMs busy.  Measured, us (16-row kernel / staged):
-//   16 sequences x 8 kv heads, 8000 keys:   64 rows 220 / 243,  128 rows 412 / 243
-//   16 x 8, 2000 keys:                      64 rows  76 /  90,  128 rows 136 /  89
-//   64 x 8, 1000 keys:                      64 rows 161 / 169,  128 rows 320 / 179
-//   4 x 8, 8000 keys:                      128 rows 116 / 137,  256 rows 215 / 141
-//   1 x 8, 16000 keys:                     256 rows 111 / 189,  512 rows 200 / 187, 1024 rows 383 / 190
+//   16 sequences x 8 kv heads, 8000 keys:   64 rows 188 / 243,  128 rows 354 / 242
+//   16 x 8, 2000 keys:                      64 rows  66 /  89,  128 rows 115 /  90
+//   64 x 8, 1000 keys:                      64 rows 137 / 168,  128 rows 272 / 179
+//   4 x 8, 8000 keys:                      128 rows  98 / 136,  256 rows 183 / 139
+//   1 x 8, 16000 keys:                     512 rows 172 / 186, 1024 rows 329 / 190
 bool kv8_staged(int batch, int max_seqlen_q, int nheads_q, int nheads_kv) {
+    if (nheads_q / nheads_kv > 128) return false;  // (more than the prefill kernel's tile packs)
     const long long rows = static_cast<long long>(max_seqlen_q) * (nheads_q / nheads_kv);
     const long long pairs = static_cast<long long>(batch) * nheads_kv;
     return rows > 112 && rows * pairs > 6144;
@@ -1107,7 +1108,6 @@ size_t attn_fwd_kvcache_fp8_workspace_bytes(int batch, int total_q, int max_seql
         kv8_sizes(batch, nheads_kv, head_dim, page_size, max_pages_per_seq, 1) != ATTN_OK)
         return 0;
     const bool staged = kv8_staged(batch, max_seqlen_q, nheads_q, nheads_kv);
-    if (staged && nheads_q / nheads_kv > 128) return 0;
     return (rotary_dim > 0 || staged
                 ? kv8_query_bytes(static_cast<long long>(total_q) * nheads_q, head_dim, rotary_dim)
                 : 0) +
@@ -1150,8 +1150,7 @@ attn_status_t attn_fwd_kvcache_fp8(const void* q, const void* k_new, const void*
     const int grid = staged ? 0
                             : kv8_grid(batch, max_seqlen_q, nheads_q, nheads_kv, page_size,
                                        max_pages_per_seq);
-    if (staged ? g > 128 || (static_cast<long long>(max_total_k) + 128LL * batch) * nheads_kv >
-                                (1LL << 31) - 1
+    if (staged ? (static_cast<long long>(max_total_k) + 128LL * batch) * nheads_kv > (1LL << 31) - 1
                : grid == 0)
         return ATTN_ERR_UNSUPPORTED;
     const size_t need = attn_fwd_kvcache_fp8_workspace_bytes(

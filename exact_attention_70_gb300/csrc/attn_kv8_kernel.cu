@@ -60,6 +60,7 @@ struct Kv8Bars {
     // the CTA's share of the work: chunks [start, start + count) of the list, the first of them
     // chunk first_off of sequence first_seq's; share: what every CTA but the last ones takes
     int first_seq, first_off, start, count, share;
+    int warp_sum[kKv8Threads / 32];
 };
 static_assert(sizeof(Kv8Bars) <= 256, "barrier block");
 
@@ -166,43 +167,45 @@ __global__ void __launch_bounds__(kKv8Threads, 2)
         bars->abort_flag = bars->fail[0] = bars->fail[1] = 0;
         mbar_fence_init();
     }
-    if (warp == 4) {  // the list's length, the share, and where this CTA's starts
-        int total = 0;
-        for (int b0 = 0; b0 < p.batch; b0 += 32) {
-            int n = 0;
-            if (b0 + lane < p.batch) {
-                const Kv8Seq s = kv8_seq(p, b0 + lane);
-                if (s.bad && cta == 0) atomicOr(p.status, kStatusBounds);
-                n = kv8_work(s);
-            }
+    // The list's length, the share, and where this CTA's starts: thread i sums the sequences
+    // [i per, (i + 1) per), the sums are scanned, and the thread in whose range the share starts
+    // finds the sequence.
+    {
+        const int per = (p.batch + kKv8Threads - 1) / kKv8Threads;
+        const int b0 = threadIdx.x * per, b1 = min(b0 + per, p.batch);
+        int mine = 0;
+        for (int b = b0; b < b1; ++b) {
+            const Kv8Seq s = kv8_seq(p, b);
+            if (s.bad && cta == 0) atomicOr(p.status, kStatusBounds);
+            mine += kv8_work(s);
+        }
+        int upto = mine;
 #pragma unroll
-            for (int o = 16; o > 0; o >>= 1) n += __shfl_xor_sync(0xffffffffu, n, o);
-            total += n;
+        for (int o = 1; o < 32; o <<= 1) {
+            const int x = __shfl_up_sync(0xffffffffu, upto, o);
+            if (lane >= o) upto += x;
+        }
+        if (lane == 31) bars->warp_sum[warp] = upto;
+        __syncthreads();
+        int total = 0, before = upto - mine;
+#pragma unroll
+        for (int i = 0; i < kKv8Threads / 32; ++i) {
+            if (i < warp) before += bars->warp_sum[i];
+            total += bars->warp_sum[i];
         }
         const int share = max((total - 1) / static_cast<int>(gridDim.x / p.Hkv) + 1, kKv8MinShare);
         const int start = static_cast<int>(min(static_cast<long long>(at_list) * share,
                                                static_cast<long long>(total)));
         const int count = min(share, total - start);
-        int before = 0;
-        for (int b0 = 0; count > 0 && b0 < p.batch; b0 += 32) {
-            const int n = b0 + lane < p.batch ? kv8_work(kv8_seq(p, b0 + lane)) : 0;
-            int upto = n;
-#pragma unroll
-            for (int o = 1; o < 32; o <<= 1) {
-                const int x = __shfl_up_sync(0xffffffffu, upto, o);
-                if (lane >= o) upto += x;
-            }
-            const int lo = before + upto - n;
-            if (lo <= start && start < lo + n) {
-                bars->first_seq = b0 + lane;
-                bars->first_off = start - lo;
-            }
-            before += __shfl_sync(0xffffffffu, upto, 31);
-            if (start < before) break;
+        if (count > 0 && before <= start && start < before + mine) {
+            int b = b0, off = start - before;
+            for (int n; off >= (n = kv8_work(kv8_seq(p, b))); ++b) off -= n;
+            bars->first_seq = b;
+            bars->first_off = off;
         }
-        if (lane == 0) {
-            bars->count = count;
+        if (threadIdx.x == 0) {
             bars->start = start;
+            bars->count = count;
             bars->share = share;
             // what kv8_combine_kernel finds of this CTA: nothing, until a segment ends a unit
             // that an earlier CTA started

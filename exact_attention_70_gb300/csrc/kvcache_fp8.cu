@@ -35,6 +35,14 @@ __device__ __forceinline__ int find_seq(const int* cu, int batch, int t) {
     return lo;
 }
 
+// One block's check that cu_seqlens describe rows of a packed tensor of `total` rows.
+__device__ __forceinline__ void check_offsets(const int* cu, int batch, int total, unsigned* status) {
+    bool ok = true;
+    for (int b = threadIdx.x; b < batch; b += blockDim.x)
+        ok = ok && 0 <= cu[b] && cu[b] <= cu[b + 1] && cu[b + 1] <= total;
+    if (!ok) atomicOr(status, kStatusBounds);
+}
+
 // a b - c d as one fp32 number, rounded to odd.
 __device__ __forceinline__ float det2_odd(float a, float b, float c, float d) {
     const float ph = __fmul_rn(a, b), pl = __fmaf_rn(a, b, -ph);
@@ -407,6 +415,7 @@ __global__ void __launch_bounds__(kAppendThreads, 5)
     __shared__ __align__(16) uint8_t stage[kAppendStages][kAppendThreads * 16 / D][kAppendRows][D * 2];
     __shared__ AppendToken place_of[kAppendTokens];
     griddep_launch_dependents();  // an attention kernel behind this one may set up
+    if (blockIdx.x == 0 && blockIdx.y == 0) check_offsets(p.cu_q, p.batch, p.total_q, p.status);
     if (blockIdx.y == kKeys)
         append_rows<D, kTurn, kKeys>(p, tokens, stage, place_of);
     else if (blockIdx.y == kValues)
@@ -522,6 +531,11 @@ __device__ __forceinline__ ReadToken read_token(const int* block_table, int b, i
                      static_cast<long long>(page) * Hkv * page_size + slot};
 }
 
+__device__ __forceinline__ void check_call(const ReadFp8Params& p) {
+    check_offsets(p.cu_k, p.batch, p.total_k, p.status);
+}
+__device__ __forceinline__ void check_call(const StageFp8Params&) {}  // (the append kernel's)
+
 __device__ __forceinline__ ReadToken place(const ReadFp8Params& p, int t, int& b) {
     b = find_seq(p.cu_k, p.batch, t);
     const int k0 = p.cu_k[b];
@@ -598,6 +612,7 @@ __global__ void __launch_bounds__(256)
     __shared__ ReadToken place_of[kReadTokens];
     __shared__ int seq_of[kReadTokens];
     const int t0 = blockIdx.x * tokens;
+    if (blockIdx.x == 0 && blockIdx.y == 0) check_call(p);
     if (threadIdx.x < tokens) {
         int b = 0;
         ReadToken r{-1, 0};

@@ -309,7 +309,9 @@ attn_status_t attn_quantize_fp8(const void* q, const void* k, const void* v,
  *   block_table       device int32 [batch, max_pages_per_seq], as for attn_decode_kvcache
  *   page_size         a multiple of 16 that divides 64 or is a multiple of 64
  *   head_dim          64 or 128
- * All four arrays are 16-byte aligned.  The caller owns every buffer; nothing is allocated.  A
+ * All four arrays are 16-byte aligned.  The caller owns every buffer; nothing is allocated;
+ * outputs and workspace must not overlap the inputs, and two calls that share a workspace must not
+ * overlap on the device.  A page that two sequences share is read by both; only one may write it.  A
  * page id outside [0, num_pages), a position past the table or the rotary tables, a negative
  * length, or cu_seqlens that leave the packed tensors raise ATTN_ERR_DEVICE_BOUNDS (read with
  * attn_get_device_status): what is written or read there is skipped, and the results of that

@@ -156,6 +156,8 @@ DECODE = [
     ([9000, 1, 0, 20000], 8, 4, 128, 192),                  # units cut into many parts
     ([100000], 2, 1, 64, 64),
     ([128 * (i % 3) for i in range(700)], 2, 1, 64, 64),    # many units a CTA, whole and cut
+    ([300, 9], 200, 1, 64, 16),                             # a group of 200 heads
+    ([50, 3], 400, 400, 64, 16),                            # more kv heads than CTAs
 ]
 
 
@@ -208,6 +210,7 @@ CHUNK = [
     ([50, 300, 900], [40, 90, 2], 30, 10, 64, 64, 0, False, False, (30, 7)),
     ([700, 5], [1, 100], 128, 2, 128, 192, 128, False, True, (64, -1)),
     ([0, 130], [400, 300], 16, 8, 128, 32, 96, False, True, (-1, -1)),
+    ([5], [40], 160, 1, 64, 16, 64, False, True, (-1, -1)),   # more heads a group than a tile packs
 ]
 
 
@@ -342,7 +345,11 @@ def test_bad_pages_and_lengths_are_reported(attn):
     for cu in ([0, 20, 90], [-4, 20, 23], [0, 23, 20]):                   # bad offsets
         c = kv8_case([100, 30], [20, 3], 4, 2, 64, 16, seed=134)
         c.cu_seqlens_q = torch.tensor(cu, dtype=torch.int32)
+        append(attn, c, gpu_cache(c))
+        assert status() == -6
         chunk(attn, c, gpu_cache(c))
+        assert status() == -6
+        attn.attn_kvcache_read_fp8(*gpu_cache(c), dev(c.block_table), dev(c.cu_seqlens_q), 23)
         assert status() == -6
 
 
