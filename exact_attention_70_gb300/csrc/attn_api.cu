@@ -1281,6 +1281,7 @@ attn_status_t attn_fwd_kvcache_fp8(const void* q, const void* k_new, const void*
             encode_3d(&fp.tm_qlo, ap.q_lo, head_dim, nheads_q, total_q, g, tpt) != ATTN_OK)
             return ATTN_ERR_CUDA;
         fp.hi_lo = ap.q_lo != nullptr ? 1 : 0;
+        fp.low_steps = rotary_dim / 16;
         fp.spans = sp.spans;
         fp.q_unit = ap.q_unit;
         fp.k_unit = sp.k_unit;

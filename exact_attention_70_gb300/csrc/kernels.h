@@ -95,6 +95,7 @@ struct FwdParams {
     const float* k_unit;  // [batch, Hkv]
     const float* v_unit;
     int hi_lo;
+    int low_steps;  // 16-component steps of q that have low parts
 };
 
 // ---- paged-cache append (chunked prefill) ---------------------------------------------------
