@@ -992,7 +992,7 @@ attn_status_t attn_kvcache_append_fp8(const void* k_new, const void* v_new, void
     ap.rot_dim = rotary_dim;
     ap.rot_rows = rotary_rows;
     ap.interleaved = rotary_interleaved ? 1 : 0;
-    if (launch_kvcache_append_fp8(ap, head_dim, static_cast<cudaStream_t>(stream)) != cudaSuccess)
+    if (launch_kvcache_append_fp8(ap, head_dim, false, static_cast<cudaStream_t>(stream)) != cudaSuccess)
         return ATTN_ERR_CUDA;
     return ATTN_OK;
 }
@@ -1198,13 +1198,38 @@ attn_status_t attn_fwd_kvcache_fp8(const void* q, const void* k_new, const void*
     ap.rot_dim = rotary_dim;
     ap.rot_rows = rotary_rows;
     ap.interleaved = rotary_interleaved ? 1 : 0;
-    if (launch_kvcache_append_fp8(ap, head_dim, s) != cudaSuccess) return ATTN_ERR_CUDA;
-
     if (staged) {
-        // 2. the keys and values the new tokens see, in f16
+        // 2. beside it (it needs the sequences' lengths only), the prefill kernel's work list
         const Kv8StageLayout l =
             kv8_stage_layout(batch, max_seqlen_q, max_total_k, nheads_q, nheads_kv, head_dim,
                              kv8_tiles(rotary_dim));
+        const int tpt = tokens_per_tile(g);
+        FwdWorkspaceHeader* header = reinterpret_cast<FwdWorkspaceHeader*>(ws + l.list);
+        FwdPrepParams pp;
+        memset(&pp, 0, sizeof(pp));
+        pp.cu_q = cu_seqlens_q;
+        pp.cache_seqlens = cache_seqlens;
+        pp.max_keys = max_pages_per_seq * page_size;
+        pp.prefix = reinterpret_cast<int*>(header + 1);
+        pp.items = reinterpret_cast<int4*>(reinterpret_cast<uint8_t*>(header + 1) +
+                                           align_up(sizeof(int) * (batch + 1), 16));
+        pp.header = header;
+        pp.status = dev->status;
+        pp.batch = batch;
+        pp.total_q = total_q;
+        pp.max_seqlen_q = max_seqlen_q;
+        pp.Hkv = nheads_kv;
+        pp.tpt = tpt;
+        pp.tiles = kv8_tiles(rotary_dim);
+        pp.capacity_pairs = static_cast<int>(l.items);
+        pp.causal = causal ? 1 : 0;
+        pp.wl = window_left;
+        pp.wr = window_right;
+        pp.heads_per_group = fwd_heads_per_group(max_total_k, nheads_kv, head_dim);
+        if (launch_fwd_prepare(pp, s) != cudaSuccess) return ATTN_ERR_CUDA;
+        if (launch_kvcache_append_fp8(ap, head_dim, true, s) != cudaSuccess) return ATTN_ERR_CUDA;
+
+        // 3. the keys and values the new tokens see, in f16
         StageFp8Params sp;
         memset(&sp, 0, sizeof(sp));
         sp.k_cache = ap.k_cache;
@@ -1230,30 +1255,7 @@ attn_status_t attn_fwd_kvcache_fp8(const void* q, const void* k_new, const void*
         sp.rows = static_cast<int>(l.rows);
         if (launch_kvcache_stage_fp8(sp, head_dim, s) != cudaSuccess) return ATTN_ERR_CUDA;
 
-        // 3. the prefill kernel on them
-        const int tpt = tokens_per_tile(g);
-        FwdWorkspaceHeader* header = reinterpret_cast<FwdWorkspaceHeader*>(ws + l.list);
-        FwdPrepParams pp;
-        memset(&pp, 0, sizeof(pp));
-        pp.cu_q = cu_seqlens_q;
-        pp.cache_seqlens = cache_seqlens;
-        pp.max_keys = max_pages_per_seq * page_size;
-        pp.prefix = reinterpret_cast<int*>(header + 1);
-        pp.items = reinterpret_cast<int4*>(reinterpret_cast<uint8_t*>(header + 1) +
-                                           align_up(sizeof(int) * (batch + 1), 16));
-        pp.header = header;
-        pp.status = dev->status;
-        pp.batch = batch;
-        pp.total_q = total_q;
-        pp.max_seqlen_q = max_seqlen_q;
-        pp.Hkv = nheads_kv;
-        pp.tpt = tpt;
-        pp.tiles = kv8_tiles(rotary_dim);
-        pp.capacity_pairs = static_cast<int>(l.items);
-        pp.causal = causal ? 1 : 0;
-        pp.wl = window_left;
-        pp.wr = window_right;
-        pp.heads_per_group = fwd_heads_per_group(max_total_k, nheads_kv, head_dim);
+        // 4. the prefill kernel on them
         FwdParams fp;
         memset(&fp, 0, sizeof(fp));
         if (encode_3d(&fp.tm_q, ap.q_rot, head_dim, nheads_q, total_q, g, tpt) != ATTN_OK ||
@@ -1286,10 +1288,11 @@ attn_status_t attn_fwd_kvcache_fp8(const void* q, const void* k_new, const void*
         fp.q_unit = ap.q_unit;
         fp.k_unit = sp.k_unit;
         fp.v_unit = sp.v_unit;
-        if (launch_fwd_prepare(pp, s) != cudaSuccess) return ATTN_ERR_CUDA;
         if (launch_fwd(fp, head_dim, dev->num_sms, s) != cudaSuccess) return ATTN_ERR_CUDA;
         return ATTN_OK;
     }
+
+    if (launch_kvcache_append_fp8(ap, head_dim, false, s) != cudaSuccess) return ATTN_ERR_CUDA;
 
     // 2. attention on the codes
     Kv8Params kp;

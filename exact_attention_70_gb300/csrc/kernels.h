@@ -279,7 +279,8 @@ struct Kv8Params {
     float scale_log2;
 };
 
-cudaError_t launch_kvcache_append_fp8(const AppendFp8Params& p, int head_dim, cudaStream_t stream);
+cudaError_t launch_kvcache_append_fp8(const AppendFp8Params& p, int head_dim, bool dependent,
+                                      cudaStream_t stream);
 cudaError_t launch_kvcache_read_fp8(const ReadFp8Params& p, int head_dim, cudaStream_t stream);
 cudaError_t launch_kvcache_stage_fp8(const StageFp8Params& p, int head_dim, cudaStream_t stream);
 cudaError_t launch_kv8_attn(const Kv8Params& p, int head_dim, int grid, bool after_append,

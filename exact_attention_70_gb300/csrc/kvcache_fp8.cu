@@ -422,6 +422,8 @@ __global__ void __launch_bounds__(kAppendThreads, 5)
         append_rows<D, kTurn, kValues>(p, tokens, stage, place_of);
     else
         append_rows<D, kTurn, kQueries>(p, tokens, stage, place_of);
+    griddep_wait();  // (attn_fwd_kvcache_fp8 builds its work list beside this grid; what waits for
+                     // this grid to finish then waits for the list too)
 }
 
 // ---- staging for the tensor-core prefill ----------------------------------------------------
@@ -451,6 +453,7 @@ __global__ void __launch_bounds__(kUnitsThreads)
     __shared__ long long sum[kWarps];
     const int b = blockIdx.x / p.Hkv, kvh = blockIdx.x % p.Hkv;
     const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+    griddep_launch_dependents();
     long long before = 0;
     for (int i = threadIdx.x; i < b; i += blockDim.x)
         before += (staged_keys(p, i).y + kFwdBlockN - 1) / kFwdBlockN * kFwdBlockN;
@@ -459,6 +462,7 @@ __global__ void __launch_bounds__(kUnitsThreads)
     if (lane == 0) sum[warp] = before;
     const int2 keys = staged_keys(p, b);
     int top[2] = {1, 1};  // scale bytes of K and V; 255 (NaN) does not count
+    griddep_wait();       // the append kernel's scales
     const int* bt = p.block_table + static_cast<size_t>(b) * p.max_pages;
     const int end = keys.x + keys.y;
     for (int g = keys.x / 16 + threadIdx.x; g * 16 < end; g += blockDim.x) {
@@ -612,6 +616,8 @@ __global__ void __launch_bounds__(256)
     __shared__ ReadToken place_of[kReadTokens];
     __shared__ int seq_of[kReadTokens];
     const int t0 = blockIdx.x * tokens;
+    griddep_launch_dependents();  // (staging: the prefill kernel may set up)
+    griddep_wait();               // (staging: the spans and units)
     if (blockIdx.x == 0 && blockIdx.y == 0) check_call(p);
     if (threadIdx.x < tokens) {
         int b = 0;
@@ -669,21 +675,37 @@ int read_tokens(int Hkv, int head_dim) {
     return n;
 }
 
+// `dependent`: may start once every CTA of the kernel before it on the stream has started; the
+// kernel waits for that grid itself (griddep_wait).
+template <typename... Params, typename... Args>
+cudaError_t launch(void (*kernel)(Params...), dim3 grid, int threads, bool dependent,
+                   cudaStream_t stream, const Args&... args) {
+    cudaLaunchConfig_t cfg = {};
+    cfg.gridDim = grid;
+    cfg.blockDim = dim3(threads);
+    cfg.stream = stream;
+    cudaLaunchAttribute attr[1];
+    attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+    attr[0].val.programmaticStreamSerializationAllowed = 1;
+    cfg.attrs = attr;
+    cfg.numAttrs = dependent ? 1 : 0;
+    return cudaLaunchKernelEx(&cfg, kernel, args...);
+}
+
 template <typename Params>
-cudaError_t launch_read(const Params& p, void* k, void* v, int rows, int head_dim, cudaStream_t stream) {
+cudaError_t launch_read(const Params& p, void* k, void* v, int rows, int head_dim, bool dependent,
+                        cudaStream_t stream) {
     const int tokens = read_tokens(p.Hkv, head_dim);
     const dim3 grid((rows + tokens - 1) / tokens, 2);
     uint16_t *ko = static_cast<uint16_t*>(k), *vo = static_cast<uint16_t*>(v);
-    if (head_dim == 128)
-        kvcache_read_fp8_kernel<128><<<grid, 256, 0, stream>>>(p, ko, vo, rows, tokens);
-    else
-        kvcache_read_fp8_kernel<64><<<grid, 256, 0, stream>>>(p, ko, vo, rows, tokens);
-    return cudaGetLastError();
+    return launch(head_dim == 128 ? kvcache_read_fp8_kernel<128, Params> : kvcache_read_fp8_kernel<64, Params>,
+                  grid, 256, dependent, stream, p, ko, vo, rows, tokens);
 }
 
 }  // namespace
 
-cudaError_t launch_kvcache_append_fp8(const AppendFp8Params& p, int head_dim, cudaStream_t stream) {
+cudaError_t launch_kvcache_append_fp8(const AppendFp8Params& p, int head_dim, bool dependent,
+                                      cudaStream_t stream) {
     if (p.total_q == 0) return cudaSuccess;
     // Single tokens spread over the GPU, about one step a group of lanes; prompts take up to 16
     // tokens a block.
@@ -697,27 +719,26 @@ cudaError_t launch_kvcache_append_fp8(const AppendFp8Params& p, int head_dim, cu
     const int turn = p.rot_dim == 0 ? kNoTurn
                      : p.rot_dim == head_dim && !p.interleaved ? kWholeTurn
                                                                : kAnyTurn;
-    const auto launch = [&](auto kernel) { kernel<<<grid, kAppendThreads, 0, stream>>>(p, tokens); };
-    if (head_dim == 128) {
-        if (turn == kNoTurn) launch(kvcache_append_fp8_kernel<128, kNoTurn>);
-        if (turn == kWholeTurn) launch(kvcache_append_fp8_kernel<128, kWholeTurn>);
-        if (turn == kAnyTurn) launch(kvcache_append_fp8_kernel<128, kAnyTurn>);
-    } else {
-        if (turn == kNoTurn) launch(kvcache_append_fp8_kernel<64, kNoTurn>);
-        if (turn == kWholeTurn) launch(kvcache_append_fp8_kernel<64, kWholeTurn>);
-        if (turn == kAnyTurn) launch(kvcache_append_fp8_kernel<64, kAnyTurn>);
-    }
-    return cudaGetLastError();
+    const auto go = [&](auto kernel) {
+        return launch(kernel, grid, kAppendThreads, dependent, stream, p, tokens);
+    };
+    if (head_dim == 128)
+        return turn == kNoTurn      ? go(kvcache_append_fp8_kernel<128, kNoTurn>)
+               : turn == kWholeTurn ? go(kvcache_append_fp8_kernel<128, kWholeTurn>)
+                                    : go(kvcache_append_fp8_kernel<128, kAnyTurn>);
+    return turn == kNoTurn      ? go(kvcache_append_fp8_kernel<64, kNoTurn>)
+           : turn == kWholeTurn ? go(kvcache_append_fp8_kernel<64, kWholeTurn>)
+                                : go(kvcache_append_fp8_kernel<64, kAnyTurn>);
 }
 
 cudaError_t launch_kvcache_stage_fp8(const StageFp8Params& p, int head_dim, cudaStream_t stream) {
-    kvcache_units_fp8_kernel<<<static_cast<unsigned>(p.batch) * p.Hkv, kUnitsThreads, 0, stream>>>(p);
-    const cudaError_t e = cudaGetLastError();
-    return e != cudaSuccess ? e : launch_read(p, p.k, p.v, p.rows, head_dim, stream);
+    const dim3 grid(static_cast<unsigned>(p.batch) * p.Hkv);
+    const cudaError_t e = launch(kvcache_units_fp8_kernel, grid, kUnitsThreads, true, stream, p);
+    return e != cudaSuccess ? e : launch_read(p, p.k, p.v, p.rows, head_dim, true, stream);
 }
 
 cudaError_t launch_kvcache_read_fp8(const ReadFp8Params& p, int head_dim, cudaStream_t stream) {
-    return p.total_k == 0 ? cudaSuccess : launch_read(p, p.k, p.v, p.total_k, head_dim, stream);
+    return p.total_k == 0 ? cudaSuccess : launch_read(p, p.k, p.v, p.total_k, head_dim, false, stream);
 }
 
 }  // namespace attn
