@@ -855,7 +855,7 @@ int kv8_grid(int batch, int max_seqlen_q, int nheads_q, int nheads_kv, int page_
     const long long groups =
         (static_cast<long long>(max_seqlen_q) * (nheads_q / nheads_kv) + kKv8Rows - 1) / kKv8Rows;
     const long long keys = static_cast<long long>(max_pages_per_seq) * page_size;
-    const long long chunks = (keys + kKv8Chunk - 1) / kKv8Chunk;
+    const long long chunks = (keys + kKv8Chunk - 1) / kKv8Chunk + kKv8SwitchChunks;
     const long long units = static_cast<long long>(batch) * groups;
     if (units > ((1LL << 31) - 1) / chunks) return 0;
     const long long cap = 2 * kGb300Sms / nheads_kv;

@@ -42,11 +42,12 @@ struct Kv8Cfg {
     static constexpr int kStages = D == 128 ? 3 : 6;
     static constexpr int kOffScale = kStages * kStageBytes;  // [stage][K, V][kKv8Chunk] scale bytes
     static constexpr int kOffMerge = kOffScale + kStages * 2 * kKv8Chunk;
-    static constexpr int kMergeStride = D + 4;               // floats a row: [16][kMergeStride] of O,
+    static constexpr int kMergeStride = D + 16;              // floats a row: [16][kMergeStride] of O,
     static constexpr int kMergeBytes = kKv8Rows * kMergeStride * 4 + 2 * 2 * 4 * kKv8Rows * 4;  // m, l
     // the unit's queries as MMA fragments [high, low][k-step][lane][4], where the merge is later
     static constexpr int kOffQ = kOffMerge;
     static constexpr int kQBytes = D / 16 * 32 * 16;
+    static_assert(4 * kKv8Rows * kMergeStride * 4 <= kOffScale, "a buffer a warp fits in the stages");
     static_assert(2 * kQBytes <= kKv8Rows * kMergeStride * 4, "queries fit in the merge buffer's O");
     static constexpr int kOffBar = kOffMerge + kMergeBytes;
     static constexpr int kSmem = kOffBar + 256 + 1024;
@@ -57,8 +58,8 @@ struct Kv8Bars {
     uint64_t full[6], empty[6];
     int abort_flag;
     int fail[2];       // a consumer warp gave up in a segment of this parity
-    // the CTA's share of the work: chunks [start, start + count) of the list, the first of them
-    // chunk first_off of sequence first_seq's; share: what every CTA but the last ones takes
+    // the CTA's share of the work: places [start, start + count) of the list, the first of them
+    // number first_off of sequence first_seq's; share: what every CTA but the last ones takes
     int first_seq, first_off, start, count, share;
     int warp_sum[kKv8Threads / 32];
 };
@@ -94,34 +95,42 @@ __device__ __forceinline__ Kv8Seq kv8_seq(const Kv8Params& p, int b) {
     return s;
 }
 
-// Its chunks (the host has made sure that the whole list counts in 31 bits).
-__device__ __forceinline__ int kv8_work(const Kv8Seq& s) { return s.ng * s.nc; }
+// Its places in the list: a unit's chunks and, behind them, kKv8SwitchChunks empty places for the
+// time that the merge and the next unit's start take (the host has made sure that the whole list
+// counts in 31 bits).
+__device__ __forceinline__ int kv8_work(const Kv8Seq& s) { return s.ng * (s.nc + kKv8SwitchChunks); }
 
 // The walk over a CTA's share: segments, each a run of chunks of one unit.
 struct Kv8Walk {
-    int left, off;  // chunks still to do; the next chunk's position inside sequence b
+    int left, off;  // places still to do; the next one's position inside sequence b
     int b;
     Kv8Seq s;
     int row0, rows, c0, c1;  // the current segment: chunks [c0, c1) of the sequence's list
     bool first, last;             // it holds its unit's first / last chunk
+    int before;                   // places of the share behind which the unit starts (negative: earlier)
 
-    __device__ __forceinline__ bool next(const Kv8Params& p) {
-        if (left <= 0) return false;
-        while (off >= kv8_work(s)) {
-            off = 0;
-            s = kv8_seq(p, ++b);
+    __device__ __forceinline__ bool next(const Kv8Params& p, int count) {
+        while (left > 0) {
+            while (off >= kv8_work(s)) {
+                off = 0;
+                s = kv8_seq(p, ++b);
+            }
+            const int places = s.nc + kKv8SwitchChunks;
+            const int unit = off / places, c = off - unit * places;
+            const int len = min(s.nc - c, left);  // not positive: at the unit's empty places
+            row0 = unit * kKv8Rows;
+            rows = min(kKv8Rows, s.Lq * p.g - row0);
+            c0 = s.lo + c;
+            c1 = c0 + len;
+            first = c == 0;
+            last = c + len == s.nc;
+            before = count - left - c;
+            const int taken = c + len < s.nc ? len : min(places - c, left);
+            off += taken;
+            left -= taken;
+            if (len > 0) return true;
         }
-        const int unit = off / s.nc, c = off - unit * s.nc;
-        const int len = min(s.nc - c, left);
-        row0 = unit * kKv8Rows;
-        rows = min(kKv8Rows, s.Lq * p.g - row0);
-        c0 = s.lo + c;
-        c1 = c0 + len;
-        first = c == 0;
-        last = c + len == s.nc;
-        off += len;
-        left -= len;
-        return true;
+        return false;
     }
 };
 
@@ -158,7 +167,10 @@ __global__ void __launch_bounds__(kKv8Threads, 2)
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
     const int cta = blockIdx.x, kvh = cta % p.Hkv, at_list = cta / p.Hkv;
     griddep_launch_dependents();
-
+    if (threadIdx.x == 128) {
+        tma_prefetch_desc(&p.tm_k);
+        tma_prefetch_desc(&p.tm_v);
+    }
     if (threadIdx.x == 0) {
         for (int i = 0; i < C::kStages; ++i) {
             mbar_init(&bars->full[i], 1);
@@ -214,24 +226,21 @@ __global__ void __launch_bounds__(kKv8Threads, 2)
     }
     __syncthreads();
     Kv8Walk w;
-    w.left = bars->count;
-    if (w.left == 0) return;
+    const int count = bars->count;
+    w.left = count;
     w.off = bars->first_off;
     w.b = bars->first_seq;
-    w.s = kv8_seq(p, w.b);
+    if (w.left > 0) w.s = kv8_seq(p, w.b);
     const Watchdog wd{&bars->abort_flag, p.status};
     griddep_wait();  // what the append kernel before this one wrote
+    if (w.left == 0) return;
 
     if (warp == 4) {
         // ---- producer: lane i gathers piece i of each chunk through block_table ----
-        if (lane == 0) {
-            tma_prefetch_desc(&p.tm_k);
-            tma_prefetch_desc(&p.tm_v);
-        }
         const int pieces = kKv8Chunk / p.box_rows;
         uint32_t issued = 0;
         bool ok = true;
-        while (ok && w.next(p)) {
+        while (ok && w.next(p, count)) {
             const int* bt = p.block_table + static_cast<size_t>(w.b) * p.max_pages;
             for (int c = w.c0; c < w.c1; ++c, ++issued) {
                 const uint32_t st = issued % C::kStages;
@@ -320,7 +329,7 @@ __global__ void __launch_bounds__(kKv8Threads, 2)
     float* const ml_all = mo + kKv8Rows * C::kMergeStride;             // [parity][m, l][4][16]
     const uint32_t qs = smem_u32(smem + C::kOffQ) + lane * 16;  // this lane's fragments
     uint32_t n = 0;  // chunks consumed
-    for (int seg = 0; w.next(p); ++seg) {
+    for (int seg = 0; w.next(p, count); ++seg) {
         const int Lq = w.s.Lq, L = w.s.L, q0 = w.s.q0, rows = w.rows, row0 = w.row0;
         float m_run[2] = {-INFINITY, -INFINITY};
         uint64_t l2[2] = {0, 0};  // the rows' denominators, even and odd keys apart
@@ -427,22 +436,27 @@ __global__ void __launch_bounds__(kKv8Threads, 2)
                         f = ld_shared_v4(qs + C::kQBytes + (u + i) * 512);
                         lo[i][0] = f.x, lo[i][1] = f.y, lo[i][2] = f.z, lo[i][3] = f.w;
                     }
+                    uint32_t b[2][8];
 #pragma unroll
                     for (int h = 0; h < 2; ++h) {
-                        uint32_t r[4], b[8];
+                        uint32_t r[4];
                         ldmatrix_x4(kbase + kv8_unit<D>(key + 16 * h, u + (mi >> 1)), r[0], r[1],
                                     r[2], r[3]);
 #pragma unroll
-                        for (int i = 0; i < 4; ++i) e4m3x4_to_f16x2(r[i], b[2 * i], b[2 * i + 1]);
-                        mma_f16_16816(s[2 * h], qa[0], b[0], b[1]);
-                        mma_f16_16816(s[2 * h + 1], qa[0], b[2], b[3]);
-                        mma_f16_16816(s[2 * h], qa[1], b[4], b[5]);
-                        mma_f16_16816(s[2 * h + 1], qa[1], b[6], b[7]);
+                        for (int i = 0; i < 4; ++i)
+                            e4m3x4_to_f16x2(r[i], b[h][2 * i], b[h][2 * i + 1]);
+                    }
+#pragma unroll
+                    for (int i = 0; i < 2; ++i) {
+#pragma unroll
+                        for (int nt = 0; nt < 4; ++nt)
+                            mma_f16_16816(s[nt], qa[i], b[nt >> 1][4 * i + 2 * (nt & 1)],
+                                          b[nt >> 1][4 * i + 2 * (nt & 1) + 1]);
                         if (kLo) {
-                            mma_f16_16816(s[2 * h], lo[0], b[0], b[1]);
-                            mma_f16_16816(s[2 * h + 1], lo[0], b[2], b[3]);
-                            mma_f16_16816(s[2 * h], lo[1], b[4], b[5]);
-                            mma_f16_16816(s[2 * h + 1], lo[1], b[6], b[7]);
+#pragma unroll
+                            for (int nt = 0; nt < 4; ++nt)
+                                mma_f16_16816(s[nt], lo[i], b[nt >> 1][4 * i + 2 * (nt & 1)],
+                                              b[nt >> 1][4 * i + 2 * (nt & 1) + 1]);
                         }
                     }
                 }
@@ -601,67 +615,80 @@ __global__ void __launch_bounds__(kKv8Threads, 2)
         // the same answer in all four warps: the flag of this parity was last written before the
         // barrier, and is written again only behind the next segment's barriers
         if (*reinterpret_cast<volatile int*>(&bars->fail[seg & 1])) return;
-        float sc[2];
+        const bool whole = w.first && w.last;
+        float sc[2];  // of the warp's O: 2^(m - M) 2^(E - 5) / l
 #pragma unroll
-        for (int r = 0; r < 2; ++r) {
-            float M = -INFINITY;
+        for (int h = 0; h < 2; ++h) {
+            const int r = gq + 8 * h;
+            float M = -INFINITY, lsum = 0.f;
 #pragma unroll
-            for (int i = 0; i < 4; ++i) M = fmaxf(M, mm[i * kKv8Rows + gq + 8 * r]);
-            if (M == -INFINITY) M = 0.f;
-            sc[r] = ex2_approx(m_run[r] - M) * (__int_as_float(e_run << 23) * 0x1p-5f);  // 2^(E - 5)
+            for (int i = 0; i < 4; ++i) M = fmaxf(M, mm[i * kKv8Rows + r]);
+            if (M == -INFINITY) M = 0.f;  // no key seen, or only NaN scores: l tells which
+#pragma unroll
+            for (int i = 0; i < 4; ++i) lsum += ml[i * kKv8Rows + r] * ex2_approx(mm[i * kKv8Rows + r] - M);
+            const float inv = lsum == 0.f ? 0.f : 1.f / lsum;
+            sc[h] = ex2_approx(m_run[h] - M) * inv * (__int_as_float(e_run << 23) * 0x1p-5f);
+            if (warp == 0 && tq == 0 && r < rows) {
+                const float lse = lsum == 0.f ? -INFINITY : M + __log2f(lsum);  // log2
+                const int tok = q0 + (row0 + r) / p.g, head = kvh * p.g + (row0 + r) % p.g;
+                if (!whole)
+                    p.part_lse[(2 * static_cast<size_t>(cta) + (w.first ? 1 : 0)) * kKv8Rows + r] = lse;
+                else if (ATTN_IN_BOUNDS(head < p.Hq && tok < p.total_q, p.status))
+                    p.lse[static_cast<size_t>(head) * p.lse_head + static_cast<size_t>(tok) * p.lse_tok] =
+                        lse * kLn2f;
+            }
         }
-        for (int turn = 0; turn < 4; ++turn) {
+        // Behind the last segment the stages are free, and each warp has a buffer there; before,
+        // the warps add to one buffer in turn.
+        const bool apart = w.left == 0;
+        float* const buf = apart ? reinterpret_cast<float*>(smem) : mo;
+        float* const own = buf + (apart ? warp * kKv8Rows * C::kMergeStride : 0);
+        for (int turn = apart ? warp : 0; turn < 4; ++turn) {
             if (turn == warp) {
 #pragma unroll
                 for (int u = 0; u < D / 16; ++u)
 #pragma unroll
                     for (int h = 0; h < 2; ++h) {
-                        float4* dst = reinterpret_cast<float4*>(mo + (gq + 8 * h) * C::kMergeStride +
+                        float4* dst = reinterpret_cast<float4*>(own + (gq + 8 * h) * C::kMergeStride +
                                                                 16 * u + 4 * tq);
                         float4 v = make_float4(o[2 * u][2 * h] * sc[h], o[2 * u + 1][2 * h] * sc[h],
                                                o[2 * u][2 * h + 1] * sc[h],
                                                o[2 * u + 1][2 * h + 1] * sc[h]);
-                        if (turn > 0) {
+                        if (!apart && turn > 0) {
                             const float4 a = *dst;
                             v = make_float4(a.x + v.x, a.y + v.y, a.z + v.z, a.w + v.w);
                         }
                         *dst = v;
                     }
             }
+            if (apart) break;
             named_bar_sync(1, 128);
         }
-        const bool whole = w.first && w.last;
-        for (int e = threadIdx.x; e < rows * (D / 4); e += 128) {
-            const int r = e / (D / 4), d = 4 * (e % (D / 4));
-            float M = -INFINITY, lsum = 0.f;
+        if (apart) named_bar_sync(1, 128);
 #pragma unroll
-            for (int i = 0; i < 4; ++i) M = fmaxf(M, mm[i * kKv8Rows + r]);
-            if (M == -INFINITY) M = 0.f;  // no key seen, or only NaN scores: l tells which
+        for (int i = 0; i < kKv8Rows * D / 4 / 128; ++i) {
+            const int e = threadIdx.x + 128 * i, r = e / (D / 4), d = 4 * (e % (D / 4));
+            if (r >= rows) break;
+            float4 v = *reinterpret_cast<const float4*>(buf + r * C::kMergeStride + d);
+            if (apart) {
 #pragma unroll
-            for (int i = 0; i < 4; ++i)
-                lsum += ml[i * kKv8Rows + r] * ex2_approx(mm[i * kKv8Rows + r] - M);
-            const float inv = lsum == 0.f ? 0.f : 1.f / lsum;
-            const float lse = lsum == 0.f ? -INFINITY : M + __log2f(lsum);  // log2
-            float4 v = *reinterpret_cast<const float4*>(mo + r * C::kMergeStride + d);
-            v = make_float4(v.x * inv, v.y * inv, v.z * inv, v.w * inv);
+                for (int j = 1; j < 4; ++j) {
+                    const float4 a = *reinterpret_cast<const float4*>(
+                        buf + (j * kKv8Rows + r) * C::kMergeStride + d);
+                    v = make_float4(v.x + a.x, v.y + a.y, v.z + a.z, v.w + a.w);
+                }
+            }
             const int tok = q0 + (row0 + r) / p.g, head = kvh * p.g + (row0 + r) % p.g;
             if (!ATTN_IN_BOUNDS(head < p.Hq && tok < p.total_q, p.status)) continue;
-            if (whole) {
+            if (whole)
                 *reinterpret_cast<uint2*>(p.out + (static_cast<size_t>(tok) * p.Hq + head) * D + d) =
                     make_uint2(pack_bf16x2(v.x, v.y), pack_bf16x2(v.z, v.w));
-                if (d == 0)
-                    p.lse[static_cast<size_t>(head) * p.lse_head + static_cast<size_t>(tok) * p.lse_tok] =
-                        lse * kLn2f;
-            } else {
-                const size_t at = (2 * static_cast<size_t>(cta) + (w.first ? 1 : 0)) * kKv8Rows + r;
-                *reinterpret_cast<float4*>(p.part_o + at * D + d) = v;
-                if (d == 0) p.part_lse[at] = lse;
-            }
+            else
+                *reinterpret_cast<float4*>(
+                    p.part_o + ((2 * static_cast<size_t>(cta) + (w.first ? 1 : 0)) * kKv8Rows + r) * D + d) = v;
         }
         if (w.last && !w.first && threadIdx.x == 0) {
-            // the unit started (c1 - lo) chunks before this segment's end
-            const int begin = bars->start + bars->count - w.left - (w.c1 - w.s.lo);
-            p.meta[cta] = make_int4(begin / bars->share, q0, row0, rows);
+            p.meta[cta] = make_int4((bars->start + w.before) / bars->share, q0, row0, rows);
         }
         named_bar_sync(1, 128);  // the merge buffer has been read: the next segment's queries may come
     }
@@ -682,31 +709,49 @@ __global__ void __launch_bounds__(kKv8Rows * 16) kv8_combine_kernel(const Kv8Par
     const auto part = [&](int s) {
         return (2 * (static_cast<size_t>(s) * p.Hkv + kvh) + (s == m.x ? 1 : 0)) * kKv8Rows + r;
     };
-    float M = -INFINITY;
-    bool nan = false;
-    for (int s = m.x; s <= last; ++s) {
-        const float x = p.part_lse[part(s)];
-        M = fmaxf(M, x);
-        nan = nan || x != x;
-    }
-    if (M == -INFINITY) M = 0.f;
-    if (nan) M = __int_as_float(0x7fffffff);
-    float sum = 0.f;
+    // One pass, four parts' loads in flight: the sums are kept relative to the running maximum.
+    float M = -INFINITY, sum = 0.f;
     float4 acc[D / 64];
 #pragma unroll
     for (int i = 0; i < D / 64; ++i) acc[i] = make_float4(0.f, 0.f, 0.f, 0.f);
-#pragma unroll 4
-    for (int s = m.x; s <= last; ++s) {
-        const size_t at = part(s);
-        const float wgt = ex2_approx(p.part_lse[at] - M);
-        sum += wgt;
+    for (int s0 = m.x; s0 <= last; s0 += 4) {
+        float x[4], top = M;
+        float4 v[4][D / 64];
+        bool nan = false;
 #pragma unroll
-        for (int i = 0; i < D / 64; ++i) {
-            const float4 v = *reinterpret_cast<const float4*>(p.part_o + at * D + d0 + 64 * i);
-            acc[i].x += wgt * v.x;
-            acc[i].y += wgt * v.y;
-            acc[i].z += wgt * v.z;
-            acc[i].w += wgt * v.w;
+        for (int j = 0; j < 4; ++j) {
+            const size_t at = part(min(s0 + j, last));
+            x[j] = p.part_lse[at];
+#pragma unroll
+            for (int i = 0; i < D / 64; ++i)
+                v[j][i] = *reinterpret_cast<const float4*>(p.part_o + at * D + d0 + 64 * i);
+        }
+#pragma unroll
+        for (int j = 0; j < 4; ++j) {
+            if (s0 + j > last) x[j] = -INFINITY;
+            nan = nan || x[j] != x[j];
+            top = fmaxf(top, x[j]);
+        }
+        if (top == -INFINITY) continue;  // no keys so far
+        if (nan) top = __int_as_float(0x7fffffff);
+        const float keep = ex2_approx(M - top);
+        M = top;
+        sum *= keep;
+#pragma unroll
+        for (int i = 0; i < D / 64; ++i)
+            acc[i] = make_float4(acc[i].x * keep, acc[i].y * keep, acc[i].z * keep, acc[i].w * keep);
+#pragma unroll
+        for (int j = 0; j < 4; ++j) {
+            const float wgt = ex2_approx(x[j] - M);
+            sum += wgt;
+            if (s0 + j > last) continue;
+#pragma unroll
+            for (int i = 0; i < D / 64; ++i) {
+                acc[i].x += wgt * v[j][i].x;
+                acc[i].y += wgt * v[j][i].y;
+                acc[i].z += wgt * v[j][i].z;
+                acc[i].w += wgt * v[j][i].w;
+            }
         }
     }
     const float inv = sum == 0.f ? 0.f : 1.f / sum;

@@ -252,6 +252,7 @@ constexpr int kKv8Chunk = 128;    // keys per pipeline stage
 constexpr int kKv8Threads = 160;  // 4 MMA warps + 1 TMA warp
 constexpr int kKv8Rows = 16;      // packed query rows of one CTA
 constexpr int kKv8MinShare = 2;   // chunks a CTA takes at least
+constexpr int kKv8SwitchChunks = 3;  // what the change from one unit to the next costs, in chunks
 
 struct Kv8Params {
     CUtensorMap tm_k;  // 3-D over the codes [num_pages * page_size, Hkv, d] u8, box {d, 1, box_rows}
