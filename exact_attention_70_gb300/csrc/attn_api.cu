@@ -882,11 +882,11 @@ size_t kv8_query_bytes(long long rows, int head_dim, int rotary_dim) {
 // head) and is spread over the whole GPU; the former pays for the staging and for a pass of 256
 // rows over all keys by one SM, whatever the rows, so it needs more of them where few (sequence,
 // kv head) pairs keep few SMs busy.  Measured, us (16-row kernel / staged):
-//   16 sequences x 8 kv heads, 8000 keys:   64 rows 188 / 243,  128 rows 354 / 242
-//   16 x 8, 2000 keys:                      64 rows  66 /  89,  128 rows 115 /  90
-//   64 x 8, 1000 keys:                      64 rows 137 / 168,  128 rows 272 / 179
-//   4 x 8, 8000 keys:                      128 rows  98 / 136,  256 rows 183 / 139
-//   1 x 8, 16000 keys:                     512 rows 172 / 186, 1024 rows 329 / 190
+//   16 sequences x 8 kv heads, 8000 keys:   64 rows 183 / 240,  128 rows 348 / 240
+//   16 x 8, 2000 keys:                      64 rows  60 /  86,  128 rows 107 /  86
+//   64 x 8, 1000 keys:                      64 rows 128 / 167,  128 rows 251 / 176
+//   4 x 8, 8000 keys:                      128 rows  94 / 133,  256 rows 177 / 137
+//   1 x 8, 16000 keys:                     512 rows 167 / 182, 1024 rows 320 / 187
 bool kv8_staged(int batch, int max_seqlen_q, int nheads_q, int nheads_kv) {
     if (nheads_q / nheads_kv > 128) return false;  // (more than the prefill kernel's tile packs)
     const long long rows = static_cast<long long>(max_seqlen_q) * (nheads_q / nheads_kv);

@@ -239,6 +239,11 @@ __device__ __forceinline__ AppendToken append_token(const AppendFp8Params& p, in
 // that rows of several kinds in one warp cost were a third of all instructions.  kTurn: no
 // rotation, the whole head in halves (a lane then has both partners and one set of table
 // entries), or any other.
+//
+// Measured: 16384 tokens of 8 kv heads, d 128, whole head rotated, 25 us, 4.4 TB/s of rows read and
+// codes written (a copy: 6.8), with start and end about 5 us of it; 64 single tokens 3.9 us, bound by
+// the chain lengths, page, table entries, rows.  Kinds mixed in one warp took 36 us, and two rows
+// straight into registers 40.
 constexpr int kKeys = 0, kValues = 1, kQueries = 2;
 
 template <int D, int kTurn, int kKind>
@@ -510,7 +515,9 @@ __global__ void __launch_bounds__(kUnitsThreads)
 //
 // Bound by memory: a byte in and two out per element.  A block takes a run of tokens' keys or
 // values (blockIdx.y); its first threads find the tokens' places (sequence, page), then every
-// thread moves 16 codes at a time, four loads in flight.
+// thread moves 16 codes at a time, four loads in flight.  158K tokens of 8 kv heads, d 128, to bf16:
+// 153 us, 6.35 TB/s read and written (keys and values by the same block: 166 us; a search per thread
+// instead of per token: 182).
 
 constexpr int kReadTokens = 128;  // tokens a block takes at most
 

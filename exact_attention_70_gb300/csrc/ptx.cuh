@@ -540,17 +540,6 @@ __device__ __forceinline__ uint32_t pack_e4m3x4(float a, float b, float c, float
     return r;
 }
 
-// Two e4m3 bytes (the low half of `codes`, low byte first) to f16x2, exactly.
-__device__ __forceinline__ uint32_t e4m3x2_to_f16x2(uint32_t codes) {
-    uint32_t r;
-    asm("{\n\t.reg .b16 lo, hi;\n\t"
-        "mov.b32 {lo, hi}, %1;\n\t"
-        "cvt.rn.f16x2.e4m3x2 %0, lo;\n\t}\n"
-        : "=r"(r)
-        : "r"(codes));
-    return r;
-}
-
 // Four e4m3 bytes to two f16x2, exactly.
 __device__ __forceinline__ void e4m3x4_to_f16x2(uint32_t codes, uint32_t& lo, uint32_t& hi) {
     asm("{\n\t.reg .b16 l, h;\n\t"
