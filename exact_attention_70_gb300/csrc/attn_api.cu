@@ -855,11 +855,11 @@ int kv8_grid(int batch, int max_seqlen_q, int nheads_q, int nheads_kv, int page_
     const long long groups =
         (static_cast<long long>(max_seqlen_q) * (nheads_q / nheads_kv) + kKv8Rows - 1) / kKv8Rows;
     const long long keys = static_cast<long long>(max_pages_per_seq) * page_size;
-    const long long chunks = (keys + kKv8Chunk - 1) / kKv8Chunk + kKv8SwitchChunks;
+    const long long places = (keys + kKv8Chunk - 1) / kKv8Chunk + kKv8SwitchChunks;  // of a unit
     const long long units = static_cast<long long>(batch) * groups;
-    if (units > ((1LL << 31) - 1) / chunks) return 0;
+    if (units > ((1LL << 31) - 1) / places) return 0;
     const long long cap = 2 * kGb300Sms / nheads_kv;
-    const long long n = (units * chunks + kKv8MinShare - 1) / kKv8MinShare;
+    const long long n = (units * places - kKv8SwitchChunks + kKv8MinShare - 1) / kKv8MinShare;
     return static_cast<int>(n < 1 || cap < 1 ? 1 : n < cap ? n : cap) * nheads_kv;
 }
 

@@ -215,6 +215,7 @@ __global__ void __launch_bounds__(kKv8Threads, 2)
             if (i < warp) before += bars->warp_sum[i];
             total += bars->warp_sum[i];
         }
+        total = max(total - kKv8SwitchChunks, 0);  // (no unit follows the last one)
         const int share = max((total - 1) / static_cast<int>(gridDim.x / p.Hkv) + 1, kKv8MinShare);
         const int start = static_cast<int>(min(static_cast<long long>(at_list) * share,
                                                static_cast<long long>(total)));
