@@ -558,6 +558,20 @@ def _kv8_sizes(k_cache, v_cache, k_scale, v_scale, block_table, batch):
     return num_pages, page_size, Hkv, d, max_pages
 
 
+def _int32(value, name):
+    """A size or bound that the library takes as a C int (ctypes would drop what is above it)."""
+    n = int(value)
+    if not -2 ** 31 <= n < 2 ** 31:
+        raise ValueError(f"{name} must fit 32 bits")
+    return n
+
+
+def _kv8_workspace(nbytes, device, workspace):
+    if workspace is not None and not workspace.is_contiguous():
+        raise ValueError("workspace must be contiguous")  # (its elements may share memory)
+    return _workspace(nbytes, device, workspace)
+
+
 def _rotary(rotary_cos, rotary_sin):
     """(cos address, sin address, rotary_dim, rows)."""
     if rotary_cos is None and rotary_sin is None:
@@ -676,7 +690,7 @@ def attn_decode_kvcache_fp8(q, k_cache, v_cache, k_scale, v_scale, cache_seqlens
     def body(s):
         o = torch.empty_like(q) if out is None else out
         l = torch.empty((batch, Hq), dtype=torch.float32, device=q.device) if lse is None else lse
-        ws = _workspace(nbytes, q.device, workspace)
+        ws = _kv8_workspace(nbytes, q.device, workspace)
         rc = lib.attn_decode_kvcache_fp8(qp, kc, vc, ks, vs, sl, bt, page_size, o.data_ptr(),
                                          l.data_ptr(), batch, Hq, Hkv, d, max_pages, num_pages,
                                          scale, _ptr(ws), nbytes, s)
@@ -722,9 +736,10 @@ def attn_fwd_kvcache_fp8(q, k_new, v_new, k_cache, v_cache, k_scale, v_scale, ca
     _maybe_at(lse, "lse", torch.float32, (Hq, total_q))
     index = _device(k_cache, v_cache, k_scale, v_scale, block_table, q, cu_seqlens_q, k_new, v_new,
                     cache_seqlens, rotary_cos, rotary_sin, out, lse, workspace)
-    max_q = int(max_seqlen_q)
+    max_q = _int32(max_seqlen_q, "max_seqlen_q")
     total_k = (min(batch * max_pages * page_size, 2 ** 31 - 1) if max_total_k is None
-               else int(max_total_k))
+               else _int32(max_total_k, "max_total_k"))
+    left, right = _int32(window_left, "window_left"), _int32(window_right, "window_right")
     scale = d ** -0.5 if softmax_scale is None else float(softmax_scale)
     nbytes = lib.attn_fwd_kvcache_fp8_workspace_bytes(batch, total_q, max_q, total_k, Hq, Hkv, d,
                                                       page_size, max_pages, rot_dim)
@@ -732,12 +747,12 @@ def attn_fwd_kvcache_fp8(q, k_new, v_new, k_cache, v_cache, k_scale, v_scale, ca
     def body(s):
         o = torch.empty_like(q) if out is None else out
         l = torch.empty((Hq, total_q), dtype=torch.float32, device=q.device) if lse is None else lse
-        ws = _workspace(nbytes, q.device, workspace)
+        ws = _kv8_workspace(nbytes, q.device, workspace)
         rc = lib.attn_fwd_kvcache_fp8(
             qp, kn, vn, kc, vc, ks, vs, sl, bt, cu, cos, sin, rot_dim, rot_rows,
             1 if rotary_interleaved else 0, o.data_ptr(), l.data_ptr(), batch, total_q, max_q,
             total_k, Hq, Hkv, d, page_size, max_pages, num_pages, scale, 1 if causal else 0,
-            int(window_left), int(window_right), _ptr(ws), nbytes, s)
+            left, right, _ptr(ws), nbytes, s)
         if rc != 0:
             raise AttnError(rc, "attn_fwd_kvcache_fp8")
         return o, l

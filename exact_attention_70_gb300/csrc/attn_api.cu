@@ -1058,7 +1058,8 @@ attn_status_t attn_decode_kvcache_fp8(const void* q, const void* k_cache, const 
     if (st != ATTN_OK) return st;
     if (nheads_q <= 0 || nheads_q % nheads_kv != 0 || !scale_ok(softmax_scale))
         return ATTN_ERR_INVALID_ARG;
-    if (static_cast<long long>(batch) * nheads_q > (1LL << 31) - 1) return ATTN_ERR_UNSUPPORTED;
+    if (nheads_q > 65535 || static_cast<long long>(batch) * nheads_q > (1LL << 31) - 1)
+        return ATTN_ERR_UNSUPPORTED;
     if (batch == 0) return ATTN_OK;
     if (!kv8_cache_ok(k_cache, v_cache, k_scale, v_scale, block_table) || !q || !cache_seqlens ||
         !out || !lse || !aligned(q, 16) || !aligned(out, 16) || !aligned(lse, 4) ||
@@ -1138,7 +1139,8 @@ attn_status_t attn_fwd_kvcache_fp8(const void* q, const void* k_new, const void*
         return ATTN_ERR_INVALID_ARG;
     st = rotary_ok(rotary_cos, rotary_sin, rotary_dim, rotary_rows, head_dim);
     if (st != ATTN_OK) return st;
-    if (static_cast<long long>(total_q) * nheads_q > (1LL << 29)) return ATTN_ERR_UNSUPPORTED;
+    if (nheads_q > 65535 || static_cast<long long>(total_q) * nheads_q > (1LL << 29))
+        return ATTN_ERR_UNSUPPORTED;
     if (batch == 0 || total_q == 0) return ATTN_OK;
     if (!kv8_cache_ok(k_cache, v_cache, k_scale, v_scale, block_table) || !q || !k_new || !v_new ||
         !cache_seqlens || !cu_seqlens_q || !out || !lse || !aligned(q, 16) || !aligned(k_new, 16) ||

@@ -208,7 +208,7 @@ __device__ __forceinline__ AppendToken append_token(const AppendFp8Params& p, in
     if (t >= p.total_q) return a;
     const int b = find_seq(p.cu_q, p.batch, t);
     const int q0 = p.cu_q[b], q1 = p.cu_q[b + 1], ctx = p.cache_seqlens[b];
-    if (t < q0 || t >= q1) return a;  // tokens outside every sequence are left alone
+    if (q0 < 0 || t < q0 || t >= q1) return a;  // tokens outside every sequence are left alone
     const long long pos = static_cast<long long>(ctx) + (t - q0);
     if (ctx >= 0 && pos < static_cast<long long>(p.max_pages) * p.page_size &&
         (p.rot_dim == 0 || pos < p.rot_rows)) {
@@ -550,7 +550,7 @@ __device__ __forceinline__ void check_call(const StageFp8Params&) {}  // (the ap
 __device__ __forceinline__ ReadToken place(const ReadFp8Params& p, int t, int& b) {
     b = find_seq(p.cu_k, p.batch, t);
     const int k0 = p.cu_k[b];
-    if (t < k0 || t >= p.cu_k[b + 1]) return ReadToken{-1, 0};  // outside every sequence
+    if (k0 < 0 || t < k0 || t >= p.cu_k[b + 1]) return ReadToken{-1, 0};  // outside every sequence
     return read_token(p.block_table, b, t - k0, p.page_size, p.max_pages, p.num_pages, p.Hkv,
                       p.status, -1);
 }

@@ -308,14 +308,15 @@ attn_status_t attn_quantize_fp8(const void* q, const void* k, const void* v,
  *   the maximum; an all-zero row gets b = 1.
  *   block_table       device int32 [batch, max_pages_per_seq], as for attn_decode_kvcache
  *   page_size         a multiple of 16 that divides 64 or is a multiple of 64
- *   head_dim          64 or 128
+ *   head_dim          64 or 128; at most 65535 sequences and heads
  * All four arrays are 16-byte aligned.  The caller owns every buffer; nothing is allocated;
  * outputs and workspace must not overlap the inputs, and two calls that share a workspace must not
  * overlap on the device.  A page that two sequences share is read by both; only one may write it.  A
  * page id outside [0, num_pages), a position past the table or the rotary tables, a negative
  * length, or cu_seqlens that leave the packed tensors raise ATTN_ERR_DEVICE_BOUNDS (read with
  * attn_get_device_status): what is written or read there is skipped, and the results of that
- * sequence are unspecified.
+ * sequence are unspecified (of the whole call where a chunk's length, cu_seqlens or max_seqlen_q is
+ * at fault).
  */
 
 /*
@@ -359,8 +360,9 @@ attn_status_t attn_kvcache_read_fp8(const void* k_cache, const void* v_cache, co
  *   cache_seqlens  device int32 [batch]; sequence b attends to its keys 0 .. cache_seqlens[b]-1
  *       (none: O = 0, LSE = -inf)
  *   workspace      attn_decode_kvcache_fp8_workspace_bytes(...) bytes, 256-byte aligned
- * The keys of all sequences are shared out evenly over the GPU; what is cut is merged.  The result is the attention of the stored values: the codes and the queries enter the tensor
- * cores exactly, the weights P with 11 significant bits.
+ * The keys of all sequences are shared out evenly over the GPU; what is cut is merged.  The result
+ * is the attention of the stored values: the codes and the queries enter the tensor cores exactly,
+ * the weights P with 11 significant bits.
  */
 attn_status_t attn_decode_kvcache_fp8(const void* q, const void* k_cache, const void* v_cache,
                                       const void* k_scale, const void* v_scale,

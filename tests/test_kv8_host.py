@@ -168,6 +168,16 @@ def test_chunk_refusals(lib):
     assert call(total=0) == 0
 
 
+def test_more_heads_than_the_kernels_index_are_refused(lib):
+    decode = lib.attn_decode_kvcache_fp8
+    assert decode(*[FAKE] * 7, 64, FAKE, FAKE, 0, 65535, 1, 128, 4, 16, 0.1, FAKE, 0, None) == 0
+    assert decode(*[FAKE] * 7, 64, FAKE, FAKE, 0, 65536, 1, 128, 4, 16, 0.1, FAKE, 0, None) == -2
+    chunk = lib.attn_fwd_kvcache_fp8
+    for heads, want in ((65535, 0), (65536, -2)):
+        assert chunk(*[FAKE] * 10, None, None, 0, 0, 0, FAKE, FAKE, 0, 16, 8, 64, heads, 1, 128, 64, 4, 16,
+                     0.1, 1, -1, -1, FAKE, 1 << 30, None) == want
+
+
 def test_binding_refuses_cpu_tensors_and_wrong_shapes(lib):
     c = kv8_exact.kv8_case([3], [2], 4, 2, 64, 16, seed=1)
     with pytest.raises(ValueError):
