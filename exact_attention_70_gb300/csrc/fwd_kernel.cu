@@ -40,9 +40,10 @@
 // two streams with their own maximum, denominator and O; the first stream merges them.
 // 8 chunks of 2048 tokens behind 2K to 16K keys, 32:8 heads, d 128: 1351 us with one part and two tiles
 // an item (1614 TFLOP/s); with two parts 2.09 ms, 1565 TFLOP/s of MMAs done, 1045 of what the formula
-// asks for, bound by the tensor cores under the power limit (1715 for a plain product that runs as
-// long).  One tile an item without the low part took 1.95 ms: K and V then pass through shared memory
-// for 128 rows only, which is as long as the low part's MMAs beside them.
+// asks for.  What bounds it are the bytes that one tile an item asks for, 64 KB of K and V for 128 rows
+// and a key block (7.5 TB/s out of L2 over all SMs; 1.95 ms without the low part's MMAs), and shared
+// memory right behind: per two blocks 576 KB of operands, P and arriving K and V, at 128 bytes a clock 4600
+// of the 4960 clocks taken.  A fourth slot in the ring gave 2%.
 #include <cuda_bf16.h>
 
 #include "kernels.h"
@@ -62,7 +63,7 @@ constexpr float kRescaleThreshold = 8.0f;  // log2 units
 constexpr float kLn2 = 0.69314718055994530942f;
 constexpr float kLog2e = 1.44269504088896340736f;
 
-template <int D>
+template <int D, int kOps = kBf16>
 struct FwdCfg {
     static constexpr int kHalves = D / 64;                 // 128-byte swizzle atoms along d
     static constexpr int kAtomBytes = 128 * 128;           // 128 rows x 128 B
@@ -81,6 +82,12 @@ struct FwdCfg {
     // TMEM columns of S_t (fp32) and O_t (fp32)
     __device__ static constexpr uint32_t col_s(int t) { return 128u * t; }
     __device__ static constexpr uint32_t col_o(int t) { return 256u + D * t; }
+    // kF16HiLo at d 64: P_t too (f16, two keys a column), where O_t leaves room.  One tile an item
+    // makes shared memory the tighter bound, and P passes through it twice otherwise (8 chunks of
+    // 2048 tokens, 8000 keys, 16:4 heads: 867 -> 820 us).  At d 128 it would lie over S_t, and S_t(j + 1)
+    // would wait for P_t(j)'s product (8 x 2048 tokens, 32:8 heads: 2290 -> 2322 us).
+    static constexpr bool kPInTmem = kOps == kF16HiLo && D == 64;
+    __device__ static constexpr uint32_t col_p(int t) { return 256u + 2 * D + 64u * t; }
 };
 
 struct FwdBars {
@@ -249,7 +256,7 @@ template <int D, bool kPaged, int kOps>
 __device__ void fwd_producer_loop(const FwdParams& p, uint8_t* smem, FwdBars* bars,
                                   const Watchdog& wd, int n_items, uint32_t& q_cnt,
                                   RingState& ring) {
-    using C = FwdCfg<D>;
+    using C = FwdCfg<D, kOps>;
     tma_prefetch_desc(&p.tm_q);
     tma_prefetch_desc(&p.tm_k);
     tma_prefetch_desc(&p.tm_v);
@@ -347,7 +354,7 @@ __device__ void fwd_producer_loop(const FwdParams& p, uint8_t* smem, FwdBars* ba
 template <int D, bool kPaged, int kOps>
 __device__ void fwd_producer(const FwdParams& p, uint8_t* smem, FwdBars* bars,
                              const Watchdog& wd, int n_items) {
-    using C = FwdCfg<D>;
+    using C = FwdCfg<D, kOps>;
     uint32_t q_cnt = 0;
     RingState ring;
     fwd_producer_loop<D, kPaged, kOps>(p, smem, bars, wd, n_items, q_cnt, ring);
@@ -368,7 +375,7 @@ __device__ void fwd_producer(const FwdParams& p, uint8_t* smem, FwdBars* bars,
 template <int D, bool kPaged, int kOps>
 __device__ void fwd_mma_s(const FwdParams& p, uint8_t* smem, FwdBars* bars, uint32_t tmem,
                           const Watchdog& wd, int n_items) {
-    using C = FwdCfg<D>;
+    using C = FwdCfg<D, kOps>;
     constexpr uint32_t kIdesc = is_f16(kOps) ? idesc_f16_f32(128, kFwdBlockN, false, false)
                                        : idesc_bf16_f32(128, kFwdBlockN, false, false);
     // K-major operand descriptors (128-byte swizzle, 8-row groups 1024 B apart), as halves
@@ -435,7 +442,7 @@ __device__ void fwd_mma_s(const FwdParams& p, uint8_t* smem, FwdBars* bars, uint
 template <int D, bool kPaged, int kOps>
 __device__ void fwd_mma_pv(const FwdParams& p, uint8_t* smem, FwdBars* bars, uint32_t tmem,
                            const Watchdog& wd, int n_items) {
-    using C = FwdCfg<D>;
+    using C = FwdCfg<D, kOps>;
     constexpr uint32_t kIdesc =
         is_f16(kOps) ? idesc_f16_f32(128, D, false, true) : idesc_bf16_f32(128, D, false, true);
     // A = P_t (K-major), B = V (MN-major: 64-wide d atoms kAtomBytes apart), as halves
@@ -474,8 +481,13 @@ __device__ void fwd_mma_pv(const FwdParams& p, uint8_t* smem, FwdBars* bars, uin
 #pragma unroll
                 for (int kk = 0; kk < kFwdBlockN / 16; ++kk) {
                     const uint32_t off = ((kk >> 2) * C::kAtomBytes + (kk & 3) * 32) >> 4;
-                    umma_ss_lh(tmem + C::col_o(t), a_lo + off, p_hi, b_lo + kk * (16 * 128 >> 4),
-                               v_hi, kIdesc, (first && kk == 0) ? 0u : 1u);
+                    if (C::kPInTmem)
+                        umma_ts(tmem + C::col_o(t), tmem + C::col_p(t) + 8 * kk,
+                                static_cast<uint64_t>(v_hi) << 32 | (b_lo + kk * (16 * 128 >> 4)), kIdesc,
+                                (first && kk == 0) ? 0u : 1u);
+                    else
+                        umma_ss_lh(tmem + C::col_o(t), a_lo + off, p_hi, b_lo + kk * (16 * 128 >> 4),
+                                   v_hi, kIdesc, (first && kk == 0) ? 0u : 1u);
                 }
                 umma_commit(&bars->pv_done[t]);
                 ++pc;
@@ -527,7 +539,7 @@ __device__ __forceinline__ uint32_t sw128_unit(uint32_t base, int r, int u) {
 template <int D, bool kPaged, bool kMods, int kOps>
 __device__ void fwd_softmax(const FwdParams& p, uint8_t* smem, FwdBars* bars, uint32_t tmem,
                             const Watchdog& wd, int n_items, int t, int k, int lane) {
-    using C = FwdCfg<D>;
+    using C = FwdCfg<D, kOps>;
     uint64_t* const s_full = &bars->s_full[t];
     uint64_t* const s_free = &bars->s_free[t];
     uint64_t* const p_full = &bars->p_full[t];
@@ -572,6 +584,15 @@ __device__ void fwd_softmax(const FwdParams& p, uint8_t* smem, FwdBars* bars, ui
     uint32_t blk = 0;  // blocks of tile t processed so far (== S_t consumed == P_t produced)
     uint32_t kv_cnt = 0;  // K/V ring slots filled for earlier items (locates paged V blocks)
     uint32_t vpar = 0;    // per-slot parity of the V blocks loaded for earlier items (paged)
+    // Waits until the previous item's O store has read P_t's shared memory.
+    const auto staging_free = [&]() {
+        if (k == 0 && lane == 0) {
+            bulk_wait_group_read_all();
+            mbar_arrive(epi_free);
+        }
+        epi_pending = false;
+        return __all_sync(0xffffffffu, wd.wait(epi_free, (epi_cnt - 1) & 1)) != 0;
+    };
     uint32_t merge_cnt = 0;  // items in which the second stream handed over its rows (kF16HiLo)
     for (uint32_t rd = 0;;) {
         const int idx = fwd_take_item_warp(bars, wd, rd, lane);
@@ -831,21 +852,24 @@ __device__ void fwd_softmax(const FwdParams& p, uint8_t* smem, FwdBars* bars, ui
                     tmem_wait_st();
                     tc_fence_before();
                 }
-                if (epi_pending) {
-                    // the previous item's O store out of P_t must have read it
-                    if (k == 0 && lane == 0) {
-                        bulk_wait_group_read_all();
-                        mbar_arrive(epi_free);
-                    }
-                    if (!__all_sync(0xffffffffu, wd.wait(epi_free, (epi_cnt - 1) & 1))) return;
-                    epi_pending = false;
-                }
-                // P_t rows of this warp: chunks (2 cp, 2 cp + 1) x (rows ra, ra + 8) per stmatrix
+                if constexpr (C::kPInTmem) {
+                    // P_t rows of this warp: column 4 c + lane % 4 holds the thread's two keys of
+                    // 8-key chunk c
+                    uint32_t pk[32];
 #pragma unroll
-                for (int cp = 0; cp < 8; ++cp)
-                    stmatrix_x4(st_addr[cp & 3] + (cp >> 2) * C::kAtomBytes, pka[2 * cp],
-                                pkb[2 * cp], pka[2 * cp + 1], pkb[2 * cp + 1]);
-                fence_proxy_async_smem();
+                    for (int c = 0; c < 16; ++c) pk[2 * c] = pka[c], pk[2 * c + 1] = pkb[c];
+                    tmem_st16x128_x16(tmem + (static_cast<uint32_t>(rbase) << 16) + C::col_p(t), pk);
+                    tmem_wait_st();
+                    tc_fence_before();
+                } else {
+                    if (epi_pending && !staging_free()) return;
+                    // P_t rows of this warp: chunks (2 cp, 2 cp + 1) x (rows ra, ra + 8) per stmatrix
+#pragma unroll
+                    for (int cp = 0; cp < 8; ++cp)
+                        stmatrix_x4(st_addr[cp & 3] + (cp >> 2) * C::kAtomBytes, pka[2 * cp],
+                                    pkb[2 * cp], pka[2 * cp + 1], pkb[2 * cp + 1]);
+                    fence_proxy_async_smem();
+                }
                 __syncwarp();
                 if (lane == 0) mbar_arrive(p_full);
                 ++blk;
@@ -896,6 +920,7 @@ __device__ void fwd_softmax(const FwdParams& p, uint8_t* smem, FwdBars* bars, ui
                     m_b = M_b;
                 }
             }
+            if (C::kPInTmem && epi_pending && !staging_free()) return;
             float inv_a = l_a > 0.f ? 1.f / l_a : 0.f;
             float inv_b = l_b > 0.f ? 1.f / l_b : 0.f;
             if constexpr (is_f16(kOps)) {
@@ -1036,7 +1061,7 @@ __device__ void fwd_softmax(const FwdParams& p, uint8_t* smem, FwdBars* bars, ui
 
 template <int D, bool kPaged, bool kMods, int kOps>
 __global__ void __launch_bounds__(kFwdThreads, 1) fwd_kernel(const __grid_constant__ FwdParams p) {
-    using C = FwdCfg<D>;
+    using C = FwdCfg<D, kOps>;
     extern __shared__ uint8_t smem_raw[];
     uint8_t* smem = reinterpret_cast<uint8_t*>(
         (reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~static_cast<uintptr_t>(1023));
