@@ -507,55 +507,103 @@ def _on(index, stream, body, *args):
         return body(stream.cuda_stream, *args)
 
 
-def _at(t, name, dtype, ndim):
-    """The address of a tensor argument (_check's conditions)."""
-    if type(t) is torch.Tensor and t.dtype is dtype and t.dim() == ndim and t.is_contiguous():
-        return t.data_ptr()  # (CPU tensors fail _device)
-    _check(t, name, dtype, ndim)
-    return t.data_ptr()
+_U8, _I32, _BF16, _F32 = torch.uint8, torch.int32, torch.bfloat16, torch.float32
+
+# Each call below asks all it wants to know of its tensors in one expression: a function call per
+# tensor was a third of a small call's time on the host.  What the expression does not accept goes
+# to _refuse.
+_WRONG = (AttributeError, TypeError, ValueError)  # of a None, another type, another number of dims
 
 
-def _maybe_at(t, name, dtype, shape):
-    """The same for an optional argument of a known shape."""
-    if t is None:
-        return None
+def _refuse(shapes, *args):
+    """Raise for the first of args, (tensor, name, dtype, dims), that is not a contiguous tensor of
+    its kind on the first one's CUDA device, or else for their sizes."""
+    for t, name, dtype, ndim in args:
+        _check(t, name, dtype, ndim)
+        if t.get_device() != args[0][0].get_device():
+            raise ValueError("all tensors must be on one CUDA device")
+    raise ValueError(shapes)
+
+
+def _kv8_sizes(k_cache, v_cache, k_scale, v_scale, block_table):
+    """(num_pages, page_size, Hkv, d, batch, max_pages, device index) of an 8-bit cache."""
+    try:
+        shape = k_cache.shape
+        num_pages, page_size, Hkv, d = shape
+        scales = (num_pages, Hkv, page_size)
+        batch, max_pages = block_table.shape
+        index = k_cache.get_device()
+        if (index >= 0 and k_cache.dtype is _U8 and v_cache.dtype is _U8 and k_scale.dtype is _U8
+                and v_scale.dtype is _U8 and block_table.dtype is _I32 and v_cache.shape == shape
+                and k_scale.shape == scales and v_scale.shape == scales
+                and k_cache.is_contiguous() and v_cache.is_contiguous()
+                and k_scale.is_contiguous() and v_scale.is_contiguous()
+                and block_table.is_contiguous()
+                and v_cache.get_device() == k_scale.get_device() == v_scale.get_device()
+                == block_table.get_device() == index):
+            return num_pages, page_size, Hkv, d, batch, max_pages, index
+    except _WRONG:
+        pass
+    _refuse("k_cache and v_cache must be [num_pages, page_size, Hkv, d], k_scale and v_scale "
+            "[num_pages, Hkv, page_size], block_table [batch, max_pages]",
+            (k_cache, "k_cache", _U8, 4), (v_cache, "v_cache", _U8, 4),
+            (k_scale, "k_scale", _U8, 3), (v_scale, "v_scale", _U8, 3),
+            (block_table, "block_table", _I32, 2))
+
+
+def _rotary(rotary_cos, rotary_sin, index):
+    """(cos address, sin address, rotary_dim, rows)."""
+    if rotary_cos is None and rotary_sin is None:
+        return None, None, 0, 0
+    try:
+        shape = rotary_cos.shape
+        rows, half = shape
+        if (rotary_cos.dtype is _F32 and rotary_sin.dtype is _F32 and rotary_sin.shape == shape
+                and rotary_cos.is_contiguous() and rotary_sin.is_contiguous()
+                and rotary_cos.get_device() == rotary_sin.get_device() == index):
+            return rotary_cos.data_ptr(), rotary_sin.data_ptr(), 2 * half, rows
+    except _WRONG:
+        pass
+    _refuse("rotary_cos and rotary_sin must both be [rows, rotary_dim / 2] on the cache's device",
+            (rotary_cos, "rotary_cos", _F32, 2), (rotary_sin, "rotary_sin", _F32, 2))
+
+
+def _new_tokens(k_new, v_new, cache_seqlens, cu_seqlens_q, batch, Hkv, d, index):
+    """The addresses of the new tokens' keys and values and of the lengths, and the tokens."""
+    try:
+        shape = k_new.shape
+        total_q, heads, dim = shape
+        if (heads == Hkv and dim == d and v_new.shape == shape and cache_seqlens.shape == (batch,)
+                and cu_seqlens_q.shape == (batch + 1,) and k_new.dtype is _BF16
+                and v_new.dtype is _BF16 and cache_seqlens.dtype is _I32
+                and cu_seqlens_q.dtype is _I32 and k_new.is_contiguous() and v_new.is_contiguous()
+                and cache_seqlens.is_contiguous() and cu_seqlens_q.is_contiguous()
+                and k_new.get_device() == v_new.get_device() == cache_seqlens.get_device()
+                == cu_seqlens_q.get_device() == index):
+            return (k_new.data_ptr(), v_new.data_ptr(), cache_seqlens.data_ptr(),
+                    cu_seqlens_q.data_ptr(), total_q)
+    except _WRONG:
+        pass
+    _refuse("k_new and v_new must be [total_q, Hkv, d] with the cache's Hkv and d, cache_seqlens "
+            "[batch] and cu_seqlens_q [batch + 1] with block_table's batch, on the cache's device",
+            (k_new, "k_new", _BF16, 3), (v_new, "v_new", _BF16, 3),
+            (cache_seqlens, "cache_seqlens", _I32, 1), (cu_seqlens_q, "cu_seqlens_q", _I32, 1))
+
+
+def _output(t, name, dtype, shape, index):
+    """Checks an output that the caller passes."""
+    _check(t, name, dtype, len(shape))
     if t.shape != shape:
         raise ValueError(f"{name} must be {list(shape)}")
-    return _at(t, name, dtype, len(shape))
+    if t.get_device() != index:
+        raise ValueError(f"{name} must be on the cache's device")
 
 
-def _device(first, *others):
-    """The index of the CUDA device that all the tensors are on."""
-    index = first.get_device()
-    for t in others:
-        if t is not None and t.get_device() != index:
-            raise ValueError("all tensors must be on one CUDA device")
-    if index < 0:
-        raise ValueError("all tensors must be CUDA tensors")
-    return index
-
-
-def _kv8_at(k_cache, v_cache, k_scale, v_scale, block_table):
-    """The addresses of what describes the 8-bit cache."""
-    u8 = torch.uint8
-    return (_at(k_cache, "k_cache", u8, 4), _at(v_cache, "v_cache", u8, 4),
-            _at(k_scale, "k_scale", u8, 3), _at(v_scale, "v_scale", u8, 3),
-            _at(block_table, "block_table", torch.int32, 2))
-
-
-def _kv8_sizes(k_cache, v_cache, k_scale, v_scale, block_table, batch):
-    """The sizes the calls on the 8-bit cache share: (num_pages, page_size, Hkv, d, max_pages)."""
-    shape = k_cache.shape
-    num_pages, page_size, Hkv, d = shape
-    if v_cache.shape != shape:
-        raise ValueError("k_cache and v_cache must both be [num_pages, page_size, Hkv, d]")
-    shape = k_scale.shape
-    if shape != (num_pages, Hkv, page_size) or v_scale.shape != shape:
-        raise ValueError("k_scale and v_scale must both be [num_pages, Hkv, page_size]")
-    rows, max_pages = block_table.shape
-    if rows != batch:
-        raise ValueError("block_table must have one row per sequence")
-    return num_pages, page_size, Hkv, d, max_pages
+def _kv8_workspace(nbytes, device, workspace):
+    if workspace is not None and not (workspace.is_contiguous() and workspace.device == device):
+        # (the elements of one that is not contiguous may share memory)
+        raise ValueError("workspace must be contiguous and on the cache's device")
+    return _workspace(nbytes, device, workspace)
 
 
 def _int32(value, name):
@@ -564,38 +612,6 @@ def _int32(value, name):
     if not -2 ** 31 <= n < 2 ** 31:
         raise ValueError(f"{name} must fit 32 bits")
     return n
-
-
-def _kv8_workspace(nbytes, device, workspace):
-    if workspace is not None and not workspace.is_contiguous():
-        raise ValueError("workspace must be contiguous")  # (its elements may share memory)
-    return _workspace(nbytes, device, workspace)
-
-
-def _rotary(rotary_cos, rotary_sin):
-    """(cos address, sin address, rotary_dim, rows)."""
-    if rotary_cos is None and rotary_sin is None:
-        return None, None, 0, 0
-    cos = _at(rotary_cos, "rotary_cos", torch.float32, 2)
-    sin = _at(rotary_sin, "rotary_sin", torch.float32, 2)
-    shape = rotary_cos.shape
-    rows, half = shape
-    if rotary_sin.shape != shape:
-        raise ValueError("rotary_cos and rotary_sin must both be [rows, rotary_dim / 2]")
-    return cos, sin, 2 * half, rows
-
-
-def _new_tokens(k_new, v_new, cache_seqlens, batch, Hkv, d):
-    """The addresses of the new keys and values and of cache_seqlens, and the tokens."""
-    at = (_at(k_new, "k_new", torch.bfloat16, 3), _at(v_new, "v_new", torch.bfloat16, 3),
-          _at(cache_seqlens, "cache_seqlens", torch.int32, 1))
-    shape = k_new.shape
-    total_q = shape[0]
-    if shape[1:] != (Hkv, d) or v_new.shape != shape:
-        raise ValueError("k_new and v_new must both be [total_q, Hkv, d] with the cache's Hkv and d")
-    if cache_seqlens.numel() != batch:
-        raise ValueError("cache_seqlens must have one entry per sequence")
-    return *at, total_q
 
 
 def attn_kvcache_append_fp8(k_new, v_new, k_cache, v_cache, k_scale, v_scale, cache_seqlens,
@@ -608,19 +624,16 @@ def attn_kvcache_append_fp8(k_new, v_new, k_cache, v_cache, k_scale, v_scale, ca
     cache_seqlens[b] + i.  rotary_cos / rotary_sin fp32 [rows, rotary_dim / 2] or None.
     """
     lib = load()
-    kc, vc, ks, vs, bt = _kv8_at(k_cache, v_cache, k_scale, v_scale, block_table)
-    cu = _at(cu_seqlens_q, "cu_seqlens_q", torch.int32, 1)
-    batch = cu_seqlens_q.numel() - 1
-    num_pages, page_size, Hkv, d, max_pages = _kv8_sizes(k_cache, v_cache, k_scale, v_scale,
-                                                         block_table, batch)
-    kn, vn, sl, total_q = _new_tokens(k_new, v_new, cache_seqlens, batch, Hkv, d)
-    cos, sin, rot_dim, rot_rows = _rotary(rotary_cos, rotary_sin)
-    index = _device(k_cache, v_cache, k_scale, v_scale, block_table, cu_seqlens_q, k_new, v_new,
-                    cache_seqlens, rotary_cos, rotary_sin)
+    num_pages, page_size, Hkv, d, batch, max_pages, index = _kv8_sizes(
+        k_cache, v_cache, k_scale, v_scale, block_table)
+    kn, vn, sl, cu, total_q = _new_tokens(k_new, v_new, cache_seqlens, cu_seqlens_q, batch, Hkv, d,
+                                          index)
+    cos, sin, rot_dim, rot_rows = _rotary(rotary_cos, rotary_sin, index)
 
     def body(s):
         return lib.attn_kvcache_append_fp8(
-            kn, vn, kc, vc, ks, vs, sl, bt, cu, cos, sin, rot_dim, rot_rows,
+            kn, vn, k_cache.data_ptr(), v_cache.data_ptr(), k_scale.data_ptr(), v_scale.data_ptr(),
+            sl, block_table.data_ptr(), cu, cos, sin, rot_dim, rot_rows,
             1 if rotary_interleaved else 0, batch, total_q, Hkv, d, page_size, max_pages,
             num_pages, s)
 
@@ -634,22 +647,30 @@ def attn_kvcache_read_fp8(k_cache, v_cache, k_scale, v_scale, block_table, cu_se
     """Read the first cu_seqlens_k[b + 1] - cu_seqlens_k[b] tokens of every sequence of the 8-bit
     cache back.  Returns (k, v), bf16 [total_k, Hkv, d], packed as attn_fwd takes them."""
     lib = load()
-    kc, vc, ks, vs, bt = _kv8_at(k_cache, v_cache, k_scale, v_scale, block_table)
-    cu = _at(cu_seqlens_k, "cu_seqlens_k", torch.int32, 1)
-    batch = cu_seqlens_k.numel() - 1
-    num_pages, page_size, Hkv, d, max_pages = _kv8_sizes(k_cache, v_cache, k_scale, v_scale,
-                                                         block_table, batch)
-    shape = (int(total_k), Hkv, d)
-    _maybe_at(k, "k", torch.bfloat16, shape)
-    _maybe_at(v, "v", torch.bfloat16, shape)
-    index = _device(k_cache, v_cache, k_scale, v_scale, block_table, cu_seqlens_k, k, v)
+    num_pages, page_size, Hkv, d, batch, max_pages, index = _kv8_sizes(
+        k_cache, v_cache, k_scale, v_scale, block_table)
+    try:
+        ok = (cu_seqlens_k.shape == (batch + 1,) and cu_seqlens_k.dtype is _I32
+              and cu_seqlens_k.is_contiguous() and cu_seqlens_k.get_device() == index)
+    except _WRONG:
+        ok = False
+    if not ok:
+        _refuse("cu_seqlens_k must be [batch + 1] with block_table's batch, on the cache's device",
+                (cu_seqlens_k, "cu_seqlens_k", _I32, 1))
+    shape = (_int32(total_k, "total_k"), Hkv, d)
+    if k is not None:
+        _output(k, "k", _BF16, shape, index)
+    if v is not None:
+        _output(v, "v", _BF16, shape, index)
 
     def body(s):
         device = k_cache.device
-        ko = torch.empty(shape, dtype=torch.bfloat16, device=device) if k is None else k
-        vo = torch.empty(shape, dtype=torch.bfloat16, device=device) if v is None else v
-        rc = lib.attn_kvcache_read_fp8(kc, vc, ks, vs, bt, cu, ko.data_ptr(), vo.data_ptr(), batch,
-                                       shape[0], Hkv, d, page_size, max_pages, num_pages, s)
+        ko = torch.empty(shape, dtype=_BF16, device=device) if k is None else k
+        vo = torch.empty(shape, dtype=_BF16, device=device) if v is None else v
+        rc = lib.attn_kvcache_read_fp8(
+            k_cache.data_ptr(), v_cache.data_ptr(), k_scale.data_ptr(), v_scale.data_ptr(),
+            block_table.data_ptr(), cu_seqlens_k.data_ptr(), ko.data_ptr(), vo.data_ptr(), batch,
+            shape[0], Hkv, d, page_size, max_pages, num_pages, s)
         if rc != 0:
             raise AttnError(rc, "attn_kvcache_read_fp8")
         return ko, vo
@@ -670,30 +691,37 @@ def attn_decode_kvcache_fp8(q, k_cache, v_cache, k_scale, v_scale, cache_seqlens
     Returns (out [batch, Hq, d] bf16, lse [batch, Hq] fp32).
     """
     lib = load()
-    kc, vc, ks, vs, bt = _kv8_at(k_cache, v_cache, k_scale, v_scale, block_table)
-    qp = _at(q, "q", torch.bfloat16, 3)
-    sl = _at(cache_seqlens, "cache_seqlens", torch.int32, 1)
-    batch, Hq, dq = q.shape
-    num_pages, page_size, Hkv, d, max_pages = _kv8_sizes(k_cache, v_cache, k_scale, v_scale,
-                                                         block_table, batch)
-    if dq != d:
-        raise ValueError("q must have the cache's head dimension")
-    if cache_seqlens.numel() != batch:
-        raise ValueError("cache_seqlens must have one entry per sequence")
-    _maybe_at(out, "out", torch.bfloat16, (batch, Hq, d))
-    _maybe_at(lse, "lse", torch.float32, (batch, Hq))
-    index = _device(k_cache, v_cache, k_scale, v_scale, block_table, q, cache_seqlens, out, lse,
-                    workspace)
+    num_pages, page_size, Hkv, d, batch, max_pages, index = _kv8_sizes(
+        k_cache, v_cache, k_scale, v_scale, block_table)
+    try:
+        rows, Hq, dim = q.shape
+        ok = (rows == batch and dim == d and cache_seqlens.shape == (batch,) and q.dtype is _BF16
+              and cache_seqlens.dtype is _I32 and q.is_contiguous()
+              and cache_seqlens.is_contiguous()
+              and q.get_device() == cache_seqlens.get_device() == index)
+    except _WRONG:
+        ok = False
+    if not ok:
+        _refuse("q must be [batch, Hq, d] with the cache's d and block_table's batch, cache_seqlens "
+                "[batch], on the cache's device",
+                (q, "q", _BF16, 3), (cache_seqlens, "cache_seqlens", _I32, 1))
+    if out is not None:
+        _output(out, "out", _BF16, (batch, Hq, d), index)
+    if lse is not None:
+        _output(lse, "lse", _F32, (batch, Hq), index)
     scale = d ** -0.5 if softmax_scale is None else float(softmax_scale)
     nbytes = lib.attn_decode_kvcache_fp8_workspace_bytes(batch, Hq, Hkv, d, page_size, max_pages)
 
     def body(s):
+        device = q.device
         o = torch.empty_like(q) if out is None else out
-        l = torch.empty((batch, Hq), dtype=torch.float32, device=q.device) if lse is None else lse
-        ws = _kv8_workspace(nbytes, q.device, workspace)
-        rc = lib.attn_decode_kvcache_fp8(qp, kc, vc, ks, vs, sl, bt, page_size, o.data_ptr(),
-                                         l.data_ptr(), batch, Hq, Hkv, d, max_pages, num_pages,
-                                         scale, _ptr(ws), nbytes, s)
+        l = torch.empty((batch, Hq), dtype=_F32, device=device) if lse is None else lse
+        ws = _kv8_workspace(nbytes, device, workspace)
+        rc = lib.attn_decode_kvcache_fp8(
+            q.data_ptr(), k_cache.data_ptr(), v_cache.data_ptr(), k_scale.data_ptr(),
+            v_scale.data_ptr(), cache_seqlens.data_ptr(), block_table.data_ptr(), page_size,
+            o.data_ptr(), l.data_ptr(), batch, Hq, Hkv, d, max_pages, num_pages, scale, _ptr(ws),
+            nbytes, s)
         if rc != 0:
             raise AttnError(rc, "attn_decode_kvcache_fp8")
         return o, l
@@ -721,21 +749,24 @@ def attn_fwd_kvcache_fp8(q, k_new, v_new, k_cache, v_cache, k_scale, v_scale, ca
     what block_table can hold).  Returns (out [total_q, Hq, d], lse [Hq, total_q]).
     """
     lib = load()
-    kc, vc, ks, vs, bt = _kv8_at(k_cache, v_cache, k_scale, v_scale, block_table)
-    qp = _at(q, "q", torch.bfloat16, 3)
-    cu = _at(cu_seqlens_q, "cu_seqlens_q", torch.int32, 1)
-    batch = cu_seqlens_q.numel() - 1
-    num_pages, page_size, Hkv, d, max_pages = _kv8_sizes(k_cache, v_cache, k_scale, v_scale,
-                                                         block_table, batch)
-    kn, vn, sl, total_q = _new_tokens(k_new, v_new, cache_seqlens, batch, Hkv, d)
-    Hq = q.shape[1]
-    if q.shape != (total_q, Hq, d):
-        raise ValueError("q, k_new and v_new must have the same tokens and head dimension")
-    cos, sin, rot_dim, rot_rows = _rotary(rotary_cos, rotary_sin)
-    _maybe_at(out, "out", torch.bfloat16, (total_q, Hq, d))
-    _maybe_at(lse, "lse", torch.float32, (Hq, total_q))
-    index = _device(k_cache, v_cache, k_scale, v_scale, block_table, q, cu_seqlens_q, k_new, v_new,
-                    cache_seqlens, rotary_cos, rotary_sin, out, lse, workspace)
+    num_pages, page_size, Hkv, d, batch, max_pages, index = _kv8_sizes(
+        k_cache, v_cache, k_scale, v_scale, block_table)
+    kn, vn, sl, cu, total_q = _new_tokens(k_new, v_new, cache_seqlens, cu_seqlens_q, batch, Hkv, d,
+                                          index)
+    try:
+        rows, Hq, dim = q.shape
+        ok = (rows == total_q and dim == d and q.dtype is _BF16 and q.is_contiguous()
+              and q.get_device() == index)
+    except _WRONG:
+        ok = False
+    if not ok:
+        _refuse("q must be [total_q, Hq, d] with k_new's tokens and d, on the cache's device",
+                (q, "q", _BF16, 3))
+    cos, sin, rot_dim, rot_rows = _rotary(rotary_cos, rotary_sin, index)
+    if out is not None:
+        _output(out, "out", _BF16, (total_q, Hq, d), index)
+    if lse is not None:
+        _output(lse, "lse", _F32, (Hq, total_q), index)
     max_q = _int32(max_seqlen_q, "max_seqlen_q")
     total_k = (min(batch * max_pages * page_size, 2 ** 31 - 1) if max_total_k is None
                else _int32(max_total_k, "max_total_k"))
@@ -745,11 +776,13 @@ def attn_fwd_kvcache_fp8(q, k_new, v_new, k_cache, v_cache, k_scale, v_scale, ca
                                                       page_size, max_pages, rot_dim)
 
     def body(s):
+        device = q.device
         o = torch.empty_like(q) if out is None else out
-        l = torch.empty((Hq, total_q), dtype=torch.float32, device=q.device) if lse is None else lse
-        ws = _kv8_workspace(nbytes, q.device, workspace)
+        l = torch.empty((Hq, total_q), dtype=_F32, device=device) if lse is None else lse
+        ws = _kv8_workspace(nbytes, device, workspace)
         rc = lib.attn_fwd_kvcache_fp8(
-            qp, kn, vn, kc, vc, ks, vs, sl, bt, cu, cos, sin, rot_dim, rot_rows,
+            q.data_ptr(), kn, vn, k_cache.data_ptr(), v_cache.data_ptr(), k_scale.data_ptr(),
+            v_scale.data_ptr(), sl, block_table.data_ptr(), cu, cos, sin, rot_dim, rot_rows,
             1 if rotary_interleaved else 0, o.data_ptr(), l.data_ptr(), batch, total_q, max_q,
             total_k, Hq, Hkv, d, page_size, max_pages, num_pages, scale, 1 if causal else 0,
             left, right, _ptr(ws), nbytes, s)
