@@ -40,10 +40,10 @@
 // two streams with their own maximum, denominator and O; the first stream merges them.
 // 8 chunks of 2048 tokens behind 2K to 16K keys, 32:8 heads, d 128: 1351 us with one part and two tiles
 // an item (1614 TFLOP/s); with two parts 2.09 ms, 1565 TFLOP/s of MMAs done, 1045 of what the formula
-// asks for.  What bounds it are the bytes that one tile an item asks for, 64 KB of K and V for 128 rows
-// and a key block (7.5 TB/s out of L2 over all SMs; 1.95 ms without the low part's MMAs), and shared
-// memory right behind: per two blocks 576 KB of operands, P and arriving K and V, at 128 bytes a clock 4600
-// of the 4960 clocks taken.  A fourth slot in the ring gave 2%.
+// asks for, where a plain product reaches 1906 in a burst and 1715 for seconds.  Bound by the tensor
+// cores: the pipe holds up the S issuer for 76% of the time and the PV issuer for 47%.  Half the bytes of K
+// and V changed nothing, Q as an operand from TMEM and a fourth ring slot 2% each.  Without the low part's
+// MMAs one tile an item takes 1.95 ms: then the two streams' softmax is the longer chain.
 #include <cuda_bf16.h>
 
 #include "kernels.h"
@@ -82,10 +82,10 @@ struct FwdCfg {
     // TMEM columns of S_t (fp32) and O_t (fp32)
     __device__ static constexpr uint32_t col_s(int t) { return 128u * t; }
     __device__ static constexpr uint32_t col_o(int t) { return 256u + D * t; }
-    // kF16HiLo at d 64: P_t too (f16, two keys a column), where O_t leaves room.  One tile an item
-    // makes shared memory the tighter bound, and P passes through it twice otherwise (8 chunks of
-    // 2048 tokens, 8000 keys, 16:4 heads: 867 -> 820 us).  At d 128 it would lie over S_t, and S_t(j + 1)
-    // would wait for P_t(j)'s product (8 x 2048 tokens, 32:8 heads: 2290 -> 2322 us).
+    // kF16HiLo at d 64: P_t too (f16, two keys a column), where O_t leaves room; it would pass through
+    // shared memory twice otherwise (8 chunks of 2048 tokens, 8000 keys, 16:4 heads: 867 -> 820 us).  At
+    // d 128 it would lie over S_t, and S_t(j + 1) would wait for P_t(j)'s product (8 x 2048 tokens, 32:8
+    // heads: 2290 -> 2322 us).
     static constexpr bool kPInTmem = kOps == kF16HiLo && D == 64;
     __device__ static constexpr uint32_t col_p(int t) { return 256u + 2 * D + 64u * t; }
 };
