@@ -164,6 +164,8 @@ __device__ __forceinline__ void scale_pair(uint32_t w, float (&f)[2]) {
 // for a unit's merge, 2 us for the kernel behind: 37 sequences up to 3000 tokens, 14:2 heads, 15.9 us.
 // kKv8SwitchChunks = 0 takes 19.9 us there, 2 to 4 take 15.9; 64 sequences take 352 us with 0 and
 // 348.5, 347.6, 348 with 2, 3, 4; 16 sequences of 300 tokens 14.1 us and 11.8, 10.9, 11.9.
+// A share of at least kKv8MinShare = 2 chunks: one sequence of 700 tokens, 8:2 heads, d 64, takes 7.6 us,
+// 8.6 with 1, 9.3 with 4.
 // Fetching a unit's queries during the merge before it cost more registers than it gained (64
 // sequences 376 us), and so did asking for the first chunks in L2 before the append kernel ends.
 template <int D, bool kLo>

@@ -675,7 +675,7 @@ __global__ void __launch_bounds__(256)
     }
 }
 
-// About 2048 moves of 16 codes a block.
+// About 2048 moves of 16 codes a block (158K tokens: 152 us; 178 with half, 151 with twice as many).
 int read_tokens(int Hkv, int head_dim) {
     int n = kReadTokens;
     while (n > 8 && n * Hkv * (head_dim / 16) > 2048) n /= 2;
@@ -714,8 +714,10 @@ cudaError_t launch_read(const Params& p, void* k, void* v, int rows, int head_di
 cudaError_t launch_kvcache_append_fp8(const AppendFp8Params& p, int head_dim, bool dependent,
                                       cudaStream_t stream) {
     if (p.total_q == 0) return cudaSuccess;
-    // Single tokens spread over the GPU, about one step a group of lanes; prompts take up to 16
-    // tokens a block.
+    // Single tokens spread over the GPU, about one step a group of lanes (64 of them: 3.9 us, 6.8 with
+    // 16 tokens a block); prompts take up to 16 tokens a block while four blocks an SM remain (16384
+    // tokens: 25.0 us, 27.3 with 8 a block, 25.0 with 32).  Whole heads that turn in halves: 25.0 us,
+    // 28.9 as any turn.
     const int blocks = (p.Hkv + kAppendRows - 1) / kAppendRows;
     const int groups = kAppendThreads / (head_dim / 16);
     int tokens = 1;
