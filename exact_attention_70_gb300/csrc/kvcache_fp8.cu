@@ -16,7 +16,9 @@
 // value again as an unevaluated sum of two fp32 numbers (Dekker's and Knuth's error-free product
 // and sum), brought to one by rounding to odd, after which rounding to a shorter format gives
 // what rounding the exact value would (S. Boldo, G. Melquiond, "Emulation of FMA and correctly
-// rounded sums: proved algorithms using rounding to odd", 2008).
+// rounded sums: proved algorithms using rounding to odd", 2008).  Both forms need their products'
+// low parts (2^-48 of the product) above fp32's 2^-149: rows below 2^-90 are formed again times 2^64,
+// and rows whose rotated elements pass fp32's range (which the cache holds: 448 2^120) times 2^-64.
 #include <cuda_bf16.h>
 
 #include "kernels.h"
@@ -112,8 +114,37 @@ __device__ __forceinline__ uint32_t row_max(uint32_t v) {
 
 // 448 = 1.75 2^8: the exponent of the largest magnitude (u: its bits) less 8, one more when its
 // significand is above 1.75.
-__device__ __forceinline__ int scale_byte(int u) {
-    return max(1, (u >> 23) - 8 + ((u & 0x7fffff) > 0x600000 ? 1 : 0));
+__device__ __forceinline__ int scale_exponent(int u) {
+    return (u >> 23) - 8 + ((u & 0x7fffff) > 0x600000 ? 1 : 0);
+}
+__device__ __forceinline__ int scale_byte(int u) { return max(1, scale_exponent(u)); }
+
+// A lane's largest rotated magnitude (its bits) that asks for the row to be formed again with another
+// exponent: below 2^-90 (zeros are exact) or beyond fp32's range.
+__device__ __forceinline__ bool off_range(int u) {
+    return static_cast<unsigned>(u - 1) < static_cast<unsigned>((127 - 90) << 23) - 1 || u >= 0x7f800000;
+}
+
+// Multiplies a staged row of bf16 by 2^k so that its products stay clear of both ends of fp32's range,
+// and gives k.  Exact but for elements 2^-190 of the row's largest.  (Rare, so in loops.)
+template <int kLanes>
+__device__ __forceinline__ int scale_row(uint8_t* row, int l) {
+    uint32_t* const w = reinterpret_cast<uint32_t*>(row) + l;  // words l, l + kLanes, ...
+    int top = 0;
+#pragma unroll 1
+    for (int j = 0; j < 8; ++j) {
+        const int a = (w[j * kLanes] >> 7) & 0xff, b = (w[j * kLanes] >> 23) & 0xff;
+        top = max(top, max(a == 255 ? 0 : a, b == 255 ? 0 : b));  // 255: not finite
+    }
+    top = row_max<kLanes>(top);
+    const int k = top >= 127 + 62 ? -64 : top < 127 - 38 ? 64 : 0;
+    const float f = exp2_int(k);
+#pragma unroll 1
+    for (int j = 0; j < 8; ++j)
+        w[j * kLanes] = pack_bf16x2(__uint_as_float(w[j * kLanes] << 16) * f,
+                                    __uint_as_float(w[j * kLanes] & 0xFFFF0000u) * f);
+    __syncwarp();
+    return k;
 }
 
 // The codes of y times f.
@@ -325,8 +356,8 @@ __device__ __forceinline__ void append_rows(const AppendFp8Params& p, int tokens
         __syncwarp();
 #pragma unroll 1
         for (int i = 0; i < most; ++i) {
-            const bool mine = i < n;  // (other rows' stages hold anything)
-            const uint8_t* const row = stage[step % kAppendStages][group][i];
+            const bool mine = i < n;  // (other rows' stages hold anything, and ask for nothing)
+            uint8_t* const row = stage[step % kAppendStages][group][i];
             uint64_t y[8];
             read_row(y, row, l, kLanes);
             if (kRotated) turn_row<kTurn, false>(y, row, turn, turns, from, p.interleaved);
@@ -357,14 +388,14 @@ __device__ __forceinline__ void append_rows(const AppendFp8Params& p, int tokens
                 continue;
             }
             // Not certain: a row with an element that is not finite (0 times it is NaN); a rotated
-            // one whose scale (it changes where the largest's significand passes 1.75) or,
-            // below, whose codes change within the rotation's error.
+            // one near the ends of fp32's range, or whose scale (it changes where the largest's
+            // significand passes 1.75) or, below, whose codes change within the rotation's error.
             uint64_t zero = 0;
 #pragma unroll
             for (int j = 0; j < 8; ++j) zero = f2_fma(y[j], 0, zero);
             float z0, z1;
             f2_split(zero, z0, z1);
-            bool redo = z0 + z1 != 0.f || (kRotated && ((u - (0x600000 - 8)) & 0x7fffff) <= 16);
+            bool redo = z0 + z1 != 0.f || (kRotated && (((u - (0x600000 - 8)) & 0x7fffff) <= 16 || off_range(u)));
             uint32_t sb = row_max<kLanes>(scale_byte(u));
             const float inv = __int_as_float((254 - min(sb, 253u)) << 23);  // 2^-e
             uint2 codes[2];
@@ -376,7 +407,9 @@ __device__ __forceinline__ void append_rows(const AppendFp8Params& p, int tokens
                     redo = redo || codes[m].x != above.x || codes[m].y != above.y;
                 }
             }
-            if (__any_sync(0xffffffffu, redo)) {
+            if (__any_sync(0xffffffffu, mine && redo)) {
+                const int k =
+                    kRotated && __any_sync(0xffffffffu, mine && off_range(u)) ? scale_row<kLanes>(row, l) : 0;
                 read_row(y, row, l, kLanes);
                 if (kRotated) turn_row<kTurn, true>(y, row, turn, turns, from, p.interleaved);
                 float top = 0.f;
@@ -385,17 +418,18 @@ __device__ __forceinline__ void append_rows(const AppendFp8Params& p, int tokens
                     float f[2];
                     f2_split(y[j], f[0], f[1]);
 #pragma unroll
-                    for (int k = 0; k < 2; ++k) {
-                        if (fabsf(f[k]) <= kFltMax)
-                            top = fmaxf(top, fabsf(f[k]));
+                    for (int i = 0; i < 2; ++i) {
+                        if (fabsf(f[i]) <= kFltMax)
+                            top = fmaxf(top, fabsf(f[i]));
                         else
-                            f[k] = __int_as_float(0x7fffffff);  // the NaN code; infinity would saturate
+                            f[i] = __int_as_float(0x7fffffff);  // the NaN code; infinity would saturate
                     }
                     y[j] = f2_make(f[0], f[1]);
                 }
-                sb = row_max<kLanes>(scale_byte(__float_as_int(top)));
+                sb = row_max<kLanes>(top == 0.f ? 1 : max(1, scale_exponent(__float_as_int(top)) - k));
+                const float inv = __int_as_float(min(254 - static_cast<int>(sb) - k, 254) << 23);
 #pragma unroll
-                for (int m = 0; m < 2; ++m) codes[m] = codes8(&y[4 * m], __int_as_float((254 - sb) << 23));
+                for (int m = 0; m < 2; ++m) codes[m] = codes8(&y[4 * m], inv);
             }
             if (mine) {
                 uint8_t* const dst = (kKind == kValues ? p.v_cache : p.k_cache) +

@@ -328,7 +328,8 @@ attn_status_t attn_quantize_fp8(const void* q, const void* k, const void* v,
  *   rotary_*      as attn_fwd_kvcache (tables 16-byte aligned): keys are rotated first, and the
  *                 rotated value is rounded once, to its code
  * Every byte written equals what rounding the exactly rotated row gives, up to ties closer than
- * 2^-45 of the row's largest element.
+ * 2^-45 of the row's largest element (and the sign of a 0 that is the sum of two zeros).  That holds
+ * for rows of any size: the cache also keeps rotated elements above fp32's largest number.
  */
 attn_status_t attn_kvcache_append_fp8(const void* k_new, const void* v_new, void* k_cache,
                                       void* v_cache, void* k_scale, void* v_scale,
@@ -345,7 +346,8 @@ attn_status_t attn_kvcache_append_fp8(const void* k_new, const void* v_new, void
  *   cu_seqlens_k  device int32 [batch + 1], non-decreasing
  *   k, v          device bf16 [total_k, nheads_kv, head_dim]; row cu_seqlens_k[b] + j is token j of
  *                 sequence b; rows outside every sequence are left as they were
- * The values are exact except where bf16 cannot hold them (below its normal range).
+ * The values are exact except where bf16 cannot hold them (below its normal range; rotated keys above
+ * its largest number read as infinity).
  */
 attn_status_t attn_kvcache_read_fp8(const void* k_cache, const void* v_cache, const void* k_scale,
                                     const void* v_scale, const int32_t* block_table,
