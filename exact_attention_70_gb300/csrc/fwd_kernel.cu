@@ -244,6 +244,15 @@ __device__ void drain_wait(uint64_t* bar, uint32_t parity) {
     }
 }
 
+// What turns S of f16 operands into a logit: sl2 times both units (powers of two).  It stays a normal
+// number: the units of zero or tiny rows multiply to less than fp32 holds (2^-126 2^-120), and 0 times
+// a masked score's -infinity would be NaN.  |S| is below 2^37, so FLT_MIN leaves such logits below 2^-89.
+__device__ __forceinline__ float f16_logit_unit(float sl2, float k_unit, float q_unit) {
+    const int n = (__float_as_int(k_unit) >> 23) + (__float_as_int(q_unit) >> 23) - 254;
+    const int half = n / 2;  // in two steps, so that a small unit and a large one meet first
+    return fminf(fmaxf(sl2 * exp2_int(half) * exp2_int(n - half), 0x1p-126f), 0x1.fffffep127f);
+}
+
 // ---- TMA producer (one thread) -----------------------------------------------------------
 
 // What the producer has put into the ring: the slot loads so far and, per slot, the parity of
@@ -613,11 +622,13 @@ __device__ void fwd_softmax(const FwdParams& p, uint8_t* smem, FwdBars* bars, ui
         // f16 operands come as multiples of a unit per query row and per (sequence, kv head)
         float sl2_a = sl2, sl2_b = sl2;
         if constexpr (is_f16(kOps)) {
-            const float unit = p.k_unit[it.b * p.Hkv + it.kvh] * sl2;
+            const float ku = p.k_unit[it.b * p.Hkv + it.kvh];
             const int ta = tv.tok0 + ra / g, tb = tv.tok0 + (ra + 8) / g;
             const float* qu = p.q_unit + it.kvh * g;
-            sl2_a = unit * (ta < it.Lq ? qu[static_cast<size_t>(it.q0 + ta) * p.Hq + ra % g] : 1.f);
-            sl2_b = unit * (tb < it.Lq ? qu[static_cast<size_t>(it.q0 + tb) * p.Hq + (ra + 8) % g] : 1.f);
+            sl2_a = f16_logit_unit(
+                sl2, ku, ta < it.Lq ? qu[static_cast<size_t>(it.q0 + ta) * p.Hq + ra % g] : 1.f);
+            sl2_b = f16_logit_unit(
+                sl2, ku, tb < it.Lq ? qu[static_cast<size_t>(it.q0 + tb) * p.Hq + (ra + 8) % g] : 1.f);
         }
         // this thread's rows ra and ra + 8; packed row r is token tok0 + r / g, head kvh g + r % g
         float m_a = -INFINITY, m_b = -INFINITY, l_a = 0.f, l_b = 0.f;  // l: this thread's part

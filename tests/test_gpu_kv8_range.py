@@ -5,18 +5,19 @@ pages that a window has left behind.
 
 The bounds are those of kv8_exact.check: a logit is off by dS d 2^-23 for its fp32 sums of d products
 (and dS 2^-20 where the query was rotated and goes to the tensor cores as two f16 numbers of 11 bits
-each), a weight by 2^-11 as an f16 operand and by 2^-20 for exp2 and the division, O by 2^-8 as
-bf16."""
+each), a weight by 2^-11 as an f16 operand (below f16's normal range as reference() says) and by 2^-20
+for exp2 and the division, O by 2^-8 as bf16."""
 import numpy as np
 import pytest
 import torch
 
 from tests import kv8_exact
 from tests.kv8_exact import kv8_case
-from tests.test_gpu_kv8 import append, attn, gpu_cache  # noqa: F401
+from tests.test_gpu_kv8 import append, attn, chunk, decode, gpu_cache  # noqa: F401
 
 pytestmark = pytest.mark.gpu
 
+SHORT, LONG = [3, 5], [200, 90]  # new tokens: on the codes; staged (32:8 heads)
 
 
 def bf16(x):
@@ -38,6 +39,112 @@ def new_rows(c, b):
     """The rows of sequence b's new tokens."""
     cu = c.cu_seqlens_q.tolist()
     return slice(cu[b], cu[b + 1])
+
+
+def same_stored(cache, arrays):
+    """The same bytes, but for the sign of zeros (a sum of two zeros has none)."""
+    for i, (got, want) in enumerate(zip(cache, arrays)):
+        got = got.cpu().numpy()
+        assert np.array_equal(*(np.where(x == 0x80, 0, x) if i < 2 else x for x in (got, want)))
+
+
+def reference(c, arrays, causal=True, window=(-1, -1)):
+    """kv8_exact.attention of c's tokens, dS over the keys that a row sees, and W with what f16 weights
+    lose below their normal range, 2^-14: 2^-25 a weight.  Either the largest weight times its value's scale,
+    P_j 2^e_j, is brought to 2^5 or above: this is then 2^-30 of it a code; or, where no scales are more than
+    2^22 apart, the largest weight is brought to 2^7: 2^-32 of |v_j|.  (check() takes 2^-11 of W.)"""
+    decode = not any(c.new)
+    new = [1] * len(c.ctx) if decode else c.new
+    T = sum(new)
+    O, LSE, dS, W = [x[:T] for x in kv8_exact.attention(c, arrays, causal, window)]
+    g = O.shape[1] // c.k_cache.shape[2]
+    table, t0 = c.block_table.numpy(), 0
+    for b, n in enumerate(new):
+        L = c.ctx[b] + (0 if decode else n)
+        pos = L - n + np.arange(n)
+        q = c.q[t0:t0 + n].double().numpy()
+        if not decode:
+            q = kv8_exact.rotate(q, pos, c.rotary_cos, c.rotary_sin, c.interleaved)
+        k, v = kv8_exact.read_back(arrays, table, b, L, c.page_size)
+        j = np.arange(L)
+        e = arrays[3][table[b, j // c.page_size], :, j % c.page_size].astype(np.float64) - 127
+        right = 0 if causal else window[1]
+        seen = np.ones((n, L), bool) if right < 0 else j <= pos[:, None] + right
+        if window[0] >= 0:
+            seen &= j >= pos[:, None] - window[0]
+        for h in range(O.shape[1] if L else 0):
+            kh, vh, eh = k[:, h // g], np.abs(v[:, h // g]), np.exp2(e[:, h // g])
+            dS[t0:t0 + n, h] = c.scale * np.where(seen, np.abs(q[:, h]) @ np.abs(kh).T, 0.0).max(1)
+            s = np.where(seen, c.scale * (q[:, h] @ kh.T), -np.inf)
+            top = (np.exp(s - np.maximum(s.max(1), -1e300)[:, None]) * eh).max(1)
+            near = np.minimum(eh, 2.0 ** 22 * eh.min(initial=np.inf))
+            W[t0:t0 + n, h] += seen @ (vh / eh[:, None] * near[:, None]) * 2.0 ** -21
+            W[t0:t0 + n, h] += top[:, None] * (seen @ (vh / eh[:, None])) * 2.0 ** -19
+        t0 += n
+    return O, LSE, dS, W
+
+
+def check_chunk(attn, c, causal=True, window=(-1, -1), what="", **kw):  # noqa: F811
+    cache = gpu_cache(c)
+    out, lse = chunk(attn, c, cache, causal, window, **kw)
+    assert attn.attn_get_device_status() == 0, what
+    arrays = kv8_exact.appended(c)
+    same_stored(cache, arrays)
+    T = sum(c.new)
+    kv8_exact.check(out[:T], lse[:, :T].t(), reference(c, arrays, causal, window), 2.0 ** -11,
+                    c.rotary_cos is not None, what)
+
+
+def check_decode(attn, c, what=""):  # noqa: F811
+    out, lse = decode(attn, c)
+    kv8_exact.check(out, lse, reference(c, [t.numpy() for t in c.cache]), 2.0 ** -11, False, what)
+
+
+@pytest.mark.parametrize("rotary", [0, 64])
+@pytest.mark.parametrize("window", [(-1, -1), (40, 0)])
+@pytest.mark.parametrize("new", [SHORT, LONG])
+def test_chunk_of_zero_and_tiny_keys_and_queries(attn, new, window, rotary):  # noqa: F811
+    """Logits of 0: uniform weights over what a row sees, whatever the units of its parts."""
+    c = kv8_case([70, 30], new, 32, 8, 64, 32, seed=400, rotary_dim=rotary, spread=0.5)
+    for b in (0, 1):
+        n = c.ctx[b]
+        k = np.zeros((n, 8, 64))
+        k[:, 4:6] = 2.0 ** -100 * np.random.default_rng(b).standard_normal((n, 2, 64))
+        k[:, 6:] = 2.0 ** -13 * np.random.default_rng(b).standard_normal((n, 2, 64))
+        put_cached(c, b, np.arange(n), k=k)
+    c.k_new[:, :4] = 0
+    c.k_new[:, 4:6] *= 2.0 ** -100
+    c.k_new[:, 6:] *= 2.0 ** -13
+    c.q[:, 0::4] = 0                 # query heads 0 of every kv head, ...
+    c.q[:, 1::4] *= 2.0 ** -10
+    c.q[:, 2::4] *= 2.0 ** -120
+    check_chunk(attn, c, True, window)
+
+
+def test_calls_on_all_zero_tensors(attn):  # noqa: F811
+    """What a program warms up with."""
+    for new in (SHORT, LONG):
+        c = kv8_case([0, 0], new, 32, 8, 128, 64, seed=401, rotary_dim=128)
+        for t in (c.q, c.k_new, c.v_new):
+            t.zero_()
+        check_chunk(attn, c)
+    c = kv8_case([33, 1], None, 4, 2, 64, 16, seed=402)
+    c.q.zero_()
+    for b, n in enumerate(c.ctx):
+        put_cached(c, b, np.arange(n), k=np.zeros((n, 2, 64)), v=np.zeros((n, 2, 64)))
+    check_decode(attn, c)
+
+
+@pytest.mark.parametrize("new", [LONG])
+@pytest.mark.parametrize("scale", [1.2e-38, 1e-20])
+def test_softmax_scales_at_the_bottom_of_their_range(attn, scale, new):  # noqa: F811
+    """Tiny queries times the smallest scales: logits of 0 to fp32, masked ones still -infinity."""
+    c = kv8_case([70, 30], new, 32, 8, 64, 32, seed=403, scale=scale)
+    c.q *= 2.0 ** -120
+    if new is None:
+        check_decode(attn, c)
+    else:
+        check_chunk(attn, c, True, (40, 0))
 
 
 @pytest.mark.parametrize("rotary,inter", [(64, False), (32, True), (48, False)])
