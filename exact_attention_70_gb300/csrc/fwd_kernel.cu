@@ -32,7 +32,7 @@
 //
 // Instances with f16 operands (kOps) serve the 8-bit cache: Q, K and V are f16 multiples of powers
 // of two (of a query row, of a sequence and kv head), which join the softmax scale and the
-// epilogue's 1 / l, and P is f16, whose 11 bits hold P <= 256 down to 2^-14.
+// epilogue's 1 / l, and P is f16 (kF16Up).
 // Rotated queries need more than 11 bits: rounding them moves LSE by 1e-5 to 1e-4 of itself where a
 // row sees few keys.  They come as hi + lo, two f16 numbers (kF16HiLo): S = Q_hi K^T + Q_lo K^T,
 // half as many MMAs again.  Both parts of two tiles would not fit in shared memory, so an item is
@@ -60,6 +60,10 @@ constexpr int kBf16 = 0, kF16 = 1, kF16HiLo = 2;
 __host__ __device__ constexpr bool is_f16(int ops) { return ops != kBf16; }
 
 constexpr float kRescaleThreshold = 8.0f;  // log2 units
+// f16 P goes to the tensor cores times 2^7: at most 2^15, and 11 bits down to weights of 2^-21 of the
+// row's largest (without it 2^-14: rows whose largest weight meets a tiny value were 9 times their bound
+// off).  The denominator carries the factor too, and LSE leaves it out.
+constexpr float kF16Up = 7.f;
 constexpr float kLn2 = 0.69314718055994530942f;
 constexpr float kLog2e = 1.44269504088896340736f;
 
@@ -787,8 +791,10 @@ __device__ void fwd_softmax(const FwdParams& p, uint8_t* smem, FwdBars* bars, ui
                     nma = f2_make(ca - ra_ref, ca - ra_ref);
                     nmb = f2_make(cb - rb_ref, cb - rb_ref);
                 } else {
-                    nma = f2_make(-ra_ref, -ra_ref);
-                    nmb = f2_make(-rb_ref, -rb_ref);
+                    const float na = is_f16(kOps) ? kF16Up - ra_ref : -ra_ref;
+                    const float nb = is_f16(kOps) ? kF16Up - rb_ref : -rb_ref;
+                    nma = f2_make(na, na);
+                    nmb = f2_make(nb, nb);
                 }
                 // P = exp2(s * scale*log2e - m): paired FFMA, MUFU ex2, paired sums
                 const uint64_t sa2 = is_f16(kOps) ? f2_make(sl2_a, sl2_a) : sl2x2;
@@ -1056,6 +1062,7 @@ __device__ void fwd_softmax(const FwdParams& p, uint8_t* smem, FwdBars* bars, ui
                 }
             }
         }
+        if constexpr (is_f16(kOps)) m_a -= kF16Up, m_b -= kF16Up;
         const int tok_a = tv.tok0 + ra / g, tok_b = tv.tok0 + (ra + 8) / g;
         const bool valid_a = ra < tile_rows && tok_a < it.Lq;
         const bool valid_b = ra + 8 < tile_rows && tok_b < it.Lq;

@@ -18,6 +18,7 @@ from tests.test_gpu_kv8 import append, attn, chunk, decode, gpu_cache  # noqa: F
 pytestmark = pytest.mark.gpu
 
 SHORT, LONG = [3, 5], [200, 90]  # new tokens: on the codes; staged (32:8 heads)
+EXPONENTS = [-124, -110, -90, 60, 80, 100, 108, 116, 124]
 
 
 def bf16(x):
@@ -145,6 +146,25 @@ def test_softmax_scales_at_the_bottom_of_their_range(attn, scale, new):  # noqa:
         check_decode(attn, c)
     else:
         check_chunk(attn, c, True, (40, 0))
+
+
+def sized(shape, e, aligned, rng):
+    """Rows of size 2^e: of any sign, or all positive, whose products with each other add up."""
+    return (rng.uniform(1, 2, shape) if aligned else rng.standard_normal(shape)) * 2.0 ** e
+
+
+@pytest.mark.parametrize("aligned", [False, True])
+@pytest.mark.parametrize("rotary", [0, 128])
+@pytest.mark.parametrize("e", EXPONENTS)
+@pytest.mark.parametrize("new", [LONG])
+def test_chunk_over_keys_of_any_size(attn, new, e, rotary, aligned):  # noqa: F811
+    c = kv8_case([200, 40], new, 32, 8, 128, 64, seed=411, rotary_dim=rotary)
+    rng = np.random.default_rng(411)
+    for b, n in enumerate(c.ctx):
+        put_cached(c, b, np.arange(n), k=sized((n, 8, 128), e, aligned, rng))
+    c.k_new = bf16(sized(c.k_new.shape, e, aligned, rng))
+    c.q = bf16(sized(c.q.shape, -e, aligned, rng))
+    check_chunk(attn, c, what=f"2^{e}")
 
 
 @pytest.mark.parametrize("rotary,inter", [(64, False), (32, True), (48, False)])
