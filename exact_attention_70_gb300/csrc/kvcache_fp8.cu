@@ -104,6 +104,18 @@ __device__ __forceinline__ float lane_top(const uint64_t (&y)[8]) {
     return top;
 }
 
+// The bits of the largest |y| of a run of 8.
+__device__ __forceinline__ int run_top(const uint64_t* y) {
+    float top = 0.f;
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+        float a, b;
+        f2_split(y[i], a, b);
+        top = fmax3(top, fabsf(a), fabsf(b));
+    }
+    return __float_as_int(top);
+}
+
 // The largest over the kLanes lanes of a row.
 template <int kLanes>
 __device__ __forceinline__ uint32_t row_max(uint32_t v) {
@@ -155,10 +167,10 @@ __device__ __forceinline__ uint2 codes8(const uint64_t* y, float f) {
     return make_uint2(pack_e4m3x4(z[0], z[1], z[2], z[3]), pack_e4m3x4(z[4], z[5], z[6], z[7]));
 }
 
-// The table entries of chunk c (8 elements) of a row at position pos; plane: the chunk that holds
-// its planes' first elements.
+// The table entries times `unit` of chunk c (8 elements) of a row at position pos; plane: the chunk that
+// holds its planes' first elements.
 __device__ __forceinline__ Turn turn_of(const AppendFp8Params& p, int pos, int c, int plane,
-                                        bool lower) {
+                                        bool lower, float unit) {
     Turn t;
     const size_t row = static_cast<size_t>(pos) * (p.rot_dim / 2);
     if (p.interleaved) {
@@ -167,18 +179,18 @@ __device__ __forceinline__ Turn turn_of(const AppendFp8Params& p, int pos, int c
         const float cc[4] = {cv.x, cv.y, cv.z, cv.w}, ss[4] = {sv.x, sv.y, sv.z, sv.w};
 #pragma unroll
         for (int i = 0; i < 4; ++i) {
-            t.c[i] = f2_make(cc[i], cc[i]);
-            t.s[i] = f2_make(-ss[i], ss[i]);
+            t.c[i] = f2_make(unit * cc[i], unit * cc[i]);
+            t.s[i] = f2_make(-unit * ss[i], unit * ss[i]);
         }
         return t;
     }
-    const float sign = lower ? -1.f : 1.f;
+    const float sign = lower ? -unit : unit;
 #pragma unroll
     for (int i = 0; i < 2; ++i) {
         const float4 cv = *reinterpret_cast<const float4*>(p.rot_cos + row + 8 * plane + 4 * i);
         const float4 sv = *reinterpret_cast<const float4*>(p.rot_sin + row + 8 * plane + 4 * i);
-        t.c[2 * i] = f2_make(cv.x, cv.y);
-        t.c[2 * i + 1] = f2_make(cv.z, cv.w);
+        t.c[2 * i] = f2_make(unit * cv.x, unit * cv.y);
+        t.c[2 * i + 1] = f2_make(unit * cv.z, unit * cv.w);
         t.s[2 * i] = f2_make(sign * sv.x, sign * sv.y);
         t.s[2 * i + 1] = f2_make(sign * sv.z, sign * sv.w);
     }
@@ -284,6 +296,9 @@ __device__ __forceinline__ void append_rows(const AppendFp8Params& p, int tokens
                                             AppendToken (&place_of)[kAppendTokens]) {
     constexpr int kLanes = D / 16, kGroups = kAppendThreads / kLanes;
     constexpr bool kRotated = kTurn != kNoTurn && kKind != kValues;
+    // Queries turn at half their size: their largest rotated elements would pass fp32's range.
+    constexpr bool kHalved = kRotated && kKind == kQueries;
+    constexpr float kUnit = kHalved ? 0.5f : 1.f;
     const int lane = threadIdx.x & 31, l = lane % kLanes, group = threadIdx.x / kLanes;
     const int t0 = blockIdx.x * tokens;
     const int H = kKind == kQueries ? p.Hq : p.Hkv;
@@ -334,7 +349,7 @@ __device__ __forceinline__ void append_rows(const AppendFp8Params& p, int tokens
         int from[2] = {l, l + kLanes};
         Turn turn[2];
         if (kRotated && kTurn == kWholeTurn && n > 0) {
-            turn[0] = turn_of(p, place.pos, l, l, true);
+            turn[0] = turn_of(p, place.pos, l, l, true, kUnit);
 #pragma unroll
             for (int j = 0; j < 4; ++j) {
                 turn[1].c[j] = turn[0].c[j];
@@ -348,7 +363,7 @@ __device__ __forceinline__ void append_rows(const AppendFp8Params& p, int tokens
                 const bool lower = c < h;
                 turns[m] = 8 * c < p.rot_dim;
                 if (turns[m] && !p.interleaved) from[m] = lower ? c + h : c - h;
-                if (turns[m] && n > 0) turn[m] = turn_of(p, place.pos, c, lower ? c : c - h, lower);
+                if (turns[m] && n > 0) turn[m] = turn_of(p, place.pos, c, lower ? c : c - h, lower, kUnit);
             }
         }
         const int most = __reduce_max_sync(0xffffffffu, n);
@@ -364,12 +379,17 @@ __device__ __forceinline__ void append_rows(const AppendFp8Params& p, int tokens
             const int u = __float_as_int(lane_top(y));
             if (kKind == kQueries) {
                 // the row's largest element to [2^13, 2^14) as f16 (kv8_query_shift)
-                const int up = kv8_query_shift(row_max<kLanes>(u >> 23));
-                const float f = __int_as_float((up + 127) << 23);
+                int e = u >> 23;
+                if (kHalved && kTurn == kWholeTurn) e = min(e + 1, 255);
+                if (kHalved && kTurn == kAnyTurn)
+                    e = min(max((run_top(&y[0]) >> 23) + turns[0], (run_top(&y[4]) >> 23) + turns[1]), 255);
+                const int up = kv8_query_shift(row_max<kLanes>(e));
+                const float unit = __int_as_float((up + 127) << 23);
                 if (!mine) continue;
                 const size_t at = static_cast<size_t>(t0 + it.tok) * p.Hq + it.h0 + i;
 #pragma unroll
                 for (int m = 0; m < 2; ++m) {
+                    const float f = kHalved && turns[m] ? 2.f * unit : unit;
                     uint32_t hi[4], lo[4];
 #pragma unroll
                     for (int j = 0; j < 4; ++j) {

@@ -201,3 +201,30 @@ def test_append_rotates_rows_of_any_size(attn, e, rotary, inter):  # noqa: F811
         for z in (x, y):
             z[(page, slot) if z.ndim == 4 else (page, slice(None), slot)] = 0
         assert np.array_equal(x, y)
+
+
+@pytest.mark.parametrize("e", [-132, -126, -118, 118, 126])
+@pytest.mark.parametrize("new", [SHORT, LONG])
+def test_rotated_queries_of_any_size(attn, new, e):  # noqa: F811
+    """Queries of 2^e on keys of 2^-e (as far as their type goes), the scale making up for the rest."""
+    k = max(-e, -118) if e > 0 else min(-e, 120)
+    c = kv8_case([100, 40], new, 32, 8, 64, 32, seed=460, rotary_dim=64, scale=2.0 ** -(e + k) / 8)
+    top = float(torch.finfo(torch.bfloat16).max)
+    for b, n in enumerate(c.ctx):
+        put_cached(c, b, np.arange(n), k=np.random.default_rng(b).standard_normal((n, 8, 64)) * 2.0 ** k)
+    c.k_new = bf16(c.k_new.double() * 2.0 ** k)
+    c.q = bf16(np.clip(c.q.double().numpy() * 2.0 ** e, -top, top))
+    cache = gpu_cache(c)
+    out, lse = chunk(attn, c, cache)
+    assert attn.attn_get_device_status() == 0
+    arrays = kv8_exact.appended(c)
+    same_stored(cache, arrays)
+    O, LSE, dS, W = reference(c, arrays)
+    # A query's elements have a floor: f16 numbers are 2^-24 apart below 2^-14 and a unit of them is
+    # 2^-120 at least, so an element is off by up to 2^-145, and a logit by scale sum_d |k_d| 2^-145
+    # more; check() takes dS 2^-20 for the rotation, so it joins dS times 2^20.
+    g = O.shape[1] // 8
+    for b, n in enumerate(c.new):
+        k = np.abs(kv8_exact.read_back(arrays, c.block_table.numpy(), b, c.ctx[b] + n, 32)[0]).sum(-1).max(0)
+        dS[new_rows(c, b)] += c.scale * np.repeat(k, g) * 2.0 ** -145 * 2.0 ** 20
+    kv8_exact.check(out, lse.t(), (O, LSE, dS, W), 2.0 ** -11, True, f"2^{e}")
