@@ -10,7 +10,8 @@
 // The arithmetic.  K and V are e4m3 codes times 2^e, one e per (token, kv head).  Codes are exact
 // in f16, so both products run on f16 tensor-core MMAs with fp32 sums and the scales
 // stay outside of them:
-//   * S_ij = 2^ek_j c_i sum_d (2^a_i q_id) k_jd with c_i = scale log2(e) 2^-a_i, where a_i brings
+//   * S_ij = 2^ek_j c_i sum_d (2^a_i q_id) k_jd (2^ek_j c_i first where the sum times 2^ek_j would pass
+//     fp32's range) with c_i = scale log2(e) 2^-a_i, where a_i brings
 //     row i's largest |q| just below 2^14: the 8 significant bits of bf16 fit f16's 11, and
 //     elements down to 2^-28 of the row's largest stay exact (below that the error is less than
 //     2^-39 of the largest).  A rotated query has no 8 significant bits: it comes as the sum of
@@ -33,6 +34,9 @@ namespace {
 
 constexpr float kLn2f = 0.69314718055994530942f;
 constexpr float kMaxScale = 0x1p127f;  // the largest scale; byte 255 reads as infinity before it is NaN
+// Scores of the scaled queries with the codes are below 2^30 (2^14 times 448, d times), so they may meet
+// key scales up to here before the query's own scale.
+constexpr float kFarScale = 0x1p90f;
 constexpr int kMinE = 8;  // E as a scale byte; its floor keeps 2^(5 - E) a normal number
 
 template <int D>
@@ -62,6 +66,7 @@ struct Kv8Bars {
     // number first_off of sequence first_seq's; share: what every CTA but the last ones takes
     int first_seq, first_off, start, count, share;
     int warp_sum[kKv8Threads / 32];
+    float unit[kKv8Rows];  // what one unit of the unit's scaled queries stands for
 };
 static_assert(sizeof(Kv8Bars) <= 256, "barrier block");
 
@@ -366,9 +371,10 @@ __global__ void __launch_bounds__(kKv8Threads, 2)
         }
         const bool there[2] = {gq < rows, gq + 8 < rows};
         const uint2 none = make_uint2(0u, 0u);
+        float unit[2];
         if (kLo) {  // rotated and scaled by the append kernel
 #pragma unroll
-            for (int h = 0; h < 2; ++h) c_row[h] = p.scale_log2 * p.q_unit[q_row[h]];
+            for (int h = 0; h < 2; ++h) unit[h] = p.q_unit[q_row[h]];
             for (int s = warp; s < D / 16; s += 4) {
 #pragma unroll
                 for (int part = 0; part < 2; ++part) {
@@ -399,7 +405,7 @@ __global__ void __launch_bounds__(kKv8Threads, 2)
                 top = max(top, __shfl_xor_sync(0xffffffffu, top, 2));
                 const int a = kv8_query_shift(top >> 7);
                 const float up = __int_as_float((a + 127) << 23);
-                c_row[h] = p.scale_log2 * __int_as_float((127 - a) << 23);
+                unit[h] = __int_as_float((127 - a) << 23);
 #pragma unroll
                 for (int s = 0; s < D / 16; ++s)
                     if (s % 4 == warp) {
@@ -413,6 +419,14 @@ __global__ void __launch_bounds__(kKv8Threads, 2)
             for (int i = 0; i < D / 64; ++i)
                 st_shared_v4(qs + (4 * i + warp) * 512, mine[i][0], mine[i][1], mine[i][2], mine[i][3]);
         }
+#pragma unroll
+        for (int h = 0; h < 2; ++h) {
+            c_row[h] = p.scale_log2 * unit[h];
+            if (warp == 0 && tq == 0) bars->unit[gq + 8 * h] = unit[h];
+        }
+        // A factor c below fp32's normal range (0 times a masked -infinity would be NaN), or a key scale
+        // above kFarScale: from that chunk on the three scales meet before the scores, and c is 1.
+        float far = fminf(c_row[0], c_row[1]) < 0x1p-126f ? -1.f : kFarScale;
         named_bar_sync(1, 128);
         // keys every row of the unit sees: [full_lo, full_hi]
         int full_lo, full_hi;
@@ -421,7 +435,6 @@ __global__ void __launch_bounds__(kKv8Threads, 2)
             row_key_interval(row0 / p.g, Lq, L, p.causal, p.wl, p.wr, lo, full_hi);
             row_key_interval((row0 + rows - 1) / p.g, Lq, L, p.causal, p.wl, p.wr, full_lo, hi);
         }
-        const uint64_t c2[2] = {f2_make(c_row[0], c_row[0]), f2_make(c_row[1], c_row[1])};
         bool ok = true;
         for (int c = w.c0; c < w.c1; ++c, ++n) {
             const uint32_t st = n % C::kStages;
@@ -499,18 +512,28 @@ __global__ void __launch_bounds__(kKv8Threads, 2)
                     k_top = fmax3(k_top, ks[nt][0], ks[nt][1]);
                     v_top = fmax3(v_top, vs[nt][0], vs[nt][1]);
                 }
-                if (__any_sync(0xffffffffu, k_top > kMaxScale)) {  // byte 255 stands for NaN
+                if (__any_sync(0xffffffffu, k_top > far)) {
+                    far = -1.f;
+                    c_row[0] = c_row[1] = 1.f;
 #pragma unroll
-                    for (int nt = 0; nt < 4; ++nt)
+                    for (int r = 0; r < 2; ++r) {
+                        const float u = bars->unit[gq + 8 * r];
 #pragma unroll
-                        for (int i = 0; i < 2; ++i)
-                            if (ks[nt][i] > kMaxScale) ks[nt][i] = __int_as_float(0x7fffffff);
-                }
+                        for (int nt = 0; nt < 4; ++nt)
 #pragma unroll
-                for (int nt = 0; nt < 4; ++nt) {
-                    const uint64_t kp = f2_make(ks[nt][0], ks[nt][1]);
-                    f2_split(f2_mul(f2_make(s[nt][0], s[nt][1]), kp), s[nt][0], s[nt][1]);
-                    f2_split(f2_mul(f2_make(s[nt][2], s[nt][3]), kp), s[nt][2], s[nt][3]);
+                            for (int i = 0; i < 2; ++i) {
+                                // (finite: a score may be 0; byte 255 stands for NaN)
+                                const float t = fminf(fminf(ks[nt][i] * u, kMaxScale) * p.scale_log2, kMaxScale);
+                                s[nt][2 * r + i] *= ks[nt][i] > kMaxScale ? __int_as_float(0x7fffffff) : t;
+                            }
+                    }
+                } else {
+#pragma unroll
+                    for (int nt = 0; nt < 4; ++nt) {
+                        const uint64_t kp = f2_make(ks[nt][0], ks[nt][1]);
+                        f2_split(f2_mul(f2_make(s[nt][0], s[nt][1]), kp), s[nt][0], s[nt][1]);
+                        f2_split(f2_mul(f2_make(s[nt][2], s[nt][3]), kp), s[nt][2], s[nt][3]);
+                    }
                 }
                 if (masked) {
 #pragma unroll
@@ -562,6 +585,7 @@ __global__ void __launch_bounds__(kKv8Threads, 2)
                         for (int e = 0; e < 4; ++e) o[x][e] *= alpha[e >> 1];
                 }
                 const uint64_t inv = f2_make(exp2_int(132 - e_run), exp2_int(132 - e_run));
+                const uint64_t c2[2] = {f2_make(c_row[0], c_row[0]), f2_make(c_row[1], c_row[1])};
                 uint64_t nm[2];
 #pragma unroll
                 for (int r = 0; r < 2; ++r) {

@@ -136,7 +136,7 @@ def test_calls_on_all_zero_tensors(attn):  # noqa: F811
     check_decode(attn, c)
 
 
-@pytest.mark.parametrize("new", [LONG])
+@pytest.mark.parametrize("new", [None, SHORT, LONG])
 @pytest.mark.parametrize("scale", [1.2e-38, 1e-20])
 def test_softmax_scales_at_the_bottom_of_their_range(attn, scale, new):  # noqa: F811
     """Tiny queries times the smallest scales: logits of 0 to fp32, masked ones still -infinity."""
@@ -154,9 +154,21 @@ def sized(shape, e, aligned, rng):
 
 
 @pytest.mark.parametrize("aligned", [False, True])
+@pytest.mark.parametrize("e", EXPONENTS)
+def test_decode_over_keys_of_any_size(attn, e, aligned):  # noqa: F811
+    """Keys of size 2^e and queries of 2^-e: moderate logits."""
+    c = kv8_case([300, 40], None, 8, 2, 128, 64, seed=410)
+    rng = np.random.default_rng(410)
+    for b, n in enumerate(c.ctx):
+        put_cached(c, b, np.arange(n), k=sized((n, 2, 128), e, aligned, rng))
+    c.q = bf16(sized(c.q.shape, -e, aligned, rng))
+    check_decode(attn, c, f"2^{e}")
+
+
+@pytest.mark.parametrize("aligned", [False, True])
 @pytest.mark.parametrize("rotary", [0, 128])
 @pytest.mark.parametrize("e", EXPONENTS)
-@pytest.mark.parametrize("new", [LONG])
+@pytest.mark.parametrize("new", [SHORT, LONG])
 def test_chunk_over_keys_of_any_size(attn, new, e, rotary, aligned):  # noqa: F811
     c = kv8_case([200, 40], new, 32, 8, 128, 64, seed=411, rotary_dim=rotary)
     rng = np.random.default_rng(411)
