@@ -17,11 +17,12 @@
 //     2^-39 of the largest).  A rotated query has no 8 significant bits: it comes as the sum of
 //     two f16 numbers, hi + lo, and both parts are multiplied (rounding it to one moved LSE by up to
 //     1e-4 of itself where a row sees few keys);
-//   * O_i = 2^(E - 5) sum_j (P_ij 2^(5 + ev_j - E)) v_j with P = exp2(x - m), where the references
-//     m (of a row) and E (of a warp) only move when a logit passes m by more than 8 (log2) or
-//     an ev_j passes E by more than 2.  The f16 factor is then at most 2^15 and keeps its 11 bits
-//     down to 2^-14, i.e. for weights down to 2^-19 of a row's largest where the V scales are alike;
-//     below that it is off by less than 2^-30.  When a reference moves, O is rescaled.
+//   * O_i = 2^(E - 5) sum_j (P_ij 2^(5 + ev_j - E)) v_j with P = exp2(x - m), where the references m
+//     and E of a row only move when a logit passes m by more than 8 (log2) or an ev_j passes E by
+//     more than 2.  E follows the row's largest P 2^ev, and lies above it by 4 at most.  The f16 factor is
+//     then at most 2^15 and keeps its 11 bits down to 2^-14, i.e. for P 2^ev down to 2^-15 of the row's
+//     largest (2^-19 where the V scales are alike); below that it is off by less than 2^-26.
+//     When a reference moves, O is rescaled.
 #include <cuda_bf16.h>
 
 #include "kernels.h"
@@ -351,7 +352,8 @@ __global__ void __launch_bounds__(kKv8Threads, 2)
         const int Lq = w.s.Lq, L = w.s.L, q0 = w.s.q0, rows = w.rows, row0 = w.row0;
         float m_run[2] = {-INFINITY, -INFINITY};
         uint64_t l2[2] = {0, 0};  // the rows' denominators, even and odd keys apart
-        int e_run = kMinE;        // E as a scale byte
+        // 2^(5 - E) of a row (E as a scale byte: 259 less this one's exponent field)
+        float inv[2] = {__int_as_float((259 - kMinE) << 23), __int_as_float((259 - kMinE) << 23)};
         float o[D / 8][4];
 #pragma unroll
         for (int x = 0; x < D / 8; ++x) o[x][0] = o[x][1] = o[x][2] = o[x][3] = 0.f;
@@ -559,32 +561,52 @@ __global__ void __launch_bounds__(kKv8Threads, 2)
                     mx[r] = x * c_row[r];
                 }
                 const bool m_moves = mx[0] > m_run[0] + 8.f || mx[1] > m_run[1] + 8.f;
-                const bool e_moves = v_top > __int_as_float((e_run + 2) << 23);
+                const bool e_moves = v_top * fmaxf(inv[0], inv[1]) > 128.f;
                 if (__any_sync(0xffffffffu, m_moves || e_moves)) {
-                    int e_new = __float_as_int(v_top) >> 23;
+                    // E follows the largest P 2^ev that a row has met, and the keys' largest scale by 4 at
+                    // most: a scale far above, of a key that the row does not see or that weighs little
+                    // in it, leaves the precision to the others.  (By more where 2^(5 + ev - E), which
+                    // meets P = 0, would pass fp32's range.)  One E a warp, 4 multiplications less a
+                    // step, took 342.9 us for the 64 sequences where this takes 344.7.
+                    int v_exp = __float_as_int(v_top) >> 23;
 #pragma unroll
                     for (int i = 16; i > 0; i >>= 1)
-                        e_new = max(e_new, __shfl_xor_sync(0xffffffffu, e_new, i));
-                    e_new = max(e_run, e_new);
-                    const float e_drop = exp2_int(e_run - e_new);
-                    e_run = min(e_new, 252);
+                        v_exp = max(v_exp, __shfl_xor_sync(0xffffffffu, v_exp, i));
+                    float pv[2] = {-INFINITY, -INFINITY};  // the chunk's largest log2 P 2^ev (a scale byte)
+#pragma unroll
+                    for (int nt = 0; nt < 4; ++nt)
+#pragma unroll
+                        for (int i = 0; i < 2; ++i) {
+                            const float ev = static_cast<float>(__float_as_int(vs[nt][i]) >> 23);
+#pragma unroll
+                            for (int r = 0; r < 2; ++r)
+                                pv[r] = fmaxf(pv[r], fmaf(s[nt][2 * r + i], c_row[r], ev));
+                        }
                     float alpha[2];
 #pragma unroll
                     for (int r = 0; r < 2; ++r) {
+                        pv[r] = fmaxf(pv[r], __shfl_xor_sync(0xffffffffu, pv[r], 1));
+                        pv[r] = fmaxf(pv[r], __shfl_xor_sync(0xffffffffu, pv[r], 2));
                         const float m_new = fmaxf(m_run[r], mx[r]);
-                        alpha[r] = m_new == -INFINITY ? 1.f : ex2_approx(m_run[r] - m_new);
+                        const bool none = m_new == -INFINITY;
+                        const float drop = none ? 0.f : m_run[r] - m_new;
+                        const float top = none ? 0.f : ceilf(pv[r] - m_new);
+                        const int e_run = 259 - (__float_as_int(inv[r]) >> 23), least = max(kMinE, v_exp - 120);
+                        const int e_new = min(max(max(static_cast<int>(ceilf(drop + e_run)), least),
+                                                  max(static_cast<int>(top), min(v_exp, static_cast<int>(top) + 4))),
+                                              252);
+                        l2[r] = f2_mul(l2[r], f2_make(ex2_approx(drop), ex2_approx(drop)));
+                        alpha[r] = ex2_approx(drop + (e_run - e_new));
                         m_run[r] = m_new;
-                        l2[r] = f2_mul(l2[r], f2_make(alpha[r], alpha[r]));
-                        alpha[r] *= e_drop;
+                        inv[r] = __int_as_float((259 - e_new) << 23);
                     }
                     // a V scale byte of 255: every output of the rows becomes NaN
-                    if (e_new == 255) alpha[0] = alpha[1] = __int_as_float(0x7fffffff);
+                    if (v_exp == 255) alpha[0] = alpha[1] = __int_as_float(0x7fffffff);
 #pragma unroll
                     for (int x = 0; x < D / 8; ++x)
 #pragma unroll
                         for (int e = 0; e < 4; ++e) o[x][e] *= alpha[e >> 1];
                 }
-                const uint64_t inv = f2_make(exp2_int(132 - e_run), exp2_int(132 - e_run));
                 const uint64_t c2[2] = {f2_make(c_row[0], c_row[0]), f2_make(c_row[1], c_row[1])};
                 uint64_t nm[2];
 #pragma unroll
@@ -595,14 +617,13 @@ __global__ void __launch_bounds__(kKv8Threads, 2)
                 uint32_t pa[2][4];  // P as the A operand of two k-steps of 16 keys
 #pragma unroll
                 for (int nt = 0; nt < 4; ++nt) {
-                    const uint64_t f = f2_mul(f2_make(vs[nt][0], vs[nt][1]), inv);
 #pragma unroll
                     for (int r = 0; r < 2; ++r) {
                         float x0, x1;
                         f2_split(f2_fma(f2_make(s[nt][2 * r], s[nt][2 * r + 1]), c2[r], nm[r]), x0, x1);
                         const uint64_t pp = f2_make(ex2_approx(x0), ex2_approx(x1));
                         l2[r] = f2_add(l2[r], pp);
-                        f2_split(f2_mul(pp, f), x0, x1);
+                        f2_split(f2_mul(pp, f2_mul(f2_make(vs[nt][0], vs[nt][1]), f2_make(inv[r], inv[r]))), x0, x1);
                         pa[nt >> 1][2 * (nt & 1) + r] = pack_f16x2(x0, x1);
                     }
                 }
@@ -664,8 +685,8 @@ __global__ void __launch_bounds__(kKv8Threads, 2)
             if (M == -INFINITY) M = 0.f;  // no key seen, or only NaN scores: l tells which
 #pragma unroll
             for (int i = 0; i < 4; ++i) lsum += ml[i * kKv8Rows + r] * ex2_approx(mm[i * kKv8Rows + r] - M);
-            const float inv = lsum == 0.f ? 0.f : 1.f / lsum;
-            sc[h] = ex2_approx(m_run[h] - M) * inv * (__int_as_float(e_run << 23) * 0x1p-5f);
+            const float over = lsum == 0.f ? 0.f : 1.f / lsum;
+            sc[h] = ex2_approx(m_run[h] - M) * over * __int_as_float((254 << 23) - __float_as_int(inv[h]));
             if (warp == 0 && tq == 0 && r < rows) {
                 const float lse = lsum == 0.f ? -INFINITY : M + __log2f(lsum);  // log2
                 const int tok = q0 + (row0 + r) / p.g, head = kvh * p.g + (row0 + r) % p.g;

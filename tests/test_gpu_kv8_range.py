@@ -19,6 +19,7 @@ pytestmark = pytest.mark.gpu
 
 SHORT, LONG = [3, 5], [200, 90]  # new tokens: on the codes; staged (32:8 heads)
 EXPONENTS = [-124, -110, -90, 60, 80, 100, 108, 116, 124]
+BIG = [2.0 ** 26, 2.0 ** 40, 2.0 ** 90, 3.3e38]
 
 
 def bf16(x):
@@ -52,7 +53,7 @@ def same_stored(cache, arrays):
 def reference(c, arrays, causal=True, window=(-1, -1)):
     """kv8_exact.attention of c's tokens, dS over the keys that a row sees, and W with what f16 weights
     lose below their normal range, 2^-14: 2^-25 a weight.  Either the largest weight times its value's scale,
-    P_j 2^e_j, is brought to 2^5 or above: this is then 2^-30 of it a code; or, where no scales are more than
+    P_j 2^e_j, is brought to 2 or above: this is then 2^-26 of it a code; or, where no scales are more than
     2^22 apart, the largest weight is brought to 2^7: 2^-32 of |v_j|.  (check() takes 2^-11 of W.)"""
     decode = not any(c.new)
     new = [1] * len(c.ctx) if decode else c.new
@@ -80,7 +81,7 @@ def reference(c, arrays, causal=True, window=(-1, -1)):
             top = (np.exp(s - np.maximum(s.max(1), -1e300)[:, None]) * eh).max(1)
             near = np.minimum(eh, 2.0 ** 22 * eh.min(initial=np.inf))
             W[t0:t0 + n, h] += seen @ (vh / eh[:, None] * near[:, None]) * 2.0 ** -21
-            W[t0:t0 + n, h] += top[:, None] * (seen @ (vh / eh[:, None])) * 2.0 ** -19
+            W[t0:t0 + n, h] += top[:, None] * (seen @ (vh / eh[:, None])) * 2.0 ** -15
         t0 += n
     return O, LSE, dS, W
 
@@ -177,6 +178,126 @@ def test_chunk_over_keys_of_any_size(attn, new, e, rotary, aligned):  # noqa: F8
     c.k_new = bf16(sized(c.k_new.shape, e, aligned, rng))
     c.q = bf16(sized(c.q.shape, -e, aligned, rng))
     check_chunk(attn, c, what=f"2^{e}")
+
+
+@pytest.mark.parametrize("new", [None, SHORT])
+def test_keys_of_all_sizes_in_one_sequence(attn, new):  # noqa: F811
+    """Keys 2^28 apart whose logits are alike: each meets the query in one component, where the query is
+    as much smaller; what is left of the keys' rows is larger by 2^7 and meets a zero."""
+    n, d = 190, 64
+    e = 4.0 * np.arange(8) - 14
+    rng = np.random.default_rng(9)
+
+    def keys(i):
+        k = np.zeros((len(i), 8, d))
+        k[np.arange(len(i)), :, i % 8] = rng.uniform(-2, 2, (len(i), 8)) * 2.0 ** e[i % 8, None]
+        k[:, :, 63] = 2.0 ** (e[i % 8, None] + 7)
+        return k
+
+    c = kv8_case([n, n], new, 32, 8, d, 32, seed=412, scale=1.0)
+    q = np.zeros(c.q.shape)
+    q[..., :8] = rng.choice([-1.0, 1.0], q[..., :8].shape) * 2.0 ** -e
+    c.q = bf16(q)
+    for b in (0, 1):
+        put_cached(c, b, np.arange(n), k=keys(rng.permutation(n)))
+    if new is None:
+        check_decode(attn, c)
+    else:
+        c.k_new = bf16(keys(rng.permutation(sum(new))))
+        check_chunk(attn, c)
+
+
+@pytest.mark.parametrize("rotary", [0, 64])
+@pytest.mark.parametrize("big", BIG)
+@pytest.mark.parametrize("new", [[9, 5]])
+def test_chunk_beside_large_values_that_rows_do_not_see(attn, new, big, rotary):  # noqa: F811
+    """The last new token's value is large, and so is one in the middle: rows before them do not see
+    them.  So is a cached one that the window of later rows leaves out."""
+    c = kv8_case([90, 130], new, 32, 8, 64, 32, seed=420, rotary_dim=rotary, spread=0.5)
+    for b in (0, 1):
+        r = new_rows(c, b)
+        c.v_new[r.stop - 1, :4] = bf16(c.v_new[r.stop - 1, :4].double() * (big / 8))
+        c.v_new[(r.start + r.stop) // 2, 5] = bf16(c.v_new[(r.start + r.stop) // 2, 5].double() * (big / 8))
+        put_cached(c, b, [c.ctx[b] - 30], v=np.random.default_rng(b).uniform(-1, 1, (1, 8, 64)) * big)
+    check_chunk(attn, c, True, (31, 0), f"{big}")
+    check_chunk(attn, c, True, (-1, -1), f"{big}")
+
+
+@pytest.mark.parametrize("big", BIG)
+@pytest.mark.parametrize("new", [[9, 5]])
+def test_chunk_beside_large_keys_that_rows_do_not_see(attn, new, big):  # noqa: F811
+    c = kv8_case([90, 130], new, 32, 8, 64, 32, seed=421, spread=0.5)
+    for b in (0, 1):
+        put_cached(c, b, [c.ctx[b] - 30], k=np.random.default_rng(b).uniform(-1, 1, (1, 8, 64)) * big)
+    # rows from the third on do not see it; the ones before have queries that keep the logits moderate
+    for b in (0, 1):
+        r = new_rows(c, b)
+        c.q[r.start:r.start + 3] = bf16(c.q[r.start:r.start + 3].double() / big)
+    check_chunk(attn, c, True, (31, 0), f"{big}")
+
+
+@pytest.mark.parametrize("far", [26, 40, 60, 100])
+@pytest.mark.parametrize("new", [None, [9, 5]])
+def test_large_values_of_small_weight(attn, new, far):  # noqa: F811
+    """A value 2^far times the others' whose weight is 2^-(far + 30): the others make the result."""
+    d = 64
+    c = kv8_case([150, 300], new, 32, 8, d, 32, seed=422, spread=0.0, scale=1.0)
+    # component 0 of q is 1 and of the keys 0, but for the far ones' -(far + 30) ln 2
+    c.q = bf16(c.q.double() * 2.0 ** -4)
+    c.q[..., 0] = 1
+    c.k_new[..., 0] = 0
+    rng = np.random.default_rng(5)
+    for b, n in enumerate(c.ctx):
+        k, v = rng.standard_normal((2, n, 8, d))
+        k[..., 0] = 0
+        at = [0, 41, n - 2]
+        k[at], v[at] = 0, v[at] * 2.0 ** far
+        k[at, :, 0] = -(far + 30) * np.log(2)
+        put_cached(c, b, np.arange(n), k=k, v=v)
+    if new is None:
+        check_decode(attn, c, f"{far}")
+    else:
+        check_chunk(attn, c, what=f"{far}")
+
+
+@pytest.mark.parametrize("new", [None, [9, 5]])
+def test_large_values_first_then_larger_logits(attn, new):  # noqa: F811
+    """A large value that carried all the weight until keys came whose logits are far above its own."""
+    d = 64
+    c = kv8_case([600, 300], new, 32, 8, d, 32, seed=423, spread=0.0, scale=1.0)
+    c.q = bf16(c.q.double() * 2.0 ** -4)
+    c.q[..., 0] = 1
+    c.k_new[..., 0] = 70
+    rng = np.random.default_rng(6)
+    for b, n in enumerate(c.ctx):
+        k, v = rng.standard_normal((2, n, 8, d))
+        k[..., 0] = np.where(np.arange(n) < 100, 0.0, 70.0)[:, None]
+        v[:100] *= 2.0 ** 60
+        put_cached(c, b, np.arange(n), k=k, v=v)
+    if new is None:
+        check_decode(attn, c)
+    else:
+        check_chunk(attn, c)
+
+
+@pytest.mark.parametrize("new", [None, SHORT])
+@pytest.mark.parametrize("e", [-60, -100, -120])
+def test_tiny_values(attn, e, new):  # noqa: F811
+    """Values down to bf16's smallest: O is as exact as its type holds it."""
+    c = kv8_case([150, 300], new, 32, 8, 64, 32, seed=424)
+    rng = np.random.default_rng(7)
+    for b, n in enumerate(c.ctx):
+        put_cached(c, b, np.arange(n), v=rng.standard_normal((n, 8, 64)) * 2.0 ** e)
+    c.v_new = bf16(c.v_new.double() * 2.0 ** e)
+    out, lse = decode(attn, c) if new is None else chunk(attn, c, gpu_cache(c))
+    O, LSE, dS, W = reference(c, [t.numpy() for t in c.cache] if new is None else kv8_exact.appended(c))
+    # (2^e taken out: bf16 values below 2^-126 are spaced 2^-133, which 2^(-133 - e) adds)
+    out = out.double().cpu().numpy() * 2.0 ** -e
+    err = np.abs(out - O * 2.0 ** -e)
+    x = dS * 64 * 2.0 ** -23
+    bound = 2.0 ** -8 * np.abs(O) * 2.0 ** -e + (1 + 2.0 ** -8) * (
+        np.expm1(2 * x) + 2.0 ** -11 + 2.0 ** -20)[..., None] * W * 2.0 ** -e + 2.0 ** (-133 - e)
+    assert np.all(err <= bound), (err / bound).max()
 
 
 @pytest.mark.parametrize("rotary,inter", [(64, False), (32, True), (48, False)])
