@@ -261,16 +261,18 @@ __global__ void __launch_bounds__(kKv8Threads, 2)
         bool ok = true;
         while (ok && w.next(p, count)) {
             const int* bt = p.block_table + static_cast<size_t>(w.b) * p.max_pages;
+            // the first key that any of the sequence's rows sees
+            const int key_lo = p.wl >= 0 ? max(0, w.s.L - w.s.Lq - p.wl) : 0;
             for (int c = w.c0; c < w.c1; ++c, ++issued) {
                 const uint32_t st = issued % C::kStages;
-                // Pieces wholly past the sequence end (whose table entries are never read) and
-                // pieces of a bad page are aimed past the end of the cache: TMA fills them with
-                // zeros.
+                // Pieces wholly past the sequence end or before its first key that is seen (whose
+                // table entries are never read) and pieces of a bad page are aimed past the end of
+                // the cache: TMA fills them with zeros.
                 int page = p.num_pages, slot = 0;
                 bool real = false;
                 if (lane < pieces) {
                     const int key = c * kKv8Chunk + lane * p.box_rows;
-                    if (key < w.s.L) {
+                    if (key < w.s.L && key + p.box_rows > key_lo) {
                         page = bt[key / p.page_size];
                         slot = key % p.page_size;
                         real = page >= 0 && page < p.num_pages;
@@ -499,14 +501,19 @@ __global__ void __launch_bounds__(kKv8Threads, 2)
                 }
                 uint32_t sel[4] = {0x3120u, 0x3120u, 0x3120u, 0x3120u};
                 const bool masked = key0 < full_lo || key0 + 31 > full_hi;
-                if (masked && key0 + 32 > L) {
-                    // keys past the end: their slots may hold anything
+                if (masked) {
+                    // keys that no row of the unit sees (past the end, behind the last row's position,
+                    // before the first one's window): their slots may hold anything
+                    int lo, hi, none;
+                    row_key_interval(row0 / p.g, Lq, L, p.causal, p.wl, p.wr, lo, none);
+                    row_key_interval((row0 + rows - 1) / p.g, Lq, L, p.causal, p.wl, p.wr, none, hi);
 #pragma unroll
                     for (int nt = 0; nt < 4; ++nt) {
                         const int j = key0 + 8 * nt + 2 * tq;
-                        if (j >= L) ks[nt][0] = vs[nt][0] = 0.f;
-                        if (j + 1 >= L) ks[nt][1] = vs[nt][1] = 0.f;
-                        sel[nt] = (j < L ? 0x0100u : 0x0404u) | (j + 1 < L ? 0x3020u : 0x4040u);
+                        const bool see0 = lo <= j && j <= hi, see1 = lo <= j + 1 && j + 1 <= hi;
+                        if (!see0) ks[nt][0] = vs[nt][0] = 0.f;
+                        if (!see1) ks[nt][1] = vs[nt][1] = 0.f;
+                        sel[nt] = (see0 ? 0x0100u : 0x0404u) | (see1 ? 0x3020u : 0x4040u);
                     }
                 }
 #pragma unroll
@@ -630,7 +637,7 @@ __global__ void __launch_bounds__(kKv8Threads, 2)
                 // O += P V.  A transposed 8 x 8 matrix of byte pairs gives the thread elements
                 // 2 gq, 2 gq + 1 of keys 2 tq, 2 tq + 1: the pair of even elements is one n-tile's
                 // operand, the odd pair the next one's.  The selector puts them in that order and
-                // takes zeros for keys past the end.
+                // takes zeros for keys that no row sees.
                 const uint32_t vbase = kbase + C::kTileBytes;
 #pragma unroll
                 for (int u = 0; u < D / 16; u += 2) {

@@ -394,8 +394,9 @@ size_t attn_decode_kvcache_fp8_workspace_bytes(int batch, int nheads_q, int nhea
  *                 ATTN_ERR_DEVICE_BOUNDS)
  *   causal, window_left, window_right   see "Visibility"
  *   workspace     attn_fwd_kvcache_fp8_workspace_bytes(...) bytes, 256-byte aligned
- * A NaN or an infinity among the new values reaches the rows that see it, and may reach the other
- * new tokens of its sequence, as in attn_fwd.
+ * A NaN or an infinity among the keys and values reaches the rows that see it, and may reach other new
+ * tokens of its sequence, as in attn_fwd.  Nothing before the first key that any new token of a sequence
+ * sees is looked at: pages that end there may be given up, their table entries may hold anything.
  */
 attn_status_t attn_fwd_kvcache_fp8(const void* q, const void* k_new, const void* v_new,
                                    void* k_cache, void* v_cache, void* k_scale, void* v_scale,

@@ -300,6 +300,30 @@ def test_tiny_values(attn, e, new):  # noqa: F811
     assert np.all(err <= bound), (err / bound).max()
 
 
+@pytest.mark.parametrize("rotary", [0, 64])
+@pytest.mark.parametrize("new", [SHORT, LONG])
+def test_nothing_before_the_window_is_looked_at(attn, new, rotary):  # noqa: F811
+    """Pages that end before the first key that a new token sees are given up (-1 in the table), and
+    the slots of its own page before it hold NaN."""
+    window = 70
+    c = kv8_case([1000, 333], new, 32, 8, 64, 16, seed=430, rotary_dim=rotary, spread=0.5)
+    for b, n in enumerate(c.ctx):
+        first = n - window
+        c.block_table[b, :first // 16] = -1
+        page = int(c.block_table[b, first // 16])
+        for t in (c.k_cache, c.v_cache):
+            t[page, :first % 16] = 0x7F
+        for t in (c.k_scale, c.v_scale):
+            t[page, :, :first % 16] = 255
+    cache = gpu_cache(c)
+    out, lse = chunk(attn, c, cache, True, (window, 0))
+    assert attn.attn_get_device_status() == 0
+    # the same with everything before the window in order
+    good = kv8_case([1000, 333], new, 32, 8, 64, 16, seed=430, rotary_dim=rotary, spread=0.5)
+    ref = reference(good, kv8_exact.appended(good), True, (window, 0))
+    kv8_exact.check(out, lse.t(), ref, 2.0 ** -11, rotary > 0)
+
+
 @pytest.mark.parametrize("rotary,inter", [(64, False), (32, True), (48, False)])
 @pytest.mark.parametrize("e", [-133, -130, -128, -126, -122, -118, -100, 0, 100, 120, 126, 127])
 def test_append_rotates_rows_of_any_size(attn, e, rotary, inter):  # noqa: F811
