@@ -1062,6 +1062,9 @@ __device__ void fwd_softmax(const FwdParams& p, uint8_t* smem, FwdBars* bars, ui
                 }
             }
         }
+        // (f16 operands: the LSE of a row that sees a NaN key is NaN, -infinity would stand for no keys)
+        const bool some_a = is_f16(kOps) ? l_a != 0.f : l_a > 0.f;
+        const bool some_b = is_f16(kOps) ? l_b != 0.f : l_b > 0.f;
         if constexpr (is_f16(kOps)) m_a -= kF16Up, m_b -= kF16Up;
         const int tok_a = tv.tok0 + ra / g, tok_b = tv.tok0 + (ra + 8) / g;
         const bool valid_a = ra < tile_rows && tok_a < it.Lq;
@@ -1069,10 +1072,10 @@ __device__ void fwd_softmax(const FwdParams& p, uint8_t* smem, FwdBars* bars, ui
         if ((lane & 3) == 0) {
             if (valid_a && ATTN_IN_BOUNDS(it.q0 + tok_a < p.total_q, p.status))
                 p.lse[static_cast<size_t>(it.kvh * g + ra % g) * p.total_q + it.q0 + tok_a] =
-                    l_a > 0.f ? (m_a + __log2f(l_a)) * kLn2 : -INFINITY;
+                    some_a ? (m_a + __log2f(l_a)) * kLn2 : -INFINITY;
             if (valid_b && ATTN_IN_BOUNDS(it.q0 + tok_b < p.total_q, p.status))
                 p.lse[static_cast<size_t>(it.kvh * g + (ra + 8) % g) * p.total_q + it.q0 + tok_b] =
-                    l_b > 0.f ? (m_b + __log2f(l_b)) * kLn2 : -INFINITY;
+                    some_b ? (m_b + __log2f(l_b)) * kLn2 : -INFINITY;
         }
     }
 }

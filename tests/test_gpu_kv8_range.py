@@ -324,6 +324,27 @@ def test_nothing_before_the_window_is_looked_at(attn, new, rotary):  # noqa: F81
     kv8_exact.check(out, lse.t(), ref, 2.0 ** -11, rotary > 0)
 
 
+@pytest.mark.parametrize("rotary", [0, 64])
+@pytest.mark.parametrize("new", [SHORT, LONG])
+def test_rows_that_see_a_nan_key_say_so(attn, new, rotary):  # noqa: F811
+    """O and LSE of every row that sees it are NaN: an LSE of -infinity would stand for no keys."""
+    c = kv8_case([40, 300], new, 32, 8, 64, 16, seed=440, rotary_dim=rotary, spread=0.5)
+    c.k_cache[int(c.block_table[0, 1]), 3, 2, 5] = 0x7F      # kv head 2 of sequence 0
+    c.v_scale[int(c.block_table[1, 0]), 5, 2] = 255          # kv head 5 of sequence 1
+    cache = gpu_cache(c)
+    out, lse = chunk(attn, c, cache)
+    arrays = kv8_exact.appended(c)
+    same_stored(cache, arrays)
+    a, b = new_rows(c, 0), new_rows(c, 1)
+    assert torch.isnan(out[a, 8:12]).all() and torch.isnan(lse[8:12, a]).all()
+    assert torch.isnan(out[b, 20:24]).all()                  # a NaN value: O alone
+    assert torch.isfinite(lse[20:24, b]).all()
+    ref = reference(c, arrays)
+    for rows, heads in ((a, slice(0, 8)), (a, slice(12, 32)), (b, slice(0, 20)), (b, slice(24, 32))):
+        kv8_exact.check(out[rows, heads], lse[heads, rows].t(), [x[rows, heads] for x in ref], 2.0 ** -11,
+                        rotary > 0)
+
+
 @pytest.mark.parametrize("rotary,inter", [(64, False), (32, True), (48, False)])
 @pytest.mark.parametrize("e", [-133, -130, -128, -126, -122, -118, -100, 0, 100, 120, 126, 127])
 def test_append_rotates_rows_of_any_size(attn, e, rotary, inter):  # noqa: F811
