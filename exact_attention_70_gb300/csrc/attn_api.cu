@@ -901,13 +901,18 @@ int kv8_tiles(int rotary_dim) { return rotary_dim > 0 ? 1 : kFwdTilesPerItem; }
 struct Kv8StageLayout {
     long long rows;   // of k and v
     long long items;  // of the work list, per kv head
-    size_t k, v, spans, k_unit, v_unit, list, total;
+    size_t k, v, spans, k_unit, v_unit, k_sb, v_sb, list, total;
 };
+
+// Every sequence ends on a whole key block; even, for the prefill kernel reads scale bytes in pairs.
+long long kv8_staged_rows(int batch, int max_total_k) {
+    return (static_cast<long long>(max_total_k) + static_cast<long long>(kFwdBlockN) * batch + 1) / 2 * 2;
+}
 
 Kv8StageLayout kv8_stage_layout(int batch, int max_seqlen_q, int max_total_k, int nheads_q,
                                 int nheads_kv, int head_dim, int tiles) {
     Kv8StageLayout l;
-    l.rows = static_cast<long long>(max_total_k) + static_cast<long long>(kFwdBlockN) * batch;
+    l.rows = kv8_staged_rows(batch, max_total_k);
     const size_t bytes = align_up(static_cast<size_t>(l.rows) * nheads_kv * head_dim * 2, 256);
     const size_t units = align_up(static_cast<size_t>(batch) * nheads_kv * sizeof(float), 256);
     l.k = 0;
@@ -915,7 +920,10 @@ Kv8StageLayout kv8_stage_layout(int batch, int max_seqlen_q, int max_total_k, in
     l.spans = 2 * bytes;
     l.k_unit = l.spans + align_up(static_cast<size_t>(batch) * sizeof(int2), 256);
     l.v_unit = l.k_unit + units;
-    l.list = l.v_unit + units;
+    const size_t scales = align_up(static_cast<size_t>(l.rows) * nheads_kv, 256);
+    l.k_sb = l.v_unit + units;
+    l.v_sb = l.k_sb + scales;
+    l.list = l.v_sb + scales;
     const long long per = static_cast<long long>(tiles) * tokens_per_tile(nheads_q / nheads_kv);
     l.items = batch * ((max_seqlen_q + per - 1) / per);
     l.total = l.list + sizeof(FwdWorkspaceHeader) + align_up(sizeof(int) * (batch + 1), 16) +
@@ -1152,7 +1160,7 @@ attn_status_t attn_fwd_kvcache_fp8(const void* q, const void* k_new, const void*
     const int grid = staged ? 0
                             : kv8_grid(batch, max_seqlen_q, nheads_q, nheads_kv, page_size,
                                        max_pages_per_seq);
-    if (staged ? (static_cast<long long>(max_total_k) + 128LL * batch) * nheads_kv > (1LL << 31) - 1
+    if (staged ? kv8_staged_rows(batch, max_total_k) * nheads_kv > (1LL << 31) - 1
                : grid == 0)
         return ATTN_ERR_UNSUPPORTED;
     const size_t need = attn_fwd_kvcache_fp8_workspace_bytes(
@@ -1246,6 +1254,9 @@ attn_status_t attn_fwd_kvcache_fp8(const void* q, const void* k_new, const void*
         sp.spans = reinterpret_cast<int2*>(ws + l.spans);
         sp.k_unit = reinterpret_cast<float*>(ws + l.k_unit);
         sp.v_unit = reinterpret_cast<float*>(ws + l.v_unit);
+        sp.k_sb = ws + l.k_sb;
+        sp.v_sb = ws + l.v_sb;
+        sp.by_row = &header->by_row;
         sp.status = dev->status;
         sp.batch = batch;
         sp.total_q = total_q;
@@ -1290,6 +1301,9 @@ attn_status_t attn_fwd_kvcache_fp8(const void* q, const void* k_new, const void*
         fp.q_unit = ap.q_unit;
         fp.k_unit = sp.k_unit;
         fp.v_unit = sp.v_unit;
+        fp.k_sb = sp.k_sb;
+        fp.v_sb = sp.v_sb;
+        fp.staged_rows = sp.rows;
         if (launch_fwd(fp, head_dim, dev->num_sms, s) != cudaSuccess) return ATTN_ERR_CUDA;
         return ATTN_OK;
     }

@@ -32,7 +32,11 @@
 //
 // Instances with f16 operands (kOps) serve the 8-bit cache: Q, K and V are f16 multiples of powers
 // of two (of a query row, of a sequence and kv head), which join the softmax scale and the
-// epilogue's 1 / l, and P is f16 (kF16Up).
+// epilogue's 1 / l, and P is f16 (kF16Up).  Where the rows' scales of a (sequence, kv head) lie too far
+// apart for one unit, K and V are the codes, the keys' scales meet S and the values' P in fp32
+// (by_row).  An instance of its own behind the other one computes such items anew: it starts as that one's
+// CTAs end and leaves at once where there are none.  The same loop for both kinds, a loop beside it, a call
+// or a second pass over the list by the same kernel cost the other items 57, 9, 7 and 4%.
 // Rotated queries need more than 11 bits: rounding them moves LSE by 1e-5 to 1e-4 of itself where a
 // row sees few keys.  They come as hi + lo, two f16 numbers (kF16HiLo): S = Q_hi K^T + Q_lo K^T,
 // half as many MMAs again.  Both parts of two tiles would not fit in shared memory, so an item is
@@ -55,9 +59,11 @@ namespace attn {
 
 namespace {
 
-// Operands of the products: bf16; f16; f16 with Q in two parts.
-constexpr int kBf16 = 0, kF16 = 1, kF16HiLo = 2;
+// Operands of the products: bf16; f16; f16 with Q in two parts; the last two with scales by row.
+constexpr int kBf16 = 0, kF16 = 1, kF16HiLo = 2, kF16Rows = 3, kF16HiLoRows = 4;
 __host__ __device__ constexpr bool is_f16(int ops) { return ops != kBf16; }
+__host__ __device__ constexpr bool is_hilo(int ops) { return ops == kF16HiLo || ops == kF16HiLoRows; }
+__host__ __device__ constexpr bool by_row(int ops) { return ops == kF16Rows || ops == kF16HiLoRows; }
 
 constexpr float kRescaleThreshold = 8.0f;  // log2 units
 // f16 P goes to the tensor cores times 2^7: at most 2^15, and 11 bits down to weights of 2^-21 of the
@@ -79,8 +85,9 @@ struct FwdCfg {
     static constexpr int kOffP = kOffQ + kFwdTilesPerItem * kQTile;
     static constexpr int kOffKV = kOffP + kFwdTilesPerItem * kPTile;
     static constexpr int kOffBar = kOffKV + kSlots * kKvTile;
-    static constexpr int kOffMerge = kOffBar + 512;        // the second stream's (m, l) [128] (kF16HiLo)
-    static constexpr int kSmem = kOffMerge + 1024 + 1024;  // + alignment slack
+    static constexpr int kOffMerge = kOffBar + 512;        // the second stream's (m, l) [128] (kF16HiLo),
+    static constexpr int kOffMergeE = kOffMerge + 1024;    //   and E [128], a byte each
+    static constexpr int kSmem = kOffMergeE + 128 + 1024;  // + alignment slack
     static_assert(kSmem <= 227 * 1024, "shared memory per CTA");
     static constexpr uint32_t kTmemCols = 512;
     // TMEM columns of S_t (fp32) and O_t (fp32)
@@ -90,7 +97,7 @@ struct FwdCfg {
     // shared memory twice otherwise (8 chunks of 2048 tokens, 8000 keys, 16:4 heads: 867 -> 820 us).  At
     // d 128 it would lie over S_t, and S_t(j + 1) would wait for P_t(j)'s product (8 x 2048 tokens, 32:8
     // heads: 2290 -> 2322 us).
-    static constexpr bool kPInTmem = kOps == kF16HiLo && D == 64;
+    static constexpr bool kPInTmem = is_hilo(kOps) && D == 64;
     __device__ static constexpr uint32_t col_p(int t) { return 256u + 2 * D + 64u * t; }
 };
 
@@ -144,6 +151,7 @@ __device__ __forceinline__ Item load_item(const FwdParams& p, int idx) {
         const int2 span = p.spans[it.b];
         it.k0 = span.x;
         it.Lk = span.y;
+        if (by_row(kOps) && p.k_unit[it.b * p.Hkv + it.kvh] != 0.f) it.Lq = 0;  // done already
     } else {
         it.k0 = p.cu_k[it.b];
         it.Lk = p.cu_k[it.b + 1] - it.k0;
@@ -153,7 +161,7 @@ __device__ __forceinline__ Item load_item(const FwdParams& p, int idx) {
     it.any = false;
 #pragma unroll
     for (int t = 0; t < 2; ++t) {
-        it.tok0[t] = (kOps == kF16HiLo ? m : 2 * m + t) * p.tpt;
+        it.tok0[t] = (is_hilo(kOps) ? m : 2 * m + t) * p.tpt;
         it.rows[t] = it.tok0[t] < it.Lq;
         it.imin[t] = it.tok0[t];
         it.imax[t] = min(it.tok0[t] + p.tpt, it.Lq) - 1;
@@ -164,7 +172,7 @@ __device__ __forceinline__ Item load_item(const FwdParams& p, int idx) {
                                              p.causal, p.wl, p.wr);
             it.lo[t] = r.lo;
             it.hi[t] = r.hi;
-            it.mma[t] = r.hi > r.lo + (kOps == kF16HiLo ? t : 0);
+            it.mma[t] = r.hi > r.lo + (is_hilo(kOps) ? t : 0);
             if (it.mma[t]) {
                 it.jlo = min(it.jlo, r.lo);
                 it.jhi = max(it.jhi, r.hi);
@@ -177,7 +185,7 @@ __device__ __forceinline__ Item load_item(const FwdParams& p, int idx) {
 
 template <int kOps>
 __device__ __forceinline__ bool tile_uses(const Item& it, int t, int j) {
-    if (kOps == kF16HiLo) return it.mma[t] && ((j - it.jlo) & 1) == t;
+    if (is_hilo(kOps)) return it.mma[t] && ((j - it.jlo) & 1) == t;
     return it.mma[t] && it.lo[t] <= j && j < it.hi[t];
 }
 
@@ -203,13 +211,14 @@ constexpr uint32_t kIdxReaders = 18;  // the two MMA issuers and the 16 softmax 
 
 // The producer's claim of ring position r (false: a wait gave up).  Slot r % 4 last held
 // position r - 4, which every reader took before its own item r - 3.
+template <int kOps>
 __device__ __forceinline__ bool fwd_claim_item(const FwdParams& p, FwdBars* bars,
                                                const Watchdog& wd, int n_items, uint32_t r,
                                                int& idx) {
     const uint32_t slot = r % kIdxRing;
     if (r >= kIdxRing && !wd.wait(&bars->idx_empty[slot], ((r / kIdxRing) - 1) & 1))
         return false;
-    idx = atomicAdd(&p.header->next_item, 1);
+    idx = atomicAdd(by_row(kOps) ? &p.header->next_by_row : &p.header->next_item, 1);
     if (idx >= n_items) idx = -1;
     bars->idx_ring[slot] = idx;
     mbar_arrive(&bars->idx_full[slot]);  // release: the index is visible to the readers
@@ -276,13 +285,13 @@ __device__ void fwd_producer_loop(const FwdParams& p, uint8_t* smem, FwdBars* ba
     const uint32_t q_box_bytes = 64u * p.g * p.tpt * 2u;
     uint32_t claims = 0;
     int idx;
-    if (!fwd_claim_item(p, bars, wd, n_items, claims++, idx)) return;
+    if (!fwd_claim_item<kOps>(p, bars, wd, n_items, claims++, idx)) return;
     while (idx >= 0) {
         const Item it = load_item<kPaged, kOps>(p, idx);
         int next = -1;
         bool claimed = false;
         if (!it.any) {
-            if (!fwd_claim_item(p, bars, wd, n_items, claims++, next)) return;
+            if (!fwd_claim_item<kOps>(p, bars, wd, n_items, claims++, next)) return;
             idx = next;
             continue;
         }
@@ -291,15 +300,15 @@ __device__ void fwd_producer_loop(const FwdParams& p, uint8_t* smem, FwdBars* ba
         uint32_t qbytes = 0;
 #pragma unroll
         for (int t = 0; t < 2; ++t)
-            if (kOps == kF16HiLo || it.mma[t]) qbytes += q_box_bytes * C::kHalves;
+            if (is_hilo(kOps) || it.mma[t]) qbytes += q_box_bytes * C::kHalves;
         mbar_arrive_expect_tx(&bars->q_full, qbytes);
 #pragma unroll
         for (int t = 0; t < 2; ++t) {
-            if (kOps != kF16HiLo && !it.mma[t]) continue;
+            if (!is_hilo(kOps) && !it.mma[t]) continue;
 #pragma unroll
             for (int h = 0; h < C::kHalves; ++h)
                 tma_load_3d(smem + C::kOffQ + t * C::kQTile + h * C::kAtomBytes,
-                            kOps == kF16HiLo && t == 1 ? &p.tm_qlo : &p.tm_q, &bars->q_full, h * 64,
+                            is_hilo(kOps) && t == 1 ? &p.tm_qlo : &p.tm_q, &bars->q_full, h * 64,
                             it.kvh * p.g, it.q0 + it.tok0[t]);
         }
         ++q_cnt;
@@ -356,7 +365,7 @@ __device__ void fwd_producer_loop(const FwdParams& p, uint8_t* smem, FwdBars* ba
             // that claims follow the order in which CTAs free up, early enough that the
             // claim's round trip is hidden behind the blocks still to come
             if (!claimed && r == max(min(1, 2 * m - 1), 2 * m - 5)) {
-                if (!fwd_claim_item(p, bars, wd, n_items, claims++, next)) return;
+                if (!fwd_claim_item<kOps>(p, bars, wd, n_items, claims++, next)) return;
                 claimed = true;
             }
         }
@@ -420,14 +429,14 @@ __device__ void fwd_mma_s(const FwdParams& p, uint8_t* smem, FwdBars* bars, uint
                 uint32_t& sc = t ? s_cnt1 : s_cnt0;
                 if (sc > 0 && !wd.wait(&bars->s_free[t], (sc - 1) & 1)) return;
                 tc_fence_after();
-                const uint32_t a_lo = q_lo + (kOps == kF16HiLo ? 0 : t * (C::kQTile >> 4));
+                const uint32_t a_lo = q_lo + (is_hilo(kOps) ? 0 : t * (C::kQTile >> 4));
 #pragma unroll
                 for (int kk = 0; kk < D / 16; ++kk) {
                     const uint32_t off = ((kk >> 2) * C::kAtomBytes + (kk & 3) * 32) >> 4;
                     umma_ss_lh(tmem + C::col_s(t), a_lo + off, d_hi, k_lo + off, d_hi, kIdesc,
                                kk > 0);
                 }
-                if (kOps == kF16HiLo) {
+                if (is_hilo(kOps)) {
 #pragma unroll
                     for (int kk = 0; kk < D / 16; ++kk) {
                         // Components that do not turn are bf16 numbers and have no low part (4 x 2048
@@ -549,9 +558,32 @@ __device__ __forceinline__ uint32_t sw128_unit(uint32_t base, int r, int u) {
     return base + (u >> 3) * (128 * 128) + r * 128 + (((u & 7) ^ (r & 7)) << 4);
 }
 
+// The scales of this thread's two keys of 8-key chunk c (byte b is 2^(b - 127); the pair's address is even,
+// staged_rows is).
+__device__ __forceinline__ float2 row_scales(const uint8_t* sb, int c) {
+    const int w = *reinterpret_cast<const uint16_t*>(sb + 8 * c);
+    return make_float2(__int_as_float((w & 0xff) << 23), __int_as_float((w & 0xff00) << 15));
+}
+
+// The largest of a row's four threads.
+__device__ __forceinline__ float quad_max(float x) {
+    x = fmaxf(x, __shfl_xor_sync(0xffffffffu, x, 1));
+    return fmaxf(x, __shfl_xor_sync(0xffffffffu, x, 2));
+}
+
+// E of a row (a scale byte) that has met P 2^ev up to 2^pv, its reference moving from m to m_new, and what O
+// is to be multiplied with.
+__device__ __forceinline__ int raised_e(int e, float pv, float m, float m_new, float& alpha) {
+    if (m_new == -INFINITY) return e;  // no key seen
+    const int e_new = min(max(static_cast<int>(ceilf(fmaxf(pv - m_new, m - m_new + e))), 0), 253);
+    alpha = ex2_approx(m - m_new + (e - e_new));
+    return e_new;
+}
+
 template <int D, bool kPaged, bool kMods, int kOps>
 __device__ void fwd_softmax(const FwdParams& p, uint8_t* smem, FwdBars* bars, uint32_t tmem,
                             const Watchdog& wd, int n_items, int t, int k, int lane) {
+    constexpr bool kByRow = by_row(kOps);
     using C = FwdCfg<D, kOps>;
     uint64_t* const s_full = &bars->s_full[t];
     uint64_t* const s_free = &bars->s_free[t];
@@ -621,18 +653,20 @@ __device__ void fwd_softmax(const FwdParams& p, uint8_t* smem, FwdBars* bars, ui
         }
         const TileView tv = tile_view(it, t);
         if (!tv.rows) continue;
-        if (kOps == kF16HiLo && t == 1 && !tv.mma) continue;  // no block for the second stream
-        const int j0 = tv.lo + (kOps == kF16HiLo ? t : 0), jstep = kOps == kF16HiLo ? 2 : 1;
+        if (is_hilo(kOps) && t == 1 && !tv.mma) continue;  // no block for the second stream
+        const int j0 = tv.lo + (is_hilo(kOps) ? t : 0), jstep = is_hilo(kOps) ? 2 : 1;
         // f16 operands come as multiples of a unit per query row and per (sequence, kv head)
-        float sl2_a = sl2, sl2_b = sl2;
+        float sl2_a = sl2, sl2_b = sl2, qu_a = 1.f, qu_b = 1.f;
+        int e_a = 0, e_b = 0;  // kByRow: the rows' E, as scale bytes
         if constexpr (is_f16(kOps)) {
-            const float ku = p.k_unit[it.b * p.Hkv + it.kvh];
             const int ta = tv.tok0 + ra / g, tb = tv.tok0 + (ra + 8) / g;
             const float* qu = p.q_unit + it.kvh * g;
-            sl2_a = f16_logit_unit(
-                sl2, ku, ta < it.Lq ? qu[static_cast<size_t>(it.q0 + ta) * p.Hq + ra % g] : 1.f);
-            sl2_b = f16_logit_unit(
-                sl2, ku, tb < it.Lq ? qu[static_cast<size_t>(it.q0 + tb) * p.Hq + (ra + 8) % g] : 1.f);
+            const float qa = ta < it.Lq ? qu[static_cast<size_t>(it.q0 + ta) * p.Hq + ra % g] : 1.f;
+            const float qb = tb < it.Lq ? qu[static_cast<size_t>(it.q0 + tb) * p.Hq + (ra + 8) % g] : 1.f;
+            const float ku = p.k_unit[it.b * p.Hkv + it.kvh];
+            sl2_a = kByRow ? 1.f : f16_logit_unit(sl2, ku, qa);
+            sl2_b = kByRow ? 1.f : f16_logit_unit(sl2, ku, qb);
+            qu_a = qa, qu_b = qb;
         }
         // this thread's rows ra and ra + 8; packed row r is token tok0 + r / g, head kvh g + r % g
         float m_a = -INFINITY, m_b = -INFINITY, l_a = 0.f, l_b = 0.f;  // l: this thread's part
@@ -668,6 +702,23 @@ __device__ void fwd_softmax(const FwdParams& p, uint8_t* smem, FwdBars* bars, ui
                 tc_fence_before();
                 __syncwarp();
                 if (lane == 0) mbar_arrive(s_free);
+                // kByRow: the scale bytes of this thread's keys
+                const size_t sb_at =
+                    kByRow ? static_cast<size_t>(it.kvh) * p.staged_rows + it.k0 + j * kFwdBlockN + cpair : 0;
+                if constexpr (kByRow) {
+#pragma unroll
+                    for (int c = 0; c < 16; ++c) {
+                        const float2 ks = row_scales(p.k_sb + sb_at, c);
+#pragma unroll
+                        for (int e = 0; e < 2; ++e) {  // (finite factors: S may be 0)
+                            const float k = e ? ks.y : ks.x;
+                            s[4 * c + e] = __float_as_uint(__uint_as_float(s[4 * c + e]) *
+                                                           fminf(fminf(k * qu_a, 0x1p127f) * sl2, 0x1p127f));
+                            s[4 * c + 2 + e] = __float_as_uint(__uint_as_float(s[4 * c + 2 + e]) *
+                                                               fminf(fminf(k * qu_b, 0x1p127f) * sl2, 0x1p127f));
+                        }
+                    }
+                }
                 // per-row constants of this block added to the logits in log2 units (ALiBi)
                 float ca = 0.f, cb = 0.f;    // this thread's columns
                 float qa = 0.f, qb = 0.f;    // S-unit shift of its columns to the block start
@@ -778,10 +829,25 @@ __device__ void fwd_softmax(const FwdParams& p, uint8_t* smem, FwdBars* bars, ui
                 const bool need_a = mba > m_a + kRescaleThreshold;
                 const bool need_b = mbb > m_b + kRescaleThreshold;
                 const float mna = need_a ? mba : m_a, mnb = need_b ? mbb : m_b;
-                const float alpha_a = need_a ? ex2_approx(m_a - mna) : 1.f;
-                const float alpha_b = need_b ? ex2_approx(m_b - mnb) : 1.f;
+                float alpha_a = need_a ? ex2_approx(m_a - mna) : 1.f;
+                float alpha_b = need_b ? ex2_approx(m_b - mnb) : 1.f;
                 l_a *= alpha_a;
                 l_b *= alpha_b;
+                if constexpr (kByRow) {
+                    float pv_a = -INFINITY, pv_b = -INFINITY;  // the block's largest log2 P 2^ev (a scale byte)
+#pragma unroll
+                    for (int c = 0; c < 16; ++c) {
+                        const float2 vs = row_scales(p.v_sb + sb_at, c);
+#pragma unroll
+                        for (int e = 0; e < 2; ++e) {
+                            const float ev = static_cast<float>(__float_as_int(e ? vs.y : vs.x) >> 23);
+                            pv_a = fmaxf(pv_a, __uint_as_float(s[4 * c + e]) + ev);
+                            pv_b = fmaxf(pv_b, __uint_as_float(s[4 * c + 2 + e]) + ev);
+                        }
+                    }
+                    e_a = raised_e(e_a, quad_max(pv_a), m_a, mna, alpha_a);
+                    e_b = raised_e(e_b, quad_max(pv_b), m_b, mnb, alpha_b);
+                }
                 m_a = mna;
                 m_b = mnb;
                 const float ra_ref = (m_a == -INFINITY) ? 0.f : m_a;
@@ -801,6 +867,8 @@ __device__ void fwd_softmax(const FwdParams& p, uint8_t* smem, FwdBars* bars, ui
                 const uint64_t sb2 = is_f16(kOps) ? f2_make(sl2_b, sl2_b) : sl2x2;
                 uint64_t suma = 0, sumb = 0;
                 uint32_t pka[16], pkb[16];
+                const float to_a = kByRow ? exp2_int(127 - e_a) : 1.f;  // 2^-E
+                const float to_b = kByRow ? exp2_int(127 - e_b) : 1.f;
 #pragma unroll
                 for (int c = 0; c < 16; ++c) {
                     const uint64_t xa = f2_fma(f2_make(__uint_as_float(s[4 * c]), __uint_as_float(s[4 * c + 1])),
@@ -810,10 +878,15 @@ __device__ void fwd_softmax(const FwdParams& p, uint8_t* smem, FwdBars* bars, ui
                     float a0, a1, b0, b1;
                     f2_split(xa, a0, a1);
                     f2_split(xb, b0, b1);
-                    const float pa0 = ex2_approx(a0), pa1 = ex2_approx(a1);
-                    const float pb0 = ex2_approx(b0), pb1 = ex2_approx(b1);
+                    float pa0 = ex2_approx(a0), pa1 = ex2_approx(a1);
+                    float pb0 = ex2_approx(b0), pb1 = ex2_approx(b1);
                     suma = f2_add(suma, f2_make(pa0, pa1));
                     sumb = f2_add(sumb, f2_make(pb0, pb1));
+                    if constexpr (kByRow) {  // (finite factors: P may be 0)
+                        const float2 vs = row_scales(p.v_sb + sb_at, c);
+                        pa0 *= fminf(vs.x * to_a, 0x1p126f), pa1 *= fminf(vs.y * to_a, 0x1p126f);
+                        pb0 *= fminf(vs.x * to_b, 0x1p126f), pb1 *= fminf(vs.y * to_b, 0x1p126f);
+                    }
                     pka[c] = is_f16(kOps) ? pack_f16x2(pa0, pa1) : pack_bf16x2(pa0, pa1);
                     pkb[c] = is_f16(kOps) ? pack_f16x2(pb0, pb1) : pack_bf16x2(pb0, pb1);
                 }
@@ -851,7 +924,7 @@ __device__ void fwd_softmax(const FwdParams& p, uint8_t* smem, FwdBars* bars, ui
                     if (!__all_sync(0xffffffffu, wd.wait(pv_done, (blk - 1) & 1))) return;
                     tc_fence_after();
                 }
-                if (__any_sync(0xffffffffu, need_a || need_b) && j > j0) {
+                if ((kByRow || __any_sync(0xffffffffu, need_a || need_b)) && j > j0) {
 #pragma unroll 1
                     for (int cc = 0; cc < D / 32; ++cc) {
                         uint32_t o[16];
@@ -902,8 +975,9 @@ __device__ void fwd_softmax(const FwdParams& p, uint8_t* smem, FwdBars* bars, ui
             // kF16HiLo: the second stream hands over its rows' m and l once its last PV is done (O_1
             // stays in TMEM); the first one weighs both
             float w_a = 1.f, w_b = 1.f, w1_a = 0.f, w1_b = 0.f;
-            if constexpr (kOps == kF16HiLo) {
+            if constexpr (is_hilo(kOps)) {
                 float2* const rows_ml = reinterpret_cast<float2*>(smem + C::kOffMerge);
+                uint8_t* const rows_e = smem + C::kOffMergeE;
                 if (t == 1) {
                     if (merge_cnt > 0 &&
                         !__all_sync(0xffffffffu, wd.wait(&bars->merge_free, (merge_cnt - 1) & 1)))
@@ -912,6 +986,7 @@ __device__ void fwd_softmax(const FwdParams& p, uint8_t* smem, FwdBars* bars, ui
                     if ((lane & 3) == 0) {
                         rows_ml[ra] = make_float2(m_a, l_a);
                         rows_ml[ra + 8] = make_float2(m_b, l_b);
+                        if (kByRow) rows_e[ra] = e_a, rows_e[ra + 8] = e_b;
                     }
                     tc_fence_before();
                     __syncwarp();
@@ -923,6 +998,7 @@ __device__ void fwd_softmax(const FwdParams& p, uint8_t* smem, FwdBars* bars, ui
                     ++merge_cnt;
                     tc_fence_after();
                     const float2 ml_a = rows_ml[ra], ml_b = rows_ml[ra + 8];
+                    const int e1_a = kByRow ? rows_e[ra] : 0, e1_b = kByRow ? rows_e[ra + 8] : 0;
                     __syncwarp();
                     if (lane == 0) mbar_arrive(&bars->merge_free);
                     const float M_a = fmaxf(m_a, ml_a.x), M_b = fmaxf(m_b, ml_b.x);
@@ -935,6 +1011,14 @@ __device__ void fwd_softmax(const FwdParams& p, uint8_t* smem, FwdBars* bars, ui
                     l_b = l_b * w_b + ml_b.y * w1_b;
                     m_a = M_a;
                     m_b = M_b;
+                    if constexpr (kByRow) {  // both streams' O in units of the larger E
+                        w_a *= exp2_int(min(e_a - e1_a, 0));
+                        w_b *= exp2_int(min(e_b - e1_b, 0));
+                        w1_a *= exp2_int(min(e1_a - e_a, 0));
+                        w1_b *= exp2_int(min(e1_b - e_b, 0));
+                        e_a = max(e_a, e1_a);
+                        e_b = max(e_b, e1_b);
+                    }
                 }
             }
             if (C::kPInTmem && epi_pending && !staging_free()) return;
@@ -942,15 +1026,15 @@ __device__ void fwd_softmax(const FwdParams& p, uint8_t* smem, FwdBars* bars, ui
             float inv_b = l_b > 0.f ? 1.f / l_b : 0.f;
             if constexpr (is_f16(kOps)) {
                 const float unit = p.v_unit[it.b * p.Hkv + it.kvh];
-                inv_a *= unit;
-                inv_b *= unit;
+                inv_a *= kByRow ? exp2_int(e_a - 127) : unit;
+                inv_b *= kByRow ? exp2_int(e_b - 127) : unit;
             }
 #pragma unroll
             for (int cc = 0; cc < D / 64; ++cc) {
                 uint32_t o[32];
                 tmem_ld16x256_x8(tO + 64 * cc, o);
                 tmem_wait_ld();
-                if constexpr (kOps == kF16HiLo) {
+                if constexpr (is_hilo(kOps)) {
                     if (it.mma[1]) {
                         uint32_t o1[32];
                         tmem_ld16x256_x8(tO + C::col_o(1) - C::col_o(0) + 64 * cc, o1);
@@ -979,7 +1063,7 @@ __device__ void fwd_softmax(const FwdParams& p, uint8_t* smem, FwdBars* bars, ui
             tc_fence_before();
             __syncwarp();
             if (lane == 0) mbar_arrive(o_free);
-            if (kOps == kF16HiLo && it.mma[1] && lane == 0) mbar_arrive(&bars->o_free[1]);
+            if (is_hilo(kOps) && it.mma[1] && lane == 0) mbar_arrive(&bars->o_free[1]);
             if (tv.tok0 + p.tpt <= it.Lq) {
                 // Every packed row of the tile is a row of this sequence: one TMA store per
                 // 64 columns writes the tile's g * tpt rows, asynchronously.
@@ -1084,6 +1168,12 @@ template <int D, bool kPaged, bool kMods, int kOps>
 __global__ void __launch_bounds__(kFwdThreads, 1) fwd_kernel(const __grid_constant__ FwdParams p) {
     using C = FwdCfg<D, kOps>;
     extern __shared__ uint8_t smem_raw[];
+    if (by_row(kOps) && *reinterpret_cast<volatile int*>(&p.header->by_row) == 0) {
+        // (the instance before this one had waited for the flag when it let this one start; what waits for
+        // this grid waits for that one, too)
+        if (blockIdx.x == 0) griddep_wait();
+        return;
+    }
     uint8_t* smem = reinterpret_cast<uint8_t*>(
         (reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~static_cast<uintptr_t>(1023));
     FwdBars* bars = reinterpret_cast<FwdBars*>(smem + C::kOffBar);
@@ -1126,6 +1216,7 @@ __global__ void __launch_bounds__(kFwdThreads, 1) fwd_kernel(const __grid_consta
     // (launched as a programmatic dependent of the work-list kernel: the set-up above overlaps
     // that kernel; the list is read only once it has finished)
     griddep_wait();
+    if (is_f16(kOps) && !by_row(kOps)) griddep_launch_dependents();  // the instance behind this one
     const int n_items = p.header->n_items;
 
     // Registers: launched at 96 per thread (640 threads); warpgroup 4 (TMA, two MMA issuers,
@@ -1236,6 +1327,7 @@ __global__ void __launch_bounds__(kPrepThreads) fwd_prepare_kernel(FwdPrepParams
             p.header->n_items = 0;
             p.header->n_pairs = 0;
             p.header->next_item = 0;
+            p.header->by_row = p.header->next_by_row = 0;
         }
         return;
     }
@@ -1259,6 +1351,7 @@ __global__ void __launch_bounds__(kPrepThreads) fwd_prepare_kernel(FwdPrepParams
             p.header->n_items = 0;
             p.header->n_pairs = 0;
             p.header->next_item = 0;
+            p.header->by_row = p.header->next_by_row = 0;
         }
         return;
     }
@@ -1304,6 +1397,7 @@ __global__ void __launch_bounds__(kPrepThreads) fwd_prepare_kernel(FwdPrepParams
         p.header->n_pairs = n_pairs;
         p.header->n_items = n_pairs * p.Hkv;
         p.header->next_item = 0;
+        p.header->by_row = p.header->next_by_row = 0;
     }
 }
 
@@ -1325,6 +1419,10 @@ cudaError_t configure_fwd_kernels() {
     if (e == cudaSuccess) e = cudaFuncSetAttribute(fwd_kernel<64, false, false, kF16>, smem, FwdCfg<64>::kSmem);
     if (e == cudaSuccess) e = cudaFuncSetAttribute(fwd_kernel<128, false, false, kF16HiLo>, smem, FwdCfg<128>::kSmem);
     if (e == cudaSuccess) e = cudaFuncSetAttribute(fwd_kernel<64, false, false, kF16HiLo>, smem, FwdCfg<64>::kSmem);
+    if (e == cudaSuccess) e = cudaFuncSetAttribute(fwd_kernel<128, false, false, kF16Rows>, smem, FwdCfg<128>::kSmem);
+    if (e == cudaSuccess) e = cudaFuncSetAttribute(fwd_kernel<64, false, false, kF16Rows>, smem, FwdCfg<64>::kSmem);
+    if (e == cudaSuccess) e = cudaFuncSetAttribute(fwd_kernel<128, false, false, kF16HiLoRows>, smem, FwdCfg<128>::kSmem);
+    if (e == cudaSuccess) e = cudaFuncSetAttribute(fwd_kernel<64, false, false, kF16HiLoRows>, smem, FwdCfg<64>::kSmem);
     return e;
 }
 
@@ -1340,7 +1438,7 @@ cudaError_t launch_fwd_instance(const FwdParams& p, int grid, cudaStream_t strea
     cudaLaunchConfig_t cfg = {};
     cfg.gridDim = dim3(grid);
     cfg.blockDim = dim3(kFwdThreads);
-    cfg.dynamicSmemBytes = FwdCfg<D>::kSmem;
+    cfg.dynamicSmemBytes = FwdCfg<D, kOps>::kSmem;
     cfg.stream = stream;
     cudaLaunchAttribute attr[1];
     attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
@@ -1358,12 +1456,22 @@ cudaError_t launch_fwd(const FwdParams& p, int head_dim, int grid, cudaStream_t 
     const bool mods = p.softcap > 0.f || p.alibi != nullptr;
     const bool half = p.spans != nullptr;
     if ((paged && mods) || (half && (paged || mods))) return cudaErrorInvalidValue;
-    if (half && p.hi_lo)
-        return head_dim == 128 ? launch_fwd_instance<128, false, false, kF16HiLo>(p, grid, stream)
-                               : launch_fwd_instance<64, false, false, kF16HiLo>(p, grid, stream);
-    if (half)
-        return head_dim == 128 ? launch_fwd_instance<128, false, false, kF16>(p, grid, stream)
-                               : launch_fwd_instance<64, false, false, kF16>(p, grid, stream);
+    if (half) {
+        const bool wide = head_dim == 128;
+        cudaError_t e;
+        if (p.hi_lo) {
+            e = wide ? launch_fwd_instance<128, false, false, kF16HiLo>(p, grid, stream)
+                     : launch_fwd_instance<64, false, false, kF16HiLo>(p, grid, stream);
+            if (e != cudaSuccess) return e;
+            return wide ? launch_fwd_instance<128, false, false, kF16HiLoRows>(p, grid, stream)
+                        : launch_fwd_instance<64, false, false, kF16HiLoRows>(p, grid, stream);
+        }
+        e = wide ? launch_fwd_instance<128, false, false, kF16>(p, grid, stream)
+                 : launch_fwd_instance<64, false, false, kF16>(p, grid, stream);
+        if (e != cudaSuccess) return e;
+        return wide ? launch_fwd_instance<128, false, false, kF16Rows>(p, grid, stream)
+                    : launch_fwd_instance<64, false, false, kF16Rows>(p, grid, stream);
+    }
     if (head_dim == 128) {
         if (paged) return launch_fwd_instance<128, true, false, kBf16>(p, grid, stream);
         if (mods) return launch_fwd_instance<128, false, true, kBf16>(p, grid, stream);

@@ -43,7 +43,9 @@ struct FwdWorkspaceHeader {
     int n_items;
     int n_pairs;
     int next_item;  // the forward kernel's claim counter (reset by the work-list kernel)
-    int pad[61];
+    int by_row;     // staged f16 K/V: some (sequence, kv head) has no unit (set by the units kernel)
+    int next_by_row;  // the claim counter of the instance for those
+    int pad[59];
 };
 
 struct FwdPrepParams {
@@ -92,8 +94,11 @@ struct FwdParams {
     CUtensorMap tm_qlo;
     const int2* spans;
     const float* q_unit;  // [total_q, Hq]
-    const float* k_unit;  // [batch, Hkv]
+    const float* k_unit;  // [batch, Hkv]; 0: k and v are the codes, and each row's scale joins later
     const float* v_unit;
+    const uint8_t* k_sb;  // [Hkv, staged_rows]: those scales
+    const uint8_t* v_sb;
+    int staged_rows;
     int hi_lo;
     int low_steps;  // 16-component steps of q that have low parts
 };
@@ -242,8 +247,11 @@ struct StageFp8Params {
     __half* k;      // [rows, Hkv, d]
     __half* v;
     int2* spans;    // [batch]: first row, keys
-    float* k_unit;  // [batch, Hkv]: what one unit of k stands for
-    float* v_unit;
+    float* k_unit;  // [batch, Hkv]: what one unit of k stands for; 0: its rows' scales are too far apart
+    float* v_unit;  //   for one (of k or of v), k and v hold the codes and
+    uint8_t* k_sb;  // [Hkv, rows] the rows' scale bytes
+    uint8_t* v_sb;
+    int* by_row;    // set where there is such a pair
     unsigned* status;
     int batch, total_q, Hkv, page_size, max_pages, num_pages, wl, rows;
 };

@@ -490,7 +490,11 @@ __global__ void __launch_bounds__(kAppendThreads, 5)
 // A chunk of many query rows reads each key once per 256 rows, so it pays to turn the codes into
 // an MMA operand once, in f16: code 2^(e - E) with E = (the largest e of the sequence and kv head) - 7.
 // The largest magnitude is then 448 2^7 = 57344, below f16's 65504, and rows whose e is up to 22
-// below the largest stay exact (the smallest code 2^-9 meets f16's smallest 2^-24).
+// below the largest stay exact (the smallest code 2^-9 meets f16's smallest 2^-24).  Where a row of the
+// pair (of k or v; rows of the smallest scale, zeros, aside) lies further below, one large row,
+// perhaps one that most queries do not see, would cost the others their bits: then the codes go in as
+// they are, the scale bytes beside them, and the prefill kernel brings them together in fp32.
+constexpr int kUnitSpan = 22;
 
 // The first key that a new token of a sequence sees, and the keys from there on.
 __device__ __forceinline__ int2 staged_keys(const StageFp8Params& p, int b) {
@@ -508,7 +512,7 @@ constexpr int kUnitsThreads = 512;
 __global__ void __launch_bounds__(kUnitsThreads)
     kvcache_units_fp8_kernel(const StageFp8Params p) {
     constexpr int kWarps = kUnitsThreads / 32;
-    __shared__ int red[2][kWarps];
+    __shared__ int red[2][kWarps], red_low[2][kWarps];
     __shared__ long long sum[kWarps];
     const int b = blockIdx.x / p.Hkv, kvh = blockIdx.x % p.Hkv;
     const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
@@ -520,7 +524,8 @@ __global__ void __launch_bounds__(kUnitsThreads)
     for (int o = 16; o > 0; o >>= 1) before += __shfl_xor_sync(0xffffffffu, before, o);
     if (lane == 0) sum[warp] = before;
     const int2 keys = staged_keys(p, b);
-    int top[2] = {1, 1};  // scale bytes of K and V; 255 (NaN) does not count
+    // scale bytes of K and V, four columns; 255 (NaN) does not count, nor, for the smallest, 0 and 1
+    uint32_t top4[2] = {0u, 0u}, low4[2] = {~0u, ~0u};
     griddep_wait();       // the append kernel's scales
     const int* bt = p.block_table + static_cast<size_t>(b) * p.max_pages;
     const int end = keys.x + keys.y;
@@ -531,37 +536,53 @@ __global__ void __launch_bounds__(kUnitsThreads)
         const uint4 kw = *reinterpret_cast<const uint4*>(p.k_scale + at);
         const uint4 vw = *reinterpret_cast<const uint4*>(p.v_scale + at);
         const uint32_t w[2][4] = {{kw.x, kw.y, kw.z, kw.w}, {vw.x, vw.y, vw.z, vw.w}};
+        const int from = keys.x - g * 16, to = end - g * 16;  // tokens [from, to) count
 #pragma unroll
-        for (int i = 0; i < 16; ++i) {
-            if (g * 16 + i < keys.x || g * 16 + i >= end) continue;
+        for (int i = 0; i < 4; ++i) {
+            uint32_t in = ~0u;
+            if (from > 4 * i) in = from >= 4 * i + 4 ? 0u : ~0u << (8 * (from - 4 * i));
+            if (to < 4 * i + 4) in &= to <= 4 * i ? 0u : ~0u >> (8 * (4 * i + 4 - to));
 #pragma unroll
             for (int j = 0; j < 2; ++j) {
-                const int e = (w[j][i / 4] >> (8 * (i % 4))) & 0xff;
-                if (e != 255) top[j] = max(top[j], e);
+                const uint32_t x = w[j][i] & in;
+                top4[j] = __vmaxu4(top4[j], x & ~__vcmpeq4(x, ~0u));
+                low4[j] = __vminu4(low4[j], x | __vcmpleu4(x, 0x01010101u));
             }
         }
+    }
+    int top[2], low[2];
+#pragma unroll
+    for (int j = 0; j < 2; ++j) {
+        top4[j] = __vmaxu4(top4[j], top4[j] >> 16);
+        top[j] = max(1, max(top4[j] & 0xff, (top4[j] >> 8) & 0xff));
+        low4[j] = __vminu4(low4[j], low4[j] >> 16 | 0xffff0000u);
+        low[j] = min(low4[j] & 0xff, (low4[j] >> 8) & 0xff);
     }
 #pragma unroll
     for (int j = 0; j < 2; ++j) {
 #pragma unroll
-        for (int o = 16; o > 0; o >>= 1) top[j] = max(top[j], __shfl_xor_sync(0xffffffffu, top[j], o));
-        if (lane == 0) red[j][warp] = top[j];
+        for (int o = 16; o > 0; o >>= 1) {
+            top[j] = max(top[j], __shfl_xor_sync(0xffffffffu, top[j], o));
+            low[j] = min(low[j], __shfl_xor_sync(0xffffffffu, low[j], o));
+        }
+        if (lane == 0) red[j][warp] = top[j], red_low[j][warp] = low[j];
     }
     __syncthreads();
     if (threadIdx.x == 0) {
         long long first = 0;
-        int e[2] = {1, 1};
+        int e[2] = {1, 1}, f[2] = {255, 255};
         for (int i = 0; i < kWarps; ++i) {
             first += sum[i];
-            e[0] = max(e[0], red[0][i]);
-            e[1] = max(e[1], red[1][i]);
+            for (int j = 0; j < 2; ++j) e[j] = max(e[j], red[j][i]), f[j] = min(f[j], red_low[j][i]);
         }
+        const bool far = e[0] - f[0] > kUnitSpan || e[1] - f[1] > kUnitSpan;
         const long long padded = (keys.y + kFwdBlockN - 1) / kFwdBlockN * kFwdBlockN;
         const bool fits = first + padded <= p.rows;
         if (!fits) atomicOr(p.status, kStatusBounds);  // more keys than the caller's bound
         if (kvh == 0) p.spans[b] = fits ? make_int2(static_cast<int>(first), keys.y) : make_int2(p.rows, 0);
-        p.k_unit[blockIdx.x] = e8m0_to_f32(max(1, e[0] - 7));
-        p.v_unit[blockIdx.x] = e8m0_to_f32(max(1, e[1] - 7));
+        if (far && keys.y > 0) *p.by_row = 1;
+        p.k_unit[blockIdx.x] = far ? 0.f : e8m0_to_f32(max(1, e[0] - 7));
+        p.v_unit[blockIdx.x] = far ? 0.f : e8m0_to_f32(max(1, e[1] - 7));
     }
 }
 
@@ -625,7 +646,7 @@ __device__ __forceinline__ ReadToken place(const StageFp8Params& p, int t, int& 
 }
 
 // 16 codes as bf16: code 2^e, exact but for the smallest scales' subnormals.
-__device__ __forceinline__ void convert16(const ReadFp8Params&, const uint4& w, int sb, int, bool,
+__device__ __forceinline__ void convert16(const ReadFp8Params&, const uint4& w, int sb, float,
                                           uint32_t (&out)[8]) {
     const float scale = e8m0_to_f32(sb);
     const uint32_t in[4] = {w.x, w.y, w.z, w.w};
@@ -641,10 +662,20 @@ __device__ __forceinline__ void convert16(const ReadFp8Params&, const uint4& w, 
     }
 }
 
-// 16 codes as f16 multiples of the (sequence, kv head)'s unit.
-__device__ __forceinline__ void convert16(const StageFp8Params& p, const uint4& w, int sb, int bh,
-                                          bool is_v, uint32_t (&out)[8]) {
-    const int e = sb - (__float_as_int((is_v ? p.v_unit : p.k_unit)[bh]) >> 23);  // at most 7
+// The unit of a (sequence, kv head); where it is 0, rows keep their scale bytes.
+__device__ __forceinline__ float unit_of(const ReadFp8Params&, int, bool) { return 1.f; }
+__device__ __forceinline__ float unit_of(const StageFp8Params& p, int bh, bool is_v) {
+    return (is_v ? p.v_unit : p.k_unit)[bh];
+}
+__device__ __forceinline__ void keep_scale(const ReadFp8Params&, int, int, int, bool) {}
+__device__ __forceinline__ void keep_scale(const StageFp8Params& p, int sb, int row, int kvh, bool is_v) {
+    (is_v ? p.v_sb : p.k_sb)[static_cast<size_t>(kvh) * p.rows + row] = sb;
+}
+
+// 16 codes as f16 multiples of the (sequence, kv head)'s unit (or as they are).
+__device__ __forceinline__ void convert16(const StageFp8Params&, const uint4& w, int sb, float unit,
+                                          uint32_t (&out)[8]) {
+    const int e = unit == 0.f ? 0 : sb - (__float_as_int(unit) >> 23);  // at most 7
     const uint32_t in[4] = {w.x, w.y, w.z, w.w};
     if (e >= -14 && sb != 255) {  // 2^e is a normal f16
         const uint32_t f = static_cast<uint32_t>(e + 15) << 10, ff = f | (f << 16);
@@ -718,8 +749,10 @@ __global__ void __launch_bounds__(256)
             if (row[u] == -1) continue;
             uint32_t out[8] = {0, 0, 0, 0, 0, 0, 0, 0};
             if (row[u] >= 0) {
-                const int tok = static_cast<int>((at[u] + 0.5f) * inv);
-                convert16(p, w[u], sb[u], seq_of[tok] * p.Hkv + at[u] - tok * p.Hkv, is_v, out);
+                const int tok = static_cast<int>((at[u] + 0.5f) * inv), kvh = at[u] - tok * p.Hkv;
+                const float unit = unit_of(p, seq_of[tok] * p.Hkv + kvh, is_v);
+                convert16(p, w[u], sb[u], unit, out);
+                if (unit == 0.f) keep_scale(p, sb[u], t0 + tok, kvh, is_v);
             }
             uint4* dst = reinterpret_cast<uint4*>(to + static_cast<size_t>(at[u]) * D +
                                                   (i0 + 256 * u) % kLanes * 16);

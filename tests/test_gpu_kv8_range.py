@@ -13,7 +13,7 @@ import torch
 
 from tests import kv8_exact
 from tests.kv8_exact import kv8_case
-from tests.test_gpu_kv8 import append, attn, chunk, decode, gpu_cache  # noqa: F401
+from tests.test_gpu_kv8 import append, attn, chunk, decode, dev, gpu_cache  # noqa: F401
 
 pytestmark = pytest.mark.gpu
 
@@ -180,7 +180,7 @@ def test_chunk_over_keys_of_any_size(attn, new, e, rotary, aligned):  # noqa: F8
     check_chunk(attn, c, what=f"2^{e}")
 
 
-@pytest.mark.parametrize("new", [None, SHORT])
+@pytest.mark.parametrize("new", [None, SHORT, LONG])
 def test_keys_of_all_sizes_in_one_sequence(attn, new):  # noqa: F811
     """Keys 2^28 apart whose logits are alike: each meets the query in one component, where the query is
     as much smaller; what is left of the keys' rows is larger by 2^7 and meets a zero."""
@@ -209,7 +209,7 @@ def test_keys_of_all_sizes_in_one_sequence(attn, new):  # noqa: F811
 
 @pytest.mark.parametrize("rotary", [0, 64])
 @pytest.mark.parametrize("big", BIG)
-@pytest.mark.parametrize("new", [[9, 5]])
+@pytest.mark.parametrize("new", [[9, 5], LONG])
 def test_chunk_beside_large_values_that_rows_do_not_see(attn, new, big, rotary):  # noqa: F811
     """The last new token's value is large, and so is one in the middle: rows before them do not see
     them.  So is a cached one that the window of later rows leaves out."""
@@ -224,7 +224,7 @@ def test_chunk_beside_large_values_that_rows_do_not_see(attn, new, big, rotary):
 
 
 @pytest.mark.parametrize("big", BIG)
-@pytest.mark.parametrize("new", [[9, 5]])
+@pytest.mark.parametrize("new", [[9, 5], LONG])
 def test_chunk_beside_large_keys_that_rows_do_not_see(attn, new, big):  # noqa: F811
     c = kv8_case([90, 130], new, 32, 8, 64, 32, seed=421, spread=0.5)
     for b in (0, 1):
@@ -237,7 +237,7 @@ def test_chunk_beside_large_keys_that_rows_do_not_see(attn, new, big):  # noqa: 
 
 
 @pytest.mark.parametrize("far", [26, 40, 60, 100])
-@pytest.mark.parametrize("new", [None, [9, 5]])
+@pytest.mark.parametrize("new", [None, [9, 5], LONG])
 def test_large_values_of_small_weight(attn, new, far):  # noqa: F811
     """A value 2^far times the others' whose weight is 2^-(far + 30): the others make the result."""
     d = 64
@@ -260,7 +260,7 @@ def test_large_values_of_small_weight(attn, new, far):  # noqa: F811
         check_chunk(attn, c, what=f"{far}")
 
 
-@pytest.mark.parametrize("new", [None, [9, 5]])
+@pytest.mark.parametrize("new", [None, [9, 5], LONG])
 def test_large_values_first_then_larger_logits(attn, new):  # noqa: F811
     """A large value that carried all the weight until keys came whose logits are far above its own."""
     d = 64
@@ -278,6 +278,66 @@ def test_large_values_first_then_larger_logits(attn, new):  # noqa: F811
         check_decode(attn, c)
     else:
         check_chunk(attn, c)
+
+
+def far_rows(c, d, seed):
+    """Rows of kv head 1, cached and new, 2^40 apart; its queries small enough for moderate logits."""
+    rng = np.random.default_rng(seed)
+    for b, n in enumerate(c.ctx):
+        if n:
+            k, v = (rng.standard_normal((n, 3, d)) for _ in "kv")
+            for x in (k, v):
+                x[:, 1] *= 2.0 ** rng.uniform(-20, 20, (n, 1))
+            put_cached(c, b, np.arange(n), k=k, v=v)
+    f = torch.from_numpy(2.0 ** rng.uniform(-20, 20, (2, c.k_new.shape[0], 1)))
+    c.k_new[:, 1], c.v_new[:, 1] = bf16(c.k_new[:, 1].double() * f[0]), bf16(c.v_new[:, 1].double() * f[1])
+    g = c.q.shape[1] // 3
+    c.q[:, g:2 * g] *= 2.0 ** -18
+
+
+@pytest.mark.parametrize("causal,window", [(True, (-1, -1)), (True, (100, 0)), (False, (30, 7)),
+                                           (False, (-1, -1))])
+@pytest.mark.parametrize("d,rotary", [(64, 0), (64, 64), (128, 0), (128, 48)])
+def test_chunk_whose_rows_are_far_apart(attn, d, rotary, causal, window):  # noqa: F811
+    """Staged, one of three kv heads: its neighbours take their usual way, an odd number of keys in all,
+    a sequence without cached tokens, one without new ones."""
+    c = kv8_case([301, 0, 77, 5], [200, 131, 0, 65], 24, 3, d, 32, seed=425, rotary_dim=rotary)
+    far_rows(c, d, 425)
+    check_chunk(attn, c, causal, window)
+
+
+@pytest.mark.parametrize("rotary", [0, 128])
+def test_graph_replayed_as_rows_move_apart(attn, rotary):  # noqa: F811
+    """A captured chunk whose rows lie close, replayed with rows far apart and with close ones again."""
+    near, far = (kv8_case([301, 77], [200, 65], 24, 3, 128, 32, seed=426, rotary_dim=rotary) for _ in "ab")
+    far_rows(far, 128, 426)
+
+    def inputs(c):
+        return [c.q, c.k_new, c.v_new, *c.cache]
+
+    held = [t.cuda() for t in inputs(near)]
+    rest = [dev(t) for t in (near.cache_seqlens, near.block_table, near.cu_seqlens_q)]
+    tables = [dev(near.rotary_cos), dev(near.rotary_sin)]
+
+    def step():
+        return attn.attn_fwd_kvcache_fp8(*held, *rest, 200, 643, near.scale, True, -1, -1, *tables)
+
+    step()
+    torch.cuda.synchronize()
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph):
+        outs = step()
+    for c in (far, near, far):
+        for h, t in zip(held, inputs(c)):
+            h.copy_(t)
+        graph.replay()
+        torch.cuda.synchronize()
+        kv8_exact.check(outs[0], outs[1].t(), reference(c, kv8_exact.appended(c)), 2.0 ** -11, rotary > 0)
+        got = [t.clone() for t in outs]
+        for h, t in zip(held, inputs(c)):
+            h.copy_(t)
+        assert all(torch.equal(a, b) for a, b in zip(got, step()))
+    assert attn.attn_get_device_status() == 0
 
 
 @pytest.mark.parametrize("new", [None, SHORT])
