@@ -693,7 +693,15 @@ __global__ void __launch_bounds__(kKv8Threads, 2)
 #pragma unroll
             for (int i = 0; i < 4; ++i) lsum += ml[i * kKv8Rows + r] * ex2_approx(mm[i * kKv8Rows + r] - M);
             const float over = lsum == 0.f ? 0.f : 1.f / lsum;
-            sc[h] = ex2_approx(m_run[h] - M) * over * __int_as_float((254 << 23) - __float_as_int(inv[h]));
+            const float un = __int_as_float((254 << 23) - __float_as_int(inv[h]));  // 2^(E - 5)
+            const bool tiny = un < 0x1p-60f;
+            if (__any_sync(0xffffffffu, tiny)) {  // (un over l may be no normal number)
+#pragma unroll
+                for (int x = 0; x < D / 8; ++x)
+#pragma unroll
+                    for (int e = 0; e < 2; ++e) o[x][2 * h + e] *= tiny ? 0x1p-60f : 1.f;
+            }
+            sc[h] = ex2_approx(m_run[h] - M) * over * (tiny ? un * 0x1p60f : un);
             if (warp == 0 && tq == 0 && r < rows) {
                 const float lse = lsum == 0.f ? -INFINITY : M + __log2f(lsum);  // log2
                 const int tok = q0 + (row0 + r) / p.g, head = kvh * p.g + (row0 + r) % p.g;

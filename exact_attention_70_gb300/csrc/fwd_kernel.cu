@@ -575,7 +575,7 @@ __device__ __forceinline__ float quad_max(float x) {
 // is to be multiplied with.
 __device__ __forceinline__ int raised_e(int e, float pv, float m, float m_new, float& alpha) {
     if (m_new == -INFINITY) return e;  // no key seen
-    const int e_new = min(max(static_cast<int>(ceilf(fmaxf(pv - m_new, m - m_new + e))), 0), 253);
+    const int e_new = min(max(static_cast<int>(ceilf(fmaxf(pv - m_new, m - m_new + e))), 1), 253);
     alpha = ex2_approx(m - m_new + (e - e_new));
     return e_new;
 }
@@ -657,7 +657,7 @@ __device__ void fwd_softmax(const FwdParams& p, uint8_t* smem, FwdBars* bars, ui
         const int j0 = tv.lo + (is_hilo(kOps) ? t : 0), jstep = is_hilo(kOps) ? 2 : 1;
         // f16 operands come as multiples of a unit per query row and per (sequence, kv head)
         float sl2_a = sl2, sl2_b = sl2, qu_a = 1.f, qu_b = 1.f;
-        int e_a = 0, e_b = 0;  // kByRow: the rows' E, as scale bytes
+        int e_a = 1, e_b = 1;  // kByRow: the rows' E, as scale bytes
         if constexpr (is_f16(kOps)) {
             const int ta = tv.tok0 + ra / g, tb = tv.tok0 + (ra + 8) / g;
             const float* qu = p.q_unit + it.kvh * g;
@@ -1024,10 +1024,16 @@ __device__ void fwd_softmax(const FwdParams& p, uint8_t* smem, FwdBars* bars, ui
             if (C::kPInTmem && epi_pending && !staging_free()) return;
             float inv_a = l_a > 0.f ? 1.f / l_a : 0.f;
             float inv_b = l_b > 0.f ? 1.f / l_b : 0.f;
+            bool tiny_a = false, tiny_b = false;
             if constexpr (is_f16(kOps)) {
                 const float unit = p.v_unit[it.b * p.Hkv + it.kvh];
-                inv_a *= kByRow ? exp2_int(e_a - 127) : unit;
-                inv_b *= kByRow ? exp2_int(e_b - 127) : unit;
+                // (by row: times 2^60, and O times 2^-60, where the unit over l would be no normal number)
+                const float unit_a = kByRow ? exp2_int(e_a - 127) : unit;
+                const float unit_b = kByRow ? exp2_int(e_b - 127) : unit;
+                tiny_a = kByRow && unit_a < 0x1p-60f;
+                tiny_b = kByRow && unit_b < 0x1p-60f;
+                inv_a *= tiny_a ? unit_a * 0x1p60f : unit_a;
+                inv_b *= tiny_b ? unit_b * 0x1p60f : unit_b;
             }
 #pragma unroll
             for (int cc = 0; cc < D / 64; ++cc) {
@@ -1045,6 +1051,11 @@ __device__ void fwd_softmax(const FwdParams& p, uint8_t* smem, FwdBars* bars, ui
                                 __uint_as_float(o[c]) * (c & 2 ? w_b : w_a) +
                                 __uint_as_float(o1[c]) * (c & 2 ? w1_b : w1_a));
                     }
+                }
+                if (kByRow && __any_sync(0xffffffffu, tiny_a || tiny_b)) {
+#pragma unroll
+                    for (int c = 0; c < 32; ++c)
+                        if (c & 2 ? tiny_b : tiny_a) o[c] = __float_as_uint(__uint_as_float(o[c]) * 0x1p-60f);
                 }
 #pragma unroll
                 for (int cp = 0; cp < 4; ++cp) {

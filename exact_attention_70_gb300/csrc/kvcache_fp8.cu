@@ -495,6 +495,9 @@ __global__ void __launch_bounds__(kAppendThreads, 5)
 // perhaps one that most queries do not see, would cost the others their bits: then the codes go in as
 // they are, the scale bytes beside them, and the prefill kernel brings them together in fp32.
 constexpr int kUnitSpan = 22;
+// The same for pairs whose largest value has a scale below 2^-60 (a scale byte): their unit over the
+// softmax denominator is no normal number.
+constexpr int kUnitLeast = 127 - 60;
 
 // The first key that a new token of a sequence sees, and the keys from there on.
 __device__ __forceinline__ int2 staged_keys(const StageFp8Params& p, int b) {
@@ -575,7 +578,7 @@ __global__ void __launch_bounds__(kUnitsThreads)
             first += sum[i];
             for (int j = 0; j < 2; ++j) e[j] = max(e[j], red[j][i]), f[j] = min(f[j], red_low[j][i]);
         }
-        const bool far = e[0] - f[0] > kUnitSpan || e[1] - f[1] > kUnitSpan;
+        const bool far = e[0] - f[0] > kUnitSpan || e[1] - f[1] > kUnitSpan || e[1] < kUnitLeast;
         const long long padded = (keys.y + kFwdBlockN - 1) / kFwdBlockN * kFwdBlockN;
         const bool fits = first + padded <= p.rows;
         if (!fits) atomicOr(p.status, kStatusBounds);  // more keys than the caller's bound

@@ -386,7 +386,8 @@ size_t attn_decode_kvcache_fp8_workspace_bytes(int batch, int nheads_q, int nhea
  * values as attn_kvcache_append_fp8 does, rotates the queries (in the workspace, to 22 significant
  * bits of their row's largest, 2^-145 at least), then attends from every new token to the cached and
  * the new ones, as they are stored (in long chunks rows of the smallest scale, below 2^-117, count as
- * zeros beside rows 2^22 times as large and more); weights as for attn_decode_kvcache_fp8.
+ * zeros beside rows 2^22 times as large and more); weights as for attn_decode_kvcache_fp8, or (in long
+ * chunks) off by up to 2^-32 of the value that they meet.
  *   q    device bf16 [total_q, nheads_q, head_dim]; out the same shape; lse device fp32
  *        [nheads_q, total_q]; rows outside every sequence are left as they were
  *   max_seqlen_q  an upper bound on the new tokens of a sequence (checked on the device)

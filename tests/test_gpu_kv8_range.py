@@ -340,7 +340,7 @@ def test_graph_replayed_as_rows_move_apart(attn, rotary):  # noqa: F811
     assert attn.attn_get_device_status() == 0
 
 
-@pytest.mark.parametrize("new", [None, SHORT])
+@pytest.mark.parametrize("new", [None, SHORT, LONG])
 @pytest.mark.parametrize("e", [-60, -100, -120])
 def test_tiny_values(attn, e, new):  # noqa: F811
     """Values down to bf16's smallest: O is as exact as its type holds it."""
