@@ -4,6 +4,7 @@
 #include <cudaTypedefs.h>
 #include <cuda_runtime.h>
 
+#include <algorithm>
 #include <math.h>
 #include <mutex>
 #include <nvtx3/nvToolsExt.h>
@@ -850,13 +851,13 @@ attn_status_t rotary_ok(const float* cos, const float* sin, int rotary_dim, int 
 // CTAs of the attention kernel: as many for each kv head as make two an SM of a GB300, fewer where
 // the largest possible work (every sequence as long as its table) would leave some without
 // any; 0 where a head's work does not count in 31 bits.
-int kv8_grid(int batch, int max_seqlen_q, int nheads_q, int nheads_kv, int page_size,
+int kv8_grid(int batch, int total_q, int max_seqlen_q, int nheads_q, int nheads_kv, int page_size,
              int max_pages_per_seq) {
-    const long long groups =
-        (static_cast<long long>(max_seqlen_q) * (nheads_q / nheads_kv) + kKv8Rows - 1) / kKv8Rows;
+    const int g = nheads_q / nheads_kv;
+    const long long groups = (static_cast<long long>(max_seqlen_q) * g + kKv8Rows - 1) / kKv8Rows;
     const long long keys = static_cast<long long>(max_pages_per_seq) * page_size;
     const long long places = (keys + kKv8Chunk - 1) / kKv8Chunk + kKv8SwitchChunks;  // of a unit
-    const long long units = static_cast<long long>(batch) * groups;
+    const long long units = std::min(batch * groups, static_cast<long long>(total_q) * g / kKv8Rows + batch);
     if (units > ((1LL << 31) - 1) / places) return 0;
     const long long cap = 2 * kGb300Sms / nheads_kv;
     const long long n = (units * places - kKv8SwitchChunks + kKv8MinShare - 1) / kKv8MinShare;
@@ -909,7 +910,7 @@ long long kv8_staged_rows(int batch, int max_total_k) {
     return (static_cast<long long>(max_total_k) + static_cast<long long>(kFwdBlockN) * batch + 1) / 2 * 2;
 }
 
-Kv8StageLayout kv8_stage_layout(int batch, int max_seqlen_q, int max_total_k, int nheads_q,
+Kv8StageLayout kv8_stage_layout(int batch, int total_q, int max_seqlen_q, int max_total_k, int nheads_q,
                                 int nheads_kv, int head_dim, int tiles) {
     Kv8StageLayout l;
     l.rows = kv8_staged_rows(batch, max_total_k);
@@ -925,7 +926,7 @@ Kv8StageLayout kv8_stage_layout(int batch, int max_seqlen_q, int max_total_k, in
     l.v_sb = l.k_sb + scales;
     l.list = l.v_sb + scales;
     const long long per = static_cast<long long>(tiles) * tokens_per_tile(nheads_q / nheads_kv);
-    l.items = batch * ((max_seqlen_q + per - 1) / per);
+    l.items = std::min(batch * ((max_seqlen_q + per - 1) / per), total_q / per + batch);
     l.total = l.list + sizeof(FwdWorkspaceHeader) + align_up(sizeof(int) * (batch + 1), 16) +
               static_cast<size_t>(l.items) * nheads_kv * sizeof(int4);
     return l;
@@ -1051,7 +1052,7 @@ size_t attn_decode_kvcache_fp8_workspace_bytes(int batch, int nheads_q, int nhea
         kv8_sizes(batch, nheads_kv, head_dim, page_size, max_pages_per_seq, 1) != ATTN_OK)
         return 0;
     return kv8_partial_bytes(
-        kv8_grid(batch, 1, nheads_q, nheads_kv, page_size, max_pages_per_seq), head_dim);
+        kv8_grid(batch, batch, 1, nheads_q, nheads_kv, page_size, max_pages_per_seq), head_dim);
 }
 
 attn_status_t attn_decode_kvcache_fp8(const void* q, const void* k_cache, const void* v_cache,
@@ -1073,7 +1074,7 @@ attn_status_t attn_decode_kvcache_fp8(const void* q, const void* k_cache, const 
         !out || !lse || !aligned(q, 16) || !aligned(out, 16) || !aligned(lse, 4) ||
         !aligned(cache_seqlens, 4))
         return ATTN_ERR_INVALID_ARG;
-    const int grid = kv8_grid(batch, 1, nheads_q, nheads_kv, page_size, max_pages_per_seq);
+    const int grid = kv8_grid(batch, batch, 1, nheads_q, nheads_kv, page_size, max_pages_per_seq);
     if (grid == 0) return ATTN_ERR_UNSUPPORTED;
     if (!workspace || workspace_bytes < kv8_partial_bytes(grid, head_dim) || !aligned(workspace, 256))
         return ATTN_ERR_WORKSPACE;
@@ -1116,14 +1117,15 @@ size_t attn_fwd_kvcache_fp8_workspace_bytes(int batch, int total_q, int max_seql
         nheads_kv <= 0 || nheads_q % nheads_kv != 0 || rotary_dim < 0 ||
         kv8_sizes(batch, nheads_kv, head_dim, page_size, max_pages_per_seq, 1) != ATTN_OK)
         return 0;
+    max_seqlen_q = std::min(max_seqlen_q, total_q);  // (no sequence has more)
     const bool staged = kv8_staged(batch, max_seqlen_q, nheads_q, nheads_kv);
     return (rotary_dim > 0 || staged
                 ? kv8_query_bytes(static_cast<long long>(total_q) * nheads_q, head_dim, rotary_dim)
                 : 0) +
-           (staged ? kv8_stage_layout(batch, max_seqlen_q, max_total_k, nheads_q, nheads_kv, head_dim,
+           (staged ? kv8_stage_layout(batch, total_q, max_seqlen_q, max_total_k, nheads_q, nheads_kv, head_dim,
                                       kv8_tiles(rotary_dim))
                          .total
-                   : kv8_partial_bytes(kv8_grid(batch, max_seqlen_q, nheads_q, nheads_kv, page_size,
+                   : kv8_partial_bytes(kv8_grid(batch, total_q, max_seqlen_q, nheads_q, nheads_kv, page_size,
                                                 max_pages_per_seq),
                                        head_dim));
 }
@@ -1156,9 +1158,10 @@ attn_status_t attn_fwd_kvcache_fp8(const void* q, const void* k_new, const void*
         !aligned(cu_seqlens_q, 4))
         return ATTN_ERR_INVALID_ARG;
     const int g = nheads_q / nheads_kv;
+    max_seqlen_q = std::min(max_seqlen_q, total_q);  // (no sequence has more)
     const bool staged = kv8_staged(batch, max_seqlen_q, nheads_q, nheads_kv);
     const int grid = staged ? 0
-                            : kv8_grid(batch, max_seqlen_q, nheads_q, nheads_kv, page_size,
+                            : kv8_grid(batch, total_q, max_seqlen_q, nheads_q, nheads_kv, page_size,
                                        max_pages_per_seq);
     if (staged ? kv8_staged_rows(batch, max_total_k) * nheads_kv > (1LL << 31) - 1
                : grid == 0)
@@ -1211,7 +1214,7 @@ attn_status_t attn_fwd_kvcache_fp8(const void* q, const void* k_new, const void*
     if (staged) {
         // 2. beside it (it needs the sequences' lengths only), the prefill kernel's work list
         const Kv8StageLayout l =
-            kv8_stage_layout(batch, max_seqlen_q, max_total_k, nheads_q, nheads_kv, head_dim,
+            kv8_stage_layout(batch, total_q, max_seqlen_q, max_total_k, nheads_q, nheads_kv, head_dim,
                              kv8_tiles(rotary_dim));
         const int tpt = tokens_per_tile(g);
         FwdWorkspaceHeader* header = reinterpret_cast<FwdWorkspaceHeader*>(ws + l.list);

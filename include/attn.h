@@ -376,7 +376,7 @@ attn_status_t attn_decode_kvcache_fp8(const void* q, const void* k_cache, const 
                                       void* workspace, size_t workspace_bytes, void* stream);
 
 /* Workspace bytes of attn_decode_kvcache_fp8: the partial results of sequences that are cut, at
- * most 5 MiB (0 on sizes the call would refuse). */
+ * most 5 MiB up to 304 kv heads and 17 KiB a kv head above (0 on sizes the call would refuse). */
 size_t attn_decode_kvcache_fp8_workspace_bytes(int batch, int nheads_q, int nheads_kv,
                                                int head_dim, int page_size,
                                                int max_pages_per_seq);
@@ -390,7 +390,8 @@ size_t attn_decode_kvcache_fp8_workspace_bytes(int batch, int nheads_q, int nhea
  * chunks) off by up to 2^-32 of the value that they meet.
  *   q    device bf16 [total_q, nheads_q, head_dim]; out the same shape; lse device fp32
  *        [nheads_q, total_q]; rows outside every sequence are left as they were
- *   max_seqlen_q  an upper bound on the new tokens of a sequence (checked on the device)
+ *   max_seqlen_q  an upper bound on the new tokens of a sequence (checked on the device; more than
+ *                 total_q counts as total_q)
  *   max_total_k   an upper bound on sum_b (cache_seqlens[b] + new tokens of b); sizes the workspace
  *                 (long chunks stage keys and values there; sequences past the bound raise
  *                 ATTN_ERR_DEVICE_BOUNDS)

@@ -466,3 +466,19 @@ def test_rotated_queries_of_any_size(attn, new, e):  # noqa: F811
         k = np.abs(kv8_exact.read_back(arrays, c.block_table.numpy(), b, c.ctx[b] + n, 32)[0]).sum(-1).max(0)
         dS[new_rows(c, b)] += c.scale * np.repeat(k, g) * 2.0 ** -145 * 2.0 ** 20
     kv8_exact.check(out, lse.t(), (O, LSE, dS, W), 2.0 ** -11, True, f"2^{e}")
+
+
+def test_max_seqlen_q_far_above_the_tokens_of_the_call(attn):  # noqa: F811
+    """No sequence has more new tokens than the call: any larger bound gives the same results."""
+    for new in (SHORT, LONG):
+        c = kv8_case([70, 30], new, 32, 8, 64, 32, seed=470, rotary_dim=64)
+        want = chunk(attn, c, gpu_cache(c))
+        args = [dev(t) for t in (c.q, c.k_new, c.v_new)]
+        rest = [dev(t) for t in (c.cache_seqlens, c.block_table, c.cu_seqlens_q)]
+        for bound in (sum(new), 10 ** 6, 2 ** 31 - 1):
+            got = attn.attn_fwd_kvcache_fp8(*args, *gpu_cache(c), *rest, bound, 100 + sum(new), c.scale, True,
+                                            -1, -1, dev(c.rotary_cos), dev(c.rotary_sin))
+            torch.cuda.synchronize()
+            assert attn.attn_get_device_status() == 0
+            for g, w in zip(got, want):
+                assert torch.allclose(g.float(), w.float(), rtol=2.0 ** -7, atol=2.0 ** -7)
