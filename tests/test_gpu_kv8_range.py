@@ -79,7 +79,8 @@ def reference(c, arrays, causal=True, window=(-1, -1)):
             dS[t0:t0 + n, h] = c.scale * np.where(seen, np.abs(q[:, h]) @ np.abs(kh).T, 0.0).max(1)
             s = np.where(seen, c.scale * (q[:, h] @ kh.T), -np.inf)
             top = (np.exp(s - np.maximum(s.max(1), -1e300)[:, None]) * eh).max(1)
-            near = np.minimum(eh, 2.0 ** 22 * eh.min(initial=np.inf))
+            # (rows of the smallest scale, zeros, do not count among the scales)
+            near = np.minimum(eh, 2.0 ** 22 * eh.min(initial=np.inf, where=eh > 2.0 ** -126))
             W[t0:t0 + n, h] += seen @ (vh / eh[:, None] * near[:, None]) * 2.0 ** -21
             W[t0:t0 + n, h] += top[:, None] * (seen @ (vh / eh[:, None])) * 2.0 ** -15
         t0 += n
