@@ -341,6 +341,45 @@ def test_graph_replayed_as_rows_move_apart(attn, rotary):  # noqa: F811
     assert attn.attn_get_device_status() == 0
 
 
+@pytest.mark.parametrize("far", [False, True])
+@pytest.mark.parametrize("rotary", [0, 128])
+def test_what_follows_a_chunk_finds_it_finished(attn, rotary, far):  # noqa: F811
+    """Kernels right behind the call on its stream, and the same call on two streams at once."""
+    cases = [kv8_case([3000, 701], [900, 333], 24, 3, 128, 64, seed=427 + i, rotary_dim=rotary) for i in (0, 1)]
+    for i, c in enumerate(cases):
+        if far:
+            far_rows(c, 128, 427 + i)
+    caches = [gpu_cache(c) for c in cases]
+    ins = [([dev(t) for t in (c.q, c.k_new, c.v_new)],
+            [dev(t) for t in (c.cache_seqlens, c.block_table, c.cu_seqlens_q)],
+            [dev(c.rotary_cos), dev(c.rotary_sin)]) for c in cases]
+
+    def call(i, out, lse, stream=None):
+        a, b, r = ins[i]
+        return attn.attn_fwd_kvcache_fp8(*a, *caches[i], *b, 900, 4934, cases[i].scale, True, -1, -1, *r, out=out,
+                                         lse=lse, stream=stream)
+
+    outs = [(torch.empty_like(x[0][0]), torch.empty(24, 1233, device="cuda")) for x in ins]
+    want = [[t.clone() for t in call(i, *o)] for i, o in enumerate(outs)]
+    torch.cuda.synchronize()
+    c = cases[0]
+    kv8_exact.check(want[0][0], want[0][1].t(), reference(c, kv8_exact.appended(c)), 2.0 ** -11, rotary > 0)
+    streams = [torch.cuda.Stream() for _ in cases]
+    got = [[], []]
+    for _ in range(20):
+        for i, s in enumerate(streams):
+            with torch.cuda.stream(s):
+                for t in outs[i]:
+                    t.fill_(7)
+                call(i, *outs[i], stream=s)
+                got[i].append([t.clone() for t in outs[i]])
+    torch.cuda.synchronize()
+    assert attn.attn_get_device_status() == 0
+    for i in (0, 1):
+        for g in got[i]:
+            assert all(torch.equal(a, b) for a, b in zip(g, want[i]))
+
+
 @pytest.mark.parametrize("new", [None, SHORT, LONG])
 @pytest.mark.parametrize("e", [-60, -100, -120])
 def test_tiny_values(attn, e, new):  # noqa: F811
