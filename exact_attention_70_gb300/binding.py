@@ -745,8 +745,12 @@ def attn_fwd_kvcache_fp8(q, k_new, v_new, k_cache, v_cache, k_scale, v_scale, ca
     """A chunk of new tokens against the 8-bit paged cache; the new k, v are written into it.
 
     q [total_q, Hq, d], k_new / v_new [total_q, Hkv, d] bf16; the cache as for
-    attn_kvcache_append_fp8; max_total_k bounds sum_b (cache_seqlens[b] + new tokens of b) (default:
-    what block_table can hold).  Returns (out [total_q, Hq, d], lse [Hq, total_q]).
+    attn_kvcache_append_fp8.  Returns (out [total_q, Hq, d], lse [Hq, total_q]).
+
+    max_total_k bounds sum_b (cache_seqlens[b] + new tokens of b) and sizes the workspace of calls
+    with a long chunk: about 4 Hkv d bytes a key.  The default is what block_table can hold, so
+    give the bound where the table is wider than the sequences are long (64 rows of 131072
+    tokens, 8 kv heads, d 128: 32 GiB).
     """
     lib = load()
     num_pages, page_size, Hkv, d, batch, max_pages, index = _kv8_sizes(

@@ -888,6 +888,8 @@ size_t kv8_query_bytes(long long rows, int head_dim, int rotary_dim) {
 //   64 x 8, 1000 keys:                      64 rows 128 / 167,  128 rows 251 / 176
 //   4 x 8, 8000 keys:                      128 rows  94 / 133,  256 rows 177 / 137
 //   1 x 8, 16000 keys:                     512 rows 167 / 182, 1024 rows 320 / 187
+// All measured with sequences of one length.  The choice is the whole call's: one long chunk beside many
+// single tokens has every sequence's keys staged.
 bool kv8_staged(int batch, int max_seqlen_q, int nheads_q, int nheads_kv) {
     if (nheads_q / nheads_kv > 128) return false;  // (more than the prefill kernel's tile packs)
     const long long rows = static_cast<long long>(max_seqlen_q) * (nheads_q / nheads_kv);

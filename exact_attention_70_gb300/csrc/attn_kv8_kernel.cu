@@ -160,17 +160,17 @@ __device__ __forceinline__ void scale_pair(uint32_t w, float (&f)[2]) {
 // next.  CTA i has kv head i % Hkv and share i / Hkv, so that CTAs side by side walk the
 // same tokens for all heads and the cache's rows are read whole (with the heads one after the
 // other in one list, each access 128 bytes out of 1 KB, 64 sequences took 562 us where they now take
-// 348).
+// 345 to 351, one GPU to another).
 // A unit cut by a share's border leaves partial results in the CTAs' slots (slot 1 of the CTA
 // that starts it, slot 0 of those that go on with it), which kv8_combine_kernel merges.
 //
-// Long caches: bound by memory.  64 sequences of 1K to 32K tokens, 32:8 heads, d 128: 348 us with the
-// merge, 7.0 TB/s of codes and scales (a plain copy reaches 6.8).  Short ones: bound by latency, about
+// Long caches: bound by memory.  64 sequences of 1K to 32K tokens, 32:8 heads, d 128: 345 to 351 us
+// with the merge, 7.0 TB/s of codes and scales (a plain copy reaches 6.8).  Short ones: bound by latency, about
 // 5 us to the first chunk (lengths, page table, keys, one after the other), 1.3 us a chunk, 2 us
-// for a unit's merge, 2 us for the kernel behind: 37 sequences up to 3000 tokens, 14:2 heads, 15.9 us.
-// kKv8SwitchChunks = 0 takes 19.9 us there, 2 to 4 take 15.9; 64 sequences take 352 us with 0 and
+// for a unit's merge, 2 us for the kernel behind: 37 sequences up to 3000 tokens, 14:2 heads, 16.0 us.
+// kKv8SwitchChunks = 0 took 19.9 us there, 2 to 4 took 15.9; 64 sequences took 352 us with 0 and
 // 348.5, 347.6, 348 with 2, 3, 4; 16 sequences of 300 tokens 14.1 us and 11.8, 10.9, 11.9.
-// A share of at least kKv8MinShare = 2 chunks: one sequence of 700 tokens, 8:2 heads, d 64, takes 7.6 us,
+// A share of at least kKv8MinShare = 2 chunks: one sequence of 700 tokens, 8:2 heads, d 64, took 7.6 us,
 // 8.6 with 1, 9.3 with 4.
 // Fetching a unit's queries during the merge before it cost more registers than it gained (64
 // sequences 376 us), and so did asking for the first chunks in L2 before the append kernel ends.

@@ -36,7 +36,9 @@
 // apart for one unit, K and V are the codes, the keys' scales meet S and the values' P in fp32
 // (by_row).  An instance of its own behind the other one computes such items anew: it starts as that one's
 // CTAs end and leaves at once where there are none.  The same loop for both kinds, a loop beside it, a call
-// or a second pass over the list by the same kernel cost the other items 57, 9, 7 and 4%.
+// or a second pass over the list by the same kernel cost the other items 57, 9, 7 and 4%; so it is 1 to 2 us a
+// call (5 ragged chunks 45.9 us, 44.0 without), and 8 chunks of 2048 tokens take 2285 us, with one of the 8
+// sequences by row 2776.
 // Rotated queries need more than 11 bits: rounding them moves LSE by 1e-5 to 1e-4 of itself where a
 // row sees few keys.  They come as hi + lo, two f16 numbers (kF16HiLo): S = Q_hi K^T + Q_lo K^T,
 // half as many MMAs again.  Both parts of two tiles would not fit in shared memory, so an item is

@@ -284,7 +284,7 @@ __device__ __forceinline__ AppendToken append_token(const AppendFp8Params& p, in
 // entries), or any other.
 //
 // Measured: 16384 tokens of 8 kv heads, d 128, whole head rotated, 25 us, 4.4 TB/s of rows read and
-// codes written (a copy: 6.8), with start and end about 5 us of it; 64 single tokens 3.9 us, bound by
+// codes written (a copy: 6.8), with start and end about 5 us of it; 64 single tokens 4.0 us, bound by
 // the chain lengths, page, table entries, rows.  Kinds mixed in one warp took 36 us, and two rows
 // straight into registers 40.
 constexpr int kKeys = 0, kValues = 1, kQueries = 2;
@@ -804,7 +804,7 @@ cudaError_t launch_read(const Params& p, void* k, void* v, int rows, int head_di
 cudaError_t launch_kvcache_append_fp8(const AppendFp8Params& p, int head_dim, bool dependent,
                                       cudaStream_t stream) {
     if (p.total_q == 0) return cudaSuccess;
-    // Single tokens spread over the GPU, about one step a group of lanes (64 of them: 3.9 us, 6.8 with
+    // Single tokens spread over the GPU, about one step a group of lanes (64 of them: 4.0 us, 6.8 with
     // 16 tokens a block); prompts take up to 16 tokens a block while four blocks an SM remain (16384
     // tokens: 25.0 us, 27.3 with 8 a block, 25.0 with 32).  Whole heads that turn in halves: 25.0 us,
     // 28.9 as any turn.

@@ -394,7 +394,8 @@ size_t attn_decode_kvcache_fp8_workspace_bytes(int batch, int nheads_q, int nhea
  *   max_seqlen_q  an upper bound on the new tokens of a sequence (checked on the device; more than
  *                 total_q counts as total_q)
  *   max_total_k   an upper bound on sum_b (cache_seqlens[b] + new tokens of b); sizes the workspace
- *                 (long chunks stage keys and values there; sequences past the bound raise
+ *                 (calls with a long chunk stage the keys and values of all their sequences there,
+ *                 4 nheads_kv (head_dim + 1/2) bytes a key of the bound; sequences past it raise
  *                 ATTN_ERR_DEVICE_BOUNDS)
  *   causal, window_left, window_right   see "Visibility"
  *   workspace     attn_fwd_kvcache_fp8_workspace_bytes(...) bytes, 256-byte aligned
