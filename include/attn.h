@@ -365,8 +365,8 @@ attn_status_t attn_kvcache_read_fp8(const void* k_cache, const void* v_cache, co
  * The keys of all sequences are shared out evenly over the GPU; what is cut is merged.  The result
  * is the attention of the stored values: the codes and the queries enter the tensor cores exactly,
  * the weights with their values' scales, P 2^e, with 11 significant bits (below 2^-15 of the row's
- * largest they are off by up to 2^-26 of it).  Logits are fp32: above 2^24 they have no fractions, and
- * rows with logits above 2^28 may turn to NaN.
+ * largest they are off by up to 2^-26 of it).  Logits are fp32: above 2^23 they have hardly any
+ * fractions, and rows with such logits may turn to NaN.
  */
 attn_status_t attn_decode_kvcache_fp8(const void* q, const void* k_cache, const void* v_cache,
                                       const void* k_scale, const void* v_scale,
