@@ -94,6 +94,27 @@ def load():
                 f32, i32, i32, i32, P, sz, P]
             lib.attn_fwd_kvcache_fp8_workspace_bytes.restype = sz
             lib.attn_fwd_kvcache_fp8_workspace_bytes.argtypes = [i32] * 10
+            i64 = ctypes.c_int64
+            how = [P, P, i32, f32, P, P, i32, i32, i32, P, i32, P, i32]  # weights .. sections_interleaved
+            lib.attn_kvcache_plan.restype = i32
+            lib.attn_kvcache_plan.argtypes = [P] * 10 + [i32] * 6 + [P, sz, P]
+            lib.attn_kvcache_plan_workspace_bytes.restype = sz
+            lib.attn_kvcache_plan_workspace_bytes.argtypes = [i32]
+            lib.attn_qk_norm_rope.restype = i32
+            lib.attn_qk_norm_rope.argtypes = [P, P, i64, i64] + how + [P, P] + [i32] * 4 + [P]
+            lib.attn_qk_norm_rope_bwd.restype = i32
+            lib.attn_qk_norm_rope_bwd.argtypes = [P] * 4 + [i64, i64] + how + [
+                P, P, i64, i64, P, P] + [i32] * 4 + [P, sz, P]
+            lib.attn_qk_norm_rope_bwd_workspace_bytes.restype = sz
+            lib.attn_qk_norm_rope_bwd_workspace_bytes.argtypes = [i32]
+            lib.attn_kvcache_append_norm_rope.restype = i32
+            lib.attn_kvcache_append_norm_rope.argtypes = [P] * 3 + [i64] * 3 + how + [
+                P, P, P, P] + [i32] * 6 + [P]
+            lib.attn_decode_kvcache_shared.restype = i32
+            lib.attn_decode_kvcache_shared.argtypes = [P] * 8 + [i32, P, P] + [i32] * 9 + [
+                f32, P, sz, P]
+            lib.attn_decode_kvcache_shared_workspace_bytes.restype = sz
+            lib.attn_decode_kvcache_shared_workspace_bytes.argtypes = [i32] * 6
             lib.attn_status_string.restype = ctypes.c_char_p
             lib.attn_status_string.argtypes = [i32]
             lib.attn_kv_block_range.restype = i32
@@ -792,6 +813,314 @@ def attn_fwd_kvcache_fp8(q, k_new, v_new, k_cache, v_cache, k_scale, v_scale, ca
             left, right, _ptr(ws), nbytes, s)
         if rc != 0:
             raise AttnError(rc, "attn_fwd_kvcache_fp8")
+        return o, l
+
+    return _on(index, stream, body)
+
+
+# ---- a step around paged attention -----------------------------------------------------------
+
+
+def _step_tensor(t, name, dtype, shape, index):
+    """Checks an input: a dense tensor of this dtype and shape (None: any size) on the call's device."""
+    try:
+        if (t.dtype is dtype and t.get_device() == index and t.is_contiguous()
+                and (t.shape == shape or (len(t.shape) == len(shape) and all(
+                    want is None or want == got for want, got in zip(shape, t.shape))))):
+            return t.data_ptr()
+    except _WRONG:
+        pass
+    _check(t, name, dtype, len(shape))
+    if t.get_device() != index:
+        raise ValueError(f"{name} must be on the device of the call's other tensors")
+    raise ValueError(f"{name} must be {['any' if n is None else n for n in shape]}, got "
+                     f"{list(t.shape)}")
+
+
+def _device_index(t, name):
+    if not isinstance(t, torch.Tensor):
+        raise TypeError(f"{name} must be a torch.Tensor")
+    if t.device.type != "cuda":
+        raise ValueError(f"{name} must be a CUDA tensor")
+    return t.get_device()
+
+
+def attn_kvcache_plan_workspace_bytes(batch) -> int:
+    return int(load().attn_kvcache_plan_workspace_bytes(batch))
+
+
+def attn_kvcache_plan(cache_seqlens, new_lens, block_table, free_pages, free_count, page_size,
+                      num_pages, total_q, cu_seqlens_q=None, seqlens_after=None, positions=None,
+                      slot_map=None, free_left=None, workspace=None, stream=None):
+    """Pages, positions and cache slots of a step's new tokens, from the lengths of its requests.
+
+    cache_seqlens, new_lens [batch]; block_table [batch, max_pages], updated in place; free_pages
+    [n], of which the first free_count[0] are free and are taken from the end; all int32.  total_q,
+    at least sum(new_lens), sizes the outputs (behind the last token: position 0, slot -1).
+    Returns (cu_seqlens_q [batch + 1], seqlens_after [batch], positions [total_q],
+    slot_map [total_q], free_left [1]), int32; free_left may be free_count and seqlens_after
+    cache_seqlens.
+    """
+    lib = load()
+    index = _device_index(block_table, "block_table")
+    table = _step_tensor(block_table, "block_table", _I32, (None, None), index)
+    batch, max_pages = block_table.shape
+    total, ps, pages = _int32(total_q, "total_q"), _int32(page_size, "page_size"), _int32(num_pages, "num_pages")
+    held = _step_tensor(cache_seqlens, "cache_seqlens", _I32, (batch,), index)
+    new = _step_tensor(new_lens, "new_lens", _I32, (batch,), index)
+    free = _step_tensor(free_pages, "free_pages", _I32, (None,), index)
+    count = _step_tensor(free_count, "free_count", _I32, (1,), index)
+    if total < 0:
+        raise AttnError(-1, "attn_kvcache_plan")
+    given = (cu_seqlens_q, seqlens_after, positions, slot_map, free_left)
+    shapes = ((batch + 1,), (batch,), (total,), (total,), (1,))
+    for t, name, shape in zip(given, ("cu_seqlens_q", "seqlens_after", "positions", "slot_map",
+                                      "free_left"), shapes):
+        if t is not None:
+            _step_tensor(t, name, _I32, shape, index)
+    nbytes = lib.attn_kvcache_plan_workspace_bytes(batch)
+
+    def body(s):
+        device = block_table.device
+        outs = tuple(torch.empty(shape, dtype=_I32, device=device) if t is None else t
+                     for t, shape in zip(given, shapes))
+        cu, after, pos, slots, left = outs
+        ws = _kv8_workspace(nbytes, device, workspace)
+        rc = lib.attn_kvcache_plan(held, new, table, free, count, left.data_ptr(), cu.data_ptr(),
+                                   after.data_ptr(), pos.data_ptr(), slots.data_ptr(), batch, total,
+                                   ps, max_pages, free_pages.shape[0], pages, _ptr(ws), nbytes, s)
+        if rc != 0:
+            raise AttnError(rc, "attn_kvcache_plan")
+        return outs
+
+    return _on(index, stream, body)
+
+
+def _rows_of(t, name, index, like=None):
+    """(address, elements between tokens) of bf16 [tokens, heads, d] whose tokens are dense but may
+    lie apart, as the parts of a projection's rows do."""
+    try:
+        tokens, heads, d = t.shape
+        st, sh, sd = t.stride()
+        if (t.dtype is _BF16 and t.get_device() == index and (like is None or t.shape == like)
+                and (sd == 1 or d == 1) and (sh == d or heads == 1)):
+            return t.data_ptr(), st if tokens > 1 else heads * d
+    except _WRONG:
+        pass
+    if not isinstance(t, torch.Tensor):
+        raise TypeError(f"{name} must be a torch.Tensor")
+    if t.device.type != "cuda" or t.get_device() != index:
+        raise ValueError(f"{name} must be a CUDA tensor on the device of the call's other tensors")
+    if t.dtype != torch.bfloat16:
+        raise TypeError(f"{name} must be torch.bfloat16, got {t.dtype}")
+    if t.dim() != 3 or (like is not None and t.shape != like):
+        raise ValueError(f"{name} must be {'[tokens, heads, d]' if like is None else list(like)}, got "
+                         f"{list(t.shape)}")
+    raise ValueError(f"the heads and components of a token of {name} must be dense")
+
+
+def _norm_rope_args(q, k, q_weight, k_weight, eps, rotary_cos, rotary_sin, positions,
+                    rotary_interleaved, sections, sections_interleaved, index):
+    """The arguments from q_weight to sections_interleaved as the library takes them."""
+    total, _, d = q.shape
+    if k.shape[0] != total or k.shape[2] != d:
+        raise ValueError("q and k must have the same tokens and components")
+    w32, weights = 0, []
+    given = [w for w in (q_weight, k_weight) if w is not None]
+    if given:
+        dtype = given[0].dtype if isinstance(given[0], torch.Tensor) else None
+        if dtype not in (_F32, _BF16):
+            raise TypeError("q_weight and k_weight must be torch.float32 or torch.bfloat16")
+        w32 = 1 if dtype is _F32 else 0
+        weights = [_step_tensor(w, "q_weight and k_weight", dtype, (d,), index) for w in given]
+    qw = weights.pop(0) if q_weight is not None else None
+    kw = weights.pop(0) if k_weight is not None else None
+    cos, sin, rot_dim, rot_rows = _rotary(rotary_cos, rotary_sin, index)
+    pos, axes, parts = None, 1, None
+    if rot_dim:
+        if positions is None:
+            raise ValueError("a rotation needs positions")
+        one = isinstance(positions, torch.Tensor) and positions.dim() == 1
+        pos = _step_tensor(positions, "positions", _I32, (total,) if one else (None, total), index)
+        axes = 1 if one else positions.shape[0]
+        if sections is not None:
+            if len(sections) != axes:
+                raise ValueError("sections must have one entry per axis of positions")
+            parts = (ctypes.c_int32 * axes)(*[_int32(n, "sections") for n in sections])
+    return (qw, kw, w32, float(eps), cos, sin, rot_dim, rot_rows, 1 if rotary_interleaved else 0, pos,
+            axes, parts, 1 if sections_interleaved else 0)
+
+
+def attn_qk_norm_rope(q, k, q_weight=None, k_weight=None, eps=1e-6, rotary_cos=None, rotary_sin=None,
+                      positions=None, rotary_interleaved=False, sections=None,
+                      sections_interleaved=False, q_out=None, k_out=None, stream=None):
+    """RMS norm of every query and key per head, then the rotation, in one pass.
+
+    q [T, Hq, d], k [T, Hkv, d] bf16, tokens dense but perhaps apart (parts of one projection's
+    rows); weights [d] fp32 or bf16, None: no norm; rotary_cos / rotary_sin fp32
+    [rows, rotary_dim / 2] or None; positions int32 [T] or, with several axes, [axes, T], and
+    sections the planes of each axis (sections_interleaved: the axes take planes in turn).
+    Returns (q_out, k_out), dense; q_out may be q and k_out k where those are dense.
+    """
+    lib = load()
+    index = _device_index(q, "q")
+    qp, qs = _rows_of(q, "q", index)
+    kp, ks = _rows_of(k, "k", index)
+    how = _norm_rope_args(q, k, q_weight, k_weight, eps, rotary_cos, rotary_sin, positions,
+                          rotary_interleaved, sections, sections_interleaved, index)
+    if q_out is not None:
+        _step_tensor(q_out, "q_out", _BF16, q.shape, index)
+    if k_out is not None:
+        _step_tensor(k_out, "k_out", _BF16, k.shape, index)
+
+    def body(s):
+        qo = torch.empty(q.shape, dtype=_BF16, device=q.device) if q_out is None else q_out
+        ko = torch.empty(k.shape, dtype=_BF16, device=q.device) if k_out is None else k_out
+        rc = lib.attn_qk_norm_rope(qp, kp, qs, ks, *how, qo.data_ptr(), ko.data_ptr(), q.shape[0],
+                                   q.shape[1], k.shape[1], q.shape[2], s)
+        if rc != 0:
+            raise AttnError(rc, "attn_qk_norm_rope")
+        return qo, ko
+
+    return _on(index, stream, body)
+
+
+def attn_qk_norm_rope_bwd(dq_out, dk_out, q, k, q_weight=None, k_weight=None, eps=1e-6,
+                          rotary_cos=None, rotary_sin=None, positions=None,
+                          rotary_interleaved=False, sections=None, sections_interleaved=False,
+                          dq=None, dk=None, workspace=None, stream=None):
+    """Backward pass of attn_qk_norm_rope: dq_out [T, Hq, d] and dk_out [T, Hkv, d] are the gradients
+    of its outputs, the other arguments its own.
+
+    Returns (dq, dk, dq_weight, dk_weight): bf16 like q and k, fp32 [d] (None without a weight).  dq
+    and dk may be given, with tokens apart (parts of a projection's gradient).
+    """
+    lib = load()
+    index = _device_index(q, "q")
+    qp, qs = _rows_of(q, "q", index)
+    kp, ks = _rows_of(k, "k", index)
+    how = _norm_rope_args(q, k, q_weight, k_weight, eps, rotary_cos, rotary_sin, positions,
+                          rotary_interleaved, sections, sections_interleaved, index)
+    gq = _step_tensor(dq_out, "dq_out", _BF16, q.shape, index)
+    gk = _step_tensor(dk_out, "dk_out", _BF16, k.shape, index)
+    if dq is not None:
+        _rows_of(dq, "dq", index, q.shape)
+    if dk is not None:
+        _rows_of(dk, "dk", index, k.shape)
+    total, Hq, d = q.shape
+    nbytes = (lib.attn_qk_norm_rope_bwd_workspace_bytes(d)
+              if q_weight is not None or k_weight is not None else 0)
+
+    def body(s):
+        device = q.device
+        dqo = torch.empty(q.shape, dtype=_BF16, device=device) if dq is None else dq
+        dko = torch.empty(k.shape, dtype=_BF16, device=device) if dk is None else dk
+        dqw = None if q_weight is None else torch.empty(d, dtype=_F32, device=device)
+        dkw = None if k_weight is None else torch.empty(d, dtype=_F32, device=device)
+        ws = _kv8_workspace(nbytes, device, workspace)
+        dqp, dqs = _rows_of(dqo, "dq", index)
+        dkp, dks = _rows_of(dko, "dk", index)
+        rc = lib.attn_qk_norm_rope_bwd(gq, gk, qp, kp, qs, ks, *how, dqp, dkp, dqs, dks, _ptr(dqw),
+                                       _ptr(dkw), total, Hq, k.shape[1], d, _ptr(ws), nbytes, s)
+        if rc != 0:
+            raise AttnError(rc, "attn_qk_norm_rope_bwd")
+        return dqo, dko, dqw, dkw
+
+    return _on(index, stream, body)
+
+
+def attn_kvcache_append_norm_rope(q, k, v, k_cache, v_cache, slot_map, q_weight=None, k_weight=None,
+                                  eps=1e-6, rotary_cos=None, rotary_sin=None, positions=None,
+                                  rotary_interleaved=False, sections=None,
+                                  sections_interleaved=False, q_out=None, stream=None):
+    """attn_qk_norm_rope for serving: the keys and the values [T, Hkv, d] go to slot_map[t] (int32;
+    negative: nowhere) of the bf16 paged cache [num_pages, page_size, Hkv, d], in place.
+
+    Returns q_out [T, Hq, d].
+    """
+    lib = load()
+    index = _device_index(q, "q")
+    qp, qs = _rows_of(q, "q", index)
+    kp, ks = _rows_of(k, "k", index)
+    vp, vs = _rows_of(v, "v", index, k.shape)
+    how = _norm_rope_args(q, k, q_weight, k_weight, eps, rotary_cos, rotary_sin, positions,
+                          rotary_interleaved, sections, sections_interleaved, index)
+    total, Hq, d = q.shape
+    cache = (None, None, k.shape[1], d)
+    kc = _step_tensor(k_cache, "k_cache", _BF16, cache, index)
+    vc = _step_tensor(v_cache, "v_cache", _BF16, k_cache.shape, index)
+    slots = _step_tensor(slot_map, "slot_map", _I32, (total,), index)
+    if q_out is not None:
+        _step_tensor(q_out, "q_out", _BF16, q.shape, index)
+
+    def body(s):
+        qo = torch.empty(q.shape, dtype=_BF16, device=q.device) if q_out is None else q_out
+        rc = lib.attn_kvcache_append_norm_rope(qp, kp, vp, qs, ks, vs, *how, qo.data_ptr(), kc, vc,
+                                               slots, total, Hq, k.shape[1], d, k_cache.shape[1],
+                                               k_cache.shape[0], s)
+        if rc != 0:
+            raise AttnError(rc, "attn_kvcache_append_norm_rope")
+        return qo
+
+    return _on(index, stream, body)
+
+
+def attn_decode_kvcache_shared_workspace_bytes(batch, num_groups, total_q, nheads_q, nheads_kv,
+                                               head_dim) -> int:
+    return int(load().attn_decode_kvcache_shared_workspace_bytes(batch, num_groups, total_q, nheads_q,
+                                                                 nheads_kv, head_dim))
+
+
+def attn_decode_kvcache_shared(q, k_cache, v_cache, cache_seqlens, block_table, group_starts=None,
+                               prefix_lens=None, cu_seqlens_q=None, max_seqlen_q=1,
+                               softmax_scale=None, out=None, lse=None, workspace=None, stream=None):
+    """Decode over the bf16 paged cache where groups of sequences share prefixes, each read once.
+
+    q [total_q, Hq, d]: one token per sequence or, with cu_seqlens_q [batch + 1], up to max_seqlen_q
+    of them, the last of the sequence's cache_seqlens[b] keys.  Sequences group_starts[i] ..
+    group_starts[i + 1] - 1 begin with the same prefix_lens[i] keys (both None: none share).
+    Returns (out like q, lse fp32 [batch, Hq], or [Hq, total_q] with cu_seqlens_q).
+    """
+    lib = load()
+    index = _device_index(q, "q")
+    qp = _step_tensor(q, "q", _BF16, (None, None, None), index)
+    total_q, Hq, d = q.shape
+    kc = _step_tensor(k_cache, "k_cache", _BF16, (None, None, None, d), index)
+    num_pages, page_size, Hkv, _ = k_cache.shape
+    vc = _step_tensor(v_cache, "v_cache", _BF16, k_cache.shape, index)
+    table = _step_tensor(block_table, "block_table", _I32, (None, None), index)
+    batch, max_pages = block_table.shape
+    lens = _step_tensor(cache_seqlens, "cache_seqlens", _I32, (batch,), index)
+    groups, starts, prefix, cu = 0, None, None, None
+    if (group_starts is None) != (prefix_lens is None):
+        raise ValueError("group_starts and prefix_lens come together")
+    if prefix_lens is not None:
+        prefix = _step_tensor(prefix_lens, "prefix_lens", _I32, (None,), index)
+        groups = prefix_lens.shape[0]
+        starts = _step_tensor(group_starts, "group_starts", _I32, (groups + 1,), index)
+    if cu_seqlens_q is not None:
+        cu = _step_tensor(cu_seqlens_q, "cu_seqlens_q", _I32, (batch + 1,), index)
+    elif total_q != batch:
+        raise ValueError("q must have one token per sequence (or cu_seqlens_q be given)")
+    max_q = _int32(max_seqlen_q, "max_seqlen_q")
+    shape = (batch, Hq) if cu is None else (Hq, total_q)
+    if out is not None:
+        _output(out, "out", _BF16, (total_q, Hq, d), index)
+    if lse is not None:
+        _output(lse, "lse", _F32, shape, index)
+    scale = d ** -0.5 if softmax_scale is None else float(softmax_scale)
+    nbytes = lib.attn_decode_kvcache_shared_workspace_bytes(batch, groups, total_q, Hq, Hkv, d)
+
+    def body(s):
+        device = q.device
+        o = torch.empty_like(q) if out is None else out
+        l = torch.empty(shape, dtype=_F32, device=device) if lse is None else lse
+        ws = _kv8_workspace(nbytes, device, workspace)
+        rc = lib.attn_decode_kvcache_shared(
+            qp, kc, vc, lens, table, starts, prefix, cu, page_size, o.data_ptr(), l.data_ptr(), batch,
+            groups, total_q, max_q, Hq, Hkv, d, max_pages, num_pages, scale, _ptr(ws), nbytes, s)
+        if rc != 0:
+            raise AttnError(rc, "attn_decode_kvcache_shared")
         return o, l
 
     return _on(index, stream, body)

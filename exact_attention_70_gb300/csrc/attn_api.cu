@@ -54,6 +54,7 @@ attn_status_t device_state(DeviceState** out) {
         if (configure_fwd_kernels() != cudaSuccess) return ATTN_ERR_CUDA;
         if (configure_decode_kernels() != cudaSuccess) return ATTN_ERR_CUDA;
         if (configure_kv8_kernels() != cudaSuccess) return ATTN_ERR_CUDA;
+        if (configure_shared_kernels() != cudaSuccess) return ATTN_ERR_CUDA;
         s.status = static_cast<unsigned*>(addr);
         s.ready = true;
     }
@@ -1387,6 +1388,399 @@ attn_status_t attn_get_device_status(void* stream) {
     if (word & kStatusTimeout) return ATTN_ERR_DEVICE_TIMEOUT;
     if (word & kStatusBounds) return ATTN_ERR_DEVICE_BOUNDS;
     return ATTN_OK;
+}
+
+// ---- a step's pages and slots ---------------------------------------------------------------
+
+size_t attn_kvcache_plan_workspace_bytes(int batch) {
+    if (batch < 0 || batch > 65535) return 0;
+    return align_up(sizeof(int) * (static_cast<size_t>(batch) + 1), 256);
+}
+
+attn_status_t attn_kvcache_plan(const int32_t* cache_seqlens, const int32_t* new_lens,
+                                int32_t* block_table, const int32_t* free_pages,
+                                const int32_t* free_count, int32_t* free_left,
+                                int32_t* cu_seqlens_q, int32_t* seqlens_after, int32_t* positions,
+                                int32_t* slot_map, int batch, int total_q, int page_size,
+                                int max_pages_per_seq, int num_free_pages, int num_pages,
+                                void* workspace, size_t workspace_bytes, void* stream) {
+    NvtxRange nvtx_range("attn_kvcache_plan");
+    if (batch < 0 || total_q < 0 || page_size <= 0 || max_pages_per_seq <= 0 || num_free_pages < 0 ||
+        num_pages <= 0)
+        return ATTN_ERR_INVALID_ARG;
+    if (batch > 65535 || static_cast<long long>(num_pages) * page_size > (1LL << 31) - 1 ||
+        static_cast<long long>(max_pages_per_seq) * page_size > (1LL << 30))
+        return ATTN_ERR_UNSUPPORTED;
+    if (!free_count || !free_left || !cu_seqlens_q ||
+        (batch > 0 && (!cache_seqlens || !new_lens || !block_table || !seqlens_after)) ||
+        (num_free_pages > 0 && !free_pages) || (total_q > 0 && (!positions || !slot_map)))
+        return ATTN_ERR_INVALID_ARG;
+    const void* const all[] = {cache_seqlens, new_lens, block_table, free_pages, free_count,
+                               free_left, cu_seqlens_q, seqlens_after, positions, slot_map};
+    for (const void* x : all)
+        if (!aligned(x, 4)) return ATTN_ERR_INVALID_ARG;
+    if (!workspace || workspace_bytes < attn_kvcache_plan_workspace_bytes(batch) || !aligned(workspace, 256))
+        return ATTN_ERR_WORKSPACE;
+    DeviceState* dev = nullptr;
+    const attn_status_t st = device_state(&dev);
+    if (st != ATTN_OK) return st;
+    PlanParams p;
+    p.cache_seqlens = cache_seqlens;
+    p.new_lens = new_lens;
+    p.block_table = block_table;
+    p.free_pages = free_pages;
+    p.free_count = free_count;
+    p.free_left = free_left;
+    p.cu_seqlens_q = cu_seqlens_q;
+    p.seqlens_after = seqlens_after;
+    p.positions = positions;
+    p.slot_map = slot_map;
+    p.page_off = static_cast<int*>(workspace);
+    p.status = dev->status;
+    p.batch = batch;
+    p.total_q = total_q;
+    p.page_size = page_size;
+    p.max_pages = max_pages_per_seq;
+    p.num_free = num_free_pages;
+    p.num_pages = num_pages;
+    return launch_plan(p, static_cast<cudaStream_t>(stream)) == cudaSuccess ? ATTN_OK : ATTN_ERR_CUDA;
+}
+
+}  // extern "C"
+
+namespace {
+
+// ---- norms of queries and keys with the rotation --------------------------------------------
+
+bool stride_ok(int64_t stride, int heads, int d) {
+    return stride >= static_cast<int64_t>(heads) * d && stride % 8 == 0 && stride <= (1LL << 31) - 1;
+}
+
+// The checks that the calls share, and what they have in common of the parameters.
+attn_status_t norm_rope_params(NormRopeParams& p, const void* q, const void* k, int64_t q_stride,
+                               int64_t k_stride, const void* q_weight, const void* k_weight,
+                               int weight_fp32, float eps, const float* rotary_cos,
+                               const float* rotary_sin, int rotary_dim, int rotary_rows,
+                               int rotary_interleaved, const int32_t* positions, int axes,
+                               const int32_t* sections, int sections_interleaved, int total,
+                               int nheads_q, int nheads_kv, int head_dim) {
+    if (total < 0 || nheads_q <= 0 || nheads_kv <= 0) return ATTN_ERR_INVALID_ARG;
+    if (head_dim != 64 && head_dim != 128) return ATTN_ERR_UNSUPPORTED;
+    if (nheads_q > 65535 || nheads_kv > 65535 ||
+        static_cast<long long>(total) * (nheads_q > nheads_kv ? nheads_q : nheads_kv) > (1LL << 31) - 1)
+        return ATTN_ERR_UNSUPPORTED;
+    if (rotary_dim < 0 || rotary_dim > head_dim || rotary_dim % 16 != 0) return ATTN_ERR_UNSUPPORTED;
+    if ((q_weight || k_weight) && !(isfinite(eps) && eps >= 0x1p-64f)) return ATTN_ERR_INVALID_ARG;
+    memset(&p, 0, sizeof(p));
+    if (rotary_dim > 0) {
+        if (axes > kNrAxes) return ATTN_ERR_UNSUPPORTED;
+        if (axes < 1 || !rotary_cos || !rotary_sin || rotary_rows <= 0 || !aligned(rotary_cos, 16) ||
+            !aligned(rotary_sin, 16) || !aligned(positions, 4) || (axes > 1 && !sections))
+            return ATTN_ERR_INVALID_ARG;
+        const int half = rotary_dim / 2;
+        int left[kNrAxes] = {half, 0, 0};
+        if (axes > 1) {
+            long long sum = 0;
+            for (int a = 0; a < axes; ++a) {
+                left[a] = sections[a];
+                if (left[a] < 0) return ATTN_ERR_INVALID_ARG;
+                sum += left[a];
+            }
+            if (sum != half) return ATTN_ERR_INVALID_ARG;
+        }
+        for (int i = 0, a = 0; i < half; ++i) {
+            if (sections_interleaved) {  // the axes in turn; planes of a section that is done go to axis 0
+                a = i % axes;
+                if (a > 0 && left[a] == 0) a = 0;
+            } else {
+                while (left[a] == 0) ++a;
+            }
+            if (--left[a] < 0) return ATTN_ERR_INVALID_ARG;
+            p.plane_axis[i / 16] |= static_cast<unsigned>(a) << (2 * (i % 16));
+        }
+    }
+    if (total == 0) return ATTN_OK;
+    if (!q || !k || (rotary_dim > 0 && !positions)) return ATTN_ERR_INVALID_ARG;
+    if (!stride_ok(q_stride, nheads_q, head_dim) || !stride_ok(k_stride, nheads_kv, head_dim) ||
+        !aligned(q, 16) || !aligned(k, 16) || !aligned(q_weight, weight_fp32 ? 4 : 2) ||
+        !aligned(k_weight, weight_fp32 ? 4 : 2))
+        return ATTN_ERR_INVALID_ARG;
+    p.q = static_cast<const __nv_bfloat16*>(q);
+    p.k = static_cast<const __nv_bfloat16*>(k);
+    p.q_stride = static_cast<int>(q_stride);
+    p.k_stride = static_cast<int>(k_stride);
+    p.q_weight = q_weight;
+    p.k_weight = k_weight;
+    p.weight_f32 = weight_fp32 ? 1 : 0;
+    p.eps = eps;
+    p.rot_cos = rotary_cos;
+    p.rot_sin = rotary_sin;
+    p.rot_dim = rotary_dim;
+    p.rot_rows = rotary_rows;
+    p.interleaved = rotary_interleaved ? 1 : 0;
+    p.positions = positions;
+    p.axes = axes;
+    p.total = total;
+    p.Hq = nheads_q;
+    p.Hkv = nheads_kv;
+    return ATTN_OK;
+}
+
+template <typename Launch>
+attn_status_t norm_rope_launch(NormRopeParams& p, Launch launch) {
+    DeviceState* dev = nullptr;
+    const attn_status_t st = device_state(&dev);
+    if (st != ATTN_OK) return st;
+    p.status = dev->status;
+    return launch(p) == cudaSuccess ? ATTN_OK : ATTN_ERR_CUDA;
+}
+
+}  // namespace
+
+extern "C" {
+
+attn_status_t attn_qk_norm_rope(const void* q, const void* k, int64_t q_stride, int64_t k_stride,
+                                const void* q_weight, const void* k_weight, int weight_fp32,
+                                float eps, const float* rotary_cos, const float* rotary_sin,
+                                int rotary_dim, int rotary_rows, int rotary_interleaved,
+                                const int32_t* positions, int axes, const int32_t* sections,
+                                int sections_interleaved, void* q_out, void* k_out, int total,
+                                int nheads_q, int nheads_kv, int head_dim, void* stream) {
+    NvtxRange nvtx_range("attn_qk_norm_rope");
+    NormRopeParams p;
+    const attn_status_t st = norm_rope_params(
+        p, q, k, q_stride, k_stride, q_weight, k_weight, weight_fp32, eps, rotary_cos, rotary_sin, rotary_dim,
+        rotary_rows, rotary_interleaved, positions, axes, sections, sections_interleaved, total, nheads_q,
+        nheads_kv, head_dim);
+    if (st != ATTN_OK || total == 0) return st;
+    if (!q_out || !k_out || !aligned(q_out, 16) || !aligned(k_out, 16)) return ATTN_ERR_INVALID_ARG;
+    p.q_out = static_cast<__nv_bfloat16*>(q_out);
+    p.k_out = static_cast<__nv_bfloat16*>(k_out);
+    return norm_rope_launch(p, [&](const NormRopeParams& x) {
+        return launch_norm_rope(x, head_dim, false, static_cast<cudaStream_t>(stream));
+    });
+}
+
+size_t attn_qk_norm_rope_bwd_workspace_bytes(int head_dim) {
+    if (head_dim != 64 && head_dim != 128) return 0;
+    return align_up(sizeof(float) * kNrBwdBlocks * static_cast<size_t>(head_dim), 256);
+}
+
+attn_status_t attn_qk_norm_rope_bwd(const void* dq_out, const void* dk_out, const void* q,
+                                    const void* k, int64_t q_stride, int64_t k_stride,
+                                    const void* q_weight, const void* k_weight, int weight_fp32,
+                                    float eps, const float* rotary_cos, const float* rotary_sin,
+                                    int rotary_dim, int rotary_rows, int rotary_interleaved,
+                                    const int32_t* positions, int axes, const int32_t* sections,
+                                    int sections_interleaved, void* dq, void* dk, int64_t dq_stride,
+                                    int64_t dk_stride, float* dq_weight, float* dk_weight, int total,
+                                    int nheads_q, int nheads_kv, int head_dim, void* workspace,
+                                    size_t workspace_bytes, void* stream) {
+    NvtxRange nvtx_range("attn_qk_norm_rope_bwd");
+    NormRopeParams p;
+    const attn_status_t st = norm_rope_params(
+        p, q, k, q_stride, k_stride, q_weight, k_weight, weight_fp32, eps, rotary_cos, rotary_sin, rotary_dim,
+        rotary_rows, rotary_interleaved, positions, axes, sections, sections_interleaved, total, nheads_q,
+        nheads_kv, head_dim);
+    if (st != ATTN_OK) return st;
+    const cudaStream_t s = static_cast<cudaStream_t>(stream);
+    if (!aligned(dq_weight, 4) || !aligned(dk_weight, 4)) return ATTN_ERR_INVALID_ARG;
+    if (total == 0) {  // sums of nothing
+        const size_t bytes = sizeof(float) * head_dim;
+        if ((dq_weight && cudaMemsetAsync(dq_weight, 0, bytes, s) != cudaSuccess) ||
+            (dk_weight && cudaMemsetAsync(dk_weight, 0, bytes, s) != cudaSuccess))
+            return ATTN_ERR_CUDA;
+        return ATTN_OK;
+    }
+    if (!dq_out || !dk_out || !dq || !dk || !aligned(dq_out, 16) || !aligned(dk_out, 16) ||
+        !aligned(dq, 16) || !aligned(dk, 16) || !stride_ok(dq_stride, nheads_q, head_dim) ||
+        !stride_ok(dk_stride, nheads_kv, head_dim) || (q_weight == nullptr) != (dq_weight == nullptr) ||
+        (k_weight == nullptr) != (dk_weight == nullptr))
+        return ATTN_ERR_INVALID_ARG;
+    if ((dq_weight || dk_weight) &&
+        (!workspace || workspace_bytes < attn_qk_norm_rope_bwd_workspace_bytes(head_dim) ||
+         !aligned(workspace, 256)))
+        return ATTN_ERR_WORKSPACE;
+    p.dq_out = static_cast<const __nv_bfloat16*>(dq_out);
+    p.dk_out = static_cast<const __nv_bfloat16*>(dk_out);
+    p.dq = static_cast<__nv_bfloat16*>(dq);
+    p.dk = static_cast<__nv_bfloat16*>(dk);
+    p.dq_stride = static_cast<int>(dq_stride);
+    p.dk_stride = static_cast<int>(dk_stride);
+    p.dq_weight = dq_weight;
+    p.dk_weight = dk_weight;
+    p.part_w = static_cast<float*>(workspace);
+    return norm_rope_launch(p, [&](const NormRopeParams& x) {
+        return launch_norm_rope_bwd(x, head_dim, s);
+    });
+}
+
+attn_status_t attn_kvcache_append_norm_rope(
+    const void* q, const void* k, const void* v, int64_t q_stride, int64_t k_stride, int64_t v_stride,
+    const void* q_weight, const void* k_weight, int weight_fp32, float eps, const float* rotary_cos,
+    const float* rotary_sin, int rotary_dim, int rotary_rows, int rotary_interleaved,
+    const int32_t* positions, int axes, const int32_t* sections, int sections_interleaved, void* q_out,
+    void* k_cache, void* v_cache, const int32_t* slot_map, int total, int nheads_q, int nheads_kv,
+    int head_dim, int page_size, int num_pages, void* stream) {
+    NvtxRange nvtx_range("attn_kvcache_append_norm_rope");
+    NormRopeParams p;
+    if (page_size <= 0 || num_pages <= 0) return ATTN_ERR_INVALID_ARG;
+    const attn_status_t st = norm_rope_params(
+        p, q, k, q_stride, k_stride, q_weight, k_weight, weight_fp32, eps, rotary_cos, rotary_sin, rotary_dim,
+        rotary_rows, rotary_interleaved, positions, axes, sections, sections_interleaved, total, nheads_q,
+        nheads_kv, head_dim);
+    if (st != ATTN_OK) return st;
+    const long long rows = static_cast<long long>(num_pages) * page_size;
+    if (rows * nheads_kv > (1LL << 31) - 1) return ATTN_ERR_UNSUPPORTED;
+    if (total == 0) return ATTN_OK;
+    if (!v || !q_out || !k_cache || !v_cache || !slot_map || !aligned(v, 16) || !aligned(q_out, 16) ||
+        !aligned(k_cache, 16) || !aligned(v_cache, 16) || !aligned(slot_map, 4) ||
+        !stride_ok(v_stride, nheads_kv, head_dim))
+        return ATTN_ERR_INVALID_ARG;
+    p.v = static_cast<const __nv_bfloat16*>(v);
+    p.v_stride = static_cast<int>(v_stride);
+    p.q_out = static_cast<__nv_bfloat16*>(q_out);
+    p.k_cache = static_cast<__nv_bfloat16*>(k_cache);
+    p.v_cache = static_cast<__nv_bfloat16*>(v_cache);
+    p.slots = slot_map;
+    p.cache_rows = static_cast<int>(rows);
+    return norm_rope_launch(p, [&](const NormRopeParams& x) {
+        return launch_norm_rope(x, head_dim, true, static_cast<cudaStream_t>(stream));
+    });
+}
+
+}  // extern "C"
+
+namespace {
+
+// ---- decode behind shared prefixes ------------------------------------------------------------
+
+struct SharedLayout {
+    long long max_units, own_units, max_items, max_parts;
+    size_t groups, units, items, part_lse, part_o, bytes;
+};
+
+// The list's bounds.  Units: every sequence and every group may end in one that is not full.  Pieces: a unit
+// takes one for each kv head and all of them together kSharedShares more.  False: sizes that the call refuses.
+bool shared_layout(int batch, int n_groups, int total_q, int nheads_q, int nheads_kv, int head_dim,
+                   SharedLayout* l) {
+    if (batch < 0 || n_groups < 0 || total_q < 0 || nheads_q <= 0 || nheads_kv <= 0 ||
+        nheads_q % nheads_kv != 0 || (head_dim != 64 && head_dim != 128))
+        return false;
+    const int g = nheads_q / nheads_kv;
+    if (g > 128 || batch > 65535 || n_groups > 65535 || nheads_kv > 65535) return false;
+    const long long per = 2ll * tokens_per_tile(g), full = total_q / per;
+    const long long rows = static_cast<long long>(total_q) * nheads_q;
+    l->own_units = batch + full;
+    l->max_units = l->own_units + n_groups + full;
+    l->max_items = l->max_units * nheads_kv + kSharedShares;
+    l->max_parts = 2 * rows + kSharedShares * std::min(per * g, static_cast<long long>(total_q) * g);
+    if (l->max_items > (1LL << 31) - 1 || l->max_parts > (1LL << 31) - 1) return false;
+    size_t at = sizeof(SharedHeader);
+    const auto take = [&at](size_t bytes) {
+        const size_t here = at;
+        at = align_up(at + bytes, 256);
+        return here;
+    };
+    l->groups = take(sizeof(int4) * n_groups);
+    l->units = take(sizeof(SharedUnit) * l->max_units);
+    l->items = take(sizeof(int2) * l->max_items);
+    l->part_lse = take(sizeof(float) * l->max_parts);
+    l->part_o = take(sizeof(float) * l->max_parts * head_dim);
+    l->bytes = at;
+    return true;
+}
+
+}  // namespace
+
+extern "C" {
+
+size_t attn_decode_kvcache_shared_workspace_bytes(int batch, int num_groups, int total_q, int nheads_q,
+                                                  int nheads_kv, int head_dim) {
+    SharedLayout l;
+    return shared_layout(batch, num_groups, total_q, nheads_q, nheads_kv, head_dim, &l) ? l.bytes : 0;
+}
+
+attn_status_t attn_decode_kvcache_shared(const void* q, const void* k_cache, const void* v_cache,
+                                         const int32_t* cache_seqlens, const int32_t* block_table,
+                                         const int32_t* group_starts, const int32_t* prefix_lens,
+                                         const int32_t* cu_seqlens_q, int page_size, void* out,
+                                         float* lse, int batch, int num_groups, int total_q,
+                                         int max_seqlen_q, int nheads_q, int nheads_kv, int head_dim,
+                                         int max_pages_per_seq, int num_pages, float softmax_scale,
+                                         void* workspace, size_t workspace_bytes, void* stream) {
+    NvtxRange nvtx_range("attn_decode_kvcache_shared");
+    if (batch < 0 || num_groups < 0 || total_q < 0 || max_seqlen_q < 0 || nheads_q <= 0 ||
+        nheads_kv <= 0 || nheads_q % nheads_kv != 0 || max_pages_per_seq <= 0 || num_pages <= 0 ||
+        page_size <= 0 || !scale_ok(softmax_scale) || (!cu_seqlens_q && total_q != batch))
+        return ATTN_ERR_INVALID_ARG;
+    if (head_dim != 64 && head_dim != 128) return ATTN_ERR_UNSUPPORTED;
+    // pages hold whole 16-row boxes and a 128-key block is whole pages or part of one
+    if (page_size % 16 != 0 || (kFwdBlockN % page_size != 0 && page_size % kFwdBlockN != 0))
+        return ATTN_ERR_UNSUPPORTED;
+    SharedLayout l;
+    if (!shared_layout(batch, num_groups, total_q, nheads_q, nheads_kv, head_dim, &l))
+        return ATTN_ERR_UNSUPPORTED;
+    const long long cache_rows = static_cast<long long>(num_pages) * page_size;
+    if (cache_rows * nheads_kv > (1LL << 31) - 1 ||
+        static_cast<long long>(max_pages_per_seq) * page_size > (1LL << 30))
+        return ATTN_ERR_UNSUPPORTED;
+    if (batch == 0 || total_q == 0) return ATTN_OK;
+    if (!q || !k_cache || !v_cache || !cache_seqlens || !block_table || !out || !lse ||
+        (num_groups > 0 && (!group_starts || !prefix_lens)))
+        return ATTN_ERR_INVALID_ARG;
+    if (!aligned(q, 16) || !aligned(k_cache, 16) || !aligned(v_cache, 16) || !aligned(out, 16) ||
+        !aligned(lse, 4) || !aligned(cache_seqlens, 4) || !aligned(block_table, 4) ||
+        !aligned(group_starts, 4) || !aligned(prefix_lens, 4) || !aligned(cu_seqlens_q, 4))
+        return ATTN_ERR_INVALID_ARG;
+    if (!workspace || workspace_bytes < l.bytes || !aligned(workspace, 256)) return ATTN_ERR_WORKSPACE;
+
+    DeviceState* dev = nullptr;
+    const attn_status_t st = device_state(&dev);
+    if (st != ATTN_OK) return st;
+    uint8_t* ws = static_cast<uint8_t*>(workspace);
+    SharedParams p;
+    memset(&p, 0, sizeof(p));
+    p.g = nheads_q / nheads_kv;
+    p.tpt = tokens_per_tile(p.g);
+    p.box_rows = page_size < kFwdBlockN ? page_size : kFwdBlockN;
+    if (encode_3d(&p.tm_q, q, head_dim, nheads_q, total_q, p.g, p.tpt) != ATTN_OK ||
+        encode_3d(&p.tm_q1, q, head_dim, nheads_q, total_q, p.g, 1) != ATTN_OK ||
+        encode_3d(&p.tm_k, k_cache, head_dim, nheads_kv, cache_rows, 1, p.box_rows) != ATTN_OK ||
+        encode_3d(&p.tm_v, v_cache, head_dim, nheads_kv, cache_rows, 1, p.box_rows) != ATTN_OK)
+        return ATTN_ERR_CUDA;
+    p.out = static_cast<__nv_bfloat16*>(out);
+    p.lse = lse;
+    p.header = reinterpret_cast<SharedHeader*>(ws);
+    p.groups = reinterpret_cast<int4*>(ws + l.groups);
+    p.units = reinterpret_cast<SharedUnit*>(ws + l.units);
+    p.items = reinterpret_cast<int2*>(ws + l.items);
+    p.part_lse = reinterpret_cast<float*>(ws + l.part_lse);
+    p.part_o = reinterpret_cast<float*>(ws + l.part_o);
+    p.cu_q = cu_seqlens_q;
+    p.seqlens = cache_seqlens;
+    p.block_table = block_table;
+    p.group_starts = group_starts;
+    p.prefix_lens = prefix_lens;
+    p.status = dev->status;
+    p.batch = batch;
+    p.n_groups = num_groups;
+    p.total_q = total_q;
+    p.max_seqlen_q = cu_seqlens_q ? max_seqlen_q : 1;
+    p.Hq = nheads_q;
+    p.Hkv = nheads_kv;
+    p.page_size = page_size;
+    p.max_pages = max_pages_per_seq;
+    p.num_pages = num_pages;
+    p.max_units = static_cast<int>(l.max_units);
+    p.max_items = static_cast<int>(l.max_items);
+    p.max_parts = static_cast<int>(l.max_parts);
+    p.lse_head = cu_seqlens_q ? total_q : 1;
+    p.lse_tok = cu_seqlens_q ? 1 : nheads_q;
+    p.scale_log2 = softmax_scale * kLog2eF;
+    return launch_shared_attn(p, head_dim, dev->num_sms, static_cast<int>(l.own_units),
+                              static_cast<cudaStream_t>(stream)) == cudaSuccess
+               ? ATTN_OK : ATTN_ERR_CUDA;
 }
 
 }  // extern "C"

@@ -1,0 +1,978 @@
+// shared_kernel.cu -- attention of few query tokens a sequence over the paged cache where sequences share
+// prefixes: the keys of a prefix are read once for all the sequences of its group.
+//
+// The method ("Attention kernels: FlashAttention and PagedAttention", sections 三.2, 五.2-五.3, 六.1 and
+// 六.3; "04 · FA4 (CuTeDSL) and engineering interfaces", sections 5 and 6.1-6.2): softmax over two
+// disjoint sets of keys is the LSE-weighted sum of the softmax over each.  A group's tokens are neighbours in q,
+// so a group against its prefix is what one long sequence is against its keys: its tokens times the g query
+// heads of a kv head fill tiles of 128 rows.  Then every sequence meets the keys behind its prefix, and
+// a last kernel merges the parts.
+//
+// GB300 mapping.  One kernel does both kinds of work (units), on tcgen05: one CTA an SM, persistent, two
+// tiles of 128 rows on the same key blocks, roles and barriers as in the prefill kernel (fwd_kernel.cu):
+//   * warp 16 claims items and gathers K and V blocks of 128 keys through block_table, a lane a page, into a
+//     ring of shared-memory slots (K_0, K_1, V_0, K_2, V_1, ..., V_{m-1});
+//   * warp 17 issues S_t = Q_t K^T, warp 18 O_t += P_t V, accumulators in TMEM;
+//   * warps 0-7 and 8-15 do the softmax of the two tiles, 16 rows a warp; a warp whose rows hold no token
+//     only keeps the barriers going.
+// A unit's key blocks are cut into pieces of about 1 / 152 of all the work, so that the CTAs finish
+// together; each piece leaves its rows' O / l and log2 LSE in fp32.
+#include <cuda_bf16.h>
+
+#include "kernels.h"
+#include "ptx.cuh"
+#include "tile_math.h"
+
+namespace attn {
+
+namespace {
+
+constexpr float kShRescale = 8.0f;  // log2: the reference of a row moves when its maximum passes it by more
+constexpr float kShLn2 = 0.69314718055994530942f;
+constexpr int kShBins = 1024;
+constexpr int kShMinPrefix = 128;  // shorter prefixes are read by every sequence
+constexpr int kShMinPiece = 2;     // key blocks a piece takes at least
+constexpr int kShCombineThreads = 256;
+constexpr int kShSoftmaxWarps = 16;
+
+// ---- units and items (one CTA) --------------------------------------------------------------------
+
+struct ShSeq {
+    int q0, n, keys;
+};
+
+__device__ __forceinline__ ShSeq sh_seq(const SharedParams& p, int b) {
+    ShSeq s;
+    s.q0 = b;
+    s.n = 1;
+    if (p.cu_q != nullptr) {
+        s.q0 = p.cu_q[b];
+        s.n = p.cu_q[b + 1] - s.q0;
+    }
+    s.keys = p.seqlens[b];
+    return s;
+}
+
+// Every query of the sequence sees the whole prefix.
+__device__ __forceinline__ bool sh_behind(const ShSeq& s, int prefix) {
+    return s.n > 0 && prefix > 0 && prefix <= s.keys - s.n + 1;
+}
+
+__device__ int sh_scan(int v, int* warp_tot, int& total) {
+    const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+    int x = v;
+#pragma unroll
+    for (int o = 1; o < 32; o <<= 1) {
+        const int y = __shfl_up_sync(0xffffffffu, x, o);
+        if (lane >= o) x += y;
+    }
+    if (lane == 31) warp_tot[warp] = x;
+    __syncthreads();
+    if (warp == 0) {
+        int w = warp_tot[lane];
+#pragma unroll
+        for (int o = 1; o < 32; o <<= 1) {
+            const int y = __shfl_up_sync(0xffffffffu, w, o);
+            if (lane >= o) w += y;
+        }
+        warp_tot[lane] = w;
+    }
+    __syncthreads();
+    const int before = (warp > 0 ? warp_tot[warp - 1] : 0) + x - v;
+    total = warp_tot[31];
+    __syncthreads();
+    return before;
+}
+
+__device__ __forceinline__ int ceil_div(int a, int b) { return (a + b - 1) / b; }
+
+// Units first those of the prefixes, then those of the sequences in order; items longest pieces first, the kv
+// heads of a piece side by side (their keys lie side by side in the cache).
+__global__ void __launch_bounds__(kShUnitsThreads) shared_units_kernel(const SharedParams p) {
+    __shared__ int hist[kShBins];
+    __shared__ int warp_tot[32];
+    __shared__ unsigned long long work;
+    const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
+    griddep_launch_dependents();
+    const long long max_keys = static_cast<long long>(p.max_pages) * p.page_size;
+    if (tid == 0) work = 0;
+    bool bad = false;
+    for (int b = tid; b < p.batch; b += kShUnitsThreads) {
+        const ShSeq s = sh_seq(p, b);
+        bad |= s.q0 < 0 || s.n < 0 || s.n > p.max_seqlen_q || static_cast<long long>(s.q0) + s.n > p.total_q ||
+               s.keys < 0 || s.keys > max_keys;
+    }
+    for (int i = tid; i < p.n_groups; i += kShUnitsThreads) {
+        const int s0 = p.group_starts[i], s1 = p.group_starts[i + 1];
+        bad |= s0 < 0 || s1 < s0 || s1 > p.batch || (i == 0 && s0 != 0) ||
+               (i == p.n_groups - 1 && s1 != p.batch) || p.prefix_lens[i] < 0;
+    }
+    if (__syncthreads_or(bad)) {
+        if (tid == 0) {
+            atomicOr(p.status, kStatusBounds);
+            p.header->n_items = p.header->next_item = p.header->n_own = p.header->n_prefix = 0;
+            p.header->bad = 1;
+        }
+        return;
+    }
+    const int per = 2 * p.tpt;  // tokens a unit
+    // 1. groups: which row of the table leads to the prefix, and which tokens meet it
+    for (int i = warp; i < p.n_groups; i += kShUnitsThreads / 32) {
+        const int s0 = p.group_starts[i], s1 = p.group_starts[i + 1], P = p.prefix_lens[i];
+        int first = -1, count = 0;
+        for (int b = s0; b < s1; b += 32) {
+            const bool on = b + lane < s1 && sh_behind(sh_seq(p, b + lane), P);
+            const unsigned m = __ballot_sync(0xffffffffu, on);
+            if (first < 0 && m != 0) first = b + __ffs(m) - 1;
+            count += __popc(m);
+        }
+        if (lane == 0) {
+            int4 r = make_int4(-1, 0, 0, 0);
+            if (count > 1 && P >= kShMinPrefix) {
+                const ShSeq a = sh_seq(p, s0), z = sh_seq(p, s1 - 1);
+                r = make_int4(first, a.q0, z.q0 + z.n - a.q0, 0);
+            }
+            p.groups[i] = r;
+        }
+    }
+    __syncthreads();
+    // 2. units
+    long long blocks = 0;  // this thread's part of the work, for one kv head
+    int n_prefix = 0;
+    for (int base = 0; base < p.n_groups; base += kShUnitsThreads) {
+        const int i = base + tid;
+        int4 r = make_int4(-1, 0, 0, 0);
+        if (i < p.n_groups) r = p.groups[i];
+        const int n = r.x >= 0 ? ceil_div(r.z, per) : 0;
+        int total;
+        const int at = n_prefix + sh_scan(n, warp_tot, total);
+        if (i < p.n_groups) p.groups[i].w = at;
+        for (int u = 0; u < n; ++u) {
+            SharedUnit x;
+            x.q0 = r.y + u * per;
+            x.ntok = min(per, r.z - u * per);
+            x.row = r.x;
+            x.key_min = 0;
+            x.key_end = p.prefix_lens[i];
+            x.pos0 = 1 << 30;
+            x.blk0 = 0;
+            x.nblk = ceil_div(x.key_end, kFwdBlockN);
+            x.rows = x.ntok * p.g;
+            x.prefix = -1;
+            x.group_q0 = 0;
+            blocks += x.nblk;
+            if (at + u < p.max_units) p.units[at + u] = x;
+        }
+        n_prefix += total;
+    }
+    int n_own = 0;
+    __syncthreads();
+    for (int base = 0; base < p.batch; base += kShUnitsThreads) {
+        const int b = base + tid;
+        ShSeq s = {0, 0, 0};
+        if (b < p.batch) s = sh_seq(p, b);
+        const int n = ceil_div(s.n, per);
+        int total;
+        const int at = n_prefix + n_own + sh_scan(n, warp_tot, total);
+        int prefix = -1, group_q0 = 0, key_min = 0;
+        if (n > 0 && p.n_groups > 0) {
+            int lo = 0, hi = p.n_groups - 1;  // the last group that starts at b or before
+            while (lo < hi) {
+                const int mid = (lo + hi + 1) >> 1;
+                if (p.group_starts[mid] <= b) lo = mid; else hi = mid - 1;
+            }
+            const int4 r = p.groups[lo];
+            if (r.x >= 0 && sh_behind(s, p.prefix_lens[lo])) {
+                prefix = r.w;
+                group_q0 = r.y;
+                key_min = p.prefix_lens[lo];
+            }
+        }
+        for (int u = 0; u < n; ++u) {
+            SharedUnit x;
+            const int t0 = u * per;
+            x.q0 = s.q0 + t0;
+            x.ntok = min(per, s.n - t0);
+            x.row = b;
+            x.key_min = key_min;
+            x.pos0 = s.keys - s.n + t0;
+            x.key_end = max(x.pos0 + x.ntok, 0);
+            x.blk0 = key_min / kFwdBlockN;
+            x.nblk = x.key_end > key_min ? ceil_div(x.key_end, kFwdBlockN) - x.blk0 : 0;
+            x.rows = x.ntok * p.g;
+            x.prefix = prefix;
+            x.group_q0 = group_q0;
+            blocks += x.nblk;
+            if (at + u < p.max_units) p.units[at + u] = x;
+        }
+        n_own += total;
+    }
+    for (int i = tid; i < kShBins; i += kShUnitsThreads) hist[i] = 0;
+    atomicAdd(&work, static_cast<unsigned long long>(blocks));
+    __syncthreads();
+    const int n_units = min(n_prefix + n_own, p.max_units);
+    const long long share_ll = (static_cast<long long>(work) * p.Hkv + kSharedShares - 1) / kSharedShares;
+    const int share = static_cast<int>(max(share_ll, static_cast<long long>(kShMinPiece)));
+    // 3. pieces, the places of their results, and how many are how long
+    int parts = 0, items = 0;
+    for (int base = 0; base < n_units; base += kShUnitsThreads) {
+        const int u = base + tid;
+        int pieces = 0, rows = 0, len = 0;
+        if (u < n_units) {
+            const int nblk = p.units[u].nblk;
+            pieces = ceil_div(nblk, share);
+            if (pieces > 0) len = ceil_div(nblk, pieces);
+            rows = pieces * p.Hkv * p.units[u].rows;
+        }
+        int total;
+        const int at = parts + sh_scan(rows, warp_tot, total);
+        parts += total;
+        sh_scan(pieces * p.Hkv, warp_tot, total);
+        items += total;
+        if (u < n_units) {
+            p.units[u].pieces = pieces;
+            p.units[u].part = at;
+            if (pieces > 0) atomicAdd(&hist[kShBins - 1 - min(len, kShBins - 1)], pieces * p.Hkv);
+        }
+    }
+    __syncthreads();
+    // (the host's bounds hold for every list that passed the checks above)
+    const bool fits = n_prefix + n_own <= p.max_units && parts <= p.max_parts && items <= p.max_items;
+    int total;
+    const int first = sh_scan(hist[tid], warp_tot, total);
+    hist[tid] = first;
+    __syncthreads();
+    for (int base = 0; base < n_units; base += kShUnitsThreads) {
+        const int u = base + tid;
+        int count = 0, at = 0;
+        if (u < n_units && fits) {
+            const int pieces = p.units[u].pieces;
+            count = pieces * p.Hkv;
+            if (count > 0)
+                at = atomicAdd(&hist[kShBins - 1 - min(ceil_div(p.units[u].nblk, pieces), kShBins - 1)], count);
+        }
+        const bool many = count > 64;  // the whole warp writes those
+        if (!many)
+            for (int i = 0; i < count; ++i) p.items[at + i] = make_int2(u, i);
+        for (unsigned m = __ballot_sync(0xffffffffu, many); m != 0; m &= m - 1) {
+            const int src = __ffs(m) - 1;
+            const int from = __shfl_sync(0xffffffffu, at, src), n = __shfl_sync(0xffffffffu, count, src);
+            for (int i = lane; i < n; i += 32) p.items[from + i] = make_int2(u - lane + src, i);
+        }
+    }
+    if (tid == 0) {
+        if (!fits) atomicOr(p.status, kStatusBounds);
+        p.header->n_items = fits ? items : 0;
+        p.header->next_item = 0;
+        p.header->n_own = n_own;
+        p.header->n_prefix = n_prefix;
+        p.header->bad = fits ? 0 : 1;
+    }
+}
+
+// ---- attention ------------------------------------------------------------------------------------
+
+template <int D>
+struct ShCfg {
+    static constexpr int kHalves = D / 64;
+    static constexpr int kAtomBytes = 128 * 128;
+    static constexpr int kQTile = kHalves * kAtomBytes;
+    static constexpr int kKvTile = kHalves * kAtomBytes;
+    static constexpr int kPTile = 2 * kAtomBytes;
+    static constexpr int kSlots = D == 128 ? 3 : 8;
+    static constexpr int kOffQ = 0;
+    static constexpr int kOffP = kOffQ + 2 * kQTile;
+    static constexpr int kOffKV = kOffP + 2 * kPTile;
+    static constexpr int kOffBar = kOffKV + kSlots * kKvTile;
+    static constexpr int kSmem = kOffBar + 768 + 1024;
+    static_assert(kSmem <= 227 * 1024, "shared memory per CTA");
+    static constexpr uint32_t kTmemCols = 512;
+    __device__ static constexpr uint32_t col_s(int t) { return 128u * t; }
+    __device__ static constexpr uint32_t col_o(int t) { return 256u + D * t; }
+};
+
+constexpr uint32_t kShRing = 4;
+constexpr uint32_t kShReaders = 18;  // the two MMA issuers and the 16 softmax warps
+
+// One item as the producer hands it to the other roles: a piece of a unit for one kv head.
+struct ShItem {
+    int q0, ntok;  // ntok = 0: no more items
+    int kvh, row, key_min, key_end, pos0;
+    int jlo, jhi;  // key blocks
+    int part;      // the row of its first result
+    int pad[2];
+};
+
+struct ShBars {
+    uint64_t q_full, q_empty;
+    uint64_t k_full[8], v_full[8], kv_empty[8];  // (one "full" a kind of block: see fwd_kernel.cu)
+    uint64_t s_full[2], s_free[2], p_full[2], pv_done[2], o_free[2];
+    uint64_t drain[2];
+    uint64_t idx_full[kShRing], idx_empty[kShRing];
+    ShItem ring[kShRing];
+    uint32_t tmem_base;
+    int abort_flag;
+};
+static_assert(sizeof(ShBars) <= 768, "barrier block");
+
+// Ring positions, relative to the item's first slot, of K_i and V_i of m blocks.
+__device__ __forceinline__ uint32_t sh_pos_k(int i) { return i == 0 ? 0u : 2u * i - 1u; }
+__device__ __forceinline__ uint32_t sh_pos_v(int i, int m) { return i == m - 1 ? 2u * m - 1u : 2u * i + 2u; }
+
+__device__ __forceinline__ uint32_t sh_parity(uint32_t bits, uint32_t st) { return (bits >> st) & 1u; }
+
+// The producer warp's claim of ring position r (false: a wait gave up).
+__device__ __forceinline__ bool sh_claim(const SharedParams& p, ShBars* bars, const Watchdog& wd, int n_items,
+                                         uint32_t r, ShItem& it, int lane) {
+    const uint32_t slot = r % kShRing;
+    const bool ok = r < kShRing || wd.wait(&bars->idx_empty[slot], ((r / kShRing) - 1) & 1);
+    if (!__all_sync(0xffffffffu, ok)) return false;
+    int idx = 0;
+    if (lane == 0) idx = atomicAdd(&p.header->next_item, 1);
+    idx = __shfl_sync(0xffffffffu, idx, 0);
+    it.ntok = 0;
+    if (idx < n_items) {
+        const int2 w = p.items[idx];
+        const SharedUnit u = p.units[w.x];
+        const int piece = w.y / p.Hkv;
+        it.q0 = u.q0;
+        it.ntok = u.ntok;
+        it.kvh = w.y - piece * p.Hkv;
+        it.row = u.row;
+        it.key_min = u.key_min;
+        it.key_end = u.key_end;
+        it.pos0 = u.pos0;
+        it.jlo = u.blk0 + static_cast<int>(static_cast<long long>(u.nblk) * piece / u.pieces);
+        it.jhi = u.blk0 + static_cast<int>(static_cast<long long>(u.nblk) * (piece + 1) / u.pieces);
+        it.part = u.part + (it.kvh * u.pieces + piece) * u.rows;
+    }
+    if (lane == 0) {
+        bars->ring[slot] = it;
+        mbar_arrive(&bars->idx_full[slot]);  // release: the item is visible to the readers
+    }
+    return true;
+}
+
+__device__ __forceinline__ bool sh_take(ShBars* bars, const Watchdog& wd, uint32_t& r, ShItem& it) {
+    const uint32_t slot = r % kShRing;
+    if (!wd.wait(&bars->idx_full[slot], (r / kShRing) & 1)) return false;
+    it = bars->ring[slot];
+    mbar_arrive(&bars->idx_empty[slot]);
+    ++r;
+    return it.ntok > 0;
+}
+
+__device__ __forceinline__ bool sh_take_warp(ShBars* bars, const Watchdog& wd, uint32_t& r, ShItem& it, int lane) {
+    const uint32_t slot = r % kShRing;
+    if (!__all_sync(0xffffffffu, wd.wait(&bars->idx_full[slot], (r / kShRing) & 1))) return false;
+    it = bars->ring[slot];
+    __syncwarp();
+    if (lane == 0) mbar_arrive(&bars->idx_empty[slot]);
+    ++r;
+    return it.ntok > 0;
+}
+
+// Wait, ignoring the abort flag, for a phase that TMA or the tensor core still owes this CTA.
+__device__ void sh_drain(uint64_t* bar, uint32_t parity) {
+    const unsigned long long t0 = global_ns();
+    while (!mbar_try(bar, parity)) {
+        if (global_ns() - t0 > 200000000ull) return;
+    }
+}
+
+struct ShRingState {
+    uint32_t n = 0, kpar = 0, vpar = 0, lastv = 0;
+};
+
+// The whole warp: lane i looks up piece i of a block in the table and loads it.
+template <int D>
+__device__ void sh_producer_loop(const SharedParams& p, uint8_t* smem, ShBars* bars, const Watchdog& wd,
+                                 int n_items, uint32_t& q_cnt, ShRingState& ring, int lane) {
+    using C = ShCfg<D>;
+    if (lane == 0) {
+        tma_prefetch_desc(&p.tm_q);
+        tma_prefetch_desc(&p.tm_q1);
+        tma_prefetch_desc(&p.tm_k);
+        tma_prefetch_desc(&p.tm_v);
+    }
+    const int boxes = kFwdBlockN / p.box_rows;
+    const int oob_row = p.num_pages * p.page_size;
+    uint32_t claims = 0;
+    ShItem it, next;
+    if (!sh_claim(p, bars, wd, n_items, claims++, it, lane)) return;
+    while (it.ntok > 0) {
+        if (!__all_sync(0xffffffffu, q_cnt == 0 || wd.wait(&bars->q_empty, (q_cnt - 1) & 1))) return;
+        if (lane == 0) {
+            uint32_t bytes = 0;
+#pragma unroll
+            for (int t = 0; t < 2; ++t) {
+                const int tokens = it.ntok - t * p.tpt;
+                if (tokens > 0) bytes += 128u * p.g * (tokens == 1 ? 1 : p.tpt) * C::kHalves;
+            }
+            mbar_arrive_expect_tx(&bars->q_full, bytes);
+#pragma unroll
+            for (int t = 0; t < 2; ++t) {
+                const int tokens = it.ntok - t * p.tpt;
+                if (tokens <= 0) continue;
+#pragma unroll
+                for (int h = 0; h < C::kHalves; ++h)
+                    tma_load_3d(smem + C::kOffQ + t * C::kQTile + h * C::kAtomBytes, tokens == 1 ? &p.tm_q1 : &p.tm_q,
+                                &bars->q_full, h * 64, it.kvh * p.g, it.q0 + t * p.tpt);
+            }
+        }
+        ++q_cnt;
+        const int m = it.jhi - it.jlo;
+        const int* bt = p.block_table + static_cast<size_t>(it.row) * p.max_pages;
+        for (int r = 0; r < 2 * m; ++r) {
+            // inverse of sh_pos_k / sh_pos_v
+            const bool last = r == 2 * m - 1;
+            const bool is_v = last || (r > 0 && (r & 1) == 0);
+            const int i = is_v ? (last ? m - 1 : (r - 2) / 2) : (r + 1) / 2;
+            // Boxes without a key of this unit (whose table entries are not read) and boxes of a bad page are
+            // aimed past the end of the cache: TMA fills them with zeros.
+            int row = oob_row;
+            if (lane < boxes) {
+                const int key = (it.jlo + i) * kFwdBlockN + lane * p.box_rows;
+                if (key < it.key_end && key + p.box_rows > it.key_min) {
+                    const int page = bt[key / p.page_size];
+                    if (page >= 0 && page < p.num_pages)
+                        row = page * p.page_size + key % p.page_size;
+                    else
+                        atomicOr(p.status, kStatusBounds);
+                }
+            }
+            const uint32_t n = ring.n, st = n % C::kSlots;
+            if (!__all_sync(0xffffffffu, n < C::kSlots || wd.wait(&bars->kv_empty[st], ((n / C::kSlots) - 1) & 1)))
+                return;
+            uint64_t* const full = is_v ? &bars->v_full[st] : &bars->k_full[st];
+            if (lane == 0) mbar_arrive_expect_tx(full, C::kKvTile);
+            __syncwarp();
+            ++ring.n;
+            if (is_v) {
+                ring.vpar ^= 1u << st;
+                ring.lastv |= 1u << st;
+            } else {
+                ring.kpar ^= 1u << st;
+                ring.lastv &= ~(1u << st);
+            }
+            if (lane < boxes) {
+                uint8_t* const dst = smem + C::kOffKV + st * C::kKvTile + lane * p.box_rows * 128;
+#pragma unroll
+                for (int h = 0; h < C::kHalves; ++h)
+                    tma_load_3d(dst + h * C::kAtomBytes, is_v ? &p.tm_v : &p.tm_k, full, h * 64, it.kvh, row);
+            }
+            // the next item's claim, behind the blocks still to come (see fwd_kernel.cu)
+            if (r == max(min(1, 2 * m - 1), 2 * m - 5) &&
+                !sh_claim(p, bars, wd, n_items, claims++, next, lane))
+                return;
+        }
+        it = next;
+    }
+}
+
+template <int D>
+__device__ void sh_producer(const SharedParams& p, uint8_t* smem, ShBars* bars, const Watchdog& wd, int n_items,
+                            int lane) {
+    using C = ShCfg<D>;
+    uint32_t q_cnt = 0;
+    ShRingState ring;
+    sh_producer_loop<D>(p, smem, bars, wd, n_items, q_cnt, ring, lane);
+    __syncwarp();
+    // what is in flight lands before the CTA's shared memory goes
+    if (q_cnt > 0) sh_drain(&bars->q_full, (q_cnt - 1) & 1);
+    for (uint32_t st = 0; st < C::kSlots && st < ring.n; ++st) {
+        const bool v = sh_parity(ring.lastv, st) != 0;
+        sh_drain(v ? &bars->v_full[st] : &bars->k_full[st], sh_parity(v ? ring.vpar : ring.kpar, st) ^ 1u);
+    }
+}
+
+template <int D>
+__device__ void sh_mma_s(const SharedParams& p, uint8_t* smem, ShBars* bars, uint32_t tmem, const Watchdog& wd) {
+    using C = ShCfg<D>;
+    constexpr uint32_t kIdesc = idesc_bf16_f32(128, kFwdBlockN, false, false);
+    const uint64_t dq = sdesc_sw128(smem_u32(smem + C::kOffQ), 16, 1024);
+    const uint64_t dkv = sdesc_sw128(smem_u32(smem + C::kOffKV), 16, 1024);
+    const uint32_t q_lo = static_cast<uint32_t>(dq), d_hi = static_cast<uint32_t>(dq >> 32);
+    const uint32_t kv_lo = static_cast<uint32_t>(dkv);
+    uint32_t q_cnt = 0, kv_cnt = 0, kpar = 0, rd = 0;
+    uint32_t s_cnt[2] = {0, 0};
+    ShItem it;
+    while (sh_take(bars, wd, rd, it)) {
+        if (!wd.wait(&bars->q_full, q_cnt & 1)) return;
+        ++q_cnt;
+        const int m = it.jhi - it.jlo;
+        const bool two = it.ntok > p.tpt;
+        for (int i = 0; i < m; ++i) {
+            const uint32_t st = (kv_cnt + sh_pos_k(i)) % C::kSlots;
+            if (!wd.wait(&bars->k_full[st], sh_parity(kpar, st))) return;
+            kpar ^= 1u << st;
+            const uint32_t k_lo = kv_lo + st * (C::kKvTile >> 4);
+#pragma unroll
+            for (int t = 0; t < 2; ++t) {
+                if (t == 1 && !two) continue;
+                if (s_cnt[t] > 0 && !wd.wait(&bars->s_free[t], (s_cnt[t] - 1) & 1)) return;
+                tc_fence_after();
+                const uint32_t a_lo = q_lo + t * (C::kQTile >> 4);
+#pragma unroll
+                for (int kk = 0; kk < D / 16; ++kk) {
+                    const uint32_t off = ((kk >> 2) * C::kAtomBytes + (kk & 3) * 32) >> 4;
+                    umma_ss_lh(tmem + C::col_s(t), a_lo + off, d_hi, k_lo + off, d_hi, kIdesc, kk > 0);
+                }
+                umma_commit(&bars->s_full[t]);
+                ++s_cnt[t];
+            }
+            umma_commit(&bars->kv_empty[st]);
+        }
+        umma_commit(&bars->q_empty);
+        kv_cnt += 2 * m;
+    }
+}
+
+template <int D>
+__device__ void sh_mma_pv(const SharedParams& p, uint8_t* smem, ShBars* bars, uint32_t tmem, const Watchdog& wd) {
+    using C = ShCfg<D>;
+    constexpr uint32_t kIdesc = idesc_bf16_f32(128, D, false, true);
+    const uint64_t dp = sdesc_sw128(smem_u32(smem + C::kOffP), 16, 1024);
+    const uint64_t dv = sdesc_sw128(smem_u32(smem + C::kOffKV), C::kAtomBytes, 1024);
+    const uint32_t p_lo = static_cast<uint32_t>(dp), p_hi = static_cast<uint32_t>(dp >> 32);
+    const uint32_t v_lo = static_cast<uint32_t>(dv), v_hi = static_cast<uint32_t>(dv >> 32);
+    uint32_t kv_cnt = 0, vpar = 0, rd = 0;
+    uint32_t pv_cnt[2] = {0, 0}, o_items[2] = {0, 0};
+    ShItem it;
+    while (sh_take(bars, wd, rd, it)) {
+        const int m = it.jhi - it.jlo;
+        const bool two = it.ntok > p.tpt;
+        for (int i = 0; i < m; ++i) {
+            const uint32_t st = (kv_cnt + sh_pos_v(i, m)) % C::kSlots;
+            if (!wd.wait(&bars->v_full[st], sh_parity(vpar, st))) return;
+            vpar ^= 1u << st;
+            const uint32_t b_lo = v_lo + st * (C::kKvTile >> 4);
+#pragma unroll
+            for (int t = 0; t < 2; ++t) {
+                if (t == 1 && !two) continue;
+                if (i == 0 && o_items[t] > 0 && !wd.wait(&bars->o_free[t], (o_items[t] - 1) & 1)) return;
+                if (!wd.wait(&bars->p_full[t], pv_cnt[t] & 1)) return;
+                tc_fence_after();
+                const uint32_t a_lo = p_lo + t * (C::kPTile >> 4);
+#pragma unroll
+                for (int kk = 0; kk < kFwdBlockN / 16; ++kk) {
+                    const uint32_t off = ((kk >> 2) * C::kAtomBytes + (kk & 3) * 32) >> 4;
+                    umma_ss_lh(tmem + C::col_o(t), a_lo + off, p_hi, b_lo + kk * (16 * 128 >> 4), v_hi, kIdesc,
+                               (i == 0 && kk == 0) ? 0u : 1u);
+                }
+                umma_commit(&bars->pv_done[t]);
+                ++pv_cnt[t];
+            }
+            umma_commit(&bars->kv_empty[st]);
+        }
+        ++o_items[0];
+        if (two) ++o_items[1];
+        kv_cnt += 2 * m;
+    }
+}
+
+// Softmax of tile t, rows 32 (k % 4) + 16 (k / 4) + [0, 16) of it by warp k, in the layout of an MMA's
+// accumulator fragment: thread i holds rows i / 4 and i / 4 + 8, two columns of each 8.
+template <int D>
+__device__ void sh_softmax(const SharedParams& p, uint8_t* smem, ShBars* bars, uint32_t tmem, const Watchdog& wd,
+                           int t, int k, int lane) {
+    using C = ShCfg<D>;
+    uint64_t* const s_full = &bars->s_full[t];
+    uint64_t* const s_free = &bars->s_free[t];
+    uint64_t* const p_full = &bars->p_full[t];
+    uint64_t* const pv_done = &bars->pv_done[t];
+    uint64_t* const o_free = &bars->o_free[t];
+    const int rbase = 32 * (k & 3) + 16 * (k >> 2);
+    const int ra = rbase + (lane >> 2);
+    const int cpair = 2 * (lane & 3);
+    const uint32_t tS = tmem + (static_cast<uint32_t>(rbase) << 16) + C::col_s(t);
+    const uint32_t tO = tmem + (static_cast<uint32_t>(rbase) << 16) + C::col_o(t);
+    const uint32_t p_tile = smem_u32(smem + C::kOffP + t * C::kPTile);
+    // stmatrix: this thread addresses row lane % 8 of matrix lane / 8 (see fwd_kernel.cu)
+    const int st_row = rbase + 8 * ((lane >> 3) & 1) + (lane & 7);
+    const int st_dc = lane >> 4;
+    uint32_t st_addr[4];
+#pragma unroll
+    for (int c = 0; c < 4; ++c) st_addr[c] = p_tile + st_row * 128 + ((((2 * c + st_dc) ^ lane) & 7) << 4);
+    const float sl2 = p.scale_log2;
+    const uint64_t sl2x2 = f2_make(sl2, sl2);
+    const int g = p.g;
+    uint32_t blk = 0, kv_cnt = 0, vpar = 0, rd = 0;
+    ShItem it;
+    while (sh_take_warp(bars, wd, rd, it, lane)) {
+        const int m = it.jhi - it.jlo;
+        const uint32_t kv_base = kv_cnt, vpar_item = vpar;
+        kv_cnt += 2 * m;
+        for (int i = 0; i < m; ++i) vpar ^= 1u << ((kv_base + sh_pos_v(i, m)) % C::kSlots);
+        const int tokens = min(p.tpt, it.ntok - t * p.tpt);
+        if (tokens <= 0) continue;
+        const int rows = tokens * g;
+        const bool busy = rbase < rows;  // a row of this warp holds a token
+        // keys [key_min, kmax] of rows ra and ra + 8
+        const int tok0 = t * p.tpt;
+        const int kmax_a = min(it.key_end - 1, it.pos0 + tok0 + ra / g);
+        const int kmax_b = min(it.key_end - 1, it.pos0 + tok0 + (ra + 8) / g);
+        const int kmax_first = min(it.key_end - 1, it.pos0 + tok0);
+        float m_a = -INFINITY, m_b = -INFINITY, l_a = 0.f, l_b = 0.f;
+        for (int j = it.jlo; j < it.jhi; ++j) {
+            if (!__all_sync(0xffffffffu, wd.wait(s_full, blk & 1))) return;
+            uint32_t pka[16], pkb[16];
+            bool need_a = false, need_b = false;
+            float alpha_a = 1.f, alpha_b = 1.f;
+            if (busy) {
+                tc_fence_after();
+                uint32_t s[64];
+                tmem_ld16x256_x8(tS, *reinterpret_cast<uint32_t(*)[32]>(&s[0]));
+                tmem_ld16x256_x8(tS + 64, *reinterpret_cast<uint32_t(*)[32]>(&s[32]));
+                tmem_wait_ld();
+                tc_fence_before();
+                __syncwarp();
+                if (lane == 0) mbar_arrive(s_free);
+                if (j * kFwdBlockN < it.key_min || (j + 1) * kFwdBlockN - 1 > kmax_first) {
+                    const int key0 = j * kFwdBlockN + cpair;
+#pragma unroll
+                    for (int c = 0; c < 16; ++c) {
+#pragma unroll
+                        for (int e = 0; e < 2; ++e) {
+                            const int key = key0 + 8 * c + e;
+                            if (key < it.key_min || key > kmax_a) s[4 * c + e] = __float_as_uint(-INFINITY);
+                            if (key < it.key_min || key > kmax_b) s[4 * c + 2 + e] = __float_as_uint(-INFINITY);
+                        }
+                    }
+                }
+                float xa0 = fmaxf(__uint_as_float(s[0]), __uint_as_float(s[4]));
+                float xa1 = fmaxf(__uint_as_float(s[1]), __uint_as_float(s[5]));
+                float xb0 = fmaxf(__uint_as_float(s[2]), __uint_as_float(s[6]));
+                float xb1 = fmaxf(__uint_as_float(s[3]), __uint_as_float(s[7]));
+#pragma unroll
+                for (int c = 2; c < 16; c += 2) {
+                    xa0 = fmax3(xa0, __uint_as_float(s[4 * c]), __uint_as_float(s[4 * c + 4]));
+                    xa1 = fmax3(xa1, __uint_as_float(s[4 * c + 1]), __uint_as_float(s[4 * c + 5]));
+                    xb0 = fmax3(xb0, __uint_as_float(s[4 * c + 2]), __uint_as_float(s[4 * c + 6]));
+                    xb1 = fmax3(xb1, __uint_as_float(s[4 * c + 3]), __uint_as_float(s[4 * c + 7]));
+                }
+                float mxa = fmaxf(xa0, xa1), mxb = fmaxf(xb0, xb1);
+                mxa = fmaxf(mxa, __shfl_xor_sync(0xffffffffu, mxa, 1));
+                mxb = fmaxf(mxb, __shfl_xor_sync(0xffffffffu, mxb, 1));
+                mxa = fmaxf(mxa, __shfl_xor_sync(0xffffffffu, mxa, 2));
+                mxb = fmaxf(mxb, __shfl_xor_sync(0xffffffffu, mxb, 2));
+                const float mba = mxa * sl2, mbb = mxb * sl2;
+                need_a = mba > m_a + kShRescale;
+                need_b = mbb > m_b + kShRescale;
+                const float mna = need_a ? mba : m_a, mnb = need_b ? mbb : m_b;
+                alpha_a = need_a ? ex2_approx(m_a - mna) : 1.f;
+                alpha_b = need_b ? ex2_approx(m_b - mnb) : 1.f;
+                l_a *= alpha_a;
+                l_b *= alpha_b;
+                m_a = mna;
+                m_b = mnb;
+                const float na = m_a == -INFINITY ? 0.f : -m_a, nb = m_b == -INFINITY ? 0.f : -m_b;
+                const uint64_t nma = f2_make(na, na), nmb = f2_make(nb, nb);
+                uint64_t suma = 0, sumb = 0;
+#pragma unroll
+                for (int c = 0; c < 16; ++c) {
+                    float a0, a1, b0, b1;
+                    f2_split(f2_fma(f2_make(__uint_as_float(s[4 * c]), __uint_as_float(s[4 * c + 1])), sl2x2, nma), a0, a1);
+                    f2_split(f2_fma(f2_make(__uint_as_float(s[4 * c + 2]), __uint_as_float(s[4 * c + 3])), sl2x2, nmb), b0, b1);
+                    const float pa0 = ex2_approx(a0), pa1 = ex2_approx(a1);
+                    const float pb0 = ex2_approx(b0), pb1 = ex2_approx(b1);
+                    suma = f2_add(suma, f2_make(pa0, pa1));
+                    sumb = f2_add(sumb, f2_make(pb0, pb1));
+                    pka[c] = pack_bf16x2(pa0, pa1);
+                    pkb[c] = pack_bf16x2(pb0, pb1);
+                }
+                float lo, hi;
+                f2_split(suma, lo, hi);
+                l_a += lo + hi;
+                f2_split(sumb, lo, hi);
+                l_b += lo + hi;
+            } else if (lane == 0) {
+                mbar_arrive(s_free);
+            }
+            // Slots outside [key_min, key_end) may hold anything, and 0 times a NaN would reach O: this
+            // tile's warps clear those rows of V.
+            const int lo_key = max(it.key_min - j * kFwdBlockN, 0);
+            const int hi_key = min(it.key_end - j * kFwdBlockN, kFwdBlockN);
+            if (lo_key > 0 || hi_key < kFwdBlockN) {
+                uint32_t bits = vpar_item;  // V parities before V_j's load
+                for (int i = 0; i < j - it.jlo; ++i) bits ^= 1u << ((kv_base + sh_pos_v(i, m)) % C::kSlots);
+                const uint32_t st = (kv_base + sh_pos_v(j - it.jlo, m)) % C::kSlots;
+                if (!__all_sync(0xffffffffu, wd.wait(&bars->v_full[st], sh_parity(bits, st)))) return;
+                const uint32_t vslot = smem_u32(smem + C::kOffKV + st * C::kKvTile);
+                const int clear = lo_key + kFwdBlockN - hi_key;
+                for (int u = k * 32 + lane; u < clear * C::kHalves * 8; u += 8 * 32) {
+                    int r = u / (C::kHalves * 8);
+                    const int hc = u % (C::kHalves * 8);
+                    if (r >= lo_key) r += hi_key - lo_key;
+                    st_shared_v4(vslot + (hc >> 3) * C::kAtomBytes + r * 128 + (hc & 7) * 16, 0u, 0u, 0u, 0u);
+                }
+                fence_proxy_async_smem();
+            }
+            // the product before this one has read P_t and added to O_t
+            if (blk > 0) {
+                if (!__all_sync(0xffffffffu, wd.wait(pv_done, (blk - 1) & 1))) return;
+                tc_fence_after();
+            }
+            if (busy) {
+                if (__any_sync(0xffffffffu, need_a || need_b) && j > it.jlo) {
+#pragma unroll 1
+                    for (int cc = 0; cc < D / 32; ++cc) {
+                        uint32_t o[16];
+                        tmem_ld16x256_x4(tO + 32 * cc, o);
+                        tmem_wait_ld();
+#pragma unroll
+                        for (int c = 0; c < 4; ++c) {
+                            o[4 * c] = __float_as_uint(__uint_as_float(o[4 * c]) * alpha_a);
+                            o[4 * c + 1] = __float_as_uint(__uint_as_float(o[4 * c + 1]) * alpha_a);
+                            o[4 * c + 2] = __float_as_uint(__uint_as_float(o[4 * c + 2]) * alpha_b);
+                            o[4 * c + 3] = __float_as_uint(__uint_as_float(o[4 * c + 3]) * alpha_b);
+                        }
+                        tmem_st16x256_x4(tO + 32 * cc, o);
+                    }
+                    tmem_wait_st();
+                    tc_fence_before();
+                }
+#pragma unroll
+                for (int cp = 0; cp < 8; ++cp)
+                    stmatrix_x4(st_addr[cp & 3] + (cp >> 2) * C::kAtomBytes, pka[2 * cp], pkb[2 * cp], pka[2 * cp + 1],
+                                pkb[2 * cp + 1]);
+                fence_proxy_async_smem();
+            }
+            __syncwarp();
+            if (lane == 0) mbar_arrive(p_full);
+            ++blk;
+        }
+        // ---- the rows' parts ----
+        if (!__all_sync(0xffffffffu, wd.wait(pv_done, (blk - 1) & 1))) return;
+        if (busy) {
+            tc_fence_after();
+            l_a += __shfl_xor_sync(0xffffffffu, l_a, 1);
+            l_b += __shfl_xor_sync(0xffffffffu, l_b, 1);
+            l_a += __shfl_xor_sync(0xffffffffu, l_a, 2);
+            l_b += __shfl_xor_sync(0xffffffffu, l_b, 2);
+            const float inv_a = l_a != 0.f ? 1.f / l_a : 0.f, inv_b = l_b != 0.f ? 1.f / l_b : 0.f;
+            const int part_a = it.part + tok0 * g + ra, part_b = part_a + 8;
+            const bool on_a = ra < rows && ATTN_IN_BOUNDS(part_a < p.max_parts, p.status);
+            const bool on_b = ra + 8 < rows && ATTN_IN_BOUNDS(part_b < p.max_parts, p.status);
+            float* const to_a = p.part_o + static_cast<size_t>(part_a) * D + cpair;
+            float* const to_b = p.part_o + static_cast<size_t>(part_b) * D + cpair;
+#pragma unroll
+            for (int cc = 0; cc < D / 64; ++cc) {
+                uint32_t o[32];
+                tmem_ld16x256_x8(tO + 64 * cc, o);
+                tmem_wait_ld();
+#pragma unroll
+                for (int c = 0; c < 8; ++c) {
+                    if (on_a)
+                        *reinterpret_cast<float2*>(to_a + 64 * cc + 8 * c) =
+                            make_float2(__uint_as_float(o[4 * c]) * inv_a, __uint_as_float(o[4 * c + 1]) * inv_a);
+                    if (on_b)
+                        *reinterpret_cast<float2*>(to_b + 64 * cc + 8 * c) =
+                            make_float2(__uint_as_float(o[4 * c + 2]) * inv_b, __uint_as_float(o[4 * c + 3]) * inv_b);
+                }
+            }
+            if ((lane & 3) == 0) {
+                if (on_a) p.part_lse[part_a] = l_a != 0.f ? m_a + __log2f(l_a) : -INFINITY;
+                if (on_b) p.part_lse[part_b] = l_b != 0.f ? m_b + __log2f(l_b) : -INFINITY;
+            }
+            tc_fence_before();
+        }
+        __syncwarp();
+        if (lane == 0) mbar_arrive(o_free);
+    }
+}
+
+template <int D>
+__global__ void __launch_bounds__(kFwdThreads, 1) shared_attn_kernel(const __grid_constant__ SharedParams p) {
+    using C = ShCfg<D>;
+    extern __shared__ uint8_t smem_raw[];
+    uint8_t* smem = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) &
+                                               ~static_cast<uintptr_t>(1023));
+    ShBars* bars = reinterpret_cast<ShBars*>(smem + C::kOffBar);
+    const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+    griddep_launch_dependents();
+    if (threadIdx.x == 0) {
+        mbar_init(&bars->q_full, 1);
+        mbar_init(&bars->q_empty, 1);
+        for (int i = 0; i < C::kSlots; ++i) {
+            mbar_init(&bars->k_full[i], 1);
+            mbar_init(&bars->v_full[i], 1);
+            mbar_init(&bars->kv_empty[i], 1);
+        }
+        for (int t = 0; t < 2; ++t) {
+            mbar_init(&bars->s_full[t], 1);
+            mbar_init(&bars->s_free[t], kShSoftmaxWarps / 2);
+            mbar_init(&bars->p_full[t], kShSoftmaxWarps / 2);
+            mbar_init(&bars->pv_done[t], 1);
+            mbar_init(&bars->o_free[t], kShSoftmaxWarps / 2);
+            mbar_init(&bars->drain[t], 1);
+        }
+        for (uint32_t i = 0; i < kShRing; ++i) {
+            mbar_init(&bars->idx_full[i], 1);
+            mbar_init(&bars->idx_empty[i], kShReaders);
+        }
+        bars->abort_flag = 0;
+        mbar_fence_init();
+    }
+    if (warp == kShSoftmaxWarps + 1) tmem_alloc(&bars->tmem_base, C::kTmemCols);
+    tc_fence_before();
+    __syncthreads();
+    tc_fence_after();
+    const uint32_t tmem = bars->tmem_base;
+    const Watchdog wd{&bars->abort_flag, p.status};
+    griddep_wait();  // the list, and what this call's predecessors wrote
+    const int n_items = p.header->n_items;
+    // registers as in fwd_kernel.cu: 128 * 64 + 512 * 104 = 640 * 96
+    if (warp >= kShSoftmaxWarps) {
+        regs_decrease<64>();
+        if (warp == kShSoftmaxWarps) {
+            sh_producer<D>(p, smem, bars, wd, n_items, lane);
+        } else if (warp <= kShSoftmaxWarps + 2) {
+            if (lane == 0) {
+                const int w = warp - kShSoftmaxWarps - 1;
+                if (w == 0)
+                    sh_mma_s<D>(p, smem, bars, tmem, wd);
+                else
+                    sh_mma_pv<D>(p, smem, bars, tmem, wd);
+                umma_commit(&bars->drain[w]);
+                sh_drain(&bars->drain[w], 0);
+            }
+        }
+    } else {
+        regs_increase<104>();
+        sh_softmax<D>(p, smem, bars, tmem, wd, warp >> 3, warp & 7, lane);
+    }
+    __syncwarp();
+    tc_fence_before();
+    __syncthreads();
+    if (warp == kShSoftmaxWarps + 1) {
+        tc_fence_after();
+        tmem_dealloc(tmem, C::kTmemCols);
+    }
+}
+
+// ---- merge --------------------------------------------------------------------------------------------
+
+// A block has one sequence's unit and one kv head, a warp one row at a time.  LSE = log2 sum_s 2^LSE_s,
+// O = sum_s 2^(LSE_s - LSE) O_s over the pieces of the row's own keys and of its prefix; no part, or none
+// with a key: O = 0, LSE = -inf.
+template <int D>
+__global__ void __launch_bounds__(kShCombineThreads) shared_combine_kernel(const SharedParams p) {
+    griddep_wait();
+    const int own = blockIdx.x, kvh = blockIdx.y;
+    const SharedHeader* h = p.header;
+    if (h->bad || own >= h->n_own) return;
+    const SharedUnit& u = p.units[h->n_prefix + own];
+    const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+    constexpr int E = D / 32;
+    const int rows = u.rows, q0 = u.q0, n1 = u.pieces, prefix = u.prefix;
+    const int per = 2 * p.tpt;
+    for (int r = warp; r < rows; r += kShCombineThreads / 32) {
+        const int tok = q0 + r / p.g, head = kvh * p.g + r % p.g;
+        const int base1 = u.part + kvh * n1 * rows + r;
+        int n2 = 0, base2 = 0, step2 = 0;
+        if (prefix >= 0) {
+            const int at = (tok - u.group_q0) / per;
+            const SharedUnit& v = p.units[prefix + at];
+            n2 = v.pieces;
+            step2 = v.rows;
+            base2 = v.part + kvh * n2 * step2 + (tok - v.q0) * p.g + r % p.g;
+        }
+        const int n = n1 + n2;
+        const auto row = [&](int s) -> size_t {
+            return static_cast<size_t>(s < n2 ? base2 + s * step2 : base1 + (s - n2) * rows);
+        };
+        float M = -INFINITY;
+        bool nan = false;
+        for (int s = lane; s < n; s += 32) {
+            const float x = p.part_lse[row(s)];
+            nan |= x != x;
+            M = fmaxf(M, x);
+        }
+#pragma unroll
+        for (int o = 16; o > 0; o >>= 1) M = fmaxf(M, __shfl_xor_sync(0xffffffffu, M, o));
+        float acc[E];
+#pragma unroll
+        for (int e = 0; e < E; ++e) acc[e] = 0.f;
+        float lse = -INFINITY;
+        if (__any_sync(0xffffffffu, nan)) {
+            lse = __int_as_float(0x7fffffff);
+#pragma unroll
+            for (int e = 0; e < E; ++e) acc[e] = lse;
+        } else if (M != -INFINITY) {
+            float sum = 0.f;
+            for (int s = lane; s < n; s += 32) sum += ex2_approx(p.part_lse[row(s)] - M);
+#pragma unroll
+            for (int o = 16; o > 0; o >>= 1) sum += __shfl_xor_sync(0xffffffffu, sum, o);
+            lse = M + __log2f(sum);
+            const float inv = 1.f / sum;
+            for (int s0 = 0; s0 < n; s0 += 4) {
+                float w[4], v[4][E];
+#pragma unroll
+                for (int i = 0; i < 4; ++i) {
+                    const size_t at = row(min(s0 + i, n - 1));
+                    w[i] = s0 + i < n ? ex2_approx(p.part_lse[at] - M) * inv : 0.f;
+                    const float* src = p.part_o + at * D + lane * E;
+                    if constexpr (E == 4) {
+                        const float4 x = *reinterpret_cast<const float4*>(src);
+                        v[i][0] = x.x, v[i][1] = x.y, v[i][2] = x.z, v[i][3] = x.w;
+                    } else {
+                        const float2 x = *reinterpret_cast<const float2*>(src);
+                        v[i][0] = x.x, v[i][1] = x.y;
+                    }
+                }
+#pragma unroll
+                for (int i = 0; i < 4; ++i)
+#pragma unroll
+                    for (int e = 0; e < E; ++e)
+                        if (s0 + i < n) acc[e] = fmaf(w[i], v[i][e], acc[e]);
+            }
+        }
+        if (!ATTN_IN_BOUNDS(tok < p.total_q && head < p.Hq, p.status)) continue;
+        __nv_bfloat16* dst = p.out + (static_cast<size_t>(tok) * p.Hq + head) * D + lane * E;
+        if constexpr (E == 4)
+            *reinterpret_cast<uint2*>(dst) = make_uint2(pack_bf16x2(acc[0], acc[1]), pack_bf16x2(acc[2], acc[3]));
+        else
+            *reinterpret_cast<uint32_t*>(dst) = pack_bf16x2(acc[0], acc[1]);
+        if (lane == 0)
+            p.lse[static_cast<size_t>(head) * p.lse_head + static_cast<size_t>(tok) * p.lse_tok] = lse * kShLn2;
+    }
+}
+
+template <typename Kernel>
+cudaError_t launch_dependent(Kernel kernel, dim3 grid, int threads, size_t smem, const SharedParams& p,
+                             cudaStream_t stream) {
+    cudaLaunchConfig_t cfg = {};
+    cfg.gridDim = grid;
+    cfg.blockDim = dim3(threads);
+    cfg.dynamicSmemBytes = smem;
+    cfg.stream = stream;
+    cudaLaunchAttribute attr[1];
+    attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+    attr[0].val.programmaticStreamSerializationAllowed = 1;
+    cfg.attrs = attr;
+    cfg.numAttrs = 1;
+    return cudaLaunchKernelEx(&cfg, kernel, p);
+}
+
+}  // namespace
+
+cudaError_t configure_shared_kernels() {
+    const cudaFuncAttribute smem = cudaFuncAttributeMaxDynamicSharedMemorySize;
+    const cudaError_t e = cudaFuncSetAttribute(shared_attn_kernel<128>, smem, ShCfg<128>::kSmem);
+    return e != cudaSuccess ? e : cudaFuncSetAttribute(shared_attn_kernel<64>, smem, ShCfg<64>::kSmem);
+}
+
+cudaError_t launch_shared_attn(const SharedParams& p, int head_dim, int grid, int own_units, cudaStream_t stream) {
+    shared_units_kernel<<<1, kShUnitsThreads, 0, stream>>>(p);
+    cudaError_t e = cudaGetLastError();
+    if (e != cudaSuccess) return e;
+    const bool wide = head_dim == 128;
+    e = launch_dependent(wide ? shared_attn_kernel<128> : shared_attn_kernel<64>, dim3(grid), kFwdThreads,
+                         wide ? ShCfg<128>::kSmem : ShCfg<64>::kSmem, p, stream);
+    if (e != cudaSuccess) return e;
+    return launch_dependent(wide ? shared_combine_kernel<128> : shared_combine_kernel<64>,
+                            dim3(own_units, p.Hkv), kShCombineThreads, 0, p, stream);
+}
+
+}  // namespace attn

@@ -421,6 +421,173 @@ size_t attn_fwd_kvcache_fp8_workspace_bytes(int batch, int total_q, int max_seql
                                             int head_dim, int page_size, int max_pages_per_seq,
                                             int rotary_dim);
 
+/*
+ * The calls around attention in a step over the bf16 paged cache of attn_decode_kvcache: places for the
+ * new tokens (attn_kvcache_plan), their queries, keys and values brought into it
+ * (attn_kvcache_append_norm_rope), and attention where sequences share prefixes
+ * (attn_decode_kvcache_shared).  attn_qk_norm_rope and its backward pass are the same preparation for
+ * training, before attn_fwd and behind attn_bwd.  Every buffer is the caller's; nothing is allocated;
+ * two calls that share a workspace must not overlap on the device; outputs must not overlap inputs but
+ * where a call says so.
+ */
+
+/*
+ * attn_kvcache_plan -- pages, slots and offsets of a step from the lengths of its requests
+ * ("Attention kernels: FlashAttention and PagedAttention", section 五.1: block tables and slots).
+ *
+ *   cache_seqlens  device int32 [batch], tokens that a sequence holds; the first
+ *                  ceil(cache_seqlens[b] / page_size) entries of its row of block_table are its pages
+ *   new_lens       device int32 [batch], tokens that it gets in this step (0 and more)
+ *   block_table    device int32 [batch, max_pages_per_seq], updated in place: the entries behind a
+ *                  sequence's pages, up to ceil((cache_seqlens[b] + new_lens[b]) / page_size), are written,
+ *                  the others left as they were
+ *   free_pages     device int32 [num_free_pages], free_count device int32 [1]: the first free_count[0] ids
+ *                  are free.  They are taken from the end: the k-th new page of the step (the sequences'
+ *                  in order) is free_pages[free_count[0] - 1 - k].  To give pages back, write them
+ *                  behind the ids that are left and raise the count.
+ *   free_left      device int32 [1]: the ids that remain (may be free_count itself)
+ *   cu_seqlens_q   device int32 [batch + 1]: the new tokens' offsets
+ *   seqlens_after  device int32 [batch]: cache_seqlens + new_lens (may be cache_seqlens itself)
+ *   positions, slot_map   device int32 [total_q]: token i of sequence b stands at position
+ *                  p = cache_seqlens[b] + i, in slot page * page_size + p % page_size of the cache; behind
+ *                  the last token up to total_q (a padded batch) the position is 0 and the slot -1
+ *   total_q        at least the sum of new_lens; page_size any positive number; batch up to 65535
+ *   workspace      attn_kvcache_plan_workspace_bytes(batch) bytes, 256-byte aligned
+ * A request that does not fit (a negative length, more tokens than total_q, a sequence past the table, too
+ * few free pages) raises ATTN_ERR_DEVICE_BOUNDS and the step is empty: no page is taken, every slot is
+ * -1, cu_seqlens_q all 0, seqlens_after and free_left as before.  A page id outside [0, num_pages) raises it
+ * too, and its tokens get slot -1.
+ */
+attn_status_t attn_kvcache_plan(const int32_t* cache_seqlens, const int32_t* new_lens,
+                                int32_t* block_table, const int32_t* free_pages,
+                                const int32_t* free_count, int32_t* free_left,
+                                int32_t* cu_seqlens_q, int32_t* seqlens_after, int32_t* positions,
+                                int32_t* slot_map, int batch, int total_q, int page_size,
+                                int max_pages_per_seq, int num_free_pages, int num_pages,
+                                void* workspace, size_t workspace_bytes, void* stream);
+
+/* Workspace bytes of attn_kvcache_plan (0 on sizes the call would refuse). */
+size_t attn_kvcache_plan_workspace_bytes(int batch);
+
+/*
+ * attn_qk_norm_rope -- RMS norm of every query and key row (one token, one head) and the rotary embedding
+ * in one pass:  y = R (x rstd w),  rstd = (sum x^2 / head_dim + eps)^(-1/2), in fp32, rounded once.
+ *   q, k          device bf16 [total, nheads_q, head_dim], [total, nheads_kv, head_dim]; q_stride, k_stride
+ *                 elements between tokens (multiples of 8, at least nheads * head_dim: parts of the rows
+ *                 of one projection will do); 16-byte aligned
+ *   q_weight, k_weight   device [head_dim] w, fp32 with weight_fp32, else bf16; NULL: no norm (x rstd w is x)
+ *   eps           finite and >= 2^-64 (not looked at without weights)
+ *   rotary_cos, rotary_sin   device fp32 [rotary_rows, rotary_dim / 2], 16-byte aligned; planes as for
+ *                 attn_fwd_kvcache; rotary_dim a multiple of 16 up to head_dim, 0: no rotation (the
+ *                 arguments from here to sections_interleaved are not looked at)
+ *   positions     device int32 [axes, total], axes 1 to 3: token t turns plane i by the angle of row
+ *                 positions[axis(i)][t].  With one axis, axis(i) is 0 (sections may be NULL).  With more
+ *                 (time, height, width), sections (host, [axes], sum rotary_dim / 2) says how many
+ *                 planes an axis has: the first sections[0] are axis 0's, and so on; with
+ *                 sections_interleaved the axes take planes in turn, axis(i) = i % axes, and planes of an
+ *                 axis whose section is full go to axis 0 (sections that do not come out so are refused)
+ *   q_out, k_out  device bf16, dense; q_out may be q and k_out may be k where those are dense
+ *   head_dim 64 or 128
+ * A token with a position outside [0, rotary_rows) raises ATTN_ERR_DEVICE_BOUNDS, and its outputs are left
+ * as they were.
+ */
+attn_status_t attn_qk_norm_rope(const void* q, const void* k, int64_t q_stride, int64_t k_stride,
+                                const void* q_weight, const void* k_weight, int weight_fp32,
+                                float eps, const float* rotary_cos, const float* rotary_sin,
+                                int rotary_dim, int rotary_rows, int rotary_interleaved,
+                                const int32_t* positions, int axes, const int32_t* sections,
+                                int sections_interleaved, void* q_out, void* k_out, int total,
+                                int nheads_q, int nheads_kv, int head_dim, void* stream);
+
+/*
+ * attn_qk_norm_rope_bwd -- its backward pass.  dq_out, dk_out (dense, bf16) are the gradients of its
+ * outputs; q, k its inputs and the other arguments as they were there:
+ *   dz = R^T dy,  dw = sum over tokens and heads of x rstd dz,  h = w dz, n = x rstd,
+ *   dx = rstd (h - n sum(n h) / head_dim)     (no weight: dx = dz, and q or k is not read)
+ *   dq, dk        device bf16, dq_stride and dk_stride elements between tokens (as q_stride); dq may be
+ *                 dq_out or q, dk may be dk_out or k, where the strides are the same
+ *   dq_weight, dk_weight   device fp32 [head_dim], where there is a weight, else NULL
+ *   workspace     attn_qk_norm_rope_bwd_workspace_bytes(head_dim) bytes, 256-byte aligned (NULL without
+ *                 weights)
+ * No atomics: the sums' order is fixed by the sizes.  Tokens with a position outside the tables give no
+ * gradient (ATTN_ERR_DEVICE_BOUNDS); their rows of dq and dk are left as they were.
+ */
+attn_status_t attn_qk_norm_rope_bwd(const void* dq_out, const void* dk_out, const void* q,
+                                    const void* k, int64_t q_stride, int64_t k_stride,
+                                    const void* q_weight, const void* k_weight, int weight_fp32,
+                                    float eps, const float* rotary_cos, const float* rotary_sin,
+                                    int rotary_dim, int rotary_rows, int rotary_interleaved,
+                                    const int32_t* positions, int axes, const int32_t* sections,
+                                    int sections_interleaved, void* dq, void* dk, int64_t dq_stride,
+                                    int64_t dk_stride, float* dq_weight, float* dk_weight, int total,
+                                    int nheads_q, int nheads_kv, int head_dim, void* workspace,
+                                    size_t workspace_bytes, void* stream);
+
+size_t attn_qk_norm_rope_bwd_workspace_bytes(int head_dim);
+
+/*
+ * attn_kvcache_append_norm_rope -- attn_qk_norm_rope for serving: queries go to q_out, keys and the values
+ * (as they are) to the slots of their tokens in the bf16 paged cache.
+ *   v             device bf16 [total, nheads_kv, head_dim], v_stride elements between tokens
+ *   k_cache, v_cache   device bf16 [num_pages, page_size, nheads_kv, head_dim], updated in place
+ *   slot_map      device int32 [total] (attn_kvcache_plan): the cache's row page * page_size + slot in page;
+ *                 a negative one writes nothing (its query is computed all the same), one past the
+ *                 cache neither, and raises ATTN_ERR_DEVICE_BOUNDS.  No two tokens have the same slot.
+ *   page_size     any positive number
+ */
+attn_status_t attn_kvcache_append_norm_rope(
+    const void* q, const void* k, const void* v, int64_t q_stride, int64_t k_stride, int64_t v_stride,
+    const void* q_weight, const void* k_weight, int weight_fp32, float eps, const float* rotary_cos,
+    const float* rotary_sin, int rotary_dim, int rotary_rows, int rotary_interleaved,
+    const int32_t* positions, int axes, const int32_t* sections, int sections_interleaved, void* q_out,
+    void* k_cache, void* v_cache, const int32_t* slot_map, int total, int nheads_q, int nheads_kv,
+    int head_dim, int page_size, int num_pages, void* stream);
+
+/*
+ * attn_decode_kvcache_shared -- attn_decode_kvcache, or attention of a few new tokens a sequence, where
+ * sequences share prefixes ("Attention kernels ...", sections 五.1-五.3 and 六.3): a prefix's keys and
+ * values are read once for all sequences of its group, those behind it by each sequence, and the two
+ * softmaxes merged by their LSE.
+ *
+ *   q             device bf16 [total_q, nheads_q, head_dim]
+ *   cu_seqlens_q  device int32 [batch + 1]: sequence b owns the tokens
+ *                 [cu_seqlens_q[b], cu_seqlens_q[b+1]) (none to max_seqlen_q); NULL: one token a sequence
+ *                 (total_q == batch)
+ *   cache_seqlens device int32 [batch]: the sequence's keys, its new tokens' among them (they are in the cache
+ *                 already); query i of n sees keys 0 .. cache_seqlens[b] - n + i
+ *   group_starts  device int32 [num_groups + 1], from 0 to batch: sequences
+ *                 [group_starts[i], group_starts[i+1]) form group i (none, one or more)
+ *   prefix_lens   device int32 [num_groups]: the group's sequences begin with the same so many keys.
+ *                 (num_groups 0, both NULL: no sequence shares.)
+ *   block_table, k_cache, v_cache, page_size   as for attn_fwd_kvcache
+ *   out           device bf16 [total_q, nheads_q, head_dim]
+ *   lse           device fp32, natural log: [batch, nheads_q] without cu_seqlens_q, else
+ *                 [nheads_q, total_q]; rows outside every sequence are left as they were
+ *   workspace     attn_decode_kvcache_shared_workspace_bytes(...) bytes, 256-byte aligned: the list of the
+ *                 work and the partial results, about 8 total_q nheads_q head_dim bytes and 20 MB
+ * The prefix is read through one row of block_table, that of a sequence of the group that has it whole; the
+ * entries of the others' pages that end before the prefix does are not looked at.  (A page in which it ends may
+ * be each sequence's own; what stands before the end is taken from that one row.)  A sequence some of
+ * whose queries do not see the whole prefix (a short one, an empty place in a padded batch) is computed alone,
+ * through its own row, as if it shared nothing; so are all of a group where fewer than two remain, or the
+ * prefix has fewer than 128 keys.  Lengths that do not fit raise ATTN_ERR_DEVICE_BOUNDS, and
+ * the call's results are unspecified; a page id outside [0, num_pages) raises it, and the results of the
+ * sequences that read it are unspecified.  A NaN among the keys or values reaches the rows that see it, and may
+ * reach other new tokens of its sequence.
+ */
+attn_status_t attn_decode_kvcache_shared(const void* q, const void* k_cache, const void* v_cache,
+                                         const int32_t* cache_seqlens, const int32_t* block_table,
+                                         const int32_t* group_starts, const int32_t* prefix_lens,
+                                         const int32_t* cu_seqlens_q, int page_size, void* out,
+                                         float* lse, int batch, int num_groups, int total_q,
+                                         int max_seqlen_q, int nheads_q, int nheads_kv, int head_dim,
+                                         int max_pages_per_seq, int num_pages, float softmax_scale,
+                                         void* workspace, size_t workspace_bytes, void* stream);
+
+/* Workspace bytes of attn_decode_kvcache_shared (0 on sizes the call would refuse). */
+size_t attn_decode_kvcache_shared_workspace_bytes(int batch, int num_groups, int total_q, int nheads_q,
+                                                  int nheads_kv, int head_dim);
+
 /* Bytes of split-partial workspace for attn_decode_kvcache; num_splits 0 sizes for the
  * automatic choice (at most 16 splits).  0 when one split needs no workspace. */
 size_t attn_decode_workspace_bytes(int batch, int nheads_q, int head_dim, int num_splits);
