@@ -1657,11 +1657,13 @@ namespace {
 
 struct SharedLayout {
     long long max_units, own_units, max_items, max_parts;
-    size_t groups, units, items, part_lse, part_o, bytes;
+    size_t groups, lengths, units, items, part_lse, part_o, bytes;
 };
 
 // The list's bounds.  Units: every sequence and every group may end in one that is not full.  Pieces: a unit
-// takes one for each kv head and all of them together kSharedShares more.  False: sizes that the call refuses.
+// takes one for each kv head and all units of a kind together that kind's shares more.  Parts: each row of q is
+// in one unit of its sequence and one of its group, where a unit has few rows in kSharedSmallSplit parts a
+// piece.  False: sizes that the call refuses.
 bool shared_layout(int batch, int n_groups, int total_q, int nheads_q, int nheads_kv, int head_dim,
                    SharedLayout* l) {
     if (batch < 0 || n_groups < 0 || total_q < 0 || nheads_q <= 0 || nheads_kv <= 0 ||
@@ -1673,8 +1675,11 @@ bool shared_layout(int batch, int n_groups, int total_q, int nheads_q, int nhead
     const long long rows = static_cast<long long>(total_q) * nheads_q;
     l->own_units = batch + full;
     l->max_units = l->own_units + n_groups + full;
-    l->max_items = l->max_units * nheads_kv + kSharedShares;
-    l->max_parts = 2 * rows + kSharedShares * std::min(per * g, static_cast<long long>(total_q) * g);
+    l->max_items = l->max_units * nheads_kv + kSharedShares + kSharedSmallShares;
+    const long long few = std::min(rows, static_cast<long long>(n_groups) * kSharedSmallRows * nheads_kv);
+    l->max_parts = rows * kSharedSmallSplit + rows + few * kSharedSmallSplit +
+                   kSharedShares * std::min(per * g, static_cast<long long>(total_q) * g) +
+                   kSharedSmallShares * kSharedSmallRows * kSharedSmallSplit;
     if (l->max_items > (1LL << 31) - 1 || l->max_parts > (1LL << 31) - 1) return false;
     size_t at = sizeof(SharedHeader);
     const auto take = [&at](size_t bytes) {
@@ -1683,6 +1688,7 @@ bool shared_layout(int batch, int n_groups, int total_q, int nheads_q, int nhead
         return here;
     };
     l->groups = take(sizeof(int4) * n_groups);
+    l->lengths = take(sizeof(int2) * l->max_units);
     l->units = take(sizeof(SharedUnit) * l->max_units);
     l->items = take(sizeof(int2) * l->max_items);
     l->part_lse = take(sizeof(float) * l->max_parts);
@@ -1747,12 +1753,16 @@ attn_status_t attn_decode_kvcache_shared(const void* q, const void* k_cache, con
     if (encode_3d(&p.tm_q, q, head_dim, nheads_q, total_q, p.g, p.tpt) != ATTN_OK ||
         encode_3d(&p.tm_q1, q, head_dim, nheads_q, total_q, p.g, 1) != ATTN_OK ||
         encode_3d(&p.tm_k, k_cache, head_dim, nheads_kv, cache_rows, 1, p.box_rows) != ATTN_OK ||
-        encode_3d(&p.tm_v, v_cache, head_dim, nheads_kv, cache_rows, 1, p.box_rows) != ATTN_OK)
+        encode_3d(&p.tm_v, v_cache, head_dim, nheads_kv, cache_rows, 1, p.box_rows) != ATTN_OK ||
+        encode_3d(&p.tm_k64, k_cache, head_dim, nheads_kv, cache_rows, 1, std::min(p.box_rows, 64)) != ATTN_OK ||
+        encode_3d(&p.tm_v64, v_cache, head_dim, nheads_kv, cache_rows, 1, std::min(p.box_rows, 64)) != ATTN_OK)
         return ATTN_ERR_CUDA;
+    p.q = static_cast<const __nv_bfloat16*>(q);
     p.out = static_cast<__nv_bfloat16*>(out);
     p.lse = lse;
     p.header = reinterpret_cast<SharedHeader*>(ws);
     p.groups = reinterpret_cast<int4*>(ws + l.groups);
+    p.lengths = reinterpret_cast<int2*>(ws + l.lengths);
     p.units = reinterpret_cast<SharedUnit*>(ws + l.units);
     p.items = reinterpret_cast<int2*>(ws + l.items);
     p.part_lse = reinterpret_cast<float*>(ws + l.part_lse);
@@ -1775,6 +1785,7 @@ attn_status_t attn_decode_kvcache_shared(const void* q, const void* k_cache, con
     p.max_units = static_cast<int>(l.max_units);
     p.max_items = static_cast<int>(l.max_items);
     p.max_parts = static_cast<int>(l.max_parts);
+    p.own_base = static_cast<int>(l.max_units - l.own_units);
     p.lse_head = cu_seqlens_q ? total_q : 1;
     p.lse_tok = cu_seqlens_q ? 1 : nheads_q;
     p.scale_log2 = softmax_scale * kLog2eF;

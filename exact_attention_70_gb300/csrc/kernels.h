@@ -354,31 +354,28 @@ cudaError_t launch_norm_rope_bwd(NormRopeParams p, int head_dim, cudaStream_t st
 
 // ---- decode behind shared prefixes -------------------------------------------------------------
 
-constexpr int kShUnitsThreads = 1024;
-
-// Workspace of attn_decode_kvcache_shared: [header][groups][units][items][LSE of the parts][O of the parts]
+// Workspace of attn_decode_kvcache_shared: [header][groups][lengths][units][items][LSE of the parts][O of the parts]
 struct SharedHeader {
-    int n_items;
-    int next_item;  // the claim counter of the attention kernel
-    int n_prefix;   // units of prefixes,
-    int n_own;      // and behind them those of the sequences' own keys
-    int bad;        // lengths that do not fit: nothing is computed
-    int pad[59];
+    int n_items[2];    // of units with many rows, and behind them in the list those of units with few
+    int next_item[2];  // the claim counters of the two kernels
+    int n_own;         // units of the sequences' own keys
+    int bad;           // lengths that do not fit: nothing is computed
+    int pad[58];
 };
 
 // Query rows that walk the same keys: up to two tiles of tokens, of one sequence against its own keys or of
-// a group against its prefix.  Its key blocks are cut into `pieces`; piece s of kv head h leaves the rows'
-// parts at part + (h pieces + s) rows.
+// a group against its prefix.  Its key blocks are cut into `pieces`, a piece's rows leave `split` parts
+// (few rows: one a warp); part s of kv head h lies at part + (h pieces split + s) rows.
 struct SharedUnit {
     int q0, ntok;          // tokens [q0, q0 + ntok) of q
     int row;               // of block_table
     int key_min, key_end;  // keys [key_min, key_end)
     int pos0;              // the key position of token q0 (prefix: beyond every key)
     int blk0, nblk;        // key blocks
-    int pieces, part, rows;
-    int prefix;  // of a sequence's unit: the first unit of its group's prefix, or -1
+    int pieces, split, part, rows;
+    int prefix;    // of a sequence's unit: the first unit of its group's prefix, or -1
     int group_q0;  // and that prefix's first token
-    int pad[3];
+    int pad[2];
 };
 
 struct SharedParams {
@@ -386,14 +383,18 @@ struct SharedParams {
     CUtensorMap tm_q1;  // the same with box {64, g, 1}
     CUtensorMap tm_k;   // 3-D over the cache [num_pages * page_size, Hkv, d], box {64, 1, box_rows}
     CUtensorMap tm_v;
+    CUtensorMap tm_k64;  // the same with box {64, 1, min(box_rows, 64)}
+    CUtensorMap tm_v64;
+    const __nv_bfloat16* q;
     __nv_bfloat16* out;
     float* lse;
     float* part_lse;  // log2
     float* part_o;    // [parts, d]
     SharedHeader* header;
-    int4* groups;  // [groups]: the row of block_table that leads to the prefix (-1: none), tokens, first unit
-    SharedUnit* units;
-    int2* items;  // {unit, piece * Hkv + kv head}
+    int4* groups;    // [groups] (where shared memory does not hold them)
+    int2* lengths;   // [units]: key blocks and rows (likewise)
+    SharedUnit* units;  // those of prefixes, and from own_base on the sequences' own
+    int2* items;        // {unit, piece << 16 | kv head}
     const int* cu_q;  // null: one query a sequence
     const int* seqlens;
     const int* block_table;
@@ -402,14 +403,17 @@ struct SharedParams {
     unsigned* status;
     int batch, n_groups, total_q, max_seqlen_q, Hq, Hkv, g, tpt;
     int page_size, box_rows, max_pages, num_pages;
-    int max_units, max_items, max_parts;
+    int max_units, max_items, max_parts, own_base;
     int lse_head, lse_tok;  // strides of lse
     float scale_log2;
 };
 
-constexpr int kSharedShares = kGb300Sms;  // pieces that the work is cut into, about
+// Pieces that the work of units with many and with few rows is cut into, about: one and two CTAs an SM.
+constexpr int kSharedShares = kGb300Sms, kSharedSmallShares = 2 * kGb300Sms;
+constexpr int kSharedSmallRows = 16;  // the rows of a unit that count as few
+constexpr int kSharedSmallSplit = 4;  // parts that their pieces leave
 
-cudaError_t launch_shared_attn(const SharedParams& p, int head_dim, int grid, int own_units, cudaStream_t stream);
+cudaError_t launch_shared_attn(const SharedParams& p, int head_dim, int num_sms, int own_units, cudaStream_t stream);
 cudaError_t configure_shared_kernels();
 
 // ---- failure-path self-test ------------------------------------------------------------

@@ -29,7 +29,9 @@ namespace {
 
 constexpr float kShRescale = 8.0f;  // log2: the reference of a row moves when its maximum passes it by more
 constexpr float kShLn2 = 0.69314718055994530942f;
-constexpr int kShBins = 1024;
+constexpr int kShUnitsThreads = 512;
+constexpr int kShFast = 1024;  // groups, and half the units, that the list's kernel keeps in shared memory
+constexpr int kShBins = 32;    // lengths that the list tells apart
 constexpr int kShMinPrefix = 128;  // shorter prefixes are read by every sequence
 constexpr int kShMinPiece = 2;     // key blocks a piece takes at least
 constexpr int kShCombineThreads = 256;
@@ -58,44 +60,41 @@ __device__ __forceinline__ bool sh_behind(const ShSeq& s, int prefix) {
     return s.n > 0 && prefix > 0 && prefix <= s.keys - s.n + 1;
 }
 
-__device__ int sh_scan(int v, int* warp_tot, int& total) {
-    const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
-    int x = v;
+__device__ __forceinline__ int ceil_div(int a, int b) { return (a + b - 1) / b; }
+
+// This thread's place behind the earlier lanes' n on a counter in shared memory (one atomic a warp).
+__device__ __forceinline__ int sh_reserve(int* counter, int n, int lane) {
+    int x = n;
 #pragma unroll
     for (int o = 1; o < 32; o <<= 1) {
         const int y = __shfl_up_sync(0xffffffffu, x, o);
         if (lane >= o) x += y;
     }
-    if (lane == 31) warp_tot[warp] = x;
-    __syncthreads();
-    if (warp == 0) {
-        int w = warp_tot[lane];
-#pragma unroll
-        for (int o = 1; o < 32; o <<= 1) {
-            const int y = __shfl_up_sync(0xffffffffu, w, o);
-            if (lane >= o) w += y;
-        }
-        warp_tot[lane] = w;
-    }
-    __syncthreads();
-    const int before = (warp > 0 ? warp_tot[warp - 1] : 0) + x - v;
-    total = warp_tot[31];
-    __syncthreads();
-    return before;
+    int at = 0;
+    if (lane == 31 && x > 0) at = atomicAdd(counter, x);
+    return __shfl_sync(0xffffffffu, at, 31) + x - n;
 }
 
-__device__ __forceinline__ int ceil_div(int a, int b) { return (a + b - 1) / b; }
+__device__ __forceinline__ bool sh_few(int rows) { return rows <= kSharedSmallRows; }
 
-// Units first those of the prefixes, then those of the sequences in order; items longest pieces first, the kv
-// heads of a piece side by side (their keys lie side by side in the cache).
+// Writes the list.  Where the parts lie and the order among units of a length depend on the warps' order;
+// no result does.  Items of a kind come longest pieces first (kShBins lengths), the kv heads of a piece
+// side by side (their keys lie side by side in the cache).
 __global__ void __launch_bounds__(kShUnitsThreads) shared_units_kernel(const SharedParams p) {
-    __shared__ int hist[kShBins];
-    __shared__ int warp_tot[32];
-    __shared__ unsigned long long work;
+    __shared__ int4 s_groups[kShFast];
+    __shared__ int2 s_lengths[2 * kShFast];
+    __shared__ int hist[2 * kShBins];
+    __shared__ unsigned long long work[2];  // key blocks of both kinds, for one kv head
+    __shared__ int n_prefix, n_own, n_parts;
     const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
-    griddep_launch_dependents();
+    griddep_launch_dependents();  // (the attention kernels wait for the list, behind their set-up)
+    // (generic addresses: shared memory as far as it goes)
+    int4* const groups = p.n_groups <= kShFast ? s_groups : p.groups;      // {first sequence, sequences, -, -}
+    int2* const lengths = p.max_units <= 2 * kShFast ? s_lengths : p.lengths;
     const long long max_keys = static_cast<long long>(p.max_pages) * p.page_size;
-    if (tid == 0) work = 0;
+    if (tid < 2 * kShBins) hist[tid] = 0;
+    if (tid < 2) work[tid] = 0;
+    if (tid == 0) n_prefix = n_own = n_parts = 0;
     bool bad = false;
     for (int b = tid; b < p.batch; b += kShUnitsThreads) {
         const ShSeq s = sh_seq(p, b);
@@ -110,70 +109,62 @@ __global__ void __launch_bounds__(kShUnitsThreads) shared_units_kernel(const Sha
     if (__syncthreads_or(bad)) {
         if (tid == 0) {
             atomicOr(p.status, kStatusBounds);
-            p.header->n_items = p.header->next_item = p.header->n_own = p.header->n_prefix = 0;
-            p.header->bad = 1;
+            SharedHeader* h = p.header;
+            h->n_items[0] = h->n_items[1] = h->next_item[0] = h->next_item[1] = h->n_own = 0;
+            h->bad = 1;
         }
         return;
     }
     const int per = 2 * p.tpt;  // tokens a unit
-    // 1. groups: which row of the table leads to the prefix, and which tokens meet it
+    // 1. a warp a group: which row of the table leads to the prefix, which tokens meet it, their units
     for (int i = warp; i < p.n_groups; i += kShUnitsThreads / 32) {
         const int s0 = p.group_starts[i], s1 = p.group_starts[i + 1], P = p.prefix_lens[i];
         int first = -1, count = 0;
-        for (int b = s0; b < s1; b += 32) {
-            const bool on = b + lane < s1 && sh_behind(sh_seq(p, b + lane), P);
-            const unsigned m = __ballot_sync(0xffffffffu, on);
-            if (first < 0 && m != 0) first = b + __ffs(m) - 1;
-            count += __popc(m);
-        }
-        if (lane == 0) {
-            int4 r = make_int4(-1, 0, 0, 0);
-            if (count > 1 && P >= kShMinPrefix) {
-                const ShSeq a = sh_seq(p, s0), z = sh_seq(p, s1 - 1);
-                r = make_int4(first, a.q0, z.q0 + z.n - a.q0, 0);
+        if (P >= kShMinPrefix) {
+            for (int b = s0; b < s1; b += 32) {
+                const bool on = b + lane < s1 && sh_behind(sh_seq(p, b + lane), P);
+                const unsigned m = __ballot_sync(0xffffffffu, on);
+                if (first < 0 && m != 0) first = b + __ffs(m) - 1;
+                count += __popc(m);
             }
-            p.groups[i] = r;
         }
+        int at = -1, q0 = 0;
+        if (count > 1) {
+            const ShSeq a = sh_seq(p, s0), z = sh_seq(p, s1 - 1);
+            q0 = a.q0;
+            const int tokens = z.q0 + z.n - q0, n = ceil_div(tokens, per), nblk = ceil_div(P, kFwdBlockN);
+            if (lane == 0) at = atomicAdd(&n_prefix, n);
+            at = __shfl_sync(0xffffffffu, at, 0);
+            for (int u = lane; u < n; u += 32) {
+                SharedUnit x;
+                x.q0 = q0 + u * per;
+                x.ntok = min(per, tokens - u * per);
+                x.row = first;
+                x.key_min = 0;
+                x.key_end = P;
+                x.pos0 = 1 << 30;
+                x.blk0 = 0;
+                x.nblk = nblk;
+                x.rows = x.ntok * p.g;
+                x.prefix = -1;
+                x.group_q0 = 0;
+                atomicAdd(&work[sh_few(x.rows)], static_cast<unsigned long long>(nblk));
+                if (at + u < p.own_base) {
+                    p.units[at + u] = x;
+                    lengths[at + u] = make_int2(nblk, x.rows);
+                }
+            }
+        }
+        if (lane == 0) groups[i] = make_int4(at, q0, 0, 0);
     }
     __syncthreads();
-    // 2. units
-    long long blocks = 0;  // this thread's part of the work, for one kv head
-    int n_prefix = 0;
-    for (int base = 0; base < p.n_groups; base += kShUnitsThreads) {
-        const int i = base + tid;
-        int4 r = make_int4(-1, 0, 0, 0);
-        if (i < p.n_groups) r = p.groups[i];
-        const int n = r.x >= 0 ? ceil_div(r.z, per) : 0;
-        int total;
-        const int at = n_prefix + sh_scan(n, warp_tot, total);
-        if (i < p.n_groups) p.groups[i].w = at;
-        for (int u = 0; u < n; ++u) {
-            SharedUnit x;
-            x.q0 = r.y + u * per;
-            x.ntok = min(per, r.z - u * per);
-            x.row = r.x;
-            x.key_min = 0;
-            x.key_end = p.prefix_lens[i];
-            x.pos0 = 1 << 30;
-            x.blk0 = 0;
-            x.nblk = ceil_div(x.key_end, kFwdBlockN);
-            x.rows = x.ntok * p.g;
-            x.prefix = -1;
-            x.group_q0 = 0;
-            blocks += x.nblk;
-            if (at + u < p.max_units) p.units[at + u] = x;
-        }
-        n_prefix += total;
-    }
-    int n_own = 0;
-    __syncthreads();
+    // 2. a thread a sequence: the keys that its group's prefix leaves to it
+    unsigned long long mine[2] = {0, 0};
     for (int base = 0; base < p.batch; base += kShUnitsThreads) {
         const int b = base + tid;
         ShSeq s = {0, 0, 0};
         if (b < p.batch) s = sh_seq(p, b);
         const int n = ceil_div(s.n, per);
-        int total;
-        const int at = n_prefix + n_own + sh_scan(n, warp_tot, total);
         int prefix = -1, group_q0 = 0, key_min = 0;
         if (n > 0 && p.n_groups > 0) {
             int lo = 0, hi = p.n_groups - 1;  // the last group that starts at b or before
@@ -181,13 +172,14 @@ __global__ void __launch_bounds__(kShUnitsThreads) shared_units_kernel(const Sha
                 const int mid = (lo + hi + 1) >> 1;
                 if (p.group_starts[mid] <= b) lo = mid; else hi = mid - 1;
             }
-            const int4 r = p.groups[lo];
+            const int4 r = groups[lo];
             if (r.x >= 0 && sh_behind(s, p.prefix_lens[lo])) {
-                prefix = r.w;
+                prefix = r.x;
                 group_q0 = r.y;
                 key_min = p.prefix_lens[lo];
             }
         }
+        const int at = p.own_base + sh_reserve(&n_own, n, lane);
         for (int u = 0; u < n; ++u) {
             SharedUnit x;
             const int t0 = u * per;
@@ -202,71 +194,103 @@ __global__ void __launch_bounds__(kShUnitsThreads) shared_units_kernel(const Sha
             x.rows = x.ntok * p.g;
             x.prefix = prefix;
             x.group_q0 = group_q0;
-            blocks += x.nblk;
-            if (at + u < p.max_units) p.units[at + u] = x;
-        }
-        n_own += total;
-    }
-    for (int i = tid; i < kShBins; i += kShUnitsThreads) hist[i] = 0;
-    atomicAdd(&work, static_cast<unsigned long long>(blocks));
-    __syncthreads();
-    const int n_units = min(n_prefix + n_own, p.max_units);
-    const long long share_ll = (static_cast<long long>(work) * p.Hkv + kSharedShares - 1) / kSharedShares;
-    const int share = static_cast<int>(max(share_ll, static_cast<long long>(kShMinPiece)));
-    // 3. pieces, the places of their results, and how many are how long
-    int parts = 0, items = 0;
-    for (int base = 0; base < n_units; base += kShUnitsThreads) {
-        const int u = base + tid;
-        int pieces = 0, rows = 0, len = 0;
-        if (u < n_units) {
-            const int nblk = p.units[u].nblk;
-            pieces = ceil_div(nblk, share);
-            if (pieces > 0) len = ceil_div(nblk, pieces);
-            rows = pieces * p.Hkv * p.units[u].rows;
-        }
-        int total;
-        const int at = parts + sh_scan(rows, warp_tot, total);
-        parts += total;
-        sh_scan(pieces * p.Hkv, warp_tot, total);
-        items += total;
-        if (u < n_units) {
-            p.units[u].pieces = pieces;
-            p.units[u].part = at;
-            if (pieces > 0) atomicAdd(&hist[kShBins - 1 - min(len, kShBins - 1)], pieces * p.Hkv);
+            mine[sh_few(x.rows)] += x.nblk;
+            if (at + u < p.max_units) {
+                p.units[at + u] = x;
+                lengths[at + u] = make_int2(x.nblk, x.rows);
+            }
         }
     }
+#pragma unroll
+    for (int k = 0; k < 2; ++k) {
+#pragma unroll
+        for (int o = 16; o > 0; o >>= 1) mine[k] += __shfl_xor_sync(0xffffffffu, mine[k], o);
+        if (lane == 0 && mine[k] > 0) atomicAdd(&work[k], mine[k]);
+    }
     __syncthreads();
+    const int n_pre = n_prefix, own = n_own;
     // (the host's bounds hold for every list that passed the checks above)
-    const bool fits = n_prefix + n_own <= p.max_units && parts <= p.max_parts && items <= p.max_items;
-    int total;
-    const int first = sh_scan(hist[tid], warp_tot, total);
-    hist[tid] = first;
-    __syncthreads();
-    for (int base = 0; base < n_units; base += kShUnitsThreads) {
-        const int u = base + tid;
-        int count = 0, at = 0;
-        if (u < n_units && fits) {
-            const int pieces = p.units[u].pieces;
-            count = pieces * p.Hkv;
-            if (count > 0)
-                at = atomicAdd(&hist[kShBins - 1 - min(ceil_div(p.units[u].nblk, pieces), kShBins - 1)], count);
+    const bool fits = n_pre <= p.own_base && p.own_base + own <= p.max_units;
+    const int n_units = fits ? n_pre + own : 0;
+    int share[2];
+#pragma unroll
+    for (int k = 0; k < 2; ++k) {
+        const int shares = k ? kSharedSmallShares : kSharedShares;
+        share[k] = static_cast<int>(max((static_cast<long long>(work[k]) * p.Hkv + shares - 1) / shares,
+                                        static_cast<long long>(kShMinPiece)));
+    }
+    // a unit's pieces and the list's bin of their length
+    const auto cut = [&](int i, int& u, int& few, int& pieces, int& rows, int& bin) {
+        u = i < n_pre ? i : p.own_base + i - n_pre;
+        const int2 x = lengths[u];
+        few = sh_few(x.y);
+        rows = x.y;
+        pieces = ceil_div(x.x, share[few]);
+        bin = 0;
+        if (pieces > 0) {
+            const int len = ceil_div(x.x, pieces);  // 1 .. share
+            bin = few * kShBins + kShBins - 1 -
+                  static_cast<int>(static_cast<long long>(len - 1) * kShBins / share[few]);
         }
+    };
+    // 3. pieces, and the places of their results
+    for (int base = 0; base < n_units; base += kShUnitsThreads) {
+        int u = 0, few = 0, pieces = 0, rows = 0, bin = 0;
+        const bool on = base + tid < n_units;
+        if (on) cut(base + tid, u, few, pieces, rows, bin);
+        const int split = few ? kSharedSmallSplit : 1;
+        const int at = sh_reserve(&n_parts, pieces * split * p.Hkv * rows, lane);
+        if (on) {
+            p.units[u].pieces = pieces;
+            p.units[u].split = split;
+            p.units[u].part = at;
+            if (pieces > 0) atomicAdd(&hist[bin], pieces * p.Hkv);
+        }
+    }
+    __syncthreads();
+    // 4. the bins' places (2 kShBins = 64: two a lane)
+    if (warp == 0) {
+        const int a = hist[2 * lane], b = hist[2 * lane + 1];
+        int x = a + b;
+#pragma unroll
+        for (int o = 1; o < 32; o <<= 1) {
+            const int y = __shfl_up_sync(0xffffffffu, x, o);
+            if (lane >= o) x += y;
+        }
+        hist[2 * lane] = x - a - b;
+        hist[2 * lane + 1] = x - b;
+        const int many = __shfl_sync(0xffffffffu, x, 15), all = __shfl_sync(0xffffffffu, x, 31);
+        if (lane == 0) {
+            const bool ok = fits && n_parts <= p.max_parts && all <= p.max_items;
+            if (!ok) atomicOr(p.status, kStatusBounds);
+            SharedHeader* h = p.header;
+            h->n_items[0] = ok ? many : 0;
+            h->n_items[1] = ok ? all - many : 0;
+            h->next_item[0] = h->next_item[1] = 0;
+            h->n_own = ok ? own : 0;
+            h->bad = ok ? 0 : 1;
+            if (!ok) n_parts = -1;
+        }
+    }
+    __syncthreads();
+    if (n_parts < 0) return;
+    // 5. items
+    for (int base = 0; base < n_units; base += kShUnitsThreads) {
+        int u = 0, few = 0, pieces = 0, rows = 0, bin = 0, at = 0;
+        if (base + tid < n_units) cut(base + tid, u, few, pieces, rows, bin);
+        const int count = pieces * p.Hkv;
+        if (count > 0) at = atomicAdd(&hist[bin], count);
         const bool many = count > 64;  // the whole warp writes those
-        if (!many)
-            for (int i = 0; i < count; ++i) p.items[at + i] = make_int2(u, i);
+        if (!many) {
+            for (int s = 0, i = 0; s < pieces; ++s)
+                for (int h = 0; h < p.Hkv; ++h, ++i) p.items[at + i] = make_int2(u, s << 16 | h);
+        }
         for (unsigned m = __ballot_sync(0xffffffffu, many); m != 0; m &= m - 1) {
             const int src = __ffs(m) - 1;
             const int from = __shfl_sync(0xffffffffu, at, src), n = __shfl_sync(0xffffffffu, count, src);
-            for (int i = lane; i < n; i += 32) p.items[from + i] = make_int2(u - lane + src, i);
+            const int unit = __shfl_sync(0xffffffffu, u, src);
+            for (int i = lane; i < n; i += 32) p.items[from + i] = make_int2(unit, (i / p.Hkv) << 16 | i % p.Hkv);
         }
-    }
-    if (tid == 0) {
-        if (!fits) atomicOr(p.status, kStatusBounds);
-        p.header->n_items = fits ? items : 0;
-        p.header->next_item = 0;
-        p.header->n_own = n_own;
-        p.header->n_prefix = n_prefix;
-        p.header->bad = fits ? 0 : 1;
     }
 }
 
@@ -292,15 +316,16 @@ struct ShCfg {
 };
 
 constexpr uint32_t kShRing = 4;
-constexpr uint32_t kShReaders = 18;  // the two MMA issuers and the 16 softmax warps
+constexpr uint32_t kShReaders = 19;  // the producer, the two MMA issuers and the 16 softmax warps
 
-// One item as the producer hands it to the other roles: a piece of a unit for one kv head.
+// One item as the scheduler hands it to the other roles: a piece of a unit for one kv head.
 struct ShItem {
     int q0, ntok;  // ntok = 0: no more items
     int kvh, row, key_min, key_end, pos0;
-    int jlo, jhi;  // key blocks
-    int part;      // the row of its first result
-    int pad[2];
+    int jlo, jhi;   // key blocks
+    int part;       // the row of its first result
+    uint32_t kv0;   // the ring's loads before its first
+    uint32_t vpar;  // per slot the parity of the V loads before its first
 };
 
 struct ShBars {
@@ -309,6 +334,7 @@ struct ShBars {
     uint64_t s_full[2], s_free[2], p_full[2], pv_done[2], o_free[2];
     uint64_t drain[2];
     uint64_t idx_full[kShRing], idx_empty[kShRing];
+    uint64_t near_end;  // the producer is about to be done with its item
     ShItem ring[kShRing];
     uint32_t tmem_base;
     int abort_flag;
@@ -321,39 +347,62 @@ __device__ __forceinline__ uint32_t sh_pos_v(int i, int m) { return i == m - 1 ?
 
 __device__ __forceinline__ uint32_t sh_parity(uint32_t bits, uint32_t st) { return (bits >> st) & 1u; }
 
-// The producer warp's claim of ring position r (false: a wait gave up).
-__device__ __forceinline__ bool sh_claim(const SharedParams& p, ShBars* bars, const Watchdog& wd, int n_items,
-                                         uint32_t r, ShItem& it, int lane) {
-    const uint32_t slot = r % kShRing;
-    const bool ok = r < kShRing || wd.wait(&bars->idx_empty[slot], ((r / kShRing) - 1) & 1);
-    if (!__all_sync(0xffffffffu, ok)) return false;
-    int idx = 0;
-    if (lane == 0) idx = atomicAdd(&p.header->next_item, 1);
-    idx = __shfl_sync(0xffffffffu, idx, 0);
-    it.ntok = 0;
-    if (idx < n_items) {
-        const int2 w = p.items[idx];
-        const SharedUnit u = p.units[w.x];
-        const int piece = w.y / p.Hkv;
-        it.q0 = u.q0;
-        it.ntok = u.ntok;
-        it.kvh = w.y - piece * p.Hkv;
-        it.row = u.row;
-        it.key_min = u.key_min;
-        it.key_end = u.key_end;
-        it.pos0 = u.pos0;
-        it.jlo = u.blk0 + static_cast<int>(static_cast<long long>(u.nblk) * piece / u.pieces);
-        it.jhi = u.blk0 + static_cast<int>(static_cast<long long>(u.nblk) * (piece + 1) / u.pieces);
-        it.part = u.part + (it.kvh * u.pieces + piece) * u.rows;
+// Warp 19 claims items and works them out when the producer is about to be done with the one before, so that no
+// load waits for it and CTAs take items as they free up (claimed as the one before begins, the CTAs that
+// have the longest items take the next longest as well: 64 requests behind 32K keys 105 -> 127 us).  The first
+// one is the block's own, later ones come off a counter.
+// kKind: which of the list's two halves.
+template <int kKind, int kSlots, typename Bars>
+__device__ void sh_scheduler(const SharedParams& p, Bars* bars, const Watchdog& wd, int lane) {
+    const int first = kKind ? p.header->n_items[0] : 0, n_items = p.header->n_items[kKind];
+    uint32_t kv = 0, vpar = 0;
+    for (uint32_t r = 0;; ++r) {
+        const uint32_t slot = r % kShRing;
+        bool ok = r < kShRing || wd.wait(&bars->idx_empty[slot], ((r / kShRing) - 1) & 1);
+        if (r >= 1) ok = ok && wd.wait(&bars->near_end, (r - 1) & 1);
+        if (!__all_sync(0xffffffffu, ok)) return;
+        int idx = blockIdx.x;
+        if (r > 0) {
+            if (lane == 0) idx = gridDim.x + atomicAdd(&p.header->next_item[kKind], 1);
+            idx = __shfl_sync(0xffffffffu, idx, 0);
+        }
+        ShItem it = {};
+        if (idx < n_items) {
+            const int2 w = p.items[first + idx];
+            const SharedUnit u = p.units[w.x];
+            const int piece = w.y >> 16;
+            // (the first nblk % pieces of them have a block more)
+            const int len = u.nblk / u.pieces, more = u.nblk - len * u.pieces;
+            it.q0 = u.q0;
+            it.ntok = u.ntok;
+            it.kvh = w.y & 0xffff;
+            it.row = u.row;
+            it.key_min = u.key_min;
+            it.key_end = u.key_end;
+            it.pos0 = u.pos0;
+            it.jlo = u.blk0 + piece * len + min(piece, more);
+            it.jhi = it.jlo + len + (piece < more ? 1 : 0);
+            it.part = u.part + (it.kvh * u.pieces + piece) * u.split * u.rows;
+            it.kv0 = kv;
+            it.vpar = vpar;
+        }
+        if (lane == 0) {
+            bars->ring[slot] = it;
+            mbar_arrive(&bars->idx_full[slot]);  // release: the item is visible to the readers
+        }
+        if (it.ntok == 0) return;
+        if (kKind == 0) {
+            const int m = it.jhi - it.jlo;
+            uint32_t mine = 0;
+            for (int i = lane; i < m; i += 32) mine ^= 1u << ((kv + sh_pos_v(i, m)) % kSlots);
+            vpar ^= __reduce_xor_sync(0xffffffffu, mine);
+            kv += 2 * m;
+        }
     }
-    if (lane == 0) {
-        bars->ring[slot] = it;
-        mbar_arrive(&bars->idx_full[slot]);  // release: the item is visible to the readers
-    }
-    return true;
 }
 
-__device__ __forceinline__ bool sh_take(ShBars* bars, const Watchdog& wd, uint32_t& r, ShItem& it) {
+template <typename Bars>
+__device__ __forceinline__ bool sh_take(Bars* bars, const Watchdog& wd, uint32_t& r, ShItem& it) {
     const uint32_t slot = r % kShRing;
     if (!wd.wait(&bars->idx_full[slot], (r / kShRing) & 1)) return false;
     it = bars->ring[slot];
@@ -362,7 +411,8 @@ __device__ __forceinline__ bool sh_take(ShBars* bars, const Watchdog& wd, uint32
     return it.ntok > 0;
 }
 
-__device__ __forceinline__ bool sh_take_warp(ShBars* bars, const Watchdog& wd, uint32_t& r, ShItem& it, int lane) {
+template <typename Bars>
+__device__ __forceinline__ bool sh_take_warp(Bars* bars, const Watchdog& wd, uint32_t& r, ShItem& it, int lane) {
     const uint32_t slot = r % kShRing;
     if (!__all_sync(0xffffffffu, wd.wait(&bars->idx_full[slot], (r / kShRing) & 1))) return false;
     it = bars->ring[slot];
@@ -387,7 +437,7 @@ struct ShRingState {
 // The whole warp: lane i looks up piece i of a block in the table and loads it.
 template <int D>
 __device__ void sh_producer_loop(const SharedParams& p, uint8_t* smem, ShBars* bars, const Watchdog& wd,
-                                 int n_items, uint32_t& q_cnt, ShRingState& ring, int lane) {
+                                 uint32_t& q_cnt, ShRingState& ring, int lane) {
     using C = ShCfg<D>;
     if (lane == 0) {
         tma_prefetch_desc(&p.tm_q);
@@ -397,10 +447,9 @@ __device__ void sh_producer_loop(const SharedParams& p, uint8_t* smem, ShBars* b
     }
     const int boxes = kFwdBlockN / p.box_rows;
     const int oob_row = p.num_pages * p.page_size;
-    uint32_t claims = 0;
-    ShItem it, next;
-    if (!sh_claim(p, bars, wd, n_items, claims++, it, lane)) return;
-    while (it.ntok > 0) {
+    uint32_t rd = 0;
+    ShItem it;
+    while (sh_take_warp(bars, wd, rd, it, lane)) {
         if (!__all_sync(0xffffffffu, q_cnt == 0 || wd.wait(&bars->q_empty, (q_cnt - 1) & 1))) return;
         if (lane == 0) {
             uint32_t bytes = 0;
@@ -441,6 +490,7 @@ __device__ void sh_producer_loop(const SharedParams& p, uint8_t* smem, ShBars* b
                         atomicOr(p.status, kStatusBounds);
                 }
             }
+            if (r == max(0, 2 * m - 6) && lane == 0) mbar_arrive(&bars->near_end);
             const uint32_t n = ring.n, st = n % C::kSlots;
             if (!__all_sync(0xffffffffu, n < C::kSlots || wd.wait(&bars->kv_empty[st], ((n / C::kSlots) - 1) & 1)))
                 return;
@@ -461,22 +511,16 @@ __device__ void sh_producer_loop(const SharedParams& p, uint8_t* smem, ShBars* b
                 for (int h = 0; h < C::kHalves; ++h)
                     tma_load_3d(dst + h * C::kAtomBytes, is_v ? &p.tm_v : &p.tm_k, full, h * 64, it.kvh, row);
             }
-            // the next item's claim, behind the blocks still to come (see fwd_kernel.cu)
-            if (r == max(min(1, 2 * m - 1), 2 * m - 5) &&
-                !sh_claim(p, bars, wd, n_items, claims++, next, lane))
-                return;
         }
-        it = next;
     }
 }
 
 template <int D>
-__device__ void sh_producer(const SharedParams& p, uint8_t* smem, ShBars* bars, const Watchdog& wd, int n_items,
-                            int lane) {
+__device__ void sh_producer(const SharedParams& p, uint8_t* smem, ShBars* bars, const Watchdog& wd, int lane) {
     using C = ShCfg<D>;
     uint32_t q_cnt = 0;
     ShRingState ring;
-    sh_producer_loop<D>(p, smem, bars, wd, n_items, q_cnt, ring, lane);
+    sh_producer_loop<D>(p, smem, bars, wd, q_cnt, ring, lane);
     __syncwarp();
     // what is in flight lands before the CTA's shared memory goes
     if (q_cnt > 0) sh_drain(&bars->q_full, (q_cnt - 1) & 1);
@@ -494,7 +538,7 @@ __device__ void sh_mma_s(const SharedParams& p, uint8_t* smem, ShBars* bars, uin
     const uint64_t dkv = sdesc_sw128(smem_u32(smem + C::kOffKV), 16, 1024);
     const uint32_t q_lo = static_cast<uint32_t>(dq), d_hi = static_cast<uint32_t>(dq >> 32);
     const uint32_t kv_lo = static_cast<uint32_t>(dkv);
-    uint32_t q_cnt = 0, kv_cnt = 0, kpar = 0, rd = 0;
+    uint32_t q_cnt = 0, kpar = 0, rd = 0;
     uint32_t s_cnt[2] = {0, 0};
     ShItem it;
     while (sh_take(bars, wd, rd, it)) {
@@ -503,7 +547,7 @@ __device__ void sh_mma_s(const SharedParams& p, uint8_t* smem, ShBars* bars, uin
         const int m = it.jhi - it.jlo;
         const bool two = it.ntok > p.tpt;
         for (int i = 0; i < m; ++i) {
-            const uint32_t st = (kv_cnt + sh_pos_k(i)) % C::kSlots;
+            const uint32_t st = (it.kv0 + sh_pos_k(i)) % C::kSlots;
             if (!wd.wait(&bars->k_full[st], sh_parity(kpar, st))) return;
             kpar ^= 1u << st;
             const uint32_t k_lo = kv_lo + st * (C::kKvTile >> 4);
@@ -524,7 +568,6 @@ __device__ void sh_mma_s(const SharedParams& p, uint8_t* smem, ShBars* bars, uin
             umma_commit(&bars->kv_empty[st]);
         }
         umma_commit(&bars->q_empty);
-        kv_cnt += 2 * m;
     }
 }
 
@@ -536,14 +579,14 @@ __device__ void sh_mma_pv(const SharedParams& p, uint8_t* smem, ShBars* bars, ui
     const uint64_t dv = sdesc_sw128(smem_u32(smem + C::kOffKV), C::kAtomBytes, 1024);
     const uint32_t p_lo = static_cast<uint32_t>(dp), p_hi = static_cast<uint32_t>(dp >> 32);
     const uint32_t v_lo = static_cast<uint32_t>(dv), v_hi = static_cast<uint32_t>(dv >> 32);
-    uint32_t kv_cnt = 0, vpar = 0, rd = 0;
+    uint32_t vpar = 0, rd = 0;
     uint32_t pv_cnt[2] = {0, 0}, o_items[2] = {0, 0};
     ShItem it;
     while (sh_take(bars, wd, rd, it)) {
         const int m = it.jhi - it.jlo;
         const bool two = it.ntok > p.tpt;
         for (int i = 0; i < m; ++i) {
-            const uint32_t st = (kv_cnt + sh_pos_v(i, m)) % C::kSlots;
+            const uint32_t st = (it.kv0 + sh_pos_v(i, m)) % C::kSlots;
             if (!wd.wait(&bars->v_full[st], sh_parity(vpar, st))) return;
             vpar ^= 1u << st;
             const uint32_t b_lo = v_lo + st * (C::kKvTile >> 4);
@@ -567,7 +610,6 @@ __device__ void sh_mma_pv(const SharedParams& p, uint8_t* smem, ShBars* bars, ui
         }
         ++o_items[0];
         if (two) ++o_items[1];
-        kv_cnt += 2 * m;
     }
 }
 
@@ -597,13 +639,10 @@ __device__ void sh_softmax(const SharedParams& p, uint8_t* smem, ShBars* bars, u
     const float sl2 = p.scale_log2;
     const uint64_t sl2x2 = f2_make(sl2, sl2);
     const int g = p.g;
-    uint32_t blk = 0, kv_cnt = 0, vpar = 0, rd = 0;
+    uint32_t blk = 0, rd = 0;
     ShItem it;
     while (sh_take_warp(bars, wd, rd, it, lane)) {
         const int m = it.jhi - it.jlo;
-        const uint32_t kv_base = kv_cnt, vpar_item = vpar;
-        kv_cnt += 2 * m;
-        for (int i = 0; i < m; ++i) vpar ^= 1u << ((kv_base + sh_pos_v(i, m)) % C::kSlots);
         const int tokens = min(p.tpt, it.ntok - t * p.tpt);
         if (tokens <= 0) continue;
         const int rows = tokens * g;
@@ -617,7 +656,7 @@ __device__ void sh_softmax(const SharedParams& p, uint8_t* smem, ShBars* bars, u
         for (int j = it.jlo; j < it.jhi; ++j) {
             if (!__all_sync(0xffffffffu, wd.wait(s_full, blk & 1))) return;
             uint32_t pka[16], pkb[16];
-            bool need_a = false, need_b = false;
+            bool moves = false;
             float alpha_a = 1.f, alpha_b = 1.f;
             if (busy) {
                 tc_fence_after();
@@ -651,21 +690,21 @@ __device__ void sh_softmax(const SharedParams& p, uint8_t* smem, ShBars* bars, u
                     xb0 = fmax3(xb0, __uint_as_float(s[4 * c + 2]), __uint_as_float(s[4 * c + 6]));
                     xb1 = fmax3(xb1, __uint_as_float(s[4 * c + 3]), __uint_as_float(s[4 * c + 7]));
                 }
-                float mxa = fmaxf(xa0, xa1), mxb = fmaxf(xb0, xb1);
-                mxa = fmaxf(mxa, __shfl_xor_sync(0xffffffffu, mxa, 1));
-                mxb = fmaxf(mxb, __shfl_xor_sync(0xffffffffu, mxb, 1));
-                mxa = fmaxf(mxa, __shfl_xor_sync(0xffffffffu, mxa, 2));
-                mxb = fmaxf(mxb, __shfl_xor_sync(0xffffffffu, mxb, 2));
-                const float mba = mxa * sl2, mbb = mxb * sl2;
-                need_a = mba > m_a + kShRescale;
-                need_b = mbb > m_b + kShRescale;
-                const float mna = need_a ? mba : m_a, mnb = need_b ? mbb : m_b;
-                alpha_a = need_a ? ex2_approx(m_a - mna) : 1.f;
-                alpha_b = need_b ? ex2_approx(m_b - mnb) : 1.f;
-                l_a *= alpha_a;
-                l_b *= alpha_b;
-                m_a = mna;
-                m_b = mnb;
+                float mba = fmaxf(xa0, xa1) * sl2, mbb = fmaxf(xb0, xb1) * sl2;
+                moves = __any_sync(0xffffffffu, mba > m_a + kShRescale || mbb > m_b + kShRescale);
+                if (moves) {  // (a row's maximum is its quad's)
+                    mba = fmaxf(mba, __shfl_xor_sync(0xffffffffu, mba, 1));
+                    mbb = fmaxf(mbb, __shfl_xor_sync(0xffffffffu, mbb, 1));
+                    mba = fmaxf(mba, __shfl_xor_sync(0xffffffffu, mba, 2));
+                    mbb = fmaxf(mbb, __shfl_xor_sync(0xffffffffu, mbb, 2));
+                    const float mna = mba > m_a + kShRescale ? mba : m_a, mnb = mbb > m_b + kShRescale ? mbb : m_b;
+                    alpha_a = mna > m_a ? ex2_approx(m_a - mna) : 1.f;
+                    alpha_b = mnb > m_b ? ex2_approx(m_b - mnb) : 1.f;
+                    l_a *= alpha_a;
+                    l_b *= alpha_b;
+                    m_a = mna;
+                    m_b = mnb;
+                }
                 const float na = m_a == -INFINITY ? 0.f : -m_a, nb = m_b == -INFINITY ? 0.f : -m_b;
                 const uint64_t nma = f2_make(na, na), nmb = f2_make(nb, nb);
                 uint64_t suma = 0, sumb = 0;
@@ -694,9 +733,9 @@ __device__ void sh_softmax(const SharedParams& p, uint8_t* smem, ShBars* bars, u
             const int lo_key = max(it.key_min - j * kFwdBlockN, 0);
             const int hi_key = min(it.key_end - j * kFwdBlockN, kFwdBlockN);
             if (lo_key > 0 || hi_key < kFwdBlockN) {
-                uint32_t bits = vpar_item;  // V parities before V_j's load
-                for (int i = 0; i < j - it.jlo; ++i) bits ^= 1u << ((kv_base + sh_pos_v(i, m)) % C::kSlots);
-                const uint32_t st = (kv_base + sh_pos_v(j - it.jlo, m)) % C::kSlots;
+                uint32_t bits = it.vpar;  // V parities before V_j's load
+                for (int i = 0; i < j - it.jlo; ++i) bits ^= 1u << ((it.kv0 + sh_pos_v(i, m)) % C::kSlots);
+                const uint32_t st = (it.kv0 + sh_pos_v(j - it.jlo, m)) % C::kSlots;
                 if (!__all_sync(0xffffffffu, wd.wait(&bars->v_full[st], sh_parity(bits, st)))) return;
                 const uint32_t vslot = smem_u32(smem + C::kOffKV + st * C::kKvTile);
                 const int clear = lo_key + kFwdBlockN - hi_key;
@@ -714,7 +753,7 @@ __device__ void sh_softmax(const SharedParams& p, uint8_t* smem, ShBars* bars, u
                 tc_fence_after();
             }
             if (busy) {
-                if (__any_sync(0xffffffffu, need_a || need_b) && j > it.jlo) {
+                if (moves && j > it.jlo) {
 #pragma unroll 1
                     for (int cc = 0; cc < D / 32; ++cc) {
                         uint32_t o[16];
@@ -790,7 +829,6 @@ __global__ void __launch_bounds__(kFwdThreads, 1) shared_attn_kernel(const __gri
                                                ~static_cast<uintptr_t>(1023));
     ShBars* bars = reinterpret_cast<ShBars*>(smem + C::kOffBar);
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
-    griddep_launch_dependents();
     if (threadIdx.x == 0) {
         mbar_init(&bars->q_full, 1);
         mbar_init(&bars->q_empty, 1);
@@ -811,6 +849,7 @@ __global__ void __launch_bounds__(kFwdThreads, 1) shared_attn_kernel(const __gri
             mbar_init(&bars->idx_full[i], 1);
             mbar_init(&bars->idx_empty[i], kShReaders);
         }
+        mbar_init(&bars->near_end, 1);
         bars->abort_flag = 0;
         mbar_fence_init();
     }
@@ -820,14 +859,16 @@ __global__ void __launch_bounds__(kFwdThreads, 1) shared_attn_kernel(const __gri
     tc_fence_after();
     const uint32_t tmem = bars->tmem_base;
     const Watchdog wd{&bars->abort_flag, p.status};
-    griddep_wait();  // the list, and what this call's predecessors wrote
-    const int n_items = p.header->n_items;
+    griddep_wait();  // the list, and what stands before this call
+    griddep_launch_dependents();  // (from here on the list may be read without waiting)
     // registers as in fwd_kernel.cu: 128 * 64 + 512 * 104 = 640 * 96
     if (warp >= kShSoftmaxWarps) {
         regs_decrease<64>();
         if (warp == kShSoftmaxWarps) {
-            sh_producer<D>(p, smem, bars, wd, n_items, lane);
-        } else if (warp <= kShSoftmaxWarps + 2) {
+            sh_producer<D>(p, smem, bars, wd, lane);
+        } else if (warp == kShSoftmaxWarps + 3) {
+            sh_scheduler<0, C::kSlots>(p, bars, wd, lane);
+        } else {
             if (lane == 0) {
                 const int w = warp - kShSoftmaxWarps - 1;
                 if (w == 0)
@@ -851,37 +892,307 @@ __global__ void __launch_bounds__(kFwdThreads, 1) shared_attn_kernel(const __gri
     }
 }
 
+// ---- few rows -------------------------------------------------------------------------------------------
+//
+// Units of up to 16 rows (a sequence's single query, a few sequences' behind a prefix) would fill an eighth of a
+// tile, and one warp's softmax over it, 3000 clocks a block, would be slower than the memory.  As in
+// decode_kernel.cu four warps take 16 keys each of a chunk of 64, on mma.sync m16n8k16, two CTAs an SM.
+// The warps never meet: each leaves a part of its own.
+
+template <int D>
+struct SmCfg {
+    static constexpr int kChunk = 64;
+    static constexpr int kHalves = D / 64;
+    static constexpr int kHalfBytes = kChunk * 128;
+    static constexpr int kKvBytes = kHalves * kHalfBytes;
+    static constexpr int kStageBytes = 2 * kKvBytes;
+    static constexpr int kStages = D == 128 ? 3 : 6;
+    static constexpr int kOffBar = kStages * kStageBytes;
+    static constexpr int kSmem = kOffBar + 512 + 1024;
+    static_assert(2 * (kSmem + 1024) <= 228 * 1024, "two CTAs per SM");
+};
+
+constexpr int kSmThreads = 192;  // 4 MMA warps, the producer and the scheduler
+constexpr uint32_t kSmReaders = 5;
+
+struct SmBars {
+    uint64_t full[6], empty[6];
+    uint64_t idx_full[kShRing], idx_empty[kShRing];
+    uint64_t near_end;
+    ShItem ring[kShRing];
+    int abort_flag;
+};
+static_assert(sizeof(SmBars) <= 512, "barrier block");
+
+// The 64-key chunks of an item.
+__device__ __forceinline__ int sm_first(const ShItem& it) { return max(2 * it.jlo, it.key_min / 64); }
+__device__ __forceinline__ int sm_last(const ShItem& it) { return min(2 * it.jhi, ceil_div(it.key_end, 64)); }
+
+template <int D>
+__device__ void sm_producer(const SharedParams& p, uint8_t* smem, SmBars* bars, const Watchdog& wd, int lane) {
+    using C = SmCfg<D>;
+    const int box = min(p.box_rows, C::kChunk), boxes = C::kChunk / box;
+    const int oob_row = p.num_pages * p.page_size;
+    uint32_t issued = 0, rd = 0;
+    bool ok = true;
+    ShItem it;
+    while (ok && sh_take_warp(bars, wd, rd, it, lane)) {
+        const int* bt = p.block_table + static_cast<size_t>(it.row) * p.max_pages;
+        const int c0 = sm_first(it), c1 = sm_last(it);
+        for (int c = c0; c < c1; ++c, ++issued) {
+            if (c == max(c0, c1 - 3) && lane == 0) mbar_arrive(&bars->near_end);
+            // lane i: box i of the chunk (see sh_producer_loop)
+            int row = oob_row;
+            if (lane < boxes) {
+                const int key = c * C::kChunk + lane * box;
+                if (key < it.key_end && key + box > it.key_min) {
+                    const int page = bt[key / p.page_size];
+                    if (page >= 0 && page < p.num_pages)
+                        row = page * p.page_size + key % p.page_size;
+                    else
+                        atomicOr(p.status, kStatusBounds);
+                }
+            }
+            const uint32_t st = issued % C::kStages;
+            ok = __all_sync(0xffffffffu, issued < C::kStages ||
+                                             wd.wait(&bars->empty[st], ((issued / C::kStages) - 1) & 1));
+            if (!ok) break;
+            if (lane == 0) mbar_arrive_expect_tx(&bars->full[st], C::kStageBytes);
+            __syncwarp();
+            if (lane < boxes) {
+                uint8_t* const dst = smem + st * C::kStageBytes + lane * box * 128;
+#pragma unroll
+                for (int h = 0; h < C::kHalves; ++h) {
+                    tma_load_3d(dst + h * C::kHalfBytes, &p.tm_k64, &bars->full[st], h * 64, it.kvh, row);
+                    tma_load_3d(dst + C::kKvBytes + h * C::kHalfBytes, &p.tm_v64, &bars->full[st], h * 64, it.kvh, row);
+                }
+            }
+        }
+    }
+    __syncwarp();
+    // what is in flight lands before the CTA's shared memory goes
+    const uint32_t n_st = min(issued, static_cast<uint32_t>(C::kStages));
+    for (uint32_t st = 0; st < n_st; ++st) {
+        const uint32_t last = st + C::kStages * ((issued - 1 - st) / C::kStages);
+        sh_drain(&bars->full[st], (last / C::kStages) & 1);
+    }
+}
+
+__device__ __forceinline__ uint32_t sm_swz(int row, int oct) {
+    return static_cast<uint32_t>(row * 128 + ((oct ^ (row & 7)) << 4));
+}
+
+// Warp w has keys [16 w, 16 w + 16) of every chunk.
+template <int D>
+__device__ void sm_consumer(const SharedParams& p, uint8_t* smem, SmBars* bars, const Watchdog& wd, int warp,
+                            int lane) {
+    using C = SmCfg<D>;
+    const int gq = lane >> 2, tq = lane & 3;
+    const int mi = lane >> 3, ri = lane & 7;  // ldmatrix: matrix id, row within matrix
+    const float sl2 = p.scale_log2;
+    uint32_t n = 0, rd = 0;
+    ShItem it;
+    while (sh_take_warp(bars, wd, rd, it, lane)) {
+        const int rows = it.ntok * p.g;
+        // rows gq and gq + 8: tokens, the last keys that they see, queries as the A operand
+        int kmax[2];
+        uint32_t qa[D / 16][4];
+#pragma unroll
+        for (int h = 0; h < 2; ++h) {
+            const int r = gq + 8 * h, tok = r / p.g;
+            const bool on = r < rows;
+            kmax[h] = min(it.key_end - 1, it.pos0 + tok);
+            const __nv_bfloat16* src =
+                p.q + (static_cast<size_t>(it.q0 + (on ? tok : 0)) * p.Hq + it.kvh * p.g + (on ? r - tok * p.g : 0)) * D;
+#pragma unroll
+            for (int kk = 0; kk < D / 16; ++kk) {
+                const uint32_t* x = reinterpret_cast<const uint32_t*>(src + kk * 16 + 2 * tq);
+                qa[kk][h] = on ? x[0] : 0u;
+                qa[kk][2 + h] = on ? x[4] : 0u;
+            }
+        }
+        const int kmax_first = min(it.key_end - 1, it.pos0);
+        float m_run[2] = {-INFINITY, -INFINITY}, l_run[2] = {0.f, 0.f};
+        float o[D / 8][4];
+#pragma unroll
+        for (int x = 0; x < D / 8; ++x) o[x][0] = o[x][1] = o[x][2] = o[x][3] = 0.f;
+        const int c1 = sm_last(it);
+        for (int c = sm_first(it); c < c1; ++c, ++n) {
+            const uint32_t st = n % C::kStages;
+            if (!__all_sync(0xffffffffu, wd.wait(&bars->full[st], (n / C::kStages) & 1))) return;
+            uint8_t* const kst = smem + st * C::kStageBytes;
+            uint8_t* const vst = kst + C::kKvBytes;
+            const int key0 = c * C::kChunk + warp * 16;
+            const int lo = max(it.key_min - key0, 0), hi = min(it.key_end - key0, 16);
+            if (lo < hi) {
+                if (lo > 0 || hi < 16) {
+                    // slots outside [key_min, key_end) may hold anything, and 0 times a NaN would reach O
+                    for (int i = lane; i < 16 * C::kHalves * 8; i += 32) {
+                        const int r = i / (C::kHalves * 8), rest = i % (C::kHalves * 8);
+                        if (r < lo || r >= hi)
+                            *reinterpret_cast<uint4*>(vst + (rest / 8) * C::kHalfBytes + (warp * 16 + r) * 128 +
+                                                      (rest % 8) * 16) = make_uint4(0, 0, 0, 0);
+                    }
+                    fence_proxy_async_smem();
+                    __syncwarp();
+                }
+                float s[2][4] = {{0.f, 0.f, 0.f, 0.f}, {0.f, 0.f, 0.f, 0.f}};
+                const uint32_t kbase = smem_u32(kst);
+#pragma unroll
+                for (int kk = 0; kk < D / 16; ++kk) {
+                    const int key = warp * 16 + (mi >> 1) * 8 + ri, oct = 2 * kk + (mi & 1);
+                    uint32_t b0, b1, b2, b3;
+                    ldmatrix_x4(kbase + (oct >> 3) * C::kHalfBytes + sm_swz(key, oct & 7), b0, b1, b2, b3);
+                    mma_bf16_16816(s[0], qa[kk], b0, b1);
+                    mma_bf16_16816(s[1], qa[kk], b2, b3);
+                }
+                if (lo > 0 || key0 + 15 > kmax_first) {
+#pragma unroll
+                    for (int nt = 0; nt < 2; ++nt)
+#pragma unroll
+                        for (int e = 0; e < 4; ++e) {
+                            const int key = key0 + nt * 8 + 2 * tq + (e & 1);
+                            if (key < it.key_min || key > kmax[e >> 1]) s[nt][e] = -INFINITY;
+                        }
+                }
+                float mx[2];
+                bool up = false;
+#pragma unroll
+                for (int r = 0; r < 2; ++r) {
+                    mx[r] = fmaxf(fmaxf(s[0][2 * r], s[0][2 * r + 1]), fmaxf(s[1][2 * r], s[1][2 * r + 1])) * sl2;
+                    up = up || mx[r] > m_run[r] + kShRescale;
+                }
+                if (__any_sync(0xffffffffu, up)) {  // a row's reference moves (rarely behind the first chunks)
+                    float alpha[2];
+#pragma unroll
+                    for (int r = 0; r < 2; ++r) {
+                        mx[r] = fmaxf(mx[r], __shfl_xor_sync(0xffffffffu, mx[r], 1));
+                        mx[r] = fmaxf(mx[r], __shfl_xor_sync(0xffffffffu, mx[r], 2));
+                        const bool moves = mx[r] > m_run[r] + kShRescale;
+                        alpha[r] = moves ? ex2_approx(m_run[r] - mx[r]) : 1.f;
+                        if (moves) m_run[r] = mx[r];
+                        l_run[r] *= alpha[r];
+                    }
+#pragma unroll
+                    for (int x = 0; x < D / 8; ++x)
+#pragma unroll
+                        for (int e = 0; e < 4; ++e) o[x][e] *= alpha[e >> 1];
+                }
+                uint32_t pa[4];
+                const float nm[2] = {m_run[0] == -INFINITY ? 0.f : -m_run[0], m_run[1] == -INFINITY ? 0.f : -m_run[1]};
+#pragma unroll
+                for (int nt = 0; nt < 2; ++nt)
+#pragma unroll
+                    for (int r = 0; r < 2; ++r) {
+                        const float p0 = ex2_approx(fmaf(s[nt][2 * r], sl2, nm[r]));
+                        const float p1 = ex2_approx(fmaf(s[nt][2 * r + 1], sl2, nm[r]));
+                        l_run[r] += p0 + p1;
+                        pa[2 * nt + r] = pack_bf16x2(p0, p1);
+                    }
+                const uint32_t vbase = smem_u32(vst);
+#pragma unroll
+                for (int x = 0; x < D / 8; x += 2) {
+                    const int key = warp * 16 + (mi & 1) * 8 + ri, oct = x + (mi >> 1);
+                    uint32_t b0, b1, b2, b3;
+                    ldmatrix_x4_trans(vbase + (oct >> 3) * C::kHalfBytes + sm_swz(key, oct & 7), b0, b1, b2, b3);
+                    mma_bf16_16816(o[x], pa, b0, b1);
+                    mma_bf16_16816(o[x + 1], pa, b2, b3);
+                }
+            }
+            __syncwarp();
+            if (lane == 0) mbar_arrive(&bars->empty[st]);
+        }
+#pragma unroll
+        for (int h = 0; h < 2; ++h) {
+            float l = l_run[h];
+            l += __shfl_xor_sync(0xffffffffu, l, 1);
+            l += __shfl_xor_sync(0xffffffffu, l, 2);
+            const int r = gq + 8 * h, part = it.part + warp * rows + r;
+            if (r >= rows || !ATTN_IN_BOUNDS(part < p.max_parts, p.status)) continue;
+            const float inv = l != 0.f ? 1.f / l : 0.f;
+            float* dst = p.part_o + static_cast<size_t>(part) * D + 2 * tq;
+#pragma unroll
+            for (int x = 0; x < D / 8; ++x)
+                *reinterpret_cast<float2*>(dst + 8 * x) = make_float2(o[x][2 * h] * inv, o[x][2 * h + 1] * inv);
+            if (tq == 0) p.part_lse[part] = l != 0.f ? m_run[h] + __log2f(l) : -INFINITY;
+        }
+    }
+}
+
+// kBehind: launched behind shared_attn_kernel, which lets this kernel start when the list is there.  Its
+// blocks take the SMs as that kernel's leave them, and end when it has ended, so that what waits for this
+// kernel waits for both.
+template <int D, bool kBehind>
+__global__ void __launch_bounds__(kSmThreads, 2) shared_small_kernel(const __grid_constant__ SharedParams p) {
+    using C = SmCfg<D>;
+    extern __shared__ uint8_t smem_raw[];
+    uint8_t* smem = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) &
+                                               ~static_cast<uintptr_t>(1023));
+    SmBars* bars = reinterpret_cast<SmBars*>(smem + C::kOffBar);
+    const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+    if (threadIdx.x == 0) {
+        for (int i = 0; i < C::kStages; ++i) {
+            mbar_init(&bars->full[i], 1);
+            mbar_init(&bars->empty[i], 4);
+        }
+        for (uint32_t i = 0; i < kShRing; ++i) {
+            mbar_init(&bars->idx_full[i], 1);
+            mbar_init(&bars->idx_empty[i], kSmReaders);
+        }
+        mbar_init(&bars->near_end, 1);
+        bars->abort_flag = 0;
+        mbar_fence_init();
+        tma_prefetch_desc(&p.tm_k64);
+        tma_prefetch_desc(&p.tm_v64);
+    }
+    __syncthreads();
+    if (!kBehind) griddep_wait();
+    griddep_launch_dependents();
+    const Watchdog wd{&bars->abort_flag, p.status};
+    if (warp < 4)
+        sm_consumer<D>(p, smem, bars, wd, warp, lane);
+    else if (warp == 4)
+        sm_producer<D>(p, smem, bars, wd, lane);
+    else
+        sh_scheduler<1, 1>(p, bars, wd, lane);
+    if (kBehind) griddep_wait();
+}
+
 // ---- merge --------------------------------------------------------------------------------------------
 
 // A block has one sequence's unit and one kv head, a warp one row at a time.  LSE = log2 sum_s 2^LSE_s,
-// O = sum_s 2^(LSE_s - LSE) O_s over the pieces of the row's own keys and of its prefix; no part, or none
+// O = sum_s 2^(LSE_s - LSE) O_s over the parts of the row's own keys and of its prefix; no part, or none
 // with a key: O = 0, LSE = -inf.
 template <int D>
 __global__ void __launch_bounds__(kShCombineThreads) shared_combine_kernel(const SharedParams p) {
-    griddep_wait();
+    // (the list is there when this kernel starts; the parts are when the one before it has ended)
     const int own = blockIdx.x, kvh = blockIdx.y;
     const SharedHeader* h = p.header;
-    if (h->bad || own >= h->n_own) return;
-    const SharedUnit& u = p.units[h->n_prefix + own];
+    const bool on = !h->bad && own < h->n_own;
+    const SharedUnit* u = p.units + p.own_base + own;
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
     constexpr int E = D / 32;
-    const int rows = u.rows, q0 = u.q0, n1 = u.pieces, prefix = u.prefix;
+    const int rows = on ? u->rows : 0, q0 = on ? u->q0 : 0, n1 = on ? u->pieces * u->split : 0;
+    const int prefix = on ? u->prefix : -1, group_q0 = on ? u->group_q0 : 0, part = on ? u->part : 0;
     const int per = 2 * p.tpt;
+    bool waited = false;
     for (int r = warp; r < rows; r += kShCombineThreads / 32) {
         const int tok = q0 + r / p.g, head = kvh * p.g + r % p.g;
-        const int base1 = u.part + kvh * n1 * rows + r;
+        const int base1 = part + kvh * n1 * rows + r;
         int n2 = 0, base2 = 0, step2 = 0;
         if (prefix >= 0) {
-            const int at = (tok - u.group_q0) / per;
-            const SharedUnit& v = p.units[prefix + at];
-            n2 = v.pieces;
-            step2 = v.rows;
-            base2 = v.part + kvh * n2 * step2 + (tok - v.q0) * p.g + r % p.g;
+            const SharedUnit* v = p.units + prefix + (tok - group_q0) / per;
+            n2 = v->pieces * v->split;
+            step2 = v->rows;
+            base2 = v->part + kvh * n2 * step2 + (tok - v->q0) * p.g + r % p.g;
         }
+        if (!waited) griddep_wait();
+        waited = true;
         const int n = n1 + n2;
         const auto row = [&](int s) -> size_t {
             return static_cast<size_t>(s < n2 ? base2 + s * step2 : base1 + (s - n2) * rows);
         };
+        // lane i has the LSE of part i (and i + 32, ...)
         float M = -INFINITY;
         bool nan = false;
         for (int s = lane; s < n; s += 32) {
@@ -891,7 +1202,7 @@ __global__ void __launch_bounds__(kShCombineThreads) shared_combine_kernel(const
         }
 #pragma unroll
         for (int o = 16; o > 0; o >>= 1) M = fmaxf(M, __shfl_xor_sync(0xffffffffu, M, o));
-        float acc[E];
+        float acc[E], sum = 0.f;
 #pragma unroll
         for (int e = 0; e < E; ++e) acc[e] = 0.f;
         float lse = -INFINITY;
@@ -900,18 +1211,12 @@ __global__ void __launch_bounds__(kShCombineThreads) shared_combine_kernel(const
 #pragma unroll
             for (int e = 0; e < E; ++e) acc[e] = lse;
         } else if (M != -INFINITY) {
-            float sum = 0.f;
-            for (int s = lane; s < n; s += 32) sum += ex2_approx(p.part_lse[row(s)] - M);
-#pragma unroll
-            for (int o = 16; o > 0; o >>= 1) sum += __shfl_xor_sync(0xffffffffu, sum, o);
-            lse = M + __log2f(sum);
-            const float inv = 1.f / sum;
             for (int s0 = 0; s0 < n; s0 += 4) {
                 float w[4], v[4][E];
 #pragma unroll
                 for (int i = 0; i < 4; ++i) {
                     const size_t at = row(min(s0 + i, n - 1));
-                    w[i] = s0 + i < n ? ex2_approx(p.part_lse[at] - M) * inv : 0.f;
+                    w[i] = s0 + i < n ? ex2_approx(p.part_lse[at] - M) : 0.f;
                     const float* src = p.part_o + at * D + lane * E;
                     if constexpr (E == 4) {
                         const float4 x = *reinterpret_cast<const float4*>(src);
@@ -922,11 +1227,17 @@ __global__ void __launch_bounds__(kShCombineThreads) shared_combine_kernel(const
                     }
                 }
 #pragma unroll
-                for (int i = 0; i < 4; ++i)
+                for (int i = 0; i < 4; ++i) {
+                    sum += w[i];
 #pragma unroll
                     for (int e = 0; e < E; ++e)
                         if (s0 + i < n) acc[e] = fmaf(w[i], v[i][e], acc[e]);
+                }
             }
+            lse = M + __log2f(sum);
+            const float inv = 1.f / sum;
+#pragma unroll
+            for (int e = 0; e < E; ++e) acc[e] *= inv;
         }
         if (!ATTN_IN_BOUNDS(tok < p.total_q && head < p.Hq, p.status)) continue;
         __nv_bfloat16* dst = p.out + (static_cast<size_t>(tok) * p.Hq + head) * D + lane * E;
@@ -937,6 +1248,7 @@ __global__ void __launch_bounds__(kShCombineThreads) shared_combine_kernel(const
         if (lane == 0)
             p.lse[static_cast<size_t>(head) * p.lse_head + static_cast<size_t>(tok) * p.lse_tok] = lse * kShLn2;
     }
+    if (!waited) griddep_wait();
 }
 
 template <typename Kernel>
@@ -959,20 +1271,39 @@ cudaError_t launch_dependent(Kernel kernel, dim3 grid, int threads, size_t smem,
 
 cudaError_t configure_shared_kernels() {
     const cudaFuncAttribute smem = cudaFuncAttributeMaxDynamicSharedMemorySize;
-    const cudaError_t e = cudaFuncSetAttribute(shared_attn_kernel<128>, smem, ShCfg<128>::kSmem);
-    return e != cudaSuccess ? e : cudaFuncSetAttribute(shared_attn_kernel<64>, smem, ShCfg<64>::kSmem);
+    cudaError_t e = cudaFuncSetAttribute(shared_attn_kernel<128>, smem, ShCfg<128>::kSmem);
+    if (e == cudaSuccess) e = cudaFuncSetAttribute(shared_attn_kernel<64>, smem, ShCfg<64>::kSmem);
+    if (e == cudaSuccess) e = cudaFuncSetAttribute(shared_small_kernel<128, false>, smem, SmCfg<128>::kSmem);
+    if (e == cudaSuccess) e = cudaFuncSetAttribute(shared_small_kernel<64, false>, smem, SmCfg<64>::kSmem);
+    if (e == cudaSuccess) e = cudaFuncSetAttribute(shared_small_kernel<128, true>, smem, SmCfg<128>::kSmem);
+    if (e == cudaSuccess) e = cudaFuncSetAttribute(shared_small_kernel<64, true>, smem, SmCfg<64>::kSmem);
+    return e;
 }
 
-cudaError_t launch_shared_attn(const SharedParams& p, int head_dim, int grid, int own_units, cudaStream_t stream) {
+namespace {
+
+template <int D>
+cudaError_t launch_shared_attn_d(const SharedParams& p, int num_sms, int own_units, cudaStream_t stream) {
     shared_units_kernel<<<1, kShUnitsThreads, 0, stream>>>(p);
     cudaError_t e = cudaGetLastError();
     if (e != cudaSuccess) return e;
-    const bool wide = head_dim == 128;
-    e = launch_dependent(wide ? shared_attn_kernel<128> : shared_attn_kernel<64>, dim3(grid), kFwdThreads,
-                         wide ? ShCfg<128>::kSmem : ShCfg<64>::kSmem, p, stream);
+    // (where all rows together are few, no unit has many)
+    const bool many = static_cast<long long>(p.total_q) * p.g > kSharedSmallRows;
+    if (many) {
+        e = launch_dependent(shared_attn_kernel<D>, dim3(num_sms), kFwdThreads, ShCfg<D>::kSmem, p, stream);
+        if (e != cudaSuccess) return e;
+    }
+    e = launch_dependent(many ? shared_small_kernel<D, true> : shared_small_kernel<D, false>, dim3(2 * num_sms),
+                         kSmThreads, SmCfg<D>::kSmem, p, stream);
     if (e != cudaSuccess) return e;
-    return launch_dependent(wide ? shared_combine_kernel<128> : shared_combine_kernel<64>,
-                            dim3(own_units, p.Hkv), kShCombineThreads, 0, p, stream);
+    return launch_dependent(shared_combine_kernel<D>, dim3(own_units, p.Hkv), kShCombineThreads, 0, p, stream);
+}
+
+}  // namespace
+
+cudaError_t launch_shared_attn(const SharedParams& p, int head_dim, int num_sms, int own_units, cudaStream_t stream) {
+    return head_dim == 128 ? launch_shared_attn_d<128>(p, num_sms, own_units, stream)
+                           : launch_shared_attn_d<64>(p, num_sms, own_units, stream);
 }
 
 }  // namespace attn

@@ -564,7 +564,7 @@ attn_status_t attn_kvcache_append_norm_rope(
  *   lse           device fp32, natural log: [batch, nheads_q] without cu_seqlens_q, else
  *                 [nheads_q, total_q]; rows outside every sequence are left as they were
  *   workspace     attn_decode_kvcache_shared_workspace_bytes(...) bytes, 256-byte aligned: the list of the
- *                 work and the partial results, about 8 total_q nheads_q head_dim bytes and 20 MB
+ *                 work and the partial results, about 20 total_q nheads_q head_dim bytes and 30 MB
  * The prefix is read through one row of block_table, that of a sequence of the group that has it whole; the
  * entries of the others' pages that end before the prefix does are not looked at.  (A page in which it ends may
  * be each sequence's own; what stands before the end is taken from that one row.)  A sequence some of
