@@ -60,7 +60,7 @@ __device__ __forceinline__ bool sh_behind(const ShSeq& s, int prefix) {
     return s.n > 0 && prefix > 0 && prefix <= s.keys - s.n + 1;
 }
 
-__device__ __forceinline__ int ceil_div(int a, int b) { return (a + b - 1) / b; }
+__host__ __device__ __forceinline__ int ceil_div(int a, int b) { return (a + b - 1) / b; }
 
 // This thread's place behind the earlier lanes' n on a counter in shared memory (one atomic a warp).
 __device__ __forceinline__ int sh_reserve(int* counter, int n, int lane) {
@@ -472,13 +472,9 @@ __device__ void sh_producer_loop(const SharedParams& p, uint8_t* smem, ShBars* b
         ++q_cnt;
         const int m = it.jhi - it.jlo;
         const int* bt = p.block_table + static_cast<size_t>(it.row) * p.max_pages;
-        for (int r = 0; r < 2 * m; ++r) {
-            // inverse of sh_pos_k / sh_pos_v
-            const bool last = r == 2 * m - 1;
-            const bool is_v = last || (r > 0 && (r & 1) == 0);
-            const int i = is_v ? (last ? m - 1 : (r - 2) / 2) : (r + 1) / 2;
-            // Boxes without a key of this unit (whose table entries are not read) and boxes of a bad page are
-            // aimed past the end of the cache: TMA fills them with zeros.
+        // The cache's row of this lane's box of block i.  Boxes without a key of this unit (whose table entries
+        // are not read) and boxes of a bad page are aimed past the end of the cache: TMA fills them with zeros.
+        const auto box_row = [&](int i) {
             int row = oob_row;
             if (lane < boxes) {
                 const int key = (it.jlo + i) * kFwdBlockN + lane * p.box_rows;
@@ -490,6 +486,14 @@ __device__ void sh_producer_loop(const SharedParams& p, uint8_t* smem, ShBars* b
                         atomicOr(p.status, kStatusBounds);
                 }
             }
+            return row;
+        };
+        for (int r = 0; r < 2 * m; ++r) {
+            // inverse of sh_pos_k / sh_pos_v
+            const bool last = r == 2 * m - 1;
+            const bool is_v = last || (r > 0 && (r & 1) == 0);
+            const int i = is_v ? (last ? m - 1 : (r - 2) / 2) : (r + 1) / 2;
+            const int row = box_row(i);
             if (r == max(0, 2 * m - 6) && lane == 0) mbar_arrive(&bars->near_end);
             const uint32_t n = ring.n, st = n % C::kSlots;
             if (!__all_sync(0xffffffffu, n < C::kSlots || wd.wait(&bars->kv_empty[st], ((n / C::kSlots) - 1) & 1)))
@@ -1160,95 +1164,96 @@ __global__ void __launch_bounds__(kSmThreads, 2) shared_small_kernel(const __gri
 
 // ---- merge --------------------------------------------------------------------------------------------
 
-// A block has one sequence's unit and one kv head, a warp one row at a time.  LSE = log2 sum_s 2^LSE_s,
-// O = sum_s 2^(LSE_s - LSE) O_s over the parts of the row's own keys and of its prefix; no part, or none
-// with a key: O = 0, LSE = -inf.
+// A warp has one row: block (i, h, j) rows [j, j + 1) * warps of sequence unit i's for kv head h.
+// LSE = log2 sum_s 2^LSE_s, O = sum_s 2^(LSE_s - LSE) O_s over the parts of the row's prefix and of its own
+// keys, a part's weight in a lane, eight parts' loads in flight; no part, or none with a key: O = 0,
+// LSE = -inf.
 template <int D>
 __global__ void __launch_bounds__(kShCombineThreads) shared_combine_kernel(const SharedParams p) {
     // (the list is there when this kernel starts; the parts are when the one before it has ended)
-    const int own = blockIdx.x, kvh = blockIdx.y;
+    const int own = blockIdx.x, kvh = blockIdx.y, lane = threadIdx.x & 31;
+    const int r = blockIdx.z * (blockDim.x >> 5) + (threadIdx.x >> 5);
     const SharedHeader* h = p.header;
-    const bool on = !h->bad && own < h->n_own;
     const SharedUnit* u = p.units + p.own_base + own;
-    const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+    const bool on = !h->bad && own < h->n_own && r < u->rows;
     constexpr int E = D / 32;
-    const int rows = on ? u->rows : 0, q0 = on ? u->q0 : 0, n1 = on ? u->pieces * u->split : 0;
-    const int prefix = on ? u->prefix : -1, group_q0 = on ? u->group_q0 : 0, part = on ? u->part : 0;
-    const int per = 2 * p.tpt;
-    bool waited = false;
-    for (int r = warp; r < rows; r += kShCombineThreads / 32) {
-        const int tok = q0 + r / p.g, head = kvh * p.g + r % p.g;
-        const int base1 = part + kvh * n1 * rows + r;
-        int n2 = 0, base2 = 0, step2 = 0;
-        if (prefix >= 0) {
-            const SharedUnit* v = p.units + prefix + (tok - group_q0) / per;
+    int n1 = 0, n2 = 0, base1 = 0, base2 = 0, step1 = 0, step2 = 0, tok = 0;
+    if (on) {
+        tok = u->q0 + r / p.g;
+        n1 = u->pieces * u->split;
+        step1 = u->rows;
+        base1 = u->part + kvh * n1 * step1 + r;
+        if (u->prefix >= 0) {
+            const SharedUnit* v = p.units + u->prefix + (tok - u->group_q0) / (2 * p.tpt);
             n2 = v->pieces * v->split;
             step2 = v->rows;
             base2 = v->part + kvh * n2 * step2 + (tok - v->q0) * p.g + r % p.g;
         }
-        if (!waited) griddep_wait();
-        waited = true;
-        const int n = n1 + n2;
-        const auto row = [&](int s) -> size_t {
-            return static_cast<size_t>(s < n2 ? base2 + s * step2 : base1 + (s - n2) * rows);
-        };
-        // lane i has the LSE of part i (and i + 32, ...)
-        float M = -INFINITY;
-        bool nan = false;
-        for (int s = lane; s < n; s += 32) {
-            const float x = p.part_lse[row(s)];
-            nan |= x != x;
-            M = fmaxf(M, x);
-        }
+    }
+    griddep_wait();
+    if (!on) return;
+    const int n = n1 + n2, head = kvh * p.g + r % p.g;
+    float M = -INFINITY, sum = 0.f, acc[E];
 #pragma unroll
-        for (int o = 16; o > 0; o >>= 1) M = fmaxf(M, __shfl_xor_sync(0xffffffffu, M, o));
-        float acc[E], sum = 0.f;
+    for (int e = 0; e < E; ++e) acc[e] = 0.f;
+    bool nan = false;
+    for (int s0 = 0; s0 < n; s0 += 32) {
+        const int s = s0 + lane;
+        const int at = s < n2 ? base2 + s * step2 : base1 + (min(s, n - 1) - n2) * step1;
+        const float x = s < n ? p.part_lse[at] : -INFINITY;
+        nan |= x != x;
+        float top = fmaxf(M, x);
 #pragma unroll
-        for (int e = 0; e < E; ++e) acc[e] = 0.f;
-        float lse = -INFINITY;
-        if (__any_sync(0xffffffffu, nan)) {
-            lse = __int_as_float(0x7fffffff);
+        for (int o = 16; o > 0; o >>= 1) top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, o));
+        if (top == -INFINITY) continue;  // no keys so far
+        const float keep = ex2_approx(M - top), w = ex2_approx(x - top);
+        M = top;
+        sum = sum * keep + w;  // (the lanes' parts)
 #pragma unroll
-            for (int e = 0; e < E; ++e) acc[e] = lse;
-        } else if (M != -INFINITY) {
-            for (int s0 = 0; s0 < n; s0 += 4) {
-                float w[4], v[4][E];
+        for (int e = 0; e < E; ++e) acc[e] *= keep;
+        const int many = min(32, n - s0);
+        for (int i0 = 0; i0 < many; i0 += 8) {
+            float v[8][E];
 #pragma unroll
-                for (int i = 0; i < 4; ++i) {
-                    const size_t at = row(min(s0 + i, n - 1));
-                    w[i] = s0 + i < n ? ex2_approx(p.part_lse[at] - M) : 0.f;
-                    const float* src = p.part_o + at * D + lane * E;
-                    if constexpr (E == 4) {
-                        const float4 x = *reinterpret_cast<const float4*>(src);
-                        v[i][0] = x.x, v[i][1] = x.y, v[i][2] = x.z, v[i][3] = x.w;
-                    } else {
-                        const float2 x = *reinterpret_cast<const float2*>(src);
-                        v[i][0] = x.x, v[i][1] = x.y;
-                    }
-                }
-#pragma unroll
-                for (int i = 0; i < 4; ++i) {
-                    sum += w[i];
-#pragma unroll
-                    for (int e = 0; e < E; ++e)
-                        if (s0 + i < n) acc[e] = fmaf(w[i], v[i][e], acc[e]);
+            for (int i = 0; i < 8; ++i) {
+                const int from = __shfl_sync(0xffffffffu, at, min(i0 + i, many - 1));
+                const float* src = p.part_o + static_cast<size_t>(from) * D + lane * E;
+                if constexpr (E == 4) {
+                    const float4 y = *reinterpret_cast<const float4*>(src);
+                    v[i][0] = y.x, v[i][1] = y.y, v[i][2] = y.z, v[i][3] = y.w;
+                } else {
+                    const float2 y = *reinterpret_cast<const float2*>(src);
+                    v[i][0] = y.x, v[i][1] = y.y;
                 }
             }
-            lse = M + __log2f(sum);
-            const float inv = 1.f / sum;
 #pragma unroll
-            for (int e = 0; e < E; ++e) acc[e] *= inv;
+            for (int i = 0; i < 8; ++i) {
+                const float wi = __shfl_sync(0xffffffffu, w, min(i0 + i, many - 1));
+#pragma unroll
+                for (int e = 0; e < E; ++e)
+                    if (i0 + i < many) acc[e] = fmaf(wi, v[i][e], acc[e]);
+            }
         }
-        if (!ATTN_IN_BOUNDS(tok < p.total_q && head < p.Hq, p.status)) continue;
-        __nv_bfloat16* dst = p.out + (static_cast<size_t>(tok) * p.Hq + head) * D + lane * E;
-        if constexpr (E == 4)
-            *reinterpret_cast<uint2*>(dst) = make_uint2(pack_bf16x2(acc[0], acc[1]), pack_bf16x2(acc[2], acc[3]));
-        else
-            *reinterpret_cast<uint32_t*>(dst) = pack_bf16x2(acc[0], acc[1]);
-        if (lane == 0)
-            p.lse[static_cast<size_t>(head) * p.lse_head + static_cast<size_t>(tok) * p.lse_tok] = lse * kShLn2;
     }
-    if (!waited) griddep_wait();
+#pragma unroll
+    for (int o = 16; o > 0; o >>= 1) sum += __shfl_xor_sync(0xffffffffu, sum, o);
+    const float inv = sum == 0.f ? 0.f : 1.f / sum;
+    float lse = sum == 0.f ? -INFINITY : M + __log2f(sum);
+#pragma unroll
+    for (int e = 0; e < E; ++e) acc[e] *= inv;
+    if (__any_sync(0xffffffffu, nan)) {
+        lse = __int_as_float(0x7fffffff);
+#pragma unroll
+        for (int e = 0; e < E; ++e) acc[e] = lse;
+    }
+    if (!ATTN_IN_BOUNDS(tok < p.total_q && head < p.Hq, p.status)) return;
+    __nv_bfloat16* dst = p.out + (static_cast<size_t>(tok) * p.Hq + head) * D + lane * E;
+    if constexpr (E == 4)
+        *reinterpret_cast<uint2*>(dst) = make_uint2(pack_bf16x2(acc[0], acc[1]), pack_bf16x2(acc[2], acc[3]));
+    else
+        *reinterpret_cast<uint32_t*>(dst) = pack_bf16x2(acc[0], acc[1]);
+    if (lane == 0)
+        p.lse[static_cast<size_t>(head) * p.lse_head + static_cast<size_t>(tok) * p.lse_tok] = lse * kShLn2;
 }
 
 template <typename Kernel>
@@ -1296,7 +1301,10 @@ cudaError_t launch_shared_attn_d(const SharedParams& p, int num_sms, int own_uni
     e = launch_dependent(many ? shared_small_kernel<D, true> : shared_small_kernel<D, false>, dim3(2 * num_sms),
                          kSmThreads, SmCfg<D>::kSmem, p, stream);
     if (e != cudaSuccess) return e;
-    return launch_dependent(shared_combine_kernel<D>, dim3(own_units, p.Hkv), kShCombineThreads, 0, p, stream);
+    const int rows = (p.max_seqlen_q < 2 * p.tpt ? p.max_seqlen_q : 2 * p.tpt) * p.g;  // of a unit, at most
+    const int warps = rows < kShCombineThreads / 32 ? rows : kShCombineThreads / 32;
+    return launch_dependent(shared_combine_kernel<D>, dim3(own_units, p.Hkv, ceil_div(rows, warps)), 32 * warps, 0, p,
+                            stream);
 }
 
 }  // namespace
