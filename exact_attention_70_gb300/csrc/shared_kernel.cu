@@ -213,11 +213,12 @@ __global__ void __launch_bounds__(kShUnitsThreads) shared_units_kernel(const Sha
     const bool fits = n_pre <= p.own_base && p.own_base + own <= p.max_units;
     const int n_units = fits ? n_pre + own : 0;
     int share[2];
+    float per_share[2];  // bins a key block
 #pragma unroll
     for (int k = 0; k < 2; ++k) {
-        const int shares = k ? kSharedSmallShares : kSharedShares;
-        share[k] = static_cast<int>(max((static_cast<long long>(work[k]) * p.Hkv + shares - 1) / shares,
-                                        static_cast<long long>(kShMinPiece)));
+        const unsigned long long shares = k ? kSharedSmallShares : kSharedShares;
+        share[k] = max(static_cast<int>((work[k] * p.Hkv + shares - 1) / shares), kShMinPiece);
+        per_share[k] = static_cast<float>(kShBins) / static_cast<float>(share[k]);
     }
     // a unit's pieces and the list's bin of their length
     const auto cut = [&](int i, int& u, int& few, int& pieces, int& rows, int& bin) {
@@ -230,7 +231,7 @@ __global__ void __launch_bounds__(kShUnitsThreads) shared_units_kernel(const Sha
         if (pieces > 0) {
             const int len = ceil_div(x.x, pieces);  // 1 .. share
             bin = few * kShBins + kShBins - 1 -
-                  static_cast<int>(static_cast<long long>(len - 1) * kShBins / share[few]);
+                  min(static_cast<int>(static_cast<float>(len - 1) * per_share[few]), kShBins - 1);
         }
     };
     // 3. pieces, and the places of their results
@@ -1164,19 +1165,23 @@ __global__ void __launch_bounds__(kSmThreads, 2) shared_small_kernel(const __gri
 
 // ---- merge --------------------------------------------------------------------------------------------
 
-// A warp has one row: block (i, h, j) rows [j, j + 1) * warps of sequence unit i's for kv head h.
-// LSE = log2 sum_s 2^LSE_s, O = sum_s 2^(LSE_s - LSE) O_s over the parts of the row's prefix and of its own
-// keys, a part's weight in a lane, eight parts' loads in flight; no part, or none with a key: O = 0,
-// LSE = -inf.
+// Four warps have a row, eight parts each at a time, whose loads all go out together: block (i, h, j) has rows
+// 2 j and 2 j + 1 of sequence unit i for kv head h.  LSE = log2 sum_s 2^LSE_s, O = sum_s 2^(LSE_s - LSE) O_s
+// over the parts of the row's prefix and of its own keys; no part, or none with a key: O = 0, LSE = -inf.
+// Bound by the latency of the parts' loads: 2048 rows of 22 parts took 9 us with a warp a row, three times
+// eight parts one after the other.
 template <int D>
 __global__ void __launch_bounds__(kShCombineThreads) shared_combine_kernel(const SharedParams p) {
+    constexpr int E = D / 32, kWarps = 4, kBatch = 8;
+    __shared__ float4 s_acc[2][kWarps][32];
+    __shared__ float s_max[2][kWarps], s_sum[2][kWarps];
     // (the list is there when this kernel starts; the parts are when the one before it has ended)
     const int own = blockIdx.x, kvh = blockIdx.y, lane = threadIdx.x & 31;
-    const int r = blockIdx.z * (blockDim.x >> 5) + (threadIdx.x >> 5);
+    const int half = threadIdx.x >> 7, w = (threadIdx.x >> 5) & 3, r = 2 * blockIdx.z + half;
     const SharedHeader* h = p.header;
     const SharedUnit* u = p.units + p.own_base + own;
-    const bool on = !h->bad && own < h->n_own && r < u->rows;
-    constexpr int E = D / 32;
+    const bool some = !h->bad && own < h->n_own && 2 * blockIdx.z < u->rows;  // the same for the block
+    const bool on = some && r < u->rows;
     int n1 = 0, n2 = 0, base1 = 0, base2 = 0, step1 = 0, step2 = 0, tok = 0;
     if (on) {
         tok = u->q0 + r / p.g;
@@ -1191,69 +1196,81 @@ __global__ void __launch_bounds__(kShCombineThreads) shared_combine_kernel(const
         }
     }
     griddep_wait();
-    if (!on) return;
-    const int n = n1 + n2, head = kvh * p.g + r % p.g;
+    if (!some) return;
+    const int n = n1 + n2;
     float M = -INFINITY, sum = 0.f, acc[E];
 #pragma unroll
     for (int e = 0; e < E; ++e) acc[e] = 0.f;
     bool nan = false;
-    for (int s0 = 0; s0 < n; s0 += 32) {
-        const int s = s0 + lane;
-        const int at = s < n2 ? base2 + s * step2 : base1 + (min(s, n - 1) - n2) * step1;
-        const float x = s < n ? p.part_lse[at] : -INFINITY;
-        nan |= x != x;
-        float top = fmaxf(M, x);
+    for (int s0 = w * kBatch; s0 < n; s0 += kWarps * kBatch) {
+        float x[kBatch], v[kBatch][E];
 #pragma unroll
-        for (int o = 16; o > 0; o >>= 1) top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, o));
-        if (top == -INFINITY) continue;  // no keys so far
-        const float keep = ex2_approx(M - top), w = ex2_approx(x - top);
-        M = top;
-        sum = sum * keep + w;  // (the lanes' parts)
-#pragma unroll
-        for (int e = 0; e < E; ++e) acc[e] *= keep;
-        const int many = min(32, n - s0);
-        for (int i0 = 0; i0 < many; i0 += 8) {
-            float v[8][E];
-#pragma unroll
-            for (int i = 0; i < 8; ++i) {
-                const int from = __shfl_sync(0xffffffffu, at, min(i0 + i, many - 1));
-                const float* src = p.part_o + static_cast<size_t>(from) * D + lane * E;
-                if constexpr (E == 4) {
-                    const float4 y = *reinterpret_cast<const float4*>(src);
-                    v[i][0] = y.x, v[i][1] = y.y, v[i][2] = y.z, v[i][3] = y.w;
-                } else {
-                    const float2 y = *reinterpret_cast<const float2*>(src);
-                    v[i][0] = y.x, v[i][1] = y.y;
-                }
-            }
-#pragma unroll
-            for (int i = 0; i < 8; ++i) {
-                const float wi = __shfl_sync(0xffffffffu, w, min(i0 + i, many - 1));
-#pragma unroll
-                for (int e = 0; e < E; ++e)
-                    if (i0 + i < many) acc[e] = fmaf(wi, v[i][e], acc[e]);
+        for (int i = 0; i < kBatch; ++i) {
+            const int s = min(s0 + i, n - 1);
+            const int at = s < n2 ? base2 + s * step2 : base1 + (s - n2) * step1;
+            x[i] = p.part_lse[at];
+            const float* src = p.part_o + static_cast<size_t>(at) * D + lane * E;
+            if constexpr (E == 4) {
+                const float4 y = *reinterpret_cast<const float4*>(src);
+                v[i][0] = y.x, v[i][1] = y.y, v[i][2] = y.z, v[i][3] = y.w;
+            } else {
+                const float2 y = *reinterpret_cast<const float2*>(src);
+                v[i][0] = y.x, v[i][1] = y.y;
             }
         }
+        float top = M;
+#pragma unroll
+        for (int i = 0; i < kBatch; ++i) {
+            if (s0 + i >= n) x[i] = -INFINITY;
+            nan = nan || x[i] != x[i];
+            top = fmaxf(top, x[i]);
+        }
+        if (top == -INFINITY) continue;  // no keys so far
+        const float keep = ex2_approx(M - top);
+        M = top;
+        sum *= keep;
+#pragma unroll
+        for (int e = 0; e < E; ++e) acc[e] *= keep;
+#pragma unroll
+        for (int i = 0; i < kBatch; ++i) {
+            const float wi = ex2_approx(x[i] - M);
+            sum += wi;
+            if (s0 + i >= n) continue;  // (no part: not even times 0)
+#pragma unroll
+            for (int e = 0; e < E; ++e) acc[e] = fmaf(wi, v[i][e], acc[e]);
+        }
     }
+    if (nan) sum = __int_as_float(0x7fffffff);  // (the warps' parts are the same in all lanes)
+    if (lane == 0) s_max[half][w] = M, s_sum[half][w] = sum;
+    float4 mine = make_float4(acc[0], acc[1], 0.f, 0.f);
+    if constexpr (E == 4) mine.z = acc[2], mine.w = acc[3];
+    s_acc[half][w][lane] = mine;
+    __syncthreads();
+    if (w != 0 || !on) return;
+    float top = -INFINITY;
 #pragma unroll
-    for (int o = 16; o > 0; o >>= 1) sum += __shfl_xor_sync(0xffffffffu, sum, o);
-    const float inv = sum == 0.f ? 0.f : 1.f / sum;
-    float lse = sum == 0.f ? -INFINITY : M + __log2f(sum);
+    for (int i = 0; i < kWarps; ++i) top = fmaxf(top, s_max[half][i]);
+    const float ref = top == -INFINITY ? 0.f : top;
+    float4 o = make_float4(0.f, 0.f, 0.f, 0.f);
+    sum = 0.f;
 #pragma unroll
-    for (int e = 0; e < E; ++e) acc[e] *= inv;
-    if (__any_sync(0xffffffffu, nan)) {
-        lse = __int_as_float(0x7fffffff);
-#pragma unroll
-        for (int e = 0; e < E; ++e) acc[e] = lse;
+    for (int i = 0; i < kWarps; ++i) {
+        const float wi = ex2_approx(s_max[half][i] - ref);
+        const float4 a = s_acc[half][i][lane];
+        sum += wi * s_sum[half][i];
+        o = make_float4(fmaf(wi, a.x, o.x), fmaf(wi, a.y, o.y), fmaf(wi, a.z, o.z), fmaf(wi, a.w, o.w));
     }
+    const int head = kvh * p.g + r % p.g;
+    const float inv = sum == 0.f ? 0.f : 1.f / sum;  // (a NaN stays one)
     if (!ATTN_IN_BOUNDS(tok < p.total_q && head < p.Hq, p.status)) return;
     __nv_bfloat16* dst = p.out + (static_cast<size_t>(tok) * p.Hq + head) * D + lane * E;
     if constexpr (E == 4)
-        *reinterpret_cast<uint2*>(dst) = make_uint2(pack_bf16x2(acc[0], acc[1]), pack_bf16x2(acc[2], acc[3]));
+        *reinterpret_cast<uint2*>(dst) = make_uint2(pack_bf16x2(o.x * inv, o.y * inv), pack_bf16x2(o.z * inv, o.w * inv));
     else
-        *reinterpret_cast<uint32_t*>(dst) = pack_bf16x2(acc[0], acc[1]);
+        *reinterpret_cast<uint32_t*>(dst) = pack_bf16x2(o.x * inv, o.y * inv);
     if (lane == 0)
-        p.lse[static_cast<size_t>(head) * p.lse_head + static_cast<size_t>(tok) * p.lse_tok] = lse * kShLn2;
+        p.lse[static_cast<size_t>(head) * p.lse_head + static_cast<size_t>(tok) * p.lse_tok] =
+            sum == 0.f ? -INFINITY : (ref + __log2f(sum)) * kShLn2;
 }
 
 template <typename Kernel>
@@ -1302,9 +1319,8 @@ cudaError_t launch_shared_attn_d(const SharedParams& p, int num_sms, int own_uni
                          kSmThreads, SmCfg<D>::kSmem, p, stream);
     if (e != cudaSuccess) return e;
     const int rows = (p.max_seqlen_q < 2 * p.tpt ? p.max_seqlen_q : 2 * p.tpt) * p.g;  // of a unit, at most
-    const int warps = rows < kShCombineThreads / 32 ? rows : kShCombineThreads / 32;
-    return launch_dependent(shared_combine_kernel<D>, dim3(own_units, p.Hkv, ceil_div(rows, warps)), 32 * warps, 0, p,
-                            stream);
+    return launch_dependent(shared_combine_kernel<D>, dim3(own_units, p.Hkv, ceil_div(rows, 2)), kShCombineThreads, 0,
+                            p, stream);
 }
 
 }  // namespace
