@@ -81,30 +81,36 @@ __device__ __forceinline__ bool sh_few(int rows) { return rows <= kSharedSmallRo
 // no result does.  Items of a kind come longest pieces first (kShBins lengths), the kv heads of a piece
 // side by side (their keys lie side by side in the cache).
 __global__ void __launch_bounds__(kShUnitsThreads) shared_units_kernel(const SharedParams p) {
-    __shared__ int4 s_groups[kShFast];
+    __shared__ int4 s_groups[kShFast];  // {first unit or -1, first token, first sequence, prefix}
     __shared__ int2 s_lengths[2 * kShFast];
+    __shared__ int s_q0[kShFast], s_n[kShFast], s_keys[kShFast];
     __shared__ int hist[2 * kShBins];
     __shared__ unsigned long long work[2];  // key blocks of both kinds, for one kv head
     __shared__ int n_prefix, n_own, n_parts;
     const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
     griddep_launch_dependents();  // (the attention kernels wait for the list, behind their set-up)
     // (generic addresses: shared memory as far as it goes)
-    int4* const groups = p.n_groups <= kShFast ? s_groups : p.groups;      // {first sequence, sequences, -, -}
+    int4* const groups = p.n_groups <= kShFast ? s_groups : p.groups;
+    const bool near = p.batch <= kShFast;
     int2* const lengths = p.max_units <= 2 * kShFast ? s_lengths : p.lengths;
     const long long max_keys = static_cast<long long>(p.max_pages) * p.page_size;
     if (tid < 2 * kShBins) hist[tid] = 0;
     if (tid < 2) work[tid] = 0;
     if (tid == 0) n_prefix = n_own = n_parts = 0;
     bool bad = false;
-    for (int b = tid; b < p.batch; b += kShUnitsThreads) {
-        const ShSeq s = sh_seq(p, b);
+    for (int base = 0; base < max(p.batch, p.n_groups); base += kShUnitsThreads) {
+        const int b = base + tid;
+        const bool is_group = b < p.n_groups, is_seq = b < p.batch;
+        int s0 = 0, s1 = 0, P = 0;
+        ShSeq s = {0, 0, 0};
+        if (is_seq) s = sh_seq(p, b);  // (all loads go out together)
+        if (is_group) s0 = p.group_starts[b], s1 = p.group_starts[b + 1], P = p.prefix_lens[b];
         bad |= s.q0 < 0 || s.n < 0 || s.n > p.max_seqlen_q || static_cast<long long>(s.q0) + s.n > p.total_q ||
                s.keys < 0 || s.keys > max_keys;
-    }
-    for (int i = tid; i < p.n_groups; i += kShUnitsThreads) {
-        const int s0 = p.group_starts[i], s1 = p.group_starts[i + 1];
-        bad |= s0 < 0 || s1 < s0 || s1 > p.batch || (i == 0 && s0 != 0) ||
-               (i == p.n_groups - 1 && s1 != p.batch) || p.prefix_lens[i] < 0;
+        bad |= is_group && (s0 < 0 || s1 < s0 || s1 > p.batch || (b == 0 && s0 != 0) ||
+                            (b == p.n_groups - 1 && s1 != p.batch) || P < 0);
+        if (is_seq && near) s_q0[b] = s.q0, s_n[b] = s.n, s_keys[b] = s.keys;
+        if (is_group) groups[b] = make_int4(-1, 0, s0, P);
     }
     if (__syncthreads_or(bad)) {
         if (tid == 0) {
@@ -115,24 +121,27 @@ __global__ void __launch_bounds__(kShUnitsThreads) shared_units_kernel(const Sha
         }
         return;
     }
+    const auto seq = [&](int b) { return near ? ShSeq{s_q0[b], s_n[b], s_keys[b]} : sh_seq(p, b); };
     const int per = 2 * p.tpt;  // tokens a unit
+    const auto units_of = [&](int tokens) { return tokens <= per ? (tokens > 0 ? 1 : 0) : ceil_div(tokens, per); };
     // 1. a warp a group: which row of the table leads to the prefix, which tokens meet it, their units
     for (int i = warp; i < p.n_groups; i += kShUnitsThreads / 32) {
-        const int s0 = p.group_starts[i], s1 = p.group_starts[i + 1], P = p.prefix_lens[i];
+        const int s0 = groups[i].z, P = groups[i].w;
+        const int s1 = i + 1 < p.n_groups ? groups[i + 1].z : p.batch;
         int first = -1, count = 0;
         if (P >= kShMinPrefix) {
             for (int b = s0; b < s1; b += 32) {
-                const bool on = b + lane < s1 && sh_behind(sh_seq(p, b + lane), P);
+                const bool on = b + lane < s1 && sh_behind(seq(b + lane), P);
                 const unsigned m = __ballot_sync(0xffffffffu, on);
                 if (first < 0 && m != 0) first = b + __ffs(m) - 1;
                 count += __popc(m);
             }
         }
-        int at = -1, q0 = 0;
         if (count > 1) {
-            const ShSeq a = sh_seq(p, s0), z = sh_seq(p, s1 - 1);
-            q0 = a.q0;
-            const int tokens = z.q0 + z.n - q0, n = ceil_div(tokens, per), nblk = ceil_div(P, kFwdBlockN);
+            int at = 0;
+            const ShSeq a = seq(s0), z = seq(s1 - 1);
+            const int q0 = a.q0;
+            const int tokens = z.q0 + z.n - q0, n = units_of(tokens), nblk = ceil_div(P, kFwdBlockN);
             if (lane == 0) at = atomicAdd(&n_prefix, n);
             at = __shfl_sync(0xffffffffu, at, 0);
             for (int u = lane; u < n; u += 32) {
@@ -154,8 +163,9 @@ __global__ void __launch_bounds__(kShUnitsThreads) shared_units_kernel(const Sha
                     lengths[at + u] = make_int2(nblk, x.rows);
                 }
             }
+            // (only x and y: other warps read z meanwhile)
+            if (lane == 0) *reinterpret_cast<int2*>(&groups[i]) = make_int2(at, q0);
         }
-        if (lane == 0) groups[i] = make_int4(at, q0, 0, 0);
     }
     __syncthreads();
     // 2. a thread a sequence: the keys that its group's prefix leaves to it
@@ -163,20 +173,20 @@ __global__ void __launch_bounds__(kShUnitsThreads) shared_units_kernel(const Sha
     for (int base = 0; base < p.batch; base += kShUnitsThreads) {
         const int b = base + tid;
         ShSeq s = {0, 0, 0};
-        if (b < p.batch) s = sh_seq(p, b);
-        const int n = ceil_div(s.n, per);
+        if (b < p.batch) s = seq(b);
+        const int n = units_of(s.n);
         int prefix = -1, group_q0 = 0, key_min = 0;
         if (n > 0 && p.n_groups > 0) {
             int lo = 0, hi = p.n_groups - 1;  // the last group that starts at b or before
             while (lo < hi) {
                 const int mid = (lo + hi + 1) >> 1;
-                if (p.group_starts[mid] <= b) lo = mid; else hi = mid - 1;
+                if (groups[mid].z <= b) lo = mid; else hi = mid - 1;
             }
             const int4 r = groups[lo];
-            if (r.x >= 0 && sh_behind(s, p.prefix_lens[lo])) {
+            if (r.x >= 0 && sh_behind(s, r.w)) {
                 prefix = r.x;
                 group_q0 = r.y;
-                key_min = p.prefix_lens[lo];
+                key_min = r.w;
             }
         }
         const int at = p.own_base + sh_reserve(&n_own, n, lane);
@@ -226,10 +236,10 @@ __global__ void __launch_bounds__(kShUnitsThreads) shared_units_kernel(const Sha
         const int2 x = lengths[u];
         few = sh_few(x.y);
         rows = x.y;
-        pieces = ceil_div(x.x, share[few]);
+        pieces = x.x <= share[few] ? (x.x > 0 ? 1 : 0) : ceil_div(x.x, share[few]);
         bin = 0;
         if (pieces > 0) {
-            const int len = ceil_div(x.x, pieces);  // 1 .. share
+            const int len = pieces == 1 ? x.x : ceil_div(x.x, pieces);  // 1 .. share
             bin = few * kShBins + kShBins - 1 -
                   min(static_cast<int>(static_cast<float>(len - 1) * per_share[few]), kShBins - 1);
         }
@@ -290,7 +300,10 @@ __global__ void __launch_bounds__(kShUnitsThreads) shared_units_kernel(const Sha
             const int src = __ffs(m) - 1;
             const int from = __shfl_sync(0xffffffffu, at, src), n = __shfl_sync(0xffffffffu, count, src);
             const int unit = __shfl_sync(0xffffffffu, u, src);
-            for (int i = lane; i < n; i += 32) p.items[from + i] = make_int2(unit, (i / p.Hkv) << 16 | i % p.Hkv);
+            for (int i = lane, s = lane / p.Hkv, h = lane - s * p.Hkv; i < n; i += 32) {
+                p.items[from + i] = make_int2(unit, s << 16 | h);
+                for (h += 32; h >= p.Hkv; h -= p.Hkv) ++s;
+            }
         }
     }
 }
