@@ -1502,8 +1502,7 @@ attn_status_t norm_rope_params(NormRopeParams& p, const void* q, const void* k, 
     if (total == 0) return ATTN_OK;
     if (!q || !k || (rotary_dim > 0 && !positions)) return ATTN_ERR_INVALID_ARG;
     if (!stride_ok(q_stride, nheads_q, head_dim) || !stride_ok(k_stride, nheads_kv, head_dim) ||
-        !aligned(q, 16) || !aligned(k, 16) || !aligned(q_weight, weight_fp32 ? 4 : 2) ||
-        !aligned(k_weight, weight_fp32 ? 4 : 2))
+        !aligned(q, 16) || !aligned(k, 16) || !aligned(q_weight, 16) || !aligned(k_weight, 16))
         return ATTN_ERR_INVALID_ARG;
     p.q = static_cast<const __nv_bfloat16*>(q);
     p.k = static_cast<const __nv_bfloat16*>(k);

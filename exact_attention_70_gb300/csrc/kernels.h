@@ -318,7 +318,7 @@ cudaError_t launch_plan(const PlanParams& p, cudaStream_t stream);
 // ---- norms of queries and keys with the rotation ------------------------------------------------
 
 constexpr int kNrAxes = 3;
-constexpr int kNrBwdBlocks = kGb300Sms * 4;  // blocks (partial sums of the weights' gradients) of the backward
+constexpr int kNrBwdBlocks = kGb300Sms * 2;  // blocks (partial sums of the weights' gradients) of the backward
 
 struct NormRopeParams {
     const __nv_bfloat16* q;  // [total, Hq, d], q_stride elements between tokens

@@ -13,6 +13,8 @@
 // rotary_dim: 8 l .. 8 l + 7).
 #include <cuda_bf16.h>
 
+#include <algorithm>
+
 #include "kernels.h"
 #include "ptx.cuh"
 
@@ -21,6 +23,7 @@ namespace attn {
 namespace {
 
 constexpr int kNrThreads = 256;
+constexpr int kNrFwdBlocksPerSm = 4, kNrFwdRows = 4;
 // Sums of squares from kFarSum on are taken again, of x times kFarUnit (128 elements of 2^128 sum to 2^115).
 constexpr float kFarSum = 0x1p120f, kFarUnit = 0x1p-70f;
 
@@ -67,21 +70,30 @@ __device__ __forceinline__ Lane lane_of(const NormRopeParams& p, int l) {
     return s;
 }
 
-// Cosines and sines of the lane's four planes at token t (false: a position outside the tables).
-__device__ __forceinline__ bool load_turn(const NormRopeParams& p, const Lane& s, int t, float* c, float* sn) {
+// A token's positions: fetched a token ahead, since the tables' rows and all that follows wait for them.
+struct Rows {
+    int r[kNrAxes];
+};
+
+__device__ __forceinline__ Rows load_rows(const NormRopeParams& p, long long t) {
+    Rows x;
+#pragma unroll
+    for (int a = 0; a < kNrAxes; ++a)
+        x.r[a] = p.rot_dim > 0 && a < p.axes && t < p.total ? __ldg(p.positions + static_cast<size_t>(a) * p.total + t) : 0;
+    return x;
+}
+
+// Cosines and sines of the lane's four planes.  False: a position outside the tables.
+__device__ __forceinline__ bool load_turn(const NormRopeParams& p, const Lane& s, const Rows& x, float* c, float* sn) {
     if (p.rot_dim == 0) return true;
-    int row[4];
     bool ok = true;
 #pragma unroll
-    for (int a = 0; a < kNrAxes; ++a) {
-        row[a] = a < p.axes ? __ldg(p.positions + static_cast<size_t>(a) * p.total + t) : 0;
-        ok = ok && row[a] >= 0 && row[a] < p.rot_rows;
-    }
+    for (int a = 0; a < kNrAxes; ++a) ok = ok && x.r[a] >= 0 && x.r[a] < p.rot_rows;
     if (!ok || !s.turns) return ok;
     const int half = p.rot_dim / 2;
     const unsigned axes = (p.plane_axis[s.plane >> 4] >> (2 * (s.plane & 15))) & 0xffu;
-    if (axes == 0u) {  // (all planes with one axis)
-        const size_t at = static_cast<size_t>(row[0]) * half + s.plane;
+    if (axes == 0u) {  // (all planes with the first axis)
+        const size_t at = static_cast<size_t>(x.r[0]) * half + s.plane;
         const float4 cv = __ldg(reinterpret_cast<const float4*>(p.rot_cos + at));
         const float4 sv = __ldg(reinterpret_cast<const float4*>(p.rot_sin + at));
         c[0] = cv.x, c[1] = cv.y, c[2] = cv.z, c[3] = cv.w;
@@ -90,7 +102,7 @@ __device__ __forceinline__ bool load_turn(const NormRopeParams& p, const Lane& s
 #pragma unroll
         for (int i = 0; i < 4; ++i) {
             const unsigned a = (axes >> (2 * i)) & 3u;
-            const int r = a == 0u ? row[0] : a == 1u ? row[1] : row[2];
+            const int r = a == 0u ? x.r[0] : a == 1u ? x.r[1] : x.r[2];
             const size_t at = static_cast<size_t>(r) * half + s.plane + i;
             c[i] = __ldg(p.rot_cos + at);
             sn[i] = __ldg(p.rot_sin + at);
@@ -113,9 +125,23 @@ __device__ __forceinline__ void turn(float (&x)[8], const float* c, const float*
     }
 }
 
-__device__ __forceinline__ float load_weight(const void* w, bool f32, int i) {
-    return f32 ? __ldg(static_cast<const float*>(w) + i)
-               : __bfloat162float(__ldg(static_cast<const __nv_bfloat16*>(w) + i));
+// The lane's eight weights (ones without a norm).
+__device__ __forceinline__ void load_weights(const void* w, bool f32, const Lane& s, float (&out)[8]) {
+    if (w == nullptr) {
+#pragma unroll
+        for (int i = 0; i < 8; ++i) out[i] = 1.f;
+    } else if (f32) {
+#pragma unroll
+        for (int i = 0; i < 2; ++i) {
+            const float4 x = __ldg(reinterpret_cast<const float4*>(static_cast<const float*>(w) + (i ? s.o1 : s.o0)));
+            out[4 * i] = x.x, out[4 * i + 1] = x.y, out[4 * i + 2] = x.z, out[4 * i + 3] = x.w;
+        }
+    } else {
+#pragma unroll
+        for (int i = 0; i < 2; ++i)
+            unpack4(__ldg(reinterpret_cast<const uint2*>(static_cast<const __nv_bfloat16*>(w) + (i ? s.o1 : s.o0))),
+                    out + 4 * i);
+    }
 }
 
 // The blocks' division: kind 0 (queries), 1 (keys), 2 (values).
@@ -134,64 +160,58 @@ __device__ __forceinline__ Kind kind_of(const NormRopeParams& p) {
     return k;
 }
 
-// A group of D / 8 << par_log2 threads does one token at a time, 1 << par_log2 of its heads side by
-// side and kRows of a thread's rows in flight.
+// Forward: no block has more than one token a group, so that many small blocks hide one another's latency
+// (persistent blocks that ask for a step's rows a step ahead, as the backward's do, took 72.9 us for the 16384
+// tokens where these take 56.7).  The rows' loads go out before those of the positions, on which the tables wait.
 template <int D, bool kInter, bool kAppend>
-__global__ void __launch_bounds__(kNrThreads) norm_rope_kernel(const NormRopeParams p) {
-    constexpr int kLanes = D / 8, kRows = 4;
+__global__ void __launch_bounds__(kNrThreads, kNrFwdBlocksPerSm) norm_rope_kernel(const NormRopeParams p) {
+    constexpr int kLanes = D / 8, kRows = kNrFwdRows;
     const Kind k = kind_of(p);
     const int l = threadIdx.x % kLanes;
     const int group_log2 = (D == 128 ? 4 : 3) + k.par_log2;  // threads a token
     const int par = 1 << k.par_log2, head0 = (threadIdx.x / kLanes) & (par - 1);
     const int t = k.block * (kNrThreads >> group_log2) + (threadIdx.x >> group_log2);
     const Lane s = lane_of<D, kInter>(p, l);
-    const bool isv = kAppend && k.kind == 2, isk = k.kind == 1;
-    const void* wp = isv ? nullptr : isk ? p.k_weight : p.q_weight;
-    bool live = t < p.total;
-    float c[4], sn[4];
-    __nv_bfloat16* dst = isk ? p.k_out : p.q_out;
-    size_t row0 = static_cast<size_t>(live ? t : 0) * k.heads;
-    if (live) {
-        live = load_turn(p, s, t, c, sn);
-        if (!live && head0 == 0 && l == 0) atomicOr(p.status, kStatusBounds);
-        if (kAppend) {
-            const int slot = __ldg(p.slots + t);
-            const bool to_cache = isk || isv;
-            if (slot >= p.cache_rows) {
-                if (head0 == 0 && l == 0) atomicOr(p.status, kStatusBounds);
-                if (to_cache) live = false;
-            }
-            if (to_cache) {
-                if (slot < 0) live = false;
-                row0 = static_cast<size_t>(live ? slot : 0) * k.heads;
-                dst = isv ? p.v_cache : p.k_cache;
-            }
-        }
-    }
-    float w[8];
-#pragma unroll
-    for (int i = 0; i < 8; ++i) w[i] = 1.f;
-    if (wp != nullptr) {
-#pragma unroll
-        for (int i = 0; i < 4; ++i) {
-            w[i] = load_weight(wp, p.weight_f32, s.o0 + i);
-            w[i + 4] = load_weight(wp, p.weight_f32, s.o1 + i);
-        }
-    }
+    const bool isv = kAppend && k.kind == 2, isk = k.kind == 1, to_cache = kAppend && k.kind != 0;
+    const bool here = t < p.total, first = head0 == 0 && l == 0;
     const __nv_bfloat16* src = isv ? p.v : isk ? p.k : p.q;
-    src += static_cast<size_t>(live ? t : 0) * (isv ? p.v_stride : isk ? p.k_stride : p.q_stride);
-    for (int h0 = 0; h0 < k.heads; h0 += par * kRows) {  // (the same count for a warp's threads)
-        uint2 raw[kRows][2];
+    src += static_cast<size_t>(here ? t : 0) * (isv ? p.v_stride : isk ? p.k_stride : p.q_stride);
+    uint2 raw[kRows][2];
+    const auto fetch = [&](int h0) {
 #pragma unroll
         for (int u = 0; u < kRows; ++u) {
-            const int h = h0 + u * par + head0;
-            const bool on = live && h < k.heads;
+            const int h = h0 + u * par;
+            const bool on = here && h < k.heads;
             raw[u][0] = on ? ld_row8(src + h * D + s.o0) : make_uint2(0u, 0u);
             raw[u][1] = on ? ld_row8(src + h * D + s.o1) : make_uint2(0u, 0u);
         }
+    };
+    fetch(head0);
+    const Rows rows = load_rows(p, t);
+    const int slot = kAppend && here ? __ldg(p.slots + t) : 0;
+    const void* wp = isv ? nullptr : isk ? p.k_weight : p.q_weight;
+    float w[8];
+    load_weights(wp, p.weight_f32, s, w);
+    float c[4], sn[4];
+    bool live = here;
+    if (here) {
+        live = load_turn(p, s, rows, c, sn);
+        if (!live && first) atomicOr(p.status, kStatusBounds);
+    }
+    __nv_bfloat16* dst = !to_cache ? (isk ? p.k_out : p.q_out) : isv ? p.v_cache : p.k_cache;
+    size_t row0 = static_cast<size_t>(here ? t : 0) * k.heads;
+    if (kAppend) {
+        if (slot >= p.cache_rows && first) atomicOr(p.status, kStatusBounds);
+        if (to_cache) {
+            live = live && slot >= 0 && slot < p.cache_rows;
+            row0 = static_cast<size_t>(live ? slot : 0) * k.heads;
+        }
+    }
+    dst += row0 * D;
+    for (int h0 = head0;;) {  // (the same count for all threads of the block)
 #pragma unroll
         for (int u = 0; u < kRows; ++u) {
-            const int h = h0 + u * par + head0;
+            const int h = h0 + u * par;
             float x[8];
             unpack4(raw[u][0], x);
             unpack4(raw[u][1], x + 4);
@@ -216,119 +236,161 @@ __global__ void __launch_bounds__(kNrThreads) norm_rope_kernel(const NormRopePar
                 for (int i = 0; i < 8; ++i) x[i] *= r * w[i];
             }
             if (!isv && s.turns) turn<kInter, false>(x, c, sn);
-            if (live && h < k.heads) {
-                __nv_bfloat16* out = dst + (row0 + h) * D;
-                if (ATTN_IN_BOUNDS(row0 + h < static_cast<size_t>(kAppend && k.kind != 0 ? p.cache_rows : p.total) * k.heads,
-                                   p.status)) {
-                    *reinterpret_cast<uint2*>(out + s.o0) = isv ? raw[u][0] : pack4(x);
-                    *reinterpret_cast<uint2*>(out + s.o1) = isv ? raw[u][1] : pack4(x + 4);
-                }
+            if (live && h < k.heads &&
+                ATTN_IN_BOUNDS(row0 + h < static_cast<size_t>(to_cache ? p.cache_rows : p.total) * k.heads, p.status)) {
+                *reinterpret_cast<uint2*>(dst + h * D + s.o0) = isv ? raw[u][0] : pack4(x);
+                *reinterpret_cast<uint2*>(dst + h * D + s.o1) = isv ? raw[u][1] : pack4(x + 4);
             }
         }
+        h0 += par * kRows;
+        if (h0 - head0 >= k.heads) break;
+        fetch(h0);
     }
 }
 
-// Persistent blocks: each sums its share of dw in registers, then over its rows in shared memory, into
-// a row of its own of part_w; norm_rope_dw_kernel adds the rows.  Fixed shares, so the sums' order too.
+// The walk of a group of D / 8 << par_log2 threads over its tokens: 1 << par_log2 heads side by side, kRows of
+// a thread's rows at a time (a step).  What a step reads is asked for a step ahead.
+struct Walk {
+    long long t, stride;  // this group's token; from one token to its next
+    long long t0;         // the block's first group's: the same for all threads of the block
+    int h;                // the step's first head
+
+    __device__ __forceinline__ bool on(const NormRopeParams& p) const { return t0 < p.total; }
+    __device__ __forceinline__ bool step(int heads, int by) {  // true: another token
+        h += by;
+        if (h < heads) return false;
+        h = 0;
+        t += stride;
+        t0 += stride;
+        return true;
+    }
+};
+
+// Each block sums its share of dw in registers, then over its rows in shared memory, into a row of its own of
+// part_w; norm_rope_dw_kernel adds the rows.  Fixed shares, so the sums' order too.
 template <int D, bool kInter>
-__global__ void __launch_bounds__(kNrThreads) norm_rope_bwd_kernel(const NormRopeParams p) {
+__global__ void __launch_bounds__(kNrThreads, 2) norm_rope_bwd_kernel(const NormRopeParams p) {
     constexpr int kLanes = D / 8, kRows = 2;
     __shared__ float sums[kNrThreads / kLanes][D];
     griddep_launch_dependents();
     const Kind k = kind_of(p);
     const int l = threadIdx.x % kLanes;
     const int group_log2 = (D == 128 ? 4 : 3) + k.par_log2;
-    const int par = 1 << k.par_log2, head0 = (threadIdx.x / kLanes) & (par - 1);
+    const int par = 1 << k.par_log2, head0 = (threadIdx.x / kLanes) & (par - 1), by = par * kRows;
     const int groups = kNrThreads >> group_log2;
     const Lane s = lane_of<D, kInter>(p, l);
-    const bool isk = k.kind == 1;
+    const bool isk = k.kind == 1, first = head0 == 0 && l == 0;
     const void* wp = isk ? p.k_weight : p.q_weight;
     const __nv_bfloat16* x_all = isk ? p.k : p.q;
     const __nv_bfloat16* g_all = isk ? p.dk_out : p.dq_out;
     __nv_bfloat16* dx_all = isk ? p.dk : p.dq;
     const int x_stride = isk ? p.k_stride : p.q_stride, dx_stride = isk ? p.dk_stride : p.dq_stride;
-    float w[8], dw[8];
+    Walk w;
+    w.t0 = static_cast<long long>(k.block) * groups;
+    w.t = w.t0 + (threadIdx.x >> group_log2);
+    w.stride = static_cast<long long>(k.blocks) * groups;
+    w.h = head0;
+    uint2 rx[kRows][2], rg[kRows][2];
+    const auto fetch = [&](const Walk& y) {
+        const __nv_bfloat16* xr = x_all + static_cast<size_t>(y.t) * x_stride + static_cast<size_t>(y.h) * D;
+        const __nv_bfloat16* gr = g_all + (static_cast<size_t>(y.t) * k.heads + y.h) * D;
 #pragma unroll
-    for (int i = 0; i < 8; ++i) w[i] = 1.f, dw[i] = 0.f;
-    if (wp != nullptr) {
-#pragma unroll
-        for (int i = 0; i < 4; ++i) {
-            w[i] = load_weight(wp, p.weight_f32, s.o0 + i);
-            w[i + 4] = load_weight(wp, p.weight_f32, s.o1 + i);
+        for (int u = 0; u < kRows; ++u) {
+            const bool on = y.t < p.total && y.h + u * par < k.heads;
+            const size_t at = static_cast<size_t>(u * par) * D;
+            const uint2 z = make_uint2(0u, 0u);
+            rg[u][0] = on ? ld_row8(gr + at + s.o0) : z;
+            rg[u][1] = on ? ld_row8(gr + at + s.o1) : z;
+            rx[u][0] = on && wp != nullptr ? ld_row8(xr + at + s.o0) : z;
+            rx[u][1] = on && wp != nullptr ? ld_row8(xr + at + s.o1) : z;
         }
-    }
-    for (long long t0 = static_cast<long long>(k.block) * groups; t0 < p.total;
-         t0 += static_cast<long long>(k.blocks) * groups) {
-        const long long tl = t0 + (threadIdx.x >> group_log2);
-        bool live = tl < p.total;
-        const int t = live ? static_cast<int>(tl) : 0;
-        float c[4], sn[4];
-        if (live) {
-            live = load_turn(p, s, t, c, sn);
-            if (!live && head0 == 0 && l == 0) atomicOr(p.status, kStatusBounds);
-        }
-        const __nv_bfloat16* xt = x_all + static_cast<size_t>(t) * x_stride;
-        const __nv_bfloat16* gt = g_all + static_cast<size_t>(t) * k.heads * D;
-        __nv_bfloat16* dxt = dx_all + static_cast<size_t>(t) * dx_stride;
-        for (int h0 = 0; h0 < k.heads; h0 += par * kRows) {
-            uint2 rx[kRows][2], rg[kRows][2];
+    };
+    float c[4], sn[4];
+    const auto enter = [&](long long t, const Rows& x) {
+        if (t >= p.total) return false;
+        const bool live = load_turn(p, s, x, c, sn);
+        if (!live && first) atomicOr(p.status, kStatusBounds);
+        return live;
+    };
+    fetch(w);
+    Rows rows = load_rows(p, w.t);
+    float wt[8], dw[8];
+    load_weights(wp, p.weight_f32, s, wt);
 #pragma unroll
-            for (int u = 0; u < kRows; ++u) {
-                const int h = h0 + u * par + head0;
-                const bool on = live && h < k.heads;
-                const uint2 z = make_uint2(0u, 0u);
-                rg[u][0] = on ? ld_row8(gt + h * D + s.o0) : z;
-                rg[u][1] = on ? ld_row8(gt + h * D + s.o1) : z;
-                rx[u][0] = on && wp != nullptr ? ld_row8(xt + h * D + s.o0) : z;
-                rx[u][1] = on && wp != nullptr ? ld_row8(xt + h * D + s.o1) : z;
+    for (int i = 0; i < 8; ++i) dw[i] = 0.f;
+    bool live = enter(w.t, rows);
+    rows = load_rows(p, w.t + w.stride);
+    while (w.on(p)) {
+        uint2 nx[kRows][2], ng[kRows][2];
+#pragma unroll
+        for (int u = 0; u < kRows; ++u)
+#pragma unroll
+            for (int i = 0; i < 2; ++i) nx[u][i] = rx[u][i], ng[u][i] = rg[u][i];
+        Walk next = w;
+        const bool other = next.step(k.heads + head0, by);
+        if (other) next.h = head0;
+        if (next.on(p)) fetch(next);
+        __nv_bfloat16* dxt = dx_all + static_cast<size_t>(w.t < p.total ? w.t : 0) * dx_stride;
+#pragma unroll
+        for (int u = 0; u < kRows; ++u) {
+            const int h = w.h + u * par;
+            const bool on = live && h < k.heads;
+            float g[8];
+            unpack4(ng[u][0], g);
+            unpack4(ng[u][1], g + 4);
+            if (!on) {  // (a token outside the tables gives nothing)
+#pragma unroll
+                for (int i = 0; i < 8; ++i) g[i] = 0.f;
+            } else if (s.turns) {
+                turn<kInter, true>(g, c, sn);
             }
+            if (wp != nullptr) {
+                float x[8], ss = 0.f, xh = 0.f;
+                unpack4(nx[u][0], x);
+                unpack4(nx[u][1], x + 4);
+                if (!on) {
 #pragma unroll
-            for (int u = 0; u < kRows; ++u) {
-                const int h = h0 + u * par + head0;
-                const bool on = live && h < k.heads;
-                float g[8];
-                unpack4(rg[u][0], g);
-                unpack4(rg[u][1], g + 4);
-                if (s.turns && on) turn<kInter, true>(g, c, sn);
-                if (wp != nullptr) {
-                    float x[8], ss = 0.f, xh = 0.f;
-                    unpack4(rx[u][0], x);
-                    unpack4(rx[u][1], x + 4);
+                    for (int i = 0; i < 8; ++i) x[i] = 0.f;
+                }
+#pragma unroll
+                for (int i = 0; i < 8; ++i) {
+                    ss = fmaf(x[i], x[i], ss);
+                    xh = fmaf(x[i], wt[i] * g[i], xh);
+                }
+                ss = row_sum<kLanes>(ss);
+                xh = row_sum<kLanes>(xh);
+                float eps = p.eps, unit = 1.f;
+                const bool far = !(ss < kFarSum);
+                if (__any_sync(0xffffffffu, far)) {
+                    float s2 = 0.f, xh2 = 0.f;
 #pragma unroll
                     for (int i = 0; i < 8; ++i) {
-                        ss = fmaf(x[i], x[i], ss);
-                        xh = fmaf(x[i], w[i] * g[i], xh);
+                        x[i] *= far ? kFarUnit : 1.f;
+                        s2 = fmaf(x[i], x[i], s2);
+                        xh2 = fmaf(x[i], wt[i] * g[i], xh2);
                     }
-                    ss = row_sum<kLanes>(ss);
-                    xh = row_sum<kLanes>(xh);
-                    float eps = p.eps, unit = 1.f;
-                    const bool far = !(ss < kFarSum);
-                    if (__any_sync(0xffffffffu, far)) {
-                        float s2 = 0.f, xh2 = 0.f;
-#pragma unroll
-                        for (int i = 0; i < 8; ++i) {
-                            x[i] *= far ? kFarUnit : 1.f;
-                            s2 = fmaf(x[i], x[i], s2);
-                            xh2 = fmaf(x[i], w[i] * g[i], xh2);
-                        }
-                        s2 = row_sum<kLanes>(s2);
-                        xh2 = row_sum<kLanes>(xh2);
-                        if (far) ss = s2, xh = xh2, eps = p.eps * kFarUnit * kFarUnit, unit = kFarUnit;
-                    }
-                    const float r = rsqrtf(fmaf(ss, 1.f / D, eps));
-                    const float m = xh * r * (1.f / D);
-#pragma unroll
-                    for (int i = 0; i < 8; ++i) {
-                        const float n = x[i] * r;
-                        dw[i] = fmaf(n, g[i], dw[i]);
-                        g[i] = r * (w[i] * g[i] - n * m) * unit;
-                    }
+                    s2 = row_sum<kLanes>(s2);
+                    xh2 = row_sum<kLanes>(xh2);
+                    if (far) ss = s2, xh = xh2, eps = p.eps * kFarUnit * kFarUnit, unit = kFarUnit;
                 }
-                if (on) {
-                    *reinterpret_cast<uint2*>(dxt + h * D + s.o0) = pack4(g);
-                    *reinterpret_cast<uint2*>(dxt + h * D + s.o1) = pack4(g + 4);
+                const float r = rsqrtf(fmaf(ss, 1.f / D, eps));
+                const float m = xh * r * (1.f / D);
+#pragma unroll
+                for (int i = 0; i < 8; ++i) {
+                    const float n = x[i] * r;
+                    dw[i] = fmaf(n, g[i], dw[i]);
+                    g[i] = r * (wt[i] * g[i] - n * m) * unit;
                 }
             }
+            if (on) {
+                *reinterpret_cast<uint2*>(dxt + static_cast<size_t>(h) * D + s.o0) = pack4(g);
+                *reinterpret_cast<uint2*>(dxt + static_cast<size_t>(h) * D + s.o1) = pack4(g + 4);
+            }
+        }
+        w = next;
+        if (other && w.on(p)) {
+            live = enter(w.t, rows);
+            rows = load_rows(p, w.t + w.stride);
         }
     }
     if (wp == nullptr) return;
@@ -366,26 +428,35 @@ __global__ void __launch_bounds__(1024) norm_rope_dw_kernel(const NormRopeParams
 }
 
 // Heads side by side (a power of two): all of a token's where there are few tokens, and fewer, so that
-// a thread does up to 8 rows with the same table entries, while threads enough remain.
-int par_of(long long total, int heads, int d) {
+// a thread does up to `most_rows` rows with the same table entries, while threads enough remain.
+int par_of(long long total, int heads, int d, int most_rows) {
     const int most = d == 128 ? 4 : 5;
     int par = 0;
     while (par < most && (1 << par) < heads) ++par;
-    while (par > 0 && (heads >> par) < 8 && ((total * (d / 8)) << (par - 1)) >= kGb300Sms * 2048ll) --par;
+    while (par > 0 && (heads >> par) < most_rows && ((total * (d / 8)) << (par - 1)) >= kGb300Sms * 2048ll) --par;
     return par;
+}
+
+// Blocks of the kinds of rows: as many as there are tokens for, or a share of `most` that follows the rows.
+int divide(NormRopeParams& p, int kinds, int head_dim, long long most, int most_rows) {
+    const long long rows = p.Hq + static_cast<long long>(kinds - 1) * p.Hkv;
+    int grid = 0;
+    for (int k = 0; k < 3; ++k) {
+        const int heads = k == 0 ? p.Hq : p.Hkv;
+        p.par_log2[k] = par_of(p.total, heads, head_dim, most_rows);
+        const int tokens = kNrThreads / (head_dim / 8) >> p.par_log2[k];  // a block
+        const long long need = (static_cast<long long>(p.total) + tokens - 1) / tokens;
+        const long long share = std::max(1ll, most * heads / rows);
+        p.blocks[k] = k < kinds ? static_cast<int>(std::min(need, share)) : 0;
+        grid += p.blocks[k];
+    }
+    return grid;
 }
 
 }  // namespace
 
 cudaError_t launch_norm_rope(NormRopeParams p, int head_dim, bool append, cudaStream_t stream) {
-    int grid = 0;
-    for (int k = 0; k < 3; ++k) {
-        const int heads = k == 0 ? p.Hq : p.Hkv;
-        p.par_log2[k] = par_of(p.total, heads, head_dim);
-        const int tokens = kNrThreads / (head_dim / 8) >> p.par_log2[k];  // a block
-        p.blocks[k] = k == 2 && !append ? 0 : (p.total + tokens - 1) / tokens;
-        grid += p.blocks[k];
-    }
+    const int grid = divide(p, append ? 3 : 2, head_dim, 1ll << 31, 16);
     const auto go = [&](auto kernel) {
         kernel<<<grid, kNrThreads, 0, stream>>>(p);
         return cudaGetLastError();
@@ -399,20 +470,7 @@ cudaError_t launch_norm_rope(NormRopeParams p, int head_dim, bool append, cudaSt
 }
 
 cudaError_t launch_norm_rope_bwd(NormRopeParams p, int head_dim, cudaStream_t stream) {
-    // the blocks' shares of queries and keys follow their rows
-    long long most[2];
-    for (int k = 0; k < 2; ++k) {
-        const int heads = k == 0 ? p.Hq : p.Hkv;
-        p.par_log2[k] = par_of(p.total, heads, head_dim);
-        const int tokens = kNrThreads / (head_dim / 8) >> p.par_log2[k];
-        most[k] = (static_cast<long long>(p.total) + tokens - 1) / tokens;
-    }
-    const long long keys = static_cast<long long>(kNrBwdBlocks) * p.Hkv / (p.Hq + p.Hkv);
-    p.blocks[1] = static_cast<int>(most[1] < keys ? most[1] : keys > 1 ? keys : 1);
-    const long long queries = kNrBwdBlocks - (keys > 1 ? keys : 1);
-    p.blocks[0] = static_cast<int>(most[0] < queries ? most[0] : queries);
-    p.blocks[2] = 0;
-    const int grid = p.blocks[0] + p.blocks[1];
+    const int grid = divide(p, 2, head_dim, kNrBwdBlocks, 8);
     const auto go = [&](auto kernel) {
         kernel<<<grid, kNrThreads, 0, stream>>>(p);
         return cudaGetLastError();

@@ -475,7 +475,8 @@ size_t attn_kvcache_plan_workspace_bytes(int batch);
  *   q, k          device bf16 [total, nheads_q, head_dim], [total, nheads_kv, head_dim]; q_stride, k_stride
  *                 elements between tokens (multiples of 8, at least nheads * head_dim: parts of the rows
  *                 of one projection will do); 16-byte aligned
- *   q_weight, k_weight   device [head_dim] w, fp32 with weight_fp32, else bf16; NULL: no norm (x rstd w is x)
+ *   q_weight, k_weight   device [head_dim] w, fp32 with weight_fp32, else bf16, 16-byte aligned; NULL: no
+ *                 norm (x rstd w is x)
  *   eps           finite and >= 2^-64 (not looked at without weights)
  *   rotary_cos, rotary_sin   device fp32 [rotary_rows, rotary_dim / 2], 16-byte aligned; planes as for
  *                 attn_fwd_kvcache; rotary_dim a multiple of 16 up to head_dim, 0: no rotation (the

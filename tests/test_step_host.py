@@ -121,7 +121,7 @@ def test_norm_rope_bwd_refusals(lib):
     for bad in (dict(ws=None), dict(wsb=16), dict(ws=P(4096 + 16))):
         assert call(gq=FAKE, **bad) == -3, bad
     norm_rope_refusals(lambda **kw: call(**({"dqw": None, "dkw": None} if kw.get("total") == 0 else {}), **kw))
-    assert binding.load().attn_qk_norm_rope_bwd_workspace_bytes(128) == 608 * 128 * 4
+    assert binding.load().attn_qk_norm_rope_bwd_workspace_bytes(128) == 304 * 128 * 4
     assert binding.load().attn_qk_norm_rope_bwd_workspace_bytes(96) == 0
 
 
