@@ -44,6 +44,25 @@ __device__ __forceinline__ uint2 pack4(const float* f) {
     return make_uint2(pack_bf16x2(f[0], f[1]), pack_bf16x2(f[2], f[3]));
 }
 
+// The same as two pairs for the paired fp32 instructions, and back.
+__device__ __forceinline__ void unpack_pairs(uint2 v, uint64_t* f) {
+    f[0] = f2_make(__uint_as_float(v.x << 16), __uint_as_float(v.x & 0xffff0000u));
+    f[1] = f2_make(__uint_as_float(v.y << 16), __uint_as_float(v.y & 0xffff0000u));
+}
+
+__device__ __forceinline__ uint2 pack_pairs(const uint64_t* f) {
+    float a, b, c, d;
+    f2_split(f[0], a, b);
+    f2_split(f[1], c, d);
+    return make_uint2(pack_bf16x2(a, b), pack_bf16x2(c, d));
+}
+
+__device__ __forceinline__ float f2_sum(uint64_t v) {
+    float a, b;
+    f2_split(v, a, b);
+    return a + b;
+}
+
 // The sum over a row's lanes.
 template <int kLanes>
 __device__ __forceinline__ float row_sum(float x) {
@@ -122,6 +141,28 @@ __device__ __forceinline__ void turn(float (&x)[8], const float* c, const float*
         const float ra = a * c[i] - b * s, rb = a * s + b * c[i];
         a = ra;
         b = rb;
+    }
+}
+
+// R^T of the lane's elements, in pairs.
+template <bool kInter>
+__device__ __forceinline__ void turn_back(uint64_t (&x)[4], const float* c, const float* sn) {
+    if (kInter) {
+        float f[8];
+#pragma unroll
+        for (int i = 0; i < 4; ++i) f2_split(x[i], f[2 * i], f[2 * i + 1]);
+        turn<true, true>(f, c, sn);
+#pragma unroll
+        for (int i = 0; i < 4; ++i) x[i] = f2_make(f[2 * i], f[2 * i + 1]);
+    } else {
+#pragma unroll
+        for (int i = 0; i < 2; ++i) {
+            const uint64_t c2 = f2_make(c[2 * i], c[2 * i + 1]), s2 = f2_make(sn[2 * i], sn[2 * i + 1]);
+            const uint64_t n2 = f2_make(-sn[2 * i], -sn[2 * i + 1]);
+            const uint64_t a = f2_fma(x[i], c2, f2_mul(x[i + 2], s2)), b = f2_fma(x[i], n2, f2_mul(x[i + 2], c2));
+            x[i] = a;
+            x[i + 2] = b;
+        }
     }
 }
 
@@ -271,7 +312,7 @@ struct Walk {
 template <int D, bool kInter>
 __global__ void __launch_bounds__(kNrThreads, 2) norm_rope_bwd_kernel(const NormRopeParams p) {
     constexpr int kLanes = D / 8, kRows = 2;
-    __shared__ float sums[kNrThreads / kLanes][D];
+    __shared__ __align__(16) float sums[kNrThreads / kLanes][D];
     griddep_launch_dependents();
     const Kind k = kind_of(p);
     const int l = threadIdx.x % kLanes;
@@ -314,10 +355,13 @@ __global__ void __launch_bounds__(kNrThreads, 2) norm_rope_bwd_kernel(const Norm
     };
     fetch(w);
     Rows rows = load_rows(p, w.t);
-    float wt[8], dw[8];
-    load_weights(wp, p.weight_f32, s, wt);
+    uint64_t wt[4], dw[4];  // pairs of the lane's elements
+    {
+        float x[8];
+        load_weights(wp, p.weight_f32, s, x);
 #pragma unroll
-    for (int i = 0; i < 8; ++i) dw[i] = 0.f;
+        for (int i = 0; i < 4; ++i) wt[i] = f2_make(x[2 * i], x[2 * i + 1]), dw[i] = 0;
+    }
     bool live = enter(w.t, rows);
     rows = load_rows(p, w.t + w.stride);
     while (w.on(p)) {
@@ -331,60 +375,54 @@ __global__ void __launch_bounds__(kNrThreads, 2) norm_rope_bwd_kernel(const Norm
         if (other) next.h = head0;
         if (next.on(p)) fetch(next);
         __nv_bfloat16* dxt = dx_all + static_cast<size_t>(w.t < p.total ? w.t : 0) * dx_stride;
+        const bool all = __all_sync(0xffffffffu, live || w.t >= p.total);
 #pragma unroll
         for (int u = 0; u < kRows; ++u) {
             const int h = w.h + u * par;
             const bool on = live && h < k.heads;
-            float g[8];
-            unpack4(ng[u][0], g);
-            unpack4(ng[u][1], g + 4);
-            if (!on) {  // (a token outside the tables gives nothing)
-#pragma unroll
-                for (int i = 0; i < 8; ++i) g[i] = 0.f;
-            } else if (s.turns) {
-                turn<kInter, true>(g, c, sn);
-            }
+            uint64_t g[4];
+            unpack_pairs(ng[u][0], g);
+            unpack_pairs(ng[u][1], g + 2);
+            if (!all && !live) g[0] = g[1] = g[2] = g[3] = 0;  // (a token outside the tables gives nothing)
+            if (s.turns && on) turn_back<kInter>(g, c, sn);
             if (wp != nullptr) {
-                float x[8], ss = 0.f, xh = 0.f;
-                unpack4(nx[u][0], x);
-                unpack4(nx[u][1], x + 4);
-                if (!on) {
+                uint64_t x[4], hg[4], s2 = 0, d2 = 0;
+                unpack_pairs(nx[u][0], x);
+                unpack_pairs(nx[u][1], x + 2);
+                if (!all && !live) x[0] = x[1] = x[2] = x[3] = 0;
 #pragma unroll
-                    for (int i = 0; i < 8; ++i) x[i] = 0.f;
+                for (int i = 0; i < 4; ++i) {
+                    hg[i] = f2_mul(wt[i], g[i]);
+                    s2 = f2_fma(x[i], x[i], s2);
+                    d2 = f2_fma(x[i], hg[i], d2);
                 }
-#pragma unroll
-                for (int i = 0; i < 8; ++i) {
-                    ss = fmaf(x[i], x[i], ss);
-                    xh = fmaf(x[i], wt[i] * g[i], xh);
-                }
-                ss = row_sum<kLanes>(ss);
-                xh = row_sum<kLanes>(xh);
+                float ss = row_sum<kLanes>(f2_sum(s2)), xh = row_sum<kLanes>(f2_sum(d2));
                 float eps = p.eps, unit = 1.f;
                 const bool far = !(ss < kFarSum);
                 if (__any_sync(0xffffffffu, far)) {
-                    float s2 = 0.f, xh2 = 0.f;
+                    const uint64_t f2 = far ? f2_make(kFarUnit, kFarUnit) : f2_make(1.f, 1.f);
+                    s2 = d2 = 0;
 #pragma unroll
-                    for (int i = 0; i < 8; ++i) {
-                        x[i] *= far ? kFarUnit : 1.f;
-                        s2 = fmaf(x[i], x[i], s2);
-                        xh2 = fmaf(x[i], wt[i] * g[i], xh2);
+                    for (int i = 0; i < 4; ++i) {
+                        x[i] = f2_mul(x[i], f2);
+                        s2 = f2_fma(x[i], x[i], s2);
+                        d2 = f2_fma(x[i], hg[i], d2);
                     }
-                    s2 = row_sum<kLanes>(s2);
-                    xh2 = row_sum<kLanes>(xh2);
-                    if (far) ss = s2, xh = xh2, eps = p.eps * kFarUnit * kFarUnit, unit = kFarUnit;
+                    const float t2 = row_sum<kLanes>(f2_sum(s2)), e2 = row_sum<kLanes>(f2_sum(d2));
+                    if (far) ss = t2, xh = e2, eps = p.eps * kFarUnit * kFarUnit, unit = kFarUnit;
                 }
-                const float r = rsqrtf(fmaf(ss, 1.f / D, eps));
-                const float m = xh * r * (1.f / D);
+                const float r = rsqrtf(fmaf(ss, 1.f / D, eps)), m = -xh * r * (1.f / D), ru = r * unit;
+                const uint64_t r2 = f2_make(r, r), m2 = f2_make(m, m), u2 = f2_make(ru, ru);
 #pragma unroll
-                for (int i = 0; i < 8; ++i) {
-                    const float n = x[i] * r;
-                    dw[i] = fmaf(n, g[i], dw[i]);
-                    g[i] = r * (wt[i] * g[i] - n * m) * unit;
+                for (int i = 0; i < 4; ++i) {
+                    const uint64_t n = f2_mul(x[i], r2);
+                    dw[i] = f2_fma(n, g[i], dw[i]);
+                    g[i] = f2_mul(u2, f2_fma(n, m2, hg[i]));
                 }
             }
             if (on) {
-                *reinterpret_cast<uint2*>(dxt + static_cast<size_t>(h) * D + s.o0) = pack4(g);
-                *reinterpret_cast<uint2*>(dxt + static_cast<size_t>(h) * D + s.o1) = pack4(g + 4);
+                *reinterpret_cast<uint2*>(dxt + static_cast<size_t>(h) * D + s.o0) = pack_pairs(g);
+                *reinterpret_cast<uint2*>(dxt + static_cast<size_t>(h) * D + s.o1) = pack_pairs(g + 2);
             }
         }
         w = next;
@@ -396,9 +434,9 @@ __global__ void __launch_bounds__(kNrThreads, 2) norm_rope_bwd_kernel(const Norm
     if (wp == nullptr) return;
     const int r = threadIdx.x / kLanes;
 #pragma unroll
-    for (int i = 0; i < 4; ++i) {
-        sums[r][s.o0 + i] = dw[i];
-        sums[r][s.o1 + i] = dw[i + 4];
+    for (int i = 0; i < 2; ++i) {
+        *reinterpret_cast<uint64_t*>(&sums[r][s.o0 + 2 * i]) = dw[i];
+        *reinterpret_cast<uint64_t*>(&sums[r][s.o1 + 2 * i]) = dw[i + 2];
     }
     __syncthreads();
     if (threadIdx.x < D) {
