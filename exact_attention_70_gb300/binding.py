@@ -99,7 +99,7 @@ def load():
             lib.attn_kvcache_plan.restype = i32
             lib.attn_kvcache_plan.argtypes = [P] * 10 + [i32] * 6 + [P, sz, P]
             lib.attn_kvcache_plan_workspace_bytes.restype = sz
-            lib.attn_kvcache_plan_workspace_bytes.argtypes = [i32]
+            lib.attn_kvcache_plan_workspace_bytes.argtypes = [i32, i32]
             lib.attn_qk_norm_rope.restype = i32
             lib.attn_qk_norm_rope.argtypes = [P, P, i64, i64] + how + [P, P] + [i32] * 4 + [P]
             lib.attn_qk_norm_rope_bwd.restype = i32
@@ -845,8 +845,11 @@ def _device_index(t, name):
     return t.get_device()
 
 
-def attn_kvcache_plan_workspace_bytes(batch) -> int:
-    return int(load().attn_kvcache_plan_workspace_bytes(batch))
+def attn_kvcache_plan_workspace_bytes(batch, total_q) -> int:
+    return int(load().attn_kvcache_plan_workspace_bytes(batch, total_q))
+
+
+_PLAN_OUTPUTS = ("cu_seqlens_q", "seqlens_after", "positions", "slot_map", "free_left")
 
 
 def attn_kvcache_plan(cache_seqlens, new_lens, block_table, free_pages, free_count, page_size,
@@ -862,36 +865,47 @@ def attn_kvcache_plan(cache_seqlens, new_lens, block_table, free_pages, free_cou
     cache_seqlens.
     """
     lib = load()
-    index = _device_index(block_table, "block_table")
-    table = _step_tensor(block_table, "block_table", _I32, (None, None), index)
-    batch, max_pages = block_table.shape
     total, ps, pages = _int32(total_q, "total_q"), _int32(page_size, "page_size"), _int32(num_pages, "num_pages")
-    held = _step_tensor(cache_seqlens, "cache_seqlens", _I32, (batch,), index)
-    new = _step_tensor(new_lens, "new_lens", _I32, (batch,), index)
-    free = _step_tensor(free_pages, "free_pages", _I32, (None,), index)
-    count = _step_tensor(free_count, "free_count", _I32, (1,), index)
+    try:
+        batch, max_pages = block_table.shape
+        index = block_table.get_device()
+        ok = (index >= 0 and cache_seqlens.shape == new_lens.shape == (batch,) and free_count.shape == (1,)
+              and cache_seqlens.dtype is _I32 and new_lens.dtype is _I32 and block_table.dtype is _I32
+              and free_pages.dtype is _I32 and free_count.dtype is _I32 and len(free_pages.shape) == 1
+              and cache_seqlens.is_contiguous() and new_lens.is_contiguous()
+              and block_table.is_contiguous() and free_pages.is_contiguous()
+              and cache_seqlens.get_device() == new_lens.get_device() == free_pages.get_device()
+              == free_count.get_device() == index)
+    except _WRONG:
+        ok = False
+    if not ok:
+        _refuse("cache_seqlens and new_lens must be [batch] with block_table's batch, free_count [1]",
+                (block_table, "block_table", _I32, 2), (cache_seqlens, "cache_seqlens", _I32, 1),
+                (new_lens, "new_lens", _I32, 1), (free_pages, "free_pages", _I32, 1),
+                (free_count, "free_count", _I32, 1))
     if total < 0:
         raise AttnError(-1, "attn_kvcache_plan")
     given = (cu_seqlens_q, seqlens_after, positions, slot_map, free_left)
-    shapes = ((batch + 1,), (batch,), (total,), (total,), (1,))
-    for t, name, shape in zip(given, ("cu_seqlens_q", "seqlens_after", "positions", "slot_map",
-                                      "free_left"), shapes):
+    sizes = (batch + 1, batch, total, total, 1)
+    for t, name, size in zip(given, _PLAN_OUTPUTS, sizes):
         if t is not None:
-            _step_tensor(t, name, _I32, shape, index)
-    nbytes = lib.attn_kvcache_plan_workspace_bytes(batch)
+            _step_tensor(t, name, _I32, (size,), index)
+    nbytes = lib.attn_kvcache_plan_workspace_bytes(batch, total)
 
     def body(s):
         device = block_table.device
-        outs = tuple(torch.empty(shape, dtype=_I32, device=device) if t is None else t
-                     for t, shape in zip(given, shapes))
-        cu, after, pos, slots, left = outs
+        outs = [torch.empty(size, dtype=_I32, device=device) if t is None else t
+                for t, size in zip(given, sizes)]
         ws = _kv8_workspace(nbytes, device, workspace)
-        rc = lib.attn_kvcache_plan(held, new, table, free, count, left.data_ptr(), cu.data_ptr(),
-                                   after.data_ptr(), pos.data_ptr(), slots.data_ptr(), batch, total,
-                                   ps, max_pages, free_pages.shape[0], pages, _ptr(ws), nbytes, s)
+        cu, after, pos, slots, left = outs
+        rc = lib.attn_kvcache_plan(
+            cache_seqlens.data_ptr(), new_lens.data_ptr(), block_table.data_ptr(),
+            free_pages.data_ptr(), free_count.data_ptr(), left.data_ptr(), cu.data_ptr(),
+            after.data_ptr(), pos.data_ptr(), slots.data_ptr(), batch, total, ps, max_pages,
+            free_pages.shape[0], pages, _ptr(ws), nbytes, s)
         if rc != 0:
             raise AttnError(rc, "attn_kvcache_plan")
-        return outs
+        return tuple(outs)
 
     return _on(index, stream, body)
 
@@ -925,24 +939,39 @@ def _norm_rope_args(q, k, q_weight, k_weight, eps, rotary_cos, rotary_sin, posit
     total, _, d = q.shape
     if k.shape[0] != total or k.shape[2] != d:
         raise ValueError("q and k must have the same tokens and components")
-    w32, weights = 0, []
-    given = [w for w in (q_weight, k_weight) if w is not None]
-    if given:
-        dtype = given[0].dtype if isinstance(given[0], torch.Tensor) else None
-        if dtype not in (_F32, _BF16):
-            raise TypeError("q_weight and k_weight must be torch.float32 or torch.bfloat16")
-        w32 = 1 if dtype is _F32 else 0
-        weights = [_step_tensor(w, "q_weight and k_weight", dtype, (d,), index) for w in given]
-    qw = weights.pop(0) if q_weight is not None else None
-    kw = weights.pop(0) if k_weight is not None else None
+    w32 = 0
+    qw = kw = None
+    if q_weight is not None or k_weight is not None:
+        given = q_weight if q_weight is not None else k_weight
+        dtype = given.dtype if isinstance(given, torch.Tensor) else None
+        if dtype is not _BF16:
+            if dtype is not _F32:
+                raise TypeError("q_weight and k_weight must be torch.float32 or torch.bfloat16")
+            w32 = 1
+        if q_weight is not None:
+            qw = _step_tensor(q_weight, "q_weight", dtype, (d,), index)
+        if k_weight is not None:
+            kw = _step_tensor(k_weight, "k_weight", dtype, (d,), index)
     cos, sin, rot_dim, rot_rows = _rotary(rotary_cos, rotary_sin, index)
     pos, axes, parts = None, 1, None
     if rot_dim:
         if positions is None:
             raise ValueError("a rotation needs positions")
-        one = isinstance(positions, torch.Tensor) and positions.dim() == 1
-        pos = _step_tensor(positions, "positions", _I32, (total,) if one else (None, total), index)
-        axes = 1 if one else positions.shape[0]
+        try:
+            shape = positions.shape
+            axes = 1 if len(shape) == 1 else shape[0]
+            if (len(shape) <= 2 and shape[-1] == total and positions.dtype is _I32
+                    and positions.get_device() == index and positions.is_contiguous()):
+                pos = positions.data_ptr()
+        except _WRONG:
+            pass
+        except IndexError:  # no dimensions
+            pass
+        if pos is None:
+            _refuse("positions must be [T] or [axes, T], on the device of the call's other tensors",
+                    (q, "q", _BF16, 3) if q.is_contiguous() else (rotary_cos, "rotary_cos", _F32, 2),
+                    (positions, "positions", _I32,
+                     2 if isinstance(positions, torch.Tensor) and positions.dim() == 2 else 1))
         if sections is not None:
             if len(sections) != axes:
                 raise ValueError("sections must have one entry per axis of positions")
@@ -1082,27 +1111,46 @@ def attn_decode_kvcache_shared(q, k_cache, v_cache, cache_seqlens, block_table, 
     Returns (out like q, lse fp32 [batch, Hq], or [Hq, total_q] with cu_seqlens_q).
     """
     lib = load()
-    index = _device_index(q, "q")
-    qp = _step_tensor(q, "q", _BF16, (None, None, None), index)
-    total_q, Hq, d = q.shape
-    kc = _step_tensor(k_cache, "k_cache", _BF16, (None, None, None, d), index)
-    num_pages, page_size, Hkv, _ = k_cache.shape
-    vc = _step_tensor(v_cache, "v_cache", _BF16, k_cache.shape, index)
-    table = _step_tensor(block_table, "block_table", _I32, (None, None), index)
-    batch, max_pages = block_table.shape
-    lens = _step_tensor(cache_seqlens, "cache_seqlens", _I32, (batch,), index)
     groups, starts, prefix, cu = 0, None, None, None
-    if (group_starts is None) != (prefix_lens is None):
-        raise ValueError("group_starts and prefix_lens come together")
-    if prefix_lens is not None:
-        prefix = _step_tensor(prefix_lens, "prefix_lens", _I32, (None,), index)
-        groups = prefix_lens.shape[0]
-        starts = _step_tensor(group_starts, "group_starts", _I32, (groups + 1,), index)
-    if cu_seqlens_q is not None:
-        cu = _step_tensor(cu_seqlens_q, "cu_seqlens_q", _I32, (batch + 1,), index)
-    elif total_q != batch:
-        raise ValueError("q must have one token per sequence (or cu_seqlens_q be given)")
-    max_q = _int32(max_seqlen_q, "max_seqlen_q")
+    try:
+        total_q, Hq, d = q.shape
+        cache = k_cache.shape
+        num_pages, page_size, Hkv, dk = cache
+        batch, max_pages = block_table.shape
+        index = q.get_device()
+        ok = (index >= 0 and dk == d and v_cache.shape == cache and cache_seqlens.shape == (batch,)
+              and q.dtype is _BF16 and k_cache.dtype is _BF16 and v_cache.dtype is _BF16
+              and cache_seqlens.dtype is _I32 and block_table.dtype is _I32 and q.is_contiguous()
+              and k_cache.is_contiguous() and v_cache.is_contiguous()
+              and cache_seqlens.is_contiguous() and block_table.is_contiguous()
+              and k_cache.get_device() == v_cache.get_device() == cache_seqlens.get_device()
+              == block_table.get_device() == index)
+        if ok and prefix_lens is not None:
+            groups, = prefix_lens.shape
+            ok = (group_starts.shape == (groups + 1,) and group_starts.dtype is _I32
+                  and prefix_lens.dtype is _I32 and group_starts.is_contiguous()
+                  and prefix_lens.is_contiguous()
+                  and group_starts.get_device() == prefix_lens.get_device() == index)
+            starts, prefix = group_starts.data_ptr(), prefix_lens.data_ptr()
+        elif group_starts is not None:
+            ok = False
+        if ok and cu_seqlens_q is not None:
+            ok = (cu_seqlens_q.shape == (batch + 1,) and cu_seqlens_q.dtype is _I32
+                  and cu_seqlens_q.is_contiguous() and cu_seqlens_q.get_device() == index)
+            cu = cu_seqlens_q.data_ptr()
+        elif total_q != batch:
+            ok = False
+    except _WRONG:
+        ok = False
+    if not ok:
+        more = [(t, n, _I32, 1) for t, n in ((group_starts, "group_starts"), (prefix_lens, "prefix_lens"),
+                                             (cu_seqlens_q, "cu_seqlens_q")) if t is not None]
+        _refuse("q must be [total_q, Hq, d] (one token per sequence, or cu_seqlens_q [batch + 1]), k_cache "
+                "and v_cache [num_pages, page_size, Hkv, d], cache_seqlens [batch], block_table "
+                "[batch, max_pages], group_starts [groups + 1] and prefix_lens [groups], both or none",
+                (q, "q", _BF16, 3), (k_cache, "k_cache", _BF16, 4), (v_cache, "v_cache", _BF16, 4),
+                (cache_seqlens, "cache_seqlens", _I32, 1), (block_table, "block_table", _I32, 2), *more)
+    max_q = 1 if cu is None else _int32(max_seqlen_q, "max_seqlen_q")
     shape = (batch, Hq) if cu is None else (Hq, total_q)
     if out is not None:
         _output(out, "out", _BF16, (total_q, Hq, d), index)
@@ -1117,7 +1165,8 @@ def attn_decode_kvcache_shared(q, k_cache, v_cache, cache_seqlens, block_table, 
         l = torch.empty(shape, dtype=_F32, device=device) if lse is None else lse
         ws = _kv8_workspace(nbytes, device, workspace)
         rc = lib.attn_decode_kvcache_shared(
-            qp, kc, vc, lens, table, starts, prefix, cu, page_size, o.data_ptr(), l.data_ptr(), batch,
+            q.data_ptr(), k_cache.data_ptr(), v_cache.data_ptr(), cache_seqlens.data_ptr(),
+            block_table.data_ptr(), starts, prefix, cu, page_size, o.data_ptr(), l.data_ptr(), batch,
             groups, total_q, max_q, Hq, Hkv, d, max_pages, num_pages, scale, _ptr(ws), nbytes, s)
         if rc != 0:
             raise AttnError(rc, "attn_decode_kvcache_shared")

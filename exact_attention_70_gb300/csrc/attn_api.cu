@@ -1392,8 +1392,9 @@ attn_status_t attn_get_device_status(void* stream) {
 
 // ---- a step's pages and slots ---------------------------------------------------------------
 
-size_t attn_kvcache_plan_workspace_bytes(int batch) {
-    if (batch < 0 || batch > 65535) return 0;
+size_t attn_kvcache_plan_workspace_bytes(int batch, int total_q) {
+    if (batch < 0 || batch > 65535 || total_q < 0) return 0;
+    if (batch <= kPlanSmall && total_q <= kPlanSmall) return 0;
     return align_up(sizeof(int) * (static_cast<size_t>(batch) + 1), 256);
 }
 
@@ -1419,8 +1420,8 @@ attn_status_t attn_kvcache_plan(const int32_t* cache_seqlens, const int32_t* new
                                free_left, cu_seqlens_q, seqlens_after, positions, slot_map};
     for (const void* x : all)
         if (!aligned(x, 4)) return ATTN_ERR_INVALID_ARG;
-    if (!workspace || workspace_bytes < attn_kvcache_plan_workspace_bytes(batch) || !aligned(workspace, 256))
-        return ATTN_ERR_WORKSPACE;
+    const size_t need = attn_kvcache_plan_workspace_bytes(batch, total_q);
+    if (need > 0 && (!workspace || workspace_bytes < need || !aligned(workspace, 256))) return ATTN_ERR_WORKSPACE;
     DeviceState* dev = nullptr;
     const attn_status_t st = device_state(&dev);
     if (st != ATTN_OK) return st;
@@ -1435,7 +1436,7 @@ attn_status_t attn_kvcache_plan(const int32_t* cache_seqlens, const int32_t* new
     p.seqlens_after = seqlens_after;
     p.positions = positions;
     p.slot_map = slot_map;
-    p.page_off = static_cast<int*>(workspace);
+    p.page_off = need > 0 ? static_cast<int*>(workspace) : nullptr;
     p.status = dev->status;
     p.batch = batch;
     p.total_q = total_q;
@@ -1749,12 +1750,18 @@ attn_status_t attn_decode_kvcache_shared(const void* q, const void* k_cache, con
     p.g = nheads_q / nheads_kv;
     p.tpt = tokens_per_tile(p.g);
     p.box_rows = page_size < kFwdBlockN ? page_size : kFwdBlockN;
-    if (encode_3d(&p.tm_q, q, head_dim, nheads_q, total_q, p.g, p.tpt) != ATTN_OK ||
-        encode_3d(&p.tm_q1, q, head_dim, nheads_q, total_q, p.g, 1) != ATTN_OK ||
-        encode_3d(&p.tm_k, k_cache, head_dim, nheads_kv, cache_rows, 1, p.box_rows) != ATTN_OK ||
-        encode_3d(&p.tm_v, v_cache, head_dim, nheads_kv, cache_rows, 1, p.box_rows) != ATTN_OK ||
-        encode_3d(&p.tm_k64, k_cache, head_dim, nheads_kv, cache_rows, 1, std::min(p.box_rows, 64)) != ATTN_OK ||
-        encode_3d(&p.tm_v64, v_cache, head_dim, nheads_kv, cache_rows, 1, std::min(p.box_rows, 64)) != ATTN_OK)
+    const int few_box = std::min(p.box_rows, 64);
+    if (encode_3d(&p.tm_k64, k_cache, head_dim, nheads_kv, cache_rows, 1, few_box) != ATTN_OK ||
+        encode_3d(&p.tm_v64, v_cache, head_dim, nheads_kv, cache_rows, 1, few_box) != ATTN_OK)
+        return ATTN_ERR_CUDA;
+    p.tm_k = p.tm_k64;
+    p.tm_v = p.tm_v64;
+    p.many = static_cast<long long>(total_q) * p.g > kSharedSmallRows;
+    if (p.many && (encode_3d(&p.tm_q, q, head_dim, nheads_q, total_q, p.g, p.tpt) != ATTN_OK ||
+                   encode_3d(&p.tm_q1, q, head_dim, nheads_q, total_q, p.g, 1) != ATTN_OK ||
+                   (p.box_rows > few_box &&
+                    (encode_3d(&p.tm_k, k_cache, head_dim, nheads_kv, cache_rows, 1, p.box_rows) != ATTN_OK ||
+                     encode_3d(&p.tm_v, v_cache, head_dim, nheads_kv, cache_rows, 1, p.box_rows) != ATTN_OK))))
         return ATTN_ERR_CUDA;
     p.q = static_cast<const __nv_bfloat16*>(q);
     p.out = static_cast<__nv_bfloat16*>(out);

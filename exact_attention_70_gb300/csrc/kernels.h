@@ -308,10 +308,14 @@ struct PlanParams {
     int* seqlens_after;  // [batch]
     int* positions;      // [total_q]
     int* slot_map;       // [total_q]
-    int* page_off;       // workspace [batch + 1]: new pages before a sequence's; free_count
+    int* page_off;       // workspace [batch + 1]: new pages before a sequence's; free_count.  Null: a small step
     unsigned* status;
     int batch, total_q, page_size, max_pages, num_free, num_pages;
 };
+
+// Steps of up to so many tokens and sequences take one launch and no workspace: 2048 tokens of 16 sequences
+// 5.1 us (two launches 5.4), 4096 tokens 7.1 (5.3), 64 single tokens 4.1 (5.9); a launch is about 2 us of host time.
+constexpr int kPlanSmall = 2048;
 
 cudaError_t launch_plan(const PlanParams& p, cudaStream_t stream);
 
@@ -402,6 +406,7 @@ struct SharedParams {
     const int* prefix_lens;
     unsigned* status;
     int batch, n_groups, total_q, max_seqlen_q, Hq, Hkv, g, tpt;
+    int many;  // some unit may have many rows (else tm_q, tm_q1 are not there)
     int page_size, box_rows, max_pages, num_pages;
     int max_units, max_items, max_parts, own_base;
     int lse_head, lse_tok;  // strides of lse

@@ -68,9 +68,8 @@ __device__ Pair plan_scan(Pair v, Pair* warp_sum, Pair& total) {
     return before;
 }
 
-__global__ void __launch_bounds__(kPlanThreads) plan_scan_kernel(const PlanParams p) {
-    __shared__ Pair warp_sum[32];
-    griddep_launch_dependents();
+// All that goes by sequence, and the offsets.
+__device__ __forceinline__ void plan_sequences(const PlanParams& p, int* page_off, Pair* warp_sum) {
     const int tid = threadIdx.x;
     const int count = *p.free_count;
     // What cannot be met as a whole changes nothing: the sums come first.
@@ -99,7 +98,7 @@ __global__ void __launch_bounds__(kPlanThreads) plan_scan_kernel(const PlanParam
         const Pair at = plan_scan({s.t, s.n}, warp_sum, total);
         if (b < p.batch) {
             p.cu_seqlens_q[b] = static_cast<int>(carry.t + at.t);
-            p.page_off[b] = static_cast<int>(carry.n + at.n);
+            page_off[b] = static_cast<int>(carry.n + at.n);
             p.seqlens_after[b] = held + s.t;  // (may be cache_seqlens: this thread has read its entry)
         }
         carry.t += total.t;
@@ -108,15 +107,13 @@ __global__ void __launch_bounds__(kPlanThreads) plan_scan_kernel(const PlanParam
     if (tid == 0) {
         if (bad) atomicOr(p.status, kStatusBounds);
         p.cu_seqlens_q[p.batch] = static_cast<int>(carry.t);
-        p.page_off[p.batch] = count;
+        page_off[p.batch] = count;
         *p.free_left = count - static_cast<int>(carry.n);  // (may be free_count)
     }
 }
 
-__global__ void __launch_bounds__(kPlanTokenThreads) plan_tokens_kernel(const PlanParams p) {
-    const int t = blockIdx.x * kPlanTokenThreads + threadIdx.x;
-    griddep_wait();
-    if (t >= p.total_q) return;
+// Token t's position and slot, and the page that begins with it.
+__device__ __forceinline__ void plan_token(const PlanParams& p, const int* page_off, int t) {
     int pos = 0, slot = -1;
     if (t < p.cu_seqlens_q[p.batch]) {
         int lo = 0, hi = p.batch - 1;  // the last sequence that starts at t or before
@@ -131,7 +128,7 @@ __global__ void __launch_bounds__(kPlanTokenThreads) plan_tokens_kernel(const Pl
         const int held = (c + p.page_size - 1) / p.page_size;
         int* entry = p.block_table + static_cast<size_t>(b) * p.max_pages + j;
         const int page = j >= held
-                             ? p.free_pages[p.page_off[p.batch] - 1 - (p.page_off[b] + j - held)]
+                             ? p.free_pages[page_off[p.batch] - 1 - (page_off[b] + j - held)]
                              : *entry;
         const bool ok = page >= 0 && page < p.num_pages;
         if (!ok) atomicOr(p.status, kStatusBounds);
@@ -142,12 +139,37 @@ __global__ void __launch_bounds__(kPlanTokenThreads) plan_tokens_kernel(const Pl
     p.slot_map[t] = slot;
 }
 
+__global__ void __launch_bounds__(kPlanThreads) plan_scan_kernel(const PlanParams p) {
+    __shared__ Pair warp_sum[32];
+    griddep_launch_dependents();
+    plan_sequences(p, p.page_off, warp_sum);
+}
+
+__global__ void __launch_bounds__(kPlanTokenThreads) plan_tokens_kernel(const PlanParams p) {
+    const int t = blockIdx.x * kPlanTokenThreads + threadIdx.x;
+    griddep_wait();
+    if (t < p.total_q) plan_token(p, p.page_off, t);
+}
+
+// Few tokens: both in one launch, by one block (which sees its own writes behind the barrier).
+__global__ void __launch_bounds__(kPlanThreads) plan_small_kernel(const PlanParams p) {
+    __shared__ Pair warp_sum[32];
+    __shared__ int page_off[kPlanSmall + 1];
+    plan_sequences(p, page_off, warp_sum);
+    __syncthreads();
+    for (int t = threadIdx.x; t < p.total_q; t += kPlanThreads) plan_token(p, page_off, t);
+}
+
 }  // namespace
 
 cudaError_t launch_plan(const PlanParams& p, cudaStream_t stream) {
+    if (p.page_off == nullptr) {
+        plan_small_kernel<<<1, kPlanThreads, 0, stream>>>(p);
+        return cudaGetLastError();
+    }
     plan_scan_kernel<<<1, kPlanThreads, 0, stream>>>(p);
     cudaError_t e = cudaGetLastError();
-    if (e != cudaSuccess || p.total_q == 0) return e;
+    if (e != cudaSuccess) return e;
     cudaLaunchConfig_t cfg = {};
     cfg.gridDim = dim3((static_cast<unsigned>(p.total_q) + kPlanTokenThreads - 1) / kPlanTokenThreads);
     cfg.blockDim = dim3(kPlanTokenThreads);

@@ -1322,8 +1322,7 @@ cudaError_t launch_shared_attn_d(const SharedParams& p, int num_sms, int own_uni
     shared_units_kernel<<<1, kShUnitsThreads, 0, stream>>>(p);
     cudaError_t e = cudaGetLastError();
     if (e != cudaSuccess) return e;
-    // (where all rows together are few, no unit has many)
-    const bool many = static_cast<long long>(p.total_q) * p.g > kSharedSmallRows;
+    const bool many = p.many;
     if (many) {
         e = launch_dependent(shared_attn_kernel<D>, dim3(num_sms), kFwdThreads, ShCfg<D>::kSmem, p, stream);
         if (e != cudaSuccess) return e;

@@ -452,7 +452,8 @@ size_t attn_fwd_kvcache_fp8_workspace_bytes(int batch, int total_q, int max_seql
  *                  p = cache_seqlens[b] + i, in slot page * page_size + p % page_size of the cache; behind
  *                  the last token up to total_q (a padded batch) the position is 0 and the slot -1
  *   total_q        at least the sum of new_lens; page_size any positive number; batch up to 65535
- *   workspace      attn_kvcache_plan_workspace_bytes(batch) bytes, 256-byte aligned
+ *   workspace      attn_kvcache_plan_workspace_bytes(batch, total_q) bytes, 256-byte aligned (may be NULL
+ *                  when that is 0)
  * A request that does not fit (a negative length, more tokens than total_q, a sequence past the table, too
  * few free pages) raises ATTN_ERR_DEVICE_BOUNDS and the step is empty: no page is taken, every slot is
  * -1, cu_seqlens_q all 0, seqlens_after and free_left as before.  A page id outside [0, num_pages) raises it
@@ -466,8 +467,9 @@ attn_status_t attn_kvcache_plan(const int32_t* cache_seqlens, const int32_t* new
                                 int max_pages_per_seq, int num_free_pages, int num_pages,
                                 void* workspace, size_t workspace_bytes, void* stream);
 
-/* Workspace bytes of attn_kvcache_plan (0 on sizes the call would refuse). */
-size_t attn_kvcache_plan_workspace_bytes(int batch);
+/* Workspace bytes of attn_kvcache_plan (0 on sizes the call would refuse, and where it needs none: small
+ * steps). */
+size_t attn_kvcache_plan_workspace_bytes(int batch, int total_q);
 
 /*
  * attn_qk_norm_rope -- RMS norm of every query and key row (one token, one head) and the rotary embedding

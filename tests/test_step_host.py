@@ -57,7 +57,7 @@ def test_plan_refusals(lib):
     names = ["sl", "new", "bt", "free", "count", "left", "cu", "after", "pos", "slots", "batch", "total", "ps",
              "mp", "nfree", "np", "ws", "wsb", "stream"]
     call = refusals(lib.attn_kvcache_plan, names,
-                    [FAKE] * 10 + [2, 16, 16, 4, 8, 16, FAKE, 1 << 20, None])
+                    [FAKE] * 10 + [2, 4000, 16, 4, 8, 16, FAKE, 1 << 20, None])
     for name in names[:10]:
         assert call(**{name: None}) == -1, name
         assert call(**{name: P(4098)}) == -1, name
@@ -69,8 +69,10 @@ def test_plan_refusals(lib):
     assert call(ws=None) == -3
     assert call(wsb=16) == -3
     assert call(ws=P(4096 + 16)) == -3
-    assert binding.attn_kvcache_plan_workspace_bytes(64) == 512
-    assert binding.attn_kvcache_plan_workspace_bytes(70000) == 0
+    assert binding.attn_kvcache_plan_workspace_bytes(64, 4000) == 512
+    assert binding.attn_kvcache_plan_workspace_bytes(3000, 0) == 12032
+    assert binding.attn_kvcache_plan_workspace_bytes(64, 64) == 0
+    assert binding.attn_kvcache_plan_workspace_bytes(70000, 64) == 0
 
 
 HOW = ["qw", "kw", "w32", "eps", "cos", "sin", "rot", "rows", "inter", "pos", "axes", "sections", "mixed"]
