@@ -910,74 +910,99 @@ def attn_kvcache_plan(cache_seqlens, new_lens, block_table, free_pages, free_cou
     return _on(index, stream, body)
 
 
-def _rows_of(t, name, index, like=None):
-    """(address, elements between tokens) of bf16 [tokens, heads, d] whose tokens are dense but may
-    lie apart, as the parts of a projection's rows do."""
+def _apart(t, heads, d):
+    """Elements between the tokens of [tokens, heads, d] whose tokens are dense but may lie apart, as the
+    parts of a projection's rows do (None: they are not dense)."""
+    st, sh, sd = t.stride()
+    if sd != 1 or (sh != d and heads != 1):
+        return None
+    return st if t.shape[0] > 1 else heads * d
+
+
+def _refuse_rows(index, *args):
+    """Raise for the first of args, (tensor, name, shape or None), that is not bf16 [tokens, heads, d]
+    with dense tokens on this device."""
+    for t, name, shape in args:
+        if not isinstance(t, torch.Tensor):
+            raise TypeError(f"{name} must be a torch.Tensor")
+        if t.device.type != "cuda" or t.get_device() != index:
+            raise ValueError(f"{name} must be a CUDA tensor on the device of the call's other tensors")
+        if t.dtype != torch.bfloat16:
+            raise TypeError(f"{name} must be torch.bfloat16, got {t.dtype}")
+        if t.dim() != 3 or (shape is not None and t.shape != shape):
+            raise ValueError(f"{name} must be {'[tokens, heads, d]' if shape is None else list(shape)}, "
+                             f"got {list(t.shape)}")
+        if _apart(t, t.shape[1], t.shape[2]) is None:
+            raise ValueError(f"the heads and components of a token of {name} must be dense")
+
+
+def _norm_rope(q, k, q_weight, k_weight, eps, rotary_cos, rotary_sin, positions, rotary_interleaved,
+               sections, sections_interleaved):
+    """(device index, q's sizes and key heads, the strides of q and k, the arguments from q_weight to
+    sections_interleaved as the library takes them)."""
+    index = _device_index(q, "q") if not isinstance(q, torch.Tensor) else q.get_device()
     try:
-        tokens, heads, d = t.shape
-        st, sh, sd = t.stride()
-        if (t.dtype is _BF16 and t.get_device() == index and (like is None or t.shape == like)
-                and (sd == 1 or d == 1) and (sh == d or heads == 1)):
-            return t.data_ptr(), st if tokens > 1 else heads * d
+        total, Hq, d = q.shape
+        tokens, Hkv, dk = k.shape
+        ok = (index >= 0 and tokens == total and dk == d and q.dtype is _BF16 and k.dtype is _BF16
+              and k.get_device() == index)
+        qs, ks = _apart(q, Hq, d), _apart(k, Hkv, d)
     except _WRONG:
-        pass
-    if not isinstance(t, torch.Tensor):
-        raise TypeError(f"{name} must be a torch.Tensor")
-    if t.device.type != "cuda" or t.get_device() != index:
-        raise ValueError(f"{name} must be a CUDA tensor on the device of the call's other tensors")
-    if t.dtype != torch.bfloat16:
-        raise TypeError(f"{name} must be torch.bfloat16, got {t.dtype}")
-    if t.dim() != 3 or (like is not None and t.shape != like):
-        raise ValueError(f"{name} must be {'[tokens, heads, d]' if like is None else list(like)}, got "
-                         f"{list(t.shape)}")
-    raise ValueError(f"the heads and components of a token of {name} must be dense")
-
-
-def _norm_rope_args(q, k, q_weight, k_weight, eps, rotary_cos, rotary_sin, positions,
-                    rotary_interleaved, sections, sections_interleaved, index):
-    """The arguments from q_weight to sections_interleaved as the library takes them."""
-    total, _, d = q.shape
-    if k.shape[0] != total or k.shape[2] != d:
+        ok = False
+    if not ok or qs is None or ks is None:
+        _device_index(q, "q")
+        _refuse_rows(index, (q, "q", None), (k, "k", None))
         raise ValueError("q and k must have the same tokens and components")
     w32 = 0
     qw = kw = None
     if q_weight is not None or k_weight is not None:
-        given = q_weight if q_weight is not None else k_weight
-        dtype = given.dtype if isinstance(given, torch.Tensor) else None
-        if dtype is not _BF16:
-            if dtype is not _F32:
+        try:
+            dtype = (k_weight if q_weight is None else q_weight).dtype
+            ok = dtype is _BF16 or dtype is _F32
+            w32 = 1 if dtype is _F32 else 0
+            if q_weight is not None:
+                qw = q_weight.data_ptr()
+                ok = (ok and q_weight.shape == (d,) and q_weight.is_contiguous()
+                      and q_weight.get_device() == index)
+            if k_weight is not None:
+                kw = k_weight.data_ptr()
+                ok = (ok and k_weight.shape == (d,) and k_weight.dtype is dtype
+                      and k_weight.is_contiguous() and k_weight.get_device() == index)
+        except _WRONG:
+            ok = False
+        if not ok:
+            given = [(w, n) for w, n in ((q_weight, "q_weight"), (k_weight, "k_weight")) if w is not None]
+            dtype = getattr(given[0][0], "dtype", None)
+            if dtype not in (_F32, _BF16):
                 raise TypeError("q_weight and k_weight must be torch.float32 or torch.bfloat16")
-            w32 = 1
-        if q_weight is not None:
-            qw = _step_tensor(q_weight, "q_weight", dtype, (d,), index)
-        if k_weight is not None:
-            kw = _step_tensor(k_weight, "k_weight", dtype, (d,), index)
+            for w, n in given:
+                _step_tensor(w, n, dtype, (d,), index)
     cos, sin, rot_dim, rot_rows = _rotary(rotary_cos, rotary_sin, index)
     pos, axes, parts = None, 1, None
     if rot_dim:
-        if positions is None:
-            raise ValueError("a rotation needs positions")
         try:
             shape = positions.shape
-            axes = 1 if len(shape) == 1 else shape[0]
-            if (len(shape) <= 2 and shape[-1] == total and positions.dtype is _I32
+            dims = len(shape)
+            if (0 < dims < 3 and shape[-1] == total and positions.dtype is _I32
                     and positions.get_device() == index and positions.is_contiguous()):
                 pos = positions.data_ptr()
+                axes = shape[0] if dims == 2 else 1
         except _WRONG:
             pass
-        except IndexError:  # no dimensions
-            pass
         if pos is None:
+            if positions is None:
+                raise ValueError("a rotation needs positions")
             _refuse("positions must be [T] or [axes, T], on the device of the call's other tensors",
-                    (q, "q", _BF16, 3) if q.is_contiguous() else (rotary_cos, "rotary_cos", _F32, 2),
+                    (rotary_cos, "rotary_cos", _F32, 2),
                     (positions, "positions", _I32,
                      2 if isinstance(positions, torch.Tensor) and positions.dim() == 2 else 1))
         if sections is not None:
             if len(sections) != axes:
                 raise ValueError("sections must have one entry per axis of positions")
             parts = (ctypes.c_int32 * axes)(*[_int32(n, "sections") for n in sections])
-    return (qw, kw, w32, float(eps), cos, sin, rot_dim, rot_rows, 1 if rotary_interleaved else 0, pos,
-            axes, parts, 1 if sections_interleaved else 0)
+    return index, total, Hq, Hkv, d, qs, ks, (
+        qw, kw, w32, float(eps), cos, sin, rot_dim, rot_rows, 1 if rotary_interleaved else 0, pos, axes,
+        parts, 1 if sections_interleaved else 0)
 
 
 def attn_qk_norm_rope(q, k, q_weight=None, k_weight=None, eps=1e-6, rotary_cos=None, rotary_sin=None,
@@ -992,21 +1017,20 @@ def attn_qk_norm_rope(q, k, q_weight=None, k_weight=None, eps=1e-6, rotary_cos=N
     Returns (q_out, k_out), dense; q_out may be q and k_out k where those are dense.
     """
     lib = load()
-    index = _device_index(q, "q")
-    qp, qs = _rows_of(q, "q", index)
-    kp, ks = _rows_of(k, "k", index)
-    how = _norm_rope_args(q, k, q_weight, k_weight, eps, rotary_cos, rotary_sin, positions,
-                          rotary_interleaved, sections, sections_interleaved, index)
+    index, total, Hq, Hkv, d, qs, ks, how = _norm_rope(
+        q, k, q_weight, k_weight, eps, rotary_cos, rotary_sin, positions, rotary_interleaved, sections,
+        sections_interleaved)
     if q_out is not None:
         _step_tensor(q_out, "q_out", _BF16, q.shape, index)
     if k_out is not None:
         _step_tensor(k_out, "k_out", _BF16, k.shape, index)
 
     def body(s):
-        qo = torch.empty(q.shape, dtype=_BF16, device=q.device) if q_out is None else q_out
-        ko = torch.empty(k.shape, dtype=_BF16, device=q.device) if k_out is None else k_out
-        rc = lib.attn_qk_norm_rope(qp, kp, qs, ks, *how, qo.data_ptr(), ko.data_ptr(), q.shape[0],
-                                   q.shape[1], k.shape[1], q.shape[2], s)
+        device = q.device
+        qo = torch.empty((total, Hq, d), dtype=_BF16, device=device) if q_out is None else q_out
+        ko = torch.empty((total, Hkv, d), dtype=_BF16, device=device) if k_out is None else k_out
+        rc = lib.attn_qk_norm_rope(q.data_ptr(), k.data_ptr(), qs, ks, *how, qo.data_ptr(), ko.data_ptr(),
+                                   total, Hq, Hkv, d, s)
         if rc != 0:
             raise AttnError(rc, "attn_qk_norm_rope")
         return qo, ko
@@ -1025,32 +1049,44 @@ def attn_qk_norm_rope_bwd(dq_out, dk_out, q, k, q_weight=None, k_weight=None, ep
     and dk may be given, with tokens apart (parts of a projection's gradient).
     """
     lib = load()
-    index = _device_index(q, "q")
-    qp, qs = _rows_of(q, "q", index)
-    kp, ks = _rows_of(k, "k", index)
-    how = _norm_rope_args(q, k, q_weight, k_weight, eps, rotary_cos, rotary_sin, positions,
-                          rotary_interleaved, sections, sections_interleaved, index)
-    gq = _step_tensor(dq_out, "dq_out", _BF16, q.shape, index)
-    gk = _step_tensor(dk_out, "dk_out", _BF16, k.shape, index)
-    if dq is not None:
-        _rows_of(dq, "dq", index, q.shape)
-    if dk is not None:
-        _rows_of(dk, "dk", index, k.shape)
-    total, Hq, d = q.shape
+    index, total, Hq, Hkv, d, qs, ks, how = _norm_rope(
+        q, k, q_weight, k_weight, eps, rotary_cos, rotary_sin, positions, rotary_interleaved, sections,
+        sections_interleaved)
+    q_shape, k_shape = (total, Hq, d), (total, Hkv, d)
+    dqs, dks = Hq * d, Hkv * d
+    try:
+        ok = (dq_out.shape == q_shape and dk_out.shape == k_shape and dq_out.dtype is _BF16
+              and dk_out.dtype is _BF16 and dq_out.is_contiguous() and dk_out.is_contiguous()
+              and dq_out.get_device() == dk_out.get_device() == index)
+        if dq is not None:
+            dqs = _apart(dq, Hq, d)
+            ok = (ok and dq.shape == q_shape and dq.dtype is _BF16 and dq.get_device() == index
+                  and dqs is not None)
+        if dk is not None:
+            dks = _apart(dk, Hkv, d)
+            ok = (ok and dk.shape == k_shape and dk.dtype is _BF16 and dk.get_device() == index
+                  and dks is not None)
+    except _WRONG:
+        ok = False
+    if not ok:
+        _step_tensor(dq_out, "dq_out", _BF16, q_shape, index)
+        _step_tensor(dk_out, "dk_out", _BF16, k_shape, index)
+        _refuse_rows(index, *[(t, n, torch.Size(shape)) for t, n, shape in (
+            (dq, "dq", q_shape), (dk, "dk", k_shape)) if t is not None])
     nbytes = (lib.attn_qk_norm_rope_bwd_workspace_bytes(d)
               if q_weight is not None or k_weight is not None else 0)
 
     def body(s):
         device = q.device
-        dqo = torch.empty(q.shape, dtype=_BF16, device=device) if dq is None else dq
-        dko = torch.empty(k.shape, dtype=_BF16, device=device) if dk is None else dk
+        dqo = torch.empty(q_shape, dtype=_BF16, device=device) if dq is None else dq
+        dko = torch.empty(k_shape, dtype=_BF16, device=device) if dk is None else dk
         dqw = None if q_weight is None else torch.empty(d, dtype=_F32, device=device)
         dkw = None if k_weight is None else torch.empty(d, dtype=_F32, device=device)
         ws = _kv8_workspace(nbytes, device, workspace)
-        dqp, dqs = _rows_of(dqo, "dq", index)
-        dkp, dks = _rows_of(dko, "dk", index)
-        rc = lib.attn_qk_norm_rope_bwd(gq, gk, qp, kp, qs, ks, *how, dqp, dkp, dqs, dks, _ptr(dqw),
-                                       _ptr(dkw), total, Hq, k.shape[1], d, _ptr(ws), nbytes, s)
+        rc = lib.attn_qk_norm_rope_bwd(
+            dq_out.data_ptr(), dk_out.data_ptr(), q.data_ptr(), k.data_ptr(), qs, ks, *how,
+            dqo.data_ptr(), dko.data_ptr(), dqs, dks, _ptr(dqw), _ptr(dkw), total, Hq, Hkv, d, _ptr(ws),
+            nbytes, s)
         if rc != 0:
             raise AttnError(rc, "attn_qk_norm_rope_bwd")
         return dqo, dko, dqw, dkw
@@ -1068,25 +1104,35 @@ def attn_kvcache_append_norm_rope(q, k, v, k_cache, v_cache, slot_map, q_weight=
     Returns q_out [T, Hq, d].
     """
     lib = load()
-    index = _device_index(q, "q")
-    qp, qs = _rows_of(q, "q", index)
-    kp, ks = _rows_of(k, "k", index)
-    vp, vs = _rows_of(v, "v", index, k.shape)
-    how = _norm_rope_args(q, k, q_weight, k_weight, eps, rotary_cos, rotary_sin, positions,
-                          rotary_interleaved, sections, sections_interleaved, index)
-    total, Hq, d = q.shape
-    cache = (None, None, k.shape[1], d)
-    kc = _step_tensor(k_cache, "k_cache", _BF16, cache, index)
-    vc = _step_tensor(v_cache, "v_cache", _BF16, k_cache.shape, index)
-    slots = _step_tensor(slot_map, "slot_map", _I32, (total,), index)
+    index, total, Hq, Hkv, d, qs, ks, how = _norm_rope(
+        q, k, q_weight, k_weight, eps, rotary_cos, rotary_sin, positions, rotary_interleaved, sections,
+        sections_interleaved)
+    try:
+        cache = k_cache.shape
+        num_pages, page_size, heads, dim = cache
+        vs = _apart(v, Hkv, d)
+        ok = (heads == Hkv and dim == d and v_cache.shape == cache and v.shape == k.shape
+              and vs is not None and slot_map.shape == (total,) and v.dtype is _BF16
+              and k_cache.dtype is _BF16 and v_cache.dtype is _BF16 and slot_map.dtype is _I32
+              and k_cache.is_contiguous() and v_cache.is_contiguous() and slot_map.is_contiguous()
+              and v.get_device() == k_cache.get_device() == v_cache.get_device()
+              == slot_map.get_device() == index)
+    except _WRONG:
+        ok = False
+    if not ok:
+        _refuse_rows(index, (v, "v", k.shape))
+        _step_tensor(k_cache, "k_cache", _BF16, (None, None, Hkv, d), index)
+        _step_tensor(v_cache, "v_cache", _BF16, k_cache.shape, index)
+        _step_tensor(slot_map, "slot_map", _I32, (total,), index)
     if q_out is not None:
         _step_tensor(q_out, "q_out", _BF16, q.shape, index)
 
     def body(s):
-        qo = torch.empty(q.shape, dtype=_BF16, device=q.device) if q_out is None else q_out
-        rc = lib.attn_kvcache_append_norm_rope(qp, kp, vp, qs, ks, vs, *how, qo.data_ptr(), kc, vc,
-                                               slots, total, Hq, k.shape[1], d, k_cache.shape[1],
-                                               k_cache.shape[0], s)
+        qo = torch.empty((total, Hq, d), dtype=_BF16, device=q.device) if q_out is None else q_out
+        rc = lib.attn_kvcache_append_norm_rope(
+            q.data_ptr(), k.data_ptr(), v.data_ptr(), qs, ks, vs, *how, qo.data_ptr(),
+            k_cache.data_ptr(), v_cache.data_ptr(), slot_map.data_ptr(), total, Hq, Hkv, d, page_size,
+            num_pages, s)
         if rc != 0:
             raise AttnError(rc, "attn_kvcache_append_norm_rope")
         return qo
