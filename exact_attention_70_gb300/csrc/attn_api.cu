@@ -1467,7 +1467,7 @@ attn_status_t norm_rope_params(NormRopeParams& p, const void* q, const void* k, 
                                int nheads_q, int nheads_kv, int head_dim) {
     if (total < 0 || nheads_q <= 0 || nheads_kv <= 0) return ATTN_ERR_INVALID_ARG;
     if (head_dim != 64 && head_dim != 128) return ATTN_ERR_UNSUPPORTED;
-    if (nheads_q > 65535 || nheads_kv > 65535 ||
+    if (nheads_q > 65535 || nheads_kv > 65535 || total > 1 << 30 ||
         static_cast<long long>(total) * (nheads_q > nheads_kv ? nheads_q : nheads_kv) > (1LL << 31) - 1)
         return ATTN_ERR_UNSUPPORTED;
     if (rotary_dim < 0 || rotary_dim > head_dim || rotary_dim % 16 != 0) return ATTN_ERR_UNSUPPORTED;

@@ -75,6 +75,17 @@ __device__ __forceinline__ int sh_reserve(int* counter, int n, int lane) {
     return __shfl_sync(0xffffffffu, at, 31) + x - n;
 }
 
+// The list is read past L1: kernels that start before the one in front of them has ended could find lines of the
+// call before there.
+__device__ __forceinline__ SharedUnit sh_unit(const SharedParams& p, int i) {
+    SharedUnit u;
+    const int4* src = reinterpret_cast<const int4*>(p.units + i);
+    int4* dst = reinterpret_cast<int4*>(&u);
+#pragma unroll
+    for (int x = 0; x < static_cast<int>(sizeof(SharedUnit) / sizeof(int4)); ++x) dst[x] = __ldcg(src + x);
+    return u;
+}
+
 __device__ __forceinline__ bool sh_few(int rows) { return rows <= kSharedSmallRows; }
 
 // Writes the list.  Where the parts lie and the order among units of a length depend on the warps' order;
@@ -368,7 +379,7 @@ __device__ __forceinline__ uint32_t sh_parity(uint32_t bits, uint32_t st) { retu
 // kKind: which of the list's two halves.
 template <int kKind, int kSlots, typename Bars>
 __device__ void sh_scheduler(const SharedParams& p, Bars* bars, const Watchdog& wd, int lane) {
-    const int first = kKind ? p.header->n_items[0] : 0, n_items = p.header->n_items[kKind];
+    const int first = kKind ? __ldcg(&p.header->n_items[0]) : 0, n_items = __ldcg(&p.header->n_items[kKind]);
     uint32_t kv = 0, vpar = 0;
     for (uint32_t r = 0;; ++r) {
         const uint32_t slot = r % kShRing;
@@ -382,8 +393,8 @@ __device__ void sh_scheduler(const SharedParams& p, Bars* bars, const Watchdog& 
         }
         ShItem it = {};
         if (idx < n_items) {
-            const int2 w = p.items[first + idx];
-            const SharedUnit u = p.units[w.x];
+            const int2 w = __ldcg(p.items + first + idx);
+            const SharedUnit u = sh_unit(p, w.x);
             const int piece = w.y >> 16;
             // (the first nblk % pieces of them have a block more)
             const int len = u.nblk / u.pieces, more = u.nblk - len * u.pieces;
@@ -1192,20 +1203,22 @@ __global__ void __launch_bounds__(kShCombineThreads) shared_combine_kernel(const
     const int own = blockIdx.x, kvh = blockIdx.y, lane = threadIdx.x & 31;
     const int half = threadIdx.x >> 7, w = (threadIdx.x >> 5) & 3, r = 2 * blockIdx.z + half;
     const SharedHeader* h = p.header;
-    const SharedUnit* u = p.units + p.own_base + own;
-    const bool some = !h->bad && own < h->n_own && 2 * blockIdx.z < u->rows;  // the same for the block
-    const bool on = some && r < u->rows;
+    const bool listed = __ldcg(&h->bad) == 0 && own < __ldcg(&h->n_own);
+    SharedUnit u = {};
+    if (listed) u = sh_unit(p, p.own_base + own);
+    const bool some = listed && 2 * blockIdx.z < u.rows;  // the same for the block
+    const bool on = some && r < u.rows;
     int n1 = 0, n2 = 0, base1 = 0, base2 = 0, step1 = 0, step2 = 0, tok = 0;
     if (on) {
-        tok = u->q0 + r / p.g;
-        n1 = u->pieces * u->split;
-        step1 = u->rows;
-        base1 = u->part + kvh * n1 * step1 + r;
-        if (u->prefix >= 0) {
-            const SharedUnit* v = p.units + u->prefix + (tok - u->group_q0) / (2 * p.tpt);
-            n2 = v->pieces * v->split;
-            step2 = v->rows;
-            base2 = v->part + kvh * n2 * step2 + (tok - v->q0) * p.g + r % p.g;
+        tok = u.q0 + r / p.g;
+        n1 = u.pieces * u.split;
+        step1 = u.rows;
+        base1 = u.part + kvh * n1 * step1 + r;
+        if (u.prefix >= 0) {
+            const SharedUnit v = sh_unit(p, u.prefix + (tok - u.group_q0) / (2 * p.tpt));
+            n2 = v.pieces * v.split;
+            step2 = v.rows;
+            base2 = v.part + kvh * n2 * step2 + (tok - v.q0) * p.g + r % p.g;
         }
     }
     griddep_wait();

@@ -72,6 +72,15 @@ def test_chunks(attn, heads):  # noqa: F811
     assert (keep[0][n:] == 3).all() and (keep[1][:, n:] == 3).all()
 
 
+@pytest.mark.parametrize("Hq,Hkv,d", [(16, 1, 128), (17, 1, 128), (32, 2, 64), (34, 2, 64), (40, 40, 64), (70, 70, 128)])
+def test_rows_at_the_border_of_few_and_many_heads(attn, Hq, Hkv, d):  # noqa: F811
+    """Units of 16 and 17 rows (the most that count as few, and one more); more kv heads than a warp's lanes."""
+    c = shared_case([(300, [(1, 40), (1, 7)]), (0, [(1, 400)])], Hq, Hkv, d, 32, seed=50 + Hq)
+    check(attn, c)
+    c = shared_case([(300, [(1, 40), (2, 7)]), (0, [(4, 400), (1, 0)])], Hq, Hkv, d, 32, seed=51 + Hq, padding=1)
+    check(attn, c)
+
+
 def test_a_group_that_fills_many_tiles(attn):  # noqa: F811
     c = shared_case([(400, [(1, i % 5) for i in range(150)])], 8, 2, 64, 16, seed=9)       # 600 rows a head
     check(attn, c)
@@ -81,6 +90,11 @@ def test_a_group_that_fills_many_tiles(attn):  # noqa: F811
 
 def test_many_groups_and_sequences(attn):  # noqa: F811
     c = shared_case([(130, [(1, 1), (1, 0)])] * 600, 2, 1, 64, 16, seed=11)
+    check(attn, c)
+
+
+def test_more_groups_and_units_than_the_lists_shared_memory_holds(attn):  # noqa: F811
+    c = shared_case([(130, [(1, 1), (1, 0)])] * 1100, 1, 1, 64, 16, seed=46)
     check(attn, c)
 
 
