@@ -33,25 +33,13 @@ __device__ __forceinline__ uint2 ld_row8(const __nv_bfloat16* p) {
     return *reinterpret_cast<const uint2*>(p);
 }
 
-// The four bf16 values of an 8-byte piece.
-__device__ __forceinline__ void unpack4(uint2 v, float* f) {
-    f[0] = __uint_as_float(v.x << 16);
-    f[1] = __uint_as_float(v.x & 0xffff0000u);
-    f[2] = __uint_as_float(v.y << 16);
-    f[3] = __uint_as_float(v.y & 0xffff0000u);
-}
-
-__device__ __forceinline__ uint2 pack4(const float* f) {
-    return make_uint2(pack_bf16x2(f[0], f[1]), pack_bf16x2(f[2], f[3]));
-}
-
 // Asynchronous 16-byte copy of this thread to shared memory; zeros with on = false.
 __device__ __forceinline__ void cp_async16z(void* smem_dst, const void* src, bool on) {
     asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" ::"r"(smem_u32(smem_dst)), "l"(src), "r"(on ? 16 : 0)
                  : "memory");
 }
 
-// The same as two pairs for the paired fp32 instructions, and back.
+// The four bf16 values of an 8-byte piece as two pairs of fp32 for the paired instructions, and back.
 __device__ __forceinline__ void unpack_pairs(uint2 v, uint64_t* f) {
     f[0] = f2_make(__uint_as_float(v.x << 16), __uint_as_float(v.x & 0xffff0000u));
     f[1] = f2_make(__uint_as_float(v.y << 16), __uint_as_float(v.y & 0xffff0000u));
@@ -137,36 +125,24 @@ __device__ __forceinline__ bool load_turn(const NormRopeParams& p, const Lane& s
     return true;
 }
 
-// The eight elements (two pieces) turned by their planes' angles, or back.
+// The lane's elements, in pairs, turned by their planes' angles, or back.
 template <bool kInter, bool kBack>
-__device__ __forceinline__ void turn(float (&x)[8], const float* c, const float* sn) {
+__device__ __forceinline__ void turn(uint64_t (&x)[4], const float* c, const float* sn) {
+    if (kInter) {  // a pair is a plane
 #pragma unroll
-    for (int i = 0; i < 4; ++i) {
-        float& a = x[kInter ? 2 * i : i];
-        float& b = x[kInter ? 2 * i + 1 : i + 4];
-        const float s = kBack ? -sn[i] : sn[i];
-        const float ra = a * c[i] - b * s, rb = a * s + b * c[i];
-        a = ra;
-        b = rb;
-    }
-}
-
-// R^T of the lane's elements, in pairs.
-template <bool kInter>
-__device__ __forceinline__ void turn_back(uint64_t (&x)[4], const float* c, const float* sn) {
-    if (kInter) {
-        float f[8];
-#pragma unroll
-        for (int i = 0; i < 4; ++i) f2_split(x[i], f[2 * i], f[2 * i + 1]);
-        turn<true, true>(f, c, sn);
-#pragma unroll
-        for (int i = 0; i < 4; ++i) x[i] = f2_make(f[2 * i], f[2 * i + 1]);
-    } else {
+        for (int i = 0; i < 4; ++i) {
+            float a, b;
+            f2_split(x[i], a, b);
+            const float s = kBack ? -sn[i] : sn[i];
+            x[i] = f2_make(a * c[i] - b * s, a * s + b * c[i]);
+        }
+    } else {  // pairs i and i + 2 are two planes
 #pragma unroll
         for (int i = 0; i < 2; ++i) {
             const uint64_t c2 = f2_make(c[2 * i], c[2 * i + 1]), s2 = f2_make(sn[2 * i], sn[2 * i + 1]);
             const uint64_t n2 = f2_make(-sn[2 * i], -sn[2 * i + 1]);
-            const uint64_t a = f2_fma(x[i], c2, f2_mul(x[i + 2], s2)), b = f2_fma(x[i], n2, f2_mul(x[i + 2], c2));
+            const uint64_t a = f2_fma(x[i], c2, f2_mul(x[i + 2], kBack ? s2 : n2));
+            const uint64_t b = f2_fma(x[i], kBack ? n2 : s2, f2_mul(x[i + 2], c2));
             x[i] = a;
             x[i + 2] = b;
         }
@@ -174,21 +150,21 @@ __device__ __forceinline__ void turn_back(uint64_t (&x)[4], const float* c, cons
 }
 
 // The lane's eight weights (ones without a norm).
-__device__ __forceinline__ void load_weights(const void* w, bool f32, const Lane& s, float (&out)[8]) {
+__device__ __forceinline__ void load_weights(const void* w, bool f32, const Lane& s, uint64_t (&out)[4]) {
     if (w == nullptr) {
 #pragma unroll
-        for (int i = 0; i < 8; ++i) out[i] = 1.f;
+        for (int i = 0; i < 4; ++i) out[i] = f2_make(1.f, 1.f);
     } else if (f32) {
 #pragma unroll
         for (int i = 0; i < 2; ++i) {
             const float4 x = __ldg(reinterpret_cast<const float4*>(static_cast<const float*>(w) + (i ? s.o1 : s.o0)));
-            out[4 * i] = x.x, out[4 * i + 1] = x.y, out[4 * i + 2] = x.z, out[4 * i + 3] = x.w;
+            out[2 * i] = f2_make(x.x, x.y), out[2 * i + 1] = f2_make(x.z, x.w);
         }
     } else {
 #pragma unroll
         for (int i = 0; i < 2; ++i)
-            unpack4(__ldg(reinterpret_cast<const uint2*>(static_cast<const __nv_bfloat16*>(w) + (i ? s.o1 : s.o0))),
-                    out + 4 * i);
+            unpack_pairs(__ldg(reinterpret_cast<const uint2*>(static_cast<const __nv_bfloat16*>(w) + (i ? s.o1 : s.o0))),
+                         out + 2 * i);
     }
 }
 
@@ -238,7 +214,7 @@ __global__ void __launch_bounds__(kNrThreads, kNrFwdBlocksPerSm) norm_rope_kerne
     const Rows rows = load_rows(p, t);
     const int slot = kAppend && here ? __ldg(p.slots + t) : 0;
     const void* wp = isv ? nullptr : isk ? p.k_weight : p.q_weight;
-    float w[8];
+    uint64_t w[4];
     load_weights(wp, p.weight_f32, s, w);
     float c[4], sn[4];
     bool live = here;
@@ -260,34 +236,36 @@ __global__ void __launch_bounds__(kNrThreads, kNrFwdBlocksPerSm) norm_rope_kerne
 #pragma unroll
         for (int u = 0; u < kRows; ++u) {
             const int h = h0 + u * par;
-            float x[8];
-            unpack4(raw[u][0], x);
-            unpack4(raw[u][1], x + 4);
+            uint64_t x[4];  // in pairs
+            unpack_pairs(raw[u][0], x);
+            unpack_pairs(raw[u][1], x + 2);
             if (wp != nullptr) {
-                float ss = 0.f;
+                uint64_t s2 = 0;
 #pragma unroll
-                for (int i = 0; i < 8; ++i) ss = fmaf(x[i], x[i], ss);
-                ss = row_sum<kLanes>(ss);
-                float eps = p.eps;
+                for (int i = 0; i < 4; ++i) s2 = f2_fma(x[i], x[i], s2);
+                float ss = row_sum<kLanes>(f2_sum(s2)), eps = p.eps;
                 const bool far = !(ss < kFarSum);
                 if (__any_sync(0xffffffffu, far)) {
+                    const uint64_t f2 = far ? f2_make(kFarUnit, kFarUnit) : f2_make(1.f, 1.f);
+                    s2 = 0;
 #pragma unroll
-                    for (int i = 0; i < 8; ++i) x[i] *= far ? kFarUnit : 1.f;
-                    float s2 = 0.f;
-#pragma unroll
-                    for (int i = 0; i < 8; ++i) s2 = fmaf(x[i], x[i], s2);
-                    s2 = row_sum<kLanes>(s2);
-                    if (far) ss = s2, eps = p.eps * kFarUnit * kFarUnit;
+                    for (int i = 0; i < 4; ++i) {
+                        x[i] = f2_mul(x[i], f2);
+                        s2 = f2_fma(x[i], x[i], s2);
+                    }
+                    const float t2 = row_sum<kLanes>(f2_sum(s2));
+                    if (far) ss = t2, eps = p.eps * kFarUnit * kFarUnit;
                 }
                 const float r = rsqrtf(fmaf(ss, 1.f / D, eps));
+                const uint64_t r2 = f2_make(r, r);
 #pragma unroll
-                for (int i = 0; i < 8; ++i) x[i] *= r * w[i];
+                for (int i = 0; i < 4; ++i) x[i] = f2_mul(x[i], f2_mul(r2, w[i]));
             }
             if (!isv && s.turns) turn<kInter, false>(x, c, sn);
             if (live && h < k.heads &&
                 ATTN_IN_BOUNDS(row0 + h < static_cast<size_t>(to_cache ? p.cache_rows : p.total) * k.heads, p.status)) {
-                *reinterpret_cast<uint2*>(dst + h * D + s.o0) = isv ? raw[u][0] : pack4(x);
-                *reinterpret_cast<uint2*>(dst + h * D + s.o1) = isv ? raw[u][1] : pack4(x + 4);
+                *reinterpret_cast<uint2*>(dst + h * D + s.o0) = isv ? raw[u][0] : pack_pairs(x);
+                *reinterpret_cast<uint2*>(dst + h * D + s.o1) = isv ? raw[u][1] : pack_pairs(x + 2);
             }
         }
         h0 += par * kRows;
@@ -382,12 +360,9 @@ __global__ void __launch_bounds__(kNrThreads, kNrBwdBlocksPerSm) norm_rope_bwd_k
     }
     Rows rows = load_rows(p, w.t);
     uint64_t wt[4], dw[4];  // pairs of the lane's elements
-    {
-        float x[8];
-        load_weights(wp, p.weight_f32, s, x);
+    load_weights(wp, p.weight_f32, s, wt);
 #pragma unroll
-        for (int i = 0; i < 4; ++i) wt[i] = f2_make(x[2 * i], x[2 * i + 1]), dw[i] = 0;
-    }
+    for (int i = 0; i < 4; ++i) dw[i] = 0;
     bool live = enter(w.t, rows);
     rows = load_rows(p, w.t + w.stride);
     int stage = 0;
@@ -406,7 +381,7 @@ __global__ void __launch_bounds__(kNrThreads, kNrBwdBlocksPerSm) norm_rope_bwd_k
             unpack_pairs(*reinterpret_cast<const uint2*>(&ring[stage][u][0][slot][s.o0]), g);
             unpack_pairs(*reinterpret_cast<const uint2*>(&ring[stage][u][0][slot][s.o1]), g + 2);
             if (!all && !live) g[0] = g[1] = g[2] = g[3] = 0;  // (a token outside the tables gives nothing)
-            if (s.turns && on) turn_back<kInter>(g, c, sn);
+            if (s.turns && on) turn<kInter, true>(g, c, sn);
             if (wp != nullptr) {
                 uint64_t x[4], hg[4], s2 = 0, d2 = 0;
                 unpack_pairs(*reinterpret_cast<const uint2*>(&ring[stage][u][1][slot][s.o0]), x);
