@@ -8,15 +8,28 @@
 // heads of a kv head fill tiles of 128 rows.  Then every sequence meets the keys behind its prefix, and
 // a last kernel merges the parts.
 //
-// GB300 mapping.  One kernel does both kinds of work (units), on tcgen05: one CTA an SM, persistent, two
-// tiles of 128 rows on the same key blocks, roles and barriers as in the prefill kernel (fwd_kernel.cu):
-//   * warp 16 claims items and gathers K and V blocks of 128 keys through block_table, a lane a page, into a
-//     ring of shared-memory slots (K_0, K_1, V_0, K_2, V_1, ..., V_{m-1});
-//   * warp 17 issues S_t = Q_t K^T, warp 18 O_t += P_t V, accumulators in TMEM;
-//   * warps 0-7 and 8-15 do the softmax of the two tiles, 16 rows a warp; a warp whose rows hold no token
-//     only keeps the barriers going.
-// A unit's key blocks are cut into pieces of about 1 / 152 of all the work, so that the CTAs finish
-// together; each piece leaves its rows' O / l and log2 LSE in fp32.
+// Four kernels, each starting while the one before it ends:
+//   * shared_units_kernel (one CTA) writes the list of the work: units (query rows that walk the same
+//     keys) cut into pieces of about 1 / 152 (1 / 304) of all the work, so that the CTAs finish together;
+//   * shared_attn_kernel does the units of more than 16 rows on tcgen05: one CTA an SM, persistent, two
+//     tiles of 128 rows on the same key blocks, roles and barriers as in the prefill kernel (fwd_kernel.cu):
+//     warp 16 gathers K and V blocks of 128 keys through block_table, a lane a page, into a ring of
+//     shared-memory slots (K_0, K_1, V_0, K_2, V_1, ..., V_{m-1}); warp 17 issues S_t = Q_t K^T, warp 18
+//     O_t += P_t V, accumulators in TMEM; warps 0-7 and 8-15 do the softmax of the two tiles, 16 rows a
+//     warp (one whose rows hold no token only keeps the barriers going); warp 19 claims items;
+//   * shared_small_kernel does the units of up to 16 rows on mma.sync;
+//   * shared_combine_kernel merges the parts (O / l and log2 LSE of a piece, fp32).
+// Both sides of the 16 rows (all on tcgen05 / as it is): 4 sequences on 512 keys 15.7 / 12.4 us, 64 sequences of
+// 1K to 16K keys of their own, 32:8 heads, 356 / 343, 2 of 100K 211 / 132, 5 ragged documents 59.5 / 52.
+//
+// Measured in a captured graph, d 128, bf16, with the shares of the time: 64 requests on 32768 shared and 100 to
+// 2000 own keys, 32:8 heads: 97.5 us (units 7, prefix 33, own keys 47, merge 8; 421 MB, 4.3 TB/s over all);
+// 16 samples of 4 tokens on 100001 keys: 107 us (units 6, prefix 80, own keys 8, merge 8).  Own keys run at 6.4 TB/s.
+// A block of 128 keys under two tiles takes 3100 to 3600 clocks where the memory would take 2800: the chain
+// S, softmax, P V of a tile, 16 warps at half their issue rate, is what bounds it, as in the prefill kernel.
+// Tried for it and not kept: P in tensor memory over S and five ring slots (the chain gets longer: 122 -> 136 us),
+// asking for blocks in L2 ahead of their loads (121 -> 138 us, the TMA unit's work doubles), two pieces a CTA
+// (107 -> 120: twice the parts).
 #include <cuda_bf16.h>
 
 #include "kernels.h"
@@ -32,9 +45,17 @@ constexpr float kShLn2 = 0.69314718055994530942f;
 constexpr int kShUnitsThreads = 512;
 constexpr int kShFast = 1024;  // groups, and half the units, that the list's kernel keeps in shared memory
 constexpr int kShBins = 32;    // lengths that the list tells apart
-constexpr int kShMinPrefix = 128;  // shorter prefixes are read by every sequence
-constexpr int kShMinPiece = 2;     // key blocks a piece takes at least
+// Shorter prefixes are read by every sequence.  (Near this size sharing costs about what it saves, a third
+// kernel against keys that L2 holds anyway: 64 sequences, 32:8 heads, on 128 shared keys 31.5 us (28.1 without
+// sharing), on 512 32.3 (35.7), on 1024 32.7 (44.6); 4 sequences on 512 12.8 (12.5), on 2048 14.8 (17.0).)
+constexpr int kShMinPrefix = 128;
+// Key blocks a piece takes at least: 2 sequences on 4096 keys, 64:8 heads, 17.9 us (22.7 with 1, 17.1 with 4),
+// 4 on 512 12.4 (11.8, 13.6), 16 on 1024 19.3 (20.8, 21.7).
+constexpr int kShMinPiece = 2;
 constexpr int kShCombineThreads = 256;
+// Rows up to which the merge gives a row eight warps, not four: 64 rows behind 16K shared keys 26.1 us (28.9 with
+// four), 128 rows behind 8K 22.6 (25.4); 512 rows behind 1K 20.7 (19.1), 2048 rows behind 32K 102 (98).
+constexpr int kShFewRows = kGb300Sms;
 constexpr int kShSoftmaxWarps = 16;
 
 // ---- units and items (one CTA) --------------------------------------------------------------------
@@ -1189,24 +1210,25 @@ __global__ void __launch_bounds__(kSmThreads, 2) shared_small_kernel(const __gri
 
 // ---- merge --------------------------------------------------------------------------------------------
 
-// Four warps have a row, eight parts each at a time, whose loads all go out together: block (i, h, j) has rows
-// 2 j and 2 j + 1 of sequence unit i for kv head h.  LSE = log2 sum_s 2^LSE_s, O = sum_s 2^(LSE_s - LSE) O_s
-// over the parts of the row's prefix and of its own keys; no part, or none with a key: O = 0, LSE = -inf.
-// Bound by the latency of the parts' loads: 2048 rows of 22 parts took 9 us with a warp a row, three times
-// eight parts one after the other.
-template <int D>
+// Four or eight warps have a row, eight parts each at a time, whose loads all go out together: block (i, h, j)
+// has rows kRows j .. kRows j + kRows - 1 of sequence unit i for kv head h.  LSE = log2 sum_s 2^LSE_s,
+// O = sum_s 2^(LSE_s - LSE) O_s over the parts of the row's prefix and of its own keys; no part, or none with
+// a key: O = 0, LSE = -inf.
+// Bound by the latency of the parts' loads, and by L2 where there are many: 2048 rows of 22 parts took 9 us
+// with a warp a row, three times eight parts one after the other, and take 8 (23 MB).
+template <int D, int kRows>
 __global__ void __launch_bounds__(kShCombineThreads) shared_combine_kernel(const SharedParams p) {
-    constexpr int E = D / 32, kWarps = 4, kBatch = 8;
-    __shared__ float4 s_acc[2][kWarps][32];
-    __shared__ float s_max[2][kWarps], s_sum[2][kWarps];
+    constexpr int E = D / 32, kWarps = kShCombineThreads / 32 / kRows, kBatch = 8;
+    __shared__ float4 s_acc[kRows][kWarps][32];
+    __shared__ float s_max[kRows][kWarps], s_sum[kRows][kWarps];
     // (the list is there when this kernel starts; the parts are when the one before it has ended)
     const int own = blockIdx.x, kvh = blockIdx.y, lane = threadIdx.x & 31;
-    const int half = threadIdx.x >> 7, w = (threadIdx.x >> 5) & 3, r = 2 * blockIdx.z + half;
+    const int half = threadIdx.x / (32 * kWarps), w = (threadIdx.x >> 5) % kWarps, r = kRows * blockIdx.z + half;
     const SharedHeader* h = p.header;
     const bool listed = __ldcg(&h->bad) == 0 && own < __ldcg(&h->n_own);
     SharedUnit u = {};
     if (listed) u = sh_unit(p, p.own_base + own);
-    const bool some = listed && 2 * blockIdx.z < u.rows;  // the same for the block
+    const bool some = listed && kRows * blockIdx.z < u.rows;  // the same for the block
     const bool on = some && r < u.rows;
     int n1 = 0, n2 = 0, base1 = 0, base2 = 0, step1 = 0, step2 = 0, tok = 0;
     if (on) {
@@ -1344,8 +1366,9 @@ cudaError_t launch_shared_attn_d(const SharedParams& p, int num_sms, int own_uni
                          kSmThreads, SmCfg<D>::kSmem, p, stream);
     if (e != cudaSuccess) return e;
     const int rows = (p.max_seqlen_q < 2 * p.tpt ? p.max_seqlen_q : 2 * p.tpt) * p.g;  // of a unit, at most
-    return launch_dependent(shared_combine_kernel<D>, dim3(own_units, p.Hkv, ceil_div(rows, 2)), kShCombineThreads, 0,
-                            p, stream);
+    const bool few = static_cast<long long>(p.total_q) * p.Hq <= kShFewRows;
+    return launch_dependent(few ? shared_combine_kernel<D, 1> : shared_combine_kernel<D, 2>,
+                            dim3(own_units, p.Hkv, few ? rows : ceil_div(rows, 2)), kShCombineThreads, 0, p, stream);
 }
 
 }  // namespace
