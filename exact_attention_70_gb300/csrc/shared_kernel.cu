@@ -32,6 +32,8 @@
 // (107 -> 120: twice the parts).
 #include <cuda_bf16.h>
 
+#include <algorithm>
+
 #include "kernels.h"
 #include "ptx.cuh"
 #include "tile_math.h"
@@ -1365,7 +1367,8 @@ cudaError_t launch_shared_attn_d(const SharedParams& p, int num_sms, int own_uni
     e = launch_dependent(many ? shared_small_kernel<D, true> : shared_small_kernel<D, false>, dim3(2 * num_sms),
                          kSmThreads, SmCfg<D>::kSmem, p, stream);
     if (e != cudaSuccess) return e;
-    const int rows = (p.max_seqlen_q < 2 * p.tpt ? p.max_seqlen_q : 2 * p.tpt) * p.g;  // of a unit, at most
+    // a unit's rows, at most (max_seqlen_q may be 0, a grid not)
+    const int rows = std::max(std::min(p.max_seqlen_q, 2 * p.tpt), 1) * p.g;
     const bool few = static_cast<long long>(p.total_q) * p.Hq <= kShFewRows;
     return launch_dependent(few ? shared_combine_kernel<D, 1> : shared_combine_kernel<D, 2>,
                             dim3(own_units, p.Hkv, few ? rows : ceil_div(rows, 2)), kShCombineThreads, 0, p, stream);

@@ -139,6 +139,16 @@ def test_no_keys_at_all(attn):  # noqa: F811
     check(attn, c)
 
 
+def test_a_step_without_tokens(attn):  # noqa: F811
+    """max_seqlen_q 0, only padding: nothing to do, and nothing is written."""
+    c = shared_case([(200, [(0, 7), (0, 9)])], 8, 2, 64, 16, seed=16, decode=False, padding=3)
+    c.longest = 0
+    out, lse = torch.full_like(c.q, 3.0).cuda(), torch.full((8, 3), 3.0, device="cuda")
+    call(attn, dev(c), out=out, lse=lse)
+    assert attn.attn_get_device_status() == 0
+    assert (out == 3).all() and (lse == 3).all()
+
+
 def test_more_queries_than_keys(attn):  # noqa: F811
     """Rows that stand before the first key see nothing."""
     c = shared_case([(0, [(5, 0), (3, 2)])], 8, 2, 64, 16, seed=17, decode=False)
