@@ -180,3 +180,10 @@ def test_binding_refuses_cpu_tensors(lib):
         binding.attn_decode_kvcache_shared(x(2, 4, 64), x(2, 16, 2, 64), x(2, 16, 2, 64), i(2), i(2, 4))
     with pytest.raises(TypeError):
         binding.attn_qk_norm_rope(None, None)
+
+
+def test_the_package_offers_the_calls():
+    import exact_attention_70_gb300 as attn
+    for name in ("attn_kvcache_plan", "attn_qk_norm_rope", "attn_qk_norm_rope_bwd",
+                 "attn_kvcache_append_norm_rope", "attn_decode_kvcache_shared"):
+        assert name in attn.__all__ and getattr(attn, name) is getattr(binding, name)
