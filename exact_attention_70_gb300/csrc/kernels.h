@@ -370,7 +370,7 @@ struct SharedHeader {
 // Query rows that walk the same keys: up to two tiles of tokens, of one sequence against its own keys or of
 // a group against its prefix.  Its key blocks are cut into `pieces`, a piece's rows leave `split` parts
 // (few rows: one a warp); part s of kv head h lies at part + (h pieces split + s) rows.
-struct SharedUnit {
+struct alignas(16) SharedUnit {
     int q0, ntok;          // tokens [q0, q0 + ntok) of q
     int row;               // of block_table
     int key_min, key_end;  // keys [key_min, key_end)

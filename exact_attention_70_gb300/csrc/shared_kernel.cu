@@ -47,6 +47,7 @@ constexpr float kShLn2 = 0.69314718055994530942f;
 constexpr int kShUnitsThreads = 512;
 constexpr int kShFast = 1024;  // groups, and half the units, that the list's kernel keeps in shared memory
 constexpr int kShBins = 32;    // lengths that the list tells apart
+constexpr int kShLimbs = 3;    // of 20 bits
 // Shorter prefixes are read by every sequence.  (Near this size sharing costs about what it saves, a third
 // kernel against keys that L2 holds anyway: 64 sequences, 32:8 heads, on 128 shared keys 31.5 us (28.1 without
 // sharing), on 512 32.3 (35.7), on 1024 32.7 (44.6); 4 sequences on 512 12.8 (12.5), on 2048 14.8 (17.0).)
@@ -83,7 +84,10 @@ __device__ __forceinline__ bool sh_behind(const ShSeq& s, int prefix) {
     return s.n > 0 && prefix > 0 && prefix <= s.keys - s.n + 1;
 }
 
-__host__ __device__ __forceinline__ int ceil_div(int a, int b) { return (a + b - 1) / b; }
+// (of numbers that are not negative: an unsigned division is shorter)
+__host__ __device__ __forceinline__ int ceil_div(int a, int b) {
+    return static_cast<int>((static_cast<unsigned>(a) + b - 1) / static_cast<unsigned>(b));
+}
 
 // This thread's place behind the earlier lanes' n on a counter in shared memory (one atomic a warp).
 __device__ __forceinline__ int sh_reserve(int* counter, int n, int lane) {
@@ -109,17 +113,29 @@ __device__ __forceinline__ SharedUnit sh_unit(const SharedParams& p, int i) {
     return u;
 }
 
+// All of it but the fields that step 3 of the list's kernel writes: its third 16 bytes.
+__device__ __forceinline__ void sh_put(const SharedParams& p, int i, const SharedUnit& u) {
+    const int4* src = reinterpret_cast<const int4*>(&u);
+    int4* dst = reinterpret_cast<int4*>(p.units + i);
+    dst[0] = src[0];
+    dst[1] = src[1];
+    dst[3] = src[3];
+}
+
 __device__ __forceinline__ bool sh_few(int rows) { return rows <= kSharedSmallRows; }
 
 // Writes the list.  Where the parts lie and the order among units of a length depend on the warps' order;
 // no result does.  Items of a kind come longest pieces first (kShBins lengths), the kv heads of a piece
 // side by side (their keys lie side by side in the cache).
+// Bound by the latency of its steps, one after the other: 10,000 to 10,600 clocks (11,300 to 16,400 with idle warps in
+// every step, units in 4-byte stores, 64-bit atomics and a thread a unit that wrote its items).
 __global__ void __launch_bounds__(kShUnitsThreads) shared_units_kernel(const SharedParams p) {
     __shared__ int4 s_groups[kShFast];  // {first unit or -1, first token, first sequence, prefix}
     __shared__ int2 s_lengths[2 * kShFast];
     __shared__ int s_q0[kShFast], s_n[kShFast], s_keys[kShFast];
-    __shared__ int hist[2 * kShBins];
-    __shared__ unsigned long long work[2];  // key blocks of both kinds, for one kv head
+    __shared__ __align__(16) int hist[2 * kShBins];
+    __shared__ int place[2 * kShBins];
+    __shared__ unsigned work[2][kShLimbs];  // key blocks of both kinds, for one kv head
     __shared__ int n_prefix, n_own, n_parts;
     const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
     griddep_launch_dependents();  // (the attention kernels wait for the list, behind their set-up)
@@ -129,11 +145,12 @@ __global__ void __launch_bounds__(kShUnitsThreads) shared_units_kernel(const Sha
     int2* const lengths = p.max_units <= 2 * kShFast ? s_lengths : p.lengths;
     const long long max_keys = static_cast<long long>(p.max_pages) * p.page_size;
     if (tid < 2 * kShBins) hist[tid] = 0;
-    if (tid < 2) work[tid] = 0;
+    if (tid < 2 * kShLimbs) work[0][tid] = 0;
     if (tid == 0) n_prefix = n_own = n_parts = 0;
     bool bad = false;
-    for (int base = 0; base < max(p.batch, p.n_groups); base += kShUnitsThreads) {
-        const int b = base + tid;
+    // (here and below a warp that has nothing of it skips a stage: its instructions would hold up the others)
+    for (int base = 32 * warp; base < max(p.batch, p.n_groups); base += kShUnitsThreads) {
+        const int b = base + lane;
         const bool is_group = b < p.n_groups, is_seq = b < p.batch;
         int s0 = 0, s1 = 0, P = 0;
         ShSeq s = {0, 0, 0};
@@ -158,6 +175,7 @@ __global__ void __launch_bounds__(kShUnitsThreads) shared_units_kernel(const Sha
     const auto seq = [&](int b) { return near ? ShSeq{s_q0[b], s_n[b], s_keys[b]} : sh_seq(p, b); };
     const int per = 2 * p.tpt;  // tokens a unit
     const auto units_of = [&](int tokens) { return tokens <= per ? (tokens > 0 ? 1 : 0) : ceil_div(tokens, per); };
+    unsigned long long mine[2] = {0, 0};  // this thread's share of work
     // 1. a warp a group: which row of the table leads to the prefix, which tokens meet it, their units
     for (int i = warp; i < p.n_groups; i += kShUnitsThreads / 32) {
         const int s0 = groups[i].z, P = groups[i].w;
@@ -179,7 +197,7 @@ __global__ void __launch_bounds__(kShUnitsThreads) shared_units_kernel(const Sha
             if (lane == 0) at = atomicAdd(&n_prefix, n);
             at = __shfl_sync(0xffffffffu, at, 0);
             for (int u = lane; u < n; u += 32) {
-                SharedUnit x;
+                SharedUnit x = {};
                 x.q0 = q0 + u * per;
                 x.ntok = min(per, tokens - u * per);
                 x.row = first;
@@ -191,9 +209,9 @@ __global__ void __launch_bounds__(kShUnitsThreads) shared_units_kernel(const Sha
                 x.rows = x.ntok * p.g;
                 x.prefix = -1;
                 x.group_q0 = 0;
-                atomicAdd(&work[sh_few(x.rows)], static_cast<unsigned long long>(nblk));
+                mine[sh_few(x.rows)] += nblk;
                 if (at + u < p.own_base) {
-                    p.units[at + u] = x;
+                    sh_put(p, at + u, x);
                     lengths[at + u] = make_int2(nblk, x.rows);
                 }
             }
@@ -203,9 +221,8 @@ __global__ void __launch_bounds__(kShUnitsThreads) shared_units_kernel(const Sha
     }
     __syncthreads();
     // 2. a thread a sequence: the keys that its group's prefix leaves to it
-    unsigned long long mine[2] = {0, 0};
-    for (int base = 0; base < p.batch; base += kShUnitsThreads) {
-        const int b = base + tid;
+    for (int base = 32 * warp; base < p.batch; base += kShUnitsThreads) {
+        const int b = base + lane;
         ShSeq s = {0, 0, 0};
         if (b < p.batch) s = seq(b);
         const int n = units_of(s.n);
@@ -225,7 +242,7 @@ __global__ void __launch_bounds__(kShUnitsThreads) shared_units_kernel(const Sha
         }
         const int at = p.own_base + sh_reserve(&n_own, n, lane);
         for (int u = 0; u < n; ++u) {
-            SharedUnit x;
+            SharedUnit x = {};
             const int t0 = u * per;
             x.q0 = s.q0 + t0;
             x.ntok = min(per, s.n - t0);
@@ -240,29 +257,38 @@ __global__ void __launch_bounds__(kShUnitsThreads) shared_units_kernel(const Sha
             x.group_q0 = group_q0;
             mine[sh_few(x.rows)] += x.nblk;
             if (at + u < p.max_units) {
-                p.units[at + u] = x;
+                sh_put(p, at + u, x);
                 lengths[at + u] = make_int2(x.nblk, x.rows);
             }
         }
     }
 #pragma unroll
     for (int k = 0; k < 2; ++k) {
-#pragma unroll
-        for (int o = 16; o > 0; o >>= 1) mine[k] += __shfl_xor_sync(0xffffffffu, mine[k], o);
-        if (lane == 0 && mine[k] > 0) atomicAdd(&work[k], mine[k]);
+        if (!__any_sync(0xffffffffu, mine[k] > 0)) continue;
+        for (int i = 0; i < kShLimbs; ++i) {  // (no warp instruction adds 64 bits)
+            const unsigned sum = __reduce_add_sync(0xffffffffu, static_cast<unsigned>(mine[k] >> (20 * i)) & 0xfffffu);
+            if (lane == 0) atomicAdd(&work[k][i], sum);
+            if (!__any_sync(0xffffffffu, mine[k] >> (20 * i + 20) != 0)) break;
+        }
     }
     __syncthreads();
     const int n_pre = n_prefix, own = n_own;
     // (the host's bounds hold for every list that passed the checks above)
     const bool fits = n_pre <= p.own_base && p.own_base + own <= p.max_units;
     const int n_units = fits ? n_pre + own : 0;
-    int share[2];
-    float per_share[2];  // bins a key block
+    int share[2] = {1, 1};
+    float per_share[2] = {0.f, 0.f};  // bins a key block
+    if (32 * warp < n_units) {
 #pragma unroll
-    for (int k = 0; k < 2; ++k) {
-        const unsigned long long shares = k ? kSharedSmallShares : kSharedShares;
-        share[k] = max(static_cast<int>((work[k] * p.Hkv + shares - 1) / shares), kShMinPiece);
-        per_share[k] = static_cast<float>(kShBins) / static_cast<float>(share[k]);
+        for (int k = 0; k < 2; ++k) {
+            const unsigned long long shares = k ? kSharedSmallShares : kSharedShares;
+            unsigned long long all = 0;
+#pragma unroll
+            for (int i = 0; i < kShLimbs; ++i) all += static_cast<unsigned long long>(work[k][i]) << (20 * i);
+            // (no unit has 2^30 blocks)
+            share[k] = max(static_cast<int>(min((all * p.Hkv + shares - 1) / shares, 1ull << 30)), kShMinPiece);
+            per_share[k] = __fdividef(static_cast<float>(kShBins), static_cast<float>(share[k]));
+        }
     }
     // a unit's pieces and the list's bin of their length
     const auto cut = [&](int i, int& u, int& few, int& pieces, int& rows, int& bin) {
@@ -279,33 +305,35 @@ __global__ void __launch_bounds__(kShUnitsThreads) shared_units_kernel(const Sha
         }
     };
     // 3. pieces, and the places of their results
-    for (int base = 0; base < n_units; base += kShUnitsThreads) {
-        int u = 0, few = 0, pieces = 0, rows = 0, bin = 0;
-        const bool on = base + tid < n_units;
-        if (on) cut(base + tid, u, few, pieces, rows, bin);
+    int u = 0, few = 0, pieces = 0, rows = 0, bin = 0;  // of the thread's last unit
+    for (int base = 32 * warp; base < n_units; base += kShUnitsThreads) {
+        const bool on = base + lane < n_units;
+        pieces = 0;
+        if (on) cut(base + lane, u, few, pieces, rows, bin);
         const int split = few ? kSharedSmallSplit : 1;
         const int at = sh_reserve(&n_parts, pieces * split * p.Hkv * rows, lane);
         if (on) {
-            p.units[u].pieces = pieces;
-            p.units[u].split = split;
-            p.units[u].part = at;
+            *reinterpret_cast<int4*>(&p.units[u].pieces) = make_int4(pieces, split, at, rows);
             if (pieces > 0) atomicAdd(&hist[bin], pieces * p.Hkv);
         }
     }
     __syncthreads();
-    // 4. the bins' places (2 kShBins = 64: two a lane)
-    if (warp == 0) {
-        const int a = hist[2 * lane], b = hist[2 * lane + 1];
-        int x = a + b;
+    // 4. the bins' places: a thread a bin adds those before it (as a warp's scan it took 2100 clocks, so 900)
+    if (tid < 2 * kShBins) {
+        int before = 0, many = 0, all = 0;
 #pragma unroll
-        for (int o = 1; o < 32; o <<= 1) {
-            const int y = __shfl_up_sync(0xffffffffu, x, o);
-            if (lane >= o) x += y;
+        for (int i = 0; i < 2 * kShBins; i += 4) {
+            const int4 x = *reinterpret_cast<const int4*>(&hist[i]);
+            const int v[4] = {x.x, x.y, x.z, x.w};
+#pragma unroll
+            for (int e = 0; e < 4; ++e) {
+                before += i + e < tid ? v[e] : 0;
+                many += i < kShBins ? v[e] : 0;
+                all += v[e];
+            }
         }
-        hist[2 * lane] = x - a - b;
-        hist[2 * lane + 1] = x - b;
-        const int many = __shfl_sync(0xffffffffu, x, 15), all = __shfl_sync(0xffffffffu, x, 31);
-        if (lane == 0) {
+        place[tid] = before;
+        if (tid == 2 * kShBins - 1) {
             const bool ok = fits && n_parts <= p.max_parts && all <= p.max_items;
             if (!ok) atomicOr(p.status, kStatusBounds);
             SharedHeader* h = p.header;
@@ -319,26 +347,29 @@ __global__ void __launch_bounds__(kShUnitsThreads) shared_units_kernel(const Sha
     }
     __syncthreads();
     if (n_parts < 0) return;
-    // 5. items
+    // 5. items: a thread a unit finds their places, a warp or eight lanes a unit write them
+    int4* const out = s_groups;
+    const int lanes_log2 = n_units <= 128 ? 5 : 3, lanes = 1 << lanes_log2;
+    const int sub = tid & (lanes - 1), sub_s = sub / p.Hkv, sub_h = sub - sub_s * p.Hkv;
+    const int step_s = lanes / p.Hkv, step_h = lanes - step_s * p.Hkv;
     for (int base = 0; base < n_units; base += kShUnitsThreads) {
-        int u = 0, few = 0, pieces = 0, rows = 0, bin = 0, at = 0;
-        if (base + tid < n_units) cut(base + tid, u, few, pieces, rows, bin);
-        const int count = pieces * p.Hkv;
-        if (count > 0) at = atomicAdd(&hist[bin], count);
-        const bool many = count > 64;  // the whole warp writes those
-        if (!many) {
-            for (int s = 0, i = 0; s < pieces; ++s)
-                for (int h = 0; h < p.Hkv; ++h, ++i) p.items[at + i] = make_int2(u, s << 16 | h);
+        const int n = min(kShUnitsThreads, n_units - base);
+        if (tid < n) {
+            if (n_units > kShUnitsThreads) cut(base + tid, u, few, pieces, rows, bin);
+            const int count = pieces * p.Hkv;
+            out[tid] = make_int4(u, count > 0 ? atomicAdd(&place[bin], count) : 0, count, 0);
         }
-        for (unsigned m = __ballot_sync(0xffffffffu, many); m != 0; m &= m - 1) {
-            const int src = __ffs(m) - 1;
-            const int from = __shfl_sync(0xffffffffu, at, src), n = __shfl_sync(0xffffffffu, count, src);
-            const int unit = __shfl_sync(0xffffffffu, u, src);
-            for (int i = lane, s = lane / p.Hkv, h = lane - s * p.Hkv; i < n; i += 32) {
-                p.items[from + i] = make_int2(unit, s << 16 | h);
-                for (h += 32; h >= p.Hkv; h -= p.Hkv) ++s;
+        __syncthreads();
+        for (int i = tid >> lanes_log2; i < n; i += kShUnitsThreads >> lanes_log2) {
+            const int4 x = out[i];
+            for (int j = sub, s = sub_s, h = sub_h; j < x.z; j += lanes) {
+                p.items[x.y + j] = make_int2(x.x, s << 16 | h);
+                s += step_s;
+                h += step_h;
+                if (h >= p.Hkv) h -= p.Hkv, ++s;
             }
         }
+        if (base + kShUnitsThreads < n_units) __syncthreads();
     }
 }
 

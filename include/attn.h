@@ -575,8 +575,8 @@ attn_status_t attn_kvcache_append_norm_rope(
  * through its own row, as if it shared nothing; so are all of a group where fewer than two remain, or the
  * prefix has fewer than 128 keys.  Lengths that do not fit raise ATTN_ERR_DEVICE_BOUNDS, and
  * the call's results are unspecified; a page id outside [0, num_pages) raises it, and the results of the
- * sequences that read it are unspecified.  A NaN among the keys or values reaches the rows that see it, and may
- * reach other new tokens of its sequence.
+ * sequences that read it are unspecified.  A NaN or an infinity among the keys and values reaches the rows that
+ * see it, and may reach other new tokens of its sequence.
  */
 attn_status_t attn_decode_kvcache_shared(const void* q, const void* k_cache, const void* v_cache,
                                          const int32_t* cache_seqlens, const int32_t* block_table,
