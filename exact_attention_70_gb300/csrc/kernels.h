@@ -364,7 +364,8 @@ struct SharedHeader {
     int next_item[2];  // the claim counters of the two kernels
     int n_own;         // units of the sequences' own keys
     int bad;           // lengths that do not fit: nothing is computed
-    int pad[58];
+    int ctas;          // CTAs that do units with many rows
+    int pad[57];
 };
 
 // Query rows that walk the same keys: up to two tiles of tokens, of one sequence against its own keys or of
@@ -413,7 +414,7 @@ struct SharedParams {
     float scale_log2;
 };
 
-// Pieces that the work of units with many and with few rows is cut into, about: one and two CTAs an SM.
+// CTAs for units with many rows, at most, and pieces that the work of units with few is cut into, about: two to an SM.
 constexpr int kSharedShares = kGb300Sms, kSharedSmallShares = 2 * kGb300Sms;
 constexpr int kSharedSmallRows = 16;  // the rows of a unit that count as few
 constexpr int kSharedSmallSplit = 4;  // parts that their pieces leave

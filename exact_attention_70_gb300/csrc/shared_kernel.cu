@@ -8,23 +8,26 @@
 // heads of a kv head fill tiles of 128 rows.  Then every sequence meets the keys behind its prefix, and
 // a last kernel merges the parts.
 //
-// Four kernels, each starting while the one before it ends:
+// Three kernels, each starting while the one before it ends:
 //   * shared_units_kernel (one CTA) writes the list of the work: units (query rows that walk the same
-//     keys) cut into pieces of about 1 / 152 (1 / 304) of all the work, so that the CTAs finish together;
-//   * shared_attn_kernel does the units of more than 16 rows on tcgen05: one CTA an SM, persistent, two
-//     tiles of 128 rows on the same key blocks, roles and barriers as in the prefill kernel (fwd_kernel.cu):
-//     warp 16 gathers K and V blocks of 128 keys through block_table, a lane a page, into a ring of
-//     shared-memory slots (K_0, K_1, V_0, K_2, V_1, ..., V_{m-1}); warp 17 issues S_t = Q_t K^T, warp 18
-//     O_t += P_t V, accumulators in TMEM; warps 0-7 and 8-15 do the softmax of the two tiles, 16 rows a
-//     warp (one whose rows hold no token only keeps the barriers going); warp 19 claims items;
-//   * shared_small_kernel does the units of up to 16 rows on mma.sync;
+//     keys) cut into pieces that keep all CTAs busy to about the same end;
+//   * shared_attn_kernel, one CTA an SM, persistent.  Some of its CTAs, as many as the units of more than 16 rows are
+//     of the work, do those on tcgen05: two tiles of 128 rows on the same key blocks, roles and barriers as in
+//     the prefill kernel (fwd_kernel.cu): warp 16 gathers K and V blocks of 128 keys through block_table, a
+//     lane a page, into a ring of shared-memory slots (K_0, K_1, V_0, K_2, V_1, ..., V_{m-1}); warp 17 issues
+//     S_t = Q_t K^T, warp 18 O_t += P_t V, accumulators in TMEM; warps 0-7 and 8-15 do the softmax of the
+//     two tiles, 16 rows a warp (one whose rows hold no token only keeps the barriers going); warp 19 claims
+//     items.  The other CTAs, and these when they are done, do the units of up to 16 rows on mma.sync, each as two.
+//     (Where no unit can have more, shared_small_kernel does them.)
 //   * shared_combine_kernel merges the parts (O / l and log2 LSE of a piece, fp32).
-// Both sides of the 16 rows (all on tcgen05 / as it is): 4 sequences on 512 keys 15.7 / 12.4 us, 64 sequences of
-// 1K to 16K keys of their own, 32:8 heads, 356 / 343, 2 of 100K 211 / 132, 5 ragged documents 59.5 / 52.
+// Both sides of the 16 rows (all on tcgen05 / as it is): 4 sequences on 512 keys 16.9 / 12.8 us, 64 sequences of
+// 1K to 16K keys of their own, 32:8 heads, 361 / 351, 2 of 100K 212 / 130, 5 ragged documents 53.9 / 47.9.
 //
-// Measured in a captured graph, d 128, bf16, with the shares of the time: 64 requests on 32768 shared and 100 to
-// 2000 own keys, 32:8 heads: 97.5 us (units 7, prefix 33, own keys 47, merge 8; 421 MB, 4.3 TB/s over all);
-// 16 samples of 4 tokens on 100001 keys: 107 us (units 6, prefix 80, own keys 8, merge 8).  Own keys run at 6.4 TB/s.
+// Measured in a captured graph, d 128, bf16: 64 requests on 32768 shared and 100 to 2000 own keys, 32:8 heads:
+// 84.4 us (list 6, attention 73, merge 5; 421 MB, 5.0 TB/s over all); 16 samples of 4 tokens on 100001 keys:
+// 102.5 us (list 6, attention 90, merge 6).  With the two kinds in two kernels one after the other, all SMs on each, the
+// first took 97.5 us: the tiles' chain left a seventh of the memory's time idle, and one kernel's last CTAs and the
+// other's first loads another 10 us.
 // A block of 128 keys under two tiles takes 3100 to 3600 clocks where the memory would take 2800: the chain
 // S, softmax, P V of a tile, 16 warps at half their issue rate, is what bounds it, as in the prefill kernel.
 // Tried for it and not kept: P in tensor memory over S and five ring slots (the chain gets longer: 122 -> 136 us),
@@ -48,17 +51,27 @@ constexpr int kShUnitsThreads = 512;
 constexpr int kShFast = 1024;  // groups, and half the units, that the list's kernel keeps in shared memory
 constexpr int kShBins = 32;    // lengths that the list tells apart
 constexpr int kShLimbs = 3;    // of 20 bits
-// Shorter prefixes are read by every sequence.  (Near this size sharing costs about what it saves, a third
-// kernel against keys that L2 holds anyway: 64 sequences, 32:8 heads, on 128 shared keys 31.5 us (28.1 without
-// sharing), on 512 32.3 (35.7), on 1024 32.7 (44.6); 4 sequences on 512 12.8 (12.5), on 2048 14.8 (17.0).)
+// Shorter prefixes are read by every sequence.  (Near this size sharing saves little, keys that L2 holds anyway: 64
+// sequences, 32:8 heads, on 128 shared keys 25.8 us (26.2 without sharing), on 512 28.1 (34.8), on 1024 28.6 (45.7);
+// 4 sequences on 512 12.8 (12.5), on 2048 13.6 (13.8), on 8192 21.6 (25.8).)
 constexpr int kShMinPrefix = 128;
-// Key blocks a piece takes at least: 2 sequences on 4096 keys, 64:8 heads, 17.9 us (22.7 with 1, 17.1 with 4),
-// 4 on 512 12.4 (11.8, 13.6), 16 on 1024 19.3 (20.8, 21.7).
+// Key blocks a piece takes at least: 2 sequences on 4096 keys, 64:8 heads, 16.2 us (18.0 with 1, 15.5 with 4),
+// 4 on 512 12.8 (12.4, 14.2), on 2048 13.6 (15.0, 15.0).
 constexpr int kShMinPiece = 2;
+// Where there are units of both kinds, those of few rows are not a kernel's only work but fill what the others leave:
+// pieces of eight blocks (16 x 4 tokens on 100001 keys, 600 of their own: 105.3 us, 111.9 with two, 106.4 with four).
+constexpr int kShMinFewPiece = 8;
+// What a block under two tiles costs in blocks under few rows.  The CTAs are divided by it: the tiles' chain leaves
+// memory idle that the few rows' loads take (64 requests on 32768 shared and 100 to 2000 own keys: 84.2 us, 90.8 with
+// 1.6, 88.8 with 5, 97.8 with all CTAs on tiles first; 5 ragged documents 47.9, 53.2, 48.8, 57.1).
+constexpr float kShManyCost = 3.f;
 constexpr int kShCombineThreads = 256;
-// Rows up to which the merge gives a row eight warps, not four: 64 rows behind 16K shared keys 26.1 us (28.9 with
-// four), 128 rows behind 8K 22.6 (25.4); 512 rows behind 1K 20.7 (19.1), 2048 rows behind 32K 102 (98).
+// The merge gives a row eight warps up to kShFewRows rows, four up to kShMostRows (the blocks that are resident at
+// once), two beyond.  Few: 64 rows behind 16K shared keys 25.5 us (28.5 with four), 128 rows behind 8K 21.6 (24.5); 512
+// rows behind 1K 18.5 (18.2 with eight).  Most: 2048 rows behind 32K 84.4 (86.7 with four, 91.8 with eight), 4096
+// rows behind 8K 51.2 (56.0, 65.3), 1204 rows of ragged documents 47.9 (49.2 with two).
 constexpr int kShFewRows = kGb300Sms;
+constexpr int kShMostRows = 10 * kGb300Sms;
 constexpr int kShSoftmaxWarps = 16;
 
 // ---- units and items (one CTA) --------------------------------------------------------------------
@@ -136,7 +149,7 @@ __global__ void __launch_bounds__(kShUnitsThreads) shared_units_kernel(const Sha
     __shared__ __align__(16) int hist[2 * kShBins];
     __shared__ int place[2 * kShBins];
     __shared__ unsigned work[2][kShLimbs];  // key blocks of both kinds, for one kv head
-    __shared__ int n_prefix, n_own, n_parts;
+    __shared__ int n_prefix, n_own, n_parts, n_many, s_ctas;
     const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
     griddep_launch_dependents();  // (the attention kernels wait for the list, behind their set-up)
     // (generic addresses: shared memory as far as it goes)
@@ -146,7 +159,7 @@ __global__ void __launch_bounds__(kShUnitsThreads) shared_units_kernel(const Sha
     const long long max_keys = static_cast<long long>(p.max_pages) * p.page_size;
     if (tid < 2 * kShBins) hist[tid] = 0;
     if (tid < 2 * kShLimbs) work[0][tid] = 0;
-    if (tid == 0) n_prefix = n_own = n_parts = 0;
+    if (tid == 0) n_prefix = n_own = n_parts = n_many = 0;
     bool bad = false;
     // (here and below a warp that has nothing of it skips a stage: its instructions would hold up the others)
     for (int base = 32 * warp; base < max(p.batch, p.n_groups); base += kShUnitsThreads) {
@@ -169,6 +182,7 @@ __global__ void __launch_bounds__(kShUnitsThreads) shared_units_kernel(const Sha
             SharedHeader* h = p.header;
             h->n_items[0] = h->n_items[1] = h->next_item[0] = h->next_item[1] = h->n_own = 0;
             h->bad = 1;
+            h->ctas = 0;
         }
         return;
     }
@@ -176,6 +190,7 @@ __global__ void __launch_bounds__(kShUnitsThreads) shared_units_kernel(const Sha
     const int per = 2 * p.tpt;  // tokens a unit
     const auto units_of = [&](int tokens) { return tokens <= per ? (tokens > 0 ? 1 : 0) : ceil_div(tokens, per); };
     unsigned long long mine[2] = {0, 0};  // this thread's share of work
+    int many_units = 0;
     // 1. a warp a group: which row of the table leads to the prefix, which tokens meet it, their units
     for (int i = warp; i < p.n_groups; i += kShUnitsThreads / 32) {
         const int s0 = groups[i].z, P = groups[i].w;
@@ -210,6 +225,7 @@ __global__ void __launch_bounds__(kShUnitsThreads) shared_units_kernel(const Sha
                 x.prefix = -1;
                 x.group_q0 = 0;
                 mine[sh_few(x.rows)] += nblk;
+                many_units += !sh_few(x.rows);
                 if (at + u < p.own_base) {
                     sh_put(p, at + u, x);
                     lengths[at + u] = make_int2(nblk, x.rows);
@@ -256,6 +272,7 @@ __global__ void __launch_bounds__(kShUnitsThreads) shared_units_kernel(const Sha
             x.prefix = prefix;
             x.group_q0 = group_q0;
             mine[sh_few(x.rows)] += x.nblk;
+            many_units += !sh_few(x.rows) && x.nblk > 0;
             if (at + u < p.max_units) {
                 sh_put(p, at + u, x);
                 lengths[at + u] = make_int2(x.nblk, x.rows);
@@ -265,6 +282,10 @@ __global__ void __launch_bounds__(kShUnitsThreads) shared_units_kernel(const Sha
 #pragma unroll
     for (int k = 0; k < 2; ++k) {
         if (!__any_sync(0xffffffffu, mine[k] > 0)) continue;
+        if (k == 0) {
+            const int n = __reduce_add_sync(0xffffffffu, many_units);
+            if (lane == 0) atomicAdd(&n_many, n);
+        }
         for (int i = 0; i < kShLimbs; ++i) {  // (no warp instruction adds 64 bits)
             const unsigned sum = __reduce_add_sync(0xffffffffu, static_cast<unsigned>(mine[k] >> (20 * i)) & 0xfffffu);
             if (lane == 0) atomicAdd(&work[k][i], sum);
@@ -276,17 +297,27 @@ __global__ void __launch_bounds__(kShUnitsThreads) shared_units_kernel(const Sha
     // (the host's bounds hold for every list that passed the checks above)
     const bool fits = n_pre <= p.own_base && p.own_base + own <= p.max_units;
     const int n_units = fits ? n_pre + own : 0;
-    int share[2] = {1, 1};
+    int share[2] = {1, 1}, ctas = 1;
     float per_share[2] = {0.f, 0.f};  // bins a key block
     if (32 * warp < n_units) {
+        unsigned long long all[2] = {0, 0};
+#pragma unroll
+        for (int i = 0; i < kShLimbs; ++i) {
+            all[0] += static_cast<unsigned long long>(work[0][i]) << (20 * i);
+            all[1] += static_cast<unsigned long long>(work[1][i]) << (20 * i);
+        }
+        if (all[0] > 0) {
+            const float a = kShManyCost * static_cast<float>(all[0]);
+            const int n = static_cast<int>(ceilf(kSharedShares * __fdividef(a, a + static_cast<float>(all[1]))));
+            ctas = min(max(n, 1), kSharedShares);
+        }
 #pragma unroll
         for (int k = 0; k < 2; ++k) {
-            const unsigned long long shares = k ? kSharedSmallShares : kSharedShares;
-            unsigned long long all = 0;
-#pragma unroll
-            for (int i = 0; i < kShLimbs; ++i) all += static_cast<unsigned long long>(work[k][i]) << (20 * i);
+            // (a unit's last piece is short by half a piece, about: so many more come out than shares)
+            const unsigned shares = k ? kSharedSmallShares : ctas == kSharedShares ? ctas : max(ctas - n_many * p.Hkv / 2, (ctas + 1) / 2);
             // (no unit has 2^30 blocks)
-            share[k] = max(static_cast<int>(min((all * p.Hkv + shares - 1) / shares, 1ull << 30)), kShMinPiece);
+            share[k] = max(static_cast<int>(min((all[k] * p.Hkv + shares - 1) / shares, 1ull << 30)),
+                           k != 0 && all[0] > 0 ? kShMinFewPiece : kShMinPiece);
             per_share[k] = __fdividef(static_cast<float>(kShBins), static_cast<float>(share[k]));
         }
     }
@@ -304,6 +335,7 @@ __global__ void __launch_bounds__(kShUnitsThreads) shared_units_kernel(const Sha
                   min(static_cast<int>(static_cast<float>(len - 1) * per_share[few]), kShBins - 1);
         }
     };
+    if (tid == 0) s_ctas = ctas;
     // 3. pieces, and the places of their results
     int u = 0, few = 0, pieces = 0, rows = 0, bin = 0;  // of the thread's last unit
     for (int base = 32 * warp; base < n_units; base += kShUnitsThreads) {
@@ -342,6 +374,7 @@ __global__ void __launch_bounds__(kShUnitsThreads) shared_units_kernel(const Sha
             h->next_item[0] = h->next_item[1] = 0;
             h->n_own = ok ? own : 0;
             h->bad = ok ? 0 : 1;
+            h->ctas = many <= kSharedShares ? many : s_ctas;  // (no item waits for another where all can go at once)
             if (!ok) n_parts = -1;
         }
     }
@@ -387,7 +420,8 @@ struct ShCfg {
     static constexpr int kOffP = kOffQ + 2 * kQTile;
     static constexpr int kOffKV = kOffP + 2 * kPTile;
     static constexpr int kOffBar = kOffKV + kSlots * kKvTile;
-    static constexpr int kSmem = kOffBar + 768 + 1024;
+    static constexpr int kOffFew = kOffBar + 768;  // two SmBars
+    static constexpr int kSmem = kOffFew + 1024 + 1024;
     static_assert(kSmem <= 227 * 1024, "shared memory per CTA");
     static constexpr uint32_t kTmemCols = 512;
     __device__ static constexpr uint32_t col_s(int t) { return 128u * t; }
@@ -416,7 +450,7 @@ struct ShBars {
     uint64_t near_end;  // the producer is about to be done with its item
     ShItem ring[kShRing];
     uint32_t tmem_base;
-    int abort_flag;
+    int abort_flag, few_left;
 };
 static_assert(sizeof(ShBars) <= 768, "barrier block");
 
@@ -429,10 +463,11 @@ __device__ __forceinline__ uint32_t sh_parity(uint32_t bits, uint32_t st) { retu
 // Warp 19 claims items and works them out when the producer is about to be done with the one before, so that no
 // load waits for it and CTAs take items as they free up (claimed as the one before begins, the CTAs that
 // have the longest items take the next longest as well: 64 requests behind 32K keys 105 -> 127 us).  The first
-// one is the block's own, later ones come off a counter.
+// one is the block's own where `ctas` blocks begin with this half of the list, all others (with 0: all) come off a
+// counter.
 // kKind: which of the list's two halves.
 template <int kKind, int kSlots, typename Bars>
-__device__ void sh_scheduler(const SharedParams& p, Bars* bars, const Watchdog& wd, int lane) {
+__device__ void sh_scheduler(const SharedParams& p, Bars* bars, const Watchdog& wd, int ctas, int lane) {
     const int first = kKind ? __ldcg(&p.header->n_items[0]) : 0, n_items = __ldcg(&p.header->n_items[kKind]);
     uint32_t kv = 0, vpar = 0;
     for (uint32_t r = 0;; ++r) {
@@ -441,8 +476,8 @@ __device__ void sh_scheduler(const SharedParams& p, Bars* bars, const Watchdog& 
         if (r >= 1) ok = ok && wd.wait(&bars->near_end, (r - 1) & 1);
         if (!__all_sync(0xffffffffu, ok)) return;
         int idx = blockIdx.x;
-        if (r > 0) {
-            if (lane == 0) idx = gridDim.x + atomicAdd(&p.header->next_item[kKind], 1);
+        if (r > 0 || ctas == 0) {
+            if (lane == 0) idx = ctas + atomicAdd(&p.header->next_item[kKind], 1);
             idx = __shfl_sync(0xffffffffu, idx, 0);
         }
         ShItem it = {};
@@ -904,82 +939,11 @@ __device__ void sh_softmax(const SharedParams& p, uint8_t* smem, ShBars* bars, u
     }
 }
 
-template <int D>
-__global__ void __launch_bounds__(kFwdThreads, 1) shared_attn_kernel(const __grid_constant__ SharedParams p) {
-    using C = ShCfg<D>;
-    extern __shared__ uint8_t smem_raw[];
-    uint8_t* smem = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) &
-                                               ~static_cast<uintptr_t>(1023));
-    ShBars* bars = reinterpret_cast<ShBars*>(smem + C::kOffBar);
-    const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
-    if (threadIdx.x == 0) {
-        mbar_init(&bars->q_full, 1);
-        mbar_init(&bars->q_empty, 1);
-        for (int i = 0; i < C::kSlots; ++i) {
-            mbar_init(&bars->k_full[i], 1);
-            mbar_init(&bars->v_full[i], 1);
-            mbar_init(&bars->kv_empty[i], 1);
-        }
-        for (int t = 0; t < 2; ++t) {
-            mbar_init(&bars->s_full[t], 1);
-            mbar_init(&bars->s_free[t], kShSoftmaxWarps / 2);
-            mbar_init(&bars->p_full[t], kShSoftmaxWarps / 2);
-            mbar_init(&bars->pv_done[t], 1);
-            mbar_init(&bars->o_free[t], kShSoftmaxWarps / 2);
-            mbar_init(&bars->drain[t], 1);
-        }
-        for (uint32_t i = 0; i < kShRing; ++i) {
-            mbar_init(&bars->idx_full[i], 1);
-            mbar_init(&bars->idx_empty[i], kShReaders);
-        }
-        mbar_init(&bars->near_end, 1);
-        bars->abort_flag = 0;
-        mbar_fence_init();
-    }
-    if (warp == kShSoftmaxWarps + 1) tmem_alloc(&bars->tmem_base, C::kTmemCols);
-    tc_fence_before();
-    __syncthreads();
-    tc_fence_after();
-    const uint32_t tmem = bars->tmem_base;
-    const Watchdog wd{&bars->abort_flag, p.status};
-    griddep_wait();  // the list, and what stands before this call
-    griddep_launch_dependents();  // (from here on the list may be read without waiting)
-    // registers as in fwd_kernel.cu: 128 * 64 + 512 * 104 = 640 * 96
-    if (warp >= kShSoftmaxWarps) {
-        regs_decrease<64>();
-        if (warp == kShSoftmaxWarps) {
-            sh_producer<D>(p, smem, bars, wd, lane);
-        } else if (warp == kShSoftmaxWarps + 3) {
-            sh_scheduler<0, C::kSlots>(p, bars, wd, lane);
-        } else {
-            if (lane == 0) {
-                const int w = warp - kShSoftmaxWarps - 1;
-                if (w == 0)
-                    sh_mma_s<D>(p, smem, bars, tmem, wd);
-                else
-                    sh_mma_pv<D>(p, smem, bars, tmem, wd);
-                umma_commit(&bars->drain[w]);
-                sh_drain(&bars->drain[w], 0);
-            }
-        }
-    } else {
-        regs_increase<104>();
-        sh_softmax<D>(p, smem, bars, tmem, wd, warp >> 3, warp & 7, lane);
-    }
-    __syncwarp();
-    tc_fence_before();
-    __syncthreads();
-    if (warp == kShSoftmaxWarps + 1) {
-        tc_fence_after();
-        tmem_dealloc(tmem, C::kTmemCols);
-    }
-}
-
 // ---- few rows -------------------------------------------------------------------------------------------
 //
 // Units of up to 16 rows (a sequence's single query, a few sequences' behind a prefix) would fill an eighth of a
 // tile, and one warp's softmax over it, 3000 clocks a block, would be slower than the memory.  As in
-// decode_kernel.cu four warps take 16 keys each of a chunk of 64, on mma.sync m16n8k16, two CTAs an SM.
+// decode_kernel.cu four warps take 16 keys each of a chunk of 64, on mma.sync m16n8k16, twice an SM.
 // The warps never meet: each leaves a part of its own.
 
 template <int D>
@@ -1202,10 +1166,21 @@ __device__ void sm_consumer(const SharedParams& p, uint8_t* smem, SmBars* bars, 
     }
 }
 
-// kBehind: launched behind shared_attn_kernel, which lets this kernel start when the list is there.  Its
-// blocks take the SMs as that kernel's leave them, and end when it has ended, so that what waits for this
-// kernel waits for both.
-template <int D, bool kBehind>
+__device__ void sm_init(SmBars* bars) {
+    for (int i = 0; i < 6; ++i) {
+        mbar_init(&bars->full[i], 1);
+        mbar_init(&bars->empty[i], 4);
+    }
+    for (uint32_t i = 0; i < kShRing; ++i) {
+        mbar_init(&bars->idx_full[i], 1);
+        mbar_init(&bars->idx_empty[i], kSmReaders);
+    }
+    mbar_init(&bars->near_end, 1);
+    bars->abort_flag = 0;
+}
+
+// Where no unit has many rows.
+template <int D>
 __global__ void __launch_bounds__(kSmThreads, 2) shared_small_kernel(const __grid_constant__ SharedParams p) {
     using C = SmCfg<D>;
     extern __shared__ uint8_t smem_raw[];
@@ -1214,22 +1189,13 @@ __global__ void __launch_bounds__(kSmThreads, 2) shared_small_kernel(const __gri
     SmBars* bars = reinterpret_cast<SmBars*>(smem + C::kOffBar);
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
     if (threadIdx.x == 0) {
-        for (int i = 0; i < C::kStages; ++i) {
-            mbar_init(&bars->full[i], 1);
-            mbar_init(&bars->empty[i], 4);
-        }
-        for (uint32_t i = 0; i < kShRing; ++i) {
-            mbar_init(&bars->idx_full[i], 1);
-            mbar_init(&bars->idx_empty[i], kSmReaders);
-        }
-        mbar_init(&bars->near_end, 1);
-        bars->abort_flag = 0;
+        sm_init(bars);
         mbar_fence_init();
         tma_prefetch_desc(&p.tm_k64);
         tma_prefetch_desc(&p.tm_v64);
     }
     __syncthreads();
-    if (!kBehind) griddep_wait();
+    griddep_wait();
     griddep_launch_dependents();
     const Watchdog wd{&bars->abort_flag, p.status};
     if (warp < 4)
@@ -1237,18 +1203,116 @@ __global__ void __launch_bounds__(kSmThreads, 2) shared_small_kernel(const __gri
     else if (warp == 4)
         sm_producer<D>(p, smem, bars, wd, lane);
     else
-        sh_scheduler<1, 1>(p, bars, wd, lane);
-    if (kBehind) griddep_wait();
+        sh_scheduler<1, 1>(p, bars, wd, gridDim.x, lane);
+}
+
+// ---- many rows, then few ----------------------------------------------------------------------------------
+
+template <int D>
+__global__ void __launch_bounds__(kFwdThreads, 1) shared_attn_kernel(const __grid_constant__ SharedParams p) {
+    using C = ShCfg<D>;
+    extern __shared__ uint8_t smem_raw[];
+    uint8_t* smem = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) &
+                                               ~static_cast<uintptr_t>(1023));
+    ShBars* bars = reinterpret_cast<ShBars*>(smem + C::kOffBar);
+    SmBars* few = reinterpret_cast<SmBars*>(smem + C::kOffFew);
+    const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+    if (threadIdx.x == 0) {
+        mbar_init(&bars->q_full, 1);
+        mbar_init(&bars->q_empty, 1);
+        for (int i = 0; i < C::kSlots; ++i) {
+            mbar_init(&bars->k_full[i], 1);
+            mbar_init(&bars->v_full[i], 1);
+            mbar_init(&bars->kv_empty[i], 1);
+        }
+        for (int t = 0; t < 2; ++t) {
+            mbar_init(&bars->s_full[t], 1);
+            mbar_init(&bars->s_free[t], kShSoftmaxWarps / 2);
+            mbar_init(&bars->p_full[t], kShSoftmaxWarps / 2);
+            mbar_init(&bars->pv_done[t], 1);
+            mbar_init(&bars->o_free[t], kShSoftmaxWarps / 2);
+            mbar_init(&bars->drain[t], 1);
+        }
+        for (uint32_t i = 0; i < kShRing; ++i) {
+            mbar_init(&bars->idx_full[i], 1);
+            mbar_init(&bars->idx_empty[i], kShReaders);
+        }
+        mbar_init(&bars->near_end, 1);
+        bars->abort_flag = 0;
+        for (int v = 0; v < 2; ++v) sm_init(few + v);
+        mbar_fence_init();
+    }
+    if (warp == kShSoftmaxWarps + 1) tmem_alloc(&bars->tmem_base, C::kTmemCols);
+    tc_fence_before();
+    __syncthreads();
+    tc_fence_after();
+    const uint32_t tmem = bars->tmem_base;
+    const Watchdog wd{&bars->abort_flag, p.status};
+    griddep_wait();  // the list, and what stands before this call
+    griddep_launch_dependents();  // (from here on the list may be read without waiting)
+    const int ctas = min(__ldcg(&p.header->ctas), static_cast<int>(gridDim.x));
+    const bool many = static_cast<int>(blockIdx.x) < ctas;
+    // registers as in fwd_kernel.cu: 128 * 64 + 512 * 104 = 640 * 96
+    if (warp >= kShSoftmaxWarps) {
+        regs_decrease<64>();
+        if (warp == kShSoftmaxWarps + 3) {
+            if (many) sh_scheduler<0, C::kSlots>(p, bars, wd, ctas, lane);
+            if (lane == 0)  // (read while the last item is done)
+                bars->few_left = __ldcg(&p.header->next_item[1]) < __ldcg(&p.header->n_items[1]);
+        } else if (!many) {
+        } else if (warp == kShSoftmaxWarps) {
+            sh_producer<D>(p, smem, bars, wd, lane);
+        } else {
+            if (lane == 0) {
+                const int w = warp - kShSoftmaxWarps - 1;
+                if (w == 0)
+                    sh_mma_s<D>(p, smem, bars, tmem, wd);
+                else
+                    sh_mma_pv<D>(p, smem, bars, tmem, wd);
+                umma_commit(&bars->drain[w]);
+                sh_drain(&bars->drain[w], 0);
+            }
+        }
+    } else {
+        regs_increase<104>();
+        if (many) sh_softmax<D>(p, smem, bars, tmem, wd, warp >> 3, warp & 7, lane);
+    }
+    __syncwarp();
+    fence_proxy_async_smem();  // (what has been written here is loaded over below)
+    tc_fence_before();
+    __syncthreads();
+    if (warp == kShSoftmaxWarps + 1) {
+        tc_fence_after();
+        tmem_dealloc(tmem, C::kTmemCols);
+    }
+    if (bars->few_left == 0 || bars->abort_flag != 0) return;
+    // The CTA becomes two of the other kind: warps 0-3 and 4-7 on mma.sync, 8 and 12 their producers, 9 and 13
+    // their schedulers.  Registers: 256 * 168 + 384 * 48 = 640 * 96
+    static_assert(2 * SmCfg<D>::kOffBar <= C::kOffBar && 2 * sizeof(SmBars) <= 1024, "both in one CTA's shared memory");
+    const int v = warp < 8 ? warp >> 2 : (warp >> 2) & 1, w = warp & 3;
+    uint8_t* const half = smem + v * SmCfg<D>::kOffBar;
+    const Watchdog wd2{&few[v].abort_flag, p.status};
+    if (warp < 8) {
+        regs_increase<168>();
+        sm_consumer<D>(p, half, few + v, wd2, w, lane);
+    } else {
+        regs_decrease<48>();
+        if (warp >= kShSoftmaxWarps) return;
+        if (w == 0)
+            sm_producer<D>(p, half, few + v, wd2, lane);
+        else if (w == 1)
+            sh_scheduler<1, 1>(p, few + v, wd2, 0, lane);
+    }
 }
 
 // ---- merge --------------------------------------------------------------------------------------------
 
-// Four or eight warps have a row, eight parts each at a time, whose loads all go out together: block (i, h, j)
+// Two, four or eight warps have a row, eight parts each at a time, whose loads all go out together: block (i, h, j)
 // has rows kRows j .. kRows j + kRows - 1 of sequence unit i for kv head h.  LSE = log2 sum_s 2^LSE_s,
 // O = sum_s 2^(LSE_s - LSE) O_s over the parts of the row's prefix and of its own keys; no part, or none with
 // a key: O = 0, LSE = -inf.
-// Bound by the latency of the parts' loads, and by L2 where there are many: 2048 rows of 22 parts took 9 us
-// with a warp a row, three times eight parts one after the other, and take 8 (23 MB).
+// Bound by the latency of the parts' loads, and by L2 where there are many: of a call's time 1 us with 32 rows, 3 with
+// 1204, 5 with 2048 rows of 37 parts (38 MB); with a warp a row, three times eight parts one after the other, a us more.
 template <int D, int kRows>
 __global__ void __launch_bounds__(kShCombineThreads) shared_combine_kernel(const SharedParams p) {
     constexpr int E = D / 32, kWarps = kShCombineThreads / 32 / kRows, kBatch = 8;
@@ -1376,10 +1440,8 @@ cudaError_t configure_shared_kernels() {
     const cudaFuncAttribute smem = cudaFuncAttributeMaxDynamicSharedMemorySize;
     cudaError_t e = cudaFuncSetAttribute(shared_attn_kernel<128>, smem, ShCfg<128>::kSmem);
     if (e == cudaSuccess) e = cudaFuncSetAttribute(shared_attn_kernel<64>, smem, ShCfg<64>::kSmem);
-    if (e == cudaSuccess) e = cudaFuncSetAttribute(shared_small_kernel<128, false>, smem, SmCfg<128>::kSmem);
-    if (e == cudaSuccess) e = cudaFuncSetAttribute(shared_small_kernel<64, false>, smem, SmCfg<64>::kSmem);
-    if (e == cudaSuccess) e = cudaFuncSetAttribute(shared_small_kernel<128, true>, smem, SmCfg<128>::kSmem);
-    if (e == cudaSuccess) e = cudaFuncSetAttribute(shared_small_kernel<64, true>, smem, SmCfg<64>::kSmem);
+    if (e == cudaSuccess) e = cudaFuncSetAttribute(shared_small_kernel<128>, smem, SmCfg<128>::kSmem);
+    if (e == cudaSuccess) e = cudaFuncSetAttribute(shared_small_kernel<64>, smem, SmCfg<64>::kSmem);
     return e;
 }
 
@@ -1390,19 +1452,16 @@ cudaError_t launch_shared_attn_d(const SharedParams& p, int num_sms, int own_uni
     shared_units_kernel<<<1, kShUnitsThreads, 0, stream>>>(p);
     cudaError_t e = cudaGetLastError();
     if (e != cudaSuccess) return e;
-    const bool many = p.many;
-    if (many) {
-        e = launch_dependent(shared_attn_kernel<D>, dim3(num_sms), kFwdThreads, ShCfg<D>::kSmem, p, stream);
-        if (e != cudaSuccess) return e;
-    }
-    e = launch_dependent(many ? shared_small_kernel<D, true> : shared_small_kernel<D, false>, dim3(2 * num_sms),
-                         kSmThreads, SmCfg<D>::kSmem, p, stream);
+    e = p.many ? launch_dependent(shared_attn_kernel<D>, dim3(num_sms), kFwdThreads, ShCfg<D>::kSmem, p, stream)
+               : launch_dependent(shared_small_kernel<D>, dim3(2 * num_sms), kSmThreads, SmCfg<D>::kSmem, p, stream);
     if (e != cudaSuccess) return e;
     // a unit's rows, at most (max_seqlen_q may be 0, a grid not)
     const int rows = std::max(std::min(p.max_seqlen_q, 2 * p.tpt), 1) * p.g;
     const bool few = static_cast<long long>(p.total_q) * p.Hq <= kShFewRows;
-    return launch_dependent(few ? shared_combine_kernel<D, 1> : shared_combine_kernel<D, 2>,
-                            dim3(own_units, p.Hkv, few ? rows : ceil_div(rows, 2)), kShCombineThreads, 0, p, stream);
+    const bool most = static_cast<long long>(p.total_q) * p.Hq > kShMostRows;
+    const int per = few ? 1 : most ? 4 : 2;
+    return launch_dependent(few ? shared_combine_kernel<D, 1> : most ? shared_combine_kernel<D, 4> : shared_combine_kernel<D, 2>,
+                            dim3(own_units, p.Hkv, ceil_div(rows, per)), kShCombineThreads, 0, p, stream);
 }
 
 }  // namespace
