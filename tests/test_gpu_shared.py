@@ -234,6 +234,20 @@ def test_random_configurations(attn, seed):  # noqa: F811
     check(attn, shared_case(groups, Hq, Hkv, d, ps, seed=seed, decode=top == 1), (seed, groups))
 
 
+@pytest.mark.parametrize("groups,Hq,Hkv,d", [
+    ([(150, [(1, 300 + 3 * i) for i in range(120)])], 8, 8, 64),                     # few rows: most of the work
+    ([(4000, [(1, 20 * (i % 7)) for i in range(40)])] * 2, 8, 2, 128),               # few rows: a small part of it
+    ([(700, [(1, 90 * (i % 5)) for i in range(20)])] * 24, 8, 8, 64),                # more tiles than CTAs
+    ([(260, [(17, 30)] * 3 + [(1, 500)] * 30), (200, [(2, 5)] * 30)], 4, 4, 128)],   # both kinds among the own keys
+    ids=["few", "many", "tiles", "own"])
+def test_units_of_both_kinds(attn, groups, Hq, Hkv, d):  # noqa: F811
+    decode = all(n == 1 for _, seqs in groups for n, _ in seqs)
+    c = shared_case(groups, Hq, Hkv, d, 16, seed=60, decode=decode)
+    out, lse = check(attn, c)
+    for _ in range(5):
+        assert all(torch.equal(a, b) for a, b in zip((out, lse), call(attn, dev(c))))
+
+
 def test_a_long_prefix_in_many_pieces(attn):  # noqa: F811
     c = shared_case([(20011, [(1, 3), (1, 2000), (1, 77)])], 4, 2, 128, 64, seed=24)
     check(attn, c)
