@@ -13,6 +13,7 @@
 
 #include "attn.h"
 #include "kernels.h"
+#include "step_kernels.h"
 #include "tile_math.h"
 
 namespace attn {

@@ -15,8 +15,8 @@
 
 #include <algorithm>
 
-#include "kernels.h"
 #include "ptx.cuh"
+#include "step_kernels.h"
 
 namespace attn {
 

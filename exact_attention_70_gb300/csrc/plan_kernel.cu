@@ -6,8 +6,8 @@
 // other.  Every new page starts with a new token, so one thread a token does all of it: the token at
 // position p with p % page_size == 0 also writes the page into the table.  The offsets (of tokens and
 // of pages) are scans over the sequences, done by one CTA before.
-#include "kernels.h"
 #include "ptx.cuh"
+#include "step_kernels.h"
 
 namespace attn {
 

@@ -37,8 +37,8 @@
 
 #include <algorithm>
 
-#include "kernels.h"
 #include "ptx.cuh"
+#include "step_kernels.h"
 #include "tile_math.h"
 
 namespace attn {
