@@ -168,8 +168,8 @@ cudaError_t launch_plan(const PlanParams& p, cudaStream_t stream) {
         return cudaGetLastError();
     }
     plan_scan_kernel<<<1, kPlanThreads, 0, stream>>>(p);
-    cudaError_t e = cudaGetLastError();
-    if (e != cudaSuccess) return e;
+    const cudaError_t e = cudaGetLastError();
+    if (e != cudaSuccess || p.total_q == 0) return e;  // (no tokens: no pages either, and a grid may not be empty)
     cudaLaunchConfig_t cfg = {};
     cfg.gridDim = dim3((static_cast<unsigned>(p.total_q) + kPlanTokenThreads - 1) / kPlanTokenThreads);
     cfg.blockDim = dim3(kPlanTokenThreads);

@@ -80,6 +80,28 @@ def test_many_tokens_and_many_sequences(attn):
     run(attn, [i % 40 for i in range(65535)], [i % 3 for i in range(65535)], 16, seed=2)
 
 
+@pytest.mark.parametrize("B", [2048, 2049, 65535])
+def test_no_tokens_of_many_sequences(attn, B):
+    """On both sides of the sizes that take one launch: a step in which nobody has a new token, and a call
+    behind it, which would report a launch error that the first left behind."""
+    ctx = [i % 40 for i in range(B)]
+    run(attn, ctx, [0] * B, 16, seed=5)
+    run(attn, [15], [3], 16, seed=6)
+    ctx, new, t, free, count = ints(ctx), ints([0] * B), ints([[0, 1, 2]] * B), ints([]), ints([0])
+    side = torch.cuda.Stream()
+    side.wait_stream(torch.cuda.current_stream())
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph, stream=side):
+        cu, after, positions, slots, left = attn.attn_kvcache_plan(ctx, new, t, free, count, 16, 3, 0)
+    graph.replay()
+    torch.cuda.synchronize()
+    assert not cu.any() and torch.equal(after, ctx) and left.tolist() == [0]
+    assert positions.shape == slots.shape == (0,) and (t == ints([0, 1, 2])).all()
+    # lengths that do not fit are reported here too
+    after = attn.attn_kvcache_plan(ctx, new - 1, t, free, count, 16, 3, 0)[1]
+    assert torch.equal(after, ctx) and attn.attn_get_device_status() == -6
+
+
 def test_no_sequences(attn):
     t = torch.empty((0, 4), dtype=torch.int32, device="cuda")
     e = ints([])
