@@ -18,7 +18,8 @@
 //     S_t = Q_t K^T, warp 18 O_t += P_t V, accumulators in TMEM; warps 0-7 and 8-15 do the softmax of the
 //     two tiles, 16 rows a warp (one whose rows hold no token only keeps the barriers going); warp 19 claims
 //     items.  The other CTAs, and these when they are done, do the units of up to 16 rows on mma.sync, each as two.
-//     (Where no unit can have more, shared_small_kernel does them.)
+//     (Where the host can tell that no unit has more, by all tokens of the call or, without groups, by the most of a
+//     sequence, shared_small_kernel does them.)
 //   * shared_combine_kernel merges the parts (O / l and log2 LSE of a piece, fp32).
 // Both sides of the 16 rows (all on tcgen05 / as it is): 4 sequences on 512 keys 16.9 / 12.8 us, 64 sequences of
 // 1K to 16K keys of their own, 32:8 heads, 361 / 351, 2 of 100K 212 / 130, 5 ragged documents 53.9 / 47.9.
@@ -1179,7 +1180,7 @@ __device__ void sm_init(SmBars* bars) {
     bars->abort_flag = 0;
 }
 
-// Where no unit has many rows.
+// Where no unit can have many rows.
 template <int D>
 __global__ void __launch_bounds__(kSmThreads, 2) shared_small_kernel(const __grid_constant__ SharedParams p) {
     using C = SmCfg<D>;

@@ -118,7 +118,7 @@ struct SharedParams {
     const int* prefix_lens;
     unsigned* status;
     int batch, n_groups, total_q, max_seqlen_q, Hq, Hkv, g, tpt;
-    int many;  // some unit may have many rows (else tm_q, tm_q1 are not there)
+    int many;  // some unit may have many rows, as far as the host knows (else tm_q, tm_q1 are not there)
     int page_size, box_rows, max_pages, num_pages;
     int max_units, max_items, max_parts, own_base;
     int lse_head, lse_tok;  // strides of lse

@@ -169,6 +169,32 @@ def test_without_groups(attn):  # noqa: F811
     assert attn.attn_get_device_status() == 0
 
 
+@pytest.mark.filterwarnings("ignore:DEBUG")
+@pytest.mark.parametrize("Hq,Hkv,new,few", [(8, 2, 1, True), (32, 8, 4, True), (16, 1, 1, True), (6, 2, 5, True),
+                                            (17, 1, 1, False), (32, 8, 5, False), (6, 2, 6, False)])
+def test_without_groups_and_few_rows_a_sequence(attn, tmp_path, Hq, Hkv, new, few):  # noqa: F811
+    """However many sequences there are, no unit has more rows than a sequence: up to 16 take the kernel for few
+    rows.  An empty group list and groups without a prefix give the same bits."""
+    seqs = [(1 + i % new, None if i == 3 else 37 * i) for i in range(23)]
+    c = shared_case([(0, seqs)], Hq, Hkv, 64, 32, seed=70 + new)
+    want = check(attn, c)
+    c = dev(c)
+    none = dataclasses.replace(c, group_starts=None, prefix_lens=None)
+    starts, lens = (torch.zeros(n, dtype=torch.int32, device="cuda") for n in (1, 0))
+    empty = dataclasses.replace(c, group_starts=starts, prefix_lens=lens)
+    for x in (call(attn, none), call(attn, empty)):
+        assert all(torch.equal(a, b) for a, b in zip(want, x))
+    graph = torch.cuda.CUDAGraph(keep_graph=True)  # (its dump names the kernels)
+    graph.enable_debug_mode()
+    with torch.cuda.graph(graph):
+        call(attn, none)
+    graph.debug_dump(str(tmp_path / "graph"))
+    text = (tmp_path / "graph").read_text()
+    assert "shared_units_kernel" in text
+    assert ("shared_small_kernel" in text) == few and ("shared_attn_kernel" in text) != few
+    assert attn.attn_get_device_status() == 0
+
+
 @pytest.mark.parametrize("scale,size", [(1e-6, 1.0), (3.0, 1.0), (0.1, 30.0), (2.0 ** -100, 1.0)])
 def test_scales(attn, scale, size):  # noqa: F811
     """Flat and sharp weights; rows whose maximum moves from block to block."""
