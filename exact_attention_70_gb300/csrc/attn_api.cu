@@ -1481,7 +1481,7 @@ attn_status_t norm_rope_params(NormRopeParams& p, const void* q, const void* k, 
             return ATTN_ERR_INVALID_ARG;
         const int half = rotary_dim / 2;
         int left[kNrAxes] = {half, 0, 0};
-        if (axes > 1) {
+        if (sections) {
             long long sum = 0;
             for (int a = 0; a < axes; ++a) {
                 left[a] = sections[a];

@@ -484,9 +484,9 @@ size_t attn_kvcache_plan_workspace_bytes(int batch, int total_q);
  *                 attn_fwd_kvcache; rotary_dim a multiple of 16 up to head_dim, 0: no rotation (the
  *                 arguments from here to sections_interleaved are not looked at)
  *   positions     device int32 [axes, total], axes 1 to 3: token t turns plane i by the angle of row
- *                 positions[axis(i)][t].  With one axis, axis(i) is 0 (sections may be NULL).  With more
- *                 (time, height, width), sections (host, [axes], sum rotary_dim / 2) says how many
- *                 planes an axis has: the first sections[0] are axis 0's, and so on; with
+ *                 positions[axis(i)][t].  With one axis, axis(i) is 0 (sections is NULL, or rotary_dim / 2
+ *                 alone).  With more (time, height, width), sections (host, [axes], sum rotary_dim / 2) says
+ *                 how many planes an axis has: the first sections[0] are axis 0's, and so on; with
  *                 sections_interleaved the axes take planes in turn, axis(i) = i % axes, and planes of an
  *                 axis whose section is full go to axis 0 (sections that do not come out so are refused)
  *   q_out, k_out  device bf16, dense; q_out may be q and k_out may be k where those are dense

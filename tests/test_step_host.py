@@ -110,6 +110,18 @@ def test_norm_rope_refusals(lib):
     assert call(qo=P(4104)) == -1
 
 
+def test_sections_of_one_axis_have_all_planes(lib):
+    """One axis needs no sections; those given have to come out all the same."""
+    names = ["q", "k", "qs", "ks"] + HOW + ["qo", "ko", "total", "hq", "hkv", "d", "stream"]
+    call = refusals(lib.attn_qk_norm_rope, names,
+                    [FAKE, FAKE, 1536, 1536] + HOW_GOOD + [FAKE, FAKE, 0, 8, 2, 128, None])
+    for mixed in (0, 1):
+        for n in (0, 31, 33, 64, -32, 2 ** 31 - 1):
+            assert call(sections=ints(n), mixed=mixed) == -1, n
+        assert call(sections=ints(32), mixed=mixed) == 0
+        assert call(mixed=mixed) == 0
+
+
 def test_norm_rope_bwd_refusals(lib):
     names = ["gq", "gk", "q", "k", "qs", "ks"] + HOW + ["dq", "dk", "dqs", "dks", "dqw", "dkw", "total", "hq",
                                                        "hkv", "d", "ws", "wsb", "stream"]
