@@ -259,7 +259,7 @@ __global__ void __launch_bounds__(kNrThreads, kNrFwdBlocksPerSm) norm_rope_kerne
                 const float r = rsqrtf(fmaf(ss, 1.f / D, eps));
                 const uint64_t r2 = f2_make(r, r);
 #pragma unroll
-                for (int i = 0; i < 4; ++i) x[i] = f2_mul(x[i], f2_mul(r2, w[i]));
+                for (int i = 0; i < 4; ++i) x[i] = f2_mul(f2_mul(x[i], r2), w[i]);  // (r w may be past fp32's range)
             }
             if (!isv && s.turns) turn<kInter, false>(x, c, sn);
             if (live && h < k.heads &&

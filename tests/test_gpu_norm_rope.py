@@ -133,6 +133,20 @@ def test_largest_numbers(attn):  # noqa: F811
     check_backward(attn, c)
 
 
+@pytest.mark.parametrize("w32", [False, True])
+def test_small_rows_under_large_weights(attn, w32):  # noqa: F811
+    """rstd w is past fp32's range where x rstd w is not: rows far below one, and of zeros."""
+    c = case(40, 6, 2, 128, 64, seed=81, size=2.0 ** -9, eps=1e-12, w32=w32)
+    c["packed"][::3] = 0
+    c["w"] = [(w.float() * 2.0 ** 120).to(w.dtype) for w in c["w"]]
+    check_forward(attn, c)
+    top = torch.finfo(BF16).max
+    c = case(40, 6, 2, 64, 64, seed=82, size=0.0, w32=w32)
+    c["w"] = [torch.where(w > 1, top, -top).to(w.dtype) for w in c["w"]]
+    qo, ko = check_forward(attn, c)
+    assert not qo.any() and not ko.any()
+
+
 def test_infinities_and_nan_stay_in_their_rows(attn):  # noqa: F811
     c = case(20, 4, 2, 128, 64, seed=12)
     c["packed"][3, 1, 7] = float("nan")
