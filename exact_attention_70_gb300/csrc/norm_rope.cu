@@ -25,7 +25,7 @@ namespace {
 constexpr int kNrThreads = 256;
 constexpr int kNrFwdBlocksPerSm = 4, kNrFwdRows = 4;
 constexpr int kNrBwdBlocksPerSm = 2, kNrStages = 2;
-// Sums of squares from kFarSum on are taken again, of x times kFarUnit (128 elements of 2^128 sum to 2^115).
+// Sums of squares from kFarSum on are taken again, of x times kFarUnit (the squares of 128 elements of 2^128 sum to 2^123).
 constexpr float kFarSum = 0x1p120f, kFarUnit = 0x1p-70f;
 
 // (a plain load: an output may be its input)
@@ -186,7 +186,7 @@ __device__ __forceinline__ Kind kind_of(const NormRopeParams& p) {
 
 // Forward: no block has more than one token a group, so that many small blocks hide one another's latency
 // (persistent blocks that ask for a step's rows a step ahead, as the backward's do, took 72.9 us for the 16384
-// tokens where these take 56.7).  The rows' loads go out before those of the positions, on which the tables wait.
+// tokens where these take 56.3).  The rows' loads go out before those of the positions, on which the tables wait.
 template <int D, bool kInter, bool kAppend>
 __global__ void __launch_bounds__(kNrThreads, kNrFwdBlocksPerSm) norm_rope_kernel(const NormRopeParams p) {
     constexpr int kLanes = D / 8, kRows = kNrFwdRows;

@@ -22,15 +22,17 @@
 //     sequence, shared_small_kernel does them.)
 //   * shared_combine_kernel merges the parts (O / l and log2 LSE of a piece, fp32).
 // Both sides of the 16 rows (all on tcgen05 / as it is): 4 sequences on 512 keys 16.9 / 12.8 us, 64 sequences of
-// 1K to 16K keys of their own, 32:8 heads, 361 / 351, 2 of 100K 212 / 130, 5 ragged documents 53.9 / 47.9.
+// 1K to 16K keys of their own, 32:8 heads, 361 / 349 (345 without a group list), 2 of 100K 212 / 131, 5 ragged
+// documents 53.9 / 47.7.
 //
 // Measured in a captured graph, d 128, bf16: 64 requests on 32768 shared and 100 to 2000 own keys, 32:8 heads:
-// 84.4 us (list 6, attention 73, merge 5; 421 MB, 5.0 TB/s over all); 16 samples of 4 tokens on 100001 keys:
-// 102.5 us (list 6, attention 90, merge 6).  With the two kinds in two kernels one after the other, all SMs on each, the
+// 84 us (one after the other, by the profiler: list 6, attention 74, merge 5 behind it; 421 MB, 5.0 TB/s over all); 16
+// samples of 4 tokens on 100001 keys: 102.5 us (list 6, attention 91, merge 6).  With the two kinds in two kernels one after the other, all SMs on each, the
 // first took 97.5 us: the tiles' chain left a seventh of the memory's time idle, and one kernel's last CTAs and the
 // other's first loads another 10 us.
-// A block of 128 keys under two tiles takes 3100 to 3600 clocks where the memory would take 2800: the chain
-// S, softmax, P V of a tile, 16 warps at half their issue rate, is what bounds it, as in the prefill kernel.
+// A block of 128 keys under two tiles takes 1.7 to 2.1 us where the memory would take 1.47 (from prefix to prefix, 50K to
+// 300K keys on all CTAs; d 64: 1.1 to 1.6, memory 0.74): the chain S, softmax, P V of a tile, 16 warps at half their
+// issue rate, is what bounds it, as in the prefill kernel.
 // Tried for it and not kept: P in tensor memory over S and five ring slots (the chain gets longer: 122 -> 136 us),
 // asking for blocks in L2 ahead of their loads (121 -> 138 us, the TMA unit's work doubles), two pieces a CTA
 // (107 -> 120: twice the parts).
@@ -55,6 +57,9 @@ constexpr int kShLimbs = 3;    // of 20 bits
 // Shorter prefixes are read by every sequence.  (Near this size sharing saves little, keys that L2 holds anyway: 64
 // sequences, 32:8 heads, on 128 shared keys 25.8 us (26.2 without sharing), on 512 28.1 (34.8), on 1024 28.6 (45.7);
 // 4 sequences on 512 12.8 (12.5), on 2048 13.6 (13.8), on 8192 21.6 (25.8).)
+// The same calls without a group list, in the kernel for few rows alone: 64 on 128 keys 23.4 us, on 512 30.9, on
+// 1024 39.9; 4 on 512 12.5, on 2048 13.9, on 8192 25.2; 16 on 1024 16.6 (18.5 with the list), 2 on 16K 23.9 (25.4),
+// on 32K 33.9 (37.5).  So a caller with two sequences, or with little in common, leaves the list out.
 constexpr int kShMinPrefix = 128;
 // Key blocks a piece takes at least: 2 sequences on 4096 keys, 64:8 heads, 16.2 us (18.0 with 1, 15.5 with 4),
 // 4 on 512 12.8 (12.4, 14.2), on 2048 13.6 (15.0, 15.0).
@@ -64,7 +69,8 @@ constexpr int kShMinPiece = 2;
 constexpr int kShMinFewPiece = 8;
 // What a block under two tiles costs in blocks under few rows.  The CTAs are divided by it: the tiles' chain leaves
 // memory idle that the few rows' loads take (64 requests on 32768 shared and 100 to 2000 own keys: 84.2 us, 90.8 with
-// 1.6, 88.8 with 5, 97.8 with all CTAs on tiles first; 5 ragged documents 47.9, 53.2, 48.8, 57.1).
+// 1.6, 88.8 with 5, 97.8 with all CTAs on tiles first; 5 ragged documents 47.9, 53.2, 48.8, 57.1).  These, and
+// the piece above, at d 128; not measured at d 64, where a tile's block takes 1.4 us and its bytes 0.74.
 constexpr float kShManyCost = 3.f;
 constexpr int kShCombineThreads = 256;
 // The merge gives a row eight warps up to kShFewRows rows, four up to kShMostRows (the blocks that are resident at
@@ -836,7 +842,7 @@ __device__ void sh_softmax(const SharedParams& p, uint8_t* smem, ShBars* bars, u
                     const float pb0 = ex2_approx(b0), pb1 = ex2_approx(b1);
                     suma = f2_add(suma, f2_make(pa0, pa1));
                     sumb = f2_add(sumb, f2_make(pb0, pb1));
-                    pka[c] = pack_bf16x2(pa0, pa1);
+                    pka[c] = pack_bf16x2(pa0, pa1);  // (operands of the product, at most 2^8; l sums them unrounded)
                     pkb[c] = pack_bf16x2(pb0, pb1);
                 }
                 float lo, hi;
@@ -1135,7 +1141,7 @@ __device__ void sm_consumer(const SharedParams& p, uint8_t* smem, SmBars* bars, 
                         const float p0 = ex2_approx(fmaf(s[nt][2 * r], sl2, nm[r]));
                         const float p1 = ex2_approx(fmaf(s[nt][2 * r + 1], sl2, nm[r]));
                         l_run[r] += p0 + p1;
-                        pa[2 * nt + r] = pack_bf16x2(p0, p1);
+                        pa[2 * nt + r] = pack_bf16x2(p0, p1);  // (as above: only the product's operand is rounded)
                     }
                 const uint32_t vbase = smem_u32(vst);
 #pragma unroll

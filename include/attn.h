@@ -436,7 +436,9 @@ size_t attn_fwd_kvcache_fp8_workspace_bytes(int batch, int total_q, int max_seql
  * ("Attention kernels: FlashAttention and PagedAttention", section 五.1: block tables and slots).
  *
  *   cache_seqlens  device int32 [batch], tokens that a sequence holds; the first
- *                  ceil(cache_seqlens[b] / page_size) entries of its row of block_table are its pages
+ *                  ceil(cache_seqlens[b] / page_size) entries of its row of block_table are its pages.
+ *                  New tokens go to the rest of the last of them, which has to be the sequence's own:
+ *                  one that was forked inside a page needs a copy of that page in its row first.
  *   new_lens       device int32 [batch], tokens that it gets in this step (0 and more)
  *   block_table    device int32 [batch, max_pages_per_seq], updated in place: the entries behind a
  *                  sequence's pages, up to ceil((cache_seqlens[b] + new_lens[b]) / page_size), are written,
@@ -507,6 +509,8 @@ attn_status_t attn_qk_norm_rope(const void* q, const void* k, int64_t q_stride, 
  * outputs; q, k its inputs and the other arguments as they were there:
  *   dz = R^T dy,  dw = sum over tokens and heads of x rstd dz,  h = w dz, n = x rstd,
  *   dx = rstd (h - n sum(n h) / head_dim)     (no weight: dx = dz, and q or k is not read)
+ * in fp32, rounded once; the sum is taken of x h: a row where one of these, or their sum, is past fp32's range
+ * gets gradients that are not finite.
  *   dq, dk        device bf16, dq_stride and dk_stride elements between tokens (as q_stride); dq may be
  *                 dq_out or q, dk may be dk_out or k, where the strides are the same
  *   dq_weight, dk_weight   device fp32 [head_dim], where there is a weight, else NULL
@@ -567,7 +571,10 @@ attn_status_t attn_kvcache_append_norm_rope(
  *   lse           device fp32, natural log: [batch, nheads_q] without cu_seqlens_q, else
  *                 [nheads_q, total_q]; rows outside every sequence are left as they were
  *   workspace     attn_decode_kvcache_shared_workspace_bytes(...) bytes, 256-byte aligned: the list of the
- *                 work and the partial results, about 20 total_q nheads_q head_dim bytes and 30 MB
+ *                 work and the partial results, about 30 MB and 20 total_q nheads_q head_dim bytes (36 where
+ *                 all is in groups of up to 16 rows a kv head)
+ * Logits, softmax statistics, sums and partial results are fp32; the weights are rounded to bf16 for the product
+ * with the values, as in attn_decode_kvcache, and the output once.
  * The prefix is read through one row of block_table, that of a sequence of the group that has it whole; the
  * entries of the others' pages that end before the prefix does are not looked at.  (A page in which it ends may
  * be each sequence's own; what stands before the end is taken from that one row.)  A sequence some of
